@@ -430,6 +430,80 @@ const char *zsolve_afs_last_error(const zsolve_afs *afs);
 /* Release the handle's buffers.  NULL is allowed. */
 void zsolve_afs_destroy(zsolve_afs *afs);
 
+/* ---------------------------------------------------------------------------
+ * Operators of a sequence layer: layer norm, the matrix product with its
+ * epilogue, and the gated delta rule.  A sweep's solutions are sequences
+ * (one token a frequency), and a model that learns them is made of these; the
+ * delta rule's chunked form is the blocked triangular solve of the
+ * factorisation above, one 64 x 64 unit triangle a chunk.  No passage: the
+ * page has no counterpart.
+ *
+ * Conventions, where they differ from the ones at the top:
+ *  - The work is on a handle of its own (zsolve_seq), whose stream
+ *    zsolve_seq_set_stream sets.  Every call enqueues its work and returns
+ *    without synchronising.  Calls that follow a change of stream are ordered
+ *    after the handle's earlier work.
+ *  - Pointers are device pointers, borrowed until the enqueued work is done.
+ *    A matrix is row-major; its ld* is the distance of two rows in elements.
+ *    A tensor of `type` holds ZSOLVE_F32, ZSOLVE_BF16 or ZSOLVE_F16 values and
+ *    is aligned to one of them (16-byte aligned pointers and row strides take
+ *    the fast paths).  Outputs may not overlap inputs unless said.
+ *  - Sums, statistics and states are float32; results are rounded once.
+ *  - The handle owns its workspace.  It grows when a call needs more, which
+ *    waits for the device; during a stream capture that is refused with
+ *    ZSOLVE_ESTATE (zsolve_seq_reserve, or the same call made once before the
+ *    capture, provides for it).  A handle is not thread-safe.
+ *  - Sizes of zero are allowed where they make sense (no rows, no tokens):
+ *    nothing is read, and gradients that are sums over nothing are zero.
+ * ------------------------------------------------------------------------- */
+#define ZSOLVE_F32 0
+#define ZSOLVE_BF16 1
+#define ZSOLVE_F16 2
+
+typedef struct zsolve_seq zsolve_seq;
+
+/* A handle on the current device. */
+int zsolve_seq_create(zsolve_seq **seq);
+
+/* Enqueue subsequent work on `stream` (a cudaStream_t; NULL = default stream).
+ * Set during a stream capture, it does not wait for the handle's earlier
+ * work: the caller has, before the capture began. */
+int zsolve_seq_set_stream(zsolve_seq *seq, void *stream);
+
+/* Grow the workspace to at least `bytes`. */
+int zsolve_seq_reserve(zsolve_seq *seq, int64_t bytes);
+
+/* Bytes of workspace held (what zsolve_seq_reserve needs to provide for the
+ * calls made so far). */
+int64_t zsolve_seq_workspace_bytes(const zsolve_seq *seq);
+
+/* Kernel launches the handle has made. */
+int64_t zsolve_seq_launches(const zsolve_seq *seq);
+
+/* Message of the handle's last failure ("" if none). */
+const char *zsolve_seq_last_error(const zsolve_seq *seq);
+
+/* Release the workspace (after the work in flight).  NULL is allowed. */
+void zsolve_seq_destroy(zsolve_seq *seq);
+
+/* y = (x - mu) rs w + b for each of `rows` rows of d values, mu = mean x,
+ * rs = (mean (x - mu)^2 + eps)^-1/2.
+ *   type   of x and y; wtype of w and b: `type` or ZSOLVE_F32
+ *   w, b   d values each (NULL: 1 and 0)
+ *   mean, rstd   rows float32 values each, for the backward pass (NULL: not
+ *                written)
+ * y may be x itself (ldy = ldx). */
+int zsolve_layernorm(zsolve_seq *seq, int type, int wtype, int64_t rows, int64_t d, const void *x, int64_t ldx,
+                     const void *w, const void *b, double eps, void *y, int64_t ldy, float *mean, float *rstd);
+
+/* Its gradients, with h = (x - mu) rs and a = dy w:
+ *   dx = rs (a - mean a - h mean(a h)), dw = sum over rows of dy h, db = sum
+ * over rows of dy.  dx has `type`, dw and db `wtype`; either may be NULL (not
+ * formed).  The sums over the rows are added in a fixed order. */
+int zsolve_layernorm_bwd(zsolve_seq *seq, int type, int wtype, int64_t rows, int64_t d, const void *dy, int64_t lddy,
+                         const void *x, int64_t ldx, const float *mean, const float *rstd, const void *w, void *dx,
+                         int64_t lddx, void *dw, void *db);
+
 /* Static string for a status code.  No passage: error reporting of the library. */
 const char *zsolve_strerror(int status);
 

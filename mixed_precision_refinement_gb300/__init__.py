@@ -141,6 +141,15 @@ def _load():
         "zsolve_afs_launches": (I64, [P]),
         "zsolve_afs_last_error": (ctypes.c_char_p, [P]),
         "zsolve_afs_destroy": (None, [P]),
+        "zsolve_seq_create": (I, [ctypes.POINTER(P)]),
+        "zsolve_seq_set_stream": (I, [P, P]),
+        "zsolve_seq_reserve": (I, [P, I64]),
+        "zsolve_seq_workspace_bytes": (I64, [P]),
+        "zsolve_seq_launches": (I64, [P]),
+        "zsolve_seq_last_error": (ctypes.c_char_p, [P]),
+        "zsolve_seq_destroy": (None, [P]),
+        "zsolve_layernorm": (I, [P, I, I, I64, I64, P, I64, P, P, D, P, I64, P, P]),
+        "zsolve_layernorm_bwd": (I, [P, I, I, I64, I64, P, I64, P, I64, P, P, P, P, I64, P, P]),
     }
     for name, (res, args) in sig.items():
         fn = getattr(lib, name)
@@ -516,3 +525,9 @@ class Afs:
             self.close()
         except Exception:
             pass
+
+
+from .seq import (  # noqa: E402  (the sequence-layer operators use the names above)
+    Seq, ZSOLVE_BF16, ZSOLVE_F16, ZSOLVE_F32, zsolve_layernorm, zsolve_layernorm_bwd, zsolve_seq_create,
+    zsolve_seq_destroy, zsolve_seq_last_error, zsolve_seq_launches, zsolve_seq_reserve, zsolve_seq_set_stream,
+    zsolve_seq_workspace_bytes)

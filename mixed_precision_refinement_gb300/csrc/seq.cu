@@ -1,0 +1,180 @@
+// The C-ABI of the sequence-layer operators: the handle, its workspace, and
+// the argument checks in front of the kernels.
+#include "seq.cuh"
+
+#include <cmath>
+#include <cstdarg>
+#include <cstdio>
+#include <new>
+
+namespace zs {
+
+int seq_fail(zsolve_seq *s, int status, const char *fmt, ...) {
+    va_list ap;
+    va_start(ap, fmt);
+    vsnprintf(s->err, sizeof(s->err), fmt, ap);
+    va_end(ap);
+    return status;
+}
+
+void *seq_workspace(zsolve_seq *s, size_t bytes, int *status) {
+    *status = ZSOLVE_OK;
+    if (bytes <= s->ws_bytes) return s->ws;
+    cudaStreamCaptureStatus cap = cudaStreamCaptureStatusNone;
+    cudaError_t e = cudaStreamIsCapturing(s->st, &cap);
+    if (e == cudaSuccess && cap != cudaStreamCaptureStatusNone) {
+        *status = seq_fail(s, ZSOLVE_ESTATE,
+                           "a workspace of %zu bytes is needed and cannot be allocated during a stream capture "
+                           "(zsolve_seq_reserve before it)",
+                           bytes);
+        return nullptr;
+    }
+    // the old one may still be in use by work in flight
+    if (e == cudaSuccess && s->ws) e = cudaDeviceSynchronize();
+    if (e == cudaSuccess && s->ws) {
+        e = cudaFree(s->ws);
+        s->ws = nullptr;
+        s->ws_bytes = 0;
+    }
+    if (e != cudaSuccess) {
+        *status = seq_fail(s, ZSOLVE_ECUDA, "workspace: %s", cudaGetErrorString(e));
+        return nullptr;
+    }
+    if (cudaMalloc(&s->ws, bytes) != cudaSuccess) {
+        cudaGetLastError();  // not sticky: the next call may fit
+        s->ws = nullptr;
+        *status = seq_fail(s, ZSOLVE_ENOMEM, "a workspace of %zu bytes could not be allocated", bytes);
+        return nullptr;
+    }
+    s->ws_bytes = bytes;
+    return s->ws;
+}
+
+}  // namespace zs
+
+using zs::seq_fail;
+
+namespace {
+
+// Whether the stream is in a capture (for the default stream: whether one
+// elsewhere bars its use).
+bool capturing(cudaStream_t st) {
+    cudaStreamCaptureStatus c = cudaStreamCaptureStatusNone;
+    if (cudaStreamIsCapturing(st, &c) != cudaSuccess) {
+        cudaGetLastError();
+        return true;
+    }
+    return c != cudaStreamCaptureStatusNone;
+}
+
+// The handle's device has to be the calling thread's current one.
+int check_device(zsolve_seq *s) {
+    int dev = 0;
+    SEQ_CU(cudaGetDevice(&dev));
+    if (dev != s->dev) return seq_fail(s, ZSOLVE_EINVAL, "the handle belongs to device %d, the current one is %d", s->dev, dev);
+    return ZSOLVE_OK;
+}
+
+}  // namespace
+
+extern "C" {
+
+int zsolve_seq_create(zsolve_seq **out) {
+    if (!out) return ZSOLVE_EINVAL;
+    *out = nullptr;
+    zsolve_seq *s = new (std::nothrow) zsolve_seq;
+    if (!s) return ZSOLVE_ENOMEM;
+    auto bail = [&](int st) {
+        zsolve_seq_destroy(s);
+        return st;
+    };
+    if (cudaGetDevice(&s->dev) != cudaSuccess) return bail(ZSOLVE_ECUDA);
+    if (cudaDeviceGetAttribute(&s->num_sms, cudaDevAttrMultiProcessorCount, s->dev) != cudaSuccess)
+        return bail(ZSOLVE_ECUDA);
+    if (cudaEventCreateWithFlags(&s->ev, cudaEventDisableTiming) != cudaSuccess) return bail(ZSOLVE_ECUDA);
+    if (cudaMalloc(&s->d_status, sizeof(unsigned)) != cudaSuccess) return bail(ZSOLVE_ENOMEM);
+    if (cudaMemset(s->d_status, 0, sizeof(unsigned)) != cudaSuccess) return bail(ZSOLVE_ECUDA);
+    *out = s;
+    return ZSOLVE_OK;
+}
+
+int zsolve_seq_set_stream(zsolve_seq *s, void *stream) {
+    if (!s) return ZSOLVE_EINVAL;
+    cudaStream_t st = (cudaStream_t)stream;
+    if (st == s->st) return ZSOLVE_OK;
+    // The workspace is shared: the new stream's work comes after the old
+    // stream's.  A capture cannot wait for work outside it; the caller has
+    // waited for that work before the capture began.
+    if (s->launches > 0 && !capturing(s->st) && !capturing(st)) {
+        SEQ_CU(cudaEventRecord(s->ev, s->st));
+        SEQ_CU(cudaStreamWaitEvent(st, s->ev, 0));
+    }
+    s->st = st;
+    return ZSOLVE_OK;
+}
+
+int zsolve_seq_reserve(zsolve_seq *s, int64_t bytes) {
+    if (!s) return ZSOLVE_EINVAL;
+    if (bytes < 0) return seq_fail(s, ZSOLVE_EINVAL, "bytes = %lld is negative", (long long)bytes);
+    int st = check_device(s);
+    if (st == ZSOLVE_OK && bytes > 0) zs::seq_workspace(s, (size_t)bytes, &st);
+    return st;
+}
+
+int64_t zsolve_seq_workspace_bytes(const zsolve_seq *s) { return s ? (int64_t)s->ws_bytes : 0; }
+
+int64_t zsolve_seq_launches(const zsolve_seq *s) { return s ? s->launches : 0; }
+
+const char *zsolve_seq_last_error(const zsolve_seq *s) { return s ? s->err : "NULL handle"; }
+
+void zsolve_seq_destroy(zsolve_seq *s) {
+    if (!s) return;
+    cudaFree(s->ws);  // waits for the work in flight
+    cudaFree(s->d_status);
+    if (s->ev) cudaEventDestroy(s->ev);
+    delete s;
+}
+
+int zsolve_layernorm(zsolve_seq *s, int type, int wtype, int64_t rows, int64_t d, const void *x, int64_t ldx,
+                     const void *w, const void *b, double eps, void *y, int64_t ldy, float *mean, float *rstd) {
+    if (!s) return ZSOLVE_EINVAL;
+    if (!zs::type_ok(type) || (wtype != type && wtype != ZSOLVE_F32))
+        return seq_fail(s, ZSOLVE_EINVAL, "type %d, wtype %d: wtype is the type of x or ZSOLVE_F32", type, wtype);
+    if (rows < 0 || rows > 0x7fffffff || d < 1 || d > 0x7fffffff)
+        return seq_fail(s, ZSOLVE_EINVAL, "rows = %lld, d = %lld", (long long)rows, (long long)d);
+    if (!(eps >= 0.0) || !std::isfinite(eps)) return seq_fail(s, ZSOLVE_EINVAL, "eps = %g", eps);
+    if (rows == 0) return ZSOLVE_OK;
+    if (!x || !y) return seq_fail(s, ZSOLVE_EINVAL, "NULL x or y");
+    if (ldx < d || ldy < d) return seq_fail(s, ZSOLVE_EINVAL, "ldx = %lld or ldy = %lld is below d = %lld", (long long)ldx, (long long)ldy, (long long)d);
+    int st = check_device(s);
+    if (st != ZSOLVE_OK) return st;
+    SEQ_CU(zs_launch_layernorm(type, wtype == ZSOLVE_F32, rows, d, x, ldx, w, b, (float)eps, y, ldy, mean, rstd, s->st,
+                               &s->launches));
+    return ZSOLVE_OK;
+}
+
+int zsolve_layernorm_bwd(zsolve_seq *s, int type, int wtype, int64_t rows, int64_t d, const void *dy, int64_t lddy,
+                         const void *x, int64_t ldx, const float *mean, const float *rstd, const void *w, void *dx,
+                         int64_t lddx, void *dw, void *db) {
+    if (!s) return ZSOLVE_EINVAL;
+    if (!zs::type_ok(type) || (wtype != type && wtype != ZSOLVE_F32))
+        return seq_fail(s, ZSOLVE_EINVAL, "type %d, wtype %d: wtype is the type of x or ZSOLVE_F32", type, wtype);
+    if (rows < 0 || rows > 0x7fffffff || d < 1 || d > 0x7fffffff)
+        return seq_fail(s, ZSOLVE_EINVAL, "rows = %lld, d = %lld", (long long)rows, (long long)d);
+    if (rows > 0 && (!dy || !x || !mean || !rstd || !dx)) return seq_fail(s, ZSOLVE_EINVAL, "NULL dy, x, mean, rstd or dx");
+    if (rows > 0 && (lddy < d || ldx < d || lddx < d))
+        return seq_fail(s, ZSOLVE_EINVAL, "a row stride (%lld, %lld, %lld) is below d = %lld", (long long)lddy, (long long)ldx, (long long)lddx, (long long)d);
+    int st = check_device(s);
+    if (st != ZSOLVE_OK) return st;
+    float *parts = nullptr;
+    if (dw || db) {
+        const int64_t n = zs_layernorm_bwd_parts(type, rows, d, s->num_sms);
+        if (n > 0) parts = (float *)zs::seq_workspace(s, (size_t)n * 4, &st);
+        if (st != ZSOLVE_OK) return st;
+    }
+    SEQ_CU(zs_launch_layernorm_bwd(type, wtype == ZSOLVE_F32, rows, d, dy, lddy, x, ldx, mean, rstd, w, dx, lddx, dw,
+                                   db, parts, s->num_sms, s->st, &s->launches));
+    return ZSOLVE_OK;
+}
+
+}  // extern "C"

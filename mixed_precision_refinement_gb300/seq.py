@@ -1,0 +1,202 @@
+"""Binding of the sequence-layer operators (layer norm, linear, delta rule) of include/zsolve.h.
+
+As in the rest of the binding, a function with a C entry point's name calls it
+on tensors that the caller holds; `Seq` owns a handle, allocates the outputs
+and runs on torch's current stream.
+"""
+from __future__ import annotations
+
+import ctypes
+
+from . import ZSOLVE_OK, ZsolveError, _lib
+
+ZSOLVE_F32 = 0
+ZSOLVE_BF16 = 1
+ZSOLVE_F16 = 2
+
+
+def _types():
+    import torch
+    return {torch.float32: ZSOLVE_F32, torch.bfloat16: ZSOLVE_BF16, torch.float16: ZSOLVE_F16}
+
+
+_TYPES = None
+
+
+def _type(t, name) -> int:
+    global _TYPES
+    if _TYPES is None:
+        _TYPES = _types()
+    if t.dtype not in _TYPES:
+        raise TypeError(f"{name}: expected float32, bfloat16 or float16, got {t.dtype}")
+    return _TYPES[t.dtype]
+
+
+def _cuda(t, name):
+    if not t.is_cuda:
+        raise ValueError(f"{name}: expected a CUDA tensor")
+
+
+def _rows(t, name, dtype=None, shape=None):
+    """(pointer, rows, d, row stride) of a matrix: a tensor (..., d) whose rows lie at one distance."""
+    _cuda(t, name)
+    if dtype is not None and t.dtype != dtype:
+        raise TypeError(f"{name}: expected {dtype}, got {t.dtype}")
+    if t.dim() != 2:
+        if t.dim() == 0:
+            raise ValueError(f"{name}: expected rows of values")
+        t = t.view(-1, t.shape[-1]) if t.numel() else t.reshape(-1, t.shape[-1])
+    m, d = t.shape
+    if shape is not None and (m, d) != shape:
+        raise ValueError(f"{name}: expected {shape[0]} rows of {shape[1]}, got {m} of {d}")
+    if d > 1 and t.stride(1) != 1:
+        raise ValueError(f"{name}: the values of a row must be contiguous")
+    return t.data_ptr(), m, d, t.stride(0) if m > 1 else max(d, 1)
+
+
+def _vector(t, name, n, dtype):
+    """Pointer of a contiguous vector of n values, or 0 for None."""
+    if t is None:
+        return 0
+    _cuda(t, name)
+    if t.dtype != dtype:
+        raise TypeError(f"{name}: expected {dtype}, got {t.dtype}")
+    if t.numel() != n or not t.is_contiguous():
+        raise ValueError(f"{name}: expected {n} contiguous values, got {tuple(t.shape)}")
+    return t.data_ptr()
+
+
+def _check_seq(seq, status):
+    if status != ZSOLVE_OK:
+        msg = _lib.zsolve_seq_last_error(seq).decode() if seq else ""
+        raise ZsolveError(status, f"{_lib.zsolve_strerror(status).decode()}: {msg}")
+
+
+# ---------------------------------------------------------------- C entry points
+
+
+def zsolve_seq_create() -> ctypes.c_void_p:
+    seq = ctypes.c_void_p()
+    _check_seq(None, _lib.zsolve_seq_create(ctypes.byref(seq)))
+    return seq
+
+
+def zsolve_seq_set_stream(seq, stream=None) -> None:
+    """stream: a torch.cuda.Stream, a raw handle, or None for torch's current stream."""
+    import torch
+    if stream is None:
+        stream = torch.cuda.current_stream()
+    handle = stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
+    _check_seq(seq, _lib.zsolve_seq_set_stream(seq, handle))
+
+
+def zsolve_seq_reserve(seq, nbytes: int) -> None:
+    _check_seq(seq, _lib.zsolve_seq_reserve(seq, int(nbytes)))
+
+
+def zsolve_seq_workspace_bytes(seq) -> int:
+    return int(_lib.zsolve_seq_workspace_bytes(seq))
+
+
+def zsolve_seq_launches(seq) -> int:
+    return int(_lib.zsolve_seq_launches(seq))
+
+
+def zsolve_seq_last_error(seq) -> str:
+    return _lib.zsolve_seq_last_error(seq).decode()
+
+
+def zsolve_seq_destroy(seq) -> None:
+    _lib.zsolve_seq_destroy(seq)
+
+
+def _norm_weights(x, w, b):
+    """Type code of w and b (the type of x, or float32), and their torch type."""
+    import torch
+    given = w if w is not None else b
+    dt = x.dtype if given is None else given.dtype
+    if dt not in (x.dtype, torch.float32):
+        raise TypeError(f"w and b: expected {x.dtype} or torch.float32, got {dt}")
+    return dt
+
+
+def zsolve_layernorm(seq, x, w, b, eps, y, mean=None, rstd=None) -> None:
+    """y <- layer norm of the rows of x (..., d); w, b: (d,) or None; mean, rstd: float32, one value a row, or None."""
+    import torch
+    xp, m, d, ldx = _rows(x, "x")
+    yp, _, _, ldy = _rows(y, "y", x.dtype, (m, d))
+    wt = _norm_weights(x, w, b)
+    _check_seq(seq, _lib.zsolve_layernorm(seq, _type(x, "x"), _TYPES[wt], m, d, xp, ldx, _vector(w, "w", d, wt),
+                                          _vector(b, "b", d, wt), eps, yp, ldy,
+                                          _vector(mean, "mean", m, torch.float32),
+                                          _vector(rstd, "rstd", m, torch.float32)))
+
+
+def zsolve_layernorm_bwd(seq, dy, x, mean, rstd, w, dx, dw=None, db=None) -> None:
+    """dx (the shape of x), dw and db (the type of w, or of x without one; None: not formed) from dy."""
+    import torch
+    xp, m, d, ldx = _rows(x, "x")
+    dyp, _, _, lddy = _rows(dy, "dy", x.dtype, (m, d))
+    dxp, _, _, lddx = _rows(dx, "dx", x.dtype, (m, d))
+    wt = _norm_weights(x, w, dw if dw is not None else db)
+    _check_seq(seq, _lib.zsolve_layernorm_bwd(seq, _type(x, "x"), _TYPES[wt], m, d, dyp, lddy, xp, ldx,
+                                              _vector(mean, "mean", m, torch.float32),
+                                              _vector(rstd, "rstd", m, torch.float32), _vector(w, "w", d, wt), dxp,
+                                              lddx, _vector(dw, "dw", d, wt), _vector(db, "db", d, wt)))
+
+
+class Seq:
+    """Owns one handle of the sequence-layer operators; runs on torch's current stream.
+
+    Example (x: bfloat16 CUDA tensor, tokens x d)::
+
+        with Seq() as s:
+            h, mean, rstd = s.layernorm(x, w, b)
+            dx, dw, db = s.layernorm_bwd(dh, x, mean, rstd, w)
+    """
+
+    def __init__(self):
+        self._stream = None
+        self.seq = zsolve_seq_create()
+
+    def _on_stream(self):
+        import torch
+        st = torch.cuda.current_stream().cuda_stream
+        if st != self._stream:
+            _check_seq(self.seq, _lib.zsolve_seq_set_stream(self.seq, st))
+            self._stream = st
+
+    def layernorm(self, x, w=None, b=None, eps=1e-5):
+        """Returns (y, mean, rstd); mean and rstd are float32, for layernorm_bwd."""
+        import torch
+        self._on_stream()
+        y = torch.empty(x.shape, dtype=x.dtype, device=x.device)
+        mean, rstd = torch.empty((2,) + x.shape[:-1], dtype=torch.float32, device=x.device).unbind(0)
+        zsolve_layernorm(self.seq, x, w, b, eps, y, mean, rstd)
+        return y, mean, rstd
+
+    def layernorm_bwd(self, dy, x, mean, rstd, w=None):
+        """Returns (dx, dw, db); dw and db have the type of w (of x without one)."""
+        import torch
+        self._on_stream()
+        dx = torch.empty(x.shape, dtype=x.dtype, device=x.device)
+        dw, db = torch.empty((2, x.shape[-1]), dtype=x.dtype if w is None else w.dtype, device=x.device).unbind(0)
+        zsolve_layernorm_bwd(self.seq, dy, x, mean, rstd, w, dx, dw, db)
+        return dx, dw, db
+
+    def close(self):
+        if self.seq:
+            zsolve_seq_destroy(self.seq)
+            self.seq = None
+
+    def __enter__(self):
+        return self
+
+    def __exit__(self, *exc):
+        self.close()
+
+    def __del__(self):
+        try:
+            self.close()
+        except Exception:
+            pass

@@ -460,6 +460,13 @@ void zsolve_afs_destroy(zsolve_afs *afs);
 #define ZSOLVE_BF16 1
 #define ZSOLVE_F16 2
 
+/* activations */
+#define ZSOLVE_ACT_NONE 0
+#define ZSOLVE_ACT_RELU 1
+#define ZSOLVE_ACT_SILU 2      /* z / (1 + exp(-z)) */
+#define ZSOLVE_ACT_GELU 3      /* z (1 + erf(z / sqrt 2)) / 2 */
+#define ZSOLVE_ACT_GELU_TANH 4 /* z (1 + tanh(sqrt(2/pi) (z + 0.044715 z^3))) / 2 */
+
 typedef struct zsolve_seq zsolve_seq;
 
 /* A handle on the current device. */
@@ -479,6 +486,10 @@ int64_t zsolve_seq_workspace_bytes(const zsolve_seq *seq);
 
 /* Kernel launches the handle has made. */
 int64_t zsolve_seq_launches(const zsolve_seq *seq);
+
+/* Wait for the handle's work: ZSOLVE_ETIMEOUT if a bounded device-side wait
+ * gave up since the last check (outputs since then are not to be used). */
+int zsolve_seq_check(zsolve_seq *seq);
 
 /* Message of the handle's last failure ("" if none). */
 const char *zsolve_seq_last_error(const zsolve_seq *seq);
@@ -503,6 +514,24 @@ int zsolve_layernorm(zsolve_seq *seq, int type, int wtype, int64_t rows, int64_t
 int zsolve_layernorm_bwd(zsolve_seq *seq, int type, int wtype, int64_t rows, int64_t d, const void *dy, int64_t lddy,
                          const void *x, int64_t ldx, const float *mean, const float *rstd, const void *w, void *dx,
                          int64_t lddx, void *dw, void *db);
+
+/* z = x W^T + b, y = act(z) + r: x is m x k, W n x k, y m x n, all of `type`
+ * (ZSOLVE_BF16 or ZSOLVE_F16), on the tensor cores with float32 sums.
+ *   b      n values (NULL: none);  r   m x n (NULL: none)
+ *   z      m x n: z rounded to `type`, for the backward pass (NULL: not kept)
+ * y may be r itself (ldy = ldr).  Operands whose pointer or row stride is not
+ * a multiple of 16 bytes are copied to the workspace first. */
+int zsolve_linear(zsolve_seq *seq, int type, int64_t m, int64_t n, int64_t k, const void *x, int64_t ldx,
+                  const void *w, int64_t ldw, const void *b, int act, const void *r, int64_t ldr, void *y,
+                  int64_t ldy, void *z, int64_t ldz);
+
+/* Its gradients: with dz = dy act'(z) rounded to `type`, dx = dz W, dW = dz^T x,
+ * and db = the sum over rows of dy act'(z) in float32 (r's gradient is dy).
+ * Each of dx, dw, db may be NULL (not formed), as may then what only it needs;
+ * z is not read without an activation. */
+int zsolve_linear_bwd(zsolve_seq *seq, int type, int64_t m, int64_t n, int64_t k, const void *dy, int64_t lddy,
+                      const void *x, int64_t ldx, const void *w, int64_t ldw, int act, const void *z, int64_t ldz,
+                      void *dx, int64_t lddx, void *dw, int64_t lddw, void *db);
 
 /* Static string for a status code.  No passage: error reporting of the library. */
 const char *zsolve_strerror(int status);

@@ -1,0 +1,769 @@
+// The matrix product with bias, activation and residual in its epilogue, and
+// its gradients, on the 5th-generation tensor cores:
+//   z = x W^T + b, y = act(z) + r            x: m x k, W: n x k
+//   dz = dy act'(z), dx = dz W, dW = dz^T x, db = sum over rows of dz
+// All three products are one kernel, D(i, j) = sum_k A(i, k) B(j, k), for
+// operands that are contiguous along k ("K-major": x and W forward, dz for
+// dx) or along their rows ("MN-major": W for dx, both for dW), so nothing is
+// transposed in memory.  kind::f16 MMAs of 128 x BN x 16 with float32
+// accumulators in TMEM; operands come by TMA in 128-byte swizzled tiles of 64
+// along k, zero-filled beyond the matrices' ends, so ragged sizes need no
+// code in the main loop.
+//
+// Warp roles (192 threads, persistent over the output tiles): warp 0 issues
+// the TMA loads into a ring of stages, warp 1 the MMAs (one thread), warps 2-5
+// drain the accumulator while the next tile's MMAs fill the other half of TMEM.
+// Products with fewer tiles than SMs are split along k: each part leaves its
+// float32 partial sums in the workspace and a second kernel adds them in a
+// fixed order and applies the epilogue.  Every mbarrier wait is bounded: on
+// give-up the kernel raises the handle's status word, stops all roles, waits
+// (bounded) for its own copies and MMAs and frees TMEM.
+#include <cuda.h>
+#include <cudaTypedefs.h>
+
+#include <algorithm>
+
+#include "seq.cuh"
+
+namespace {
+
+using namespace zs;
+
+constexpr int BM = 128;       // rows of an output tile
+constexpr int BK = 64;        // k values of a stage: 128 bytes, one swizzle row
+constexpr int kThreads = 192;
+constexpr uint32_t kTmemCols = 512;
+constexpr uint32_t kWaitLimit = 1u << 19;  // try_wait polls before a wait gives up: about a second
+
+template <int BN>
+struct Cfg {
+    static constexpr int A_BYTES = BM * BK * 2;
+    static constexpr int B_BYTES = BN * BK * 2;
+    static constexpr int STAGE = A_BYTES + B_BYTES;
+    static constexpr int STAGES = BN == 256 ? 4 : 6;
+    static constexpr int SMEM = STAGES * STAGE + 1024;  // + alignment slack
+};
+
+// ---------------------------------------------------------------- PTX
+
+__device__ __forceinline__ uint32_t smem_u32(const void *p) { return (uint32_t)__cvta_generic_to_shared(p); }
+
+__device__ __forceinline__ void mbar_init(uint32_t bar, uint32_t count) {
+    asm volatile("mbarrier.init.shared::cta.b64 [%0], %1;" ::"r"(bar), "r"(count) : "memory");
+}
+__device__ __forceinline__ void mbar_expect_tx(uint32_t bar, uint32_t bytes) {
+    asm volatile("mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;" ::"r"(bar), "r"(bytes) : "memory");
+}
+__device__ __forceinline__ void mbar_arrive(uint32_t bar) {
+    asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(bar) : "memory");
+}
+__device__ __forceinline__ bool mbar_try_wait(uint32_t bar, uint32_t parity) {
+    uint32_t ok;
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
+        "selp.u32 %0, 1, 0, p;\n\t}"
+        : "=r"(ok)
+        : "r"(bar), "r"(parity)
+        : "memory");
+    return ok != 0;
+}
+// Bounded wait: false once it or another role of the block has given up.
+__device__ __forceinline__ bool mbar_wait(uint32_t bar, uint32_t parity, volatile int *abort_flag, unsigned *status) {
+    uint32_t it = 0;
+    while (!mbar_try_wait(bar, parity)) {
+        if (*abort_flag) return false;
+        if (++it > kWaitLimit) {
+            *abort_flag = 1;
+            atomicOr(status, 1u);
+            return false;
+        }
+    }
+    return true;
+}
+__device__ __forceinline__ void tma_load_2d(uint32_t dst, const CUtensorMap *map, int c0, int c1, uint32_t bar) {
+    asm volatile(
+        "cp.async.bulk.tensor.2d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
+        " [%0], [%1, {%2, %3}], [%4];" ::"r"(dst),
+        "l"((uint64_t)map), "r"(c0), "r"(c1), "r"(bar)
+        : "memory");
+}
+__device__ __forceinline__ void mma_f16(uint32_t d_tmem, uint64_t a, uint64_t b, uint32_t idesc, uint32_t accumulate) {
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "setp.ne.b32 p, %4, 0;\n\t"
+        "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d_tmem),
+        "l"(a), "l"(b), "r"(idesc), "r"(accumulate)
+        : "memory");
+}
+__device__ __forceinline__ void mma_commit(uint32_t bar) {
+    asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(bar) : "memory");
+}
+__device__ __forceinline__ void tc_fence_before() { asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory"); }
+__device__ __forceinline__ void tc_fence_after() { asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory"); }
+
+// 32 lanes x 32 consecutive float32 columns of the accumulator
+__device__ __forceinline__ void tmem_ld32(uint32_t taddr, float (&v)[32]) {
+    uint32_t r[32];
+    asm volatile(
+        "tcgen05.ld.sync.aligned.32x32b.x32.b32 "
+        "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, "
+        "%16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31}, [%32];"
+        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]),
+          "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15]),
+          "=r"(r[16]), "=r"(r[17]), "=r"(r[18]), "=r"(r[19]), "=r"(r[20]), "=r"(r[21]), "=r"(r[22]),
+          "=r"(r[23]), "=r"(r[24]), "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]),
+          "=r"(r[30]), "=r"(r[31])
+        : "r"(taddr)
+        : "memory");
+    asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
+#pragma unroll
+    for (int i = 0; i < 32; i++) v[i] = __uint_as_float(r[i]);
+}
+
+// Shared-memory descriptor of a 128-byte swizzled operand.  K-major: rows of
+// 128 bytes (64 k values), groups of 8 rows 1024 bytes apart (stride offset).
+// MN-major: rows of 128 bytes hold 64 values along M or N for one k; groups of
+// 8 k 1024 bytes apart (stride offset), the next 64 along M or N a box of
+// 64 k rows further (leading offset).
+constexpr uint32_t kBox = 64 * 128;  // bytes of an MN-major box: 64 k rows
+template <bool MN>
+__device__ __forceinline__ uint64_t smem_desc(uint32_t addr) {
+    return (uint64_t)((addr >> 4) & 0x3FFF) | (uint64_t)(MN ? kBox >> 4 : 1) << 16 | (uint64_t)(1024 >> 4) << 32 |
+           (uint64_t)1 << 46 | (uint64_t)2 << 61;
+}
+
+// ---------------------------------------------------------------- epilogue
+
+enum { ACT_NONE = ZSOLVE_ACT_NONE, ACT_RELU = ZSOLVE_ACT_RELU, ACT_SILU = ZSOLVE_ACT_SILU, ACT_GELU = ZSOLVE_ACT_GELU, ACT_GELU_TANH = ZSOLVE_ACT_GELU_TANH };
+
+__device__ __forceinline__ float sigmoid(float x) { return __fdividef(1.f, 1.f + __expf(-x)); }
+
+// The tanh form in the sigmoid: (1 + tanh u) / 2 = sigmoid(2 u), without the
+// cancellation of 1 + tanh u for negative u.
+constexpr float kTanhC = 0.7978845608028654f, kTanhA = 0.044715f;
+
+template <int ACT>
+__device__ __forceinline__ float act1(float z) {
+    if (ACT == ACT_RELU) return z <= 0.f ? 0.f : z;
+    if (ACT == ACT_SILU) return __fdividef(z, 1.f + __expf(-z));
+    if (ACT == ACT_GELU) return 0.5f * z * (1.f + erff(z * 0.7071067811865476f));
+    if (ACT == ACT_GELU_TANH) return __fdividef(z, 1.f + __expf(-2.f * kTanhC * fmaf(kTanhA * z * z, z, z)));
+    return z;
+}
+template <int ACT>
+__device__ __forceinline__ float slope1(float z) {
+    if (ACT == ACT_RELU) return z > 0.f ? 1.f : 0.f;
+    if (ACT == ACT_SILU) {
+        const float p = sigmoid(z);
+        return p * fmaf(z, 1.f - p, 1.f);
+    }
+    if (ACT == ACT_GELU)
+        return fmaf(z * 0.3989422804014327f, __expf(-0.5f * z * z), 0.5f * (1.f + erff(z * 0.7071067811865476f)));
+    if (ACT == ACT_GELU_TANH) {
+        const float p = sigmoid(2.f * kTanhC * fmaf(kTanhA * z * z, z, z));
+        return fmaf(2.f * kTanhC * fmaf(3.f * kTanhA * z, z, 1.f), z * p * (1.f - p), p);
+    }
+    return 1.f;
+}
+
+template <int N>
+__device__ __forceinline__ void act_all(float (&v)[N], int act) {
+#define ACT_CASE(A)                                        \
+    case A: {                                              \
+        _Pragma("unroll") for (int i = 0; i < N; i++) v[i] = act1<A>(v[i]); \
+        break;                                             \
+    }
+    switch (act) {
+        ACT_CASE(ACT_RELU)
+        ACT_CASE(ACT_SILU)
+        ACT_CASE(ACT_GELU)
+        ACT_CASE(ACT_GELU_TANH)
+    }
+#undef ACT_CASE
+}
+
+// What happens to a tile of the product: part (float32 partial sums, row
+// stride ldp, one matrix of prows rows a split) or the finished result.
+struct Epilogue {
+    const void *bias;  // NULL: none
+    const void *r;     // residual, NULL: none
+    void *y;
+    void *z;           // product and bias before the activation, NULL: not kept
+    int64_t ldr, ldy, ldz;
+    float *part;
+    int64_t ldp;
+    int act;
+    int vec;           // 16-byte accesses allowed in bias, r, y, z
+};
+
+// 8 consecutive values of row `row` from column c on, of which nc (1..8) exist
+template <typename T>
+__device__ __forceinline__ void load8(const void *base, int64_t at, int nc, int vec, float (&f)[8]) {
+    const T *p = reinterpret_cast<const T *>(base) + at;
+    if (vec && nc == 8) {
+        Vec<T, 8> u;
+        u.load(p);
+        u.get(f);
+    } else {
+#pragma unroll
+        for (int i = 0; i < 8; i++) f[i] = i < nc ? to_f32(p[i]) : 0.f;
+    }
+}
+template <typename T>
+__device__ __forceinline__ void store8(void *base, int64_t at, int nc, int vec, const float (&f)[8]) {
+    T *p = reinterpret_cast<T *>(base) + at;
+    if (vec && nc == 8) {
+        Vec<T, 8> u;
+        u.set(f);
+        u.store(p);
+    } else {
+#pragma unroll
+        for (int i = 0; i < 8; i++)
+            if (i < nc) p[i] = from_f32<T>(f[i]);
+    }
+}
+
+// bias, activation, residual and the stores of 8 values
+template <typename T>
+__device__ __forceinline__ void finish8(const Epilogue &e, int64_t row, int64_t c, int nc, float (&v)[8]) {
+    float f[8];
+    if (e.bias) {
+        load8<T>(e.bias, c, nc, e.vec, f);
+#pragma unroll
+        for (int i = 0; i < 8; i++) v[i] += f[i];
+    }
+    if (e.z) store8<T>(e.z, row * e.ldz + c, nc, e.vec, v);
+    act_all(v, e.act);
+    if (e.r) {
+        load8<T>(e.r, row * e.ldr + c, nc, e.vec, f);
+#pragma unroll
+        for (int i = 0; i < 8; i++) v[i] += f[i];
+    }
+    store8<T>(e.y, row * e.ldy + c, nc, e.vec, v);
+}
+
+// ---------------------------------------------------------------- product
+
+// Output tile t of the launch: bands of kBand row tiles, column by column
+// within a band, so that the blocks at work at one time share few operand
+// rows and find most of them in L2.
+constexpr int kBand = 16;
+struct TileAt {
+    int tm, tn, split;
+};
+__device__ __forceinline__ TileAt tile_at(int t, int mt, int nt) {
+    TileAt x;
+    const int per = mt * nt;
+    x.split = t / per;
+    t -= x.split * per;
+    const int band = t / (kBand * nt), in = t - band * kBand * nt;
+    const int rows = min(kBand, mt - band * kBand);
+    x.tm = band * kBand + in % rows;
+    x.tn = in / rows;
+    return x;
+}
+
+template <typename T, int BN, bool A_MN, bool B_MN>
+__global__ void __launch_bounds__(kThreads, 1)
+k_linear_tc(const __grid_constant__ CUtensorMap amap, const __grid_constant__ CUtensorMap bmap, int64_t M, int64_t N,
+            int kblocks, int splits, const Epilogue epi, unsigned *__restrict__ status) {
+    using C = Cfg<BN>;
+    extern __shared__ uint8_t smem_raw[];
+    __shared__ __align__(8) uint64_t bar_full[C::STAGES], bar_empty[C::STAGES], bar_accf[2], bar_acce[2], bar_drain;
+    __shared__ uint32_t s_tmem;
+    __shared__ volatile int s_abort;
+    const uint32_t base = (smem_u32(smem_raw) + 1023u) & ~1023u;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int mt = (int)((M + BM - 1) / BM), nt = (int)((N + BN - 1) / BN);
+    const int total = mt * nt * splits;
+    // kind::f16: D float32, A and B of one type, majors, N, M
+    constexpr uint32_t fmt = sizeof(T) == 2 && std::is_same<T, bf16>::value ? 1u : 0u;
+    constexpr uint32_t idesc = (1u << 4) | (fmt << 7) | (fmt << 10) | ((A_MN ? 1u : 0u) << 15) |
+                               ((B_MN ? 1u : 0u) << 16) | ((uint32_t)(BN >> 3) << 17) | ((uint32_t)(BM >> 4) << 24);
+
+    if (threadIdx.x == 0) {
+        s_abort = 0;
+        for (int s = 0; s < C::STAGES; s++) {
+            mbar_init(smem_u32(&bar_full[s]), 1);
+            mbar_init(smem_u32(&bar_empty[s]), 1);
+        }
+        for (int b = 0; b < 2; b++) {
+            mbar_init(smem_u32(&bar_accf[b]), 1);
+            mbar_init(smem_u32(&bar_acce[b]), 4);
+        }
+        mbar_init(smem_u32(&bar_drain), 1);
+        asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+    }
+    if (warp == 1) {
+        asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(&s_tmem)),
+                     "r"(kTmemCols)
+                     : "memory");
+        asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
+    }
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem = s_tmem;
+    // k blocks of split s: an equal share, the first ones one more
+    auto kfirst = [&](int s) { return (int)((int64_t)kblocks * s / splits); };
+
+    if (warp == 0) {
+        // ------------------------------------------------ TMA producer
+        if (lane == 0) {
+            asm volatile("prefetch.tensormap [%0];" ::"l"((uint64_t)&amap) : "memory");
+            asm volatile("prefetch.tensormap [%0];" ::"l"((uint64_t)&bmap) : "memory");
+            uint32_t g = 0;
+            bool ok = true;
+            for (int t = blockIdx.x; t < total && ok; t += gridDim.x) {
+                const TileAt x = tile_at(t, mt, nt);
+                const int k1 = kfirst(x.split + 1);
+                for (int kb = kfirst(x.split); kb < k1; kb++, g++) {
+                    const uint32_t st = g % C::STAGES, ph = (g / C::STAGES) & 1u;
+                    if (!mbar_wait(smem_u32(&bar_empty[st]), ph ^ 1u, &s_abort, status)) {
+                        ok = false;
+                        break;
+                    }
+                    const uint32_t fb = smem_u32(&bar_full[st]);
+                    mbar_expect_tx(fb, C::STAGE);
+                    const uint32_t sa = base + st * C::STAGE, sb = sa + C::A_BYTES;
+                    if (A_MN) {
+#pragma unroll
+                        for (int i = 0; i < BM / 64; i++)
+                            tma_load_2d(sa + i * kBox, &amap, x.tm * BM + i * 64, kb * BK, fb);
+                    } else {
+                        tma_load_2d(sa, &amap, kb * BK, x.tm * BM, fb);
+                    }
+                    if (B_MN) {
+#pragma unroll
+                        for (int i = 0; i < BN / 64; i++)
+                            tma_load_2d(sb + i * kBox, &bmap, x.tn * BN + i * 64, kb * BK, fb);
+                    } else {
+                        tma_load_2d(sb, &bmap, kb * BK, x.tn * BN, fb);
+                    }
+                }
+            }
+            // our own copies in flight: wait (bounded) for the last stages to land
+            for (uint32_t q = g > (uint32_t)C::STAGES ? g - C::STAGES : 0; q < g; q++) {
+                uint32_t it = 0;
+                while (!mbar_try_wait(smem_u32(&bar_full[q % C::STAGES]), (q / C::STAGES) & 1u) && ++it < kWaitLimit) {
+                }
+            }
+        }
+    } else if (warp == 1) {
+        // ------------------------------------------------ MMA issuer
+        if (lane == 0) {
+            uint32_t g = 0, it = 0;
+            bool ok = true;
+            for (int t = blockIdx.x; t < total && ok; t += gridDim.x, it++) {
+                const TileAt x = tile_at(t, mt, nt);
+                const int k0 = kfirst(x.split), k1 = kfirst(x.split + 1);
+                const uint32_t buf = it & 1u, aph = (it >> 1) & 1u;
+                if (!mbar_wait(smem_u32(&bar_acce[buf]), aph ^ 1u, &s_abort, status)) break;
+                tc_fence_after();
+                const uint32_t d = tmem + buf * 256u;
+                for (int kb = k0; kb < k1; kb++, g++) {
+                    const uint32_t st = g % C::STAGES, ph = (g / C::STAGES) & 1u;
+                    if (!mbar_wait(smem_u32(&bar_full[st]), ph, &s_abort, status)) {
+                        ok = false;
+                        break;
+                    }
+                    tc_fence_after();
+                    const uint32_t sa = base + st * C::STAGE, sb = sa + C::A_BYTES;
+#pragma unroll
+                    for (int ks = 0; ks < BK / 16; ks++)  // 16 k: 32 bytes of a K-major row, 16 rows of an MN-major box
+                        mma_f16(d, smem_desc<A_MN>(sa + ks * (A_MN ? 2048 : 32)),
+                                smem_desc<B_MN>(sb + ks * (B_MN ? 2048 : 32)), idesc, (kb > k0 || ks) ? 1u : 0u);
+                    mma_commit(smem_u32(&bar_empty[st]));  // stage free once these MMAs finish
+                }
+                if (!ok) break;
+                mma_commit(smem_u32(&bar_accf[buf]));  // accumulator ready
+            }
+            // every MMA issued so far completes before TMEM is freed
+            mma_commit(smem_u32(&bar_drain));
+            uint32_t w = 0;
+            while (!mbar_try_wait(smem_u32(&bar_drain), 0) && ++w < kWaitLimit) {
+            }
+        }
+    } else {
+        // ------------------------------------------------ epilogue (warps 2-5)
+        const int quad = warp & 3;  // TMEM lanes 32 quad .. 32 quad + 31
+        uint32_t it = 0;
+        for (int t = blockIdx.x; t < total; t += gridDim.x, it++) {
+            const TileAt x = tile_at(t, mt, nt);
+            const uint32_t buf = it & 1u, aph = (it >> 1) & 1u;
+            const bool ok = mbar_wait(smem_u32(&bar_accf[buf]), aph, &s_abort, status);
+            if (!__all_sync(0xffffffffu, ok)) break;
+            tc_fence_after();
+            const int64_t row = (int64_t)x.tm * BM + quad * 32 + lane;
+#pragma unroll 1
+            for (int c = 0; c < BN / 32; c++) {
+                float v[32];
+                tmem_ld32(tmem + buf * 256u + (uint32_t)(c * 32) + ((uint32_t)(quad * 32) << 16), v);
+                if (c == BN / 32 - 1) {  // accumulator fully read: hand it back to the MMA warp
+                    tc_fence_before();
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(smem_u32(&bar_acce[buf]));
+                }
+                const int64_t col = (int64_t)x.tn * BN + c * 32;
+                if (row >= M) continue;
+#pragma unroll
+                for (int j = 0; j < 4; j++) {
+                    const int64_t cj = col + j * 8;
+                    const int nc = (int)min((int64_t)8, N - cj);
+                    if (nc <= 0) break;
+                    float f[8];
+#pragma unroll
+                    for (int i = 0; i < 8; i++) f[i] = v[j * 8 + i];
+                    if (epi.part) {  // ldp is a multiple of 8 and the padding is ours
+                        float4 *p = reinterpret_cast<float4 *>(epi.part + ((int64_t)x.split * M + row) * epi.ldp + cj);
+                        p[0] = make_float4(f[0], f[1], f[2], f[3]);
+                        p[1] = make_float4(f[4], f[5], f[6], f[7]);
+                    } else {
+                        finish8<T>(epi, row, cj, nc, f);
+                    }
+                }
+            }
+        }
+    }
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    if (warp == 1)
+        asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(kTmemCols) : "memory");
+}
+
+// The parts of a product split along k, added in order, and the epilogue; a
+// thread for 8 columns of a row.
+template <typename T>
+__global__ void __launch_bounds__(256)
+k_linear_join(int64_t M, int64_t N, int splits, const Epilogue epi) {
+    const int64_t groups = (N + 7) / 8;
+    const int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x;
+    if (i >= M * groups) return;
+    const int64_t row = i / groups, c = (i - row * groups) * 8;
+    float v[8] = {};
+    for (int s = 0; s < splits; s++) {
+        const float4 *p = reinterpret_cast<const float4 *>(epi.part + ((int64_t)s * M + row) * epi.ldp + c);
+        const float4 a = p[0], b = p[1];
+        v[0] += a.x, v[1] += a.y, v[2] += a.z, v[3] += a.w;
+        v[4] += b.x, v[5] += b.y, v[6] += b.z, v[7] += b.w;
+    }
+    finish8<T>(epi, row, c, (int)min((int64_t)8, N - c), v);
+}
+
+// Rows that TMA cannot address (base or row stride not a multiple of 16
+// bytes) copied to rows that it can; 16-bit values.
+__global__ void __launch_bounds__(256)
+k_linear_pack(const uint16_t *__restrict__ src, int64_t ld, int64_t rows, int cols, uint16_t *__restrict__ dst,
+              int64_t ldd) {
+    const int64_t groups = ldd / 8;
+    for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < rows * groups; i += (int64_t)gridDim.x * 256) {
+        const int64_t row = i / groups;
+        const int c = (int)(i - row * groups) * 8;
+        uint32_t u[8];
+#pragma unroll
+        for (int j = 0; j < 8; j++) u[j] = c + j < cols ? src[row * ld + c + j] : 0;
+        *reinterpret_cast<uint4 *>(dst + row * ldd + c) =
+            make_uint4(u[0] | u[1] << 16, u[2] | u[3] << 16, u[4] | u[5] << 16, u[6] | u[7] << 16);
+    }
+}
+
+// dz = dy act'(z) into rows of stride ldo (a multiple of 8; NULL: not written)
+// and, per block row, the columns' float32 sums of it before it is rounded
+// (parts, one row of n a block row; NULL: not formed).  dz is rounded to the
+// inputs' type because it is the tensor cores' operand: it adds one rounding
+// of an input to each product's terms.
+template <typename T>
+__global__ void __launch_bounds__(256)
+k_linear_dz(const T *__restrict__ dy, int64_t lddy, const T *__restrict__ z, int64_t ldz, int act, int64_t m, int n,
+            T *__restrict__ dz, int64_t ldo, float *__restrict__ parts, int vec) {
+    __shared__ float red[8][32][9];
+    const int tx = threadIdx.x & 31, ty = threadIdx.x >> 5;
+    const int64_t c = ((int64_t)blockIdx.x * 32 + tx) * 8;
+    const int nc = (int)min((int64_t)8, (int64_t)n - c);
+    float sum[8] = {};
+    if (nc > 0) {
+        for (int64_t row = (int64_t)blockIdx.y * 8 + ty; row < m; row += (int64_t)gridDim.y * 8) {
+            float v[8], f[8];
+            load8<T>(dy, row * lddy + c, nc, vec, v);
+            if (z) {
+                load8<T>(z, row * ldz + c, nc, vec, f);
+#define SLOPE_CASE(A)                                                          \
+    case A: {                                                                  \
+        _Pragma("unroll") for (int i = 0; i < 8; i++) v[i] *= slope1<A>(f[i]); \
+        break;                                                                 \
+    }
+                switch (act) {
+                    SLOPE_CASE(ACT_RELU)
+                    SLOPE_CASE(ACT_SILU)
+                    SLOPE_CASE(ACT_GELU)
+                    SLOPE_CASE(ACT_GELU_TANH)
+                }
+#undef SLOPE_CASE
+            }
+#pragma unroll
+            for (int i = 0; i < 8; i++) {
+                if (i >= nc) v[i] = 0.f;
+                sum[i] += v[i];
+            }
+            if (dz) {
+                Vec<T, 8> u;
+                u.set(v);
+                u.store(dz + row * ldo + c);
+            }
+        }
+    }
+    if (!parts) return;
+#pragma unroll
+    for (int i = 0; i < 8; i++) red[ty][tx][i] = sum[i];
+    __syncthreads();
+    // thread (ty, tx): column 8 tx + ty of the block's 256
+    float s = 0.f;
+#pragma unroll
+    for (int r = 0; r < 8; r++) s += red[r][tx][ty];
+    const int64_t col = ((int64_t)blockIdx.x * 32 + tx) * 8 + ty;
+    if (col < n) parts[(int64_t)blockIdx.y * n + col] = s;
+}
+
+template <typename T>
+__global__ void __launch_bounds__(256)
+k_linear_db(const float *__restrict__ parts, int nparts, int n, T *__restrict__ db) {
+    __shared__ float red[8][32];
+    const int tx = threadIdx.x & 31, ty = threadIdx.x >> 5;
+    const int c = blockIdx.x * 32 + tx;
+    float s = 0.f;
+    if (c < n)
+        for (int p = ty; p < nparts; p += 8) s += parts[(int64_t)p * n + c];
+    red[ty][tx] = s;
+    __syncthreads();
+    if (ty != 0 || c >= n) return;
+#pragma unroll
+    for (int r = 1; r < 8; r++) s += red[r][tx];
+    db[c] = from_f32<T>(s);
+}
+
+// ---------------------------------------------------------------- host
+
+PFN_cuTensorMapEncodeTiled_v12000 get_encode() {
+    static const PFN_cuTensorMapEncodeTiled_v12000 fn = [] {
+        cudaDriverEntryPointQueryResult q;
+        void *p = nullptr;
+        if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &p, 12000, cudaEnableDefault, &q) !=
+                cudaSuccess ||
+            q != cudaDriverEntryPointSuccess)
+            p = nullptr;
+        return (PFN_cuTensorMapEncodeTiled_v12000)p;
+    }();
+    return fn;
+}
+
+// Map of a matrix of `rows` rows of `cols` contiguous 16-bit values, row
+// stride ld, in boxes of 64 values x box_rows.
+cudaError_t encode(CUtensorMap *map, int type, const void *p, int64_t rows, int64_t cols, int64_t ld, int box_rows) {
+    const PFN_cuTensorMapEncodeTiled_v12000 enc = get_encode();
+    if (!enc) return cudaErrorNotSupported;
+    const cuuint64_t dims[2] = {(cuuint64_t)cols, (cuuint64_t)rows};
+    const cuuint64_t strides[1] = {(cuuint64_t)ld * 2};
+    const cuuint32_t box[2] = {64, (cuuint32_t)box_rows}, estr[2] = {1, 1};
+    const CUresult r = enc(map, type == ZSOLVE_BF16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16,
+                           2, (void *)p, dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
+                           CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                           CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+    return r == CUDA_SUCCESS ? cudaSuccess : cudaErrorInvalidValue;
+}
+
+// A 16-bit matrix as the kernels take it.
+struct Mat {
+    const void *p;
+    int64_t rows, cols, ld;
+    bool tma_ok() const { return ((uintptr_t)p & 15) == 0 && ld % 8 == 0; }
+    size_t packed_values() const { return (size_t)rows * ((cols + 7) / 8 * 8); }
+};
+
+// A product's tile width and parts along k.  256 columns give each operand
+// byte the most MMAs; 128 twice the tiles, where those of 256 would leave SMs
+// without one.  Parts are for what still leaves SMs idle, of 4 k blocks at
+// least, so that a part's loads outweigh the pass that joins them.
+struct Plan {
+    int bn, splits, kblocks;
+};
+Plan plan_of(int64_t M, int64_t N, int64_t K, int num_sms) {
+    Plan p;
+    const int64_t mt = (M + BM - 1) / BM;
+    p.kblocks = (int)((K + BK - 1) / BK);
+    p.bn = mt * ((N + 255) / 256) >= num_sms ? 256 : 128;
+    const int64_t tiles = mt * ((N + p.bn - 1) / p.bn);
+    p.splits = (int)std::max<int64_t>(1, std::min<int64_t>({num_sms / tiles, p.kblocks / 4, 32}));
+    return p;
+}
+int64_t ld_part(int64_t N) { return (N + 7) / 8 * 8; }
+size_t part_values(int64_t M, int64_t N, const Plan &p) {
+    return p.splits > 1 ? (size_t)p.splits * M * ld_part(N) : 0;
+}
+
+template <typename T, int BN, bool A_MN, bool B_MN>
+cudaError_t launch_tc(const CUtensorMap &a, const CUtensorMap &b, int64_t M, int64_t N, const Plan &p,
+                      const Epilogue &epi, zsolve_seq *s) {
+    using C = Cfg<BN>;
+    // once per process (thread-safe initialisation of a local static)
+    static const cudaError_t attr =
+        cudaFuncSetAttribute(k_linear_tc<T, BN, A_MN, B_MN>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM);
+    if (attr != cudaSuccess) return attr;
+    const int64_t total = (M + BM - 1) / BM * ((N + BN - 1) / BN) * p.splits;
+    k_linear_tc<T, BN, A_MN, B_MN><<<(unsigned)std::min<int64_t>(total, s->num_sms), kThreads, C::SMEM, s->st>>>(
+        a, b, M, N, p.kblocks, p.splits, epi, s->d_status);
+    s->launches++;
+    return cudaGetLastError();
+}
+
+// D(i, j) = sum_k A(i, k) B(j, k) and the epilogue; a_mn: A is stored k x M, else M x k.
+template <typename T>
+cudaError_t product(zsolve_seq *s, int type, int64_t M, int64_t N, int64_t K, const Mat &A, bool a_mn, const Mat &B,
+                    bool b_mn, Epilogue epi, float *part) {
+    const Plan p = plan_of(M, N, K, s->num_sms);
+    CUtensorMap ma, mb;
+    cudaError_t e = encode(&ma, type, A.p, A.rows, A.cols, A.ld, a_mn ? 64 : BM);
+    if (e == cudaSuccess) e = encode(&mb, type, B.p, B.rows, B.cols, B.ld, b_mn ? 64 : p.bn);
+    if (e != cudaSuccess) return e;
+    epi.part = p.splits > 1 ? part : nullptr;
+    epi.ldp = ld_part(N);
+#define LIN_GO(AM, BMN)                                                           \
+    e = p.bn == 256 ? launch_tc<T, 256, AM, BMN>(ma, mb, M, N, p, epi, s)         \
+                    : launch_tc<T, 128, AM, BMN>(ma, mb, M, N, p, epi, s)
+    if (!a_mn && !b_mn) LIN_GO(false, false);
+    else if (!a_mn) LIN_GO(false, true);
+    else LIN_GO(true, true);
+#undef LIN_GO
+    if (e != cudaSuccess || p.splits == 1) return e;
+    const int64_t n8 = M * ((N + 7) / 8);
+    k_linear_join<T><<<(unsigned)((n8 + 255) / 256), 256, 0, s->st>>>(M, N, p.splits, epi);
+    s->launches++;
+    return cudaGetLastError();
+}
+
+// A matrix that TMA can address: itself, or its copy at dst.
+cudaError_t packed(zsolve_seq *s, Mat *a, void *dst) {
+    if (a->tma_ok()) return cudaSuccess;
+    const int64_t ldd = (a->cols + 7) / 8 * 8, n = a->rows * (ldd / 8);
+    const unsigned blocks = (unsigned)std::min<int64_t>((n + 255) / 256, (int64_t)s->num_sms * 8);
+    k_linear_pack<<<blocks, 256, 0, s->st>>>((const uint16_t *)a->p, a->ld, a->rows, (int)a->cols, (uint16_t *)dst, ldd);
+    s->launches++;
+    a->p = dst;
+    a->ld = ldd;
+    return cudaGetLastError();
+}
+
+bool vec8(const void *p, int64_t ld) { return !p || (((uintptr_t)p & 15) == 0 && ld % 8 == 0); }
+
+template <typename T>
+int linear_fwd(zsolve_seq *s, int type, int64_t m, int64_t n, int64_t k, Mat x, Mat w, const Epilogue &epi) {
+    const Plan p = plan_of(m, n, k, s->num_sms);
+    uint16_t *xp, *wp;
+    float *part;
+    int st = ZSOLVE_OK;
+    auto carve = [&](void *base) {
+        Carve c(base);
+        xp = x.tma_ok() ? nullptr : c.take<uint16_t>(x.packed_values());
+        wp = w.tma_ok() ? nullptr : c.take<uint16_t>(w.packed_values());
+        part = p.splits > 1 ? c.take<float>(part_values(m, n, p)) : nullptr;
+        return c.at;
+    };
+    const size_t bytes = carve(nullptr);
+    if (bytes) {
+        void *ws = seq_workspace(s, bytes, &st);
+        if (!ws) return st;
+        carve(ws);
+    }
+    SEQ_CU(packed(s, &x, xp));
+    SEQ_CU(packed(s, &w, wp));
+    SEQ_CU(product<T>(s, type, m, n, k, x, false, w, false, epi, part));
+    return ZSOLVE_OK;
+}
+
+constexpr int kDzRows = 64;  // block rows of k_linear_dz at most: parts of db
+
+template <typename T>
+int linear_bwd(zsolve_seq *s, int type, int64_t m, int64_t n, int64_t k, Mat dy, Mat x, Mat w, int act, Mat z, void *dx,
+               int64_t lddx, void *dw, int64_t lddw, void *db) {
+    if (m == 0) {
+        if (dw) SEQ_CU(cudaMemset2DAsync(dw, (size_t)lddw * 2, 0, (size_t)k * 2, (size_t)n, s->st));
+        if (db) SEQ_CU(cudaMemsetAsync(db, 0, (size_t)n * 2, s->st));
+        return ZSOLVE_OK;
+    }
+    const Plan px = plan_of(m, k, n, s->num_sms), pw = plan_of(n, k, m, s->num_sms);
+    const bool has_act = act != ACT_NONE;
+    const bool products = dx || dw;
+    const bool form_dz = products && (has_act || !dy.tma_ok());
+    const int dzrows = (int)std::min<int64_t>((m + 7) / 8, kDzRows);
+    const int64_t ldz8 = (n + 7) / 8 * 8;
+    uint16_t *dzp = nullptr, *xp = nullptr, *wp = nullptr;
+    float *part = nullptr, *sums = nullptr;
+    int st = ZSOLVE_OK;
+    auto carve = [&](void *base) {
+        Carve c(base);
+        dzp = form_dz ? c.take<uint16_t>((size_t)m * ldz8) : nullptr;
+        xp = dw && !x.tma_ok() ? c.take<uint16_t>(x.packed_values()) : nullptr;
+        wp = dx && !w.tma_ok() ? c.take<uint16_t>(w.packed_values()) : nullptr;
+        const size_t parts = std::max(dx ? part_values(m, k, px) : 0, dw ? part_values(n, k, pw) : 0);
+        part = parts ? c.take<float>(parts) : nullptr;
+        sums = db ? c.take<float>((size_t)dzrows * n) : nullptr;
+        return c.at;
+    };
+    const size_t bytes = carve(nullptr);
+    if (bytes) {
+        void *ws = seq_workspace(s, bytes, &st);
+        if (!ws) return st;
+        carve(ws);
+    }
+    if (form_dz || db) {
+        const int vec = vec8(dy.p, dy.ld) && (!has_act || vec8(z.p, z.ld));
+        k_linear_dz<T><<<dim3((unsigned)((n + 255) / 256), dzrows), 256, 0, s->st>>>(
+            (const T *)dy.p, dy.ld, has_act ? (const T *)z.p : nullptr, z.ld, act, m, (int)n, (T *)dzp, ldz8, sums, vec);
+        s->launches++;
+        SEQ_CU(cudaGetLastError());
+    }
+    if (db) {
+        k_linear_db<T><<<(unsigned)((n + 31) / 32), 256, 0, s->st>>>(sums, dzrows, (int)n, (T *)db);
+        s->launches++;
+        SEQ_CU(cudaGetLastError());
+    }
+    Mat dz = dy;
+    if (form_dz) dz.p = dzp, dz.ld = ldz8;
+    Epilogue epi{};
+    if (dx) {
+        SEQ_CU(packed(s, &w, wp));
+        epi.y = dx, epi.ldy = lddx, epi.vec = vec8(dx, lddx);
+        SEQ_CU(product<T>(s, type, m, k, n, dz, false, w, true, epi, part));
+    }
+    if (dw) {
+        SEQ_CU(packed(s, &x, xp));
+        epi.y = dw, epi.ldy = lddw, epi.vec = vec8(dw, lddw);
+        SEQ_CU(product<T>(s, type, n, k, m, dz, true, x, true, epi, part));
+    }
+    return ZSOLVE_OK;
+}
+
+}  // namespace
+
+int zs_linear(zsolve_seq *s, int type, int64_t m, int64_t n, int64_t k, const void *x, int64_t ldx, const void *w,
+              int64_t ldw, const void *b, int act, const void *r, int64_t ldr, void *y, int64_t ldy, void *z,
+              int64_t ldz) {
+    Epilogue epi{};
+    epi.bias = b, epi.r = r, epi.y = y, epi.z = z;
+    epi.ldr = ldr, epi.ldy = ldy, epi.ldz = ldz;
+    epi.act = act;
+    epi.vec = vec8(b, 0) && vec8(r, ldr) && vec8(y, ldy) && vec8(z, ldz);
+    const Mat mx{x, m, k, ldx}, mw{w, n, k, ldw};
+    return type == ZSOLVE_BF16 ? linear_fwd<bf16>(s, type, m, n, k, mx, mw, epi)
+                               : linear_fwd<f16>(s, type, m, n, k, mx, mw, epi);
+}
+
+int zs_linear_bwd(zsolve_seq *s, int type, int64_t m, int64_t n, int64_t k, const void *dy, int64_t lddy,
+                  const void *x, int64_t ldx, const void *w, int64_t ldw, int act, const void *z, int64_t ldz,
+                  void *dx, int64_t lddx, void *dw, int64_t lddw, void *db) {
+    const Mat md{dy, m, n, lddy}, mx{x, m, k, ldx}, mw{w, n, k, ldw}, mz{z, m, n, ldz};
+    return type == ZSOLVE_BF16
+               ? linear_bwd<bf16>(s, type, m, n, k, md, mx, mw, act, mz, dx, lddx, dw, lddw, db)
+               : linear_bwd<f16>(s, type, m, n, k, md, mx, mw, act, mz, dx, lddx, dw, lddw, db);
+}

@@ -75,6 +75,18 @@ int check_device(zsolve_seq *s) {
     return ZSOLVE_OK;
 }
 
+int check_linear(zsolve_seq *s, int type, int act, int64_t m, int64_t n, int64_t k) {
+    if (type != ZSOLVE_BF16 && type != ZSOLVE_F16)
+        return seq_fail(s, ZSOLVE_EINVAL, "type %d: ZSOLVE_BF16 or ZSOLVE_F16", type);
+    if (act < ZSOLVE_ACT_NONE || act > ZSOLVE_ACT_GELU_TANH) return seq_fail(s, ZSOLVE_EINVAL, "act = %d", act);
+    const int64_t most = 1 << 24;  // rows times tiles stay within 32 bits
+    if (m < 0 || m > 0x7fffff00 || n < 1 || n > most || k < 1 || k > most ||
+        ((m + 127) / 128) * ((n + 127) / 128) > 0x3ffffff || ((n + 127) / 128) * ((k + 127) / 128) > 0x3ffffff ||
+        ((m + 127) / 128) * ((k + 127) / 128) > 0x3ffffff)
+        return seq_fail(s, ZSOLVE_EINVAL, "m = %lld, n = %lld, k = %lld", (long long)m, (long long)n, (long long)k);
+    return ZSOLVE_OK;
+}
+
 }  // namespace
 
 extern "C" {
@@ -175,6 +187,48 @@ int zsolve_layernorm_bwd(zsolve_seq *s, int type, int wtype, int64_t rows, int64
     SEQ_CU(zs_launch_layernorm_bwd(type, wtype == ZSOLVE_F32, rows, d, dy, lddy, x, ldx, mean, rstd, w, dx, lddx, dw,
                                    db, parts, s->num_sms, s->st, &s->launches));
     return ZSOLVE_OK;
+}
+
+int zsolve_seq_check(zsolve_seq *s) {
+    if (!s) return ZSOLVE_EINVAL;
+    int st = check_device(s);
+    if (st != ZSOLVE_OK) return st;
+    unsigned word = 0;
+    SEQ_CU(cudaMemcpyAsync(&word, s->d_status, sizeof(word), cudaMemcpyDeviceToHost, s->st));
+    SEQ_CU(cudaStreamSynchronize(s->st));
+    if (!word) return ZSOLVE_OK;
+    SEQ_CU(cudaMemsetAsync(s->d_status, 0, sizeof(word), s->st));
+    return seq_fail(s, ZSOLVE_ETIMEOUT, "a bounded device-side wait gave up");
+}
+
+int zsolve_linear(zsolve_seq *s, int type, int64_t m, int64_t n, int64_t k, const void *x, int64_t ldx, const void *w,
+                  int64_t ldw, const void *b, int act, const void *r, int64_t ldr, void *y, int64_t ldy, void *z,
+                  int64_t ldz) {
+    if (!s) return ZSOLVE_EINVAL;
+    int st = check_linear(s, type, act, m, n, k);
+    if (st != ZSOLVE_OK || m == 0) return st;
+    if (!x || !w || !y) return seq_fail(s, ZSOLVE_EINVAL, "NULL x, w or y");
+    if (ldx < k || ldw < k || ldy < n || (r && ldr < n) || (z && ldz < n))
+        return seq_fail(s, ZSOLVE_EINVAL, "a row stride is below its row's length");
+    st = check_device(s);
+    if (st != ZSOLVE_OK) return st;
+    return zs_linear(s, type, m, n, k, x, ldx, w, ldw, b, act, r, ldr, y, ldy, z, ldz);
+}
+
+int zsolve_linear_bwd(zsolve_seq *s, int type, int64_t m, int64_t n, int64_t k, const void *dy, int64_t lddy,
+                      const void *x, int64_t ldx, const void *w, int64_t ldw, int act, const void *z, int64_t ldz,
+                      void *dx, int64_t lddx, void *dw, int64_t lddw, void *db) {
+    if (!s) return ZSOLVE_EINVAL;
+    int st = check_linear(s, type, act, m, n, k);
+    if (st != ZSOLVE_OK) return st;
+    if (m > 0 && (!dy || (dw && !x) || (dx && !w) || (act != ZSOLVE_ACT_NONE && !z)))
+        return seq_fail(s, ZSOLVE_EINVAL, "NULL dy, x, w or z that the gradients asked for need");
+    if ((m > 0 && (lddy < n || (dw && ldx < k) || (dx && (ldw < k || lddx < k)) ||
+                   (act != ZSOLVE_ACT_NONE && ldz < n))) || (dw && lddw < k))
+        return seq_fail(s, ZSOLVE_EINVAL, "a row stride is below its row's length");
+    st = check_device(s);
+    if (st != ZSOLVE_OK) return st;
+    return zs_linear_bwd(s, type, m, n, k, dy, lddy, x, ldx, w, ldw, act, z, ldz, dx, lddx, dw, lddw, db);
 }
 
 }  // extern "C"

@@ -172,3 +172,11 @@ cudaError_t zs_launch_layernorm_bwd(int type, int wf32, int64_t rows, int64_t d,
                                     const void *x, int64_t ldx, const float *mean, const float *rstd, const void *w,
                                     void *dx, int64_t lddx, void *dw, void *db, float *parts, int num_sms,
                                     cudaStream_t st, int64_t *launches);
+
+// linear.cu: the whole call (arguments checked), a ZSOLVE_* status.
+int zs_linear(zsolve_seq *s, int type, int64_t m, int64_t n, int64_t k, const void *x, int64_t ldx, const void *w,
+              int64_t ldw, const void *b, int act, const void *r, int64_t ldr, void *y, int64_t ldy, void *z,
+              int64_t ldz);
+int zs_linear_bwd(zsolve_seq *s, int type, int64_t m, int64_t n, int64_t k, const void *dy, int64_t lddy,
+                  const void *x, int64_t ldx, const void *w, int64_t ldw, int act, const void *z, int64_t ldz,
+                  void *dx, int64_t lddx, void *dw, int64_t lddw, void *db);

@@ -14,6 +14,8 @@ ZSOLVE_F32 = 0
 ZSOLVE_BF16 = 1
 ZSOLVE_F16 = 2
 
+ZSOLVE_ACTS = {"none": 0, "relu": 1, "silu": 2, "gelu": 3, "gelu_tanh": 4}
+
 
 def _types():
     import torch
@@ -106,6 +108,10 @@ def zsolve_seq_last_error(seq) -> str:
     return _lib.zsolve_seq_last_error(seq).decode()
 
 
+def zsolve_seq_check(seq) -> None:
+    _check_seq(seq, _lib.zsolve_seq_check(seq))
+
+
 def zsolve_seq_destroy(seq) -> None:
     _lib.zsolve_seq_destroy(seq)
 
@@ -145,6 +151,43 @@ def zsolve_layernorm_bwd(seq, dy, x, mean, rstd, w, dx, dw=None, db=None) -> Non
                                               lddx, _vector(dw, "dw", d, wt), _vector(db, "db", d, wt)))
 
 
+def _act(act) -> int:
+    if act not in ZSOLVE_ACTS:
+        raise ValueError(f"act: expected one of {', '.join(ZSOLVE_ACTS)}, got {act!r}")
+    return ZSOLVE_ACTS[act]
+
+
+def _optional_rows(t, name, dtype, shape):
+    """(pointer, row stride) of a matrix, or zeros for None."""
+    if t is None:
+        return 0, 0
+    p, _, _, ld = _rows(t, name, dtype, shape)
+    return p, ld
+
+
+def zsolve_linear(seq, x, w, b, act, r, y, z=None) -> None:
+    """y <- act(x w^T + b) + r; x (..., k), w (n, k), b (n,) or None, r and y (..., n), r or None; z: as y, or None."""
+    xp, m, k, ldx = _rows(x, "x")
+    wp, n, _, ldw = _rows(w, "w", x.dtype, (w.shape[0], k))
+    rp, ldr = _optional_rows(r, "r", x.dtype, (m, n))
+    yp, _, _, ldy = _rows(y, "y", x.dtype, (m, n))
+    zp, ldz = _optional_rows(z, "z", x.dtype, (m, n))
+    _check_seq(seq, _lib.zsolve_linear(seq, _type(x, "x"), m, n, k, xp, ldx, wp, ldw, _vector(b, "b", n, x.dtype),
+                                       _act(act), rp, ldr, yp, ldy, zp, ldz))
+
+
+def zsolve_linear_bwd(seq, dy, x, w, act, z, dx=None, dw=None, db=None) -> None:
+    """dx, dw and db (shapes of x, w and the bias; None: not formed) from dy; z: as zsolve_linear kept it."""
+    xp, m, k, ldx = _rows(x, "x")
+    wp, n, _, ldw = _rows(w, "w", x.dtype, (w.shape[0], k))
+    dyp, _, _, lddy = _rows(dy, "dy", x.dtype, (m, n))
+    zp, ldz = _optional_rows(z, "z", x.dtype, (m, n))
+    dxp, lddx = _optional_rows(dx, "dx", x.dtype, (m, k))
+    dwp, lddw = _optional_rows(dw, "dw", x.dtype, (n, k))
+    _check_seq(seq, _lib.zsolve_linear_bwd(seq, _type(x, "x"), m, n, k, dyp, lddy, xp, ldx, wp, ldw, _act(act), zp,
+                                           ldz, dxp, lddx, dwp, lddw, _vector(db, "db", n, x.dtype)))
+
+
 class Seq:
     """Owns one handle of the sequence-layer operators; runs on torch's current stream.
 
@@ -182,6 +225,26 @@ class Seq:
         dx = torch.empty(x.shape, dtype=x.dtype, device=x.device)
         dw, db = torch.empty((2, x.shape[-1]), dtype=x.dtype if w is None else w.dtype, device=x.device).unbind(0)
         zsolve_layernorm_bwd(self.seq, dy, x, mean, rstd, w, dx, dw, db)
+        return dx, dw, db
+
+    def linear(self, x, w, b=None, act="none", r=None, keep=False):
+        """y = act(x w^T + b) + r; with keep=True (y, z), z for linear_bwd."""
+        import torch
+        self._on_stream()
+        shape = x.shape[:-1] + w.shape[:1]
+        y = torch.empty(shape, dtype=x.dtype, device=x.device)
+        z = torch.empty(shape, dtype=x.dtype, device=x.device) if keep else None
+        zsolve_linear(self.seq, x, w, b, act, r, y, z)
+        return (y, z) if keep else y
+
+    def linear_bwd(self, dy, x, w, z=None, act="none"):
+        """Returns (dx, dw, db); z as linear(keep=True) returned it (not needed without an activation)."""
+        import torch
+        self._on_stream()
+        dx = torch.empty(x.shape, dtype=x.dtype, device=x.device)
+        dw = torch.empty(w.shape, dtype=x.dtype, device=x.device)
+        db = torch.empty(w.shape[:1], dtype=x.dtype, device=x.device)
+        zsolve_linear_bwd(self.seq, dy, x, w, act, z, dx, dw, db)
         return dx, dw, db
 
     def close(self):

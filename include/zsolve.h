@@ -533,6 +533,39 @@ int zsolve_linear_bwd(zsolve_seq *seq, int type, int64_t m, int64_t n, int64_t k
                       const void *x, int64_t ldx, const void *w, int64_t ldw, int act, const void *z, int64_t ldz,
                       void *dx, int64_t lddx, void *dw, int64_t lddw, void *db);
 
+/* The gated delta rule.  Each value head of a sequence has a state S (dk x dv,
+ * float32), and every token t, with a_t = exp(g_t),
+ *   u_t = beta_t (v_t - a_t S^T k_t),  S <- a_t S + k_t u_t^T,  o_t = scale S^T q_t.
+ * Value head h uses key head h / (hv / hk).  g_t = -infinity empties the state. */
+#define ZSOLVE_DELTA_MAX_DK 128
+
+typedef struct {
+    int type;               /* of q, k, v and o: ZSOLVE_F32, ZSOLVE_BF16 or ZSOLVE_F16 */
+    int hk, hv;             /* key and value heads; hv is a multiple of hk */
+    int dk, dv;             /* their sizes; dk <= ZSOLVE_DELTA_MAX_DK */
+    int nseq;               /* sequences */
+    int64_t tokens;         /* of all sequences together, one after the other */
+    const int64_t *offsets; /* device, nseq + 1: sequence i holds the tokens offsets[i] .. offsets[i+1]-1,
+                               ascending within 0 .. tokens; equal ones are an empty sequence.
+                               NULL: every sequence has tokens / nseq */
+    const void *q, *k, *v;  /* tokens x heads x d; the heads of a token are packed */
+    int64_t ldq, ldk, ldv;  /* distance of two tokens, elements */
+    const float *g, *beta;  /* tokens x hv, packed: log decays and step sizes */
+    const float *s0;        /* nseq x hv x dk x dv: the states to start from (NULL: zero) */
+    double scale;
+} zsolve_delta_args;
+
+/* o (tokens x hv x dv, token stride ldo) and the states after the last tokens,
+ * s (as s0, and may be s0; NULL: not written).  In chunks of 64 tokens, whose
+ * products run on the tensor cores at float32 accuracy (3xTF32; o itself, where
+ * it is rounded to 16 bits, from tf32 products); sequences of a few tokens at
+ * most go token by token (zsolve_delta_step). */
+int zsolve_delta(zsolve_seq *seq, const zsolve_delta_args *args, void *o, int64_t ldo, float *s);
+
+/* The same token by token in float32, one kernel and no workspace: for
+ * decoding, one or a few tokens a sequence. */
+int zsolve_delta_step(zsolve_seq *seq, const zsolve_delta_args *args, void *o, int64_t ldo, float *s);
+
 /* Static string for a status code.  No passage: error reporting of the library. */
 const char *zsolve_strerror(int status);
 

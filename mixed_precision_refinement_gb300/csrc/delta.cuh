@@ -1,0 +1,209 @@
+// The gated delta rule's shared parts: geometry of the chunks, the float32-class
+// products on the tensor cores, operand fragments in shared memory.
+//
+// Per value head, with the state S (dk x dv), a_t = exp g_t and
+//   S_t = a_t S_{t-1} + k_t u_t^T,  u_t = beta_t (v_t - a_t S_{t-1}^T k_t),  o_t = scale S_t^T q_t,
+// a chunk of 64 tokens with b_i = g_1 + ... + g_i, c_i = exp b_i, e_ij = exp(b_i - b_j) is
+//   A_ij = beta_i (k_i . k_j) e_ij (j < i),  T = (I + A)^-1,  X = beta (V - c K S),  U = T X,
+//   O = scale (c Q S) + P U,  P_ij = scale (q_i . k_j) e_ij (j <= i),
+//   S' = c_64 S + (e_64,j K)^T U
+// : a unit lower-triangular solve and a rank-64 update, the two steps of the
+// blocked factorisation.
+//
+// States, U and gradients of the gates are float32 results, so every product
+// that feeds them keeps float32 accuracy on the tensor cores: an operand that
+// is not exact in tf32 (float32 inputs, S, T, U, X) is split into a tf32 hi
+// part and a tf32 lo part; the product is hi.hi + hi.lo + lo.hi, and
+// hi.exact + lo.exact where the other operand is a bfloat16 or float16 input
+// (exact in tf32).  The lo.lo term is below float32 rounding.  The
+// instructions are mma.sync m16n8k8: a chunk's matrices are 64 wide and each
+// step waits for the one before, so what counts is the latency from one
+// product to the next, and register operands hand results on without a trip
+// through TMEM (S^T, kept as the accumulator of S'^T = ... + U^T K, is the
+// next chunk's A operand as it stands).
+#pragma once
+
+#include "seq.cuh"
+
+namespace zs {
+
+constexpr int kChunk = 64;  // tokens of a chunk
+
+// Inputs of a call and the chunk table.
+struct DeltaGeom {
+    const void *q, *k, *v;         // tokens x heads x d, token strides ld*
+    int64_t ldq, ldk, ldv;
+    const float *g, *beta;         // tokens x hv
+    int hk, hv, dk, dv, nseq;
+    int64_t tokens;
+    float scale;
+    const int *first;              // nseq + 1: first chunk of each sequence
+    const int2 *seq;               // nseq: first token and length
+    const int2 *chunk;             // per chunk: first token, tokens (1..64); 0 tokens: unused
+    int nchunks;                   // room in the tables
+};
+
+// Per chunk and value head, what does not depend on the state (float32):
+// T (64 x 64), P (64 x 64) and the vectors c_i, e_64,i, beta_i (64 each).
+struct DeltaTerms {
+    float *t, *p, *vec;
+};
+constexpr int kVec = 3 * kChunk;
+
+// ---------------------------------------------------------------- products
+
+__device__ __forceinline__ uint32_t tf32(float x) {
+    uint32_t r;
+    asm("cvt.rna.tf32.f32 %0, %1;" : "=r"(r) : "f"(x));
+    return r;
+}
+
+__device__ __forceinline__ void mma8(float (&c)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+    asm volatile(
+        "mma.sync.aligned.m16n8k8.row.col.f32.tf32.tf32.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
+        "{%0, %1, %2, %3};"
+        : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+        : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+
+// An A operand of 16 x 8 in two tf32 parts.  The instruction's k slots t and
+// t + 4 hold the columns 2t and 2t + 1 (any order serves as long as A and B
+// agree): the accumulator's columns, so an accumulator is an A operand, and a
+// pair of neighbours in memory.
+struct SplitA {
+    uint32_t hi[4], lo[4];
+    // c: (g, 2t), (g, 2t+1), (g+8, 2t), (g+8, 2t+1)
+    __device__ __forceinline__ void set(float c0, float c1, float c2, float c3) {
+        const float x[4] = {c0, c2, c1, c3};
+#pragma unroll
+        for (int i = 0; i < 4; i++) {
+            hi[i] = tf32(x[i]);
+            lo[i] = tf32(x[i] - __uint_as_float(hi[i]));
+        }
+    }
+    __device__ __forceinline__ void set(const float (&c)[4]) { set(c[0], c[1], c[2], c[3]); }
+};
+
+// c += A B for one 16 x 8 x 8 step, b = (B(2t, g), B(2t+1, g)); EXACT: b is
+// exact in tf32; HALF: A's hi part alone (results that are rounded to 16 bits).
+template <bool EXACT, bool HALF = false>
+__device__ __forceinline__ void mma_split(float (&c)[4], const SplitA &a, float2 b) {
+    if (EXACT) {
+        const uint32_t b0 = __float_as_uint(b.x), b1 = __float_as_uint(b.y);
+        if (!HALF) mma8(c, a.lo, b0, b1);
+        mma8(c, a.hi, b0, b1);
+    } else {
+        const uint32_t b0 = tf32(b.x), b1 = tf32(b.y);
+        if (!HALF) {
+            mma8(c, a.lo, b0, b1);
+            mma8(c, a.hi, tf32(b.x - __uint_as_float(b0)), tf32(b.y - __uint_as_float(b1)));
+        }
+        mma8(c, a.hi, b0, b1);
+    }
+}
+
+// ---------------------------------------------------------------- fragments
+
+// Row stride (values) of a tile of D columns in shared memory: 16 bytes more
+// for 16-bit values, 32 for float32, so that the eight rows of a fragment lie
+// in different banks.
+template <typename T>
+__host__ __device__ constexpr int tile_ld(int d) {
+    return d + 8;
+}
+
+// Four fragments of 8 x 8 from a tile X of row stride LD.
+//   row: f[i] = (X(r0 + g, c0 + 8 i + 2t), X(r0 + g, c0 + 8 i + 2t + 1))
+//   col: f[i] = (X(r0 + 2t, c0 + 8 i + g), X(r0 + 2t + 1, c0 + 8 i + g))
+template <typename T, int LD, bool COL>
+__device__ __forceinline__ void frag4(const T *x, int r0, int c0, float2 (&f)[4]) {
+    const int lane = threadIdx.x & 31;
+    if constexpr (sizeof(T) == 2) {
+        const uint32_t a = (uint32_t)__cvta_generic_to_shared(x + (r0 + (lane & 7)) * LD + c0 + 8 * (lane >> 3));
+        uint32_t u[4];
+        if (COL)
+            asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0, %1, %2, %3}, [%4];"
+                         : "=r"(u[0]), "=r"(u[1]), "=r"(u[2]), "=r"(u[3])
+                         : "r"(a)
+                         : "memory");
+        else
+            asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0, %1, %2, %3}, [%4];"
+                         : "=r"(u[0]), "=r"(u[1]), "=r"(u[2]), "=r"(u[3])
+                         : "r"(a)
+                         : "memory");
+#pragma unroll
+        for (int i = 0; i < 4; i++) f[i] = unpack2<T>(u[i]);
+    } else {
+        const int g = lane >> 2, t = lane & 3;
+#pragma unroll
+        for (int i = 0; i < 4; i++) {
+            if (COL)
+                f[i] = make_float2(x[(r0 + 2 * t) * LD + c0 + 8 * i + g], x[(r0 + 2 * t + 1) * LD + c0 + 8 * i + g]);
+            else
+                f[i] = *reinterpret_cast<const float2 *>(x + (r0 + g) * LD + c0 + 8 * i + 2 * t);
+        }
+    }
+}
+
+// ---------------------------------------------------------------- loads
+
+__device__ __forceinline__ void cp_async16(void *dst, const void *src, int bytes) {
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"((uint32_t)__cvta_generic_to_shared(dst)),
+                 "l"(src), "r"(bytes)
+                 : "memory");
+}
+__device__ __forceinline__ void cp_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N>
+__device__ __forceinline__ void cp_wait() {
+    asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+}
+
+// A tile of 64 rows x D columns, rows of `d` values (d <= D) at stride ld in
+// memory, n rows of them; zeros elsewhere.  vec: 16-byte copies are allowed
+// (pointer, stride and d are multiples of 16 bytes).
+template <typename T, int D, int NT>
+__device__ __forceinline__ void load_tile(T *dst, const T *src, int64_t ld, int n, int d, int vec) {
+    constexpr int LD = tile_ld<T>(D);
+    if (vec) {
+        constexpr int VE = 16 / (int)sizeof(T), PER = D / VE;
+        for (int i = threadIdx.x; i < kChunk * PER; i += NT) {
+            const int r = i / PER, c = (i - r * PER) * VE;
+            const bool in = r < n && c < d;
+            cp_async16(dst + r * LD + c, src + (in ? r * ld + c : 0), in ? 16 : 0);
+        }
+    } else {
+        for (int i = threadIdx.x; i < kChunk * D; i += NT) {
+            const int r = i / D, c = i - r * D;
+            dst[r * LD + c] = r < n && c < d ? src[r * ld + c] : from_f32<T>(0.f);
+        }
+    }
+}
+
+// A packed 64 x 64 float32 matrix into rows of stride 72.
+constexpr int kLdT = kChunk + 8;
+template <int NT>
+__device__ __forceinline__ void load_square(float *dst, const float *src) {
+    for (int i = threadIdx.x; i < kChunk * kChunk / 4; i += NT) {
+        const int r = i >> 4, c = (i & 15) * 4;
+        cp_async16(dst + r * kLdT + c, src + r * kChunk + c, 16);
+    }
+}
+
+}  // namespace zs
+
+// ---------------------------------------------------------------- launchers
+
+// delta.cu
+cudaError_t zs_launch_delta_plan(const int64_t *offsets, int nseq, int64_t tokens, int nchunks, int *first, int2 *seq,
+                                 int2 *chunk, cudaStream_t st, int64_t *launches);
+cudaError_t zs_launch_delta_terms(int type, const zs::DeltaGeom &g, const zs::DeltaTerms &t, cudaStream_t st,
+                                  int64_t *launches);
+// The recurrence over the chunks.  o (NULL: not formed), sn (the last states;
+// NULL: not written); states, us (NULL: not kept): the state each chunk
+// starts from (per chunk and value head dk x dv) and U (64 x dv).
+cudaError_t zs_launch_delta_chain(int type, const zs::DeltaGeom &g, const zs::DeltaTerms &t, const float *s0, void *o,
+                                  int64_t ldo, float *sn, float *states, float *us, cudaStream_t st,
+                                  int64_t *launches);
+// Token by token (delta_step.cu): every sequence's tokens one after the other.
+cudaError_t zs_launch_delta_step(int type, const zs::DeltaGeom &g, const int64_t *offsets, const float *s0, void *o,
+                                 int64_t ldo, float *sn, cudaStream_t st, int64_t *launches);

@@ -1,5 +1,6 @@
 // The C-ABI of the sequence-layer operators: the handle, its workspace, and
 // the argument checks in front of the kernels.
+#include "delta.cuh"
 #include "seq.cuh"
 
 #include <cmath>
@@ -86,6 +87,77 @@ int check_linear(zsolve_seq *s, int type, int act, int64_t m, int64_t n, int64_t
         return seq_fail(s, ZSOLVE_EINVAL, "m = %lld, n = %lld, k = %lld", (long long)m, (long long)n, (long long)k);
     return ZSOLVE_OK;
 }
+
+// The longest a sequence of the call can be.
+int64_t longest(const zsolve_delta_args *a) {
+    return a->nseq == 0 ? 0 : a->offsets ? a->tokens : a->tokens / a->nseq;
+}
+
+// Up to so many tokens a sequence, one kernel that takes them one by one
+// (about a microsecond each) is sooner done than the chunked form's three.
+constexpr int64_t kStepTokens = 8;
+
+// The arguments of a delta rule call, checked, as the kernels take them.
+int check_delta(zsolve_seq *s, const zsolve_delta_args *a, const void *o, int64_t ldo, zs::DeltaGeom *g) {
+    if (!a) return seq_fail(s, ZSOLVE_EINVAL, "NULL arguments");
+    if (!zs::type_ok(a->type)) return seq_fail(s, ZSOLVE_EINVAL, "type %d", a->type);
+    if (a->hk < 1 || a->hv < 1 || a->hv % a->hk != 0 || a->hk > 65535)
+        return seq_fail(s, ZSOLVE_EINVAL, "hk = %d, hv = %d: hv is a multiple of hk", a->hk, a->hv);
+    if (a->dk < 1 || a->dk > ZSOLVE_DELTA_MAX_DK || a->dv < 1 || a->dv > 65536)
+        return seq_fail(s, ZSOLVE_EINVAL, "dk = %d outside 1..%d or dv = %d outside 1..65536", a->dk, ZSOLVE_DELTA_MAX_DK, a->dv);
+    if (a->nseq < 0 || a->tokens < 0 || a->tokens > 0x7fffff00 || (int64_t)a->nseq * a->hv > 0x7fffffff ||
+        (a->nseq == 0 && a->tokens > 0) || (!a->offsets && a->nseq > 0 && a->tokens % a->nseq != 0))
+        return seq_fail(s, ZSOLVE_EINVAL, "nseq = %d, tokens = %lld", a->nseq, (long long)a->tokens);
+    if (!std::isfinite(a->scale)) return seq_fail(s, ZSOLVE_EINVAL, "scale = %g", a->scale);
+    if (a->tokens > 0) {
+        if (!a->q || !a->k || !a->v || !a->g || !a->beta || !o)
+            return seq_fail(s, ZSOLVE_EINVAL, "NULL q, k, v, g, beta or output");
+        const int64_t rk = (int64_t)a->hk * a->dk, rv = (int64_t)a->hv * a->dv;
+        if (a->ldq < rk || a->ldk < rk || a->ldv < rv || ldo < rv)
+            return seq_fail(s, ZSOLVE_EINVAL, "a token stride is below its heads' values");
+    }
+    *g = zs::DeltaGeom{a->q, a->k, a->v, a->ldq, a->ldk, a->ldv, a->g, a->beta, a->hk, a->hv, a->dk, a->dv, a->nseq,
+                       a->tokens, (float)a->scale, nullptr, nullptr, nullptr, 0};
+    return ZSOLVE_OK;
+}
+
+// The chunked form's workspace.
+struct DeltaWork {
+    int nchunks = 0;
+    int *first = nullptr;
+    int2 *seq = nullptr, *chunk = nullptr;
+    zs::DeltaTerms terms{};
+
+    void carve(zs::Carve &c, const zsolve_delta_args *a, bool out) {
+        const size_t slots = (size_t)nchunks * a->hv, sq = (size_t)zs::kChunk * zs::kChunk;
+        first = c.take<int>((size_t)a->nseq + 1);
+        seq = c.take<int2>((size_t)a->nseq);
+        chunk = c.take<int2>((size_t)nchunks);
+        terms.t = c.take<float>(slots * sq);
+        terms.p = out ? c.take<float>(slots * sq) : nullptr;
+        terms.vec = c.take<float>(slots * zs::kVec);
+    }
+    int place(zsolve_seq *s, const zsolve_delta_args *a, bool out) {
+        // a sequence's last chunk may be short: one more each at most
+        const int64_t most = a->tokens / zs::kChunk + a->nseq;
+        if (most > 0x7fffffff / zs::kChunk) return seq_fail(s, ZSOLVE_EINVAL, "too many chunks");
+        nchunks = (int)most;
+        zs::Carve size(nullptr);
+        carve(size, a, out);
+        int st = ZSOLVE_OK;
+        void *ws = zs::seq_workspace(s, size.at, &st);
+        if (!ws) return st;
+        zs::Carve c(ws);
+        carve(c, a, out);
+        return ZSOLVE_OK;
+    }
+    void bind(zs::DeltaGeom *g) const {
+        g->first = first;
+        g->seq = seq;
+        g->chunk = chunk;
+        g->nchunks = nchunks;
+    }
+};
 
 }  // namespace
 
@@ -229,6 +301,38 @@ int zsolve_linear_bwd(zsolve_seq *s, int type, int64_t m, int64_t n, int64_t k, 
     st = check_device(s);
     if (st != ZSOLVE_OK) return st;
     return zs_linear_bwd(s, type, m, n, k, dy, lddy, x, ldx, w, ldw, act, z, ldz, dx, lddx, dw, lddw, db);
+}
+
+int zsolve_delta(zsolve_seq *s, const zsolve_delta_args *a, void *o, int64_t ldo, float *sn) {
+    if (!s) return ZSOLVE_EINVAL;
+    zs::DeltaGeom g;
+    int st = check_delta(s, a, o, ldo, &g);
+    if (st != ZSOLVE_OK || a->nseq == 0) return st;
+    st = check_device(s);
+    if (st != ZSOLVE_OK) return st;
+    if (longest(a) <= kStepTokens) {
+        SEQ_CU(zs_launch_delta_step(a->type, g, a->offsets, a->s0, o, ldo, sn, s->st, &s->launches));
+        return ZSOLVE_OK;
+    }
+    DeltaWork w;
+    st = w.place(s, a, true);
+    if (st != ZSOLVE_OK) return st;
+    w.bind(&g);
+    SEQ_CU(zs_launch_delta_plan(a->offsets, a->nseq, a->tokens, w.nchunks, w.first, w.seq, w.chunk, s->st, &s->launches));
+    SEQ_CU(zs_launch_delta_terms(a->type, g, w.terms, s->st, &s->launches));
+    SEQ_CU(zs_launch_delta_chain(a->type, g, w.terms, a->s0, o, ldo, sn, nullptr, nullptr, s->st, &s->launches));
+    return ZSOLVE_OK;
+}
+
+int zsolve_delta_step(zsolve_seq *s, const zsolve_delta_args *a, void *o, int64_t ldo, float *sn) {
+    if (!s) return ZSOLVE_EINVAL;
+    zs::DeltaGeom g;
+    int st = check_delta(s, a, o, ldo, &g);
+    if (st != ZSOLVE_OK || a->nseq == 0) return st;
+    st = check_device(s);
+    if (st != ZSOLVE_OK) return st;
+    SEQ_CU(zs_launch_delta_step(a->type, g, a->offsets, a->s0, o, ldo, sn, s->st, &s->launches));
+    return ZSOLVE_OK;
 }
 
 }  // extern "C"

@@ -188,6 +188,78 @@ def zsolve_linear_bwd(seq, dy, x, w, act, z, dx=None, dw=None, db=None) -> None:
                                            ldz, dxp, lddx, dwp, lddw, _vector(db, "db", n, x.dtype)))
 
 
+class zsolve_delta_args(ctypes.Structure):
+    _fields_ = [("type", ctypes.c_int), ("hk", ctypes.c_int), ("hv", ctypes.c_int), ("dk", ctypes.c_int),
+                ("dv", ctypes.c_int), ("nseq", ctypes.c_int), ("tokens", ctypes.c_int64),
+                ("offsets", ctypes.c_void_p), ("q", ctypes.c_void_p), ("k", ctypes.c_void_p),
+                ("v", ctypes.c_void_p), ("ldq", ctypes.c_int64), ("ldk", ctypes.c_int64), ("ldv", ctypes.c_int64),
+                ("g", ctypes.c_void_p), ("beta", ctypes.c_void_p), ("s0", ctypes.c_void_p),
+                ("scale", ctypes.c_double)]
+
+
+def _tokens(t, name, dtype=None, shape=None):
+    """(pointer, tokens, heads, d, token stride) of a tensor (tokens, heads, d) or (sequences, tokens, heads, d)."""
+    _cuda(t, name)
+    if dtype is not None and t.dtype != dtype:
+        raise TypeError(f"{name}: expected {dtype}, got {t.dtype}")
+    if t.dim() == 4:
+        t = t.flatten(0, 1) if t.numel() == 0 else t.view((-1,) + t.shape[2:])
+    if t.dim() != 3:
+        raise ValueError(f"{name}: expected tokens x heads x values, got {tuple(t.shape)}")
+    n, h, d = t.shape
+    if shape is not None and (n, h, d) != shape:
+        raise ValueError(f"{name}: expected {shape[0]} x {shape[1]} x {shape[2]}, got {n} x {h} x {d}")
+    if t.numel() and ((d > 1 and t.stride(2) != 1) or (h > 1 and t.stride(1) != d)):
+        raise ValueError(f"{name}: the heads of a token must be packed")
+    return t.data_ptr(), n, h, d, t.stride(0) if n > 1 else h * d
+
+
+def _delta_args(q, k, v, g, beta, s0, offsets, scale):
+    import torch
+    qp, n, hk, dk, ldq = _tokens(q, "q")
+    kp, _, _, _, ldk = _tokens(k, "k", q.dtype, (n, hk, dk))
+    vp, _, hv, dv, ldv = _tokens(v, "v", q.dtype)
+    if v.shape[:-2] != q.shape[:-2]:
+        raise ValueError(f"v: expected the tokens of q, {tuple(q.shape[:-2])}, got {tuple(v.shape[:-2])}")
+    if offsets is not None:
+        nseq = offsets.numel() - 1
+        if nseq < 0:
+            raise ValueError("offsets: expected one more than the sequences")
+    else:
+        nseq = q.shape[0] if q.dim() == 4 else 1
+    a = zsolve_delta_args(_type(q, "q"), hk, hv, dk, dv, nseq, n,
+                          _vector(offsets, "offsets", nseq + 1, torch.int64) or None, qp, kp, vp, ldq, ldk, ldv,
+                          _vector(g, "g", n * hv, torch.float32), _vector(beta, "beta", n * hv, torch.float32),
+                          _vector(s0, "s0", nseq * hv * dk * dv, torch.float32),
+                          dk ** -0.5 if scale is None else scale)
+    return a
+
+
+def zsolve_delta(seq, q, k, v, g, beta, o, s=None, s0=None, offsets=None, scale=None) -> None:
+    """o, s <- the gated delta rule over whole sequences.
+
+    q, k: (tokens, hk, dk), v, o: (tokens, hv, dv), g, beta: float32 (tokens, hv); or with two leading
+    dimensions, sequences x tokens.  offsets: int64 (sequences + 1,) for sequences of different lengths in the
+    packed form (without: one sequence).  s0, s: float32 (sequences, hv, dk, dv) or None; s may be s0.
+    scale: 1 / sqrt(dk) unless given.
+    """
+    a = _delta_args(q, k, v, g, beta, s0, offsets, scale)
+    op, _, _, _, ldo = _tokens(o, "o", q.dtype, (a.tokens, a.hv, a.dv))
+    _check_seq(seq, _lib.zsolve_delta(seq, ctypes.byref(a), op, ldo, _state(s, a)))
+
+
+def zsolve_delta_step(seq, q, k, v, g, beta, o, s=None, s0=None, offsets=None, scale=None) -> None:
+    """As zsolve_delta, token by token: for one or a few tokens a sequence."""
+    a = _delta_args(q, k, v, g, beta, s0, offsets, scale)
+    op, _, _, _, ldo = _tokens(o, "o", q.dtype, (a.tokens, a.hv, a.dv))
+    _check_seq(seq, _lib.zsolve_delta_step(seq, ctypes.byref(a), op, ldo, _state(s, a)))
+
+
+def _state(s, a):
+    import torch
+    return _vector(s, "s", a.nseq * a.hv * a.dk * a.dv, torch.float32)
+
+
 class Seq:
     """Owns one handle of the sequence-layer operators; runs on torch's current stream.
 
@@ -246,6 +318,31 @@ class Seq:
         db = torch.empty(w.shape[:1], dtype=x.dtype, device=x.device)
         zsolve_linear_bwd(self.seq, dy, x, w, act, z, dx, dw, db)
         return dx, dw, db
+
+    def delta(self, q, k, v, g, beta, s0=None, offsets=None, scale=None):
+        """Returns (o, s): the gated delta rule over whole sequences, from the states s0 (zero without) to s.
+
+        Shapes as for zsolve_delta; s is (sequences, hv, dk, dv) float32.
+        """
+        import torch
+        self._on_stream()
+        o = torch.empty(v.shape, dtype=v.dtype, device=v.device)
+        nseq = offsets.numel() - 1 if offsets is not None else q.shape[0] if q.dim() == 4 else 1
+        s = torch.empty((nseq, v.shape[-2], q.shape[-1], v.shape[-1]), dtype=torch.float32, device=v.device)
+        zsolve_delta(self.seq, q, k, v, g, beta, o, s, s0, offsets, scale)
+        return o, s
+
+    def delta_step(self, q, k, v, g, beta, s, s_out=None, scale=None):
+        """Returns (o, s): the next token of every sequence, q (sequences, hk, dk) and so on (or the next few,
+        with two leading dimensions).  The states are updated in place, or written to s_out."""
+        import torch
+        self._on_stream()
+        o = torch.empty(v.shape, dtype=v.dtype, device=v.device)
+        s_out = s if s_out is None else s_out
+        if q.dim() == 3:
+            q, k, v = q.unsqueeze(1), k.unsqueeze(1), v.unsqueeze(1)
+        zsolve_delta_step(self.seq, q, k, v, g, beta, o.view(v.shape), s_out, s, None, scale)
+        return o, s_out
 
     def close(self):
         if self.seq:

@@ -566,6 +566,16 @@ int zsolve_delta(zsolve_seq *seq, const zsolve_delta_args *args, void *o, int64_
  * decoding, one or a few tokens a sequence. */
 int zsolve_delta_step(zsolve_seq *seq, const zsolve_delta_args *args, void *o, int64_t ldo, float *s);
 
+/* The gradients of zsolve_delta from those of its outputs, dout (tokens x hv x dv
+ * of args->type, token stride lddo) and ds (as s; NULL: zero).  dq, dk: tokens x hk
+ * x dk and dv: tokens x hv x dv of args->type, dg, dbeta: tokens x hv float32,
+ * ds0: as s0 (NULL: not formed); all packed, key heads summed over the value
+ * heads that share them in a fixed order.  The states are computed once more
+ * from the inputs; the workspace holds them and their gradients at every 64th
+ * token. */
+int zsolve_delta_bwd(zsolve_seq *seq, const zsolve_delta_args *args, const void *dout, int64_t lddo, const float *ds,
+                     void *dq, void *dk, void *dv, float *dg, float *dbeta, float *ds0);
+
 /* Static string for a status code.  No passage: error reporting of the library. */
 const char *zsolve_strerror(int status);
 

@@ -152,6 +152,7 @@ def _load():
         "zsolve_linear": (I, [P, I, I64, I64, I64, P, I64, P, I64, P, I, P, I64, P, I64, P, I64]),
         "zsolve_linear_bwd": (I, [P, I, I64, I64, I64, P, I64, P, I64, P, I64, I, P, I64, P, I64, P, I64, P]),
         "zsolve_delta": (I, [P, P, P, I64, P]),
+        "zsolve_delta_bwd": (I, [P, P, P, I64, P, P, P, P, P, P, P]),
         "zsolve_delta_step": (I, [P, P, P, I64, P]),
         "zsolve_layernorm": (I, [P, I, I, I64, I64, P, I64, P, P, D, P, I64, P, P]),
         "zsolve_layernorm_bwd": (I, [P, I, I, I64, I64, P, I64, P, I64, P, P, P, P, I64, P, P]),
@@ -533,6 +534,6 @@ class Afs:
 
 
 from .seq import (  # noqa: E402  (the sequence-layer operators use the names above)
-    Seq, ZSOLVE_ACTS, ZSOLVE_BF16, ZSOLVE_F16, ZSOLVE_F32, zsolve_delta, zsolve_delta_args, zsolve_delta_step,
+    Seq, ZSOLVE_ACTS, ZSOLVE_BF16, ZSOLVE_F16, ZSOLVE_F32, zsolve_delta, zsolve_delta_args, zsolve_delta_bwd, zsolve_delta_step,
     zsolve_layernorm, zsolve_layernorm_bwd, zsolve_linear, zsolve_linear_bwd, zsolve_seq_check, zsolve_seq_create, zsolve_seq_destroy, zsolve_seq_last_error, zsolve_seq_launches, zsolve_seq_reserve, zsolve_seq_set_stream,
     zsolve_seq_workspace_bytes)

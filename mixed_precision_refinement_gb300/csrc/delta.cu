@@ -219,26 +219,7 @@ k_delta_terms(const DeltaGeom geo, const DeltaTerms out, int vec) {
         const int64_t slot = (int64_t)blockIdx.x * geo.hv + hv;
         __syncthreads();  // kk, qk complete; the previous head's readers done
         if (warp == 0) {
-            // b_i in float64 (a few additions), kept as two floats: the
-            // differences b_i - b_j keep their digits after a strong decay.
-            // exp(-1e4) is 0, and finite sums leave no inf - inf.
-            double x[2];
-#pragma unroll
-            for (int e = 0; e < 2; e++) {
-                const int i = 2 * lane + e;
-                float gi = i < n ? geo.g[(int64_t)(ch.x + i) * geo.hv + hv] : 0.f;
-                if (gi < -1e4f) gi = -1e4f;
-                x[e] = gi;
-            }
-            double s = x[0] + x[1];
-#pragma unroll
-            for (int o = 1; o < 32; o <<= 1) {
-                const double v = __shfl_up_sync(0xffffffffu, s, o);
-                if (lane >= o) s += v;
-            }
-            const double b0 = s - x[1], b1 = s;
-            sm.bh[2 * lane] = (float)b0, sm.bl[2 * lane] = (float)(b0 - (double)(float)b0);
-            sm.bh[2 * lane + 1] = (float)b1, sm.bl[2 * lane + 1] = (float)(b1 - (double)(float)b1);
+            gate_sums(geo, ch, hv, sm.bh, sm.bl);
         } else if (warp == 1) {
 #pragma unroll
             for (int e = 0; e < 2; e++) {
@@ -311,20 +292,6 @@ struct ChainSmem {
     float x[C::NV][16 * kLdT];
     float u[C::NV][16 * kLdT];
 };
-
-template <int WK>
-__device__ __forceinline__ int tile_of(int w, int i) {
-    return (i & 1) ? (i + 1) * WK - 1 - w : i * WK + w;
-}
-
-// The warps of one column group wait for each other.
-template <int WK>
-__device__ __forceinline__ void group_sync(int group) {
-    if (WK == 1)
-        __syncwarp();
-    else
-        asm volatile("bar.sync %0, %1;" ::"r"(group + 1), "n"(WK * 32) : "memory");
-}
 
 template <typename T, int DK, bool OUT>
 __global__ void __launch_bounds__(ChainCfg<T, DK>::NT, 1)
@@ -546,10 +513,6 @@ k_delta_chain(const DeltaGeom geo, const DeltaTerms terms, const float *__restri
     if (sn) put_state(sn + state_at);
 }
 
-bool mult16(const void *p, int64_t ld, int64_t d, size_t e) {
-    return (((uintptr_t)p | (uint64_t)ld * e | (uint64_t)d * e) & 15) == 0;
-}
-
 template <typename T, int DK>
 cudaError_t terms_dk(const DeltaGeom &g, const DeltaTerms &t, cudaStream_t st) {
     const size_t smem = sizeof(TermSmem<T, DK>);
@@ -581,12 +544,6 @@ cudaError_t chain_dk(const DeltaGeom &g, const DeltaTerms &t, const float *s0, v
     }
     return cudaGetLastError();
 }
-
-#define DELTA_DK(T, FN, ...) (g.dk <= 32 ? FN<T, 32>(__VA_ARGS__) : g.dk <= 64 ? FN<T, 64>(__VA_ARGS__) : FN<T, 128>(__VA_ARGS__))
-#define DELTA_TYPE(FN, ...)                                                   \
-    (type == ZSOLVE_F32    ? DELTA_DK(float, FN, __VA_ARGS__)                 \
-     : type == ZSOLVE_BF16 ? DELTA_DK(bf16, FN, __VA_ARGS__)                  \
-                           : DELTA_DK(f16, FN, __VA_ARGS__))
 
 }  // namespace
 

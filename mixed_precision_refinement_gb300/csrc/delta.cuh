@@ -189,7 +189,61 @@ __device__ __forceinline__ void load_square(float *dst, const float *src) {
     }
 }
 
+// One warp: b_i of a chunk's tokens, summed in float64 (a few additions) and
+// kept as two floats, so that the differences b_i - b_j keep their digits after
+// a strong decay.  exp(-1e4) is 0, and finite sums leave no inf - inf.
+__device__ __forceinline__ void gate_sums(const DeltaGeom &geo, int2 ch, int hv, float *bh, float *bl) {
+    const int lane = threadIdx.x & 31;
+    double x[2];
+#pragma unroll
+    for (int e = 0; e < 2; e++) {
+        const int i = 2 * lane + e;
+        float gi = i < ch.y ? geo.g[(int64_t)(ch.x + i) * geo.hv + hv] : 0.f;
+        if (gi < -1e4f) gi = -1e4f;
+        x[e] = gi;
+    }
+    double s = x[0] + x[1];
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const double v = __shfl_up_sync(0xffffffffu, s, o);
+        if (lane >= o) s += v;
+    }
+    const double b0 = s - x[1], b1 = s;
+    bh[2 * lane] = (float)b0, bl[2 * lane] = (float)(b0 - (double)(float)b0);
+    bh[2 * lane + 1] = (float)b1, bl[2 * lane + 1] = (float)(b1 - (double)(float)b1);
+}
+
+// ---------------------------------------------------------------- chains
+
+// Token tile i (of 8) of warp w of WK: dealt so that triangular work is an
+// equal share for every warp.
+template <int WK>
+__device__ __forceinline__ int tile_of(int w, int i) {
+    return (i & 1) ? (i + 1) * WK - 1 - w : i * WK + w;
+}
+
+// The warps of one column group wait for each other.
+template <int WK>
+__device__ __forceinline__ void group_sync(int group) {
+    if (WK == 1)
+        __syncwarp();
+    else
+        asm volatile("bar.sync %0, %1;" ::"r"(group + 1), "n"(WK * 32) : "memory");
+}
+
+inline bool mult16(const void *p, int64_t ld, int64_t d, size_t e) {
+    return (((uintptr_t)p | (uint64_t)ld * e | (uint64_t)d * e) & 15) == 0;
+}
+
 }  // namespace zs
+
+// FN<T, DK>(...) for the call's type and the key columns it needs (`type` and
+// `g` in scope)
+#define DELTA_DK(T, FN, ...) (g.dk <= 32 ? FN<T, 32>(__VA_ARGS__) : g.dk <= 64 ? FN<T, 64>(__VA_ARGS__) : FN<T, 128>(__VA_ARGS__))
+#define DELTA_TYPE(FN, ...)                                                   \
+    (type == ZSOLVE_F32    ? DELTA_DK(float, FN, __VA_ARGS__)                 \
+     : type == ZSOLVE_BF16 ? DELTA_DK(bf16, FN, __VA_ARGS__)                  \
+                           : DELTA_DK(f16, FN, __VA_ARGS__))
 
 // ---------------------------------------------------------------- launchers
 
@@ -204,6 +258,20 @@ cudaError_t zs_launch_delta_terms(int type, const zs::DeltaGeom &g, const zs::De
 cudaError_t zs_launch_delta_chain(int type, const zs::DeltaGeom &g, const zs::DeltaTerms &t, const float *s0, void *o,
                                   int64_t ldo, float *sn, float *states, float *us, cudaStream_t st,
                                   int64_t *launches);
+// The recurrence backwards (delta_bwd.cu): from the gradients of o and of the
+// last states (ds; NULL: zero), per chunk and value head the gradient of the
+// state after the chunk (dends, dk x dv) and dX (64 x dv), dv, and the
+// gradient of the first states (ds0; NULL: not written).
+cudaError_t zs_launch_delta_rchain(int type, const zs::DeltaGeom &g, const zs::DeltaTerms &t, const void *dout,
+                                   int64_t lddo, const float *ds, float *dends, float *dxs, void *dv, float *ds0,
+                                   cudaStream_t st, int64_t *launches);
+// The gradients that the chunks give on their own.  parts (tokens x hv x dk
+// float32, one for dq and one for dk) are needed where value heads share a key
+// head; dq, dk: tokens x hk x dk.
+cudaError_t zs_launch_delta_grads(int type, const zs::DeltaGeom &g, const zs::DeltaTerms &t, const void *dout,
+                                  int64_t lddo, const float *states, const float *dends, const float *us,
+                                  const float *dxs, float *dqp, float *dkp, void *dq, void *dk, float *dg,
+                                  float *dbeta, cudaStream_t st, int64_t *launches);
 // Token by token (delta_step.cu): every sequence's tokens one after the other.
 cudaError_t zs_launch_delta_step(int type, const zs::DeltaGeom &g, const int64_t *offsets, const float *s0, void *o,
                                  int64_t ldo, float *sn, cudaStream_t st, int64_t *launches);

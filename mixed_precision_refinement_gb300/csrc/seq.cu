@@ -127,6 +127,8 @@ struct DeltaWork {
     int *first = nullptr;
     int2 *seq = nullptr, *chunk = nullptr;
     zs::DeltaTerms terms{};
+    bool backward = false;
+    float *states = nullptr, *us = nullptr, *dends = nullptr, *dxs = nullptr, *dqp = nullptr, *dkp = nullptr;
 
     void carve(zs::Carve &c, const zsolve_delta_args *a, bool out) {
         const size_t slots = (size_t)nchunks * a->hv, sq = (size_t)zs::kChunk * zs::kChunk;
@@ -136,6 +138,15 @@ struct DeltaWork {
         terms.t = c.take<float>(slots * sq);
         terms.p = out ? c.take<float>(slots * sq) : nullptr;
         terms.vec = c.take<float>(slots * zs::kVec);
+        if (!backward) return;
+        const size_t state = (size_t)a->dk * a->dv, rows = (size_t)zs::kChunk * a->dv;
+        states = c.take<float>(slots * state);
+        us = c.take<float>(slots * rows);
+        dends = c.take<float>(slots * state);
+        dxs = c.take<float>(slots * rows);
+        if (a->hv == a->hk) return;
+        dqp = c.take<float>((size_t)a->tokens * a->hv * a->dk);
+        dkp = c.take<float>((size_t)a->tokens * a->hv * a->dk);
     }
     int place(zsolve_seq *s, const zsolve_delta_args *a, bool out) {
         // a sequence's last chunk may be short: one more each at most
@@ -332,6 +343,36 @@ int zsolve_delta_step(zsolve_seq *s, const zsolve_delta_args *a, void *o, int64_
     st = check_device(s);
     if (st != ZSOLVE_OK) return st;
     SEQ_CU(zs_launch_delta_step(a->type, g, a->offsets, a->s0, o, ldo, sn, s->st, &s->launches));
+    return ZSOLVE_OK;
+}
+
+int zsolve_delta_bwd(zsolve_seq *s, const zsolve_delta_args *a, const void *dout, int64_t lddo, const float *ds,
+                     void *dq, void *dk, void *dv, float *dg, float *dbeta, float *ds0) {
+    if (!s) return ZSOLVE_EINVAL;
+    zs::DeltaGeom g;
+    int st = check_delta(s, a, dout, lddo, &g);
+    if (st != ZSOLVE_OK || a->nseq == 0) return st;
+    if (a->tokens > 0 && (!dq || !dk || !dv || !dg || !dbeta))
+        return seq_fail(s, ZSOLVE_EINVAL, "NULL dq, dk, dv, dg or dbeta");
+    if (a->hv > 65535) return seq_fail(s, ZSOLVE_EINVAL, "hv = %d", a->hv);
+    st = check_device(s);
+    if (st != ZSOLVE_OK) return st;
+    DeltaWork w;
+    w.backward = true;
+    st = w.place(s, a, true);
+    if (st != ZSOLVE_OK) return st;
+    w.bind(&g);
+    SEQ_CU(zs_launch_delta_plan(a->offsets, a->nseq, a->tokens, w.nchunks, w.first, w.seq, w.chunk, s->st, &s->launches));
+    if (a->tokens > 0) {
+        SEQ_CU(zs_launch_delta_terms(a->type, g, w.terms, s->st, &s->launches));
+        // the states and U once more: keeping them from the forward pass would hold 96 KB a chunk and head
+        // at 128 x 128 until the backward pass
+        SEQ_CU(zs_launch_delta_chain(a->type, g, w.terms, a->s0, nullptr, 0, nullptr, w.states, w.us, s->st, &s->launches));
+    }
+    SEQ_CU(zs_launch_delta_rchain(a->type, g, w.terms, dout, lddo, ds, w.dends, w.dxs, dv, ds0, s->st, &s->launches));
+    if (a->tokens > 0)
+        SEQ_CU(zs_launch_delta_grads(a->type, g, w.terms, dout, lddo, w.states, w.dends, w.us, w.dxs, w.dqp, w.dkp, dq,
+                                     dk, dg, dbeta, s->st, &s->launches));
     return ZSOLVE_OK;
 }
 

@@ -255,6 +255,19 @@ def zsolve_delta_step(seq, q, k, v, g, beta, o, s=None, s0=None, offsets=None, s
     _check_seq(seq, _lib.zsolve_delta_step(seq, ctypes.byref(a), op, ldo, _state(s, a)))
 
 
+def zsolve_delta_bwd(seq, dout, q, k, v, g, beta, dq, dk, dv, dg, dbeta, ds0=None, s0=None, ds=None, offsets=None,
+                     scale=None) -> None:
+    """dq .. dbeta and ds0 (shapes of q .. beta and s0, contiguous) from dout (as o) and ds (as s, or None)."""
+    import torch
+    a = _delta_args(q, k, v, g, beta, s0, offsets, scale)
+    op, _, _, _, lddo = _tokens(dout, "dout", q.dtype, (a.tokens, a.hv, a.dv))
+    nk, nv, n = a.tokens * a.hk * a.dk, a.tokens * a.hv * a.dv, a.tokens * a.hv
+    _check_seq(seq, _lib.zsolve_delta_bwd(seq, ctypes.byref(a), op, lddo, _state(ds, a), _vector(dq, "dq", nk, q.dtype),
+                                          _vector(dk, "dk", nk, q.dtype), _vector(dv, "dv", nv, q.dtype),
+                                          _vector(dg, "dg", n, torch.float32),
+                                          _vector(dbeta, "dbeta", n, torch.float32), _state(ds0, a)))
+
+
 def _state(s, a):
     import torch
     return _vector(s, "s", a.nseq * a.hv * a.dk * a.dv, torch.float32)
@@ -331,6 +344,17 @@ class Seq:
         s = torch.empty((nseq, v.shape[-2], q.shape[-1], v.shape[-1]), dtype=torch.float32, device=v.device)
         zsolve_delta(self.seq, q, k, v, g, beta, o, s, s0, offsets, scale)
         return o, s
+
+    def delta_bwd(self, dout, q, k, v, g, beta, s0=None, ds=None, offsets=None, scale=None):
+        """Returns (dq, dk, dv, dg, dbeta, ds0) from the gradients of o and, unless None, of s."""
+        import torch
+        self._on_stream()
+        dq, dk, dv = (torch.empty(t.shape, dtype=t.dtype, device=t.device) for t in (q, k, v))
+        dg, dbeta = torch.empty_like(g), torch.empty_like(beta)
+        nseq = offsets.numel() - 1 if offsets is not None else q.shape[0] if q.dim() == 4 else 1
+        ds0 = torch.empty((nseq, v.shape[-2], q.shape[-1], v.shape[-1]), dtype=torch.float32, device=v.device)
+        zsolve_delta_bwd(self.seq, dout, q, k, v, g, beta, dq, dk, dv, dg, dbeta, ds0, s0, ds, offsets, scale)
+        return dq, dk, dv, dg, dbeta, ds0
 
     def delta_step(self, q, k, v, g, beta, s, s_out=None, scale=None):
         """Returns (o, s): the next token of every sequence, q (sequences, hk, dk) and so on (or the next few,

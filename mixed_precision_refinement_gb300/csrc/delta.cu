@@ -80,95 +80,39 @@ k_delta_plan(const int64_t *__restrict__ offsets, int nseq, int64_t tokens, int 
 
 // ---------------------------------------------------------------- terms
 
+// One block for a chunk and a key head: K K^T and Q K^T once (tensor cores),
+// then, a half block of four warps a value head that shares the key head, A, T
+// and P.  The inverse T of I + A by blocks of 16: the diagonal blocks by
+// substitution, a lane a column; then warp j finds block column j below them,
+//   T_ij = -T_ii (A_ij T_jj + ... + A_i,i-1 T_i-1,j),
+// transposed, so that each finished block is, as an accumulator, the A operand
+// of the next products.  Bound by the latency of these steps; two blocks an SM.
 constexpr int kTermThreads = 256;
 constexpr int kLdA = kChunk + 4;
-
-// T <- inverse of I + A for a strictly lower A, both in shared memory (row
-// stride kLdA), by blocks: the four 16 x 16 diagonal blocks by substitution,
-// then pairs of blocks joined: [T1 0; -T2 A21 T1, T2].  tmp: 32 x kLdA.
-__device__ void invert_unit_lower(const float *A, float *T, float *tmp) {
-    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-    for (int i = tid; i < kChunk * kChunk; i += kTermThreads) {
-        const int r = i >> 6, c = i & 63;
-        if ((r >> 4) != (c >> 4)) T[r * kLdA + c] = 0.f;
-    }
-    if (warp < 4 && lane < 16) {  // column `lane` of diagonal block `warp`
-        const float *a = A + (warp * 16) * kLdA + warp * 16;
-        float x[16];
-#pragma unroll
-        for (int i = 0; i < 16; i++) {
-            float s = i == lane ? 1.f : 0.f;
-#pragma unroll
-            for (int l = 0; l < i; l++) s = fmaf(-a[i * kLdA + l], x[l], s);
-            x[i] = s;
-            T[(warp * 16 + i) * kLdA + warp * 16 + lane] = s;
-        }
-    }
-    __syncthreads();
-    // 16 -> 32: both pairs at once, an output pair of columns a thread
-    {
-        const int p = tid >> 7, r = (tid >> 3) & 15, c = (tid & 7) * 2, o = p * 32;
-        float s0 = 0.f, s1 = 0.f;
-#pragma unroll
-        for (int l = 0; l < 16; l++) {  // A21 T1
-            const float a = A[(o + 16 + r) * kLdA + o + l];
-            s0 = fmaf(a, T[(o + l) * kLdA + o + c], s0);
-            s1 = fmaf(a, T[(o + l) * kLdA + o + c + 1], s1);
-        }
-        tmp[(p * 16 + r) * kLdA + c] = s0;
-        tmp[(p * 16 + r) * kLdA + c + 1] = s1;
-        __syncthreads();
-        s0 = s1 = 0.f;
-#pragma unroll
-        for (int l = 0; l < 16; l++) {  // T2 (A21 T1)
-            const float a = T[(o + 16 + r) * kLdA + o + 16 + l];
-            s0 = fmaf(a, tmp[(p * 16 + l) * kLdA + c], s0);
-            s1 = fmaf(a, tmp[(p * 16 + l) * kLdA + c + 1], s1);
-        }
-        T[(o + 16 + r) * kLdA + o + c] = -s0;
-        T[(o + 16 + r) * kLdA + o + c + 1] = -s1;
-    }
-    __syncthreads();
-    // 32 -> 64: four columns a thread
-    {
-        const int r = tid >> 3, c = (tid & 7) * 4;
-        float s[4] = {};
-#pragma unroll 8
-        for (int l = 0; l < 32; l++) {
-            const float a = A[(32 + r) * kLdA + l];
-            const float4 b = *reinterpret_cast<const float4 *>(T + l * kLdA + c);
-            s[0] = fmaf(a, b.x, s[0]), s[1] = fmaf(a, b.y, s[1]), s[2] = fmaf(a, b.z, s[2]), s[3] = fmaf(a, b.w, s[3]);
-        }
-        *reinterpret_cast<float4 *>(tmp + r * kLdA + c) = make_float4(s[0], s[1], s[2], s[3]);
-        __syncthreads();
-        s[0] = s[1] = s[2] = s[3] = 0.f;
-#pragma unroll 8
-        for (int l = 0; l < 32; l++) {
-            const float a = T[(32 + r) * kLdA + 32 + l];
-            const float4 b = *reinterpret_cast<const float4 *>(tmp + l * kLdA + c);
-            s[0] = fmaf(a, b.x, s[0]), s[1] = fmaf(a, b.y, s[1]), s[2] = fmaf(a, b.z, s[2]), s[3] = fmaf(a, b.w, s[3]);
-        }
-        *reinterpret_cast<float4 *>(T + (32 + r) * kLdA + c) = make_float4(-s[0], -s[1], -s[2], -s[3]);
-    }
-    __syncthreads();
-}
+constexpr int kLdD = 20;
 
 template <typename T, int DK>
 struct TermSmem {
-    T k[kChunk * tile_ld<T>(DK)];
-    T q[kChunk * tile_ld<T>(DK)];
+    union {
+        struct {
+            T k[kChunk * tile_ld<T>(DK)];
+            T q[kChunk * tile_ld<T>(DK)];
+        };
+        float a[2][kChunk * kLdT];  // a value head each, once the products are done
+    };
     float kk[kChunk * kLdA];
     float qk[kChunk * kLdA];
-    float a[kChunk * kLdA];
-    float t[kChunk * kLdA];
-    float tmp[32 * kLdA];
-    float bh[kChunk], bl[kChunk], beta[kChunk];
+    float diag[2][4][16 * kLdD];
+    float bh[2][kChunk], bl[2][kChunk], beta[2][kChunk];
 };
 
-// One block for a chunk and a key head: K K^T and Q K^T once, then A, T, P and
-// the vectors of each value head that shares the key head.
+// A 16 x 16 block as two A operands' worth of accumulators
+struct Block {
+    Acc n[2];  // columns 0-7, 8-15
+};
+
 template <typename T, int DK>
-__global__ void __launch_bounds__(kTermThreads)
+__global__ void __launch_bounds__(kTermThreads, 2)
 k_delta_terms(const DeltaGeom geo, const DeltaTerms out, int vec) {
     extern __shared__ __align__(16) uint8_t smem_raw[];
     TermSmem<T, DK> &sm = *reinterpret_cast<TermSmem<T, DK> *>(smem_raw);
@@ -189,7 +133,9 @@ k_delta_terms(const DeltaGeom geo, const DeltaTerms out, int vec) {
         const int m = (warp & 3) * 16;
         const T *x = warp < 4 ? sm.k : sm.q;
         float *dst = warp < 4 ? sm.kk : sm.qk;
-        float acc[8][4] = {};
+        Acc acc[8];
+#pragma unroll
+        for (int j = 0; j < 8; j++) acc[j].zero();
 #pragma unroll 1
         for (int c = 0; c < DK; c += 32) {
             float2 r0[4], r1[4], b[4];
@@ -209,48 +155,127 @@ k_delta_terms(const DeltaGeom geo, const DeltaTerms out, int vec) {
 #pragma unroll
         for (int j = 0; j < 8; j++) {
             if (j * 8 > m + 8) continue;
-            *reinterpret_cast<float2 *>(dst + (m + g) * kLdA + j * 8 + 2 * t) = make_float2(acc[j][0], acc[j][1]);
-            *reinterpret_cast<float2 *>(dst + (m + g + 8) * kLdA + j * 8 + 2 * t) = make_float2(acc[j][2], acc[j][3]);
+            *reinterpret_cast<float2 *>(dst + (m + g) * kLdA + j * 8 + 2 * t) = make_float2(acc[j].get(0), acc[j].get(1));
+            *reinterpret_cast<float2 *>(dst + (m + g + 8) * kLdA + j * 8 + 2 * t) = make_float2(acc[j].get(2), acc[j].get(3));
         }
     }
-    const int group = geo.hv / geo.hk;
-    for (int r = 0; r < group; r++) {
-        const int hv = hk * group + r;
-        const int64_t slot = (int64_t)blockIdx.x * geo.hv + hv;
-        __syncthreads();  // kk, qk complete; the previous head's readers done
-        if (warp == 0) {
-            gate_sums(geo, ch, hv, sm.bh, sm.bl);
-        } else if (warp == 1) {
+    const int group = geo.hv / geo.hk, half = warp >> 2, w = warp & 3, ht = tid & 127;
+    __syncthreads();  // kk, qk complete; k and q give way to A
+    for (int r0 = 0; r0 < group; r0 += 2) {
+        const int r = r0 + half;
+        if (r < group) {  // the half blocks go their own way: barriers of 128 threads
+            const int hv = hk * group + r;
+            const int64_t slot = (int64_t)blockIdx.x * geo.hv + hv;
+            float *A = sm.a[half], *bh = sm.bh[half], *bl = sm.bl[half], *beta = sm.beta[half];
+            if (w == 0) {
+                gate_sums(geo, ch, hv, bh, bl);
+            } else if (w == 1) {
 #pragma unroll
-            for (int e = 0; e < 2; e++) {
-                const int i = 2 * lane + e;
-                sm.beta[i] = i < n ? geo.beta[(int64_t)(ch.x + i) * geo.hv + hv] : 0.f;
+                for (int e = 0; e < 2; e++) {
+                    const int i = 2 * lane + e;
+                    beta[i] = i < n ? geo.beta[(int64_t)(ch.x + i) * geo.hv + hv] : 0.f;
+                }
             }
-        }
-        __syncthreads();
-        if (tid < kChunk) {
-            float *v = out.vec + slot * kVec;
-            v[tid] = expf(sm.bh[tid] + sm.bl[tid]);
-            v[kChunk + tid] = expf((sm.bh[kChunk - 1] - sm.bh[tid]) + (sm.bl[kChunk - 1] - sm.bl[tid]));
-            v[2 * kChunk + tid] = sm.beta[tid];
-        }
-        for (int i = tid; i < kChunk * kChunk; i += kTermThreads) {
-            const int y = i >> 6, x = i & 63;
-            float av = 0.f, pv = 0.f;
-            if (x <= y) {
-                const float e = expf((sm.bh[y] - sm.bh[x]) + (sm.bl[y] - sm.bl[x]));
-                if (x < y) av = sm.beta[y] * sm.kk[y * kLdA + x] * e;
-                pv = geo.scale * sm.qk[y * kLdA + x] * e;
+            asm volatile("bar.sync %0, 128;" ::"r"(half + 1) : "memory");
+            if (ht < kChunk) {
+                float *v = out.vec + slot * kVec;
+                v[ht] = expf(bh[ht] + bl[ht]);
+                v[kChunk + ht] = expf((bh[kChunk - 1] - bh[ht]) + (bl[kChunk - 1] - bl[ht]));
+                v[2 * kChunk + ht] = beta[ht];
             }
-            sm.a[y * kLdA + x] = av;
-            if (out.p) out.p[slot * (kChunk * kChunk) + i] = pv;
-        }
-        __syncthreads();
-        invert_unit_lower(sm.a, sm.t, sm.tmp);
-        for (int i = tid; i < kChunk * kChunk / 4; i += kTermThreads) {
-            const int y = i >> 4, x = (i & 15) * 4;
-            *reinterpret_cast<float4 *>(out.t + slot * (kChunk * kChunk) + y * kChunk + x) =
-                *reinterpret_cast<const float4 *>(sm.t + y * kLdA + x);
+            float *P = out.p ? out.p + slot * kSquare : nullptr, *Tg = out.t + slot * kSquare;
+#pragma unroll 4
+            for (int i = ht; i < kChunk * kChunk; i += 128) {
+                const int y = i >> 6, x = i & 63;
+                float av = 0.f, pv = 0.f;
+                if (x <= y) {
+                    const float e = expf((bh[y] - bh[x]) + (bl[y] - bl[x]));
+                    if (x < y) av = beta[y] * sm.kk[y * kLdA + x] * e;
+                    pv = geo.scale * sm.qk[y * kLdA + x] * e;
+                }
+                A[y * kLdT + x] = av;
+                if (P) P[y * kLdT + x] = pv;
+            }
+            asm volatile("bar.sync %0, 128;" ::"r"(half + 1) : "memory");
+            {  // diagonal block w: lane l its column l (the upper half of the warp repeats the lower)
+                const float *a = A + (w * 16) * kLdT + w * 16;
+                const int c = lane & 15;
+                float x[16];
+#pragma unroll
+                for (int i = 0; i < 16; i++) {
+                    float s0 = i == c ? 1.f : 0.f, s1 = 0.f;
+#pragma unroll
+                    for (int l = 0; l + 1 < i; l += 2) {
+                        const float2 al = *reinterpret_cast<const float2 *>(a + i * kLdT + l);
+                        s0 = fmaf(-al.x, x[l], s0);
+                        s1 = fmaf(-al.y, x[l + 1], s1);
+                    }
+                    if (i & 1) s0 = fmaf(-a[i * kLdT + i - 1], x[i - 1], s0);
+                    x[i] = s0 + s1;
+                }
+                if (lane < 16) {
+#pragma unroll
+                    for (int i = 0; i < 16; i++) {
+                        sm.diag[half][w][i * kLdD + c] = x[i];
+                        Tg[(w * 16 + i) * kLdT + w * 16 + c] = x[i];
+                    }
+                }
+            }
+            asm volatile("bar.sync %0, 128;" ::"r"(half + 1) : "memory");
+            // block column w, transposed: Y_i = T_iw^T = -(sum over k of Y_k A_ik^T) T_ii^T
+            SplitA y[4][2];
+            {
+                const float *d = sm.diag[half][w];  // Y_w = T_ww^T
+#pragma unroll
+                for (int k = 0; k < 2; k++) {
+                    const int at = (k * 8 + 2 * t) * kLdD + g;
+                    const float c0 = d[at], c1 = d[at + kLdD], c2 = d[at + 8], c3 = d[at + kLdD + 8];
+#pragma unroll
+                    for (int i = 0; i < 4; i++)
+                        if (i == w) y[i][k].set(c0, c1, c2, c3);
+                }
+            }
+#pragma unroll
+            for (int i = 1; i < 4; i++) {
+                if (i <= w) continue;
+                Block s;
+                s.n[0].zero(), s.n[1].zero();
+#pragma unroll
+                for (int k = 0; k < i; k++) {
+                    if (k < w) continue;
+#pragma unroll
+                    for (int kk = 0; kk < 2; kk++)
+#pragma unroll
+                        for (int nn = 0; nn < 2; nn++)
+                            mma_split<false, false>(s.n[nn], y[k][kk],
+                                                    *reinterpret_cast<const float2 *>(A + (i * 16 + nn * 8 + g) * kLdT + k * 16 + kk * 8 + 2 * t));
+                }
+                Block z;
+                z.n[0].zero(), z.n[1].zero();
+#pragma unroll
+                for (int kk = 0; kk < 2; kk++) {
+                    SplitA a;
+                    a.set(-s.n[kk].get(0), -s.n[kk].get(1), -s.n[kk].get(2), -s.n[kk].get(3));
+#pragma unroll
+                    for (int nn = 0; nn < 2; nn++)
+                        mma_split<false, false>(z.n[nn], a,
+                                                *reinterpret_cast<const float2 *>(sm.diag[half][i] + (nn * 8 + g) * kLdD + kk * 8 + 2 * t));
+                }
+#pragma unroll
+                for (int nn = 0; nn < 2; nn++) {
+                    const float v[4] = {z.n[nn].get(0), z.n[nn].get(1), z.n[nn].get(2), z.n[nn].get(3)};
+                    if (i < 3) y[i][nn].set(v);
+#pragma unroll
+                    for (int e = 0; e < 4; e++)
+                        Tg[(i * 16 + nn * 8 + 2 * t + (e & 1)) * kLdT + w * 16 + g + (e >> 1) * 8] = v[e];
+                }
+            }
+            // above the diagonal blocks: zero
+            for (int i = ht; i < 6 * 64; i += 128) {
+                const int b = i >> 6, q = i & 63, bi = b < 3 ? 0 : b < 5 ? 1 : 2, bj = b < 3 ? b + 1 : b < 5 ? b - 1 : 3;
+                *reinterpret_cast<float4 *>(Tg + (bi * 16 + (q >> 2)) * kLdT + bj * 16 + (q & 3) * 4) = make_float4(0.f, 0.f, 0.f, 0.f);
+            }
+            asm volatile("bar.sync %0, 128;" ::"r"(half + 1) : "memory");  // A, diag free for the next head
         }
     }
 }
@@ -262,12 +287,14 @@ k_delta_terms(const DeltaGeom geo, const DeltaTerms out, int vec) {
 // group the 32 x 16 block of S^T for key columns 32 w ..: its accumulators,
 // which are also its A operands.  Per chunk the group exchanges three small
 // results through shared memory: the partial sums of S^T K^T (over the warps'
-// key columns), X^T and U^T; token tiles of 8 are dealt so that the triangular
-// products are equal shares (tile_of).
+// key columns), X^T and U^T, the latter two already split into tf32 parts by
+// the warp that wrote them; token tiles of 8 are dealt so that the triangular
+// products are equal shares (tile_of).  Two stages of chunk operands arrive by
+// bulk copies while the chunk before is at work.
 template <typename T, int DK>
 struct ChainCfg {
     static constexpr int WK = DK / 32;
-    static constexpr int NV = WK == 4 ? 2 : 4;
+    static constexpr int NV = DK == 32 ? 4 : 2;
     static constexpr int NT = 32 * WK * NV;
     static constexpr int NTILE = 8 / WK;
     static constexpr int LD = tile_ld<T>(DK);
@@ -279,48 +306,78 @@ template <typename T, int DK>
 struct ChainStage {
     T k[kChunk * tile_ld<T>(DK)];
     T q[kChunk * tile_ld<T>(DK)];
-    float t[kChunk * kLdT];
-    float p[kChunk * kLdT];
+    float t[kSquare];
+    float p[kSquare];
     float vec[kVec];
 };
+
+// Rows of 32 split pairs, 64 bytes more apart: the rows of a fragment's loads lie in different banks.
+constexpr int kLdPair = 36;
 
 template <typename T, int DK>
 struct ChainSmem {
     using C = ChainCfg<T, DK>;
     ChainStage<T, DK> st[C::STAGES];
     float part[C::NV][C::WK][16 * kLdT];
-    float x[C::NV][16 * kLdT];
-    float u[C::NV][16 * kLdT];
+    float4 x[C::NV][16 * kLdPair];  // X^T, then the chunk's outputs
+    float4 u[C::NV][16 * kLdPair];  // (e U)^T
+    float2 un[C::NV][16 * kLdPair]; // U^T in tf32, for P U
+    uint64_t full[C::STAGES];
 };
 
 template <typename T, int DK, bool OUT>
 __global__ void __launch_bounds__(ChainCfg<T, DK>::NT, 1)
 k_delta_chain(const DeltaGeom geo, const DeltaTerms terms, const float *__restrict__ s0, T *__restrict__ o,
-              int64_t ldo, float *__restrict__ sn, float *__restrict__ states, float *__restrict__ us, int vec) {
+              int64_t ldo, float *__restrict__ sn, float *__restrict__ states, float *__restrict__ us, int vec, int veco,
+              unsigned *__restrict__ status) {
     using C = ChainCfg<T, DK>;
     constexpr int WK = C::WK, NV = C::NV, NT = C::NT, LD = C::LD, NTILE = C::NTILE;
     constexpr bool EXACT = sizeof(T) == 2;
     extern __shared__ __align__(16) uint8_t smem_raw[];
     ChainSmem<T, DK> &sm = *reinterpret_cast<ChainSmem<T, DK> *>(smem_raw);
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g = lane >> 2, t = lane & 3;
     const int grp = warp / WK, w = warp - grp * WK;
     const int si = blockIdx.x / geo.hv, hv = blockIdx.x - si * geo.hv, hk = hv / (geo.hv / geo.hk);
     const int v0 = ((int)blockIdx.y * NV + grp) * 16;  // the group's value columns
     const int d0 = w * 32;                             // the warp's key columns
     const int64_t state_at = ((int64_t)si * geo.hv + hv) * geo.dk * geo.dv;
+    const T *kp = (const T *)geo.k + (int64_t)hk * geo.dk, *qp = (const T *)geo.q + (int64_t)hk * geo.dk;
+
+    if (tid == 0)
+        for (int i = 0; i < C::STAGES; i++) bar_init(&sm.full[i]);
+    if (vec && geo.dk < DK)  // the copies leave the columns beyond dk alone
+        for (int i = tid; i < C::STAGES * kChunk * (DK / 8); i += NT) {
+            const int s = i / (kChunk * (DK / 8)), rest = i - s * kChunk * (DK / 8), row = rest / (DK / 8), c = rest % (DK / 8) * 8;
+#pragma unroll
+            for (int e = 0; e < 8; e++)
+                if (c + e >= geo.dk) sm.st[s].k[row * LD + c + e] = sm.st[s].q[row * LD + c + e] = from_f32<T>(0.f);
+        }
+    asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+    __syncthreads();
 
     auto load = [&](int c, int stage) {
         const int2 ch = geo.chunk[c];
         ChainStage<T, DK> &s = sm.st[stage];
         const int64_t slot = (int64_t)c * geo.hv + hv;
-        load_tile<T, DK, NT>(s.k, (const T *)geo.k + (int64_t)ch.x * geo.ldk + (int64_t)hk * geo.dk, geo.ldk, ch.y, geo.dk, vec);
-        load_square<NT>(s.t, terms.t + slot * (kChunk * kChunk));
-        if (OUT) {
-            load_tile<T, DK, NT>(s.q, (const T *)geo.q + (int64_t)ch.x * geo.ldq + (int64_t)hk * geo.dk, geo.ldq, ch.y, geo.dk, vec);
-            load_square<NT>(s.p, terms.p + slot * (kChunk * kChunk));
+        uint64_t *bar = &sm.full[stage];
+        if (tid == 0) {
+            const uint32_t rows = vec ? (uint32_t)(ch.y * geo.dk * sizeof(T)) : 0u;
+            bar_expect(bar, (OUT ? 2 : 1) * (rows + kSquare * 4) + kVec * 4);
+            bulk_load(s.t, terms.t + slot * kSquare, kSquare * 4, bar);
+            if (OUT) bulk_load(s.p, terms.p + slot * kSquare, kSquare * 4, bar);
+            bulk_load(s.vec, terms.vec + slot * kVec, kVec * 4, bar);
         }
-        for (int i = threadIdx.x; i < kVec / 4; i += NT) cp_async16(s.vec + 4 * i, terms.vec + slot * kVec + 4 * i, 16);
-        cp_commit();
+        if (vec) {
+            for (int r = tid; r < 2 * kChunk; r += NT) {
+                if (r < kChunk)
+                    bulk_row<T, DK>(s.k, kp + (int64_t)ch.x * geo.ldk, geo.ldk, ch.y, geo.dk, r, bar);
+                else if (OUT)
+                    bulk_row<T, DK>(s.q, qp + (int64_t)ch.x * geo.ldq, geo.ldq, ch.y, geo.dk, r - kChunk, bar);
+            }
+        } else {
+            load_tile<T, DK, NT>(s.k, kp + (int64_t)ch.x * geo.ldk, geo.ldk, ch.y, geo.dk, 0);
+            if (OUT) load_tile<T, DK, NT>(s.q, qp + (int64_t)ch.x * geo.ldq, geo.ldq, ch.y, geo.dk, 0);
+        }
     };
 
     // S^T: rows v0 + g, v0 + g + 8, columns d0 + 8 j + 2t, + 1
@@ -341,30 +398,51 @@ k_delta_chain(const DeltaGeom geo, const DeltaTerms terms, const float *__restri
                 if (v < geo.dv && d < geo.dk) dst[(int64_t)d * geo.dv + v] = S[j][e];
             }
     };
+    // The outputs of a chunk, from the group's staging rows (64 tokens x 16 columns), 16 bytes a thread
+    constexpr int PIECE = 16 / (int)sizeof(T), PPR = 16 / PIECE;
+    auto put_out = [&](int2 ch) {
+        const T *stage = reinterpret_cast<const T *>(sm.x[grp]);
+        for (int i = w * 32 + lane; i < kChunk * PPR; i += WK * 32) {
+            const int tok = i / PPR, c = (i - tok * PPR) * PIECE;
+            if (tok < ch.y && v0 + c < geo.dv)
+                *reinterpret_cast<uint4 *>(o + (int64_t)(ch.x + tok) * ldo + (int64_t)hv * geo.dv + v0 + c) =
+                    *reinterpret_cast<const uint4 *>(stage + tok * 16 + c);
+        }
+    };
 
     const int c0 = geo.first[si], c1 = geo.first[si + 1];
     if (c0 < c1) load(c0, 0);
+    int2 before = make_int2(0, 0);  // the chunk whose outputs are staged
     for (int c = c0; c < c1; c++) {
-        const int stage = C::STAGES == 2 ? (c - c0) & 1 : 0;
-        cp_wait<0>();
-        __syncthreads();  // the stage is complete, and every warp is done with the previous chunk
+        const int it = c - c0, stage = C::STAGES == 2 ? it & 1 : 0;
+        // the stage is complete, and every warp is done with the previous chunk
+        const bool ok = bar_wait(&sm.full[stage], (C::STAGES == 2 ? it >> 1 : it) & 1);
+        if (!__syncthreads_and(ok)) {
+            if (tid == 0) atomicOr(status, 1u);
+            return;
+        }
         if (C::STAGES == 2 && c + 1 < c1) load(c + 1, stage ^ 1);
         ChainStage<T, DK> &st = sm.st[stage];
         const int2 ch = geo.chunk[c];
         const int64_t slot = (int64_t)c * geo.hv + hv;
+        if (OUT && veco && it > 0) put_out(before);
         if (states) put_state(states + slot * geo.dk * geo.dv);
 
         // V^T of the warp's token tiles, for X (the loads run during the products)
         float vt[NTILE][4];
+        {
+            const T *vp = (const T *)geo.v + (int64_t)ch.x * geo.ldv + (int64_t)hv * geo.dv + v0 + g;
+            const bool in0 = v0 + g < geo.dv, in1 = v0 + g + 8 < geo.dv;
 #pragma unroll
-        for (int i = 0; i < NTILE; i++)
+            for (int i = 0; i < NTILE; i++)
 #pragma unroll
-            for (int e = 0; e < 4; e++) {
-                const int v = v0 + g + (e >> 1) * 8, tok = tile_of<WK>(w, i) * 8 + 2 * t + (e & 1);
-                vt[i][e] = v < geo.dv && tok < ch.y
-                               ? to_f32(((const T *)geo.v)[(int64_t)(ch.x + tok) * geo.ldv + (int64_t)hv * geo.dv + v])
-                               : 0.f;
-            }
+                for (int e = 0; e < 2; e++) {
+                    const int tok = tile_of<WK>(w, i) * 8 + 2 * t + e;
+                    const T *p = vp + (int64_t)tok * geo.ldv;
+                    vt[i][e] = in0 && tok < ch.y ? to_f32(p[0]) : 0.f;
+                    vt[i][2 + e] = in1 && tok < ch.y ? to_f32(p[8]) : 0.f;
+                }
+        }
 
         // partial S^T K^T and S^T Q^T over the warp's key columns
         float po[8][4];
@@ -374,20 +452,43 @@ k_delta_chain(const DeltaGeom geo, const DeltaTerms terms, const float *__restri
             for (int j = 0; j < 4; j++) a[j].set(S[j]);
             float *part = sm.part[grp][w];
 #pragma unroll
-            for (int n = 0; n < 8; n++) {
-                float2 b[4];
-                float r[4] = {};
-                frag4<T, LD, false>(st.k, n * 8, d0, b);
+            for (int h = 0; h < 8; h += 4) {
+                Acc r[4];
+                float2 b[4][4];
 #pragma unroll
-                for (int j = 0; j < 4; j++) mma_split<EXACT>(r, a[j], b[j]);
-                *reinterpret_cast<float2 *>(part + g * kLdT + n * 8 + 2 * t) = make_float2(r[0], r[1]);
-                *reinterpret_cast<float2 *>(part + (g + 8) * kLdT + n * 8 + 2 * t) = make_float2(r[2], r[3]);
-                if (OUT) {
-                    frag4<T, LD, false>(st.q, n * 8, d0, b);
+                for (int n = 0; n < 4; n++) {
+                    r[n].zero();
+                    frag4<T, LD, false>(st.k, (h + n) * 8, d0, b[n]);
+                }
 #pragma unroll
-                    for (int e = 0; e < 4; e++) po[n][e] = 0.f;
+                for (int j = 0; j < 4; j++)
 #pragma unroll
-                    for (int j = 0; j < 4; j++) mma_split<EXACT, EXACT>(po[n], a[j], b[j]);
+                    for (int n = 0; n < 4; n++) mma_split<false, EXACT>(r[n], a[j], b[n][j]);
+#pragma unroll
+                for (int n = 0; n < 4; n++) {
+                    float *p = part + g * kLdT + (h + n) * 8 + 2 * t;
+                    *reinterpret_cast<float2 *>(p) = make_float2(r[n].get(0), r[n].get(1));
+                    *reinterpret_cast<float2 *>(p + 8 * kLdT) = make_float2(r[n].get(2), r[n].get(3));
+                }
+            }
+            if (OUT) {
+#pragma unroll
+                for (int h = 0; h < 8; h += 4) {
+                    Acc r[4];
+                    float2 b[4][4];
+#pragma unroll
+                    for (int n = 0; n < 4; n++) {
+                        r[n].zero();
+                        frag4<T, LD, false>(st.q, (h + n) * 8, d0, b[n]);
+                    }
+#pragma unroll
+                    for (int j = 0; j < 4; j++)
+#pragma unroll
+                        for (int n = 0; n < 4; n++) mma_split<false, EXACT, EXACT>(r[n], a[j], b[n][j]);
+#pragma unroll
+                    for (int n = 0; n < 4; n++)
+#pragma unroll
+                        for (int e = 0; e < 4; e++) po[h + n][e] = EXACT ? r[n].c[e] : r[n].get(e);
                 }
             }
         }
@@ -403,11 +504,11 @@ k_delta_chain(const DeltaGeom geo, const DeltaTerms terms, const float *__restri
                 const float2 z = *reinterpret_cast<const float2 *>(sm.part[grp][p] + (g + 8) * kLdT + n);
                 lo.x += y.x, lo.y += y.y, hi.x += z.x, hi.y += z.y;
             }
-            const float ca = st.vec[n], cb = st.vec[n + 1], ba = st.vec[2 * kChunk + n], bb = st.vec[2 * kChunk + n + 1];
-            *reinterpret_cast<float2 *>(sm.x[grp] + g * kLdT + n) =
-                make_float2(ba * (vt[i][0] - ca * lo.x), bb * (vt[i][1] - cb * lo.y));
-            *reinterpret_cast<float2 *>(sm.x[grp] + (g + 8) * kLdT + n) =
-                make_float2(ba * (vt[i][2] - ca * hi.x), bb * (vt[i][3] - cb * hi.y));
+            const float2 cv = *reinterpret_cast<const float2 *>(st.vec + n);
+            const float2 bv = *reinterpret_cast<const float2 *>(st.vec + 2 * kChunk + n);
+            float4 *x = sm.x[grp] + g * kLdPair + n / 2;
+            x[0] = split_pair(bv.x * (vt[i][0] - cv.x * lo.x), bv.y * (vt[i][1] - cv.y * lo.y));
+            x[8 * kLdPair] = split_pair(bv.x * (vt[i][2] - cv.x * hi.x), bv.y * (vt[i][3] - cv.y * hi.y));
         }
         group_sync<WK>(grp);
         if (OUT) {
@@ -420,82 +521,98 @@ k_delta_chain(const DeltaGeom geo, const DeltaTerms terms, const float *__restri
         }
         // U^T = X^T T^T at the warp's token tiles
         {
-            float u[NTILE][4] = {};
+            Acc u[NTILE];
+#pragma unroll
+            for (int i = 0; i < NTILE; i++) u[i].zero();
 #pragma unroll
             for (int k = 0; k < 8; k++) {
                 SplitA a;
-                const float2 y = *reinterpret_cast<const float2 *>(sm.x[grp] + g * kLdT + k * 8 + 2 * t);
-                const float2 z = *reinterpret_cast<const float2 *>(sm.x[grp] + (g + 8) * kLdT + k * 8 + 2 * t);
-                a.set(y.x, y.y, z.x, z.y);
+                a.set(sm.x[grp][g * kLdPair + k * 4 + t], sm.x[grp][(g + 8) * kLdPair + k * 4 + t]);
 #pragma unroll
                 for (int i = 0; i < NTILE; i++) {
                     const int n = tile_of<WK>(w, i);
                     if (k > n) continue;
-                    const float2 b = *reinterpret_cast<const float2 *>(st.t + (n * 8 + g) * kLdT + k * 8 + 2 * t);
-                    mma_split<false>(u[i], a, b);
+                    mma_split<false, false>(u[i], a, *reinterpret_cast<const float2 *>(st.t + (n * 8 + g) * kLdT + k * 8 + 2 * t));
                 }
             }
 #pragma unroll
             for (int i = 0; i < NTILE; i++) {
-                const int n = tile_of<WK>(w, i) * 8 + 2 * t;
-                *reinterpret_cast<float2 *>(sm.u[grp] + g * kLdT + n) = make_float2(u[i][0], u[i][1]);
-                *reinterpret_cast<float2 *>(sm.u[grp] + (g + 8) * kLdT + n) = make_float2(u[i][2], u[i][3]);
+                const int n = tile_of<WK>(w, i) * 8 + 2 * t, at = g * kLdPair + n / 2;
+                const float2 ev = *reinterpret_cast<const float2 *>(st.vec + kChunk + n);
+                const float v[4] = {u[i].get(0), u[i].get(1), u[i].get(2), u[i].get(3)};
+                sm.u[grp][at] = split_pair(ev.x * v[0], ev.y * v[1]);
+                sm.u[grp][at + 8 * kLdPair] = split_pair(ev.x * v[2], ev.y * v[3]);
+                if (OUT) {
+                    sm.un[grp][at] = make_float2(v[0], v[1]);
+                    sm.un[grp][at + 8 * kLdPair] = make_float2(v[2], v[3]);
+                }
                 if (us) {
 #pragma unroll
                     for (int e = 0; e < 4; e++) {
-                        const int v = v0 + g + (e >> 1) * 8;
-                        if (v < geo.dv) us[(slot * kChunk + n + (e & 1)) * geo.dv + v] = u[i][e];
+                        const int vc = v0 + g + (e >> 1) * 8;
+                        if (vc < geo.dv) us[(slot * kChunk + n + (e & 1)) * geo.dv + vc] = v[e];
                     }
                 }
             }
         }
         group_sync<WK>(grp);
         // S'^T = c_64 S^T + (e U)^T K: the chunk's sum starts from zero, so that
-        // the state is rounded once a chunk; and O^T = scale c (Q S)^T + U^T P^T
+        // the state is rounded once a chunk
         {
-            float acc[4][4] = {}, oa[NTILE][4] = {};
+            Acc acc[4];
+#pragma unroll
+            for (int j = 0; j < 4; j++) acc[j].zero();
 #pragma unroll
             for (int k = 0; k < 8; k++) {
-                const float2 y = *reinterpret_cast<const float2 *>(sm.u[grp] + g * kLdT + k * 8 + 2 * t);
-                const float2 z = *reinterpret_cast<const float2 *>(sm.u[grp] + (g + 8) * kLdT + k * 8 + 2 * t);
-                const float ea = st.vec[kChunk + k * 8 + 2 * t], eb = st.vec[kChunk + k * 8 + 2 * t + 1];
                 SplitA a;
-                a.set(ea * y.x, eb * y.y, ea * z.x, eb * z.y);
+                a.set(sm.u[grp][g * kLdPair + k * 4 + t], sm.u[grp][(g + 8) * kLdPair + k * 4 + t]);
                 float2 b[4];
                 frag4<T, LD, true>(st.k, k * 8, d0, b);
 #pragma unroll
-                for (int j = 0; j < 4; j++) mma_split<EXACT>(acc[j], a, b[j]);
-                if (OUT) {
-                    SplitA ua;
-                    ua.set(y.x, y.y, z.x, z.y);
-#pragma unroll
-                    for (int i = 0; i < NTILE; i++) {
-                        const int n = tile_of<WK>(w, i);
-                        if (k > n) continue;
-                        const float2 p = *reinterpret_cast<const float2 *>(st.p + (n * 8 + g) * kLdT + k * 8 + 2 * t);
-                        mma_split<false, EXACT>(oa[i], ua, p);
-                    }
-                }
+                for (int j = 0; j < 4; j++) mma_split<false, EXACT>(acc[j], a, b[j]);
             }
             const float cend = st.vec[kChunk - 1];
 #pragma unroll
             for (int j = 0; j < 4; j++)
 #pragma unroll
-                for (int e = 0; e < 4; e++) S[j][e] = fmaf(cend, S[j][e], acc[j][e]);
-            if (OUT) {
+                for (int e = 0; e < 4; e++) S[j][e] = fmaf(cend, S[j][e], acc[j].get(e));
+        }
+        // O^T = scale c (Q S)^T + U^T P^T at the warp's token tiles
+        if (OUT) {
+            Acc oa[NTILE];
+#pragma unroll
+            for (int i = 0; i < NTILE; i++) oa[i].zero();
+#pragma unroll
+            for (int k = 0; k < 8; k++) {
+                const float2 y = sm.un[grp][g * kLdPair + k * 4 + t], z = sm.un[grp][(g + 8) * kLdPair + k * 4 + t];
+                SplitA a;
+                a.set(y.x, y.y, z.x, z.y);
 #pragma unroll
                 for (int i = 0; i < NTILE; i++) {
-                    const int n = tile_of<WK>(w, i) * 8 + 2 * t;
-                    float2 lo = make_float2(0.f, 0.f), hi = lo;
+                    const int n = tile_of<WK>(w, i);
+                    if (k > n) continue;
+                    mma_split<false, false, EXACT>(oa[i], a, *reinterpret_cast<const float2 *>(st.p + (n * 8 + g) * kLdT + k * 8 + 2 * t));
+                }
+            }
+            T *stg = reinterpret_cast<T *>(sm.x[grp]);
 #pragma unroll
-                    for (int p = 0; p < WK; p++) {
-                        const float2 y = *reinterpret_cast<const float2 *>(sm.part[grp][p] + g * kLdT + n);
-                        const float2 z = *reinterpret_cast<const float2 *>(sm.part[grp][p] + (g + 8) * kLdT + n);
-                        lo.x += y.x, lo.y += y.y, hi.x += z.x, hi.y += z.y;
-                    }
-                    const float ca = geo.scale * st.vec[n], cb = geo.scale * st.vec[n + 1];
-                    const float r[4] = {fmaf(ca, lo.x, oa[i][0]), fmaf(cb, lo.y, oa[i][1]), fmaf(ca, hi.x, oa[i][2]),
-                                        fmaf(cb, hi.y, oa[i][3])};
+            for (int i = 0; i < NTILE; i++) {
+                const int n = tile_of<WK>(w, i) * 8 + 2 * t;
+                float2 lo = make_float2(0.f, 0.f), hi = lo;
+#pragma unroll
+                for (int p = 0; p < WK; p++) {
+                    const float2 y = *reinterpret_cast<const float2 *>(sm.part[grp][p] + g * kLdT + n);
+                    const float2 z = *reinterpret_cast<const float2 *>(sm.part[grp][p] + (g + 8) * kLdT + n);
+                    lo.x += y.x, lo.y += y.y, hi.x += z.x, hi.y += z.y;
+                }
+                const float2 cv = *reinterpret_cast<const float2 *>(st.vec + n);
+                const float ca = geo.scale * cv.x, cb = geo.scale * cv.y;
+                const float r[4] = {fmaf(ca, lo.x, oa[i].get(0)), fmaf(cb, lo.y, oa[i].get(1)),
+                                    fmaf(ca, hi.x, oa[i].get(2)), fmaf(cb, hi.y, oa[i].get(3))};
+                if (veco) {
+#pragma unroll
+                    for (int e = 0; e < 4; e++) stg[(n + (e & 1)) * 16 + g + (e >> 1) * 8] = from_f32<T>(r[e]);
+                } else {
 #pragma unroll
                     for (int e = 0; e < 4; e++) {
                         const int v = v0 + g + (e >> 1) * 8, tok = n + (e & 1);
@@ -504,11 +621,16 @@ k_delta_chain(const DeltaGeom geo, const DeltaTerms terms, const float *__restri
                     }
                 }
             }
+            before = ch;
         }
         if (C::STAGES == 1) {
             __syncthreads();  // the only stage is free
             if (c + 1 < c1) load(c + 1, 0);
         }
+    }
+    if (OUT && veco && c0 < c1) {
+        group_sync<WK>(grp);
+        put_out(before);
     }
     if (sn) put_state(sn + state_at);
 }
@@ -526,8 +648,9 @@ cudaError_t terms_dk(const DeltaGeom &g, const DeltaTerms &t, cudaStream_t st) {
 
 template <typename T, int DK>
 cudaError_t chain_dk(const DeltaGeom &g, const DeltaTerms &t, const float *s0, void *o, int64_t ldo, float *sn,
-                     float *states, float *us, cudaStream_t st) {
+                     float *states, float *us, unsigned *status, cudaStream_t st) {
     using C = ChainCfg<T, DK>;
+    static_assert(sizeof(ChainSmem<T, DK>) <= 232448, "shared memory of a block");
     const size_t smem = sizeof(ChainSmem<T, DK>);
     const int vec = mult16(g.q, g.ldq, g.dk, sizeof(T)) && mult16(g.k, g.ldk, g.dk, sizeof(T));
     const dim3 grid((unsigned)(g.nseq * g.hv), (unsigned)((g.dv + 16 * C::NV - 1) / (16 * C::NV)));
@@ -535,12 +658,13 @@ cudaError_t chain_dk(const DeltaGeom &g, const DeltaTerms &t, const float *s0, v
         static const cudaError_t attr = cudaFuncSetAttribute(
             k_delta_chain<T, DK, true>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)sizeof(ChainSmem<T, DK>));
         if (attr != cudaSuccess) return attr;
-        k_delta_chain<T, DK, true><<<grid, C::NT, smem, st>>>(g, t, s0, (T *)o, ldo, sn, states, us, vec);
+        k_delta_chain<T, DK, true><<<grid, C::NT, smem, st>>>(g, t, s0, (T *)o, ldo, sn, states, us, vec,
+                                                                    mult16(o, ldo, g.dv, sizeof(T)), status);
     } else {
         static const cudaError_t attr = cudaFuncSetAttribute(
             k_delta_chain<T, DK, false>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)sizeof(ChainSmem<T, DK>));
         if (attr != cudaSuccess) return attr;
-        k_delta_chain<T, DK, false><<<grid, C::NT, smem, st>>>(g, t, s0, nullptr, 0, sn, states, us, vec);
+        k_delta_chain<T, DK, false><<<grid, C::NT, smem, st>>>(g, t, s0, nullptr, 0, sn, states, us, vec, 0, status);
     }
     return cudaGetLastError();
 }
@@ -561,8 +685,8 @@ cudaError_t zs_launch_delta_terms(int type, const DeltaGeom &g, const DeltaTerms
 }
 
 cudaError_t zs_launch_delta_chain(int type, const DeltaGeom &g, const DeltaTerms &t, const float *s0, void *o,
-                                  int64_t ldo, float *sn, float *states, float *us, cudaStream_t st,
+                                  int64_t ldo, float *sn, float *states, float *us, unsigned *status, cudaStream_t st,
                                   int64_t *launches) {
     ++*launches;
-    return DELTA_TYPE(chain_dk, g, t, s0, o, ldo, sn, states, us, st);
+    return DELTA_TYPE(chain_dk, g, t, s0, o, ldo, sn, states, us, status, st);
 }

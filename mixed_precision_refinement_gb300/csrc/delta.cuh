@@ -44,7 +44,7 @@ struct DeltaGeom {
 };
 
 // Per chunk and value head, what does not depend on the state (float32):
-// T (64 x 64), P (64 x 64) and the vectors c_i, e_64,i, beta_i (64 each).
+// T and P (64 rows of stride 72) and the vectors c_i, e_64,i, beta_i (64 each).
 struct DeltaTerms {
     float *t, *p, *vec;
 };
@@ -54,16 +54,23 @@ constexpr int kVec = 3 * kChunk;
 
 __device__ __forceinline__ uint32_t tf32(float x) {
     uint32_t r;
-    asm("cvt.rna.tf32.f32 %0, %1;" : "=r"(r) : "f"(x));
+    asm("cvt.rn.tf32.f32 %0, %1;" : "=r"(r) : "f"(x));
     return r;
 }
 
 __device__ __forceinline__ void mma8(float (&c)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
-    asm volatile(
-        "mma.sync.aligned.m16n8k8.row.col.f32.tf32.tf32.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
+    asm("mma.sync.aligned.m16n8k8.row.col.f32.tf32.tf32.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
         "{%0, %1, %2, %3};"
         : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
         : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+
+// c = A B of one step, from zero
+__device__ __forceinline__ void mma8_first(float (&c)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+    asm("mma.sync.aligned.m16n8k8.row.col.f32.tf32.tf32.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
+        "{%10, %10, %10, %10};"
+        : "=f"(c[0]), "=f"(c[1]), "=f"(c[2]), "=f"(c[3])
+        : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1), "f"(0.f));
 }
 
 // An A operand of 16 x 8 in two tf32 parts.  The instruction's k slots t and
@@ -82,24 +89,64 @@ struct SplitA {
         }
     }
     __device__ __forceinline__ void set(const float (&c)[4]) { set(c[0], c[1], c[2], c[3]); }
+    // two rows of pairs as Pair keeps them
+    __device__ __forceinline__ void set(float4 y, float4 z) {
+        hi[0] = __float_as_uint(y.x), hi[2] = __float_as_uint(y.y), lo[0] = __float_as_uint(y.z), lo[2] = __float_as_uint(y.w);
+        hi[1] = __float_as_uint(z.x), hi[3] = __float_as_uint(z.y), lo[1] = __float_as_uint(z.z), lo[3] = __float_as_uint(z.w);
+    }
 };
 
-// c += A B for one 16 x 8 x 8 step, b = (B(2t, g), B(2t+1, g)); EXACT: b is
-// exact in tf32; HALF: A's hi part alone (results that are rounded to 16 bits).
-template <bool EXACT, bool HALF = false>
-__device__ __forceinline__ void mma_split(float (&c)[4], const SplitA &a, float2 b) {
-    if (EXACT) {
-        const uint32_t b0 = __float_as_uint(b.x), b1 = __float_as_uint(b.y);
-        if (!HALF) mma8(c, a.lo, b0, b1);
-        mma8(c, a.hi, b0, b1);
-    } else {
-        const uint32_t b0 = tf32(b.x), b1 = tf32(b.y);
-        if (!HALF) {
-            mma8(c, a.lo, b0, b1);
-            mma8(c, a.hi, tf32(b.x - __uint_as_float(b0)), tf32(b.y - __uint_as_float(b1)));
-        }
-        mma8(c, a.hi, b0, b1);
+// Two neighbours split for later use as an A operand: (hi, hi, lo, lo).
+__device__ __forceinline__ float4 split_pair(float a, float b) {
+    const float ha = __uint_as_float(tf32(a)), hb = __uint_as_float(tf32(b));
+    return make_float4(ha, hb, __uint_as_float(tf32(a - ha)), __uint_as_float(tf32(b - hb)));
+}
+
+// A product in two sums, c of the hi.hi terms and l of the small ones: the
+// tensor cores round their sums toward zero, and apart the small terms do not
+// add to how often c is rounded.
+struct Acc {
+    float c[4], l[4];
+    __device__ __forceinline__ void zero() {
+#pragma unroll
+        for (int e = 0; e < 4; e++) c[e] = l[e] = 0.f;
     }
+    __device__ __forceinline__ float get(int e) const { return c[e] + l[e]; }
+};
+
+// acc += A B for one 16 x 8 x 8 step, b = (B(2t, g), B(2t+1, g)).  B_EXACT or
+// A_EXACT: that operand is exact in tf32; HALF: the hi parts alone (results
+// that are rounded to 16 bits).
+template <bool A_EXACT, bool B_EXACT, bool HALF = false>
+__device__ __forceinline__ void mma_split(Acc &acc, const SplitA &a, float2 b) {
+    uint32_t b0 = __float_as_uint(b.x), b1 = __float_as_uint(b.y);
+    if (!B_EXACT) {
+        b0 = tf32(b.x), b1 = tf32(b.y);
+        if (!HALF) mma8(acc.l, a.hi, tf32(b.x - __uint_as_float(b0)), tf32(b.y - __uint_as_float(b1)));
+    }
+    if (!A_EXACT && !HALF) mma8(acc.l, a.lo, b0, b1);
+    mma8(acc.c, a.hi, b0, b1);
+}
+
+// The same into one float32 sum that is rounded to nearest: the step's terms
+// start from zero.
+template <bool A_EXACT, bool B_EXACT>
+__device__ __forceinline__ void mma_add(float (&c)[4], const SplitA &a, float2 b) {
+    float d[4];
+    uint32_t b0 = __float_as_uint(b.x), b1 = __float_as_uint(b.y);
+    if (!B_EXACT) {
+        b0 = tf32(b.x), b1 = tf32(b.y);
+        mma8_first(d, a.hi, tf32(b.x - __uint_as_float(b0)), tf32(b.y - __uint_as_float(b1)));
+        if (!A_EXACT) mma8(d, a.lo, b0, b1);
+        mma8(d, a.hi, b0, b1);
+    } else if (!A_EXACT) {
+        mma8_first(d, a.lo, b0, b1);
+        mma8(d, a.hi, b0, b1);
+    } else {
+        mma8_first(d, a.hi, b0, b1);
+    }
+#pragma unroll
+    for (int e = 0; e < 4; e++) c[e] += d[e];
 }
 
 // ---------------------------------------------------------------- fragments
@@ -158,7 +205,7 @@ __device__ __forceinline__ void cp_wait() {
     asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
 }
 
-// A tile of 64 rows x D columns, rows of `d` values (d <= D) at stride ld in
+// By all NT threads: a tile of 64 rows x D columns, rows of `d` values (d <= D) at stride ld in
 // memory, n rows of them; zeros elsewhere.  vec: 16-byte copies are allowed
 // (pointer, stride and d are multiples of 16 bytes).
 template <typename T, int D, int NT>
@@ -179,13 +226,55 @@ __device__ __forceinline__ void load_tile(T *dst, const T *src, int64_t ld, int 
     }
 }
 
-// A packed 64 x 64 float32 matrix into rows of stride 72.
+// Row stride of the 64 x 64 float32 matrices T and P, in memory as in shared
+// memory (a copy is one bulk copy, and a fragment's rows lie in different banks).
 constexpr int kLdT = kChunk + 8;
-template <int NT>
-__device__ __forceinline__ void load_square(float *dst, const float *src) {
-    for (int i = threadIdx.x; i < kChunk * kChunk / 4; i += NT) {
-        const int r = i >> 4, c = (i & 15) * 4;
-        cp_async16(dst + r * kLdT + c, src + r * kChunk + c, 16);
+constexpr int kSquare = kChunk * kLdT;
+
+// A chunk's operands arrive by bulk copies on an mbarrier.  Waits are bounded:
+// false once the limit is reached.
+__device__ __forceinline__ void bar_init(uint64_t *bar) {
+    asm volatile("mbarrier.init.shared::cta.b64 [%0], 1;" ::"r"((uint32_t)__cvta_generic_to_shared(bar)) : "memory");
+}
+__device__ __forceinline__ void bar_expect(uint64_t *bar, uint32_t bytes) {
+    asm volatile("mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;" ::"r"((uint32_t)__cvta_generic_to_shared(bar)),
+                 "r"(bytes)
+                 : "memory");
+}
+__device__ __forceinline__ bool bar_wait(uint64_t *bar, uint32_t parity) {
+    const uint32_t a = (uint32_t)__cvta_generic_to_shared(bar);
+    for (uint32_t it = 0; it < (1u << 19); it++) {  // about a second
+        uint32_t ok;
+        asm volatile(
+            "{\n\t.reg .pred p;\n\t"
+            "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
+            "selp.u32 %0, 1, 0, p;\n\t}"
+            : "=r"(ok)
+            : "r"(a), "r"(parity)
+            : "memory");
+        if (ok) return true;
+    }
+    return false;
+}
+__device__ __forceinline__ void bulk_load(void *dst, const void *src, uint32_t bytes, uint64_t *bar) {
+    asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(
+                     (uint32_t)__cvta_generic_to_shared(dst)),
+                 "l"(src), "r"(bytes), "r"((uint32_t)__cvta_generic_to_shared(bar))
+                 : "memory");
+}
+
+// Rows 0 .. n-1 of d values into a tile of D columns: with vec, one bulk copy a
+// row (row = the caller's row, one caller a row; rows beyond n are set to zero
+// and columns beyond d are left), else plain copies by all NT threads.
+template <typename T, int D>
+__device__ __forceinline__ void bulk_row(T *dst, const T *src, int64_t ld, int n, int d, int row, uint64_t *bar) {
+    constexpr int LD = tile_ld<T>(D);
+    if (row < n) {
+        bulk_load(dst + row * LD, src + row * ld, (uint32_t)(d * sizeof(T)), bar);
+    } else {
+        uint4 *p = reinterpret_cast<uint4 *>(dst + row * LD);
+#pragma unroll 1
+        for (int i = 0; i < D * (int)sizeof(T) / 16; i++) p[i] = make_uint4(0, 0, 0, 0);
     }
 }
 
@@ -254,9 +343,10 @@ cudaError_t zs_launch_delta_terms(int type, const zs::DeltaGeom &g, const zs::De
                                   int64_t *launches);
 // The recurrence over the chunks.  o (NULL: not formed), sn (the last states;
 // NULL: not written); states, us (NULL: not kept): the state each chunk
-// starts from (per chunk and value head dk x dv) and U (64 x dv).
+// starts from (per chunk and value head dk x dv) and U (64 x dv).  status: a
+// word that a bounded wait sets when it gives up.
 cudaError_t zs_launch_delta_chain(int type, const zs::DeltaGeom &g, const zs::DeltaTerms &t, const float *s0, void *o,
-                                  int64_t ldo, float *sn, float *states, float *us, cudaStream_t st,
+                                  int64_t ldo, float *sn, float *states, float *us, unsigned *status, cudaStream_t st,
                                   int64_t *launches);
 // The recurrence backwards (delta_bwd.cu): from the gradients of o and of the
 // last states (ds; NULL: zero), per chunk and value head the gradient of the
@@ -264,7 +354,7 @@ cudaError_t zs_launch_delta_chain(int type, const zs::DeltaGeom &g, const zs::De
 // gradient of the first states (ds0; NULL: not written).
 cudaError_t zs_launch_delta_rchain(int type, const zs::DeltaGeom &g, const zs::DeltaTerms &t, const void *dout,
                                    int64_t lddo, const float *ds, float *dends, float *dxs, void *dv, float *ds0,
-                                   cudaStream_t st, int64_t *launches);
+                                   unsigned *status, cudaStream_t st, int64_t *launches);
 // The gradients that the chunks give on their own.  parts (tokens x hv x dk
 // float32, one for dq and one for dk) are needed where value heads share a key
 // head; dq, dk: tokens x hk x dk.

@@ -23,15 +23,16 @@ using namespace zs;
 // ---------------------------------------------------------------- chain backwards
 
 // Laid out as the forward chain: a group of WK warps owns 16 value columns of
-// dS^T, 32 key columns a warp.
+// dS^T, 32 key columns a warp; the exchanges are the partial sums of
+// (K dS')^T, then dU^T, then dX^T and (scale c dO)^T, split where they are written.
 template <typename T, int DK>
 struct RChainCfg {
     static constexpr int WK = DK / 32;
-    static constexpr int NV = WK == 4 ? 2 : 4;
+    static constexpr int NV = DK == 32 ? 4 : 2;
     static constexpr int NT = 32 * WK * NV;
     static constexpr int NTILE = 8 / WK;
     static constexpr int COLS = 16 * NV;
-    static constexpr int STAGES = sizeof(T) == 2 || DK == 32 ? 2 : 1;  // as many as fit
+    static constexpr int STAGES = sizeof(T) == 2 ? 2 : 1;  // as many as fit
 };
 
 template <typename T, int DK>
@@ -39,57 +40,107 @@ struct RChainStage {
     T k[kChunk * tile_ld<T>(DK)];
     T q[kChunk * tile_ld<T>(DK)];
     T dout[kChunk * tile_ld<T>(RChainCfg<T, DK>::COLS)];
-    float t[kChunk * kLdT];
-    float p[kChunk * kLdT];
+    float t[kSquare];
+    float p[kSquare];
     float vec[kVec];
 };
+
+constexpr int kLdPair = 36;  // float4: rows of 32 split pairs, 64 bytes more apart
 
 template <typename T, int DK>
 struct RChainSmem {
     using C = RChainCfg<T, DK>;
     RChainStage<T, DK> st[C::STAGES];
-    float part[C::NV][C::WK][16 * kLdT];
-    float x[C::NV][16 * kLdT];
-    float u[C::NV][16 * kLdT];
+    // the partial sums, then (scale c dO)^T: 16 rows of split pairs
+    float part[C::NV][C::WK > 2 ? C::WK : 2][16 * kLdT];
+    float4 u[C::NV][16 * kLdPair];  // dU^T
+    float4 x[C::NV][16 * kLdPair];  // -(beta c dX)^T
+    uint64_t full[C::STAGES];
 };
 
-// c += A B where A may be exact in tf32 (its lo part then is zero) and B is float32
-template <bool EXACT_A>
-__device__ __forceinline__ void mma_split_b(float (&c)[4], const SplitA &a, float2 b) {
-    const uint32_t b0 = tf32(b.x), b1 = tf32(b.y);
-    if (!EXACT_A) mma8(c, a.lo, b0, b1);
-    mma8(c, a.hi, tf32(b.x - __uint_as_float(b0)), tf32(b.y - __uint_as_float(b1)));
-    mma8(c, a.hi, b0, b1);
+// (X(r0 + 2t, c0 + g), X(r0 + 2t + 1, c0 + g)) and the same eight columns on
+template <typename T, int LD>
+__device__ __forceinline__ void frag2_col(const T *x, int r0, int c0, float2 &f0, float2 &f1) {
+    const int lane = threadIdx.x & 31;
+    if constexpr (sizeof(T) == 2) {
+        const uint32_t a = (uint32_t)__cvta_generic_to_shared(x + (r0 + (lane & 7)) * LD + c0 + 8 * ((lane >> 3) & 1));
+        uint32_t u0, u1;
+        asm volatile("ldmatrix.sync.aligned.m8n8.x2.trans.shared.b16 {%0, %1}, [%2];" : "=r"(u0), "=r"(u1) : "r"(a) : "memory");
+        f0 = unpack2<T>(u0);
+        f1 = unpack2<T>(u1);
+    } else {
+        const T *p = x + (r0 + 2 * (lane & 3)) * LD + c0 + (lane >> 2);
+        f0 = make_float2(p[0], p[LD]);
+        f1 = make_float2(p[8], p[LD + 8]);
+    }
 }
 
 template <typename T, int DK>
 __global__ void __launch_bounds__(RChainCfg<T, DK>::NT, 1)
 k_delta_rchain(const DeltaGeom geo, const DeltaTerms terms, const T *__restrict__ dout, int64_t lddo,
                const float *__restrict__ ds, float *__restrict__ dends, float *__restrict__ dxs, T *__restrict__ dv,
-               float *__restrict__ ds0, int vec, int veco) {
+               float *__restrict__ ds0, int vec, int veco, unsigned *__restrict__ status) {
     using C = RChainCfg<T, DK>;
-    constexpr int WK = C::WK, NV = C::NV, NT = C::NT, NTILE = C::NTILE;
+    constexpr int WK = C::WK, NT = C::NT, NTILE = C::NTILE;
+    static_assert(2 * 16 * kLdT * sizeof(float) >= 16 * kLdPair * sizeof(float4), "room for the split pairs");
     constexpr int LD = tile_ld<T>(DK), LDO = tile_ld<T>(C::COLS);
     constexpr bool EXACT = sizeof(T) == 2;
     extern __shared__ __align__(16) uint8_t smem_raw[];
     RChainSmem<T, DK> &sm = *reinterpret_cast<RChainSmem<T, DK> *>(smem_raw);
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g = lane >> 2, t = lane & 3;
     const int grp = warp / WK, w = warp - grp * WK;
     const int si = blockIdx.x / geo.hv, hv = blockIdx.x - si * geo.hv, hk = hv / (geo.hv / geo.hk);
     const int vb = (int)blockIdx.y * C::COLS, v0 = vb + grp * 16, d0 = w * 32;
+    const int cols = min(C::COLS, geo.dv - vb);  // of the block's dO
     const int64_t state_at = ((int64_t)si * geo.hv + hv) * geo.dk * geo.dv;
+    const T *kp = (const T *)geo.k + (int64_t)hk * geo.dk, *qp = (const T *)geo.q + (int64_t)hk * geo.dk;
+    const T *op = dout + (int64_t)hv * geo.dv + vb;
+
+    if (tid == 0)
+        for (int i = 0; i < C::STAGES; i++) bar_init(&sm.full[i]);
+    // the copies leave the columns beyond dk and dv alone
+    if (vec && geo.dk < DK)
+        for (int i = tid; i < C::STAGES * kChunk * DK; i += NT) {
+            const int s = i / (kChunk * DK), rest = i - s * kChunk * DK, row = rest / DK, c = rest % DK;
+            if (c >= geo.dk) sm.st[s].k[row * LD + c] = sm.st[s].q[row * LD + c] = from_f32<T>(0.f);
+        }
+    if (veco && cols < C::COLS)
+        for (int i = tid; i < C::STAGES * kChunk * C::COLS; i += NT) {
+            const int s = i / (kChunk * C::COLS), rest = i - s * kChunk * C::COLS, row = rest / C::COLS, c = rest % C::COLS;
+            if (c >= cols) sm.st[s].dout[row * LDO + c] = from_f32<T>(0.f);
+        }
+    asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+    __syncthreads();
 
     auto load = [&](int c, int stage) {
         const int2 ch = geo.chunk[c];
         RChainStage<T, DK> &s = sm.st[stage];
         const int64_t slot = (int64_t)c * geo.hv + hv;
-        load_tile<T, DK, NT>(s.k, (const T *)geo.k + (int64_t)ch.x * geo.ldk + (int64_t)hk * geo.dk, geo.ldk, ch.y, geo.dk, vec);
-        load_tile<T, DK, NT>(s.q, (const T *)geo.q + (int64_t)ch.x * geo.ldq + (int64_t)hk * geo.dk, geo.ldq, ch.y, geo.dk, vec);
-        load_tile<T, C::COLS, NT>(s.dout, dout + (int64_t)ch.x * lddo + (int64_t)hv * geo.dv + vb, lddo, ch.y, geo.dv - vb, veco);
-        load_square<NT>(s.t, terms.t + slot * (kChunk * kChunk));
-        load_square<NT>(s.p, terms.p + slot * (kChunk * kChunk));
-        for (int i = threadIdx.x; i < kVec / 4; i += NT) cp_async16(s.vec + 4 * i, terms.vec + slot * kVec + 4 * i, 16);
-        cp_commit();
+        uint64_t *bar = &sm.full[stage];
+        if (tid == 0) {
+            const uint32_t e = (uint32_t)(ch.y * sizeof(T));
+            bar_expect(bar, (vec ? 2 * e * geo.dk : 0u) + (veco ? e * cols : 0u) + 2 * kSquare * 4 + kVec * 4);
+            bulk_load(s.t, terms.t + slot * kSquare, kSquare * 4, bar);
+            bulk_load(s.p, terms.p + slot * kSquare, kSquare * 4, bar);
+            bulk_load(s.vec, terms.vec + slot * kVec, kVec * 4, bar);
+        }
+        if (vec) {
+            for (int r = tid; r < 2 * kChunk; r += NT) {
+                if (r < kChunk)
+                    bulk_row<T, DK>(s.k, kp + (int64_t)ch.x * geo.ldk, geo.ldk, ch.y, geo.dk, r, bar);
+                else
+                    bulk_row<T, DK>(s.q, qp + (int64_t)ch.x * geo.ldq, geo.ldq, ch.y, geo.dk, r - kChunk, bar);
+            }
+        } else {
+            load_tile<T, DK, NT>(s.k, kp + (int64_t)ch.x * geo.ldk, geo.ldk, ch.y, geo.dk, 0);
+            load_tile<T, DK, NT>(s.q, qp + (int64_t)ch.x * geo.ldq, geo.ldq, ch.y, geo.dk, 0);
+        }
+        if (veco) {
+            for (int r = tid; r < kChunk; r += NT)
+                bulk_row<T, C::COLS>(s.dout, op + (int64_t)ch.x * lddo, lddo, ch.y, cols, r, bar);
+        } else {
+            load_tile<T, C::COLS, NT>(s.dout, op + (int64_t)ch.x * lddo, lddo, ch.y, cols, 0);
+        }
     };
 
     float D[4][4];  // dS^T: rows v0 + g, + 8, columns d0 + 8 j + 2t, + 1
@@ -113,9 +164,13 @@ k_delta_rchain(const DeltaGeom geo, const DeltaTerms terms, const T *__restrict_
     const int c0 = geo.first[si], c1 = geo.first[si + 1];
     if (c0 < c1) load(c1 - 1, 0);
     for (int c = c1 - 1; c >= c0; c--) {
-        const int stage = C::STAGES == 2 ? (c1 - 1 - c) & 1 : 0;
-        cp_wait<0>();
-        __syncthreads();  // the stage is complete, and every warp is done with the previous chunk
+        const int it = c1 - 1 - c, stage = C::STAGES == 2 ? it & 1 : 0;
+        // the stage is complete, and every warp is done with the previous chunk
+        const bool ok = bar_wait(&sm.full[stage], (C::STAGES == 2 ? it >> 1 : it) & 1);
+        if (!__syncthreads_and(ok)) {
+            if (tid == 0) atomicOr(status, 1u);
+            return;
+        }
         if (C::STAGES == 2 && c > c0) load(c - 1, stage ^ 1);
         RChainStage<T, DK> &st = sm.st[stage];
         const int2 ch = geo.chunk[c];
@@ -129,36 +184,42 @@ k_delta_rchain(const DeltaGeom geo, const DeltaTerms terms, const T *__restrict_
             for (int j = 0; j < 4; j++) a[j].set(D[j]);
             float *part = sm.part[grp][w];
 #pragma unroll
-            for (int n = 0; n < 8; n++) {
-                float2 b[4];
-                float r[4] = {};
-                frag4<T, LD, false>(st.k, n * 8, d0, b);
+            for (int h = 0; h < 8; h += 4) {
+                Acc r[4];
+                float2 b[4][4];
 #pragma unroll
-                for (int j = 0; j < 4; j++) mma_split<EXACT>(r, a[j], b[j]);
-                *reinterpret_cast<float2 *>(part + g * kLdT + n * 8 + 2 * t) = make_float2(r[0], r[1]);
-                *reinterpret_cast<float2 *>(part + (g + 8) * kLdT + n * 8 + 2 * t) = make_float2(r[2], r[3]);
+                for (int n = 0; n < 4; n++) {
+                    r[n].zero();
+                    frag4<T, LD, false>(st.k, (h + n) * 8, d0, b[n]);
+                }
+#pragma unroll
+                for (int j = 0; j < 4; j++)
+#pragma unroll
+                    for (int n = 0; n < 4; n++) mma_split<false, EXACT>(r[n], a[j], b[n][j]);
+#pragma unroll
+                for (int n = 0; n < 4; n++) {
+                    float *p = part + g * kLdT + (h + n) * 8 + 2 * t;
+                    *reinterpret_cast<float2 *>(p) = make_float2(r[n].get(0), r[n].get(1));
+                    *reinterpret_cast<float2 *>(p + 8 * kLdT) = make_float2(r[n].get(2), r[n].get(3));
+                }
             }
         }
-        // dO^T as an A operand: rows v, columns the tokens of tile k
-        auto dout_at = [&](int k, float (&f)[4]) {
-            const T *x = st.dout + (k * 8 + 2 * t) * LDO + grp * 16 + g;
-            f[0] = to_f32(x[0]), f[1] = to_f32(x[LDO]);
-            f[2] = to_f32(x[8]), f[3] = to_f32(x[LDO + 8]);
-        };
-        // (P^T dO)^T at the warp's token tiles: P's rows from the tile on
-        float du[NTILE][4] = {};
+        // (P^T dO)^T at the warp's token tiles: dO^T is the A operand, P's rows from the tile on
+        Acc du[NTILE];
+#pragma unroll
+        for (int i = 0; i < NTILE; i++) du[i].zero();
 #pragma unroll
         for (int k = 0; k < 8; k++) {
-            float f[4];
-            dout_at(k, f);
+            float2 f0, f1;
+            frag2_col<T, LDO>(st.dout, k * 8, grp * 16, f0, f1);
             SplitA a;
-            a.set(f);
+            a.set(f0.x, f0.y, f1.x, f1.y);
 #pragma unroll
             for (int i = 0; i < NTILE; i++) {
                 const int n = tile_of<WK>(w, i);
                 if (k < n) continue;
                 const float *p = st.p + (k * 8 + 2 * t) * kLdT + n * 8 + g;
-                mma_split_b<EXACT>(du[i], a, make_float2(p[0], p[kLdT]));
+                mma_split<EXACT, false>(du[i], a, make_float2(p[0], p[kLdT]));
             }
         }
         group_sync<WK>(grp);
@@ -172,76 +233,82 @@ k_delta_rchain(const DeltaGeom geo, const DeltaTerms terms, const T *__restrict_
                 const float2 z = *reinterpret_cast<const float2 *>(sm.part[grp][p] + (g + 8) * kLdT + n);
                 lo.x += y.x, lo.y += y.y, hi.x += z.x, hi.y += z.y;
             }
-            const float ea = st.vec[kChunk + n], eb = st.vec[kChunk + n + 1];
-            *reinterpret_cast<float2 *>(sm.u[grp] + g * kLdT + n) =
-                make_float2(fmaf(ea, lo.x, du[i][0]), fmaf(eb, lo.y, du[i][1]));
-            *reinterpret_cast<float2 *>(sm.u[grp] + (g + 8) * kLdT + n) =
-                make_float2(fmaf(ea, hi.x, du[i][2]), fmaf(eb, hi.y, du[i][3]));
+            const float2 ev = *reinterpret_cast<const float2 *>(st.vec + kChunk + n);
+            float4 *u = sm.u[grp] + g * kLdPair + n / 2;
+            u[0] = split_pair(fmaf(ev.x, lo.x, du[i].get(0)), fmaf(ev.y, lo.y, du[i].get(1)));
+            u[8 * kLdPair] = split_pair(fmaf(ev.x, hi.x, du[i].get(2)), fmaf(ev.y, hi.y, du[i].get(3)));
         }
         group_sync<WK>(grp);
         // dX^T = dU^T T at the warp's token tiles: T's rows from the tile on
         {
-            float x[NTILE][4] = {};
+            Acc x[NTILE];
+#pragma unroll
+            for (int i = 0; i < NTILE; i++) x[i].zero();
 #pragma unroll
             for (int k = 0; k < 8; k++) {
-                const float2 y = *reinterpret_cast<const float2 *>(sm.u[grp] + g * kLdT + k * 8 + 2 * t);
-                const float2 z = *reinterpret_cast<const float2 *>(sm.u[grp] + (g + 8) * kLdT + k * 8 + 2 * t);
                 SplitA a;
-                a.set(y.x, y.y, z.x, z.y);
+                a.set(sm.u[grp][g * kLdPair + k * 4 + t], sm.u[grp][(g + 8) * kLdPair + k * 4 + t]);
 #pragma unroll
                 for (int i = 0; i < NTILE; i++) {
                     const int n = tile_of<WK>(w, i);
                     if (k < n) continue;
                     const float *p = st.t + (k * 8 + 2 * t) * kLdT + n * 8 + g;
-                    mma_split<false>(x[i], a, make_float2(p[0], p[kLdT]));
+                    mma_split<false, false>(x[i], a, make_float2(p[0], p[kLdT]));
                 }
             }
+            // the partial sums' place is free: (scale c dO)^T, split, goes there
+            float4 *y = reinterpret_cast<float4 *>(sm.part[grp][0]);
 #pragma unroll
             for (int i = 0; i < NTILE; i++) {
-                const int n = tile_of<WK>(w, i) * 8 + 2 * t;
-                *reinterpret_cast<float2 *>(sm.x[grp] + g * kLdT + n) = make_float2(x[i][0], x[i][1]);
-                *reinterpret_cast<float2 *>(sm.x[grp] + (g + 8) * kLdT + n) = make_float2(x[i][2], x[i][3]);
+                const int n = tile_of<WK>(w, i) * 8 + 2 * t, at = g * kLdPair + n / 2;
+                const float2 cv = *reinterpret_cast<const float2 *>(st.vec + n);
+                const float2 bv = *reinterpret_cast<const float2 *>(st.vec + 2 * kChunk + n);
+                const float v[4] = {x[i].get(0), x[i].get(1), x[i].get(2), x[i].get(3)};
+                const float ba = -bv.x * cv.x, bb = -bv.y * cv.y;
+                sm.x[grp][at] = split_pair(ba * v[0], bb * v[1]);
+                sm.x[grp][at + 8 * kLdPair] = split_pair(ba * v[2], bb * v[3]);
+                float2 f0, f1;
+                frag2_col<T, LDO>(st.dout, n - 2 * t, grp * 16, f0, f1);
+                const float ca = geo.scale * cv.x, cb = geo.scale * cv.y;
+                y[at] = split_pair(ca * f0.x, cb * f0.y);
+                y[at + 8 * kLdPair] = split_pair(ca * f1.x, cb * f1.y);
 #pragma unroll
                 for (int e = 0; e < 4; e++) {
-                    const int v = v0 + g + (e >> 1) * 8, tok = n + (e & 1);
-                    if (v < geo.dv) {
-                        dxs[(slot * kChunk + tok) * geo.dv + v] = x[i][e];
+                    const int vc = v0 + g + (e >> 1) * 8, tok = n + (e & 1);
+                    if (vc < geo.dv) {
+                        dxs[(slot * kChunk + tok) * geo.dv + vc] = v[e];
                         if (tok < ch.y)
-                            dv[((int64_t)(ch.x + tok) * geo.hv + hv) * geo.dv + v] =
-                                from_f32<T>(st.vec[2 * kChunk + tok] * x[i][e]);
+                            dv[((int64_t)(ch.x + tok) * geo.hv + hv) * geo.dv + vc] =
+                                from_f32<T>((e & 1 ? bv.y : bv.x) * v[e]);
                     }
                 }
             }
         }
         group_sync<WK>(grp);
-        // dS^T = c_64 dS'^T + (scale c dO)^T Q - (beta c dX)^T K
-        float acc[4][4] = {};
+        // dS^T = c_64 dS'^T + (scale c dO)^T Q - (beta c dX)^T K, each sum from zero
+        Acc ak[4], aq[4];
+#pragma unroll
+        for (int j = 0; j < 4; j++) ak[j].zero(), aq[j].zero();
+        const float4 *yq = reinterpret_cast<const float4 *>(sm.part[grp][0]);
 #pragma unroll
         for (int k = 0; k < 8; k++) {
-            const int tok = k * 8 + 2 * t;
-            const float ca = st.vec[tok], cb = st.vec[tok + 1];
-            const float ba = -ca * st.vec[2 * kChunk + tok], bb = -cb * st.vec[2 * kChunk + tok + 1];
-            const float2 y = *reinterpret_cast<const float2 *>(sm.x[grp] + g * kLdT + tok);
-            const float2 z = *reinterpret_cast<const float2 *>(sm.x[grp] + (g + 8) * kLdT + tok);
+            const int at = g * kLdPair + k * 4 + t;
             SplitA a;
             float2 b[4];
-            a.set(ba * y.x, bb * y.y, ba * z.x, bb * z.y);
+            a.set(sm.x[grp][at], sm.x[grp][at + 8 * kLdPair]);
             frag4<T, LD, true>(st.k, k * 8, d0, b);
 #pragma unroll
-            for (int j = 0; j < 4; j++) mma_split<EXACT>(acc[j], a, b[j]);
-            float f[4];
-            dout_at(k, f);
-            const float sa = geo.scale * ca, sb = geo.scale * cb;
-            a.set(sa * f[0], sb * f[1], sa * f[2], sb * f[3]);
+            for (int j = 0; j < 4; j++) mma_split<false, EXACT>(ak[j], a, b[j]);
+            a.set(yq[at], yq[at + 8 * kLdPair]);
             frag4<T, LD, true>(st.q, k * 8, d0, b);
 #pragma unroll
-            for (int j = 0; j < 4; j++) mma_split<EXACT>(acc[j], a, b[j]);
+            for (int j = 0; j < 4; j++) mma_split<false, EXACT>(aq[j], a, b[j]);
         }
         const float cend = st.vec[kChunk - 1];
 #pragma unroll
         for (int j = 0; j < 4; j++)
 #pragma unroll
-            for (int e = 0; e < 4; e++) D[j][e] = fmaf(cend, D[j][e], acc[j][e]);
+            for (int e = 0; e < 4; e++) D[j][e] = fmaf(cend, D[j][e], ak[j].get(e) + aq[j].get(e));
         if (C::STAGES == 1) {
             __syncthreads();  // the only stage is free
             if (c > c0) load(c - 1, 0);
@@ -394,16 +461,16 @@ k_delta_grads(const DeltaGeom geo, const DeltaTerms terms, const T *__restrict__
 #pragma unroll
             for (int j = 0; j < 4; j++) {
                 const float2 b = frag1<float, kLdS>(s.s, d0 + 8 * j, c);
-                mma_split_b<EXACT>(F[j], ao, b);
-                mma_split<false>(E[j], ax, b);
-                mma_split<false>(H[j], au, frag1<float, kLdS>(s.ds, d0 + 8 * j, c));
+                mma_add<EXACT, false>(F[j], ao, b);
+                mma_add<false, false>(E[j], ax, b);
+                mma_add<false, false>(H[j], au, frag1<float, kLdS>(s.ds, d0 + 8 * j, c));
             }
 #pragma unroll
             for (int j = 0; j < PT; j++) {
                 if (p0 + 8 * j > m0 + 8) continue;  // above the diagonal
                 const float2 b = frag1<float, kLdS>(s.u, p0 + 8 * j, c);
-                mma_split_b<EXACT>(dp[j], ao, b);
-                mma_split<false>(da[j], ax, b);
+                mma_add<EXACT, false>(dp[j], ao, b);
+                mma_add<false, false>(da[j], ax, b);
             }
         }
         // dX_i . v_i and <S, dS'>
@@ -440,8 +507,8 @@ k_delta_grads(const DeltaGeom geo, const DeltaTerms terms, const T *__restrict__
             for (int j = 0; j < PT; j++) {
                 if (p0 + 8 * j > m0 + 8) continue;
                 const float2 b = frag1<T, LD>(sm.k, p0 + 8 * j, c);
-                mma_split<EXACT, EXACT>(kk[j], ak, b);
-                mma_split<EXACT, EXACT>(qk[j], aq, b);
+                mma_add<EXACT, EXACT>(kk[j], ak, b);
+                mma_add<EXACT, EXACT>(qk[j], aq, b);
             }
         }
         // r, beta w and their sums with the raw products
@@ -573,8 +640,8 @@ k_delta_grads(const DeltaGeom geo, const DeltaTerms terms, const T *__restrict__
         }
 #pragma unroll
         for (int j = 0; j < 4; j++) {
-            mma_split<EXACT>(aq[j], ar, b[j]);
-            mma_split<EXACT>(ak[j], aw, b[j]);
+            mma_add<false, EXACT>(aq[j], ar, b[j]);
+            mma_add<false, EXACT>(ak[j], aw, b[j]);
         }
     }
     // dk += r^T Q + (beta w)^T K: the transposes' rows, columns from the diagonal on
@@ -589,8 +656,8 @@ k_delta_grads(const DeltaGeom geo, const DeltaTerms terms, const T *__restrict__
         aw.set(sm.sq.w[at], sm.sq.w[at + kLdT], sm.sq.w[at + 8], sm.sq.w[at + kLdT + 8]);
 #pragma unroll
         for (int j = 0; j < 4; j++) {
-            mma_split<EXACT>(ak[j], ar, bq[j]);
-            mma_split<EXACT>(ak[j], aw, bk[j]);
+            mma_add<false, EXACT>(ak[j], ar, bq[j]);
+            mma_add<false, EXACT>(ak[j], aw, bk[j]);
         }
     }
 #pragma unroll
@@ -631,7 +698,7 @@ k_delta_join(const float *__restrict__ dqp, const float *__restrict__ dkp, int64
 
 template <typename T, int DK>
 cudaError_t rchain_dk(const DeltaGeom &g, const DeltaTerms &t, const void *dout, int64_t lddo, const float *ds,
-                      float *dends, float *dxs, void *dv, float *ds0, cudaStream_t st) {
+                      float *dends, float *dxs, void *dv, float *ds0, unsigned *status, cudaStream_t st) {
     using C = RChainCfg<T, DK>;
     static_assert(sizeof(RChainSmem<T, DK>) <= 232448, "shared memory of a block");
     static const cudaError_t attr = cudaFuncSetAttribute(
@@ -641,7 +708,7 @@ cudaError_t rchain_dk(const DeltaGeom &g, const DeltaTerms &t, const void *dout,
     const int veco = mult16(dout, lddo, g.dv, sizeof(T));
     const dim3 grid((unsigned)(g.nseq * g.hv), (unsigned)((g.dv + C::COLS - 1) / C::COLS));
     k_delta_rchain<T, DK><<<grid, C::NT, sizeof(RChainSmem<T, DK>), st>>>(g, t, (const T *)dout, lddo, ds, dends, dxs,
-                                                                          (T *)dv, ds0, vec, veco);
+                                                                          (T *)dv, ds0, vec, veco, status);
     return cudaGetLastError();
 }
 
@@ -664,10 +731,10 @@ cudaError_t grads_dk(const DeltaGeom &g, const DeltaTerms &t, const void *dout, 
 }  // namespace
 
 cudaError_t zs_launch_delta_rchain(int type, const DeltaGeom &g, const DeltaTerms &t, const void *dout, int64_t lddo,
-                                   const float *ds, float *dends, float *dxs, void *dv, float *ds0, cudaStream_t st,
-                                   int64_t *launches) {
+                                   const float *ds, float *dends, float *dxs, void *dv, float *ds0, unsigned *status,
+                                   cudaStream_t st, int64_t *launches) {
     ++*launches;
-    return DELTA_TYPE(rchain_dk, g, t, dout, lddo, ds, dends, dxs, dv, ds0, st);
+    return DELTA_TYPE(rchain_dk, g, t, dout, lddo, ds, dends, dxs, dv, ds0, status, st);
 }
 
 cudaError_t zs_launch_delta_grads(int type, const DeltaGeom &g, const DeltaTerms &t, const void *dout, int64_t lddo,

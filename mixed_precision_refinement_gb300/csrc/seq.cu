@@ -131,7 +131,7 @@ struct DeltaWork {
     float *states = nullptr, *us = nullptr, *dends = nullptr, *dxs = nullptr, *dqp = nullptr, *dkp = nullptr;
 
     void carve(zs::Carve &c, const zsolve_delta_args *a, bool out) {
-        const size_t slots = (size_t)nchunks * a->hv, sq = (size_t)zs::kChunk * zs::kChunk;
+        const size_t slots = (size_t)nchunks * a->hv, sq = (size_t)zs::kSquare;
         first = c.take<int>((size_t)a->nseq + 1);
         seq = c.take<int2>((size_t)a->nseq);
         chunk = c.take<int2>((size_t)nchunks);
@@ -331,7 +331,7 @@ int zsolve_delta(zsolve_seq *s, const zsolve_delta_args *a, void *o, int64_t ldo
     w.bind(&g);
     SEQ_CU(zs_launch_delta_plan(a->offsets, a->nseq, a->tokens, w.nchunks, w.first, w.seq, w.chunk, s->st, &s->launches));
     SEQ_CU(zs_launch_delta_terms(a->type, g, w.terms, s->st, &s->launches));
-    SEQ_CU(zs_launch_delta_chain(a->type, g, w.terms, a->s0, o, ldo, sn, nullptr, nullptr, s->st, &s->launches));
+    SEQ_CU(zs_launch_delta_chain(a->type, g, w.terms, a->s0, o, ldo, sn, nullptr, nullptr, s->d_status, s->st, &s->launches));
     return ZSOLVE_OK;
 }
 
@@ -367,9 +367,11 @@ int zsolve_delta_bwd(zsolve_seq *s, const zsolve_delta_args *a, const void *dout
         SEQ_CU(zs_launch_delta_terms(a->type, g, w.terms, s->st, &s->launches));
         // the states and U once more: keeping them from the forward pass would hold 96 KB a chunk and head
         // at 128 x 128 until the backward pass
-        SEQ_CU(zs_launch_delta_chain(a->type, g, w.terms, a->s0, nullptr, 0, nullptr, w.states, w.us, s->st, &s->launches));
+        SEQ_CU(zs_launch_delta_chain(a->type, g, w.terms, a->s0, nullptr, 0, nullptr, w.states, w.us, s->d_status, s->st,
+                                     &s->launches));
     }
-    SEQ_CU(zs_launch_delta_rchain(a->type, g, w.terms, dout, lddo, ds, w.dends, w.dxs, dv, ds0, s->st, &s->launches));
+    SEQ_CU(zs_launch_delta_rchain(a->type, g, w.terms, dout, lddo, ds, w.dends, w.dxs, dv, ds0, s->d_status, s->st,
+                                  &s->launches));
     if (a->tokens > 0)
         SEQ_CU(zs_launch_delta_grads(a->type, g, w.terms, dout, lddo, w.states, w.dends, w.us, w.dxs, w.dqp, w.dkp, dq,
                                      dk, dg, dbeta, s->st, &s->launches));

@@ -101,7 +101,7 @@ struct TermSmem {
         float a[2][kChunk * kLdT];  // a value head each, once the products are done
     };
     float kk[kChunk * kLdA];
-    float qk[kChunk * kLdA];
+    float kq[kChunk * kLdA];  // K Q^T: the transpose of Q K^T
     float diag[2][4][16 * kLdD];
     float bh[2][kChunk], bl[2][kChunk], beta[2][kChunk];
 };
@@ -113,7 +113,7 @@ struct Block {
 
 template <typename T, int DK>
 __global__ void __launch_bounds__(kTermThreads, 2)
-k_delta_terms(const DeltaGeom geo, const DeltaTerms out, int vec) {
+k_delta_terms(const DeltaGeom geo, const DeltaTerms out) {
     extern __shared__ __align__(16) uint8_t smem_raw[];
     TermSmem<T, DK> &sm = *reinterpret_cast<TermSmem<T, DK> *>(smem_raw);
     constexpr bool EXACT = sizeof(T) == 2;
@@ -123,8 +123,8 @@ k_delta_terms(const DeltaGeom geo, const DeltaTerms out, int vec) {
     if (n == 0) return;
     const int hk = blockIdx.y, tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const int g = lane >> 2, t = lane & 3;
-    load_tile<T, DK, kTermThreads>(sm.k, (const T *)geo.k + (int64_t)ch.x * geo.ldk + (int64_t)hk * geo.dk, geo.ldk, n, geo.dk, vec);
-    load_tile<T, DK, kTermThreads>(sm.q, (const T *)geo.q + (int64_t)ch.x * geo.ldq + (int64_t)hk * geo.dk, geo.ldq, n, geo.dk, vec);
+    load_tile<T, DK, kTermThreads>(sm.k, (const T *)geo.k + (int64_t)ch.x * geo.ldk + (int64_t)hk * geo.dkp, geo.ldk, n, geo.dkp);
+    load_tile<T, DK, kTermThreads>(sm.q, (const T *)geo.q + (int64_t)ch.x * geo.ldq + (int64_t)hk * geo.dkp, geo.ldq, n, geo.dkp);
     cp_commit();
     cp_wait<0>();
     __syncthreads();
@@ -132,7 +132,6 @@ k_delta_terms(const DeltaGeom geo, const DeltaTerms out, int vec) {
         // warps 0-3: rows 16 w of K K^T, warps 4-7: of Q K^T; tiles on and below the diagonal
         const int m = (warp & 3) * 16;
         const T *x = warp < 4 ? sm.k : sm.q;
-        float *dst = warp < 4 ? sm.kk : sm.qk;
         Acc acc[8];
 #pragma unroll
         for (int j = 0; j < 8; j++) acc[j].zero();
@@ -155,12 +154,18 @@ k_delta_terms(const DeltaGeom geo, const DeltaTerms out, int vec) {
 #pragma unroll
         for (int j = 0; j < 8; j++) {
             if (j * 8 > m + 8) continue;
-            *reinterpret_cast<float2 *>(dst + (m + g) * kLdA + j * 8 + 2 * t) = make_float2(acc[j].get(0), acc[j].get(1));
-            *reinterpret_cast<float2 *>(dst + (m + g + 8) * kLdA + j * 8 + 2 * t) = make_float2(acc[j].get(2), acc[j].get(3));
+            const float v[4] = {acc[j].get(0), acc[j].get(1), acc[j].get(2), acc[j].get(3)};
+            if (warp < 4) {
+                *reinterpret_cast<float2 *>(sm.kk + (m + g) * kLdA + j * 8 + 2 * t) = make_float2(v[0], v[1]);
+                *reinterpret_cast<float2 *>(sm.kk + (m + g + 8) * kLdA + j * 8 + 2 * t) = make_float2(v[2], v[3]);
+            } else {
+#pragma unroll
+                for (int e = 0; e < 4; e++) sm.kq[(j * 8 + 2 * t + (e & 1)) * kLdA + m + g + (e >> 1) * 8] = v[e];
+            }
         }
     }
     const int group = geo.hv / geo.hk, half = warp >> 2, w = warp & 3, ht = tid & 127;
-    __syncthreads();  // kk, qk complete; k and q give way to A
+    __syncthreads();  // kk, kq complete; k and q give way to A
     for (int r0 = 0; r0 < group; r0 += 2) {
         const int r = r0 + half;
         if (r < group) {  // the half blocks go their own way: barriers of 128 threads
@@ -183,18 +188,15 @@ k_delta_terms(const DeltaGeom geo, const DeltaTerms out, int vec) {
                 v[kChunk + ht] = expf((bh[kChunk - 1] - bh[ht]) + (bl[kChunk - 1] - bl[ht]));
                 v[2 * kChunk + ht] = beta[ht];
             }
-            float *P = out.p ? out.p + slot * kSquare : nullptr, *Tg = out.t + slot * kSquare;
+            float *TP = out.tp + slot * kSquare;
 #pragma unroll 4
             for (int i = ht; i < kChunk * kChunk; i += 128) {
-                const int y = i >> 6, x = i & 63;
-                float av = 0.f, pv = 0.f;
-                if (x <= y) {
-                    const float e = expf((bh[y] - bh[x]) + (bl[y] - bl[x]));
-                    if (x < y) av = beta[y] * sm.kk[y * kLdA + x] * e;
-                    pv = geo.scale * sm.qk[y * kLdA + x] * e;
-                }
-                A[y * kLdT + x] = av;
-                if (P) P[y * kLdT + x] = pv;
+                const int r = i >> 6, c = i & 63, y = max(r, c), x = min(r, c);
+                const float e = expf((bh[y] - bh[x]) + (bl[y] - bl[x]));
+                if (c < r)
+                    A[r * kLdT + c] = beta[r] * sm.kk[r * kLdA + c] * e;
+                else
+                    TP[r * kLdT + c] = geo.scale * sm.kq[r * kLdA + c] * e;  // P(c, r)
             }
             asm volatile("bar.sync %0, 128;" ::"r"(half + 1) : "memory");
             {  // diagonal block w: lane l its column l (the upper half of the warp repeats the lower)
@@ -217,7 +219,7 @@ k_delta_terms(const DeltaGeom geo, const DeltaTerms out, int vec) {
 #pragma unroll
                     for (int i = 0; i < 16; i++) {
                         sm.diag[half][w][i * kLdD + c] = x[i];
-                        Tg[(w * 16 + i) * kLdT + w * 16 + c] = x[i];
+                        if (i > c) TP[(w * 16 + i) * kLdT + w * 16 + c] = x[i];
                     }
                 }
             }
@@ -267,16 +269,26 @@ k_delta_terms(const DeltaGeom geo, const DeltaTerms out, int vec) {
                     if (i < 3) y[i][nn].set(v);
 #pragma unroll
                     for (int e = 0; e < 4; e++)
-                        Tg[(i * 16 + nn * 8 + 2 * t + (e & 1)) * kLdT + w * 16 + g + (e >> 1) * 8] = v[e];
+                        TP[(i * 16 + nn * 8 + 2 * t + (e & 1)) * kLdT + w * 16 + g + (e >> 1) * 8] = v[e];
                 }
-            }
-            // above the diagonal blocks: zero
-            for (int i = ht; i < 6 * 64; i += 128) {
-                const int b = i >> 6, q = i & 63, bi = b < 3 ? 0 : b < 5 ? 1 : 2, bj = b < 3 ? b + 1 : b < 5 ? b - 1 : 3;
-                *reinterpret_cast<float4 *>(Tg + (bi * 16 + (q >> 2)) * kLdT + bj * 16 + (q & 3) * 4) = make_float4(0.f, 0.f, 0.f, 0.f);
             }
             asm volatile("bar.sync %0, 128;" ::"r"(half + 1) : "memory");  // A, diag free for the next head
         }
+    }
+}
+
+// ---------------------------------------------------------------- alignment
+
+// Heads whose rows the bulk copies cannot address (16 bytes) copied to rows
+// that they can, each head padded with zeros to dp values.
+template <typename T>
+__global__ void __launch_bounds__(256)
+k_delta_pack(const T *__restrict__ src, int64_t ld, int64_t tokens, int heads, int d, int dp, T *__restrict__ dst) {
+    const int64_t n = tokens * heads * dp;
+    for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < n; i += (int64_t)gridDim.x * 256) {
+        const int64_t row = i / dp, tok = row / heads;
+        const int c = (int)(i - row * dp), h = (int)(row - tok * heads);
+        dst[i] = c < d ? src[tok * ld + (int64_t)h * d + c] : from_f32<T>(0.f);
     }
 }
 
@@ -287,98 +299,105 @@ k_delta_terms(const DeltaGeom geo, const DeltaTerms out, int vec) {
 // group the 32 x 16 block of S^T for key columns 32 w ..: its accumulators,
 // which are also its A operands.  Per chunk the group exchanges three small
 // results through shared memory: the partial sums of S^T K^T (over the warps'
-// key columns), X^T and U^T, the latter two already split into tf32 parts by
-// the warp that wrote them; token tiles of 8 are dealt so that the triangular
-// products are equal shares (tile_of).  Two stages of chunk operands arrive by
-// bulk copies while the chunk before is at work.
+// key columns), X^T and U^T, the latter two already split by the warp that
+// wrote them; token tiles of 8 are dealt so that the triangular products are
+// equal shares (tile_of).  One more warp keeps two stages of chunk operands
+// filled.  The groups do not wait for each other, so one's
+// exchanges run beside the other's products.
 template <typename T, int DK>
 struct ChainCfg {
     static constexpr int WK = DK / 32;
     static constexpr int NV = DK == 32 ? 4 : 2;
-    static constexpr int NT = 32 * WK * NV;
+    static constexpr int NC = 32 * WK * NV;  // threads of the groups
+    static constexpr int NT = NC + 32;
     static constexpr int NTILE = 8 / WK;
-    static constexpr int LD = tile_ld<T>(DK);
+    static constexpr int COLS = 16 * NV;
+    static constexpr int LD = tile_ld<T>(DK), LDV = tile_ld<T>(COLS);
     // two stages of the chunk's operands where they fit
-    static constexpr int STAGES = sizeof(T) == 2 || DK < 128 ? 2 : 1;
+    static constexpr int STAGES = sizeof(T) == 2 || DK == 64 ? 2 : 1;
 };
 
 template <typename T, int DK>
 struct ChainStage {
     T k[kChunk * tile_ld<T>(DK)];
     T q[kChunk * tile_ld<T>(DK)];
-    float t[kSquare];
-    float p[kSquare];
+    T v[kChunk * tile_ld<T>(ChainCfg<T, DK>::COLS)];
+    float tp[kSquare];
     float vec[kVec];
 };
-
-// Rows of 32 split pairs, 64 bytes more apart: the rows of a fragment's loads lie in different banks.
-constexpr int kLdPair = 36;
 
 template <typename T, int DK>
 struct ChainSmem {
     using C = ChainCfg<T, DK>;
     ChainStage<T, DK> st[C::STAGES];
     float part[C::NV][C::WK][16 * kLdT];
-    float4 x[C::NV][16 * kLdPair];  // X^T, then the chunk's outputs
-    float4 u[C::NV][16 * kLdPair];  // (e U)^T
-    float2 un[C::NV][16 * kLdPair]; // U^T in tf32, for P U
-    uint64_t full[C::STAGES];
+    float4 x[C::NV][16 * kLdPair];   // X^T, then the chunk's outputs
+    float4 u[C::NV][16 * kLdPair];   // (e U)^T
+    float2 un[C::NV][16 * kLdPair];  // U^T, for P U
+    uint64_t full[C::STAGES], empty[C::STAGES];
+    int abort_word;
 };
 
 template <typename T, int DK, bool OUT>
 __global__ void __launch_bounds__(ChainCfg<T, DK>::NT, 1)
 k_delta_chain(const DeltaGeom geo, const DeltaTerms terms, const float *__restrict__ s0, T *__restrict__ o,
-              int64_t ldo, float *__restrict__ sn, float *__restrict__ states, float *__restrict__ us, int vec, int veco,
+              int64_t ldo, float *__restrict__ sn, float *__restrict__ states, float *__restrict__ us, int veco,
               unsigned *__restrict__ status) {
     using C = ChainCfg<T, DK>;
-    constexpr int WK = C::WK, NV = C::NV, NT = C::NT, LD = C::LD, NTILE = C::NTILE;
+    constexpr int WK = C::WK, LD = C::LD, LDV = C::LDV, NTILE = C::NTILE;
     constexpr bool EXACT = sizeof(T) == 2;
     extern __shared__ __align__(16) uint8_t smem_raw[];
     ChainSmem<T, DK> &sm = *reinterpret_cast<ChainSmem<T, DK> *>(smem_raw);
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g = lane >> 2, t = lane & 3;
-    const int grp = warp / WK, w = warp - grp * WK;
     const int si = blockIdx.x / geo.hv, hv = blockIdx.x - si * geo.hv, hk = hv / (geo.hv / geo.hk);
-    const int v0 = ((int)blockIdx.y * NV + grp) * 16;  // the group's value columns
-    const int d0 = w * 32;                             // the warp's key columns
-    const int64_t state_at = ((int64_t)si * geo.hv + hv) * geo.dk * geo.dv;
-    const T *kp = (const T *)geo.k + (int64_t)hk * geo.dk, *qp = (const T *)geo.q + (int64_t)hk * geo.dk;
+    const int vb = (int)blockIdx.y * C::COLS;
+    const int c0 = geo.first[si], c1 = geo.first[si + 1];
+    const int vcols = min(C::COLS, geo.dvp - vb);
 
-    if (tid == 0)
-        for (int i = 0; i < C::STAGES; i++) bar_init(&sm.full[i]);
-    if (vec && geo.dk < DK)  // the copies leave the columns beyond dk alone
-        for (int i = tid; i < C::STAGES * kChunk * (DK / 8); i += NT) {
-            const int s = i / (kChunk * (DK / 8)), rest = i - s * kChunk * (DK / 8), row = rest / (DK / 8), c = rest % (DK / 8) * 8;
-#pragma unroll
-            for (int e = 0; e < 8; e++)
-                if (c + e >= geo.dk) sm.st[s].k[row * LD + c + e] = sm.st[s].q[row * LD + c + e] = from_f32<T>(0.f);
+    if (tid == 0) {
+        sm.abort_word = 0;
+        for (int i = 0; i < C::STAGES; i++) {
+            bar_init(&sm.full[i], 33);  // the fetching warp's lanes, and the bulk copies
+            bar_init(&sm.empty[i], C::NC / 32);
         }
-    asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+        asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+    }
     __syncthreads();
 
-    auto load = [&](int c, int stage) {
-        const int2 ch = geo.chunk[c];
-        ChainStage<T, DK> &s = sm.st[stage];
-        const int64_t slot = (int64_t)c * geo.hv + hv;
-        uint64_t *bar = &sm.full[stage];
-        if (tid == 0) {
-            const uint32_t rows = vec ? (uint32_t)(ch.y * geo.dk * sizeof(T)) : 0u;
-            bar_expect(bar, (OUT ? 2 : 1) * (rows + kSquare * 4) + kVec * 4);
-            bulk_load(s.t, terms.t + slot * kSquare, kSquare * 4, bar);
-            if (OUT) bulk_load(s.p, terms.p + slot * kSquare, kSquare * 4, bar);
-            bulk_load(s.vec, terms.vec + slot * kVec, kVec * 4, bar);
-        }
-        if (vec) {
-            for (int r = tid; r < 2 * kChunk; r += NT) {
-                if (r < kChunk)
-                    bulk_row<T, DK>(s.k, kp + (int64_t)ch.x * geo.ldk, geo.ldk, ch.y, geo.dk, r, bar);
-                else if (OUT)
-                    bulk_row<T, DK>(s.q, qp + (int64_t)ch.x * geo.ldq, geo.ldq, ch.y, geo.dk, r - kChunk, bar);
+    if (warp == C::NC / 32) {
+        // ------------------------------------------------ the chunks' operands
+        const T *kp = (const T *)geo.k + (int64_t)hk * geo.dkp, *qp = (const T *)geo.q + (int64_t)hk * geo.dkp;
+        const T *vp = (const T *)geo.v + (int64_t)hv * geo.dvp + vb;
+        int it = 0;
+        for (int c = c0; c < c1; c++, it++) {
+            const int stage = it % C::STAGES;
+            if (!bar_wait(&sm.empty[stage], ((it / C::STAGES) & 1) ^ 1, &sm.abort_word, status)) break;
+            const int2 ch = geo.chunk[c];
+            ChainStage<T, DK> &s = sm.st[stage];
+            const int64_t slot = (int64_t)c * geo.hv + hv;
+            uint64_t *bar = &sm.full[stage];
+            warp_tile<T, DK>(s.k, kp + (int64_t)ch.x * geo.ldk, geo.ldk, ch.y, geo.dkp);
+            if (OUT) warp_tile<T, DK>(s.q, qp + (int64_t)ch.x * geo.ldq, geo.ldq, ch.y, geo.dkp);
+            warp_tile<T, C::COLS>(s.v, vp + (int64_t)ch.x * geo.ldv, geo.ldv, ch.y, vcols);
+            cp_arrive(bar);
+            if (lane == 0) {
+                bar_expect(bar, (kSquare + kVec) * 4);
+                bulk_load(s.tp, terms.tp + slot * kSquare, kSquare * 4, bar);
+                bulk_load(s.vec, terms.vec + slot * kVec, kVec * 4, bar);
             }
-        } else {
-            load_tile<T, DK, NT>(s.k, kp + (int64_t)ch.x * geo.ldk, geo.ldk, ch.y, geo.dk, 0);
-            if (OUT) load_tile<T, DK, NT>(s.q, qp + (int64_t)ch.x * geo.ldq, geo.ldq, ch.y, geo.dk, 0);
         }
-    };
+        // copies in flight end before the block does
+        for (int q = it > C::STAGES ? it - C::STAGES : 0; q < it; q++)
+            for (uint32_t n = 0; n < kWaitLimit && !bar_try(&sm.full[q % C::STAGES], (q / C::STAGES) & 1); n++) {
+            }
+        return;
+    }
+
+    // ---------------------------------------------------- the groups
+    const int grp = warp / WK, w = warp - grp * WK;
+    const int v0 = vb + grp * 16;  // the group's value columns
+    const int d0 = w * 32;         // the warp's key columns
+    const int64_t state_at = ((int64_t)si * geo.hv + hv) * geo.dk * geo.dv;
 
     // S^T: rows v0 + g, v0 + g + 8, columns d0 + 8 j + 2t, + 1
     float S[4][4];
@@ -410,86 +429,37 @@ k_delta_chain(const DeltaGeom geo, const DeltaTerms terms, const float *__restri
         }
     };
 
-    const int c0 = geo.first[si], c1 = geo.first[si + 1];
-    if (c0 < c1) load(c0, 0);
     int2 before = make_int2(0, 0);  // the chunk whose outputs are staged
     for (int c = c0; c < c1; c++) {
-        const int it = c - c0, stage = C::STAGES == 2 ? it & 1 : 0;
-        // the stage is complete, and every warp is done with the previous chunk
-        const bool ok = bar_wait(&sm.full[stage], (C::STAGES == 2 ? it >> 1 : it) & 1);
-        if (!__syncthreads_and(ok)) {
-            if (tid == 0) atomicOr(status, 1u);
-            return;
-        }
-        if (C::STAGES == 2 && c + 1 < c1) load(c + 1, stage ^ 1);
+        const int it = c - c0, stage = it % C::STAGES;
+        bar_wait(&sm.full[stage], (it / C::STAGES) & 1, &sm.abort_word, status);
         ChainStage<T, DK> &st = sm.st[stage];
         const int2 ch = geo.chunk[c];
         const int64_t slot = (int64_t)c * geo.hv + hv;
-        if (OUT && veco && it > 0) put_out(before);
         if (states) put_state(states + slot * geo.dk * geo.dv);
-
-        // V^T of the warp's token tiles, for X (the loads run during the products)
-        float vt[NTILE][4];
-        {
-            const T *vp = (const T *)geo.v + (int64_t)ch.x * geo.ldv + (int64_t)hv * geo.dv + v0 + g;
-            const bool in0 = v0 + g < geo.dv, in1 = v0 + g + 8 < geo.dv;
-#pragma unroll
-            for (int i = 0; i < NTILE; i++)
-#pragma unroll
-                for (int e = 0; e < 2; e++) {
-                    const int tok = tile_of<WK>(w, i) * 8 + 2 * t + e;
-                    const T *p = vp + (int64_t)tok * geo.ldv;
-                    vt[i][e] = in0 && tok < ch.y ? to_f32(p[0]) : 0.f;
-                    vt[i][2 + e] = in1 && tok < ch.y ? to_f32(p[8]) : 0.f;
-                }
-        }
+        group_sync<WK>(grp);  // the group is done with the previous chunk's exchanges
+        if (OUT && veco && it > 0) put_out(before);
 
         // partial S^T K^T and S^T Q^T over the warp's key columns
-        float po[8][4];
+        float po[2][4][4];
         {
-            SplitA a[4];
-#pragma unroll
-            for (int j = 0; j < 4; j++) a[j].set(S[j]);
+            StateSplit<T> a;
+            a.set(S);
             float *part = sm.part[grp][w];
 #pragma unroll
-            for (int h = 0; h < 8; h += 4) {
-                Acc r[4];
-                float2 b[4][4];
+            for (int h = 0; h < 2; h++) {
+                float r[4][4];
+                state_times_rows<T, LD, false>(a, st.k, 4 * h, d0, r);
 #pragma unroll
                 for (int n = 0; n < 4; n++) {
-                    r[n].zero();
-                    frag4<T, LD, false>(st.k, (h + n) * 8, d0, b[n]);
-                }
-#pragma unroll
-                for (int j = 0; j < 4; j++)
-#pragma unroll
-                    for (int n = 0; n < 4; n++) mma_split<false, EXACT>(r[n], a[j], b[n][j]);
-#pragma unroll
-                for (int n = 0; n < 4; n++) {
-                    float *p = part + g * kLdT + (h + n) * 8 + 2 * t;
-                    *reinterpret_cast<float2 *>(p) = make_float2(r[n].get(0), r[n].get(1));
-                    *reinterpret_cast<float2 *>(p + 8 * kLdT) = make_float2(r[n].get(2), r[n].get(3));
+                    float *p = part + g * kLdT + (4 * h + n) * 8 + 2 * t;
+                    *reinterpret_cast<float2 *>(p) = make_float2(r[n][0], r[n][1]);
+                    *reinterpret_cast<float2 *>(p + 8 * kLdT) = make_float2(r[n][2], r[n][3]);
                 }
             }
             if (OUT) {
 #pragma unroll
-                for (int h = 0; h < 8; h += 4) {
-                    Acc r[4];
-                    float2 b[4][4];
-#pragma unroll
-                    for (int n = 0; n < 4; n++) {
-                        r[n].zero();
-                        frag4<T, LD, false>(st.q, (h + n) * 8, d0, b[n]);
-                    }
-#pragma unroll
-                    for (int j = 0; j < 4; j++)
-#pragma unroll
-                        for (int n = 0; n < 4; n++) mma_split<false, EXACT, EXACT>(r[n], a[j], b[n][j]);
-#pragma unroll
-                    for (int n = 0; n < 4; n++)
-#pragma unroll
-                        for (int e = 0; e < 4; e++) po[h + n][e] = EXACT ? r[n].c[e] : r[n].get(e);
-                }
+                for (int h = 0; h < 2; h++) state_times_rows<T, LD, true>(a, st.q, 4 * h, d0, po[h]);
             }
         }
         group_sync<WK>(grp);
@@ -506,17 +476,20 @@ k_delta_chain(const DeltaGeom geo, const DeltaTerms terms, const float *__restri
             }
             const float2 cv = *reinterpret_cast<const float2 *>(st.vec + n);
             const float2 bv = *reinterpret_cast<const float2 *>(st.vec + 2 * kChunk + n);
+            float2 va, vb8;
+            frag2_col<T, LDV>(st.v, n - 2 * t, grp * 16, va, vb8);
             float4 *x = sm.x[grp] + g * kLdPair + n / 2;
-            x[0] = split_pair(bv.x * (vt[i][0] - cv.x * lo.x), bv.y * (vt[i][1] - cv.y * lo.y));
-            x[8 * kLdPair] = split_pair(bv.x * (vt[i][2] - cv.x * hi.x), bv.y * (vt[i][3] - cv.y * hi.y));
+            x[0] = split_pair(bv.x * (va.x - cv.x * lo.x), bv.y * (va.y - cv.y * lo.y));
+            x[8 * kLdPair] = split_pair(bv.x * (vb8.x - cv.x * hi.x), bv.y * (vb8.y - cv.y * hi.y));
         }
         group_sync<WK>(grp);
         if (OUT) {
             float *part = sm.part[grp][w];
 #pragma unroll
             for (int n = 0; n < 8; n++) {
-                *reinterpret_cast<float2 *>(part + g * kLdT + n * 8 + 2 * t) = make_float2(po[n][0], po[n][1]);
-                *reinterpret_cast<float2 *>(part + (g + 8) * kLdT + n * 8 + 2 * t) = make_float2(po[n][2], po[n][3]);
+                const float(&r)[4] = po[n >> 2][n & 3];
+                *reinterpret_cast<float2 *>(part + g * kLdT + n * 8 + 2 * t) = make_float2(r[0], r[1]);
+                *reinterpret_cast<float2 *>(part + (g + 8) * kLdT + n * 8 + 2 * t) = make_float2(r[2], r[3]);
             }
         }
         // U^T = X^T T^T at the warp's token tiles
@@ -532,7 +505,7 @@ k_delta_chain(const DeltaGeom geo, const DeltaTerms terms, const float *__restri
                 for (int i = 0; i < NTILE; i++) {
                     const int n = tile_of<WK>(w, i);
                     if (k > n) continue;
-                    mma_split<false, false>(u[i], a, *reinterpret_cast<const float2 *>(st.t + (n * 8 + g) * kLdT + k * 8 + 2 * t));
+                    mma_split<false, false>(u[i], a, frag_t_earlier(st.tp, k, n));
                 }
             }
 #pragma unroll
@@ -540,8 +513,8 @@ k_delta_chain(const DeltaGeom geo, const DeltaTerms terms, const float *__restri
                 const int n = tile_of<WK>(w, i) * 8 + 2 * t, at = g * kLdPair + n / 2;
                 const float2 ev = *reinterpret_cast<const float2 *>(st.vec + kChunk + n);
                 const float v[4] = {u[i].get(0), u[i].get(1), u[i].get(2), u[i].get(3)};
-                sm.u[grp][at] = split_pair(ev.x * v[0], ev.y * v[1]);
-                sm.u[grp][at + 8 * kLdPair] = split_pair(ev.x * v[2], ev.y * v[3]);
+                put_pair<T>(sm.u[grp] + at, ev.x * v[0], ev.y * v[1]);
+                put_pair<T>(sm.u[grp] + at + 8 * kLdPair, ev.x * v[2], ev.y * v[3]);
                 if (OUT) {
                     sm.un[grp][at] = make_float2(v[0], v[1]);
                     sm.un[grp][at + 8 * kLdPair] = make_float2(v[2], v[3]);
@@ -559,23 +532,13 @@ k_delta_chain(const DeltaGeom geo, const DeltaTerms terms, const float *__restri
         // S'^T = c_64 S^T + (e U)^T K: the chunk's sum starts from zero, so that
         // the state is rounded once a chunk
         {
-            Acc acc[4];
-#pragma unroll
-            for (int j = 0; j < 4; j++) acc[j].zero();
-#pragma unroll
-            for (int k = 0; k < 8; k++) {
-                SplitA a;
-                a.set(sm.u[grp][g * kLdPair + k * 4 + t], sm.u[grp][(g + 8) * kLdPair + k * 4 + t]);
-                float2 b[4];
-                frag4<T, LD, true>(st.k, k * 8, d0, b);
-#pragma unroll
-                for (int j = 0; j < 4; j++) mma_split<false, EXACT>(acc[j], a, b[j]);
-            }
+            float r[4][4];
+            tokens_product<T, LD>(sm.u[grp], st.k, d0, r);
             const float cend = st.vec[kChunk - 1];
 #pragma unroll
             for (int j = 0; j < 4; j++)
 #pragma unroll
-                for (int e = 0; e < 4; e++) S[j][e] = fmaf(cend, S[j][e], acc[j].get(e));
+                for (int e = 0; e < 4; e++) S[j][e] = fmaf(cend, S[j][e], r[j][e]);
         }
         // O^T = scale c (Q S)^T + U^T P^T at the warp's token tiles
         if (OUT) {
@@ -591,7 +554,7 @@ k_delta_chain(const DeltaGeom geo, const DeltaTerms terms, const float *__restri
                 for (int i = 0; i < NTILE; i++) {
                     const int n = tile_of<WK>(w, i);
                     if (k > n) continue;
-                    mma_split<false, false, EXACT>(oa[i], a, *reinterpret_cast<const float2 *>(st.p + (n * 8 + g) * kLdT + k * 8 + 2 * t));
+                    mma_split<false, false, EXACT>(oa[i], a, frag_p_earlier(st.tp, k, n));
                 }
             }
             T *stg = reinterpret_cast<T *>(sm.x[grp]);
@@ -607,8 +570,8 @@ k_delta_chain(const DeltaGeom geo, const DeltaTerms terms, const float *__restri
                 }
                 const float2 cv = *reinterpret_cast<const float2 *>(st.vec + n);
                 const float ca = geo.scale * cv.x, cb = geo.scale * cv.y;
-                const float r[4] = {fmaf(ca, lo.x, oa[i].get(0)), fmaf(cb, lo.y, oa[i].get(1)),
-                                    fmaf(ca, hi.x, oa[i].get(2)), fmaf(cb, hi.y, oa[i].get(3))};
+                const float r[4] = {fmaf(ca, lo.x, EXACT ? oa[i].c[0] : oa[i].get(0)), fmaf(cb, lo.y, EXACT ? oa[i].c[1] : oa[i].get(1)),
+                                    fmaf(ca, hi.x, EXACT ? oa[i].c[2] : oa[i].get(2)), fmaf(cb, hi.y, EXACT ? oa[i].c[3] : oa[i].get(3))};
                 if (veco) {
 #pragma unroll
                     for (int e = 0; e < 4; e++) stg[(n + (e & 1)) * 16 + g + (e >> 1) * 8] = from_f32<T>(r[e]);
@@ -623,10 +586,8 @@ k_delta_chain(const DeltaGeom geo, const DeltaTerms terms, const float *__restri
             }
             before = ch;
         }
-        if (C::STAGES == 1) {
-            __syncthreads();  // the only stage is free
-            if (c + 1 < c1) load(c + 1, 0);
-        }
+        __syncwarp();
+        if (lane == 0) bar_arrive(&sm.empty[stage]);
     }
     if (OUT && veco && c0 < c1) {
         group_sync<WK>(grp);
@@ -641,8 +602,7 @@ cudaError_t terms_dk(const DeltaGeom &g, const DeltaTerms &t, cudaStream_t st) {
     static const cudaError_t attr = cudaFuncSetAttribute(
         k_delta_terms<T, DK>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)sizeof(TermSmem<T, DK>));
     if (attr != cudaSuccess) return attr;
-    const int vec = mult16(g.q, g.ldq, g.dk, sizeof(T)) && mult16(g.k, g.ldk, g.dk, sizeof(T));
-    k_delta_terms<T, DK><<<dim3(g.nchunks, g.hk), kTermThreads, smem, st>>>(g, t, vec);
+    k_delta_terms<T, DK><<<dim3(g.nchunks, g.hk), kTermThreads, smem, st>>>(g, t);
     return cudaGetLastError();
 }
 
@@ -652,19 +612,18 @@ cudaError_t chain_dk(const DeltaGeom &g, const DeltaTerms &t, const float *s0, v
     using C = ChainCfg<T, DK>;
     static_assert(sizeof(ChainSmem<T, DK>) <= 232448, "shared memory of a block");
     const size_t smem = sizeof(ChainSmem<T, DK>);
-    const int vec = mult16(g.q, g.ldq, g.dk, sizeof(T)) && mult16(g.k, g.ldk, g.dk, sizeof(T));
     const dim3 grid((unsigned)(g.nseq * g.hv), (unsigned)((g.dv + 16 * C::NV - 1) / (16 * C::NV)));
     if (o) {
         static const cudaError_t attr = cudaFuncSetAttribute(
             k_delta_chain<T, DK, true>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)sizeof(ChainSmem<T, DK>));
         if (attr != cudaSuccess) return attr;
-        k_delta_chain<T, DK, true><<<grid, C::NT, smem, st>>>(g, t, s0, (T *)o, ldo, sn, states, us, vec,
+        k_delta_chain<T, DK, true><<<grid, C::NT, smem, st>>>(g, t, s0, (T *)o, ldo, sn, states, us,
                                                                     mult16(o, ldo, g.dv, sizeof(T)), status);
     } else {
         static const cudaError_t attr = cudaFuncSetAttribute(
             k_delta_chain<T, DK, false>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)sizeof(ChainSmem<T, DK>));
         if (attr != cudaSuccess) return attr;
-        k_delta_chain<T, DK, false><<<grid, C::NT, smem, st>>>(g, t, s0, nullptr, 0, sn, states, us, vec, 0, status);
+        k_delta_chain<T, DK, false><<<grid, C::NT, smem, st>>>(g, t, s0, nullptr, 0, sn, states, us, 0, status);
     }
     return cudaGetLastError();
 }
@@ -675,6 +634,18 @@ cudaError_t zs_launch_delta_plan(const int64_t *offsets, int nseq, int64_t token
                                  int2 *chunk, cudaStream_t st, int64_t *launches) {
     k_delta_plan<<<1, 1024, 0, st>>>(offsets, nseq, tokens, nchunks, first, seq, chunk);
     ++*launches;
+    return cudaGetLastError();
+}
+
+cudaError_t zs_launch_delta_pack(int type, const void *src, int64_t ld, int64_t tokens, int heads, int d, int dp,
+                                 void *dst, int num_sms, cudaStream_t st, int64_t *launches) {
+    ++*launches;
+    const int64_t n = tokens * heads * dp;
+    const unsigned blocks = (unsigned)std::min<int64_t>((n + 255) / 256, (int64_t)num_sms * 8);
+    if (type == ZSOLVE_F32)
+        k_delta_pack<<<blocks, 256, 0, st>>>((const float *)src, ld, tokens, heads, d, dp, (float *)dst);
+    else  // a copy: both 16-bit types alike
+        k_delta_pack<<<blocks, 256, 0, st>>>((const bf16 *)src, ld, tokens, heads, d, dp, (bf16 *)dst);
     return cudaGetLastError();
 }
 

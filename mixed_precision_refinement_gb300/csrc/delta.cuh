@@ -23,6 +23,8 @@
 // next chunk's A operand as it stands).
 #pragma once
 
+#include <type_traits>
+
 #include "seq.cuh"
 
 namespace zs {
@@ -33,6 +35,8 @@ constexpr int kChunk = 64;  // tokens of a chunk
 struct DeltaGeom {
     const void *q, *k, *v;         // tokens x heads x d, token strides ld*
     int64_t ldq, ldk, ldv;
+    int dkp, dvp;                  // dk, dv in whole 16 bytes: distance of two heads in the chunked form
+                                   // (there q, k, v are aligned, or packed copies padded with zeros)
     const float *g, *beta;         // tokens x hv
     int hk, hv, dk, dv, nseq;
     int64_t tokens;
@@ -43,10 +47,12 @@ struct DeltaGeom {
     int nchunks;                   // room in the tables
 };
 
-// Per chunk and value head, what does not depend on the state (float32):
-// T and P (64 rows of stride 72) and the vectors c_i, e_64,i, beta_i (64 each).
+// Per chunk and value head, what does not depend on the state (float32): T and P
+// in one matrix of 64 rows of stride 72, T strictly below the diagonal (its
+// diagonal is 1) and P transposed on and above it; and the vectors c_i, e_64,i,
+// beta_i (64 each).
 struct DeltaTerms {
-    float *t, *p, *vec;
+    float *tp, *vec;
 };
 constexpr int kVec = 3 * kChunk;
 
@@ -149,7 +155,72 @@ __device__ __forceinline__ void mma_add(float (&c)[4], const SplitA &a, float2 b
     for (int e = 0; e < 4; e++) c[e] += d[e];
 }
 
+// bfloat16 inputs: a float32 operand in three bfloat16 parts (24 bits), so that
+// the other, exact operand needs no conversion and a step covers 16 k:
+// m16n8k16, three products for the tf32 form's four.
+struct Split3 {
+    uint32_t p[3][4];
+    // the accumulators of two neighbouring tiles of 8 columns
+    __device__ __forceinline__ void set(const float (&c)[4], const float (&d)[4]) {
+        split(c[0], c[1], 0), split(c[2], c[3], 1), split(d[0], d[1], 2), split(d[2], d[3], 3);
+    }
+    // as split3_pair left them: rows g and g + 8, pairs t and t + 4 of the tile
+    __device__ __forceinline__ void set(uint4 a, uint4 b, uint4 c, uint4 d) {
+        p[0][0] = a.x, p[1][0] = a.y, p[2][0] = a.z;
+        p[0][1] = b.x, p[1][1] = b.y, p[2][1] = b.z;
+        p[0][2] = c.x, p[1][2] = c.y, p[2][2] = c.z;
+        p[0][3] = d.x, p[1][3] = d.y, p[2][3] = d.z;
+    }
+    static __device__ __forceinline__ uint32_t part(float &x, float &y) {
+        const uint32_t u = pack2<bf16>(x, y);
+        const float2 f = unpack2<bf16>(u);
+        x -= f.x;
+        y -= f.y;
+        return u;
+    }
+    __device__ __forceinline__ void split(float x, float y, int i) {
+        p[0][i] = part(x, y);
+        p[1][i] = part(x, y);
+        p[2][i] = pack2<bf16>(x, y);
+    }
+};
+
+__device__ __forceinline__ uint4 split3_pair(float x, float y) {
+    uint4 u;
+    u.x = Split3::part(x, y);
+    u.y = Split3::part(x, y);
+    u.z = pack2<bf16>(x, y);
+    u.w = 0u;
+    return u;
+}
+
+__device__ __forceinline__ void mma16(float (&c)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+    asm("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
+        "{%0, %1, %2, %3};"
+        : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+        : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+__device__ __forceinline__ void mma16_first(float (&c)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+    asm("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
+        "{%10, %10, %10, %10};"
+        : "=f"(c[0]), "=f"(c[1]), "=f"(c[2]), "=f"(c[3])
+        : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1), "f"(0.f));
+}
+
 // ---------------------------------------------------------------- fragments
+
+__device__ __forceinline__ void ldmatrix4(uint32_t (&u)[4], const void *p) {
+    asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0, %1, %2, %3}, [%4];"
+                 : "=r"(u[0]), "=r"(u[1]), "=r"(u[2]), "=r"(u[3])
+                 : "r"((uint32_t)__cvta_generic_to_shared(p))
+                 : "memory");
+}
+__device__ __forceinline__ void ldmatrix4_trans(uint32_t (&u)[4], const void *p) {
+    asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0, %1, %2, %3}, [%4];"
+                 : "=r"(u[0]), "=r"(u[1]), "=r"(u[2]), "=r"(u[3])
+                 : "r"((uint32_t)__cvta_generic_to_shared(p))
+                 : "memory");
+}
 
 // Row stride (values) of a tile of D columns in shared memory: 16 bytes more
 // for 16-bit values, 32 for float32, so that the eight rows of a fragment lie
@@ -166,18 +237,12 @@ template <typename T, int LD, bool COL>
 __device__ __forceinline__ void frag4(const T *x, int r0, int c0, float2 (&f)[4]) {
     const int lane = threadIdx.x & 31;
     if constexpr (sizeof(T) == 2) {
-        const uint32_t a = (uint32_t)__cvta_generic_to_shared(x + (r0 + (lane & 7)) * LD + c0 + 8 * (lane >> 3));
+        const T *p = x + (r0 + (lane & 7)) * LD + c0 + 8 * (lane >> 3);
         uint32_t u[4];
         if (COL)
-            asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0, %1, %2, %3}, [%4];"
-                         : "=r"(u[0]), "=r"(u[1]), "=r"(u[2]), "=r"(u[3])
-                         : "r"(a)
-                         : "memory");
+            ldmatrix4_trans(u, p);
         else
-            asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0, %1, %2, %3}, [%4];"
-                         : "=r"(u[0]), "=r"(u[1]), "=r"(u[2]), "=r"(u[3])
-                         : "r"(a)
-                         : "memory");
+            ldmatrix4(u, p);
 #pragma unroll
         for (int i = 0; i < 4; i++) f[i] = unpack2<T>(u[i]);
     } else {
@@ -189,6 +254,149 @@ __device__ __forceinline__ void frag4(const T *x, int r0, int c0, float2 (&f)[4]
             else
                 f[i] = *reinterpret_cast<const float2 *>(x + (r0 + g) * LD + c0 + 8 * i + 2 * t);
         }
+    }
+}
+
+// (X(r0 + 2t, c0 + g), X(r0 + 2t + 1, c0 + g)) and the same eight columns on
+template <typename T, int LD>
+__device__ __forceinline__ void frag2_col(const T *x, int r0, int c0, float2 &f0, float2 &f1) {
+    const int lane = threadIdx.x & 31;
+    if constexpr (sizeof(T) == 2) {
+        const uint32_t a = (uint32_t)__cvta_generic_to_shared(x + (r0 + (lane & 7)) * LD + c0 + 8 * ((lane >> 3) & 1));
+        uint32_t u0, u1;
+        asm volatile("ldmatrix.sync.aligned.m8n8.x2.trans.shared.b16 {%0, %1}, [%2];" : "=r"(u0), "=r"(u1) : "r"(a) : "memory");
+        f0 = unpack2<T>(u0);
+        f1 = unpack2<T>(u1);
+    } else {
+        const T *p = x + (r0 + 2 * (lane & 3)) * LD + c0 + (lane >> 2);
+        f0 = make_float2(p[0], p[LD]);
+        f1 = make_float2(p[8], p[LD + 8]);
+    }
+}
+
+// A 16 x 32 block of a state's transpose, as accumulators, split for the
+// products with K and Q.
+template <typename T>
+struct StateSplit {
+    SplitA a[4];
+    __device__ __forceinline__ void set(const float (&s)[4][4]) {
+#pragma unroll
+        for (int j = 0; j < 4; j++) a[j].set(s[j]);
+    }
+};
+template <>
+struct StateSplit<bf16> {
+    Split3 a[2];
+    __device__ __forceinline__ void set(const float (&s)[4][4]) {
+        a[0].set(s[0], s[1]);
+        a[1].set(s[2], s[3]);
+    }
+};
+
+// r[n] = S^T X^T at token tiles n0 .. n0 + 3 over key columns d0 .. d0 + 31 of
+// the tile X; HALF: for results of 16 bits.
+template <typename T, int LD, bool HALF>
+__device__ __forceinline__ void state_times_rows(const StateSplit<T> &s, const T *x, int n0, int d0, float (&r)[4][4]) {
+    constexpr bool EXACT = sizeof(T) == 2;
+    if constexpr (std::is_same<T, bf16>::value) {
+        const int lane = threadIdx.x & 31;
+        uint32_t b[4][4];
+#pragma unroll
+        for (int n = 0; n < 4; n++) ldmatrix4(b[n], x + ((n0 + n) * 8 + (lane & 7)) * LD + d0 + 8 * (lane >> 3));
+        // the small parts first
+#pragma unroll
+        for (int i = HALF ? 1 : 2; i >= 0; i--)
+#pragma unroll
+            for (int k = 0; k < 2; k++)
+#pragma unroll
+                for (int n = 0; n < 4; n++) {
+                    if (i == (HALF ? 1 : 2) && k == 0)
+                        mma16_first(r[n], s.a[k].p[i], b[n][2 * k], b[n][2 * k + 1]);
+                    else
+                        mma16(r[n], s.a[k].p[i], b[n][2 * k], b[n][2 * k + 1]);
+                }
+    } else {
+        Acc acc[4];
+        float2 b[4][4];
+#pragma unroll
+        for (int n = 0; n < 4; n++) {
+            acc[n].zero();
+            frag4<T, LD, false>(x, (n0 + n) * 8, d0, b[n]);
+        }
+#pragma unroll
+        for (int j = 0; j < 4; j++)
+#pragma unroll
+            for (int n = 0; n < 4; n++) mma_split<false, EXACT, EXACT && HALF>(acc[n], s.a[j], b[n][j]);
+#pragma unroll
+        for (int n = 0; n < 4; n++)
+#pragma unroll
+            for (int e = 0; e < 4; e++) r[n][e] = EXACT && HALF ? acc[n].c[e] : acc[n].get(e);
+    }
+}
+
+// Split pairs in shared memory: rows of 32 pairs of 16 bytes, 64 bytes more
+// apart, so that the rows of a fragment's loads lie in different banks.
+constexpr int kLdPair = 36;
+template <typename T>
+__device__ __forceinline__ void put_pair(float4 *p, float a, float b) {
+    if constexpr (std::is_same<T, bf16>::value)
+        *reinterpret_cast<uint4 *>(p) = split3_pair(a, b);
+    else
+        *p = split_pair(a, b);
+}
+
+// r[j] = Y X over the chunk's 64 tokens: Y 16 x 64 from put_pair, X(tokens, key
+// columns d0 + 8 j ..) of the tile, each sum from zero.
+template <typename T, int LD>
+__device__ __forceinline__ void tokens_product(const float4 *y, const T *x, int d0, float (&r)[4][4]) {
+    const int lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
+    if constexpr (std::is_same<T, bf16>::value) {
+        const uint4 *u = reinterpret_cast<const uint4 *>(y);
+        float small[4][4];
+#pragma unroll
+        for (int k = 0; k < 4; k++) {
+            const int at = g * kLdPair + k * 8 + t;
+            Split3 a;
+            a.set(u[at], u[at + 8 * kLdPair], u[at + 4], u[at + 8 * kLdPair + 4]);
+            uint32_t b[2][4];
+#pragma unroll
+            for (int j = 0; j < 2; j++)
+                ldmatrix4_trans(b[j], x + (k * 16 + (lane & 15)) * LD + d0 + 16 * j + 8 * (lane >> 4));
+#pragma unroll
+            for (int j = 0; j < 4; j++) {
+                const uint32_t b0 = b[j >> 1][(j & 1) * 2], b1 = b[j >> 1][(j & 1) * 2 + 1];
+                if (k == 0) {
+                    mma16_first(small[j], a.p[2], b0, b1);
+                    mma16_first(r[j], a.p[0], b0, b1);
+                } else {
+                    mma16(small[j], a.p[2], b0, b1);
+                    mma16(r[j], a.p[0], b0, b1);
+                }
+            }
+#pragma unroll
+            for (int j = 0; j < 4; j++) mma16(small[j], a.p[1], b[j >> 1][(j & 1) * 2], b[j >> 1][(j & 1) * 2 + 1]);
+        }
+#pragma unroll
+        for (int j = 0; j < 4; j++)
+#pragma unroll
+            for (int e = 0; e < 4; e++) r[j][e] += small[j][e];
+    } else {
+        Acc acc[4];
+#pragma unroll
+        for (int j = 0; j < 4; j++) acc[j].zero();
+#pragma unroll
+        for (int k = 0; k < 8; k++) {
+            SplitA a;
+            a.set(y[g * kLdPair + k * 4 + t], y[(g + 8) * kLdPair + k * 4 + t]);
+            float2 b[4];
+            frag4<T, LD, true>(x, k * 8, d0, b);
+#pragma unroll
+            for (int j = 0; j < 4; j++) mma_split<false, sizeof(T) == 2>(acc[j], a, b[j]);
+        }
+#pragma unroll
+        for (int j = 0; j < 4; j++)
+#pragma unroll
+            for (int e = 0; e < 4; e++) r[j][e] = acc[j].get(e);
     }
 }
 
@@ -205,56 +413,103 @@ __device__ __forceinline__ void cp_wait() {
     asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
 }
 
-// By all NT threads: a tile of 64 rows x D columns, rows of `d` values (d <= D) at stride ld in
-// memory, n rows of them; zeros elsewhere.  vec: 16-byte copies are allowed
-// (pointer, stride and d are multiples of 16 bytes).
+// By all NT threads: a tile of 64 rows x D columns from n rows of d values (whole
+// 16 bytes) at stride ld; zeros elsewhere.
 template <typename T, int D, int NT>
-__device__ __forceinline__ void load_tile(T *dst, const T *src, int64_t ld, int n, int d, int vec) {
-    constexpr int LD = tile_ld<T>(D);
-    if (vec) {
-        constexpr int VE = 16 / (int)sizeof(T), PER = D / VE;
-        for (int i = threadIdx.x; i < kChunk * PER; i += NT) {
-            const int r = i / PER, c = (i - r * PER) * VE;
-            const bool in = r < n && c < d;
-            cp_async16(dst + r * LD + c, src + (in ? r * ld + c : 0), in ? 16 : 0);
-        }
-    } else {
-        for (int i = threadIdx.x; i < kChunk * D; i += NT) {
-            const int r = i / D, c = i - r * D;
-            dst[r * LD + c] = r < n && c < d ? src[r * ld + c] : from_f32<T>(0.f);
-        }
+__device__ __forceinline__ void load_tile(T *dst, const T *src, int64_t ld, int n, int d) {
+    constexpr int LD = tile_ld<T>(D), VE = 16 / (int)sizeof(T), PER = D / VE;
+    for (int i = threadIdx.x; i < kChunk * PER; i += NT) {
+        const int r = i / PER, c = (i - r * PER) * VE;
+        const bool in = r < n && c < d;
+        cp_async16(dst + r * LD + c, src + (in ? r * ld + c : 0), in ? 16 : 0);
     }
 }
 
-// Row stride of the 64 x 64 float32 matrices T and P, in memory as in shared
-// memory (a copy is one bulk copy, and a fragment's rows lie in different banks).
+// Row stride of the matrix that holds T and P, in memory as in shared memory (a
+// copy is one bulk copy, and a fragment's rows lie in different banks).
 constexpr int kLdT = kChunk + 8;
 constexpr int kSquare = kChunk * kLdT;
 
-// A chunk's operands arrive by bulk copies on an mbarrier.  Waits are bounded:
-// false once the limit is reached.
-__device__ __forceinline__ void bar_init(uint64_t *bar) {
-    asm volatile("mbarrier.init.shared::cta.b64 [%0], 1;" ::"r"((uint32_t)__cvta_generic_to_shared(bar)) : "memory");
+// B operands from it for the 8 x 8 tile of tokens k (the sum's) and n (the
+// result's): T^T and P^T for products that run over earlier tokens (k <= n), T and
+// P for those over later ones (k >= n).
+__device__ __forceinline__ float2 frag_t_earlier(const float *m, int k, int n) {
+    const int lane = threadIdx.x & 31, g = lane >> 2, t2 = 2 * (lane & 3);
+    float2 b = *reinterpret_cast<const float2 *>(m + (n * 8 + g) * kLdT + k * 8 + t2);  // T(n g, k t)
+    if (k == n) {
+        b.x = t2 < g ? b.x : t2 == g ? 1.f : 0.f;
+        b.y = t2 + 1 < g ? b.y : t2 + 1 == g ? 1.f : 0.f;
+    }
+    return b;
+}
+__device__ __forceinline__ float2 frag_p_earlier(const float *m, int k, int n) {
+    const int lane = threadIdx.x & 31, g = lane >> 2, t2 = 2 * (lane & 3);
+    const float *p = m + (k * 8 + t2) * kLdT + n * 8 + g;  // P(n g, k t), stored transposed
+    float2 b = make_float2(p[0], p[kLdT]);
+    if (k == n) {
+        if (t2 > g) b.x = 0.f;
+        if (t2 + 1 > g) b.y = 0.f;
+    }
+    return b;
+}
+__device__ __forceinline__ float2 frag_t_later(const float *m, int k, int n) {
+    const int lane = threadIdx.x & 31, g = lane >> 2, t2 = 2 * (lane & 3);
+    const float *p = m + (k * 8 + t2) * kLdT + n * 8 + g;  // T(k t, n g)
+    float2 b = make_float2(p[0], p[kLdT]);
+    if (k == n) {
+        b.x = t2 > g ? b.x : t2 == g ? 1.f : 0.f;
+        b.y = t2 + 1 > g ? b.y : t2 + 1 == g ? 1.f : 0.f;
+    }
+    return b;
+}
+__device__ __forceinline__ float2 frag_p_later(const float *m, int k, int n) {
+    const int lane = threadIdx.x & 31, g = lane >> 2, t2 = 2 * (lane & 3);
+    float2 b = *reinterpret_cast<const float2 *>(m + (n * 8 + g) * kLdT + k * 8 + t2);  // P(k t, n g), stored transposed
+    if (k == n) {
+        if (t2 < g) b.x = 0.f;
+        if (t2 + 1 < g) b.y = 0.f;
+    }
+    return b;
+}
+
+// A chunk's operands arrive on an mbarrier, fetched by a warp of their own as
+// stages become free.  Waits are bounded: on give-up the block's
+// abort word and the status word are set, and every later wait of the block
+// returns at once, so that all warps run to their end.
+__device__ __forceinline__ void bar_init(uint64_t *bar, uint32_t count) {
+    asm volatile("mbarrier.init.shared::cta.b64 [%0], %1;" ::"r"((uint32_t)__cvta_generic_to_shared(bar)), "r"(count)
+                 : "memory");
 }
 __device__ __forceinline__ void bar_expect(uint64_t *bar, uint32_t bytes) {
     asm volatile("mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;" ::"r"((uint32_t)__cvta_generic_to_shared(bar)),
                  "r"(bytes)
                  : "memory");
 }
-__device__ __forceinline__ bool bar_wait(uint64_t *bar, uint32_t parity) {
-    const uint32_t a = (uint32_t)__cvta_generic_to_shared(bar);
-    for (uint32_t it = 0; it < (1u << 19); it++) {  // about a second
-        uint32_t ok;
-        asm volatile(
-            "{\n\t.reg .pred p;\n\t"
-            "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
-            "selp.u32 %0, 1, 0, p;\n\t}"
-            : "=r"(ok)
-            : "r"(a), "r"(parity)
-            : "memory");
-        if (ok) return true;
+__device__ __forceinline__ void bar_arrive(uint64_t *bar) {
+    asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"((uint32_t)__cvta_generic_to_shared(bar)) : "memory");
+}
+__device__ __forceinline__ bool bar_try(uint64_t *bar, uint32_t parity) {
+    uint32_t ok;
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
+        "selp.u32 %0, 1, 0, p;\n\t}"
+        : "=r"(ok)
+        : "r"((uint32_t)__cvta_generic_to_shared(bar)), "r"(parity)
+        : "memory");
+    return ok != 0;
+}
+constexpr uint32_t kWaitLimit = 1u << 19;  // about a second
+__device__ __forceinline__ bool bar_wait(uint64_t *bar, uint32_t parity, volatile int *abort_word, unsigned *status) {
+    for (uint32_t it = 0; !bar_try(bar, parity); it++) {
+        if (*abort_word) return false;
+        if (it >= kWaitLimit) {
+            *abort_word = 1;
+            atomicOr(status, 1u);
+            return false;
+        }
     }
-    return false;
+    return true;
 }
 __device__ __forceinline__ void bulk_load(void *dst, const void *src, uint32_t bytes, uint64_t *bar) {
     asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(
@@ -263,19 +518,29 @@ __device__ __forceinline__ void bulk_load(void *dst, const void *src, uint32_t b
                  : "memory");
 }
 
-// Rows 0 .. n-1 of d values into a tile of D columns: with vec, one bulk copy a
-// row (row = the caller's row, one caller a row; rows beyond n are set to zero
-// and columns beyond d are left), else plain copies by all NT threads.
+// One warp: a tile of 64 rows x D columns from n rows of d values (whole 16
+// bytes) at stride ld, by 16-byte copies that write zeros elsewhere (a bulk copy
+// a row is issued a lane at a time, and 192 of them took longer than a chunk's
+// products).
 template <typename T, int D>
-__device__ __forceinline__ void bulk_row(T *dst, const T *src, int64_t ld, int n, int d, int row, uint64_t *bar) {
-    constexpr int LD = tile_ld<T>(D);
-    if (row < n) {
-        bulk_load(dst + row * LD, src + row * ld, (uint32_t)(d * sizeof(T)), bar);
-    } else {
-        uint4 *p = reinterpret_cast<uint4 *>(dst + row * LD);
-#pragma unroll 1
-        for (int i = 0; i < D * (int)sizeof(T) / 16; i++) p[i] = make_uint4(0, 0, 0, 0);
+__device__ __forceinline__ void warp_tile(T *dst, const T *src, int64_t ld, int n, int d) {
+    constexpr int LD = tile_ld<T>(D), VE = 16 / (int)sizeof(T), PER = D / VE, ROWS = 32 / PER;
+    const int lane = threadIdx.x & 31, r = lane / PER, c = (lane % PER) * VE;
+    const T *p = src + (int64_t)r * ld + c;
+    T *q = dst + r * LD + c;
+#pragma unroll 8
+    for (int i = 0; i < kChunk; i += ROWS) {
+        const bool in = i + r < n && c < d;
+        cp_async16(q, in ? p : src, in ? 16 : 0);
+        p += ROWS * ld;
+        q += ROWS * LD;
     }
+}
+
+// Arrive on bar once the calling thread's copies so far are complete.
+__device__ __forceinline__ void cp_arrive(uint64_t *bar) {
+    asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"((uint32_t)__cvta_generic_to_shared(bar))
+                 : "memory");
 }
 
 // One warp: b_i of a chunk's tokens, summed in float64 (a few additions) and
@@ -339,6 +604,9 @@ inline bool mult16(const void *p, int64_t ld, int64_t d, size_t e) {
 // delta.cu
 cudaError_t zs_launch_delta_plan(const int64_t *offsets, int nseq, int64_t tokens, int nchunks, int *first, int2 *seq,
                                  int2 *chunk, cudaStream_t st, int64_t *launches);
+// tokens x heads x d values at token stride ld into packed heads of dp values
+cudaError_t zs_launch_delta_pack(int type, const void *src, int64_t ld, int64_t tokens, int heads, int d, int dp,
+                                 void *dst, int num_sms, cudaStream_t st, int64_t *launches);
 cudaError_t zs_launch_delta_terms(int type, const zs::DeltaGeom &g, const zs::DeltaTerms &t, cudaStream_t st,
                                   int64_t *launches);
 // The recurrence over the chunks.  o (NULL: not formed), sn (the last states;

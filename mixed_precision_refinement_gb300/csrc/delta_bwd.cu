@@ -23,16 +23,18 @@ using namespace zs;
 // ---------------------------------------------------------------- chain backwards
 
 // Laid out as the forward chain: a group of WK warps owns 16 value columns of
-// dS^T, 32 key columns a warp; the exchanges are the partial sums of
-// (K dS')^T, then dU^T, then dX^T and (scale c dO)^T, split where they are written.
+// dS^T, 32 key columns a warp, and one more warp fetches the chunks' operands;
+// the exchanges are the partial sums of (K dS')^T, then dU^T, then dX^T and
+// (scale c dO)^T, split where they are written.
 template <typename T, int DK>
 struct RChainCfg {
     static constexpr int WK = DK / 32;
     static constexpr int NV = DK == 32 ? 4 : 2;
-    static constexpr int NT = 32 * WK * NV;
+    static constexpr int NC = 32 * WK * NV;  // threads of the groups
+    static constexpr int NT = NC + 32;
     static constexpr int NTILE = 8 / WK;
     static constexpr int COLS = 16 * NV;
-    static constexpr int STAGES = sizeof(T) == 2 ? 2 : 1;  // as many as fit
+    static constexpr int STAGES = sizeof(T) == 2 || DK == 64 ? 2 : 1;  // as many as fit
 };
 
 template <typename T, int DK>
@@ -40,12 +42,9 @@ struct RChainStage {
     T k[kChunk * tile_ld<T>(DK)];
     T q[kChunk * tile_ld<T>(DK)];
     T dout[kChunk * tile_ld<T>(RChainCfg<T, DK>::COLS)];
-    float t[kSquare];
-    float p[kSquare];
+    float tp[kSquare];
     float vec[kVec];
 };
-
-constexpr int kLdPair = 36;  // float4: rows of 32 split pairs, 64 bytes more apart
 
 template <typename T, int DK>
 struct RChainSmem {
@@ -55,94 +54,71 @@ struct RChainSmem {
     float part[C::NV][C::WK > 2 ? C::WK : 2][16 * kLdT];
     float4 u[C::NV][16 * kLdPair];  // dU^T
     float4 x[C::NV][16 * kLdPair];  // -(beta c dX)^T
-    uint64_t full[C::STAGES];
+    uint64_t full[C::STAGES], empty[C::STAGES];
+    int abort_word;
 };
-
-// (X(r0 + 2t, c0 + g), X(r0 + 2t + 1, c0 + g)) and the same eight columns on
-template <typename T, int LD>
-__device__ __forceinline__ void frag2_col(const T *x, int r0, int c0, float2 &f0, float2 &f1) {
-    const int lane = threadIdx.x & 31;
-    if constexpr (sizeof(T) == 2) {
-        const uint32_t a = (uint32_t)__cvta_generic_to_shared(x + (r0 + (lane & 7)) * LD + c0 + 8 * ((lane >> 3) & 1));
-        uint32_t u0, u1;
-        asm volatile("ldmatrix.sync.aligned.m8n8.x2.trans.shared.b16 {%0, %1}, [%2];" : "=r"(u0), "=r"(u1) : "r"(a) : "memory");
-        f0 = unpack2<T>(u0);
-        f1 = unpack2<T>(u1);
-    } else {
-        const T *p = x + (r0 + 2 * (lane & 3)) * LD + c0 + (lane >> 2);
-        f0 = make_float2(p[0], p[LD]);
-        f1 = make_float2(p[8], p[LD + 8]);
-    }
-}
 
 template <typename T, int DK>
 __global__ void __launch_bounds__(RChainCfg<T, DK>::NT, 1)
 k_delta_rchain(const DeltaGeom geo, const DeltaTerms terms, const T *__restrict__ dout, int64_t lddo,
                const float *__restrict__ ds, float *__restrict__ dends, float *__restrict__ dxs, T *__restrict__ dv,
-               float *__restrict__ ds0, int vec, int veco, unsigned *__restrict__ status) {
+               float *__restrict__ ds0, unsigned *__restrict__ status) {
     using C = RChainCfg<T, DK>;
-    constexpr int WK = C::WK, NT = C::NT, NTILE = C::NTILE;
-    static_assert(2 * 16 * kLdT * sizeof(float) >= 16 * kLdPair * sizeof(float4), "room for the split pairs");
+    constexpr int WK = C::WK, NTILE = C::NTILE;
     constexpr int LD = tile_ld<T>(DK), LDO = tile_ld<T>(C::COLS);
     constexpr bool EXACT = sizeof(T) == 2;
+    static_assert(2 * 16 * kLdT * sizeof(float) >= 16 * kLdPair * sizeof(float4), "room for the split pairs");
     extern __shared__ __align__(16) uint8_t smem_raw[];
     RChainSmem<T, DK> &sm = *reinterpret_cast<RChainSmem<T, DK> *>(smem_raw);
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g = lane >> 2, t = lane & 3;
-    const int grp = warp / WK, w = warp - grp * WK;
     const int si = blockIdx.x / geo.hv, hv = blockIdx.x - si * geo.hv, hk = hv / (geo.hv / geo.hk);
-    const int vb = (int)blockIdx.y * C::COLS, v0 = vb + grp * 16, d0 = w * 32;
-    const int cols = min(C::COLS, geo.dv - vb);  // of the block's dO
-    const int64_t state_at = ((int64_t)si * geo.hv + hv) * geo.dk * geo.dv;
-    const T *kp = (const T *)geo.k + (int64_t)hk * geo.dk, *qp = (const T *)geo.q + (int64_t)hk * geo.dk;
-    const T *op = dout + (int64_t)hv * geo.dv + vb;
+    const int vb = (int)blockIdx.y * C::COLS;
+    const int cols = min(C::COLS, geo.dvp - vb);  // of the block's dO
+    const int c0 = geo.first[si], c1 = geo.first[si + 1];
 
-    if (tid == 0)
-        for (int i = 0; i < C::STAGES; i++) bar_init(&sm.full[i]);
-    // the copies leave the columns beyond dk and dv alone
-    if (vec && geo.dk < DK)
-        for (int i = tid; i < C::STAGES * kChunk * DK; i += NT) {
-            const int s = i / (kChunk * DK), rest = i - s * kChunk * DK, row = rest / DK, c = rest % DK;
-            if (c >= geo.dk) sm.st[s].k[row * LD + c] = sm.st[s].q[row * LD + c] = from_f32<T>(0.f);
+    if (tid == 0) {
+        sm.abort_word = 0;
+        for (int i = 0; i < C::STAGES; i++) {
+            bar_init(&sm.full[i], 33);  // the fetching warp's lanes, and the bulk copies
+            bar_init(&sm.empty[i], C::NC / 32);
         }
-    if (veco && cols < C::COLS)
-        for (int i = tid; i < C::STAGES * kChunk * C::COLS; i += NT) {
-            const int s = i / (kChunk * C::COLS), rest = i - s * kChunk * C::COLS, row = rest / C::COLS, c = rest % C::COLS;
-            if (c >= cols) sm.st[s].dout[row * LDO + c] = from_f32<T>(0.f);
-        }
-    asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+        asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+    }
     __syncthreads();
 
-    auto load = [&](int c, int stage) {
-        const int2 ch = geo.chunk[c];
-        RChainStage<T, DK> &s = sm.st[stage];
-        const int64_t slot = (int64_t)c * geo.hv + hv;
-        uint64_t *bar = &sm.full[stage];
-        if (tid == 0) {
-            const uint32_t e = (uint32_t)(ch.y * sizeof(T));
-            bar_expect(bar, (vec ? 2 * e * geo.dk : 0u) + (veco ? e * cols : 0u) + 2 * kSquare * 4 + kVec * 4);
-            bulk_load(s.t, terms.t + slot * kSquare, kSquare * 4, bar);
-            bulk_load(s.p, terms.p + slot * kSquare, kSquare * 4, bar);
-            bulk_load(s.vec, terms.vec + slot * kVec, kVec * 4, bar);
-        }
-        if (vec) {
-            for (int r = tid; r < 2 * kChunk; r += NT) {
-                if (r < kChunk)
-                    bulk_row<T, DK>(s.k, kp + (int64_t)ch.x * geo.ldk, geo.ldk, ch.y, geo.dk, r, bar);
-                else
-                    bulk_row<T, DK>(s.q, qp + (int64_t)ch.x * geo.ldq, geo.ldq, ch.y, geo.dk, r - kChunk, bar);
+    if (warp == C::NC / 32) {
+        // ------------------------------------------------ the chunks' operands, the last chunk first
+        const T *kp = (const T *)geo.k + (int64_t)hk * geo.dkp, *qp = (const T *)geo.q + (int64_t)hk * geo.dkp;
+        const T *op = dout + (int64_t)hv * geo.dvp + vb;
+        int it = 0;
+        for (int c = c1 - 1; c >= c0; c--, it++) {
+            const int stage = it % C::STAGES;
+            if (!bar_wait(&sm.empty[stage], ((it / C::STAGES) & 1) ^ 1, &sm.abort_word, status)) break;
+            const int2 ch = geo.chunk[c];
+            RChainStage<T, DK> &s = sm.st[stage];
+            const int64_t slot = (int64_t)c * geo.hv + hv;
+            uint64_t *bar = &sm.full[stage];
+            warp_tile<T, DK>(s.k, kp + (int64_t)ch.x * geo.ldk, geo.ldk, ch.y, geo.dkp);
+            warp_tile<T, DK>(s.q, qp + (int64_t)ch.x * geo.ldq, geo.ldq, ch.y, geo.dkp);
+            warp_tile<T, C::COLS>(s.dout, op + (int64_t)ch.x * lddo, lddo, ch.y, cols);
+            cp_arrive(bar);
+            if (lane == 0) {
+                bar_expect(bar, (kSquare + kVec) * 4);
+                bulk_load(s.tp, terms.tp + slot * kSquare, kSquare * 4, bar);
+                bulk_load(s.vec, terms.vec + slot * kVec, kVec * 4, bar);
             }
-        } else {
-            load_tile<T, DK, NT>(s.k, kp + (int64_t)ch.x * geo.ldk, geo.ldk, ch.y, geo.dk, 0);
-            load_tile<T, DK, NT>(s.q, qp + (int64_t)ch.x * geo.ldq, geo.ldq, ch.y, geo.dk, 0);
         }
-        if (veco) {
-            for (int r = tid; r < kChunk; r += NT)
-                bulk_row<T, C::COLS>(s.dout, op + (int64_t)ch.x * lddo, lddo, ch.y, cols, r, bar);
-        } else {
-            load_tile<T, C::COLS, NT>(s.dout, op + (int64_t)ch.x * lddo, lddo, ch.y, cols, 0);
-        }
-    };
+        // copies in flight end before the block does
+        for (int q = it > C::STAGES ? it - C::STAGES : 0; q < it; q++)
+            for (uint32_t n = 0; n < kWaitLimit && !bar_try(&sm.full[q % C::STAGES], (q / C::STAGES) & 1); n++) {
+            }
+        return;
+    }
 
+    // ---------------------------------------------------- the groups
+    const int grp = warp / WK, w = warp - grp * WK;
+    const int v0 = vb + grp * 16, d0 = w * 32;
+    const int64_t state_at = ((int64_t)si * geo.hv + hv) * geo.dk * geo.dv;
     float D[4][4];  // dS^T: rows v0 + g, + 8, columns d0 + 8 j + 2t, + 1
 #pragma unroll
     for (int j = 0; j < 4; j++)
@@ -161,46 +137,29 @@ k_delta_rchain(const DeltaGeom geo, const DeltaTerms terms, const T *__restrict_
             }
     };
 
-    const int c0 = geo.first[si], c1 = geo.first[si + 1];
-    if (c0 < c1) load(c1 - 1, 0);
     for (int c = c1 - 1; c >= c0; c--) {
-        const int it = c1 - 1 - c, stage = C::STAGES == 2 ? it & 1 : 0;
-        // the stage is complete, and every warp is done with the previous chunk
-        const bool ok = bar_wait(&sm.full[stage], (C::STAGES == 2 ? it >> 1 : it) & 1);
-        if (!__syncthreads_and(ok)) {
-            if (tid == 0) atomicOr(status, 1u);
-            return;
-        }
-        if (C::STAGES == 2 && c > c0) load(c - 1, stage ^ 1);
+        const int it = c1 - 1 - c, stage = it % C::STAGES;
+        bar_wait(&sm.full[stage], (it / C::STAGES) & 1, &sm.abort_word, status);
         RChainStage<T, DK> &st = sm.st[stage];
         const int2 ch = geo.chunk[c];
         const int64_t slot = (int64_t)c * geo.hv + hv;
         put_state(dends + slot * geo.dk * geo.dv);
+        group_sync<WK>(grp);  // the group is done with the previous chunk's exchanges
 
         // partial (K dS')^T over the warp's key columns
         {
-            SplitA a[4];
-#pragma unroll
-            for (int j = 0; j < 4; j++) a[j].set(D[j]);
+            StateSplit<T> a;
+            a.set(D);
             float *part = sm.part[grp][w];
 #pragma unroll
-            for (int h = 0; h < 8; h += 4) {
-                Acc r[4];
-                float2 b[4][4];
+            for (int h = 0; h < 2; h++) {
+                float r[4][4];
+                state_times_rows<T, LD, false>(a, st.k, 4 * h, d0, r);
 #pragma unroll
                 for (int n = 0; n < 4; n++) {
-                    r[n].zero();
-                    frag4<T, LD, false>(st.k, (h + n) * 8, d0, b[n]);
-                }
-#pragma unroll
-                for (int j = 0; j < 4; j++)
-#pragma unroll
-                    for (int n = 0; n < 4; n++) mma_split<false, EXACT>(r[n], a[j], b[n][j]);
-#pragma unroll
-                for (int n = 0; n < 4; n++) {
-                    float *p = part + g * kLdT + (h + n) * 8 + 2 * t;
-                    *reinterpret_cast<float2 *>(p) = make_float2(r[n].get(0), r[n].get(1));
-                    *reinterpret_cast<float2 *>(p + 8 * kLdT) = make_float2(r[n].get(2), r[n].get(3));
+                    float *p = part + g * kLdT + (4 * h + n) * 8 + 2 * t;
+                    *reinterpret_cast<float2 *>(p) = make_float2(r[n][0], r[n][1]);
+                    *reinterpret_cast<float2 *>(p + 8 * kLdT) = make_float2(r[n][2], r[n][3]);
                 }
             }
         }
@@ -218,8 +177,7 @@ k_delta_rchain(const DeltaGeom geo, const DeltaTerms terms, const T *__restrict_
             for (int i = 0; i < NTILE; i++) {
                 const int n = tile_of<WK>(w, i);
                 if (k < n) continue;
-                const float *p = st.p + (k * 8 + 2 * t) * kLdT + n * 8 + g;
-                mma_split<EXACT, false>(du[i], a, make_float2(p[0], p[kLdT]));
+                mma_split<EXACT, false>(du[i], a, frag_p_later(st.tp, k, n));
             }
         }
         group_sync<WK>(grp);
@@ -252,8 +210,7 @@ k_delta_rchain(const DeltaGeom geo, const DeltaTerms terms, const T *__restrict_
                 for (int i = 0; i < NTILE; i++) {
                     const int n = tile_of<WK>(w, i);
                     if (k < n) continue;
-                    const float *p = st.t + (k * 8 + 2 * t) * kLdT + n * 8 + g;
-                    mma_split<false, false>(x[i], a, make_float2(p[0], p[kLdT]));
+                    mma_split<false, false>(x[i], a, frag_t_later(st.tp, k, n));
                 }
             }
             // the partial sums' place is free: (scale c dO)^T, split, goes there
@@ -265,13 +222,13 @@ k_delta_rchain(const DeltaGeom geo, const DeltaTerms terms, const T *__restrict_
                 const float2 bv = *reinterpret_cast<const float2 *>(st.vec + 2 * kChunk + n);
                 const float v[4] = {x[i].get(0), x[i].get(1), x[i].get(2), x[i].get(3)};
                 const float ba = -bv.x * cv.x, bb = -bv.y * cv.y;
-                sm.x[grp][at] = split_pair(ba * v[0], bb * v[1]);
-                sm.x[grp][at + 8 * kLdPair] = split_pair(ba * v[2], bb * v[3]);
+                put_pair<T>(sm.x[grp] + at, ba * v[0], bb * v[1]);
+                put_pair<T>(sm.x[grp] + at + 8 * kLdPair, ba * v[2], bb * v[3]);
                 float2 f0, f1;
                 frag2_col<T, LDO>(st.dout, n - 2 * t, grp * 16, f0, f1);
                 const float ca = geo.scale * cv.x, cb = geo.scale * cv.y;
-                y[at] = split_pair(ca * f0.x, cb * f0.y);
-                y[at + 8 * kLdPair] = split_pair(ca * f1.x, cb * f1.y);
+                put_pair<T>(y + at, ca * f0.x, cb * f0.y);
+                put_pair<T>(y + at + 8 * kLdPair, ca * f1.x, cb * f1.y);
 #pragma unroll
                 for (int e = 0; e < 4; e++) {
                     const int vc = v0 + g + (e >> 1) * 8, tok = n + (e & 1);
@@ -286,33 +243,16 @@ k_delta_rchain(const DeltaGeom geo, const DeltaTerms terms, const T *__restrict_
         }
         group_sync<WK>(grp);
         // dS^T = c_64 dS'^T + (scale c dO)^T Q - (beta c dX)^T K, each sum from zero
-        Acc ak[4], aq[4];
-#pragma unroll
-        for (int j = 0; j < 4; j++) ak[j].zero(), aq[j].zero();
-        const float4 *yq = reinterpret_cast<const float4 *>(sm.part[grp][0]);
-#pragma unroll
-        for (int k = 0; k < 8; k++) {
-            const int at = g * kLdPair + k * 4 + t;
-            SplitA a;
-            float2 b[4];
-            a.set(sm.x[grp][at], sm.x[grp][at + 8 * kLdPair]);
-            frag4<T, LD, true>(st.k, k * 8, d0, b);
-#pragma unroll
-            for (int j = 0; j < 4; j++) mma_split<false, EXACT>(ak[j], a, b[j]);
-            a.set(yq[at], yq[at + 8 * kLdPair]);
-            frag4<T, LD, true>(st.q, k * 8, d0, b);
-#pragma unroll
-            for (int j = 0; j < 4; j++) mma_split<false, EXACT>(aq[j], a, b[j]);
-        }
+        float rk[4][4], rq[4][4];
+        tokens_product<T, LD>(sm.x[grp], st.k, d0, rk);
+        tokens_product<T, LD>(reinterpret_cast<const float4 *>(sm.part[grp][0]), st.q, d0, rq);
         const float cend = st.vec[kChunk - 1];
 #pragma unroll
         for (int j = 0; j < 4; j++)
 #pragma unroll
-            for (int e = 0; e < 4; e++) D[j][e] = fmaf(cend, D[j][e], ak[j].get(e) + aq[j].get(e));
-        if (C::STAGES == 1) {
-            __syncthreads();  // the only stage is free
-            if (c > c0) load(c - 1, 0);
-        }
+            for (int e = 0; e < 4; e++) D[j][e] = fmaf(cend, D[j][e], rk[j][e] + rq[j][e]);
+        __syncwarp();
+        if (lane == 0) bar_arrive(&sm.empty[stage]);
     }
     if (ds0) put_state(ds0 + state_at);
 }
@@ -399,7 +339,7 @@ __global__ void __launch_bounds__(GradCfg<T, DK>::NT, 1)
 k_delta_grads(const DeltaGeom geo, const DeltaTerms terms, const T *__restrict__ dout, int64_t lddo,
               const float *__restrict__ states, const float *__restrict__ dends, const float *__restrict__ us,
               const float *__restrict__ dxs, float *__restrict__ dqp, float *__restrict__ dkp, T *__restrict__ dq,
-              T *__restrict__ dk, float *__restrict__ dg, float *__restrict__ dbeta, int vec, int vecv, int veco) {
+              T *__restrict__ dk, float *__restrict__ dg, float *__restrict__ dbeta, int vecv) {
     using C = GradCfg<T, DK>;
     constexpr int NG = C::NG, NT = C::NT, PT = C::PT, LD = C::LD;
     constexpr bool EXACT = sizeof(T) == 2;
@@ -414,8 +354,8 @@ k_delta_grads(const DeltaGeom geo, const DeltaTerms terms, const T *__restrict__
     const int64_t slot = (int64_t)blockIdx.x * geo.hv + hv;
     const float *S = states + slot * geo.dk * geo.dv, *DS = dends + slot * geo.dk * geo.dv;
     const float *Us = us + slot * kChunk * geo.dv, *DXs = dxs + slot * kChunk * geo.dv;
-    const T *DO = dout + (int64_t)ch.x * lddo + (int64_t)hv * geo.dv;
-    const T *V = (const T *)geo.v + (int64_t)ch.x * geo.ldv + (int64_t)hv * geo.dv;
+    const T *DO = dout + (int64_t)ch.x * lddo + (int64_t)hv * geo.dvp;
+    const T *V = (const T *)geo.v + (int64_t)ch.x * geo.ldv + (int64_t)hv * geo.dvp;
 
     auto load = [&](int v, int stage) {
         GradSlab<T, DK> &s = sm.slab[stage];
@@ -424,12 +364,12 @@ k_delta_grads(const DeltaGeom geo, const DeltaTerms terms, const T *__restrict__
         load_slab<float, DK, NT>(s.ds, DS + v, geo.dv, geo.dk, cols, vecv);
         load_slab<float, kChunk, NT>(s.u, Us + v, geo.dv, kChunk, cols, vecv);
         load_slab<float, kChunk, NT>(s.dx, DXs + v, geo.dv, kChunk, cols, vecv);
-        load_slab<T, kChunk, NT>(s.dout, DO + v, lddo, n, cols, veco);
+        load_slab<T, kChunk, NT>(s.dout, DO + v, lddo, n, geo.dvp - v, 1);
         cp_commit();
     };
 
-    load_tile<T, DK, NT>(sm.k, (const T *)geo.k + (int64_t)ch.x * geo.ldk + (int64_t)hk * geo.dk, geo.ldk, n, geo.dk, vec);
-    load_tile<T, DK, NT>(sm.q, (const T *)geo.q + (int64_t)ch.x * geo.ldq + (int64_t)hk * geo.dk, geo.ldq, n, geo.dk, vec);
+    load_tile<T, DK, NT>(sm.k, (const T *)geo.k + (int64_t)ch.x * geo.ldk + (int64_t)hk * geo.dkp, geo.ldk, n, geo.dkp);
+    load_tile<T, DK, NT>(sm.q, (const T *)geo.q + (int64_t)ch.x * geo.ldq + (int64_t)hk * geo.dkp, geo.ldq, n, geo.dkp);
     for (int i = tid; i < kVec / 4; i += NT) cp_async16(sm.vec + 4 * i, terms.vec + slot * kVec + 4 * i, 16);
     load(0, 0);
     if (warp == 0) gate_sums(geo, ch, hv, sm.bh, sm.bl);
@@ -704,11 +644,9 @@ cudaError_t rchain_dk(const DeltaGeom &g, const DeltaTerms &t, const void *dout,
     static const cudaError_t attr = cudaFuncSetAttribute(
         k_delta_rchain<T, DK>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)sizeof(RChainSmem<T, DK>));
     if (attr != cudaSuccess) return attr;
-    const int vec = mult16(g.q, g.ldq, g.dk, sizeof(T)) && mult16(g.k, g.ldk, g.dk, sizeof(T));
-    const int veco = mult16(dout, lddo, g.dv, sizeof(T));
     const dim3 grid((unsigned)(g.nseq * g.hv), (unsigned)((g.dv + C::COLS - 1) / C::COLS));
     k_delta_rchain<T, DK><<<grid, C::NT, sizeof(RChainSmem<T, DK>), st>>>(g, t, (const T *)dout, lddo, ds, dends, dxs,
-                                                                          (T *)dv, ds0, vec, veco, status);
+                                                                          (T *)dv, ds0, status);
     return cudaGetLastError();
 }
 
@@ -721,10 +659,8 @@ cudaError_t grads_dk(const DeltaGeom &g, const DeltaTerms &t, const void *dout, 
     static const cudaError_t attr = cudaFuncSetAttribute(
         k_delta_grads<T, DK>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)sizeof(GradSmem<T, DK>));
     if (attr != cudaSuccess) return attr;
-    const int vec = mult16(g.q, g.ldq, g.dk, sizeof(T)) && mult16(g.k, g.ldk, g.dk, sizeof(T));
-    const int veco = mult16(dout, lddo, g.dv, sizeof(T));
     k_delta_grads<T, DK><<<dim3(g.nchunks, g.hv), C::NT, sizeof(GradSmem<T, DK>), st>>>(
-        g, t, (const T *)dout, lddo, states, dends, us, dxs, dqp, dkp, (T *)dq, (T *)dk, dg, dbeta, vec, g.dv % 4 == 0, veco);
+        g, t, (const T *)dout, lddo, states, dends, us, dxs, dqp, dkp, (T *)dq, (T *)dk, dg, dbeta, g.dv % 4 == 0);
     return cudaGetLastError();
 }
 

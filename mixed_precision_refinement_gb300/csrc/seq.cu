@@ -116,7 +116,8 @@ int check_delta(zsolve_seq *s, const zsolve_delta_args *a, const void *o, int64_
         if (a->ldq < rk || a->ldk < rk || a->ldv < rv || ldo < rv)
             return seq_fail(s, ZSOLVE_EINVAL, "a token stride is below its heads' values");
     }
-    *g = zs::DeltaGeom{a->q, a->k, a->v, a->ldq, a->ldk, a->ldv, a->g, a->beta, a->hk, a->hv, a->dk, a->dv, a->nseq,
+    const int ve = 16 / (int)zs::type_bytes(a->type);
+    *g = zs::DeltaGeom{a->q, a->k, a->v, a->ldq, a->ldk, a->ldv, (a->dk + ve - 1) / ve * ve, (a->dv + ve - 1) / ve * ve, a->g, a->beta, a->hk, a->hv, a->dk, a->dv, a->nseq,
                        a->tokens, (float)a->scale, nullptr, nullptr, nullptr, 0};
     return ZSOLVE_OK;
 }
@@ -128,17 +129,30 @@ struct DeltaWork {
     int2 *seq = nullptr, *chunk = nullptr;
     zs::DeltaTerms terms{};
     bool backward = false;
+    void *qp = nullptr, *kp = nullptr, *vp = nullptr, *dop = nullptr;  // packed copies, where needed
     float *states = nullptr, *us = nullptr, *dends = nullptr, *dxs = nullptr, *dqp = nullptr, *dkp = nullptr;
 
-    void carve(zs::Carve &c, const zsolve_delta_args *a, bool out) {
+    const void *dout = nullptr;  // backward: the gradient of o
+    int64_t lddo = 0;
+
+    static bool aligned(const void *p, int64_t ld, int64_t d, size_t e) {
+        return (((uintptr_t)p | (uint64_t)ld * e | (uint64_t)d * e) & 15) == 0;
+    }
+    void carve(zs::Carve &c, const zsolve_delta_args *a) {
         const size_t slots = (size_t)nchunks * a->hv, sq = (size_t)zs::kSquare;
         first = c.take<int>((size_t)a->nseq + 1);
         seq = c.take<int2>((size_t)a->nseq);
         chunk = c.take<int2>((size_t)nchunks);
-        terms.t = c.take<float>(slots * sq);
-        terms.p = out ? c.take<float>(slots * sq) : nullptr;
+        terms.tp = c.take<float>(slots * sq);
         terms.vec = c.take<float>(slots * zs::kVec);
+        const size_t e = zs::type_bytes(a->type), ve = 16 / e;
+        const size_t nk = (size_t)a->tokens * a->hk * ((a->dk + ve - 1) / ve * ve) * e;
+        const size_t nv = (size_t)a->tokens * a->hv * ((a->dv + ve - 1) / ve * ve) * e;
+        qp = aligned(a->q, a->ldq, a->dk, e) ? nullptr : c.take<char>(nk);
+        kp = aligned(a->k, a->ldk, a->dk, e) ? nullptr : c.take<char>(nk);
+        vp = aligned(a->v, a->ldv, a->dv, e) ? nullptr : c.take<char>(nv);
         if (!backward) return;
+        dop = aligned(dout, lddo, a->dv, e) ? nullptr : c.take<char>(nv);
         const size_t state = (size_t)a->dk * a->dv, rows = (size_t)zs::kChunk * a->dv;
         states = c.take<float>(slots * state);
         us = c.take<float>(slots * rows);
@@ -148,25 +162,43 @@ struct DeltaWork {
         dqp = c.take<float>((size_t)a->tokens * a->hv * a->dk);
         dkp = c.take<float>((size_t)a->tokens * a->hv * a->dk);
     }
-    int place(zsolve_seq *s, const zsolve_delta_args *a, bool out) {
+    int place(zsolve_seq *s, const zsolve_delta_args *a) {
         // a sequence's last chunk may be short: one more each at most
         const int64_t most = a->tokens / zs::kChunk + a->nseq;
         if (most > 0x7fffffff / zs::kChunk) return seq_fail(s, ZSOLVE_EINVAL, "too many chunks");
         nchunks = (int)most;
         zs::Carve size(nullptr);
-        carve(size, a, out);
+        carve(size, a);
         int st = ZSOLVE_OK;
         void *ws = zs::seq_workspace(s, size.at, &st);
         if (!ws) return st;
         zs::Carve c(ws);
-        carve(c, a, out);
+        carve(c, a);
         return ZSOLVE_OK;
     }
-    void bind(zs::DeltaGeom *g) const {
+    // The geometry on the workspace's tables and, where they are needed, packed copies.
+    int bind(zsolve_seq *s, const zsolve_delta_args *a, zs::DeltaGeom *g) {
+        struct {
+            const void **p;
+            int64_t *ld;
+            void *copy;
+            int heads, d, dp;
+        } const t[4] = {{&g->q, &g->ldq, qp, a->hk, a->dk, g->dkp},
+                        {&g->k, &g->ldk, kp, a->hk, a->dk, g->dkp},
+                        {&g->v, &g->ldv, vp, a->hv, a->dv, g->dvp},
+                        {&dout, &lddo, dop, a->hv, a->dv, g->dvp}};
+        for (const auto &x : t) {
+            if (!x.copy || a->tokens == 0) continue;
+            SEQ_CU(zs_launch_delta_pack(a->type, *x.p, *x.ld, a->tokens, x.heads, x.d, x.dp, x.copy, s->num_sms, s->st,
+                                        &s->launches));
+            *x.p = x.copy;
+            *x.ld = (int64_t)x.heads * x.dp;
+        }
         g->first = first;
         g->seq = seq;
         g->chunk = chunk;
         g->nchunks = nchunks;
+        return ZSOLVE_OK;
     }
 };
 
@@ -326,9 +358,9 @@ int zsolve_delta(zsolve_seq *s, const zsolve_delta_args *a, void *o, int64_t ldo
         return ZSOLVE_OK;
     }
     DeltaWork w;
-    st = w.place(s, a, true);
+    st = w.place(s, a);
+    if (st == ZSOLVE_OK) st = w.bind(s, a, &g);
     if (st != ZSOLVE_OK) return st;
-    w.bind(&g);
     SEQ_CU(zs_launch_delta_plan(a->offsets, a->nseq, a->tokens, w.nchunks, w.first, w.seq, w.chunk, s->st, &s->launches));
     SEQ_CU(zs_launch_delta_terms(a->type, g, w.terms, s->st, &s->launches));
     SEQ_CU(zs_launch_delta_chain(a->type, g, w.terms, a->s0, o, ldo, sn, nullptr, nullptr, s->d_status, s->st, &s->launches));
@@ -359,9 +391,11 @@ int zsolve_delta_bwd(zsolve_seq *s, const zsolve_delta_args *a, const void *dout
     if (st != ZSOLVE_OK) return st;
     DeltaWork w;
     w.backward = true;
-    st = w.place(s, a, true);
+    w.dout = dout;
+    w.lddo = lddo;
+    st = w.place(s, a);
+    if (st == ZSOLVE_OK) st = w.bind(s, a, &g);
     if (st != ZSOLVE_OK) return st;
-    w.bind(&g);
     SEQ_CU(zs_launch_delta_plan(a->offsets, a->nseq, a->tokens, w.nchunks, w.first, w.seq, w.chunk, s->st, &s->launches));
     if (a->tokens > 0) {
         SEQ_CU(zs_launch_delta_terms(a->type, g, w.terms, s->st, &s->launches));
@@ -370,10 +404,10 @@ int zsolve_delta_bwd(zsolve_seq *s, const zsolve_delta_args *a, const void *dout
         SEQ_CU(zs_launch_delta_chain(a->type, g, w.terms, a->s0, nullptr, 0, nullptr, w.states, w.us, s->d_status, s->st,
                                      &s->launches));
     }
-    SEQ_CU(zs_launch_delta_rchain(a->type, g, w.terms, dout, lddo, ds, w.dends, w.dxs, dv, ds0, s->d_status, s->st,
+    SEQ_CU(zs_launch_delta_rchain(a->type, g, w.terms, w.dout, w.lddo, ds, w.dends, w.dxs, dv, ds0, s->d_status, s->st,
                                   &s->launches));
     if (a->tokens > 0)
-        SEQ_CU(zs_launch_delta_grads(a->type, g, w.terms, dout, lddo, w.states, w.dends, w.us, w.dxs, w.dqp, w.dkp, dq,
+        SEQ_CU(zs_launch_delta_grads(a->type, g, w.terms, w.dout, w.lddo, w.states, w.dends, w.us, w.dxs, w.dqp, w.dkp, dq,
                                      dk, dg, dbeta, s->st, &s->launches));
     return ZSOLVE_OK;
 }

@@ -338,6 +338,12 @@ struct ChainSmem {
     int abort_word;
 };
 
+// U as P U takes it: rounded to tf32 where o has 16 bits.
+template <typename T>
+__device__ __forceinline__ float2 out_pair(float a, float b) {
+    return sizeof(T) == 2 ? make_float2(__uint_as_float(tf32(a)), __uint_as_float(tf32(b))) : make_float2(a, b);
+}
+
 template <typename T, int DK, bool OUT>
 __global__ void __launch_bounds__(ChainCfg<T, DK>::NT, 1)
 k_delta_chain(const DeltaGeom geo, const DeltaTerms terms, const float *__restrict__ s0, T *__restrict__ o,
@@ -494,30 +500,20 @@ k_delta_chain(const DeltaGeom geo, const DeltaTerms terms, const float *__restri
         }
         // U^T = X^T T^T at the warp's token tiles
         {
-            Acc u[NTILE];
-#pragma unroll
-            for (int i = 0; i < NTILE; i++) u[i].zero();
-#pragma unroll
-            for (int k = 0; k < 8; k++) {
-                SplitA a;
-                a.set(sm.x[grp][g * kLdPair + k * 4 + t], sm.x[grp][(g + 8) * kLdPair + k * 4 + t]);
-#pragma unroll
-                for (int i = 0; i < NTILE; i++) {
-                    const int n = tile_of<WK>(w, i);
-                    if (k > n) continue;
-                    mma_split<false, false>(u[i], a, frag_t_earlier(st.tp, k, n));
-                }
-            }
+            float u[NTILE][4];
+            triangular<WK, true, false, false>(
+                w, u, [&](int k, SplitA &a) { a.set(sm.x[grp][g * kLdPair + k * 4 + t], sm.x[grp][(g + 8) * kLdPair + k * 4 + t]); },
+                [&](int k, int n) { return frag_t_earlier(st.tp, k, n); });
 #pragma unroll
             for (int i = 0; i < NTILE; i++) {
                 const int n = tile_of<WK>(w, i) * 8 + 2 * t, at = g * kLdPair + n / 2;
                 const float2 ev = *reinterpret_cast<const float2 *>(st.vec + kChunk + n);
-                const float v[4] = {u[i].get(0), u[i].get(1), u[i].get(2), u[i].get(3)};
+                const float(&v)[4] = u[i];
                 put_pair<T>(sm.u[grp] + at, ev.x * v[0], ev.y * v[1]);
                 put_pair<T>(sm.u[grp] + at + 8 * kLdPair, ev.x * v[2], ev.y * v[3]);
                 if (OUT) {
-                    sm.un[grp][at] = make_float2(v[0], v[1]);
-                    sm.un[grp][at + 8 * kLdPair] = make_float2(v[2], v[3]);
+                    sm.un[grp][at] = out_pair<T>(v[0], v[1]);
+                    sm.un[grp][at + 8 * kLdPair] = out_pair<T>(v[2], v[3]);
                 }
                 if (us) {
 #pragma unroll
@@ -542,21 +538,17 @@ k_delta_chain(const DeltaGeom geo, const DeltaTerms terms, const float *__restri
         }
         // O^T = scale c (Q S)^T + U^T P^T at the warp's token tiles
         if (OUT) {
-            Acc oa[NTILE];
-#pragma unroll
-            for (int i = 0; i < NTILE; i++) oa[i].zero();
-#pragma unroll
-            for (int k = 0; k < 8; k++) {
-                const float2 y = sm.un[grp][g * kLdPair + k * 4 + t], z = sm.un[grp][(g + 8) * kLdPair + k * 4 + t];
-                SplitA a;
-                a.set(y.x, y.y, z.x, z.y);
-#pragma unroll
-                for (int i = 0; i < NTILE; i++) {
-                    const int n = tile_of<WK>(w, i);
-                    if (k > n) continue;
-                    mma_split<false, false, EXACT>(oa[i], a, frag_p_earlier(st.tp, k, n));
-                }
-            }
+            float oa[NTILE][4];
+            triangular<WK, true, false, EXACT>(
+                w, oa,
+                [&](int k, SplitA &a) {
+                    const float2 y = sm.un[grp][g * kLdPair + k * 4 + t], z = sm.un[grp][(g + 8) * kLdPair + k * 4 + t];
+                    if (EXACT)
+                        a.hi[0] = __float_as_uint(y.x), a.hi[1] = __float_as_uint(z.x), a.hi[2] = __float_as_uint(y.y), a.hi[3] = __float_as_uint(z.y);
+                    else
+                        a.set(y.x, y.y, z.x, z.y);
+                },
+                [&](int k, int n) { return frag_p_earlier(st.tp, k, n); });
             T *stg = reinterpret_cast<T *>(sm.x[grp]);
 #pragma unroll
             for (int i = 0; i < NTILE; i++) {
@@ -570,8 +562,8 @@ k_delta_chain(const DeltaGeom geo, const DeltaTerms terms, const float *__restri
                 }
                 const float2 cv = *reinterpret_cast<const float2 *>(st.vec + n);
                 const float ca = geo.scale * cv.x, cb = geo.scale * cv.y;
-                const float r[4] = {fmaf(ca, lo.x, EXACT ? oa[i].c[0] : oa[i].get(0)), fmaf(cb, lo.y, EXACT ? oa[i].c[1] : oa[i].get(1)),
-                                    fmaf(ca, hi.x, EXACT ? oa[i].c[2] : oa[i].get(2)), fmaf(cb, hi.y, EXACT ? oa[i].c[3] : oa[i].get(3))};
+                const float r[4] = {fmaf(ca, lo.x, oa[i][0]), fmaf(cb, lo.y, oa[i][1]), fmaf(ca, hi.x, oa[i][2]),
+                                    fmaf(cb, hi.y, oa[i][3])};
                 if (veco) {
 #pragma unroll
                     for (int e = 0; e < 4; e++) stg[(n + (e & 1)) * 16 + g + (e >> 1) * 8] = from_f32<T>(r[e]);

@@ -576,6 +576,64 @@ __device__ __forceinline__ int tile_of(int w, int i) {
     return (i & 1) ? (i + 1) * WK - 1 - w : i * WK + w;
 }
 
+// The triangular products of a warp's pair p of token tiles, n0 < n1, one step of
+// 8 x 8 x 8 after the other: as many for every warp of the group, so that the
+// steps unroll without a branch and their loads run ahead.  EARLIER: tile n takes
+// the tiles k = 0 .. n; else k = n .. 7.
+template <int WK, bool EARLIER>
+__host__ __device__ constexpr int steps_of(int p) {
+    return EARLIER ? (4 * p + 2) * WK + 1 : 17 - (4 * p + 2) * WK;
+}
+template <int WK, bool EARLIER>
+__device__ __forceinline__ void step_of(int w, int p, int s, int &k, int &n, bool &first) {
+    const int n0 = tile_of<WK>(w, 2 * p), n1 = tile_of<WK>(w, 2 * p + 1);
+    if (EARLIER) {
+        first = s <= n0;
+        k = first ? s : s - n0 - 1;
+    } else {
+        first = s < 8 - n0;
+        k = first ? n0 + s : n1 + s - (8 - n0);
+    }
+    n = first ? n0 : n1;
+}
+
+// x[2p], x[2p + 1] = the pair's results: sums of steps, each from zero and rounded
+// to nearest.  A(k): the step's A operand; B(k, n): its B operand; HALF: see mma_split.
+template <int WK, bool EARLIER, bool A_EXACT, bool HALF, typename FA, typename FB>
+__device__ __forceinline__ void triangular(int w, float (&x)[8 / WK][4], FA A, FB B) {
+#pragma unroll
+    for (int p = 0; p < 4 / WK; p++) {
+        float a0[4] = {}, a1[4] = {};
+#pragma unroll
+        for (int s = 0; s < steps_of<WK, EARLIER>(p); s++) {
+            int k, n;
+            bool first;
+            step_of<WK, EARLIER>(w, p, s, k, n, first);
+            SplitA a;
+            A(k, a);
+            const float2 b = B(k, n);
+            const uint32_t b0 = tf32(b.x), b1 = tf32(b.y);
+            float d[4];
+            if (HALF) {
+                mma8_first(d, a.hi, b0, b1);
+            } else {
+                mma8_first(d, a.hi, tf32(b.x - __uint_as_float(b0)), tf32(b.y - __uint_as_float(b1)));
+                if (!A_EXACT) mma8(d, a.lo, b0, b1);
+                mma8(d, a.hi, b0, b1);
+            }
+            if (first) {
+#pragma unroll
+                for (int e = 0; e < 4; e++) a0[e] += d[e];
+            } else {
+#pragma unroll
+                for (int e = 0; e < 4; e++) a1[e] += d[e];
+            }
+        }
+#pragma unroll
+        for (int e = 0; e < 4; e++) x[2 * p][e] = a0[e], x[2 * p + 1][e] = a1[e];
+    }
+}
+
 // The warps of one column group wait for each other.
 template <int WK>
 __device__ __forceinline__ void group_sync(int group) {

@@ -164,22 +164,15 @@ k_delta_rchain(const DeltaGeom geo, const DeltaTerms terms, const T *__restrict_
             }
         }
         // (P^T dO)^T at the warp's token tiles: dO^T is the A operand, P's rows from the tile on
-        Acc du[NTILE];
-#pragma unroll
-        for (int i = 0; i < NTILE; i++) du[i].zero();
-#pragma unroll
-        for (int k = 0; k < 8; k++) {
-            float2 f0, f1;
-            frag2_col<T, LDO>(st.dout, k * 8, grp * 16, f0, f1);
-            SplitA a;
-            a.set(f0.x, f0.y, f1.x, f1.y);
-#pragma unroll
-            for (int i = 0; i < NTILE; i++) {
-                const int n = tile_of<WK>(w, i);
-                if (k < n) continue;
-                mma_split<EXACT, false>(du[i], a, frag_p_later(st.tp, k, n));
-            }
-        }
+        float du[NTILE][4];
+        triangular<WK, false, EXACT, false>(
+            w, du,
+            [&](int k, SplitA &a) {
+                float2 f0, f1;
+                frag2_col<T, LDO>(st.dout, k * 8, grp * 16, f0, f1);
+                a.set(f0.x, f0.y, f1.x, f1.y);
+            },
+            [&](int k, int n) { return frag_p_later(st.tp, k, n); });
         group_sync<WK>(grp);
 #pragma unroll
         for (int i = 0; i < NTILE; i++) {
@@ -193,26 +186,16 @@ k_delta_rchain(const DeltaGeom geo, const DeltaTerms terms, const T *__restrict_
             }
             const float2 ev = *reinterpret_cast<const float2 *>(st.vec + kChunk + n);
             float4 *u = sm.u[grp] + g * kLdPair + n / 2;
-            u[0] = split_pair(fmaf(ev.x, lo.x, du[i].get(0)), fmaf(ev.y, lo.y, du[i].get(1)));
-            u[8 * kLdPair] = split_pair(fmaf(ev.x, hi.x, du[i].get(2)), fmaf(ev.y, hi.y, du[i].get(3)));
+            u[0] = split_pair(fmaf(ev.x, lo.x, du[i][0]), fmaf(ev.y, lo.y, du[i][1]));
+            u[8 * kLdPair] = split_pair(fmaf(ev.x, hi.x, du[i][2]), fmaf(ev.y, hi.y, du[i][3]));
         }
         group_sync<WK>(grp);
         // dX^T = dU^T T at the warp's token tiles: T's rows from the tile on
         {
-            Acc x[NTILE];
-#pragma unroll
-            for (int i = 0; i < NTILE; i++) x[i].zero();
-#pragma unroll
-            for (int k = 0; k < 8; k++) {
-                SplitA a;
-                a.set(sm.u[grp][g * kLdPair + k * 4 + t], sm.u[grp][(g + 8) * kLdPair + k * 4 + t]);
-#pragma unroll
-                for (int i = 0; i < NTILE; i++) {
-                    const int n = tile_of<WK>(w, i);
-                    if (k < n) continue;
-                    mma_split<false, false>(x[i], a, frag_t_later(st.tp, k, n));
-                }
-            }
+            float x[NTILE][4];
+            triangular<WK, false, false, false>(
+                w, x, [&](int k, SplitA &a) { a.set(sm.u[grp][g * kLdPair + k * 4 + t], sm.u[grp][(g + 8) * kLdPair + k * 4 + t]); },
+                [&](int k, int n) { return frag_t_later(st.tp, k, n); });
             // the partial sums' place is free: (scale c dO)^T, split, goes there
             float4 *y = reinterpret_cast<float4 *>(sm.part[grp][0]);
 #pragma unroll
@@ -220,7 +203,7 @@ k_delta_rchain(const DeltaGeom geo, const DeltaTerms terms, const T *__restrict_
                 const int n = tile_of<WK>(w, i) * 8 + 2 * t, at = g * kLdPair + n / 2;
                 const float2 cv = *reinterpret_cast<const float2 *>(st.vec + n);
                 const float2 bv = *reinterpret_cast<const float2 *>(st.vec + 2 * kChunk + n);
-                const float v[4] = {x[i].get(0), x[i].get(1), x[i].get(2), x[i].get(3)};
+                const float(&v)[4] = x[i];
                 const float ba = -bv.x * cv.x, bb = -bv.y * cv.y;
                 put_pair<T>(sm.x[grp] + at, ba * v[0], bb * v[1]);
                 put_pair<T>(sm.x[grp] + at + 8 * kLdPair, ba * v[2], bb * v[3]);

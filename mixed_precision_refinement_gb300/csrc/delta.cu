@@ -392,10 +392,7 @@ k_delta_chain(const DeltaGeom geo, const DeltaTerms terms, const float *__restri
                 bulk_load(s.vec, terms.vec + slot * kVec, kVec * 4, bar);
             }
         }
-        // copies in flight end before the block does
-        for (int q = it > C::STAGES ? it - C::STAGES : 0; q < it; q++)
-            for (uint32_t n = 0; n < kWaitLimit && !bar_try(&sm.full[q % C::STAGES], (q / C::STAGES) & 1); n++) {
-            }
+        bar_drain(sm.full, C::STAGES, it);  // copies in flight end before the block does
         return;
     }
 

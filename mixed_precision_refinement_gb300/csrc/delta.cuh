@@ -472,52 +472,6 @@ __device__ __forceinline__ float2 frag_p_later(const float *m, int k, int n) {
     return b;
 }
 
-// A chunk's operands arrive on an mbarrier, fetched by a warp of their own as
-// stages become free.  Waits are bounded: on give-up the block's
-// abort word and the status word are set, and every later wait of the block
-// returns at once, so that all warps run to their end.
-__device__ __forceinline__ void bar_init(uint64_t *bar, uint32_t count) {
-    asm volatile("mbarrier.init.shared::cta.b64 [%0], %1;" ::"r"((uint32_t)__cvta_generic_to_shared(bar)), "r"(count)
-                 : "memory");
-}
-__device__ __forceinline__ void bar_expect(uint64_t *bar, uint32_t bytes) {
-    asm volatile("mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;" ::"r"((uint32_t)__cvta_generic_to_shared(bar)),
-                 "r"(bytes)
-                 : "memory");
-}
-__device__ __forceinline__ void bar_arrive(uint64_t *bar) {
-    asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"((uint32_t)__cvta_generic_to_shared(bar)) : "memory");
-}
-__device__ __forceinline__ bool bar_try(uint64_t *bar, uint32_t parity) {
-    uint32_t ok;
-    asm volatile(
-        "{\n\t.reg .pred p;\n\t"
-        "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
-        "selp.u32 %0, 1, 0, p;\n\t}"
-        : "=r"(ok)
-        : "r"((uint32_t)__cvta_generic_to_shared(bar)), "r"(parity)
-        : "memory");
-    return ok != 0;
-}
-constexpr uint32_t kWaitLimit = 1u << 19;  // about a second
-__device__ __forceinline__ bool bar_wait(uint64_t *bar, uint32_t parity, volatile int *abort_word, unsigned *status) {
-    for (uint32_t it = 0; !bar_try(bar, parity); it++) {
-        if (*abort_word) return false;
-        if (it >= kWaitLimit) {
-            *abort_word = 1;
-            atomicOr(status, 1u);
-            return false;
-        }
-    }
-    return true;
-}
-__device__ __forceinline__ void bulk_load(void *dst, const void *src, uint32_t bytes, uint64_t *bar) {
-    asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(
-                     (uint32_t)__cvta_generic_to_shared(dst)),
-                 "l"(src), "r"(bytes), "r"((uint32_t)__cvta_generic_to_shared(bar))
-                 : "memory");
-}
-
 // One warp: a tile of 64 rows x D columns from n rows of d values (whole 16
 // bytes) at stride ld, by 16-byte copies that write zeros elsewhere (a bulk copy
 // a row is issued a lane at a time, and 192 of them took longer than a chunk's

@@ -17,7 +17,7 @@ constexpr int kMaxRows = 4;   // of 32 key rows: dk <= 128
 // VE: value columns of a thread (4: dv a multiple of 4), 32 / VE threads a
 // row, ROWS rows a thread.
 template <typename T, int VE>
-__global__ void __launch_bounds__(kThreads)
+__global__ void __launch_bounds__(kThreads, 5)
 k_delta_step(const DeltaGeom geo, const int64_t *__restrict__ offsets, const float *__restrict__ s0,
              T *__restrict__ o, int64_t ldo, float *__restrict__ sn) {
     constexpr int TPR = kCols / VE;               // threads a row
@@ -25,8 +25,8 @@ k_delta_step(const DeltaGeom geo, const int64_t *__restrict__ offsets, const flo
     constexpr int NR = 128 / RPP;                 // passes
     constexpr int NW = kThreads / 32;
     __shared__ float qs[128], ks[128];
-    __shared__ float red[NW][2][kCols];
-    __shared__ float dots[NW];
+    __shared__ __align__(16) float red[NW][2][kCols];
+    __shared__ __align__(16) float dots[NW];
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int si = blockIdx.x / geo.hv, hv = blockIdx.x - si * geo.hv, hk = hv / (geo.hv / geo.hk);
     const int col = (tid % TPR) * VE, row = tid / TPR;
@@ -99,18 +99,23 @@ k_delta_step(const DeltaGeom geo, const int64_t *__restrict__ offsets, const flo
         float qk = 0.f;
 #pragma unroll
         for (int w = 0; w < NW; w++) qk += dots[w];
-        float u[VE];
+        float s1[VE] = {}, s2[VE] = {}, u[VE];
+#pragma unroll
+        for (int w = 0; w < NW; w++) {
+            float x[VE], y[VE];
+            Vec<float, VE> f;
+            f.load(&red[w][0][col]);
+            f.get(x);
+            f.load(&red[w][1][col]);
+            f.get(y);
+#pragma unroll
+            for (int e = 0; e < VE; e++) s1[e] += x[e], s2[e] += y[e];
+        }
 #pragma unroll
         for (int e = 0; e < VE; e++) {
-            float s1 = 0.f, s2 = 0.f;
-#pragma unroll
-            for (int w = 0; w < NW; w++) {
-                s1 += red[w][0][col + e];
-                s2 += red[w][1][col + e];
-            }
-            u[e] = beta * (vv[e] - a * s1);
+            u[e] = beta * (vv[e] - a * s1[e]);
             if (row == 0 && live)
-                o[tok * ldo + (int64_t)hv * geo.dv + v + e] = from_f32<T>(geo.scale * fmaf(a, s2, qk * u[e]));
+                o[tok * ldo + (int64_t)hv * geo.dv + v + e] = from_f32<T>(geo.scale * fmaf(a, s2[e], qk * u[e]));
         }
 #pragma unroll
         for (int p = 0; p < NR; p++) {

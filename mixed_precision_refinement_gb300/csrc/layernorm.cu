@@ -28,10 +28,23 @@ __device__ __forceinline__ float2 row_sum(float2 v, float2 *red, int flip) {
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     if (lane == 0) r[warp] = v;
     __syncthreads();
-    float2 t = lane < NW ? r[lane] : make_float2(0.f, 0.f);
-    t.x = warp_sum(t.x);
-    t.y = warp_sum(t.y);
-    return t;
+    // every thread adds the warps' sums itself: broadcast reads, without the
+    // latency of five more shuffles
+    float2 t = r[0], u = r[1];
+#pragma unroll
+    for (int w = 2; w < NW; w += 2) {
+        t.x += r[w].x, t.y += r[w].y;
+        u.x += r[w + 1].x, u.y += r[w + 1].y;
+    }
+    return make_float2(t.x + u.x, t.y + u.y);
+}
+
+// A load that stays where it is written: the next rows' mean and rstd, which the
+// compiler would otherwise be free to move down to their use, a row later.
+__device__ __forceinline__ float load_early(const float *p) {
+    float v;
+    asm volatile("ld.global.nc.f32 %0, [%1];" : "=f"(v) : "l"(p));
+    return v;
 }
 
 template <typename T>
@@ -50,6 +63,18 @@ __device__ __forceinline__ void load_wv(const void *w, int wf32, int64_t i, floa
     }
 #pragma unroll
     for (int e = 0; e < N; e++) f[e] = load_w<T>(w, wf32, i + e);
+}
+
+// The same from shared memory, where both types of w are aligned.
+template <typename T, int N>
+__device__ __forceinline__ void load_ws(const void *w, int wf32, int i, float *f) {
+    if (N > 1 && wf32) {
+#pragma unroll
+        for (int e = 0; e < N; e += 4)
+            *reinterpret_cast<float4 *>(f + e) = *reinterpret_cast<const float4 *>(reinterpret_cast<const float *>(w) + i + e);
+    } else {
+        load_wv<T, N>(w, wf32, i, f);
+    }
 }
 
 // Forward: TPR threads hold a row, VE consecutive values at a time (VE = 1
@@ -188,10 +213,12 @@ k_layernorm_bwd(const T *__restrict__ dy, int64_t lddy, const T *__restrict__ x,
             }
         }
     };
+    float mu_next = 0.f, rs_next = 0.f;
+    if (row < rows) mu_next = mean[row], rs_next = rstd[row];
     fetch(row);
     int flip = 0;
     for (; row < rows; row += step, flip ^= 1) {  // TPR > 32: the same rows in all of the block's threads
-        const float mu = mean[row], rs = rstd[row];
+        const float mu = mu_next, rs = rs_next;
         float h[NI * VE], a[NI * VE];
         float2 s = make_float2(0.f, 0.f);
 #pragma unroll
@@ -203,6 +230,7 @@ k_layernorm_bwd(const T *__restrict__ dy, int64_t lddy, const T *__restrict__ x,
             }
         }
         fetch(row + step);  // the next row's loads run during this row's reduction
+        if (row + step < rows) mu_next = load_early(mean + row + step), rs_next = load_early(rstd + row + step);
 #pragma unroll
         for (int i = 0; i < NI; i++) {
             const int c = (i * TPR + t) * VE;
@@ -249,6 +277,163 @@ k_layernorm_bwd(const T *__restrict__ dy, int64_t lddy, const T *__restrict__ x,
             for (int e = 0; e < VE; e++) {
                 pw[c + e] = aw[i * VE + e];
                 pw[d + c + e] = ab[i * VE + e];
+            }
+        }
+    }
+}
+
+// The same for longer rows, where registers alone do not keep enough bytes on
+// their way: rows of x and dy arrive in a ring of kRing rows in shared memory, a
+// bulk copy each, issued as soon as a row's reduction shows that every thread
+// has read it.  A row need not start on 16 bytes (the tensors do): the copy takes
+// the whole 16 bytes that begin in it, and the last values are read directly.
+// mean and rstd are fetched two rows ahead.
+constexpr int kRing = 4;
+// threads of an SM that hold E values each: up to 85 or 64 registers
+template <int E>
+__host__ __device__ constexpr int ring_threads() {
+    return E > 8 ? 768 : 1024;
+}
+template <typename T>
+__host__ __device__ constexpr int ring_row(int d) {  // values of a ring row
+    return (d + 2 * (16 / (int)sizeof(T)) - 1) / (16 / (int)sizeof(T)) * (16 / (int)sizeof(T));
+}
+
+template <typename T, int VE, int TPR, int NI>
+__global__ void __launch_bounds__(TPR, ring_threads<NI * VE>() / TPR > 0 ? ring_threads<NI * VE>() / TPR : 1)
+k_layernorm_bwd_ring(const T *__restrict__ dy, int64_t lddy, const T *__restrict__ x, int64_t ldx,
+                     const float *__restrict__ mean, const float *__restrict__ rstd, const void *__restrict__ w,
+                     int wf32, int64_t rows, int d, T *__restrict__ dx, int64_t lddx, float *__restrict__ parts,
+                     unsigned *__restrict__ status) {
+    extern __shared__ __align__(16) uint8_t smem_raw[];
+    __shared__ float2 red[2 * (TPR / 32)];
+    __shared__ __align__(8) uint64_t full[kRing];
+    __shared__ volatile int s_abort;
+    T *ring = reinterpret_cast<T *>(smem_raw);
+    const int rr = ring_row<T>(d), t = threadIdx.x;
+    void *ws = ring + 2 * kRing * rr;  // w, read again for every row
+    if (w)
+        for (int c = t; c < d; c += TPR) {
+            if (wf32)
+                reinterpret_cast<float *>(ws)[c] = reinterpret_cast<const float *>(w)[c];
+            else
+                reinterpret_cast<T *>(ws)[c] = reinterpret_cast<const T *>(w)[c];
+        }
+    constexpr int A = 16 / (int)sizeof(T);
+    const float inv = 1.f / (float)d;
+    if (t == 0) {
+        s_abort = 0;
+        for (int i = 0; i < kRing; i++) bar_init(&full[i], 1);
+        asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+    }
+    __syncthreads();
+    // a row that starts at value `at` begins `off` values into its ring row (at most
+    // one group of 16 bytes); its values 0 .. whole - off - 1 are copied
+    auto offset = [&](int64_t at) { return (int)((unsigned)at % A); };
+    auto whole = [&](int off) { return (off + d) / A * A; };
+    auto issue = [&](int64_t row, int i) {
+        const int64_t ax = row * ldx, ad = row * lddy;
+        const int ox = offset(ax), od = offset(ad);
+        const uint32_t bx = (uint32_t)(whole(ox) * sizeof(T)), bd = (uint32_t)(whole(od) * sizeof(T));
+        bar_expect(&full[i], bx + bd);
+        bulk_load(ring + 2 * i * rr, x + (ax - ox), bx, &full[i]);
+        bulk_load(ring + (2 * i + 1) * rr, dy + (ad - od), bd, &full[i]);
+    };
+    // a block's rows are neighbours: eight of them share a sector of mean and rstd
+    const int64_t row0 = rows * blockIdx.x / gridDim.x, row1 = rows * (blockIdx.x + 1) / gridDim.x;
+    if (t == 0)
+        for (int i = 0; i < kRing; i++)
+            if (row0 + i < row1) issue(row0 + i, i);
+    constexpr int NP = NI * VE / 2;  // pairs of values a thread holds
+    float2 aw[NP], ab[NP];
+#pragma unroll
+    for (int i = 0; i < NP; i++) aw[i] = ab[i] = make_float2(0.f, 0.f);
+    float mu_next = 0.f, rs_next = 0.f, mu_later = 0.f, rs_later = 0.f;
+    if (row0 < row1) mu_next = mean[row0], rs_next = rstd[row0];
+    if (row0 + 1 < row1) mu_later = mean[row0 + 1], rs_later = rstd[row0 + 1];
+    int it = 0;
+    for (int64_t row = row0; row < row1; row++, it++) {
+        const float mu = mu_next, rs = rs_next;
+        mu_next = mu_later, rs_next = rs_later;
+        if (row + 2 < row1) mu_later = load_early(mean + row + 2), rs_later = load_early(rstd + row + 2);
+        const int slot = it % kRing;
+        bar_wait(&full[slot], (it / kRing) & 1, &s_abort, status);
+        const int offx = offset(row * ldx), nx = whole(offx) - offx, offd = offset(row * lddy), nd = whole(offd) - offd;
+        const T *xs = ring + 2 * slot * rr + offx, *ds = ring + (2 * slot + 1) * rr + offd;
+        // values beyond the row count as zeros of dy
+        float2 h[NP], a[NP], sx = make_float2(0.f, 0.f), sy = sx;
+        const float2 rs2 = make_float2(rs, rs), nm2 = make_float2(-mu * rs, -mu * rs);
+        constexpr int G = VE > 1 ? VE : 2;  // values at a time
+#pragma unroll
+        for (int i = 0; i < NI * VE / G; i++) {
+            float hf[G], af[G], wf[G];
+#pragma unroll
+            for (int e = 0; e < G; e++) hf[e] = af[e] = 0.f, wf[e] = 1.f;
+            if (VE > 1) {
+                const int c = (i * TPR + t) * VE;
+                if (c < d) {  // whole 16 bytes: all of them copied
+                    Vec<T, VE> u;
+                    u.load(xs + c);
+                    u.get(hf);
+                    u.load(ds + c);
+                    u.get(af);
+                    if (w) load_ws<T, VE>(ws, wf32, c, wf);
+                }
+            } else {
+#pragma unroll
+                for (int e = 0; e < G; e++) {
+                    const int c = (i * G + e) * TPR + t;
+                    if (c < d) {
+                        hf[e] = to_f32(c < nx ? xs[c] : x[row * ldx + c]);
+                        af[e] = to_f32(c < nd ? ds[c] : dy[row * lddy + c]);
+                        if (w) wf[e] = load_w<T>(ws, wf32, c);
+                    }
+                }
+            }
+#pragma unroll
+            for (int e = 0; e < G / 2; e++) {
+                const int j = i * (G / 2) + e;
+                const float2 v = make_float2(af[2 * e], af[2 * e + 1]);
+                h[j] = fma2(make_float2(hf[2 * e], hf[2 * e + 1]), rs2, nm2);
+                aw[j] = fma2(v, h[j], aw[j]);
+                ab[j] = add2(v, ab[j]);
+                a[j] = w ? mul2(v, make_float2(wf[2 * e], wf[2 * e + 1])) : v;
+                sx = add2(a[j], sx);
+                sy = fma2(a[j], h[j], sy);
+            }
+        }
+        float2 s = make_float2(sx.x + sx.y, sy.x + sy.y);
+        s = row_sum<TPR>(s, red, it & 1);
+        if (t == 0 && row + kRing < row1) issue(row + kRing, slot);
+        const float m1 = -rs * s.x * inv, m2 = -rs * s.y * inv;
+        const float2 m12 = make_float2(m1, m1), m22 = make_float2(m2, m2);
+#pragma unroll
+        for (int j = 0; j < NP; j++) a[j] = fma2(h[j], m22, fma2(a[j], rs2, m12));
+#pragma unroll
+        for (int i = 0; i < NI; i++) {
+            const int c = (i * TPR + t) * VE;
+            if (c < d) {
+                float o[VE];
+#pragma unroll
+                for (int e = 0; e < VE; e++) o[e] = (i * VE + e) & 1 ? a[(i * VE + e) / 2].y : a[(i * VE + e) / 2].x;
+                Vec<T, VE> r;
+                r.set(o);
+                r.store(dx + row * lddx + c);
+            }
+        }
+    }
+    if (t == 0 && s_abort) bar_drain(full, kRing, it);
+    if (!parts) return;
+    float *pw = parts + (int64_t)blockIdx.x * 2 * d;
+#pragma unroll
+    for (int i = 0; i < NI; i++) {
+        const int c = (i * TPR + t) * VE;
+        if (c < d) {
+#pragma unroll
+            for (int e = 0; e < VE; e++) {
+                const int j = i * VE + e;
+                pw[c + e] = j & 1 ? aw[j / 2].y : aw[j / 2].x;
+                pw[d + c + e] = j & 1 ? ab[j / 2].y : ab[j / 2].x;
             }
         }
     }
@@ -346,10 +531,10 @@ void launch_fwd(int64_t rows, int d, const T *x, int64_t ldx, const void *w, con
 #undef LN_GO
 }
 
-// Blocks of the backward kernel for a row held by tpr threads.
+// Blocks of the backward kernel (at most) for a row held by tpr threads.
 int64_t bwd_blocks(int64_t rows, int tpr, int num_sms) {
     const int64_t groups = tpr == 32 ? (rows + 3) / 4 : rows;
-    const int64_t per_sm = tpr <= 128 ? 8 : 1024 / tpr * 1;
+    const int64_t per_sm = tpr == 32 ? 8 : tpr <= 128 ? 12 : tpr == 256 ? 6 : tpr == 512 ? 3 : 1;
     return std::max<int64_t>(1, std::min<int64_t>(groups, (int64_t)num_sms * std::max<int64_t>(1, per_sm)));
 }
 
@@ -358,11 +543,36 @@ int bwd_tpr(int64_t d) { return d <= 256 ? 32 : d <= 1024 ? 128 : d <= 2048 ? 25
 constexpr int64_t kColParts = 64;
 
 template <typename T, int VE>
-void launch_bwd(int64_t rows, int d, const T *dy, int64_t lddy, const T *x, int64_t ldx, const float *mean,
-                const float *rstd, const void *w, int wf32, T *dx, int64_t lddx, float *parts, int64_t blocks,
-                cudaStream_t st) {
+cudaError_t launch_bwd(int64_t rows, int d, const T *dy, int64_t lddy, const T *x, int64_t ldx, const float *mean,
+                const float *rstd, const void *w, int wf32, T *dx, int64_t lddx, float *parts, int64_t *blocks,
+                int num_sms, unsigned *status, cudaStream_t st) {
+    // rows of less than half a kilobyte a warp and tensors that do not start on 16 bytes: without the ring
+    if (d > 256 && aligned16(x) && aligned16(dy)) {
+        const size_t smem = (size_t)2 * kRing * ring_row<T>(d) * sizeof(T) + (w ? (size_t)d * (wf32 ? 4 : sizeof(T)) : 0);
+#define LN_RING(TPR, E)                                                                                             \
+    do {                                                                                                           \
+        constexpr int kMost = 2 * kRing * ring_row<T>((TPR) * (E)) * (int)sizeof(T) + (TPR) * (E) * 4;               \
+        static const cudaError_t attr = cudaFuncSetAttribute(                                                      \
+            k_layernorm_bwd_ring<T, VE, TPR, (E) / VE>, cudaFuncAttributeMaxDynamicSharedMemorySize, kMost);        \
+        if (attr != cudaSuccess) return attr;                                                                      \
+        const int64_t per_sm = std::max<int64_t>(1, std::min<int64_t>(ring_threads<E>() / (TPR), 227 * 1024 / (smem + 1536))); \
+        *blocks = std::min({*blocks, rows, per_sm * num_sms});                                                     \
+        k_layernorm_bwd_ring<T, VE, TPR, (E) / VE><<<(unsigned)*blocks, TPR, smem, st>>>(                           \
+            dy, lddy, x, ldx, mean, rstd, w, wf32, rows, d, dx, lddx, parts, status);                              \
+        return cudaGetLastError();                                                                                 \
+    } while (0)
+        // values a thread: 16 of them share the cost of a row's reduction best, but
+        // read one by one they leave too few threads to hide their loads (6614 rows
+        // of 2157 float32: 63 us with 16, 50 us with 8)
+        constexpr int E = VE > 1 ? 16 : 8, F = VE > 1 ? 1 : 2;
+        if (d <= 1024) LN_RING(64 * F, E);
+        if (d <= 2048) LN_RING(128 * F, E);
+        if (d <= 4096) LN_RING(256 * F, E);
+        if ((size_t)2 * kRing * ring_row<T>(8192) * sizeof(T) + 8192 * 4 <= 220 * 1024) LN_RING(512 * F, E);
+#undef LN_RING
+    }
 #define LN_GO(TPR, E)                                                                                              \
-    k_layernorm_bwd<T, VE, TPR, (E) / VE><<<(unsigned)blocks, (TPR) < 128 ? 128 : (TPR), 0, st>>>(                 \
+    k_layernorm_bwd<T, VE, TPR, (E) / VE><<<(unsigned)*blocks, (TPR) < 128 ? 128 : (TPR), 0, st>>>(                 \
         dy, lddy, x, ldx, mean, rstd, w, wf32, rows, d, dx, lddx, parts)
     if (d <= 256) LN_GO(32, 8);
     else if (d <= 1024) LN_GO(128, 8);
@@ -370,6 +580,7 @@ void launch_bwd(int64_t rows, int d, const T *dy, int64_t lddy, const T *x, int6
     else if (d <= 4096) LN_GO(512, 8);
     else LN_GO(1024, 8);
 #undef LN_GO
+    return cudaGetLastError();
 }
 
 template <typename T>
@@ -392,7 +603,7 @@ cudaError_t fwd(int64_t rows, int64_t d, const void *x, int64_t ldx, const void 
 template <typename T>
 cudaError_t bwd(int64_t rows, int64_t d, const void *dy, int64_t lddy, const void *x, int64_t ldx, const float *mean,
                 const float *rstd, const void *w, int wf32, void *dx, int64_t lddx, void *dw, void *db, float *parts,
-                int num_sms, cudaStream_t st, int64_t *launches) {
+                int num_sms, unsigned *status, cudaStream_t st, int64_t *launches) {
     constexpr int VE = 16 / (int)sizeof(T);
     const T *pd = (const T *)dy, *px = (const T *)x;
     T *po = (T *)dx;
@@ -409,14 +620,14 @@ cudaError_t bwd(int64_t rows, int64_t d, const void *dy, int64_t lddy, const voi
             ++*launches;
         }
     } else if (rows > 0) {
-        const int64_t blocks = bwd_blocks(rows, bwd_tpr(d), num_sms);
+        int64_t blocks = bwd_blocks(rows, bwd_tpr(d), num_sms);
         const bool vec = d % VE == 0 && ldx % VE == 0 && lddy % VE == 0 && lddx % VE == 0 && aligned16(x) &&
                          aligned16(dy) && aligned16(dx) && (wf32 || !w || aligned16(w));
         float *p = sums ? parts : nullptr;
-        if (vec)
-            launch_bwd<T, VE>(rows, (int)d, pd, lddy, px, ldx, mean, rstd, w, wf32, po, lddx, p, blocks, st);
-        else
-            launch_bwd<T, 1>(rows, (int)d, pd, lddy, px, ldx, mean, rstd, w, wf32, po, lddx, p, blocks, st);
+        const cudaError_t e =
+            vec ? launch_bwd<T, VE>(rows, (int)d, pd, lddy, px, ldx, mean, rstd, w, wf32, po, lddx, p, &blocks, num_sms, status, st)
+                : launch_bwd<T, 1>(rows, (int)d, pd, lddy, px, ldx, mean, rstd, w, wf32, po, lddx, p, &blocks, num_sms, status, st);
+        if (e != cudaSuccess) return e;
         ++*launches;
         nparts = blocks * (bwd_tpr(d) == 32 ? 4 : 1);
     }
@@ -448,10 +659,13 @@ int64_t zs_layernorm_bwd_parts(int, int64_t rows, int64_t d, int num_sms) {
 cudaError_t zs_launch_layernorm_bwd(int type, int wf32, int64_t rows, int64_t d, const void *dy, int64_t lddy,
                                     const void *x, int64_t ldx, const float *mean, const float *rstd, const void *w,
                                     void *dx, int64_t lddx, void *dw, void *db, float *parts, int num_sms,
-                                    cudaStream_t st, int64_t *launches) {
+                                    unsigned *status, cudaStream_t st, int64_t *launches) {
     if (type == ZSOLVE_F32)
-        return bwd<float>(rows, d, dy, lddy, x, ldx, mean, rstd, w, wf32, dx, lddx, dw, db, parts, num_sms, st, launches);
+        return bwd<float>(rows, d, dy, lddy, x, ldx, mean, rstd, w, wf32, dx, lddx, dw, db, parts, num_sms, status, st,
+                   launches);
     if (type == ZSOLVE_BF16)
-        return bwd<bf16>(rows, d, dy, lddy, x, ldx, mean, rstd, w, wf32, dx, lddx, dw, db, parts, num_sms, st, launches);
-    return bwd<f16>(rows, d, dy, lddy, x, ldx, mean, rstd, w, wf32, dx, lddx, dw, db, parts, num_sms, st, launches);
+        return bwd<bf16>(rows, d, dy, lddy, x, ldx, mean, rstd, w, wf32, dx, lddx, dw, db, parts, num_sms, status, st,
+                   launches);
+    return bwd<f16>(rows, d, dy, lddy, x, ldx, mean, rstd, w, wf32, dx, lddx, dw, db, parts, num_sms, status, st,
+                   launches);
 }

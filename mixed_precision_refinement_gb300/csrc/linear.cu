@@ -484,6 +484,7 @@ k_linear_dz(const T *__restrict__ dy, int64_t lddy, const T *__restrict__ z, int
     const int nc = (int)min((int64_t)8, (int64_t)n - c);
     float sum[8] = {};
     if (nc > 0) {
+#pragma unroll 2
         for (int64_t row = (int64_t)blockIdx.y * 8 + ty; row < m; row += (int64_t)gridDim.y * 8) {
             float v[8], f[8];
             load8<T>(dy, row * lddy + c, nc, vec, v);

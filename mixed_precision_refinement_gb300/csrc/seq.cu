@@ -300,7 +300,7 @@ int zsolve_layernorm_bwd(zsolve_seq *s, int type, int wtype, int64_t rows, int64
         if (st != ZSOLVE_OK) return st;
     }
     SEQ_CU(zs_launch_layernorm_bwd(type, wtype == ZSOLVE_F32, rows, d, dy, lddy, x, ldx, mean, rstd, w, dx, lddx, dw,
-                                   db, parts, s->num_sms, s->st, &s->launches));
+                                   db, parts, s->num_sms, s->d_status, s->st, &s->launches));
     return ZSOLVE_OK;
 }
 

@@ -17,21 +17,23 @@ ZSOLVE_F16 = 2
 ZSOLVE_ACTS = {"none": 0, "relu": 1, "silu": 2, "gelu": 3, "gelu_tanh": 4}
 
 
-def _types():
-    import torch
-    return {torch.float32: ZSOLVE_F32, torch.bfloat16: ZSOLVE_BF16, torch.float16: ZSOLVE_F16}
+torch = None  # imported with the first handle: the rest of the package loads without it
+_TYPES = {}
 
 
-_TYPES = None
+def _use_torch():
+    global torch
+    if torch is None:
+        import torch as module
+        torch = module
+        _TYPES.update({torch.float32: ZSOLVE_F32, torch.bfloat16: ZSOLVE_BF16, torch.float16: ZSOLVE_F16})
 
 
 def _type(t, name) -> int:
-    global _TYPES
-    if _TYPES is None:
-        _TYPES = _types()
-    if t.dtype not in _TYPES:
+    code = _TYPES.get(t.dtype)
+    if code is None:
         raise TypeError(f"{name}: expected float32, bfloat16 or float16, got {t.dtype}")
-    return _TYPES[t.dtype]
+    return code
 
 
 def _cuda(t, name):
@@ -41,31 +43,44 @@ def _cuda(t, name):
 
 def _rows(t, name, dtype=None, shape=None):
     """(pointer, rows, d, row stride) of a matrix: a tensor (..., d) whose rows lie at one distance."""
-    _cuda(t, name)
+    if not t.is_cuda:
+        raise ValueError(f"{name}: expected a CUDA tensor")
     if dtype is not None and t.dtype != dtype:
         raise TypeError(f"{name}: expected {dtype}, got {t.dtype}")
-    if t.dim() != 2:
-        if t.dim() == 0:
+    size = t.shape
+    if len(size) != 2:
+        if not size:
             raise ValueError(f"{name}: expected rows of values")
-        t = t.view(-1, t.shape[-1]) if t.numel() else t.reshape(-1, t.shape[-1])
-    m, d = t.shape
-    if shape is not None and (m, d) != shape:
+        t = t.view(-1, size[-1]) if t.numel() else t.reshape(-1, size[-1])
+        size = t.shape
+    m, d = size
+    if shape is not None and shape != (m, d):
         raise ValueError(f"{name}: expected {shape[0]} rows of {shape[1]}, got {m} of {d}")
-    if d > 1 and t.stride(1) != 1:
+    ld, one = t.stride()
+    if one != 1 and d > 1:
         raise ValueError(f"{name}: the values of a row must be contiguous")
-    return t.data_ptr(), m, d, t.stride(0) if m > 1 else max(d, 1)
+    return t.data_ptr(), m, d, ld if m > 1 else max(d, 1)
 
 
 def _vector(t, name, n, dtype):
     """Pointer of a contiguous vector of n values, or 0 for None."""
     if t is None:
         return 0
-    _cuda(t, name)
+    if not t.is_cuda:
+        raise ValueError(f"{name}: expected a CUDA tensor")
     if t.dtype != dtype:
         raise TypeError(f"{name}: expected {dtype}, got {t.dtype}")
     if t.numel() != n or not t.is_contiguous():
         raise ValueError(f"{name}: expected {n} contiguous values, got {tuple(t.shape)}")
     return t.data_ptr()
+
+
+def _current_stream() -> int:
+    """The handle of torch's current stream on the current device."""
+    try:  # without making a Stream object, where torch offers that
+        return torch._C._cuda_getCurrentRawStream(torch._C._cuda_getDevice())
+    except AttributeError:
+        return torch.cuda.current_stream().cuda_stream
 
 
 def _check_seq(seq, status):
@@ -78,6 +93,7 @@ def _check_seq(seq, status):
 
 
 def zsolve_seq_create() -> ctypes.c_void_p:
+    _use_torch()
     seq = ctypes.c_void_p()
     _check_seq(None, _lib.zsolve_seq_create(ctypes.byref(seq)))
     return seq
@@ -85,7 +101,6 @@ def zsolve_seq_create() -> ctypes.c_void_p:
 
 def zsolve_seq_set_stream(seq, stream=None) -> None:
     """stream: a torch.cuda.Stream, a raw handle, or None for torch's current stream."""
-    import torch
     if stream is None:
         stream = torch.cuda.current_stream()
     handle = stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
@@ -118,7 +133,6 @@ def zsolve_seq_destroy(seq) -> None:
 
 def _norm_weights(x, w, b):
     """Type code of w and b (the type of x, or float32), and their torch type."""
-    import torch
     given = w if w is not None else b
     dt = x.dtype if given is None else given.dtype
     if dt not in (x.dtype, torch.float32):
@@ -128,7 +142,6 @@ def _norm_weights(x, w, b):
 
 def zsolve_layernorm(seq, x, w, b, eps, y, mean=None, rstd=None) -> None:
     """y <- layer norm of the rows of x (..., d); w, b: (d,) or None; mean, rstd: float32, one value a row, or None."""
-    import torch
     xp, m, d, ldx = _rows(x, "x")
     yp, _, _, ldy = _rows(y, "y", x.dtype, (m, d))
     wt = _norm_weights(x, w, b)
@@ -140,7 +153,6 @@ def zsolve_layernorm(seq, x, w, b, eps, y, mean=None, rstd=None) -> None:
 
 def zsolve_layernorm_bwd(seq, dy, x, mean, rstd, w, dx, dw=None, db=None) -> None:
     """dx (the shape of x), dw and db (the type of w, or of x without one; None: not formed) from dy."""
-    import torch
     xp, m, d, ldx = _rows(x, "x")
     dyp, _, _, lddy = _rows(dy, "dy", x.dtype, (m, d))
     dxp, _, _, lddx = _rows(dx, "dx", x.dtype, (m, d))
@@ -215,7 +227,6 @@ def _tokens(t, name, dtype=None, shape=None):
 
 
 def _delta_args(q, k, v, g, beta, s0, offsets, scale):
-    import torch
     qp, n, hk, dk, ldq = _tokens(q, "q")
     kp, _, _, _, ldk = _tokens(k, "k", q.dtype, (n, hk, dk))
     vp, _, hv, dv, ldv = _tokens(v, "v", q.dtype)
@@ -258,7 +269,6 @@ def zsolve_delta_step(seq, q, k, v, g, beta, o, s=None, s0=None, offsets=None, s
 def zsolve_delta_bwd(seq, dout, q, k, v, g, beta, dq, dk, dv, dg, dbeta, ds0=None, s0=None, ds=None, offsets=None,
                      scale=None) -> None:
     """dq .. dbeta and ds0 (shapes of q .. beta and s0, contiguous) from dout (as o) and ds (as s, or None)."""
-    import torch
     a = _delta_args(q, k, v, g, beta, s0, offsets, scale)
     op, _, _, _, lddo = _tokens(dout, "dout", q.dtype, (a.tokens, a.hv, a.dv))
     nk, nv, n = a.tokens * a.hk * a.dk, a.tokens * a.hv * a.dv, a.tokens * a.hv
@@ -269,7 +279,6 @@ def zsolve_delta_bwd(seq, dout, q, k, v, g, beta, dq, dk, dv, dg, dbeta, ds0=Non
 
 
 def _state(s, a):
-    import torch
     return _vector(s, "s", a.nseq * a.hv * a.dk * a.dv, torch.float32)
 
 
@@ -284,37 +293,33 @@ class Seq:
     """
 
     def __init__(self):
-        self._stream = None
         self.seq = zsolve_seq_create()
 
     def _on_stream(self):
-        import torch
-        st = torch.cuda.current_stream().cuda_stream
-        if st != self._stream:
-            _check_seq(self.seq, _lib.zsolve_seq_set_stream(self.seq, st))
-            self._stream = st
+        _check_seq(self.seq, _lib.zsolve_seq_set_stream(self.seq, _current_stream()))
 
     def layernorm(self, x, w=None, b=None, eps=1e-5):
         """Returns (y, mean, rstd); mean and rstd are float32, for layernorm_bwd."""
-        import torch
         self._on_stream()
-        y = torch.empty(x.shape, dtype=x.dtype, device=x.device)
-        mean, rstd = torch.empty((2,) + x.shape[:-1], dtype=torch.float32, device=x.device).unbind(0)
+        y = torch.empty_like(x)
+        rows = x.shape[:-1]
+        mean = torch.empty(rows, dtype=torch.float32, device=x.device)
+        rstd = torch.empty(rows, dtype=torch.float32, device=x.device)
         zsolve_layernorm(self.seq, x, w, b, eps, y, mean, rstd)
         return y, mean, rstd
 
     def layernorm_bwd(self, dy, x, mean, rstd, w=None):
         """Returns (dx, dw, db); dw and db have the type of w (of x without one)."""
-        import torch
         self._on_stream()
-        dx = torch.empty(x.shape, dtype=x.dtype, device=x.device)
-        dw, db = torch.empty((2, x.shape[-1]), dtype=x.dtype if w is None else w.dtype, device=x.device).unbind(0)
+        dx = torch.empty_like(x)
+        dt = x.dtype if w is None else w.dtype
+        dw = torch.empty(x.shape[-1], dtype=dt, device=x.device)
+        db = torch.empty(x.shape[-1], dtype=dt, device=x.device)
         zsolve_layernorm_bwd(self.seq, dy, x, mean, rstd, w, dx, dw, db)
         return dx, dw, db
 
     def linear(self, x, w, b=None, act="none", r=None, keep=False):
         """y = act(x w^T + b) + r; with keep=True (y, z), z for linear_bwd."""
-        import torch
         self._on_stream()
         shape = x.shape[:-1] + w.shape[:1]
         y = torch.empty(shape, dtype=x.dtype, device=x.device)
@@ -324,10 +329,9 @@ class Seq:
 
     def linear_bwd(self, dy, x, w, z=None, act="none"):
         """Returns (dx, dw, db); z as linear(keep=True) returned it (not needed without an activation)."""
-        import torch
         self._on_stream()
-        dx = torch.empty(x.shape, dtype=x.dtype, device=x.device)
-        dw = torch.empty(w.shape, dtype=x.dtype, device=x.device)
+        dx = torch.empty_like(x)
+        dw = torch.empty_like(w)
         db = torch.empty(w.shape[:1], dtype=x.dtype, device=x.device)
         zsolve_linear_bwd(self.seq, dy, x, w, act, z, dx, dw, db)
         return dx, dw, db
@@ -337,7 +341,6 @@ class Seq:
 
         Shapes as for zsolve_delta; s is (sequences, hv, dk, dv) float32.
         """
-        import torch
         self._on_stream()
         o = torch.empty(v.shape, dtype=v.dtype, device=v.device)
         nseq = offsets.numel() - 1 if offsets is not None else q.shape[0] if q.dim() == 4 else 1
@@ -347,7 +350,6 @@ class Seq:
 
     def delta_bwd(self, dout, q, k, v, g, beta, s0=None, ds=None, offsets=None, scale=None):
         """Returns (dq, dk, dv, dg, dbeta, ds0) from the gradients of o and, unless None, of s."""
-        import torch
         self._on_stream()
         dq, dk, dv = (torch.empty(t.shape, dtype=t.dtype, device=t.device) for t in (q, k, v))
         dg, dbeta = torch.empty_like(g), torch.empty_like(beta)
@@ -359,7 +361,6 @@ class Seq:
     def delta_step(self, q, k, v, g, beta, s, s_out=None, scale=None):
         """Returns (o, s): the next token of every sequence, q (sequences, hk, dk) and so on (or the next few,
         with two leading dimensions).  The states are updated in place, or written to s_out."""
-        import torch
         self._on_stream()
         o = torch.empty(v.shape, dtype=v.dtype, device=v.device)
         s_out = s if s_out is None else s_out

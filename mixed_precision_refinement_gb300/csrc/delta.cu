@@ -301,21 +301,27 @@ k_delta_pack(const T *__restrict__ src, int64_t ld, int64_t tokens, int heads, i
 // results through shared memory: the partial sums of S^T K^T (over the warps'
 // key columns), X^T and U^T, the latter two already split by the warp that
 // wrote them; token tiles of 8 are dealt so that the triangular products are
-// equal shares (tile_of).  One more warp keeps two stages of chunk operands
-// filled.  The groups do not wait for each other, so one's
-// exchanges run beside the other's products.
+// equal shares.  What the next chunk does not wait for is done by helper warps
+// beside the groups: they keep two stages of chunk operands filled, and form
+// the outputs from S and U as the groups leave them in shared memory (with the
+// outputs in the groups themselves a chunk took 4.0 us).  The groups do not wait
+// for each other, so one's exchanges run beside the other's products.
 template <typename T, int DK>
 struct ChainCfg {
     static constexpr int WK = DK / 32;
     static constexpr int NV = DK == 32 ? 4 : 2;
     static constexpr int NC = 32 * WK * NV;  // threads of the groups
-    static constexpr int NT = NC + 32;
     static constexpr int NTILE = 8 / WK;
     static constexpr int COLS = 16 * NV;
     static constexpr int LD = tile_ld<T>(DK), LDV = tile_ld<T>(COLS);
     // two stages of the chunk's operands where they fit
     static constexpr int STAGES = sizeof(T) == 2 || DK == 64 ? 2 : 1;
+    // registers of a thread's S that the outputs need, in fours: two bfloat16
+    // parts, or the tf32 hi part, and for float32 outputs lo as well
+    static constexpr int NS = sizeof(T) == 2 ? 4 : 8;
 };
+template <bool OUT>
+constexpr int helpers() { return OUT ? 4 : 1; }
 
 template <typename T, int DK>
 struct ChainStage {
@@ -331,10 +337,13 @@ struct ChainSmem {
     using C = ChainCfg<T, DK>;
     ChainStage<T, DK> st[C::STAGES];
     float part[C::NV][C::WK][16 * kLdT];
-    float4 x[C::NV][16 * kLdPair];   // X^T, then the chunk's outputs
-    float4 u[C::NV][16 * kLdPair];   // (e U)^T
-    float2 un[C::NV][16 * kLdPair];  // U^T, for P U
+    float4 x[C::NV][16 * kLdPair];            // X^T
+    float4 u[C::NV][16 * kLdPair];            // (e U)^T
+    float2 un[C::NV][16 * kLdPair];           // U^T, for P U
+    uint4 s[C::NV][C::WK][C::NS][32];         // S^T, for Q S, as the lanes hold it
+    T out[helpers<true>()][2][8 * 16];        // two tiles of outputs a helper
     uint64_t full[C::STAGES], empty[C::STAGES];
+    uint64_t sfull[C::NV], sempty[C::NV], ufull[C::NV], uempty[C::NV];
     int abort_word;
 };
 
@@ -344,13 +353,58 @@ __device__ __forceinline__ float2 out_pair(float a, float b) {
     return sizeof(T) == 2 ? make_float2(__uint_as_float(tf32(a)), __uint_as_float(tf32(b))) : make_float2(a, b);
 }
 
+// The parts of S^T that the outputs need, NS words of four registers.
+template <typename T, int NS>
+__device__ __forceinline__ void put_parts(uint4 (*dst)[32], const StateSplit<T> &s, int lane) {
+#pragma unroll
+    for (int i = 0; i < NS; i++) {
+        const uint32_t *r;
+        if constexpr (std::is_same<T, bf16>::value)
+            r = s.a[i >> 1].p[i & 1];
+        else if constexpr (sizeof(T) == 2)
+            r = s.a[i].hi;
+        else
+            r = i & 1 ? s.a[i >> 1].lo : s.a[i >> 1].hi;
+        dst[i][lane] = make_uint4(r[0], r[1], r[2], r[3]);
+    }
+}
+
+// acc += S^T Q^T at token tile n over one warp's 32 key columns
+template <typename T, int LD, int NS>
+__device__ __forceinline__ void parts_times_rows(const uint4 (*src)[32], const T *q, int n, int d0, int lane, Acc &acc) {
+    if constexpr (std::is_same<T, bf16>::value) {
+        uint32_t b[4];
+        ldmatrix4(b, q + (n * 8 + (lane & 7)) * LD + d0 + 8 * (lane >> 3));
+#pragma unroll
+        for (int i = NS - 1; i >= 0; i--) {  // part i & 1 of k step i >> 1
+            const uint4 u = src[i][lane];
+            const uint32_t a[4] = {u.x, u.y, u.z, u.w};
+            mma16(i & 1 ? acc.l : acc.c, a, b[2 * (i >> 1)], b[2 * (i >> 1) + 1]);
+        }
+    } else {
+        float2 b[4];
+        frag4<T, LD, false>(q, n * 8, d0, b);
+#pragma unroll
+        for (int j = 0; j < 4; j++) {
+            SplitA a;
+            const uint4 h = src[sizeof(T) == 2 ? j : 2 * j][lane];
+            a.hi[0] = h.x, a.hi[1] = h.y, a.hi[2] = h.z, a.hi[3] = h.w;
+            if (sizeof(T) == 4) {
+                const uint4 l = src[(2 * j + 1) % NS][lane];
+                a.lo[0] = l.x, a.lo[1] = l.y, a.lo[2] = l.z, a.lo[3] = l.w;
+            }
+            mma_split<false, sizeof(T) == 2, sizeof(T) == 2>(acc, a, b[j]);
+        }
+    }
+}
+
 template <typename T, int DK, bool OUT>
-__global__ void __launch_bounds__(ChainCfg<T, DK>::NT, 1)
+__global__ void __launch_bounds__(ChainCfg<T, DK>::NC + 32 * helpers<OUT>(), 1)
 k_delta_chain(const DeltaGeom geo, const DeltaTerms terms, const float *__restrict__ s0, T *__restrict__ o,
               int64_t ldo, float *__restrict__ sn, float *__restrict__ states, float *__restrict__ us, int veco,
               unsigned *__restrict__ status) {
     using C = ChainCfg<T, DK>;
-    constexpr int WK = C::WK, LD = C::LD, LDV = C::LDV, NTILE = C::NTILE;
+    constexpr int WK = C::WK, NV = C::NV, LD = C::LD, LDV = C::LDV, NTILE = C::NTILE, NH = helpers<OUT>();
     constexpr bool EXACT = sizeof(T) == 2;
     extern __shared__ __align__(16) uint8_t smem_raw[];
     ChainSmem<T, DK> &sm = *reinterpret_cast<ChainSmem<T, DK> *>(smem_raw);
@@ -358,41 +412,121 @@ k_delta_chain(const DeltaGeom geo, const DeltaTerms terms, const float *__restri
     const int si = blockIdx.x / geo.hv, hv = blockIdx.x - si * geo.hv, hk = hv / (geo.hv / geo.hk);
     const int vb = (int)blockIdx.y * C::COLS;
     const int c0 = geo.first[si], c1 = geo.first[si + 1];
-    const int vcols = min(C::COLS, geo.dvp - vb);
 
     if (tid == 0) {
         sm.abort_word = 0;
         for (int i = 0; i < C::STAGES; i++) {
-            bar_init(&sm.full[i], 33);  // the fetching warp's lanes, and the bulk copies
-            bar_init(&sm.empty[i], C::NC / 32);
+            bar_init(&sm.full[i], 32 * NH + 1);  // the helpers' lanes, and the bulk copies
+            bar_init(&sm.empty[i], C::NC / 32 + (OUT ? NH : 0));
+        }
+        for (int i = 0; i < NV; i++) {
+            bar_init(&sm.sfull[i], WK);
+            bar_init(&sm.sempty[i], NH);
+            bar_init(&sm.ufull[i], WK);
+            bar_init(&sm.uempty[i], NH);
         }
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     }
     __syncthreads();
+    auto wait = [&](uint64_t *bar, int parity) { return bar_wait(bar, parity & 1, &sm.abort_word, status); };
 
-    if (warp == C::NC / 32) {
-        // ------------------------------------------------ the chunks' operands
+    if (warp >= C::NC / 32) {
+        // ------------------------------------------------ helpers
+        const int hw = warp - C::NC / 32;
         const T *kp = (const T *)geo.k + (int64_t)hk * geo.dkp, *qp = (const T *)geo.q + (int64_t)hk * geo.dkp;
         const T *vp = (const T *)geo.v + (int64_t)hv * geo.dvp + vb;
-        int it = 0;
-        for (int c = c0; c < c1; c++, it++) {
-            const int stage = it % C::STAGES;
-            if (!bar_wait(&sm.empty[stage], ((it / C::STAGES) & 1) ^ 1, &sm.abort_word, status)) break;
-            const int2 ch = geo.chunk[c];
+        const int vcols = min(C::COLS, geo.dvp - vb), count = c1 - c0;
+        int fetched = 0;
+        auto fetch = [&]() {
+            const int it = fetched++, stage = it % C::STAGES;
+            if (!wait(&sm.empty[stage], it / C::STAGES + 1)) return;  // an early return: nothing more is fetched
+            const int2 ch = geo.chunk[c0 + it];
             ChainStage<T, DK> &s = sm.st[stage];
-            const int64_t slot = (int64_t)c * geo.hv + hv;
+            const int64_t slot = (int64_t)(c0 + it) * geo.hv + hv;
             uint64_t *bar = &sm.full[stage];
-            warp_tile<T, DK>(s.k, kp + (int64_t)ch.x * geo.ldk, geo.ldk, ch.y, geo.dkp);
-            if (OUT) warp_tile<T, DK>(s.q, qp + (int64_t)ch.x * geo.ldq, geo.ldq, ch.y, geo.dkp);
-            warp_tile<T, C::COLS>(s.v, vp + (int64_t)ch.x * geo.ldv, geo.ldv, ch.y, vcols);
+            warp_tile<T, DK, NH>(s.k, kp + (int64_t)ch.x * geo.ldk, geo.ldk, ch.y, geo.dkp, hw);
+            if (OUT) warp_tile<T, DK, NH>(s.q, qp + (int64_t)ch.x * geo.ldq, geo.ldq, ch.y, geo.dkp, hw);
+            warp_tile<T, C::COLS, NH>(s.v, vp + (int64_t)ch.x * geo.ldv, geo.ldv, ch.y, vcols, hw);
             cp_arrive(bar);
-            if (lane == 0) {
+            if (hw == 0 && lane == 0) {
                 bar_expect(bar, (kSquare + kVec) * 4);
                 bulk_load(s.tp, terms.tp + slot * kSquare, kSquare * 4, bar);
                 bulk_load(s.vec, terms.vec + slot * kVec, kVec * 4, bar);
             }
+        };
+        if (C::STAGES > 1 && count > 0) fetch();
+        for (int it = 0; it < count && !*(volatile int *)&sm.abort_word; it++) {
+            if (fetched < count) fetch();
+            if (!OUT) continue;
+            const int stage = it % C::STAGES;
+            ChainStage<T, DK> &st = sm.st[stage];
+            const int2 ch = geo.chunk[c0 + it];
+            wait(&sm.full[stage], it / C::STAGES);
+            // S^T Q^T at this helper's two token tiles
+            Acc qs[NV][2];
+#pragma unroll
+            for (int grp = 0; grp < NV; grp++) {
+                qs[grp][0].zero(), qs[grp][1].zero();
+                wait(&sm.sfull[grp], it);
+#pragma unroll
+                for (int w = 0; w < WK; w++)
+#pragma unroll
+                    for (int i = 0; i < 2; i++)
+                        parts_times_rows<T, LD, C::NS>(sm.s[grp][w], st.q, tile_of<4>(hw, i), 32 * w, lane, qs[grp][i]);
+                __syncwarp();
+                if (lane == 0) bar_arrive(&sm.sempty[grp]);
+            }
+            // O^T = scale c (Q S)^T + U^T P^T
+#pragma unroll
+            for (int grp = 0; grp < NV; grp++) {
+                wait(&sm.ufull[grp], it);
+                float oa[2][4];
+                triangular<4, true, false, EXACT>(
+                    hw, oa,
+                    [&](int k, SplitA &a) {
+                        const float2 y = sm.un[grp][g * kLdPair + k * 4 + t], z = sm.un[grp][(g + 8) * kLdPair + k * 4 + t];
+                        if (EXACT)
+                            a.hi[0] = __float_as_uint(y.x), a.hi[1] = __float_as_uint(z.x), a.hi[2] = __float_as_uint(y.y), a.hi[3] = __float_as_uint(z.y);
+                        else
+                            a.set(y.x, y.y, z.x, z.y);
+                    },
+                    [&](int k, int n) { return frag_p_earlier(st.tp, k, n); });
+                __syncwarp();
+                if (lane == 0) bar_arrive(&sm.uempty[grp]);
+                const int v0 = vb + grp * 16;
+#pragma unroll
+                for (int i = 0; i < 2; i++) {
+                    const int n = tile_of<4>(hw, i) * 8;
+                    const float2 cv = *reinterpret_cast<const float2 *>(st.vec + n + 2 * t);
+                    const float ca = geo.scale * cv.x, cb = geo.scale * cv.y;
+                    const Acc &q = qs[grp][i];
+                    const float r[4] = {fmaf(ca, q.get(0), oa[i][0]), fmaf(cb, q.get(1), oa[i][1]),
+                                        fmaf(ca, q.get(2), oa[i][2]), fmaf(cb, q.get(3), oa[i][3])};
+#pragma unroll
+                    for (int e = 0; e < 4; e++) sm.out[hw][i][(2 * t + (e & 1)) * 16 + g + (e >> 1) * 8] = from_f32<T>(r[e]);
+                }
+                __syncwarp();
+                T *op = o + (int64_t)hv * geo.dv + v0;
+                if (veco) {  // 16 bytes a lane: rows of 16 values
+                    constexpr int PIECE = 16 / (int)sizeof(T), PPR = 16 / PIECE;
+#pragma unroll
+                    for (int j = lane; j < 2 * 8 * PPR; j += 32) {
+                        const int i = j / (8 * PPR), r = j / PPR % 8, c = j % PPR * PIECE, tok = tile_of<4>(hw, i) * 8 + r;
+                        if (tok < ch.y && v0 + c < geo.dv)
+                            *reinterpret_cast<uint4 *>(op + (int64_t)(ch.x + tok) * ldo + c) =
+                                *reinterpret_cast<const uint4 *>(&sm.out[hw][i][r * 16 + c]);
+                    }
+                } else {
+                    for (int j = lane; j < 2 * 8 * 16; j += 32) {
+                        const int i = j / 128, r = j / 16 % 8, c = j % 16, tok = tile_of<4>(hw, i) * 8 + r;
+                        if (tok < ch.y && v0 + c < geo.dv) op[(int64_t)(ch.x + tok) * ldo + c] = sm.out[hw][i][r * 16 + c];
+                    }
+                }
+                __syncwarp();
+            }
+            if (lane == 0) bar_arrive(&sm.empty[stage]);
         }
-        bar_drain(sm.full, C::STAGES, it);  // copies in flight end before the block does
+        bar_drain(sm.full, C::STAGES, fetched);  // copies in flight end before the block does
         return;
     }
 
@@ -420,49 +554,36 @@ k_delta_chain(const DeltaGeom geo, const DeltaTerms terms, const float *__restri
                 if (v < geo.dv && d < geo.dk) dst[(int64_t)d * geo.dv + v] = S[j][e];
             }
     };
-    // The outputs of a chunk, from the group's staging rows (64 tokens x 16 columns), 16 bytes a thread
-    constexpr int PIECE = 16 / (int)sizeof(T), PPR = 16 / PIECE;
-    auto put_out = [&](int2 ch) {
-        const T *stage = reinterpret_cast<const T *>(sm.x[grp]);
-        for (int i = w * 32 + lane; i < kChunk * PPR; i += WK * 32) {
-            const int tok = i / PPR, c = (i - tok * PPR) * PIECE;
-            if (tok < ch.y && v0 + c < geo.dv)
-                *reinterpret_cast<uint4 *>(o + (int64_t)(ch.x + tok) * ldo + (int64_t)hv * geo.dv + v0 + c) =
-                    *reinterpret_cast<const uint4 *>(stage + tok * 16 + c);
-        }
-    };
 
-    int2 before = make_int2(0, 0);  // the chunk whose outputs are staged
     for (int c = c0; c < c1; c++) {
         const int it = c - c0, stage = it % C::STAGES;
-        bar_wait(&sm.full[stage], (it / C::STAGES) & 1, &sm.abort_word, status);
+        StateSplit<T> a;
+        a.set(S);
+        if (OUT) {
+            wait(&sm.sempty[grp], it + 1);
+            put_parts<T, C::NS>(sm.s[grp][w], a, lane);
+            __syncwarp();
+            if (lane == 0) bar_arrive(&sm.sfull[grp]);
+        }
+        wait(&sm.full[stage], it / C::STAGES);
         ChainStage<T, DK> &st = sm.st[stage];
-        const int2 ch = geo.chunk[c];
         const int64_t slot = (int64_t)c * geo.hv + hv;
         if (states) put_state(states + slot * geo.dk * geo.dv);
         group_sync<WK>(grp);  // the group is done with the previous chunk's exchanges
-        if (OUT && veco && it > 0) put_out(before);
 
-        // partial S^T K^T and S^T Q^T over the warp's key columns
-        float po[2][4][4];
+        // partial S^T K^T over the warp's key columns
         {
-            StateSplit<T> a;
-            a.set(S);
             float *part = sm.part[grp][w];
 #pragma unroll
             for (int h = 0; h < 2; h++) {
                 float r[4][4];
-                state_times_rows<T, LD, false>(a, st.k, 4 * h, d0, r);
+                state_times_rows<T, LD>(a, st.k, 4 * h, d0, r);
 #pragma unroll
                 for (int n = 0; n < 4; n++) {
                     float *p = part + g * kLdT + (4 * h + n) * 8 + 2 * t;
                     *reinterpret_cast<float2 *>(p) = make_float2(r[n][0], r[n][1]);
                     *reinterpret_cast<float2 *>(p + 8 * kLdT) = make_float2(r[n][2], r[n][3]);
                 }
-            }
-            if (OUT) {
-#pragma unroll
-                for (int h = 0; h < 2; h++) state_times_rows<T, LD, true>(a, st.q, 4 * h, d0, po[h]);
             }
         }
         group_sync<WK>(grp);
@@ -486,21 +607,13 @@ k_delta_chain(const DeltaGeom geo, const DeltaTerms terms, const float *__restri
             x[8 * kLdPair] = split_pair(bv.x * (vb8.x - cv.x * hi.x), bv.y * (vb8.y - cv.y * hi.y));
         }
         group_sync<WK>(grp);
-        if (OUT) {
-            float *part = sm.part[grp][w];
-#pragma unroll
-            for (int n = 0; n < 8; n++) {
-                const float(&r)[4] = po[n >> 2][n & 3];
-                *reinterpret_cast<float2 *>(part + g * kLdT + n * 8 + 2 * t) = make_float2(r[0], r[1]);
-                *reinterpret_cast<float2 *>(part + (g + 8) * kLdT + n * 8 + 2 * t) = make_float2(r[2], r[3]);
-            }
-        }
         // U^T = X^T T^T at the warp's token tiles
         {
             float u[NTILE][4];
             triangular<WK, true, false, false>(
-                w, u, [&](int k, SplitA &a) { a.set(sm.x[grp][g * kLdPair + k * 4 + t], sm.x[grp][(g + 8) * kLdPair + k * 4 + t]); },
+                w, u, [&](int k, SplitA &f) { f.set(sm.x[grp][g * kLdPair + k * 4 + t], sm.x[grp][(g + 8) * kLdPair + k * 4 + t]); },
                 [&](int k, int n) { return frag_t_earlier(st.tp, k, n); });
+            if (OUT) wait(&sm.uempty[grp], it + 1);
 #pragma unroll
             for (int i = 0; i < NTILE; i++) {
                 const int n = tile_of<WK>(w, i) * 8 + 2 * t, at = g * kLdPair + n / 2;
@@ -520,6 +633,10 @@ k_delta_chain(const DeltaGeom geo, const DeltaTerms terms, const float *__restri
                     }
                 }
             }
+            if (OUT) {
+                __syncwarp();
+                if (lane == 0) bar_arrive(&sm.ufull[grp]);
+            }
         }
         group_sync<WK>(grp);
         // S'^T = c_64 S^T + (e U)^T K: the chunk's sum starts from zero, so that
@@ -533,54 +650,8 @@ k_delta_chain(const DeltaGeom geo, const DeltaTerms terms, const float *__restri
 #pragma unroll
                 for (int e = 0; e < 4; e++) S[j][e] = fmaf(cend, S[j][e], r[j][e]);
         }
-        // O^T = scale c (Q S)^T + U^T P^T at the warp's token tiles
-        if (OUT) {
-            float oa[NTILE][4];
-            triangular<WK, true, false, EXACT>(
-                w, oa,
-                [&](int k, SplitA &a) {
-                    const float2 y = sm.un[grp][g * kLdPair + k * 4 + t], z = sm.un[grp][(g + 8) * kLdPair + k * 4 + t];
-                    if (EXACT)
-                        a.hi[0] = __float_as_uint(y.x), a.hi[1] = __float_as_uint(z.x), a.hi[2] = __float_as_uint(y.y), a.hi[3] = __float_as_uint(z.y);
-                    else
-                        a.set(y.x, y.y, z.x, z.y);
-                },
-                [&](int k, int n) { return frag_p_earlier(st.tp, k, n); });
-            T *stg = reinterpret_cast<T *>(sm.x[grp]);
-#pragma unroll
-            for (int i = 0; i < NTILE; i++) {
-                const int n = tile_of<WK>(w, i) * 8 + 2 * t;
-                float2 lo = make_float2(0.f, 0.f), hi = lo;
-#pragma unroll
-                for (int p = 0; p < WK; p++) {
-                    const float2 y = *reinterpret_cast<const float2 *>(sm.part[grp][p] + g * kLdT + n);
-                    const float2 z = *reinterpret_cast<const float2 *>(sm.part[grp][p] + (g + 8) * kLdT + n);
-                    lo.x += y.x, lo.y += y.y, hi.x += z.x, hi.y += z.y;
-                }
-                const float2 cv = *reinterpret_cast<const float2 *>(st.vec + n);
-                const float ca = geo.scale * cv.x, cb = geo.scale * cv.y;
-                const float r[4] = {fmaf(ca, lo.x, oa[i][0]), fmaf(cb, lo.y, oa[i][1]), fmaf(ca, hi.x, oa[i][2]),
-                                    fmaf(cb, hi.y, oa[i][3])};
-                if (veco) {
-#pragma unroll
-                    for (int e = 0; e < 4; e++) stg[(n + (e & 1)) * 16 + g + (e >> 1) * 8] = from_f32<T>(r[e]);
-                } else {
-#pragma unroll
-                    for (int e = 0; e < 4; e++) {
-                        const int v = v0 + g + (e >> 1) * 8, tok = n + (e & 1);
-                        if (v < geo.dv && tok < ch.y)
-                            o[(int64_t)(ch.x + tok) * ldo + (int64_t)hv * geo.dv + v] = from_f32<T>(r[e]);
-                    }
-                }
-            }
-            before = ch;
-        }
         __syncwarp();
         if (lane == 0) bar_arrive(&sm.empty[stage]);
-    }
-    if (OUT && veco && c0 < c1) {
-        group_sync<WK>(grp);
-        put_out(before);
     }
     if (sn) put_state(sn + state_at);
 }
@@ -606,13 +677,13 @@ cudaError_t chain_dk(const DeltaGeom &g, const DeltaTerms &t, const float *s0, v
         static const cudaError_t attr = cudaFuncSetAttribute(
             k_delta_chain<T, DK, true>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)sizeof(ChainSmem<T, DK>));
         if (attr != cudaSuccess) return attr;
-        k_delta_chain<T, DK, true><<<grid, C::NT, smem, st>>>(g, t, s0, (T *)o, ldo, sn, states, us,
+        k_delta_chain<T, DK, true><<<grid, C::NC + 32 * helpers<true>(), smem, st>>>(g, t, s0, (T *)o, ldo, sn, states, us,
                                                                     mult16(o, ldo, g.dv, sizeof(T)), status);
     } else {
         static const cudaError_t attr = cudaFuncSetAttribute(
             k_delta_chain<T, DK, false>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)sizeof(ChainSmem<T, DK>));
         if (attr != cudaSuccess) return attr;
-        k_delta_chain<T, DK, false><<<grid, C::NT, smem, st>>>(g, t, s0, nullptr, 0, sn, states, us, 0, status);
+        k_delta_chain<T, DK, false><<<grid, C::NC + 32 * helpers<false>(), smem, st>>>(g, t, s0, nullptr, 0, sn, states, us, 0, status);
     }
     return cudaGetLastError();
 }

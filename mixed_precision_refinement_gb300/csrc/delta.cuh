@@ -294,10 +294,9 @@ struct StateSplit<bf16> {
 };
 
 // r[n] = S^T X^T at token tiles n0 .. n0 + 3 over key columns d0 .. d0 + 31 of
-// the tile X; HALF: for results of 16 bits.
-template <typename T, int LD, bool HALF>
+// the tile X.
+template <typename T, int LD>
 __device__ __forceinline__ void state_times_rows(const StateSplit<T> &s, const T *x, int n0, int d0, float (&r)[4][4]) {
-    constexpr bool EXACT = sizeof(T) == 2;
     if constexpr (std::is_same<T, bf16>::value) {
         const int lane = threadIdx.x & 31;
         uint32_t b[4][4];
@@ -305,12 +304,12 @@ __device__ __forceinline__ void state_times_rows(const StateSplit<T> &s, const T
         for (int n = 0; n < 4; n++) ldmatrix4(b[n], x + ((n0 + n) * 8 + (lane & 7)) * LD + d0 + 8 * (lane >> 3));
         // the small parts first
 #pragma unroll
-        for (int i = HALF ? 1 : 2; i >= 0; i--)
+        for (int i = 2; i >= 0; i--)
 #pragma unroll
             for (int k = 0; k < 2; k++)
 #pragma unroll
                 for (int n = 0; n < 4; n++) {
-                    if (i == (HALF ? 1 : 2) && k == 0)
+                    if (i == 2 && k == 0)
                         mma16_first(r[n], s.a[k].p[i], b[n][2 * k], b[n][2 * k + 1]);
                     else
                         mma16(r[n], s.a[k].p[i], b[n][2 * k], b[n][2 * k + 1]);
@@ -326,11 +325,11 @@ __device__ __forceinline__ void state_times_rows(const StateSplit<T> &s, const T
 #pragma unroll
         for (int j = 0; j < 4; j++)
 #pragma unroll
-            for (int n = 0; n < 4; n++) mma_split<false, EXACT, EXACT && HALF>(acc[n], s.a[j], b[n][j]);
+            for (int n = 0; n < 4; n++) mma_split<false, sizeof(T) == 2>(acc[n], s.a[j], b[n][j]);
 #pragma unroll
         for (int n = 0; n < 4; n++)
 #pragma unroll
-            for (int e = 0; e < 4; e++) r[n][e] = EXACT && HALF ? acc[n].c[e] : acc[n].get(e);
+            for (int e = 0; e < 4; e++) r[n][e] = acc[n].get(e);
     }
 }
 
@@ -472,18 +471,18 @@ __device__ __forceinline__ float2 frag_p_later(const float *m, int k, int n) {
     return b;
 }
 
-// One warp: a tile of 64 rows x D columns from n rows of d values (whole 16
-// bytes) at stride ld, by 16-byte copies that write zeros elsewhere (a bulk copy
-// a row is issued a lane at a time, and 192 of them took longer than a chunk's
-// products).
-template <typename T, int D>
-__device__ __forceinline__ void warp_tile(T *dst, const T *src, int64_t ld, int n, int d) {
+// NW warps, of which this is warp w: a tile of 64 rows x D columns from n rows of d
+// values (whole 16 bytes) at stride ld, by 16-byte copies that write zeros
+// elsewhere (a bulk copy a row is issued a lane at a time, and 192 of them took
+// longer than a chunk's products).
+template <typename T, int D, int NW>
+__device__ __forceinline__ void warp_tile(T *dst, const T *src, int64_t ld, int n, int d, int w) {
     constexpr int LD = tile_ld<T>(D), VE = 16 / (int)sizeof(T), PER = D / VE, ROWS = 32 / PER;
-    const int lane = threadIdx.x & 31, r = lane / PER, c = (lane % PER) * VE;
+    const int lane = threadIdx.x & 31, r = w * (kChunk / NW) + lane / PER, c = (lane % PER) * VE;
     const T *p = src + (int64_t)r * ld + c;
     T *q = dst + r * LD + c;
 #pragma unroll 8
-    for (int i = 0; i < kChunk; i += ROWS) {
+    for (int i = 0; i < kChunk / NW; i += ROWS) {
         const bool in = i + r < n && c < d;
         cp_async16(q, in ? p : src, in ? 16 : 0);
         p += ROWS * ld;

@@ -98,9 +98,9 @@ k_delta_rchain(const DeltaGeom geo, const DeltaTerms terms, const T *__restrict_
             RChainStage<T, DK> &s = sm.st[stage];
             const int64_t slot = (int64_t)c * geo.hv + hv;
             uint64_t *bar = &sm.full[stage];
-            warp_tile<T, DK>(s.k, kp + (int64_t)ch.x * geo.ldk, geo.ldk, ch.y, geo.dkp);
-            warp_tile<T, DK>(s.q, qp + (int64_t)ch.x * geo.ldq, geo.ldq, ch.y, geo.dkp);
-            warp_tile<T, C::COLS>(s.dout, op + (int64_t)ch.x * lddo, lddo, ch.y, cols);
+            warp_tile<T, DK, 1>(s.k, kp + (int64_t)ch.x * geo.ldk, geo.ldk, ch.y, geo.dkp, 0);
+            warp_tile<T, DK, 1>(s.q, qp + (int64_t)ch.x * geo.ldq, geo.ldq, ch.y, geo.dkp, 0);
+            warp_tile<T, C::COLS, 1>(s.dout, op + (int64_t)ch.x * lddo, lddo, ch.y, cols, 0);
             cp_arrive(bar);
             if (lane == 0) {
                 bar_expect(bar, (kSquare + kVec) * 4);
@@ -151,7 +151,7 @@ k_delta_rchain(const DeltaGeom geo, const DeltaTerms terms, const T *__restrict_
 #pragma unroll
             for (int h = 0; h < 2; h++) {
                 float r[4][4];
-                state_times_rows<T, LD, false>(a, st.k, 4 * h, d0, r);
+                state_times_rows<T, LD>(a, st.k, 4 * h, d0, r);
 #pragma unroll
                 for (int n = 0; n < 4; n++) {
                     float *p = part + g * kLdT + (4 * h + n) * 8 + 2 * t;

@@ -23,7 +23,7 @@
 
 #include <algorithm>
 
-#include "seq.cuh"
+#include "linear.cuh"
 
 namespace {
 
@@ -131,116 +131,6 @@ template <bool MN>
 __device__ __forceinline__ uint64_t smem_desc(uint32_t addr) {
     return (uint64_t)((addr >> 4) & 0x3FFF) | (uint64_t)(MN ? kBox >> 4 : 1) << 16 | (uint64_t)(1024 >> 4) << 32 |
            (uint64_t)1 << 46 | (uint64_t)2 << 61;
-}
-
-// ---------------------------------------------------------------- epilogue
-
-enum { ACT_NONE = ZSOLVE_ACT_NONE, ACT_RELU = ZSOLVE_ACT_RELU, ACT_SILU = ZSOLVE_ACT_SILU, ACT_GELU = ZSOLVE_ACT_GELU, ACT_GELU_TANH = ZSOLVE_ACT_GELU_TANH };
-
-__device__ __forceinline__ float sigmoid(float x) { return __fdividef(1.f, 1.f + __expf(-x)); }
-
-// The tanh form in the sigmoid: (1 + tanh u) / 2 = sigmoid(2 u), without the
-// cancellation of 1 + tanh u for negative u.
-constexpr float kTanhC = 0.7978845608028654f, kTanhA = 0.044715f;
-
-template <int ACT>
-__device__ __forceinline__ float act1(float z) {
-    if (ACT == ACT_RELU) return z <= 0.f ? 0.f : z;
-    if (ACT == ACT_SILU) return __fdividef(z, 1.f + __expf(-z));
-    if (ACT == ACT_GELU) return 0.5f * z * (1.f + erff(z * 0.7071067811865476f));
-    if (ACT == ACT_GELU_TANH) return __fdividef(z, 1.f + __expf(-2.f * kTanhC * fmaf(kTanhA * z * z, z, z)));
-    return z;
-}
-template <int ACT>
-__device__ __forceinline__ float slope1(float z) {
-    if (ACT == ACT_RELU) return z > 0.f ? 1.f : 0.f;
-    if (ACT == ACT_SILU) {
-        const float p = sigmoid(z);
-        return p * fmaf(z, 1.f - p, 1.f);
-    }
-    if (ACT == ACT_GELU)
-        return fmaf(z * 0.3989422804014327f, __expf(-0.5f * z * z), 0.5f * (1.f + erff(z * 0.7071067811865476f)));
-    if (ACT == ACT_GELU_TANH) {
-        const float p = sigmoid(2.f * kTanhC * fmaf(kTanhA * z * z, z, z));
-        return fmaf(2.f * kTanhC * fmaf(3.f * kTanhA * z, z, 1.f), z * p * (1.f - p), p);
-    }
-    return 1.f;
-}
-
-template <int N>
-__device__ __forceinline__ void act_all(float (&v)[N], int act) {
-#define ACT_CASE(A)                                        \
-    case A: {                                              \
-        _Pragma("unroll") for (int i = 0; i < N; i++) v[i] = act1<A>(v[i]); \
-        break;                                             \
-    }
-    switch (act) {
-        ACT_CASE(ACT_RELU)
-        ACT_CASE(ACT_SILU)
-        ACT_CASE(ACT_GELU)
-        ACT_CASE(ACT_GELU_TANH)
-    }
-#undef ACT_CASE
-}
-
-// What happens to a tile of the product: part (float32 partial sums, row
-// stride ldp, one matrix of prows rows a split) or the finished result.
-struct Epilogue {
-    const void *bias;  // NULL: none
-    const void *r;     // residual, NULL: none
-    void *y;
-    void *z;           // product and bias before the activation, NULL: not kept
-    int64_t ldr, ldy, ldz;
-    float *part;
-    int64_t ldp;
-    int act;
-    int vec;           // 16-byte accesses allowed in bias, r, y, z
-};
-
-// 8 consecutive values of row `row` from column c on, of which nc (1..8) exist
-template <typename T>
-__device__ __forceinline__ void load8(const void *base, int64_t at, int nc, int vec, float (&f)[8]) {
-    const T *p = reinterpret_cast<const T *>(base) + at;
-    if (vec && nc == 8) {
-        Vec<T, 8> u;
-        u.load(p);
-        u.get(f);
-    } else {
-#pragma unroll
-        for (int i = 0; i < 8; i++) f[i] = i < nc ? to_f32(p[i]) : 0.f;
-    }
-}
-template <typename T>
-__device__ __forceinline__ void store8(void *base, int64_t at, int nc, int vec, const float (&f)[8]) {
-    T *p = reinterpret_cast<T *>(base) + at;
-    if (vec && nc == 8) {
-        Vec<T, 8> u;
-        u.set(f);
-        u.store(p);
-    } else {
-#pragma unroll
-        for (int i = 0; i < 8; i++)
-            if (i < nc) p[i] = from_f32<T>(f[i]);
-    }
-}
-
-// bias, activation, residual and the stores of 8 values
-template <typename T>
-__device__ __forceinline__ void finish8(const Epilogue &e, int64_t row, int64_t c, int nc, float (&v)[8]) {
-    float f[8];
-    if (e.bias) {
-        load8<T>(e.bias, c, nc, e.vec, f);
-#pragma unroll
-        for (int i = 0; i < 8; i++) v[i] += f[i];
-    }
-    if (e.z) store8<T>(e.z, row * e.ldz + c, nc, e.vec, v);
-    act_all(v, e.act);
-    if (e.r) {
-        load8<T>(e.r, row * e.ldr + c, nc, e.vec, f);
-#pragma unroll
-        for (int i = 0; i < 8; i++) v[i] += f[i];
-    }
-    store8<T>(e.y, row * e.ldy + c, nc, e.vec, v);
 }
 
 // ---------------------------------------------------------------- product
@@ -453,18 +343,24 @@ k_linear_join(int64_t M, int64_t N, int splits, const Epilogue epi) {
 }
 
 // Rows that TMA cannot address (base or row stride not a multiple of 16
-// bytes) copied to rows that it can; 16-bit values.
+// bytes) copied to rows that it can; 16-bit values, up to two matrices a launch.
+struct PackJob {
+    const uint16_t *src;
+    uint16_t *dst;  // rows of whole 16 bytes
+    int64_t ld, rows;
+    int cols;
+};
 __global__ void __launch_bounds__(256)
-k_linear_pack(const uint16_t *__restrict__ src, int64_t ld, int64_t rows, int cols, uint16_t *__restrict__ dst,
-              int64_t ldd) {
-    const int64_t groups = ldd / 8;
-    for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < rows * groups; i += (int64_t)gridDim.x * 256) {
+k_linear_pack(const PackJob a, const PackJob b) {
+    const PackJob &j = blockIdx.y ? b : a;
+    const int64_t ldd = (j.cols + 7) / 8 * 8, groups = ldd / 8;
+    for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < j.rows * groups; i += (int64_t)gridDim.x * 256) {
         const int64_t row = i / groups;
         const int c = (int)(i - row * groups) * 8;
         uint32_t u[8];
 #pragma unroll
-        for (int j = 0; j < 8; j++) u[j] = c + j < cols ? src[row * ld + c + j] : 0;
-        *reinterpret_cast<uint4 *>(dst + row * ldd + c) =
+        for (int e = 0; e < 8; e++) u[e] = c + e < j.cols ? j.src[row * j.ld + c + e] : 0;
+        *reinterpret_cast<uint4 *>(j.dst + row * ldd + c) =
             make_uint4(u[0] | u[1] << 16, u[2] | u[3] << 16, u[4] | u[5] << 16, u[6] | u[7] << 16);
     }
 }
@@ -643,15 +539,26 @@ cudaError_t product(zsolve_seq *s, int type, int64_t M, int64_t N, int64_t K, co
     return cudaGetLastError();
 }
 
-// A matrix that TMA can address: itself, or its copy at dst.
-cudaError_t packed(zsolve_seq *s, Mat *a, void *dst) {
-    if (a->tma_ok()) return cudaSuccess;
-    const int64_t ldd = (a->cols + 7) / 8 * 8, n = a->rows * (ldd / 8);
-    const unsigned blocks = (unsigned)std::min<int64_t>((n + 255) / 256, (int64_t)s->num_sms * 8);
-    k_linear_pack<<<blocks, 256, 0, s->st>>>((const uint16_t *)a->p, a->ld, a->rows, (int)a->cols, (uint16_t *)dst, ldd);
+// Matrices that TMA can address: themselves, or their copies.
+cudaError_t packed(zsolve_seq *s, Mat *a, void *dsta, Mat *b, void *dstb) {
+    PackJob job[2];
+    int n = 0;
+    int64_t most = 0;
+    Mat *const mats[2] = {a, b};
+    void *const dst[2] = {dsta, dstb};
+    for (int i = 0; i < 2; i++) {
+        Mat *m = mats[i];
+        if (!m || !dst[i]) continue;
+        const int64_t ldd = (m->cols + 7) / 8 * 8;
+        job[n++] = PackJob{(const uint16_t *)m->p, (uint16_t *)dst[i], m->ld, m->rows, (int)m->cols};
+        most = std::max(most, m->rows * (ldd / 8));
+        m->p = dst[i];
+        m->ld = ldd;
+    }
+    if (n == 0) return cudaSuccess;
+    const unsigned blocks = (unsigned)std::min<int64_t>((most + 255) / 256, (int64_t)s->num_sms * 8);
+    k_linear_pack<<<dim3(blocks, n), 256, 0, s->st>>>(job[0], job[n - 1]);
     s->launches++;
-    a->p = dst;
-    a->ld = ldd;
     return cudaGetLastError();
 }
 
@@ -676,8 +583,7 @@ int linear_fwd(zsolve_seq *s, int type, int64_t m, int64_t n, int64_t k, Mat x, 
         if (!ws) return st;
         carve(ws);
     }
-    SEQ_CU(packed(s, &x, xp));
-    SEQ_CU(packed(s, &w, wp));
+    SEQ_CU(packed(s, &x, xp, &w, wp));
     SEQ_CU(product<T>(s, type, m, n, k, x, false, w, false, epi, part));
     return ZSOLVE_OK;
 }
@@ -731,14 +637,13 @@ int linear_bwd(zsolve_seq *s, int type, int64_t m, int64_t n, int64_t k, Mat dy,
     }
     Mat dz = dy;
     if (form_dz) dz.p = dzp, dz.ld = ldz8;
+    SEQ_CU(packed(s, &w, wp, &x, xp));
     Epilogue epi{};
     if (dx) {
-        SEQ_CU(packed(s, &w, wp));
         epi.y = dx, epi.ldy = lddx, epi.vec = vec8(dx, lddx);
         SEQ_CU(product<T>(s, type, m, k, n, dz, false, w, true, epi, part));
     }
     if (dw) {
-        SEQ_CU(packed(s, &x, xp));
         epi.y = dw, epi.ldy = lddw, epi.vec = vec8(dw, lddw);
         SEQ_CU(product<T>(s, type, n, k, m, dz, true, x, true, epi, part));
     }
@@ -755,6 +660,14 @@ int zs_linear(zsolve_seq *s, int type, int64_t m, int64_t n, int64_t k, const vo
     epi.ldr = ldr, epi.ldy = ldy, epi.ldz = ldz;
     epi.act = act;
     epi.vec = vec8(b, 0) && vec8(r, ldr) && vec8(y, ldy) && vec8(z, ldz);
+    // One kernel for few rows, against a split product and its join.  4096 x 2048: 4.6 us
+    // for 1 .. 8 rows, 6.6 for 16, against 10; 8192 x 4096: 16 and 19.7 against 18; rows
+    // read value by value (1000 x 2157): 9.4 and 15.4 against 12.3.
+    const bool aligned = Mat{x, m, k, ldx}.tma_ok() && Mat{w, n, k, ldw}.tma_ok();
+    if (m <= 8 || (m <= kFewRows && aligned && n * k <= 1 << 24)) {
+        SEQ_CU(zs_launch_linear_few(type, m, n, k, x, ldx, w, ldw, epi, s->st, &s->launches));
+        return ZSOLVE_OK;
+    }
     const Mat mx{x, m, k, ldx}, mw{w, n, k, ldw};
     return type == ZSOLVE_BF16 ? linear_fwd<bf16>(s, type, m, n, k, mx, mw, epi)
                                : linear_fwd<f16>(s, type, m, n, k, mx, mw, epi);

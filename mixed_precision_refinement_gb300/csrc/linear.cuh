@@ -1,0 +1,121 @@
+// The epilogue of the matrix product: bias, activation, residual, stores.
+#pragma once
+
+#include "seq.cuh"
+
+namespace zs {
+
+enum { ACT_NONE = ZSOLVE_ACT_NONE, ACT_RELU = ZSOLVE_ACT_RELU, ACT_SILU = ZSOLVE_ACT_SILU, ACT_GELU = ZSOLVE_ACT_GELU, ACT_GELU_TANH = ZSOLVE_ACT_GELU_TANH };
+
+__device__ __forceinline__ float sigmoid(float x) { return __fdividef(1.f, 1.f + __expf(-x)); }
+
+// The tanh form in the sigmoid: (1 + tanh u) / 2 = sigmoid(2 u), without the
+// cancellation of 1 + tanh u for negative u.
+constexpr float kTanhC = 0.7978845608028654f, kTanhA = 0.044715f;
+
+template <int ACT>
+__device__ __forceinline__ float act1(float z) {
+    if (ACT == ACT_RELU) return z <= 0.f ? 0.f : z;
+    if (ACT == ACT_SILU) return __fdividef(z, 1.f + __expf(-z));
+    if (ACT == ACT_GELU) return 0.5f * z * (1.f + erff(z * 0.7071067811865476f));
+    if (ACT == ACT_GELU_TANH) return __fdividef(z, 1.f + __expf(-2.f * kTanhC * fmaf(kTanhA * z * z, z, z)));
+    return z;
+}
+template <int ACT>
+__device__ __forceinline__ float slope1(float z) {
+    if (ACT == ACT_RELU) return z > 0.f ? 1.f : 0.f;
+    if (ACT == ACT_SILU) {
+        const float p = sigmoid(z);
+        return p * fmaf(z, 1.f - p, 1.f);
+    }
+    if (ACT == ACT_GELU)
+        return fmaf(z * 0.3989422804014327f, __expf(-0.5f * z * z), 0.5f * (1.f + erff(z * 0.7071067811865476f)));
+    if (ACT == ACT_GELU_TANH) {
+        const float p = sigmoid(2.f * kTanhC * fmaf(kTanhA * z * z, z, z));
+        return fmaf(2.f * kTanhC * fmaf(3.f * kTanhA * z, z, 1.f), z * p * (1.f - p), p);
+    }
+    return 1.f;
+}
+
+template <int N>
+__device__ __forceinline__ void act_all(float (&v)[N], int act) {
+#define ACT_CASE(A)                                        \
+    case A: {                                              \
+        _Pragma("unroll") for (int i = 0; i < N; i++) v[i] = act1<A>(v[i]); \
+        break;                                             \
+    }
+    switch (act) {
+        ACT_CASE(ACT_RELU)
+        ACT_CASE(ACT_SILU)
+        ACT_CASE(ACT_GELU)
+        ACT_CASE(ACT_GELU_TANH)
+    }
+#undef ACT_CASE
+}
+
+// What happens to a tile of the product: part (float32 partial sums, row
+// stride ldp, one matrix of prows rows a split) or the finished result.
+struct Epilogue {
+    const void *bias;  // NULL: none
+    const void *r;     // residual, NULL: none
+    void *y;
+    void *z;           // product and bias before the activation, NULL: not kept
+    int64_t ldr, ldy, ldz;
+    float *part;
+    int64_t ldp;
+    int act;
+    int vec;           // 16-byte accesses allowed in bias, r, y, z
+};
+
+// 8 consecutive values of row `row` from column c on, of which nc (1..8) exist
+template <typename T>
+__device__ __forceinline__ void load8(const void *base, int64_t at, int nc, int vec, float (&f)[8]) {
+    const T *p = reinterpret_cast<const T *>(base) + at;
+    if (vec && nc == 8) {
+        Vec<T, 8> u;
+        u.load(p);
+        u.get(f);
+    } else {
+#pragma unroll
+        for (int i = 0; i < 8; i++) f[i] = i < nc ? to_f32(p[i]) : 0.f;
+    }
+}
+template <typename T>
+__device__ __forceinline__ void store8(void *base, int64_t at, int nc, int vec, const float (&f)[8]) {
+    T *p = reinterpret_cast<T *>(base) + at;
+    if (vec && nc == 8) {
+        Vec<T, 8> u;
+        u.set(f);
+        u.store(p);
+    } else {
+#pragma unroll
+        for (int i = 0; i < 8; i++)
+            if (i < nc) p[i] = from_f32<T>(f[i]);
+    }
+}
+
+// bias, activation, residual and the stores of 8 values
+template <typename T>
+__device__ __forceinline__ void finish8(const Epilogue &e, int64_t row, int64_t c, int nc, float (&v)[8]) {
+    float f[8];
+    if (e.bias) {
+        load8<T>(e.bias, c, nc, e.vec, f);
+#pragma unroll
+        for (int i = 0; i < 8; i++) v[i] += f[i];
+    }
+    if (e.z) store8<T>(e.z, row * e.ldz + c, nc, e.vec, v);
+    act_all(v, e.act);
+    if (e.r) {
+        load8<T>(e.r, row * e.ldr + c, nc, e.vec, f);
+#pragma unroll
+        for (int i = 0; i < 8; i++) v[i] += f[i];
+    }
+    store8<T>(e.y, row * e.ldy + c, nc, e.vec, v);
+}
+
+}  // namespace zs
+
+// linear_few.cu: y for at most kFewRows rows of x, in one kernel without a workspace.
+constexpr int kFewRows = 16;
+cudaError_t zs_launch_linear_few(int type, int64_t m, int64_t n, int64_t k, const void *x, int64_t ldx, const void *w,
+                                 int64_t ldw, const zs::Epilogue &epi, cudaStream_t st, int64_t *launches);

@@ -187,6 +187,8 @@ k_delta_terms(const DeltaGeom geo, const DeltaTerms out) {
                 v[ht] = expf(bh[ht] + bl[ht]);
                 v[kChunk + ht] = expf((bh[kChunk - 1] - bh[ht]) + (bl[kChunk - 1] - bl[ht]));
                 v[2 * kChunk + ht] = beta[ht];
+                v[3 * kChunk + ht] = bh[ht];
+                v[4 * kChunk + ht] = bl[ht];
             }
             float *TP = out.tp + slot * kSquare;
 #pragma unroll 4
@@ -369,31 +371,38 @@ __device__ __forceinline__ void put_parts(uint4 (*dst)[32], const StateSplit<T> 
     }
 }
 
-// acc += S^T Q^T at token tile n over one warp's 32 key columns
+// acc[i] += S^T Q^T at token tiles n[i] over one warp's 32 key columns
 template <typename T, int LD, int NS>
-__device__ __forceinline__ void parts_times_rows(const uint4 (*src)[32], const T *q, int n, int d0, int lane, Acc &acc) {
-    if constexpr (std::is_same<T, bf16>::value) {
-        uint32_t b[4];
-        ldmatrix4(b, q + (n * 8 + (lane & 7)) * LD + d0 + 8 * (lane >> 3));
+__device__ __forceinline__ void parts_times_rows(const uint4 (*src)[32], const T *q, const int (&n)[2], int d0, int lane,
+                                                 Acc (&acc)[2]) {
+    uint4 parts[NS];
 #pragma unroll
-        for (int i = NS - 1; i >= 0; i--) {  // part i & 1 of k step i >> 1
-            const uint4 u = src[i][lane];
-            const uint32_t a[4] = {u.x, u.y, u.z, u.w};
-            mma16(i & 1 ? acc.l : acc.c, a, b[2 * (i >> 1)], b[2 * (i >> 1) + 1]);
+    for (int i = 0; i < NS; i++) parts[i] = src[i][lane];
+    if constexpr (std::is_same<T, bf16>::value) {
+        uint32_t b[2][4];
+#pragma unroll
+        for (int i = 0; i < 2; i++) ldmatrix4(b[i], q + (n[i] * 8 + (lane & 7)) * LD + d0 + 8 * (lane >> 3));
+#pragma unroll
+        for (int j = NS - 1; j >= 0; j--) {  // part j & 1 of k step j >> 1
+            const uint32_t a[4] = {parts[j].x, parts[j].y, parts[j].z, parts[j].w};
+#pragma unroll
+            for (int i = 0; i < 2; i++) mma16(j & 1 ? acc[i].l : acc[i].c, a, b[i][2 * (j >> 1)], b[i][2 * (j >> 1) + 1]);
         }
     } else {
-        float2 b[4];
-        frag4<T, LD, false>(q, n * 8, d0, b);
+        float2 b[2][4];
+#pragma unroll
+        for (int i = 0; i < 2; i++) frag4<T, LD, false>(q, n[i] * 8, d0, b[i]);
 #pragma unroll
         for (int j = 0; j < 4; j++) {
             SplitA a;
-            const uint4 h = src[sizeof(T) == 2 ? j : 2 * j][lane];
+            const uint4 h = parts[sizeof(T) == 2 ? j : 2 * j];
             a.hi[0] = h.x, a.hi[1] = h.y, a.hi[2] = h.z, a.hi[3] = h.w;
             if (sizeof(T) == 4) {
-                const uint4 l = src[(2 * j + 1) % NS][lane];
+                const uint4 l = parts[(2 * j + 1) % NS];
                 a.lo[0] = l.x, a.lo[1] = l.y, a.lo[2] = l.z, a.lo[3] = l.w;
             }
-            mma_split<false, sizeof(T) == 2, sizeof(T) == 2>(acc, a, b[j]);
+#pragma unroll
+            for (int i = 0; i < 2; i++) mma_split<false, sizeof(T) == 2, sizeof(T) == 2>(acc[i], a, b[i][j]);
         }
     }
 }
@@ -468,11 +477,9 @@ k_delta_chain(const DeltaGeom geo, const DeltaTerms terms, const float *__restri
             for (int grp = 0; grp < NV; grp++) {
                 qs[grp][0].zero(), qs[grp][1].zero();
                 wait(&sm.sfull[grp], it);
+                const int n[2] = {tile_of<4>(hw, 0), tile_of<4>(hw, 1)};
 #pragma unroll
-                for (int w = 0; w < WK; w++)
-#pragma unroll
-                    for (int i = 0; i < 2; i++)
-                        parts_times_rows<T, LD, C::NS>(sm.s[grp][w], st.q, tile_of<4>(hw, i), 32 * w, lane, qs[grp][i]);
+                for (int w = 0; w < WK; w++) parts_times_rows<T, LD, C::NS>(sm.s[grp][w], st.q, n, 32 * w, lane, qs[grp]);
                 __syncwarp();
                 if (lane == 0) bar_arrive(&sm.sempty[grp]);
             }

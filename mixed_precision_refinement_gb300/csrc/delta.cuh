@@ -50,11 +50,11 @@ struct DeltaGeom {
 // Per chunk and value head, what does not depend on the state (float32): T and P
 // in one matrix of 64 rows of stride 72, T strictly below the diagonal (its
 // diagonal is 1) and P transposed on and above it; and the vectors c_i, e_64,i,
-// beta_i (64 each).
+// beta_i and b_i in two floats (64 each).
 struct DeltaTerms {
     float *tp, *vec;
 };
-constexpr int kVec = 3 * kChunk;
+constexpr int kVec = 5 * kChunk;
 
 // ---------------------------------------------------------------- products
 
@@ -134,6 +134,12 @@ __device__ __forceinline__ void mma_split(Acc &acc, const SplitA &a, float2 b) {
     mma8(acc.c, a.hi, b0, b1);
 }
 
+__device__ __forceinline__ void add_to(float (&c)[4], const float (&d)[4]) {
+    const float2 x = add2(make_float2(c[0], c[1]), make_float2(d[0], d[1]));
+    const float2 y = add2(make_float2(c[2], c[3]), make_float2(d[2], d[3]));
+    c[0] = x.x, c[1] = x.y, c[2] = y.x, c[3] = y.y;
+}
+
 // The same into one float32 sum that is rounded to nearest: the step's terms
 // start from zero.
 template <bool A_EXACT, bool B_EXACT>
@@ -151,8 +157,7 @@ __device__ __forceinline__ void mma_add(float (&c)[4], const SplitA &a, float2 b
     } else {
         mma8_first(d, a.hi, b0, b1);
     }
-#pragma unroll
-    for (int e = 0; e < 4; e++) c[e] += d[e];
+    add_to(c, d);
 }
 
 // bfloat16 inputs: a float32 operand in three bfloat16 parts (24 bits), so that

@@ -239,18 +239,19 @@ k_delta_rchain(const DeltaGeom geo, const DeltaTerms terms, const T *__restrict_
 
 // ---------------------------------------------------------------- gradients of a chunk
 
-// One block for a chunk and a value head; warp (m, n): tokens 16 m .., key
-// columns 32 n .. (of F, E, H, dq, dk) and 64 / NG of the 64 x 64 products'
-// columns.  The products over the value columns run in slabs of 32 of them, two
-// stages of slabs where they fit; the 64 x 64 matrices then take the slabs'
-// place.
+// One block for a chunk and a value head; warp (m, n): 16 MT tokens, key columns
+// 32 n .. (of F, E, H, dq, dk) and 64 / NG of the 64 x 64 products' columns.  The
+// products over the value columns run in slabs of 32 of them, two stages of slabs;
+// the 64 x 64 matrices then take the slabs' place.
 constexpr int kSlab = 32;
 constexpr int kLdS = kSlab + 8;
 
 template <typename T, int DK>
 struct GradCfg {
     static constexpr int NG = DK / 32;
-    static constexpr int NT = 128 * NG;
+    static constexpr int MT = 1;  // token tiles of 16 a warp (two share the B splits, but leave two warps a scheduler: 2104 us for 2047)
+    static constexpr int MG = 4 / MT;
+    static constexpr int NT = 32 * MG * NG;
     static constexpr int PT = 8 / NG;  // 8-column tiles of the 64 x 64 products a warp
     static constexpr int LD = tile_ld<T>(DK);
 };
@@ -278,11 +279,10 @@ struct GradSmem {
         GradSquares sq;
     };
     float vec[kVec];
-    float bh[kChunk], bl[kChunk];
     float row_kE[C::NG][kChunk], row_kH[C::NG][kChunk], row_qF[C::NG][kChunk];
-    float row_m[C::NG][kChunk], row_w[C::NG][kChunk], col_m[4][kChunk];
+    float row_m[C::NG][kChunk], row_w[C::NG][kChunk], col_m[C::MG][kChunk];
     float row_xv[kChunk];
-    float dot[C::NG * 4];
+    float dot[C::NG * C::MG];
 };
 
 // (X(r0 + g, c0 + 2t), X(r0 + g, c0 + 2t + 1))
@@ -294,6 +294,50 @@ __device__ __forceinline__ float2 frag1(const T *x, int r0, int c0) {
         return unpack2<T>(*reinterpret_cast<const uint32_t *>(p));
     else
         return *reinterpret_cast<const float2 *>(p);
+}
+
+// A 16 x 8 A operand from rows r0 .. of a tile: the parts, of which a 16-bit
+// value has only the first.
+template <typename T, int LD>
+__device__ __forceinline__ SplitA rows_a(const T *x, int r0, int c0) {
+    const float2 a = frag1<T, LD>(x, r0, c0), b = frag1<T, LD>(x, r0 + 8, c0);
+    SplitA s;
+    if constexpr (sizeof(T) == 2) {
+        s.hi[0] = __float_as_uint(a.x), s.hi[1] = __float_as_uint(b.x), s.hi[2] = __float_as_uint(a.y), s.hi[3] = __float_as_uint(b.y);
+        s.lo[0] = s.lo[1] = s.lo[2] = s.lo[3] = 0u;
+    } else {
+        s.set(a.x, a.y, b.x, b.y);
+    }
+    return s;
+}
+
+// A float32 B operand in two tf32 parts, for several products.
+struct SplitB {
+    uint32_t h0, h1, l0, l1;
+};
+__device__ __forceinline__ SplitB split_b(float2 b) {
+    SplitB s;
+    s.h0 = tf32(b.x), s.h1 = tf32(b.y);
+    s.l0 = tf32(b.x - __uint_as_float(s.h0)), s.l1 = tf32(b.y - __uint_as_float(s.h1));
+    return s;
+}
+template <bool A_EXACT>
+__device__ __forceinline__ void mma_add(float (&c)[4], const SplitA &a, const SplitB &b) {
+    float d[4];
+    mma8_first(d, a.hi, b.l0, b.l1);
+    if (!A_EXACT) mma8(d, a.lo, b.h0, b.h1);
+    mma8(d, a.hi, b.h0, b.h1);
+    add_to(c, d);
+}
+
+// Two neighbouring values as they lie in memory.
+template <typename T>
+struct alignas(2 * sizeof(T)) Pair {
+    T x, y;
+};
+template <typename T>
+__device__ __forceinline__ float2 pair_f32(const Pair<T> &p) {
+    return make_float2(to_f32(p.x), to_f32(p.y));
 }
 
 // R rows of a slab: `cols` columns of rows at stride ld, zeros beyond
@@ -321,7 +365,7 @@ k_delta_grads(const DeltaGeom geo, const DeltaTerms terms, const T *__restrict__
               const float *__restrict__ dxs, float *__restrict__ dqp, float *__restrict__ dkp, T *__restrict__ dq,
               T *__restrict__ dk, float *__restrict__ dg, float *__restrict__ dbeta, int vecv) {
     using C = GradCfg<T, DK>;
-    constexpr int NG = C::NG, NT = C::NT, PT = C::PT, LD = C::LD;
+    constexpr int NG = C::NG, MG = C::MG, MT = C::MT, NT = C::NT, PT = C::PT, LD = C::LD;
     constexpr bool EXACT = sizeof(T) == 2;
     extern __shared__ __align__(16) uint8_t smem_raw[];
     GradSmem<T, DK> &sm = *reinterpret_cast<GradSmem<T, DK> *>(smem_raw);
@@ -330,7 +374,7 @@ k_delta_grads(const DeltaGeom geo, const DeltaTerms terms, const T *__restrict__
     if (n == 0) return;
     const int hv = blockIdx.y, hk = hv / (geo.hv / geo.hk);
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g = lane >> 2, t = lane & 3;
-    const int wm = warp & 3, wn = warp >> 2, m0 = wm * 16, d0 = wn * 32, p0 = wn * PT * 8;
+    const int wm = warp % MG, wn = warp / MG, m0 = wm * 16 * MT, d0 = wn * 32, p0 = wn * PT * 8;
     const int64_t slot = (int64_t)blockIdx.x * geo.hv + hv;
     const float *S = states + slot * geo.dk * geo.dv, *DS = dends + slot * geo.dk * geo.dv;
     const float *Us = us + slot * kChunk * geo.dv, *DXs = dxs + slot * kChunk * geo.dv;
@@ -352,109 +396,128 @@ k_delta_grads(const DeltaGeom geo, const DeltaTerms terms, const T *__restrict__
     load_tile<T, DK, NT>(sm.q, (const T *)geo.q + (int64_t)ch.x * geo.ldq + (int64_t)hk * geo.dkp, geo.ldq, n, geo.dkp);
     for (int i = tid; i < kVec / 4; i += NT) cp_async16(sm.vec + 4 * i, terms.vec + slot * kVec + 4 * i, 16);
     load(0, 0);
-    if (warp == 0) gate_sums(geo, ch, hv, sm.bh, sm.bl);
     if (tid < kChunk) sm.row_xv[tid] = 0.f;
 
     // the products over the value columns
-    float F[4][4] = {}, E[4][4] = {}, H[4][4] = {}, dp[PT][4] = {}, da[PT][4] = {};
+    float F[MT][4][4] = {}, E[MT][4][4] = {}, H[MT][4][4] = {}, dp[MT][PT][4] = {}, da[MT][PT][4] = {};
     float sds = 0.f;
     for (int v = 0, it = 0; v < geo.dv; v += kSlab, it++) {
         cp_wait<0>();
         __syncthreads();
         if (v + kSlab < geo.dv) load(v + kSlab, (it + 1) & 1);
         GradSlab<T, DK> &s = sm.slab[it & 1];
+        // v for the dot products below: on its way during the products
+        constexpr int NV2 = kChunk * kSlab / 2 / NT;
+        Pair<T> vv[NV2];
 #pragma unroll
+        for (int i = 0; i < NV2; i++) {
+            const int r = (tid >> 4) + i * (NT / 16), c = v + (tid & 15) * 2;
+            vv[i] = Pair<T>{};
+            if (r < n && c < geo.dvp) vv[i] = *reinterpret_cast<const Pair<T> *>(V + r * geo.ldv + c);  // dX is zero beyond dv
+        }
+#pragma unroll 1
         for (int c = 0; c < kSlab; c += 8) {
-            SplitA ao, ax, au;
-            {
-                const float2 a = frag1<T, kLdS>(s.dout, m0, c), b = frag1<T, kLdS>(s.dout, m0 + 8, c);
-                ao.set(a.x, a.y, b.x, b.y);
-            }
-            {
-                const float2 a = frag1<float, kLdS>(s.dx, m0, c), b = frag1<float, kLdS>(s.dx, m0 + 8, c);
-                ax.set(a.x, a.y, b.x, b.y);
-            }
-            {
-                const float2 a = frag1<float, kLdS>(s.u, m0, c), b = frag1<float, kLdS>(s.u, m0 + 8, c);
-                au.set(a.x, a.y, b.x, b.y);
+            SplitA ao[MT], ax[MT], au[MT];
+#pragma unroll
+            for (int i = 0; i < MT; i++) {
+                const int m = m0 + 16 * i;
+                ao[i] = rows_a<T, kLdS>(s.dout, m, c);
+                ax[i] = rows_a<float, kLdS>(s.dx, m, c);
+                au[i] = rows_a<float, kLdS>(s.u, m, c);
             }
 #pragma unroll
             for (int j = 0; j < 4; j++) {
-                const float2 b = frag1<float, kLdS>(s.s, d0 + 8 * j, c);
-                mma_add<EXACT, false>(F[j], ao, b);
-                mma_add<false, false>(E[j], ax, b);
-                mma_add<false, false>(H[j], au, frag1<float, kLdS>(s.ds, d0 + 8 * j, c));
+                const SplitB b = split_b(frag1<float, kLdS>(s.s, d0 + 8 * j, c)), e = split_b(frag1<float, kLdS>(s.ds, d0 + 8 * j, c));
+#pragma unroll
+                for (int i = 0; i < MT; i++) {
+                    mma_add<EXACT>(F[i][j], ao[i], b);
+                    mma_add<false>(E[i][j], ax[i], b);
+                    mma_add<false>(H[i][j], au[i], e);
+                }
             }
 #pragma unroll
             for (int j = 0; j < PT; j++) {
-                if (p0 + 8 * j > m0 + 8) continue;  // above the diagonal
-                const float2 b = frag1<float, kLdS>(s.u, p0 + 8 * j, c);
-                mma_add<EXACT, false>(dp[j], ao, b);
-                mma_add<false, false>(da[j], ax, b);
+                if (p0 + 8 * j > m0 + 16 * MT - 8) continue;  // above the diagonal
+                const SplitB b = split_b(frag1<float, kLdS>(s.u, p0 + 8 * j, c));
+#pragma unroll
+                for (int i = 0; i < MT; i++) {
+                    mma_add<EXACT>(dp[i][j], ao[i], b);
+                    mma_add<false>(da[i][j], ax[i], b);
+                }
             }
         }
-        // dX_i . v_i and <S, dS'>
-        for (int i = tid; i < kChunk * kSlab; i += NT) {
-            const int r = i / kSlab, c = i - r * kSlab;
-            const float x = r < n && v + c < geo.dv ? s.dx[r * kLdS + c] * to_f32(V[r * geo.ldv + v + c]) : 0.f;
-            const float sum = warp_sum(x);
-            if (lane == 0) sm.row_xv[r] += sum;  // a warp is a row's 32 columns
+        // dX_i . v_i, two columns a lane, and <S, dS'>
+#pragma unroll
+        for (int i = 0; i < NV2; i++) {
+            const int r = (tid >> 4) + i * (NT / 16);
+            const float2 x = *reinterpret_cast<const float2 *>(s.dx + r * kLdS + (tid & 15) * 2), y = pair_f32<T>(vv[i]);
+            float sum = fmaf(x.x, y.x, x.y * y.y);
+#pragma unroll
+            for (int q = 1; q < 16; q <<= 1) sum += __shfl_xor_sync(0xffffffffu, sum, q);
+            if ((tid & 15) == 0) sm.row_xv[r] += sum;  // one half warp a row
         }
-        for (int i = tid; i < DK * kSlab; i += NT) {
-            const int r = i / kSlab, c = i - r * kSlab;
-            sds = fmaf(s.s[r * kLdS + c], s.ds[r * kLdS + c], sds);
+        for (int i = tid; i < DK * kSlab / 4; i += NT) {
+            const int r = i / (kSlab / 4), c = (i - r * (kSlab / 4)) * 4;
+            const float4 x = *reinterpret_cast<const float4 *>(s.s + r * kLdS + c), y = *reinterpret_cast<const float4 *>(s.ds + r * kLdS + c);
+            sds += fmaf(x.x, y.x, fmaf(x.y, y.y, fmaf(x.z, y.z, x.w * y.w)));
         }
     }
     sds = warp_sum(sds);
     if (lane == 0) sm.dot[warp] = sds;
     __syncthreads();  // the slabs are read; the 64 x 64 matrices take their place
 
-    // K K^T and Q K^T: the warp's tiles
+    // K K^T: the warp's tiles; of Q K^T only P is needed, which the terms have
     {
-        float kk[PT][4] = {}, qk[PT][4] = {};
-#pragma unroll 1
+        const float *bh = sm.vec + 3 * kChunk, *bl = sm.vec + 4 * kChunk;
+        float pt[MT][PT][4];
+#pragma unroll
+        for (int i = 0; i < MT; i++)
+#pragma unroll
+            for (int j = 0; j < PT; j++)
+#pragma unroll
+                for (int e = 0; e < 4; e++) {
+                    const int y = m0 + 16 * i + g + (e >> 1) * 8, x = p0 + 8 * j + 2 * t + (e & 1);
+                    pt[i][j][e] = x <= y ? terms.tp[slot * kSquare + x * kLdT + y] : 0.f;
+                }
+        float kk[MT][PT][4] = {};
+#pragma unroll 4
         for (int c = 0; c < DK; c += 8) {
-            SplitA ak, aq;
-            {
-                const float2 a = frag1<T, LD>(sm.k, m0, c), b = frag1<T, LD>(sm.k, m0 + 8, c);
-                ak.set(a.x, a.y, b.x, b.y);
-            }
-            {
-                const float2 a = frag1<T, LD>(sm.q, m0, c), b = frag1<T, LD>(sm.q, m0 + 8, c);
-                aq.set(a.x, a.y, b.x, b.y);
-            }
+            SplitA ak[MT];
+#pragma unroll
+            for (int i = 0; i < MT; i++) ak[i] = rows_a<T, LD>(sm.k, m0 + 16 * i, c);
 #pragma unroll
             for (int j = 0; j < PT; j++) {
-                if (p0 + 8 * j > m0 + 8) continue;
                 const float2 b = frag1<T, LD>(sm.k, p0 + 8 * j, c);
-                mma_add<EXACT, EXACT>(kk[j], ak, b);
-                mma_add<EXACT, EXACT>(qk[j], aq, b);
+#pragma unroll
+                for (int i = 0; i < MT; i++) mma_add<EXACT, EXACT>(kk[i][j], ak[i], b);
             }
         }
         // r, beta w and their sums with the raw products
-        float rm[2] = {}, rw[2] = {};
+        float rm[MT][2] = {}, rw[MT][2] = {};
 #pragma unroll
         for (int j = 0; j < PT; j++) {
             float cm[2] = {};
 #pragma unroll
-            for (int e = 0; e < 4; e++) {
-                const int y = m0 + g + (e >> 1) * 8, x = p0 + 8 * j + 2 * t + (e & 1);
-                float r = 0.f, w = 0.f;
-                if (x <= y) {
-                    const float ex = expf((sm.bh[y] - sm.bh[x]) + (sm.bl[y] - sm.bl[x]));
-                    r = geo.scale * ex * dp[j][e];
-                    if (x < y) w = -ex * da[j][e];
-                }
-                const float bw = sm.vec[2 * kChunk + y] * w;
-                sm.sq.r[y * kLdT + x] = r;
-                sm.sq.w[y * kLdT + x] = bw;
-                const float mm = x <= y ? fmaf(r, qk[j][e], bw * kk[j][e]) : 0.f;
-                rm[e >> 1] += mm;
-                cm[e & 1] += mm;
-                if (x < y) rw[e >> 1] = fmaf(w, kk[j][e], rw[e >> 1]);
-            }
+            for (int i = 0; i < MT; i++)
 #pragma unroll
-            for (int e = 0; e < 2; e++) {  // over the 16 rows
+                for (int e = 0; e < 4; e++) {
+                    const int y = m0 + 16 * i + g + (e >> 1) * 8, x = p0 + 8 * j + 2 * t + (e & 1);
+                    float r = 0.f, w = 0.f;
+                    if (x <= y) {
+                        const float ex = expf((bh[y] - bh[x]) + (bl[y] - bl[x]));
+                        r = geo.scale * ex * dp[i][j][e];
+                        if (x < y) w = -ex * da[i][j][e];
+                    }
+                    const float bw = sm.vec[2 * kChunk + y] * w;
+                    sm.sq.r[y * kLdT + x] = r;
+                    sm.sq.w[y * kLdT + x] = bw;
+                    const float mm = x <= y ? fmaf(dp[i][j][e], pt[i][j][e], bw * kk[i][j][e]) : 0.f;
+                    rm[i][e >> 1] += mm;
+                    cm[e & 1] += mm;
+                    if (x < y) rw[i][e >> 1] = fmaf(w, kk[i][j][e], rw[i][e >> 1]);
+                }
+#pragma unroll
+            for (int e = 0; e < 2; e++) {  // over the warp's rows
                 cm[e] += __shfl_xor_sync(0xffffffffu, cm[e], 4);
                 cm[e] += __shfl_xor_sync(0xffffffffu, cm[e], 8);
                 cm[e] += __shfl_xor_sync(0xffffffffu, cm[e], 16);
@@ -462,37 +525,39 @@ k_delta_grads(const DeltaGeom geo, const DeltaTerms terms, const T *__restrict__
             }
         }
 #pragma unroll
-        for (int h = 0; h < 2; h++) {
+        for (int i = 0; i < MT; i++)
 #pragma unroll
-            for (int o = 1; o < 4; o <<= 1) {
-                rm[h] += __shfl_xor_sync(0xffffffffu, rm[h], o);
-                rw[h] += __shfl_xor_sync(0xffffffffu, rw[h], o);
+            for (int h = 0; h < 2; h++) {
+#pragma unroll
+                for (int o = 1; o < 4; o <<= 1) {
+                    rm[i][h] += __shfl_xor_sync(0xffffffffu, rm[i][h], o);
+                    rw[i][h] += __shfl_xor_sync(0xffffffffu, rw[i][h], o);
+                }
+                if (t == 0) {
+                    sm.row_m[wn][m0 + 16 * i + g + 8 * h] = rm[i][h];
+                    sm.row_w[wn][m0 + 16 * i + g + 8 * h] = rw[i][h];
+                }
             }
-            if (t == 0) {
-                sm.row_m[wn][m0 + g + 8 * h] = rm[h];
-                sm.row_w[wn][m0 + g + 8 * h] = rw[h];
-            }
-        }
     }
-    // rows' products with k and q, then dq and dk begin with c F and e H - beta c E
-    float aq[4][4], ak[4][4];
-    {
+    // rows' products with k and q; then dq and dk begin with c F and e H - beta c E, in F's and H's place
+#pragma unroll
+    for (int i = 0; i < MT; i++) {
         float kE[2] = {}, kH[2] = {}, qF[2] = {};
-        const int y0 = m0 + g;
+        const int y0 = m0 + 16 * i + g;
 #pragma unroll
         for (int j = 0; j < 4; j++)
 #pragma unroll
             for (int h = 0; h < 2; h++) {
-                const float2 kv = frag1<T, LD>(sm.k, m0 + 8 * h, d0 + 8 * j), qv = frag1<T, LD>(sm.q, m0 + 8 * h, d0 + 8 * j);
+                const float2 kv = frag1<T, LD>(sm.k, m0 + 16 * i + 8 * h, d0 + 8 * j), qv = frag1<T, LD>(sm.q, m0 + 16 * i + 8 * h, d0 + 8 * j);
                 const int y = y0 + 8 * h, e = 2 * h;
-                kE[h] = fmaf(kv.x, E[j][e], fmaf(kv.y, E[j][e + 1], kE[h]));
-                kH[h] = fmaf(kv.x, H[j][e], fmaf(kv.y, H[j][e + 1], kH[h]));
-                qF[h] = fmaf(qv.x, F[j][e], fmaf(qv.y, F[j][e + 1], qF[h]));
+                kE[h] = fmaf(kv.x, E[i][j][e], fmaf(kv.y, E[i][j][e + 1], kE[h]));
+                kH[h] = fmaf(kv.x, H[i][j][e], fmaf(kv.y, H[i][j][e + 1], kH[h]));
+                qF[h] = fmaf(qv.x, F[i][j][e], fmaf(qv.y, F[i][j][e + 1], qF[h]));
                 const float c = sm.vec[y], en = sm.vec[kChunk + y], bc = sm.vec[2 * kChunk + y] * c;
 #pragma unroll
-                for (int i = e; i < e + 2; i++) {
-                    aq[j][i] = geo.scale * c * F[j][i];
-                    ak[j][i] = fmaf(en, H[j][i], -bc * E[j][i]);
+                for (int q = e; q < e + 2; q++) {
+                    F[i][j][q] *= geo.scale * c;
+                    H[i][j][q] = fmaf(en, H[i][j][q], -bc * E[i][j][q]);
                 }
             }
 #pragma unroll
@@ -511,10 +576,9 @@ k_delta_grads(const DeltaGeom geo, const DeltaTerms terms, const T *__restrict__
         }
     }
     __syncthreads();
-    // dbeta, and dg as the sums of db from the end (float64: a few additions)
-    if (warp == 0) {
-        double db[2];
-        float endsum = 0.f, dots = 0.f;
+    // dbeta, and dg as the sums of db from the end, on the last warp
+    if (warp == NT / 32 - 1) {
+        float db[2], endsum = 0.f, dots = 0.f;
 #pragma unroll
         for (int e = 0; e < 2; e++) {
             const int i = 2 * lane + e;
@@ -525,77 +589,83 @@ k_delta_grads(const DeltaGeom geo, const DeltaTerms terms, const T *__restrict__
                 rm += sm.row_m[p][i], rw += sm.row_w[p][i];
             }
 #pragma unroll
-            for (int p = 0; p < 4; p++) cm += sm.col_m[p][i];
+            for (int p = 0; p < MG; p++) cm += sm.col_m[p][i];
             const float c = sm.vec[i], en = sm.vec[kChunk + i], b = sm.vec[2 * kChunk + i];
-            db[e] = (double)(geo.scale * c * qF) + (double)rm - (double)cm - (double)(en * kH) - (double)(b * c * kE);
+            db[e] = (geo.scale * c * qF - b * c * kE) + (rm - cm) - en * kH;
             endsum = fmaf(en, kH, endsum);
             if (i < n) dbeta[(int64_t)(ch.x + i) * geo.hv + hv] = sm.row_xv[i] - c * kE + rw;
         }
-        for (int i = lane; i < NG * 4; i += 32) dots += sm.dot[i];
+        for (int i = lane; i < NG * MG; i += 32) dots += sm.dot[i];
         const float last = fmaf(sm.vec[kChunk - 1], warp_sum(dots), warp_sum(endsum));
-        if (lane == 31) db[1] += (double)last;
-        double s = db[0] + db[1];
+        if (lane == 31) db[1] += last;
+        float s = db[0] + db[1];
 #pragma unroll
         for (int o = 1; o < 32; o <<= 1) {
-            const double x = __shfl_down_sync(0xffffffffu, s, o);
+            const float x = __shfl_down_sync(0xffffffffu, s, o);
             if (lane + o < 32) s += x;
         }
-        const double d0v = s, d1v = s - db[0];
-        if (2 * lane < n) dg[(int64_t)(ch.x + 2 * lane) * geo.hv + hv] = (float)d0v;
-        if (2 * lane + 1 < n) dg[(int64_t)(ch.x + 2 * lane + 1) * geo.hv + hv] = (float)d1v;
+        float after = __shfl_down_sync(0xffffffffu, s, 1);
+        if (lane == 31) after = 0.f;
+        const float d1 = db[1] + after;
+        if (2 * lane < n) dg[(int64_t)(ch.x + 2 * lane) * geo.hv + hv] = db[0] + d1;
+        if (2 * lane + 1 < n) dg[(int64_t)(ch.x + 2 * lane + 1) * geo.hv + hv] = d1;
     }
-    // dq += r K, dk += (beta w) K: rows of the tile, columns up to the diagonal
-#pragma unroll 1
-    for (int k = 0; k < 2 * wm + 2; k++) {
+    // dq += r K, dk += (beta w) K: columns up to the diagonal
+#pragma unroll 2
+    for (int k = 0; k < 2 * MT * (wm + 1); k++) {
         float2 b[4];
         frag4<T, LD, true>(sm.k, k * 8, d0, b);
-        SplitA ar, aw;
-        {
-            const float2 x = frag1<float, kLdT>(sm.sq.r, m0, k * 8), y = frag1<float, kLdT>(sm.sq.r, m0 + 8, k * 8);
-            ar.set(x.x, x.y, y.x, y.y);
-        }
-        {
-            const float2 x = frag1<float, kLdT>(sm.sq.w, m0, k * 8), y = frag1<float, kLdT>(sm.sq.w, m0 + 8, k * 8);
-            aw.set(x.x, x.y, y.x, y.y);
-        }
 #pragma unroll
-        for (int j = 0; j < 4; j++) {
-            mma_add<false, EXACT>(aq[j], ar, b[j]);
-            mma_add<false, EXACT>(ak[j], aw, b[j]);
+        for (int i = 0; i < MT; i++) {
+            const SplitA ar = rows_a<float, kLdT>(sm.sq.r, m0 + 16 * i, k * 8), aw = rows_a<float, kLdT>(sm.sq.w, m0 + 16 * i, k * 8);
+#pragma unroll
+            for (int j = 0; j < 4; j++) {
+                mma_add<false, EXACT>(F[i][j], ar, b[j]);
+                mma_add<false, EXACT>(H[i][j], aw, b[j]);
+            }
         }
     }
     // dk += r^T Q + (beta w)^T K: the transposes' rows, columns from the diagonal on
-#pragma unroll 1
-    for (int k = 2 * wm; k < 8; k++) {
+#pragma unroll 2
+    for (int k = 2 * MT * wm; k < 8; k++) {
         float2 bq[4], bk[4];
         frag4<T, LD, true>(sm.q, k * 8, d0, bq);
         frag4<T, LD, true>(sm.k, k * 8, d0, bk);
-        const int at = (k * 8 + 2 * t) * kLdT + m0 + g;
-        SplitA ar, aw;
-        ar.set(sm.sq.r[at], sm.sq.r[at + kLdT], sm.sq.r[at + 8], sm.sq.r[at + kLdT + 8]);
-        aw.set(sm.sq.w[at], sm.sq.w[at + kLdT], sm.sq.w[at + 8], sm.sq.w[at + kLdT + 8]);
 #pragma unroll
-        for (int j = 0; j < 4; j++) {
-            mma_add<false, EXACT>(ak[j], ar, bq[j]);
-            mma_add<false, EXACT>(ak[j], aw, bk[j]);
+        for (int i = 0; i < MT; i++) {
+            const int at = (k * 8 + 2 * t) * kLdT + m0 + 16 * i + g;
+            SplitA ar, aw;
+            ar.set(sm.sq.r[at], sm.sq.r[at + kLdT], sm.sq.r[at + 8], sm.sq.r[at + kLdT + 8]);
+            aw.set(sm.sq.w[at], sm.sq.w[at + kLdT], sm.sq.w[at + 8], sm.sq.w[at + kLdT + 8]);
+#pragma unroll
+            for (int j = 0; j < 4; j++) {
+                mma_add<false, EXACT>(H[i][j], ar, bq[j]);
+                mma_add<false, EXACT>(H[i][j], aw, bk[j]);
+            }
         }
     }
 #pragma unroll
-    for (int j = 0; j < 4; j++)
+    for (int i = 0; i < MT; i++)
 #pragma unroll
-        for (int e = 0; e < 4; e++) {
-            const int y = m0 + g + (e >> 1) * 8, d = d0 + 8 * j + 2 * t + (e & 1);
-            if (y >= n || d >= geo.dk) continue;
-            if (dqp) {
-                const int64_t at = ((int64_t)(ch.x + y) * geo.hv + hv) * geo.dk + d;
-                dqp[at] = aq[j][e];
-                dkp[at] = ak[j][e];
-            } else {
-                const int64_t at = ((int64_t)(ch.x + y) * geo.hk + hk) * geo.dk + d;
-                dq[at] = from_f32<T>(aq[j][e]);
-                dk[at] = from_f32<T>(ak[j][e]);
+        for (int j = 0; j < 4; j++)
+#pragma unroll
+            for (int h = 0; h < 2; h++) {
+                const int y = m0 + 16 * i + g + 8 * h, d = d0 + 8 * j + 2 * t;
+                if (y >= n) continue;
+#pragma unroll
+                for (int e = 0; e < 2; e++) {
+                    if (d + e >= geo.dk) continue;
+                    if (dqp) {
+                        const int64_t at = ((int64_t)(ch.x + y) * geo.hv + hv) * geo.dk + d + e;
+                        dqp[at] = F[i][j][2 * h + e];
+                        dkp[at] = H[i][j][2 * h + e];
+                    } else {
+                        const int64_t at = ((int64_t)(ch.x + y) * geo.hk + hk) * geo.dk + d + e;
+                        dq[at] = from_f32<T>(F[i][j][2 * h + e]);
+                        dk[at] = from_f32<T>(H[i][j][2 * h + e]);
+                    }
+                }
             }
-        }
 }
 
 // dq and dk of the key heads: the sums over the value heads that share them, in order.

@@ -452,7 +452,9 @@ void zsolve_afs_destroy(zsolve_afs *afs);
  *  - The handle owns its workspace.  It grows when a call needs more, which
  *    waits for the device; during a stream capture that is refused with
  *    ZSOLVE_ESTATE (zsolve_seq_reserve, or the same call made once before the
- *    capture, provides for it).  A handle is not thread-safe.
+ *    capture, provides for it).  A workspace that a captured graph uses is kept
+ *    until the handle is destroyed; the graph may not be replayed beside other
+ *    work on the handle, nor after that.  A handle is not thread-safe.
  *  - Sizes of zero are allowed where they make sense (no rows, no tokens):
  *    nothing is read, and gradients that are sums over nothing are zero.
  * ------------------------------------------------------------------------- */

@@ -20,27 +20,39 @@ int seq_fail(zsolve_seq *s, int status, const char *fmt, ...) {
 
 void *seq_workspace(zsolve_seq *s, size_t bytes, int *status) {
     *status = ZSOLVE_OK;
-    if (bytes <= s->ws_bytes) return s->ws;
     cudaStreamCaptureStatus cap = cudaStreamCaptureStatusNone;
     cudaError_t e = cudaStreamIsCapturing(s->st, &cap);
-    if (e == cudaSuccess && cap != cudaStreamCaptureStatusNone) {
+    const bool capturing = e == cudaSuccess && cap != cudaStreamCaptureStatusNone;
+    if (e == cudaSuccess && bytes <= s->ws_bytes) {
+        s->ws_captured = s->ws_captured || capturing;
+        return s->ws;
+    }
+    if (capturing) {
         *status = seq_fail(s, ZSOLVE_ESTATE,
                            "a workspace of %zu bytes is needed and cannot be allocated during a stream capture "
                            "(zsolve_seq_reserve before it)",
                            bytes);
         return nullptr;
     }
-    // the old one may still be in use by work in flight
-    if (e == cudaSuccess && s->ws) e = cudaDeviceSynchronize();
-    if (e == cudaSuccess && s->ws) {
-        e = cudaFree(s->ws);
-        s->ws = nullptr;
-        s->ws_bytes = 0;
+    // the old one may still be in use by work in flight, or by a graph
+    if (e == cudaSuccess && s->ws && s->ws_captured) {
+        try {
+            s->retired.push_back(s->ws);
+        } catch (...) {
+            *status = seq_fail(s, ZSOLVE_ENOMEM, "out of host memory");
+            return nullptr;
+        }
+    } else if (e == cudaSuccess && s->ws) {
+        e = cudaDeviceSynchronize();
+        if (e == cudaSuccess) e = cudaFree(s->ws);
     }
     if (e != cudaSuccess) {
         *status = seq_fail(s, ZSOLVE_ECUDA, "workspace: %s", cudaGetErrorString(e));
         return nullptr;
     }
+    s->ws = nullptr;
+    s->ws_bytes = 0;
+    s->ws_captured = false;
     if (cudaMalloc(&s->ws, bytes) != cudaSuccess) {
         cudaGetLastError();  // not sticky: the next call may fit
         s->ws = nullptr;
@@ -257,6 +269,7 @@ const char *zsolve_seq_last_error(const zsolve_seq *s) { return s ? s->err : "NU
 void zsolve_seq_destroy(zsolve_seq *s) {
     if (!s) return;
     cudaFree(s->ws);  // waits for the work in flight
+    for (void *p : s->retired) cudaFree(p);
     cudaFree(s->d_status);
     if (s->ev) cudaEventDestroy(s->ev);
     delete s;

@@ -8,6 +8,8 @@
 #include <cuda_runtime.h>
 #include <stdint.h>
 
+#include <vector>
+
 #include "zsolve.h"
 
 struct zsolve_seq {
@@ -15,6 +17,8 @@ struct zsolve_seq {
     cudaEvent_t ev = nullptr;  // orders the workspace's users when the stream changes
     void *ws = nullptr;
     size_t ws_bytes = 0;
+    bool ws_captured = false;      // a captured graph uses ws: it is kept until the handle goes
+    std::vector<void *> retired;   // such workspaces that a larger one took the place of
     int num_sms = 0;
     int dev = 0;
     int64_t launches = 0;

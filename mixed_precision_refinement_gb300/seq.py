@@ -51,7 +51,7 @@ def _rows(t, name, dtype=None, shape=None):
     if len(size) != 2:
         if not size:
             raise ValueError(f"{name}: expected rows of values")
-        t = t.view(-1, size[-1]) if t.numel() else t.reshape(-1, size[-1])
+        t = _flat(t, name)
         size = t.shape
     m, d = size
     if shape is not None and shape != (m, d):
@@ -60,6 +60,15 @@ def _rows(t, name, dtype=None, shape=None):
     if one != 1 and d > 1:
         raise ValueError(f"{name}: the values of a row must be contiguous")
     return t.data_ptr(), m, d, ld if m > 1 else max(d, 1)
+
+
+def _flat(t, name):
+    if not t.numel():
+        return t.reshape(-1, t.shape[-1])
+    try:
+        return t.view(-1, t.shape[-1])
+    except RuntimeError:
+        raise ValueError(f"{name}: the rows must lie at one distance") from None
 
 
 def _vector(t, name, n, dtype):
@@ -215,7 +224,10 @@ def _tokens(t, name, dtype=None, shape=None):
     if dtype is not None and t.dtype != dtype:
         raise TypeError(f"{name}: expected {dtype}, got {t.dtype}")
     if t.dim() == 4:
-        t = t.flatten(0, 1) if t.numel() == 0 else t.view((-1,) + t.shape[2:])
+        try:
+            t = t.flatten(0, 1) if t.numel() == 0 else t.view((-1,) + t.shape[2:])
+        except RuntimeError:
+            raise ValueError(f"{name}: the tokens must lie at one distance") from None
     if t.dim() != 3:
         raise ValueError(f"{name}: expected tokens x heads x values, got {tuple(t.shape)}")
     n, h, d = t.shape

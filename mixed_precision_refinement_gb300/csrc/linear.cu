@@ -35,12 +35,12 @@ constexpr int kThreads = 192;
 constexpr uint32_t kTmemCols = 512;
 constexpr uint32_t kWaitLimit = 1u << 19;  // try_wait polls before a wait gives up: about a second
 
-template <int BN>
+constexpr int BN = 128;       // columns of an output tile of one CTA
 struct Cfg {
     static constexpr int A_BYTES = BM * BK * 2;
     static constexpr int B_BYTES = BN * BK * 2;
     static constexpr int STAGE = A_BYTES + B_BYTES;
-    static constexpr int STAGES = BN == 256 ? 4 : 6;
+    static constexpr int STAGES = 6;
     static constexpr int SMEM = STAGES * STAGE + 1024;  // + alignment slack
 };
 
@@ -154,11 +154,11 @@ __device__ __forceinline__ TileAt tile_at(int t, int mt, int nt) {
     return x;
 }
 
-template <typename T, int BN, bool A_MN, bool B_MN>
+template <typename T, bool A_MN, bool B_MN>
 __global__ void __launch_bounds__(kThreads, 1)
 k_linear_tc(const __grid_constant__ CUtensorMap amap, const __grid_constant__ CUtensorMap bmap, int64_t M, int64_t N,
             int kblocks, int splits, const Epilogue epi, unsigned *__restrict__ status) {
-    using C = Cfg<BN>;
+    using C = Cfg;
     extern __shared__ uint8_t smem_raw[];
     __shared__ __align__(8) uint64_t bar_full[C::STAGES], bar_empty[C::STAGES], bar_accf[2], bar_acce[2], bar_drain;
     __shared__ uint32_t s_tmem;
@@ -323,6 +323,216 @@ k_linear_tc(const __grid_constant__ CUtensorMap amap, const __grid_constant__ CU
         asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(kTmemCols) : "memory");
 }
 
+// The same for large products on pairs of SMs (cta_group::2): a pair's MMA is 256
+// x 256 x 16, each CTA holds its 128 rows of A and of B and drains its 128 rows of
+// the result.  A CTA then stages 32 KB a k block for the 48 KB of a 128 x 256 tile
+// of its own, and shared memory, which feeds the MMAs and takes the copies, no
+// longer bounds the rate.  The leader's threads issue the MMAs and own the
+// barriers of full stages and of free accumulators; a stage's release and a
+// finished accumulator are told to both.
+constexpr int kPairStages = 6;
+constexpr int kPairStage = 2 * BM * BK * 2;  // A and B rows of one CTA
+constexpr int kPairSmem = kPairStages * kPairStage + 1024;
+
+__device__ __forceinline__ uint32_t cluster_addr(uint32_t addr, uint32_t rank) {
+    uint32_t r;
+    asm("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(r) : "r"(addr), "r"(rank));
+    return r;
+}
+__device__ __forceinline__ void mbar_arrive_remote(uint32_t cluster_bar) {
+    asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(cluster_bar) : "memory");
+}
+__device__ __forceinline__ void tma_load_2d_pair(uint32_t dst, const CUtensorMap *map, int c0, int c1, uint32_t cluster_bar) {
+    asm volatile(
+        "cp.async.bulk.tensor.2d.shared::cluster.global.tile.mbarrier::complete_tx::bytes.cta_group::2"
+        " [%0], [%1, {%2, %3}], [%4];" ::"r"(dst),
+        "l"((uint64_t)map), "r"(c0), "r"(c1), "r"(cluster_bar)
+        : "memory");
+}
+__device__ __forceinline__ void mma_f16_pair(uint32_t d_tmem, uint64_t a, uint64_t b, uint32_t idesc, uint32_t accumulate) {
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "setp.ne.b32 p, %4, 0;\n\t"
+        "tcgen05.mma.cta_group::2.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d_tmem),
+        "l"(a), "l"(b), "r"(idesc), "r"(accumulate)
+        : "memory");
+}
+// arrive on the barrier at this offset in both CTAs
+__device__ __forceinline__ void mma_commit_both(uint32_t bar) {
+    asm volatile(
+        "tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;" ::"r"(bar),
+        "h"((uint16_t)3)
+        : "memory");
+}
+__device__ __forceinline__ void mma_commit_pair(uint32_t bar) {
+    asm volatile("tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(bar) : "memory");
+}
+__device__ __forceinline__ void cluster_sync() {
+    asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
+    asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
+
+template <typename T, bool A_MN, bool B_MN>
+__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
+k_linear_pair(const __grid_constant__ CUtensorMap amap, const __grid_constant__ CUtensorMap bmap, int64_t M, int64_t N,
+              int kblocks, const Epilogue epi, unsigned *__restrict__ status) {
+    extern __shared__ uint8_t smem_raw[];
+    __shared__ __align__(8) uint64_t bar_full[kPairStages], bar_empty[kPairStages], bar_accf[2], bar_acce[2], bar_drain;
+    __shared__ uint32_t s_tmem;
+    __shared__ volatile int s_abort;
+    const uint32_t base = (smem_u32(smem_raw) + 1023u) & ~1023u;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const uint32_t rank = blockIdx.x & 1u;
+    const int mt = (int)((M + 2 * BM - 1) / (2 * BM)), nt = (int)((N + 255) / 256);
+    const int total = mt * nt, first = blockIdx.x >> 1, step = gridDim.x >> 1;
+    constexpr uint32_t fmt = std::is_same<T, bf16>::value ? 1u : 0u;
+    constexpr uint32_t idesc = (1u << 4) | (fmt << 7) | (fmt << 10) | ((A_MN ? 1u : 0u) << 15) |
+                               ((B_MN ? 1u : 0u) << 16) | ((uint32_t)(256 >> 3) << 17) | ((uint32_t)(256 >> 4) << 24);
+
+    if (threadIdx.x == 0) {
+        s_abort = 0;
+        for (int s = 0; s < kPairStages; s++) {
+            mbar_init(smem_u32(&bar_full[s]), 1);
+            mbar_init(smem_u32(&bar_empty[s]), 1);
+        }
+        for (int b = 0; b < 2; b++) {
+            mbar_init(smem_u32(&bar_accf[b]), 1);
+            mbar_init(smem_u32(&bar_acce[b]), 8);  // the epilogue warps of both CTAs
+        }
+        mbar_init(smem_u32(&bar_drain), 1);
+        asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+    }
+    if (warp == 1) {
+        asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(&s_tmem)),
+                     "r"(kTmemCols)
+                     : "memory");
+        asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;" ::: "memory");
+    }
+    tc_fence_before();
+    __syncthreads();
+    cluster_sync();  // both CTAs' barriers are there before anything arrives on them
+    tc_fence_after();
+    const uint32_t tmem = s_tmem;
+
+    if (warp == 0) {
+        // ------------------------------------------------ TMA producer, of its CTA's rows
+        if (lane == 0) {
+            asm volatile("prefetch.tensormap [%0];" ::"l"((uint64_t)&amap) : "memory");
+            asm volatile("prefetch.tensormap [%0];" ::"l"((uint64_t)&bmap) : "memory");
+            uint32_t g = 0;
+            bool ok = true;
+            for (int t = first; t < total && ok; t += step) {
+                const TileAt x = tile_at(t, mt, nt);
+                const int ra = x.tm * 2 * BM + (int)rank * BM, rb = x.tn * 256 + (int)rank * 128;
+                for (int kb = 0; kb < kblocks; kb++, g++) {
+                    const uint32_t st = g % kPairStages, ph = (g / kPairStages) & 1u;
+                    if (!mbar_wait(smem_u32(&bar_empty[st]), ph ^ 1u, &s_abort, status)) {
+                        ok = false;
+                        break;
+                    }
+                    const uint32_t own = smem_u32(&bar_full[st]), fb = cluster_addr(own, 0);
+                    if (rank == 0) mbar_expect_tx(own, 2 * kPairStage);
+                    const uint32_t sa = base + st * kPairStage, sb = sa + BM * BK * 2;
+#pragma unroll
+                    for (int i = 0; i < (A_MN ? 2 : 1); i++) {
+                        if (A_MN)
+                            tma_load_2d_pair(sa + i * kBox, &amap, ra + i * 64, kb * BK, fb);
+                        else
+                            tma_load_2d_pair(sa, &amap, kb * BK, ra, fb);
+                    }
+#pragma unroll
+                    for (int i = 0; i < (B_MN ? 2 : 1); i++) {
+                        if (B_MN)
+                            tma_load_2d_pair(sb + i * kBox, &bmap, rb + i * 64, kb * BK, fb);
+                        else
+                            tma_load_2d_pair(sb, &bmap, kb * BK, rb, fb);
+                    }
+                }
+            }
+            // the pair's copies in flight: the leader waits (bounded) for the last stages to land
+            if (rank == 0)
+                for (uint32_t q = g > (uint32_t)kPairStages ? g - kPairStages : 0; q < g; q++) {
+                    uint32_t it = 0;
+                    while (!mbar_try_wait(smem_u32(&bar_full[q % kPairStages]), (q / kPairStages) & 1u) && ++it < kWaitLimit) {
+                    }
+                }
+        }
+    } else if (warp == 1) {
+        // ------------------------------------------------ MMA issuer, of the pair
+        if (lane == 0 && rank == 0) {
+            uint32_t g = 0, it = 0;
+            bool ok = true;
+            for (int t = first; t < total && ok; t += step, it++) {
+                const uint32_t buf = it & 1u, aph = (it >> 1) & 1u;
+                if (!mbar_wait(smem_u32(&bar_acce[buf]), aph ^ 1u, &s_abort, status)) break;
+                tc_fence_after();
+                const uint32_t d = tmem + buf * 256u;
+                for (int kb = 0; kb < kblocks; kb++, g++) {
+                    const uint32_t st = g % kPairStages, ph = (g / kPairStages) & 1u;
+                    if (!mbar_wait(smem_u32(&bar_full[st]), ph, &s_abort, status)) {
+                        ok = false;
+                        break;
+                    }
+                    tc_fence_after();
+                    const uint32_t sa = base + st * kPairStage, sb = sa + BM * BK * 2;
+#pragma unroll
+                    for (int ks = 0; ks < BK / 16; ks++)
+                        mma_f16_pair(d, smem_desc<A_MN>(sa + ks * (A_MN ? 2048 : 32)),
+                                     smem_desc<B_MN>(sb + ks * (B_MN ? 2048 : 32)), idesc, (kb || ks) ? 1u : 0u);
+                    mma_commit_both(smem_u32(&bar_empty[st]));
+                }
+                if (!ok) break;
+                mma_commit_both(smem_u32(&bar_accf[buf]));
+            }
+            // every MMA issued so far completes before TMEM is freed
+            mma_commit_pair(smem_u32(&bar_drain));
+            uint32_t w = 0;
+            while (!mbar_try_wait(smem_u32(&bar_drain), 0) && ++w < kWaitLimit) {
+            }
+        }
+    } else {
+        // ------------------------------------------------ epilogue (warps 2-5), of its CTA's rows
+        const int quad = warp & 3;
+        uint32_t it = 0;
+        for (int t = first; t < total; t += step, it++) {
+            const TileAt x = tile_at(t, mt, nt);
+            const uint32_t buf = it & 1u, aph = (it >> 1) & 1u;
+            const bool ok = mbar_wait(smem_u32(&bar_accf[buf]), aph, &s_abort, status);
+            if (!__all_sync(0xffffffffu, ok)) break;
+            tc_fence_after();
+            const int64_t row = (int64_t)x.tm * 2 * BM + rank * BM + quad * 32 + lane;
+#pragma unroll 1
+            for (int c = 0; c < 8; c++) {
+                float v[32];
+                tmem_ld32(tmem + buf * 256u + (uint32_t)(c * 32) + ((uint32_t)(quad * 32) << 16), v);
+                if (c == 7) {  // accumulator fully read: hand it back to the leader's MMA warp
+                    tc_fence_before();
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive_remote(cluster_addr(smem_u32(&bar_acce[buf]), 0));
+                }
+                const int64_t col = (int64_t)x.tn * 256 + c * 32;
+                if (row >= M) continue;
+#pragma unroll
+                for (int j = 0; j < 4; j++) {
+                    const int64_t cj = col + j * 8;
+                    const int nc = (int)min((int64_t)8, N - cj);
+                    if (nc <= 0) break;
+                    float f[8];
+#pragma unroll
+                    for (int i = 0; i < 8; i++) f[i] = v[j * 8 + i];
+                    finish8<T>(epi, row, cj, nc, f);
+                }
+            }
+        }
+    }
+    tc_fence_before();
+    __syncthreads();
+    cluster_sync();  // neither CTA leaves while the other may still use its memory or barriers
+    tc_fence_after();
+    if (warp == 1)
+        asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(kTmemCols) : "memory");
+}
+
 // The parts of a product split along k, added in order, and the epilogue; a
 // thread for 8 columns of a row.
 template <typename T>
@@ -478,20 +688,22 @@ struct Mat {
     size_t packed_values() const { return (size_t)rows * ((cols + 7) / 8 * 8); }
 };
 
-// A product's tile width and parts along k.  256 columns give each operand
-// byte the most MMAs; 128 twice the tiles, where those of 256 would leave SMs
-// without one.  Parts are for what still leaves SMs idle, of 4 k blocks at
-// least, so that a part's loads outweigh the pass that joins them.
+// A product's tiles and parts along k.  Pairs of SMs on 256 x 256 tiles where
+// there is a tile for every pair (and rows of tiles enough that a half empty last
+// one does not matter), else single SMs on 128 x 128: four times the tiles.  Parts
+// are for what still leaves SMs idle, of 4 k blocks at least, so that a part's
+// loads outweigh the pass that joins them.
 struct Plan {
-    int bn, splits, kblocks;
+    bool pair;
+    int splits, kblocks;
 };
 Plan plan_of(int64_t M, int64_t N, int64_t K, int num_sms) {
     Plan p;
     const int64_t mt = (M + BM - 1) / BM;
     p.kblocks = (int)((K + BK - 1) / BK);
-    p.bn = mt * ((N + 255) / 256) >= num_sms ? 256 : 128;
-    const int64_t tiles = mt * ((N + p.bn - 1) / p.bn);
-    p.splits = (int)std::max<int64_t>(1, std::min<int64_t>({num_sms / tiles, p.kblocks / 4, 32}));
+    p.pair = (mt + 1) / 2 * ((N + 255) / 256) >= num_sms / 2 && (mt % 2 == 0 || mt >= 8);
+    const int64_t tiles = mt * ((N + BN - 1) / BN);
+    p.splits = p.pair ? 1 : (int)std::max<int64_t>(1, std::min<int64_t>({num_sms / tiles, p.kblocks / 4, 32}));
     return p;
 }
 int64_t ld_part(int64_t N) { return (N + 7) / 8 * 8; }
@@ -499,18 +711,26 @@ size_t part_values(int64_t M, int64_t N, const Plan &p) {
     return p.splits > 1 ? (size_t)p.splits * M * ld_part(N) : 0;
 }
 
-template <typename T, int BN, bool A_MN, bool B_MN>
+template <typename T, bool A_MN, bool B_MN>
 cudaError_t launch_tc(const CUtensorMap &a, const CUtensorMap &b, int64_t M, int64_t N, const Plan &p,
                       const Epilogue &epi, zsolve_seq *s) {
-    using C = Cfg<BN>;
-    // once per process (thread-safe initialisation of a local static)
+    s->launches++;
+    // attributes once per process (thread-safe initialisation of a local static)
+    if (p.pair) {
+        static const cudaError_t attr =
+            cudaFuncSetAttribute(k_linear_pair<T, A_MN, B_MN>, cudaFuncAttributeMaxDynamicSharedMemorySize, kPairSmem);
+        if (attr != cudaSuccess) return attr;
+        const int64_t total = (M + 2 * BM - 1) / (2 * BM) * ((N + 255) / 256);
+        const unsigned pairs = (unsigned)std::min<int64_t>(total, s->num_sms / 2);
+        k_linear_pair<T, A_MN, B_MN><<<2 * pairs, kThreads, kPairSmem, s->st>>>(a, b, M, N, p.kblocks, epi, s->d_status);
+        return cudaGetLastError();
+    }
     static const cudaError_t attr =
-        cudaFuncSetAttribute(k_linear_tc<T, BN, A_MN, B_MN>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM);
+        cudaFuncSetAttribute(k_linear_tc<T, A_MN, B_MN>, cudaFuncAttributeMaxDynamicSharedMemorySize, Cfg::SMEM);
     if (attr != cudaSuccess) return attr;
     const int64_t total = (M + BM - 1) / BM * ((N + BN - 1) / BN) * p.splits;
-    k_linear_tc<T, BN, A_MN, B_MN><<<(unsigned)std::min<int64_t>(total, s->num_sms), kThreads, C::SMEM, s->st>>>(
+    k_linear_tc<T, A_MN, B_MN><<<(unsigned)std::min<int64_t>(total, s->num_sms), kThreads, Cfg::SMEM, s->st>>>(
         a, b, M, N, p.kblocks, p.splits, epi, s->d_status);
-    s->launches++;
     return cudaGetLastError();
 }
 
@@ -521,13 +741,11 @@ cudaError_t product(zsolve_seq *s, int type, int64_t M, int64_t N, int64_t K, co
     const Plan p = plan_of(M, N, K, s->num_sms);
     CUtensorMap ma, mb;
     cudaError_t e = encode(&ma, type, A.p, A.rows, A.cols, A.ld, a_mn ? 64 : BM);
-    if (e == cudaSuccess) e = encode(&mb, type, B.p, B.rows, B.cols, B.ld, b_mn ? 64 : p.bn);
+    if (e == cudaSuccess) e = encode(&mb, type, B.p, B.rows, B.cols, B.ld, b_mn ? 64 : BN);
     if (e != cudaSuccess) return e;
     epi.part = p.splits > 1 ? part : nullptr;
     epi.ldp = ld_part(N);
-#define LIN_GO(AM, BMN)                                                           \
-    e = p.bn == 256 ? launch_tc<T, 256, AM, BMN>(ma, mb, M, N, p, epi, s)         \
-                    : launch_tc<T, 128, AM, BMN>(ma, mb, M, N, p, epi, s)
+#define LIN_GO(AM, BMN) e = launch_tc<T, AM, BMN>(ma, mb, M, N, p, epi, s)
     if (!a_mn && !b_mn) LIN_GO(false, false);
     else if (!a_mn) LIN_GO(false, true);
     else LIN_GO(true, true);

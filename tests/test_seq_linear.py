@@ -79,7 +79,8 @@ def _check(seq, m, n, k, dtype, act, bias=True, res=True, seed=0, pads=(0, 0, 0)
 
 
 SHAPES = [(1, 1, 1), (1, 8, 16), (3, 5, 7), (128, 128, 64), (129, 257, 65), (200, 130, 1000), (64, 1024, 2048),
-          (1000, 520, 72), (2, 40, 5000), (300, 2157, 331), (2500, 1500, 136), (4000, 2300, 64)]
+          (1000, 520, 72), (2, 40, 5000), (300, 2157, 331), (2500, 1500, 136), (4000, 2300, 64),
+          (2600, 3300, 1900)]
 
 
 @pytest.mark.gpu

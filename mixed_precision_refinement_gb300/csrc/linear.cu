@@ -580,8 +580,9 @@ k_linear_pack(const PackJob a, const PackJob b) {
 // (parts, one row of n a block row; NULL: not formed).  dz is rounded to the
 // inputs' type because it is the tensor cores' operand: it adds one rounding
 // of an input to each product's terms.
+constexpr int kDzBlocks = 4;  // of an SM
 template <typename T>
-__global__ void __launch_bounds__(256)
+__global__ void __launch_bounds__(256, kDzBlocks)
 k_linear_dz(const T *__restrict__ dy, int64_t lddy, const T *__restrict__ z, int64_t ldz, int act, int64_t m, int n,
             T *__restrict__ dz, int64_t ldo, float *__restrict__ parts, int vec) {
     __shared__ float red[8][32][9];
@@ -806,7 +807,11 @@ int linear_fwd(zsolve_seq *s, int type, int64_t m, int64_t n, int64_t k, Mat x, 
     return ZSOLVE_OK;
 }
 
-constexpr int kDzRows = 64;  // block rows of k_linear_dz at most: parts of db
+// Block rows of k_linear_dz, which are parts of db: as many blocks as the SMs hold at a time.
+int dz_rows(int64_t m, int64_t n, int num_sms) {
+    const int64_t most = std::max<int64_t>(1, (int64_t)num_sms * kDzBlocks / ((n + 255) / 256));
+    return (int)std::min<int64_t>({(m + 7) / 8, most, 1024});
+}
 
 template <typename T>
 int linear_bwd(zsolve_seq *s, int type, int64_t m, int64_t n, int64_t k, Mat dy, Mat x, Mat w, int act, Mat z, void *dx,
@@ -820,7 +825,7 @@ int linear_bwd(zsolve_seq *s, int type, int64_t m, int64_t n, int64_t k, Mat dy,
     const bool has_act = act != ACT_NONE;
     const bool products = dx || dw;
     const bool form_dz = products && (has_act || !dy.tma_ok());
-    const int dzrows = (int)std::min<int64_t>((m + 7) / 8, kDzRows);
+    const int dzrows = dz_rows(m, n, s->num_sms);
     const int64_t ldz8 = (n + 7) / 8 * 8;
     uint16_t *dzp = nullptr, *xp = nullptr, *wp = nullptr;
     float *part = nullptr, *sums = nullptr;

@@ -16,15 +16,14 @@ using namespace zs;
 // brought into that range one after the other, so that no later access leaves
 // the tensors.  One block: the sequences are few beside the tokens.
 __global__ void __launch_bounds__(1024)
-k_delta_plan(const int64_t *__restrict__ offsets, int nseq, int64_t tokens, int nchunks, int *__restrict__ first,
-             int2 *__restrict__ seq, int2 *__restrict__ chunk) {
+k_delta_plan(const int64_t *__restrict__ offsets, int nseq, int64_t tokens, int nchunks, int *first, int2 *seq,
+             int2 *chunk) {
     __shared__ int64_t s_end[32];
     __shared__ int s_sum[32];
     __shared__ int64_t s_carry;
     __shared__ int s_chunks;
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     if (threadIdx.x == 0) s_carry = 0, s_chunks = 0;
-    for (int i = threadIdx.x; i < nchunks; i += 1024) chunk[i] = make_int2(0, 0);
     __syncthreads();
     for (int base = 0; base < nseq; base += 1024) {
         const int i = base + threadIdx.x;
@@ -63,10 +62,6 @@ k_delta_plan(const int64_t *__restrict__ offsets, int nseq, int64_t tokens, int 
         if (i < nseq) {
             first[i] = at;
             seq[i] = make_int2((int)start, (int)(end - start));
-            for (int c = 0; c < n; c++) {
-                const int64_t left = end - start - (int64_t)c * kChunk;
-                chunk[at + c] = make_int2((int)start + c * kChunk, left < kChunk ? (int)left : kChunk);
-            }
         }
         __syncthreads();
         if (threadIdx.x == 1023) {
@@ -75,7 +70,27 @@ k_delta_plan(const int64_t *__restrict__ offsets, int nseq, int64_t tokens, int 
         }
         __syncthreads();
     }
-    if (threadIdx.x == 0) first[nseq] = s_chunks;
+    const int used = s_chunks;
+    if (threadIdx.x == 0) first[nseq] = used;
+    // a thread a chunk: its sequence is the last whose first chunk is not after it
+    // (among empty ones, which share their first chunk with the next)
+    for (int c = threadIdx.x; c < nchunks; c += 1024) {
+        int2 ch = make_int2(0, 0);
+        if (c < used) {
+            int lo = 0, hi = nseq;
+            while (hi - lo > 1) {
+                const int mid = (lo + hi) >> 1;
+                if (first[mid] <= c)
+                    lo = mid;
+                else
+                    hi = mid;
+            }
+            const int2 sq = seq[lo];
+            const int at = (c - first[lo]) * kChunk;
+            ch = make_int2(sq.x + at, min(sq.y - at, kChunk));
+        }
+        chunk[c] = ch;
+    }
 }
 
 // ---------------------------------------------------------------- terms

@@ -474,9 +474,10 @@ typedef struct zsolve_seq zsolve_seq;
 /* A handle on the current device. */
 int zsolve_seq_create(zsolve_seq **seq);
 
-/* Enqueue subsequent work on `stream` (a cudaStream_t; NULL = default stream).
- * Set during a stream capture, it does not wait for the handle's earlier
- * work: the caller has, before the capture began. */
+/* Enqueue subsequent work on `stream` (a cudaStream_t; NULL = default stream);
+ * the stream set before still exists.  Set during a stream capture, it does
+ * not wait for the handle's earlier work: the caller has, before the capture
+ * began. */
 int zsolve_seq_set_stream(zsolve_seq *seq, void *stream);
 
 /* Grow the workspace to at least `bytes`. */
@@ -559,8 +560,8 @@ typedef struct {
 
 /* o (tokens x hv x dv, token stride ldo) and the states after the last tokens,
  * s (as s0, and may be s0; NULL: not written).  In chunks of 64 tokens, whose
- * products run on the tensor cores at float32 accuracy (3xTF32; o itself, where
- * it is rounded to 16 bits, from tf32 products); sequences of a few tokens at
+ * products run on the tensor cores at float32 accuracy (3xTF32, or bfloat16 in
+ * three parts; bfloat16 o itself from fewer); sequences of a few tokens at
  * most go token by token (zsolve_delta_step). */
 int zsolve_delta(zsolve_seq *seq, const zsolve_delta_args *args, void *o, int64_t ldo, float *s);
 

@@ -269,12 +269,21 @@ k_delta_terms(const DeltaGeom geo, const DeltaTerms out) {
                             mma_split<false, false>(s.n[nn], y[k][kk],
                                                     *reinterpret_cast<const float2 *>(A + (i * 16 + nn * 8 + g) * kLdT + k * 16 + kk * 8 + 2 * t));
                 }
+                // T_ii is zero above its diagonal: an infinity or NaN of a token counts as
+                // zero there, and is put back in its own row (those after it have it from A)
                 Block z;
                 z.n[0].zero(), z.n[1].zero();
+                float sv[2][4];
 #pragma unroll
                 for (int kk = 0; kk < 2; kk++) {
+                    float neg[4];
+#pragma unroll
+                    for (int e = 0; e < 4; e++) {
+                        sv[kk][e] = s.n[kk].get(e);
+                        neg[e] = isfinite(sv[kk][e]) ? -sv[kk][e] : 0.f;
+                    }
                     SplitA a;
-                    a.set(-s.n[kk].get(0), -s.n[kk].get(1), -s.n[kk].get(2), -s.n[kk].get(3));
+                    a.set(neg);
 #pragma unroll
                     for (int nn = 0; nn < 2; nn++)
                         mma_split<false, false>(z.n[nn], a,
@@ -282,7 +291,9 @@ k_delta_terms(const DeltaGeom geo, const DeltaTerms out) {
                 }
 #pragma unroll
                 for (int nn = 0; nn < 2; nn++) {
-                    const float v[4] = {z.n[nn].get(0), z.n[nn].get(1), z.n[nn].get(2), z.n[nn].get(3)};
+                    float v[4];
+#pragma unroll
+                    for (int e = 0; e < 4; e++) v[e] = z.n[nn].get(e) + (sv[nn][e] - sv[nn][e]);
                     if (i < 3) y[i][nn].set(v);
 #pragma unroll
                     for (int e = 0; e < 4; e++)
@@ -333,9 +344,9 @@ struct ChainCfg {
     static constexpr int LD = tile_ld<T>(DK), LDV = tile_ld<T>(COLS);
     // two stages of the chunk's operands where they fit
     static constexpr int STAGES = sizeof(T) == 2 || DK == 64 ? 2 : 1;
-    // registers of a thread's S that the outputs need, in fours: two bfloat16
-    // parts, or the tf32 hi part, and for float32 outputs lo as well
-    static constexpr int NS = sizeof(T) == 2 ? 4 : 8;
+    // bfloat16 outputs come from two bfloat16 parts of S and from U and P in tf32:
+    // a quarter of their own rounding.  float16's would be as large as that rounding.
+    static constexpr bool HALF = std::is_same<T, bf16>::value;
 };
 template <bool OUT>
 constexpr int helpers() { return OUT ? 4 : 1; }
@@ -357,48 +368,64 @@ struct ChainSmem {
     float4 x[C::NV][16 * kLdPair];            // X^T
     float4 u[C::NV][16 * kLdPair];            // (e U)^T
     float2 un[C::NV][16 * kLdPair];           // U^T, for P U
-    uint4 s[C::NV][C::WK][C::NS][32];         // S^T, for Q S, as the lanes hold it
+    uint4 s[C::NV][C::WK][4][32];             // S^T, for Q S, as the lanes hold it
     T out[helpers<true>()][2][8 * 16];        // two tiles of outputs a helper
     uint64_t full[C::STAGES], empty[C::STAGES];
     uint64_t sfull[C::NV], sempty[C::NV], ufull[C::NV], uempty[C::NV];
+    uint32_t bad[C::NV][4];                   // a warp's part of U^T is not finite
     int abort_word;
 };
 
-// U as P U takes it: rounded to tf32 where o has 16 bits.
-template <typename T>
+// Element (v, token) of X^T and U^T as the groups leave them in shared memory.
+struct PairAt {
+    const float4 *x;
+    __device__ __forceinline__ float operator()(int v, int j) const {
+        const float *p = reinterpret_cast<const float *>(x + v * kLdPair + j / 2) + (j & 1);
+        return p[0] + p[2];
+    }
+};
+struct PlainAt {
+    const float2 *u;
+    __device__ __forceinline__ float operator()(int v, int j) const {
+        const float2 p = u[v * kLdPair + j / 2];
+        return j & 1 ? p.y : p.x;
+    }
+};
+
+// U as P U takes it.
+template <bool HALF>
 __device__ __forceinline__ float2 out_pair(float a, float b) {
-    return sizeof(T) == 2 ? make_float2(__uint_as_float(tf32(a)), __uint_as_float(tf32(b))) : make_float2(a, b);
+    return HALF ? make_float2(__uint_as_float(tf32(a)), __uint_as_float(tf32(b))) : make_float2(a, b);
 }
 
-// The parts of S^T that the outputs need, NS words of four registers.
-template <typename T, int NS>
-__device__ __forceinline__ void put_parts(uint4 (*dst)[32], const StateSplit<T> &s, int lane) {
+// A warp's block of S^T for the outputs, four words of four registers a lane:
+// bfloat16, two parts of each k step of 16; else the float32 values.
+template <typename T>
+__device__ __forceinline__ void put_parts(uint4 (*dst)[32], const StateSplit<T> &s, const float (&S)[4][4], int lane) {
 #pragma unroll
-    for (int i = 0; i < NS; i++) {
-        const uint32_t *r;
-        if constexpr (std::is_same<T, bf16>::value)
-            r = s.a[i >> 1].p[i & 1];
-        else if constexpr (sizeof(T) == 2)
-            r = s.a[i].hi;
-        else
-            r = i & 1 ? s.a[i >> 1].lo : s.a[i >> 1].hi;
-        dst[i][lane] = make_uint4(r[0], r[1], r[2], r[3]);
+    for (int i = 0; i < 4; i++) {
+        if constexpr (std::is_same<T, bf16>::value) {
+            const uint32_t(&r)[4] = s.a[i >> 1].p[i & 1];
+            dst[i][lane] = make_uint4(r[0], r[1], r[2], r[3]);
+        } else {
+            *reinterpret_cast<float4 *>(&dst[i][lane]) = make_float4(S[i][0], S[i][1], S[i][2], S[i][3]);
+        }
     }
 }
 
 // acc[i] += S^T Q^T at token tiles n[i] over one warp's 32 key columns
-template <typename T, int LD, int NS>
+template <typename T, int LD>
 __device__ __forceinline__ void parts_times_rows(const uint4 (*src)[32], const T *q, const int (&n)[2], int d0, int lane,
                                                  Acc (&acc)[2]) {
-    uint4 parts[NS];
+    uint4 parts[4];
 #pragma unroll
-    for (int i = 0; i < NS; i++) parts[i] = src[i][lane];
+    for (int i = 0; i < 4; i++) parts[i] = src[i][lane];
     if constexpr (std::is_same<T, bf16>::value) {
         uint32_t b[2][4];
 #pragma unroll
         for (int i = 0; i < 2; i++) ldmatrix4(b[i], q + (n[i] * 8 + (lane & 7)) * LD + d0 + 8 * (lane >> 3));
 #pragma unroll
-        for (int j = NS - 1; j >= 0; j--) {  // part j & 1 of k step j >> 1
+        for (int j = 3; j >= 0; j--) {  // part j & 1 of k step j >> 1
             const uint32_t a[4] = {parts[j].x, parts[j].y, parts[j].z, parts[j].w};
 #pragma unroll
             for (int i = 0; i < 2; i++) mma16(j & 1 ? acc[i].l : acc[i].c, a, b[i][2 * (j >> 1)], b[i][2 * (j >> 1) + 1]);
@@ -410,14 +437,9 @@ __device__ __forceinline__ void parts_times_rows(const uint4 (*src)[32], const T
 #pragma unroll
         for (int j = 0; j < 4; j++) {
             SplitA a;
-            const uint4 h = parts[sizeof(T) == 2 ? j : 2 * j];
-            a.hi[0] = h.x, a.hi[1] = h.y, a.hi[2] = h.z, a.hi[3] = h.w;
-            if (sizeof(T) == 4) {
-                const uint4 l = parts[(2 * j + 1) % NS];
-                a.lo[0] = l.x, a.lo[1] = l.y, a.lo[2] = l.z, a.lo[3] = l.w;
-            }
+            a.set(__uint_as_float(parts[j].x), __uint_as_float(parts[j].y), __uint_as_float(parts[j].z), __uint_as_float(parts[j].w));
 #pragma unroll
-            for (int i = 0; i < 2; i++) mma_split<false, sizeof(T) == 2, sizeof(T) == 2>(acc[i], a, b[i][j]);
+            for (int i = 0; i < 2; i++) mma_split<false, sizeof(T) == 2>(acc[i], a, b[i][j]);
         }
     }
 }
@@ -429,7 +451,7 @@ k_delta_chain(const DeltaGeom geo, const DeltaTerms terms, const float *__restri
               unsigned *__restrict__ status) {
     using C = ChainCfg<T, DK>;
     constexpr int WK = C::WK, NV = C::NV, LD = C::LD, LDV = C::LDV, NTILE = C::NTILE, NH = helpers<OUT>();
-    constexpr bool EXACT = sizeof(T) == 2;
+    constexpr bool HALF = C::HALF;
     extern __shared__ __align__(16) uint8_t smem_raw[];
     ChainSmem<T, DK> &sm = *reinterpret_cast<ChainSmem<T, DK> *>(smem_raw);
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g = lane >> 2, t = lane & 3;
@@ -494,7 +516,7 @@ k_delta_chain(const DeltaGeom geo, const DeltaTerms terms, const float *__restri
                 wait(&sm.sfull[grp], it);
                 const int n[2] = {tile_of<4>(hw, 0), tile_of<4>(hw, 1)};
 #pragma unroll
-                for (int w = 0; w < WK; w++) parts_times_rows<T, LD, C::NS>(sm.s[grp][w], st.q, n, 32 * w, lane, qs[grp]);
+                for (int w = 0; w < WK; w++) parts_times_rows<T, LD>(sm.s[grp][w], st.q, n, 32 * w, lane, qs[grp]);
                 __syncwarp();
                 if (lane == 0) bar_arrive(&sm.sempty[grp]);
             }
@@ -503,16 +525,28 @@ k_delta_chain(const DeltaGeom geo, const DeltaTerms terms, const float *__restri
             for (int grp = 0; grp < NV; grp++) {
                 wait(&sm.ufull[grp], it);
                 float oa[2][4];
-                triangular<4, true, false, EXACT>(
+                triangular<4, true, false, HALF>(
                     hw, oa,
                     [&](int k, SplitA &a) {
                         const float2 y = sm.un[grp][g * kLdPair + k * 4 + t], z = sm.un[grp][(g + 8) * kLdPair + k * 4 + t];
-                        if (EXACT)
+                        if (HALF)
                             a.hi[0] = __float_as_uint(y.x), a.hi[1] = __float_as_uint(z.x), a.hi[2] = __float_as_uint(y.y), a.hi[3] = __float_as_uint(z.y);
                         else
                             a.set(y.x, y.y, z.x, z.y);
                     },
                     [&](int k, int n) { return frag_p_earlier(st.tp, k, n); });
+                uint32_t bad = 0;
+#pragma unroll
+                for (int w = 0; w < WK; w++) bad |= sm.bad[grp][w];
+                if (bad && not_finite(oa)) {
+#pragma unroll
+                    for (int i = 0; i < 2; i++)
+#pragma unroll
+                        for (int e = 0; e < 4; e++)
+                            if (!isfinite(oa[i][e]))
+                                oa[i][e] = row_again<true>(PlainAt{sm.un[grp]}, st.tp, g + (e >> 1) * 8,
+                                                           tile_of<4>(hw, i) * 8 + 2 * t + (e & 1));
+                }
                 __syncwarp();
                 if (lane == 0) bar_arrive(&sm.uempty[grp]);
                 const int v0 = vb + grp * 16;
@@ -583,14 +617,14 @@ k_delta_chain(const DeltaGeom geo, const DeltaTerms terms, const float *__restri
         a.set(S);
         if (OUT) {
             wait(&sm.sempty[grp], it + 1);
-            put_parts<T, C::NS>(sm.s[grp][w], a, lane);
+            put_parts<T>(sm.s[grp][w], a, S, lane);
             __syncwarp();
             if (lane == 0) bar_arrive(&sm.sfull[grp]);
         }
         wait(&sm.full[stage], it / C::STAGES);
         ChainStage<T, DK> &st = sm.st[stage];
         const int64_t slot = (int64_t)c * geo.hv + hv;
-        if (states) put_state(states + slot * geo.dk * geo.dv);
+        if (!OUT) put_state(states + slot * geo.dk * geo.dv);
         group_sync<WK>(grp);  // the group is done with the previous chunk's exchanges
 
         // partial S^T K^T over the warp's key columns
@@ -644,10 +678,10 @@ k_delta_chain(const DeltaGeom geo, const DeltaTerms terms, const float *__restri
                 put_pair<T>(sm.u[grp] + at, ev.x * v[0], ev.y * v[1]);
                 put_pair<T>(sm.u[grp] + at + 8 * kLdPair, ev.x * v[2], ev.y * v[3]);
                 if (OUT) {
-                    sm.un[grp][at] = out_pair<T>(v[0], v[1]);
-                    sm.un[grp][at + 8 * kLdPair] = out_pair<T>(v[2], v[3]);
+                    sm.un[grp][at] = out_pair<HALF>(v[0], v[1]);
+                    sm.un[grp][at + 8 * kLdPair] = out_pair<HALF>(v[2], v[3]);
                 }
-                if (us) {
+                if (!OUT) {
 #pragma unroll
                     for (int e = 0; e < 4; e++) {
                         const int vc = v0 + g + (e >> 1) * 8;
@@ -655,7 +689,26 @@ k_delta_chain(const DeltaGeom geo, const DeltaTerms terms, const float *__restri
                     }
                 }
             }
+            // What an infinity or NaN of a later token made NaN is put right, one value at
+            // a time and from memory: from the registers and unrolled, this branch that is
+            // hardly ever taken took 10% of the loop (2230 us instead of 2003 at 32768
+            // tokens x 32 heads).  S' needs no repair: its value column is not finite
+            // either way.
+            const bool bad = not_finite(u);
+            if (bad) {
+#pragma unroll 1
+                for (int b = 0; b < 4 * NTILE; b++) {
+                    const int r = g + (b & 2) * 4, n = tile_of<WK>(w, b >> 2) * 8 + 2 * t + (b & 1);
+                    float *p = OUT ? reinterpret_cast<float *>(sm.un[grp]) + r * 2 * kLdPair + n
+                                   : us + (slot * kChunk + n) * geo.dv + v0 + r;
+                    if ((OUT || v0 + r < geo.dv) && !isfinite(*p)) {
+                        const float v = row_again<false>(PairAt{sm.x[grp]}, st.tp, r, n);
+                        *p = OUT ? out_pair<HALF>(v, v).x : v;
+                    }
+                }
+            }
             if (OUT) {
+                if (lane == 0) sm.bad[grp][w] = bad;
                 __syncwarp();
                 if (lane == 0) bar_arrive(&sm.ufull[grp]);
             }

@@ -121,16 +121,15 @@ struct Acc {
 };
 
 // acc += A B for one 16 x 8 x 8 step, b = (B(2t, g), B(2t+1, g)).  B_EXACT or
-// A_EXACT: that operand is exact in tf32; HALF: the hi parts alone (results
-// that are rounded to 16 bits).
-template <bool A_EXACT, bool B_EXACT, bool HALF = false>
+// A_EXACT: that operand is exact in tf32.
+template <bool A_EXACT, bool B_EXACT>
 __device__ __forceinline__ void mma_split(Acc &acc, const SplitA &a, float2 b) {
     uint32_t b0 = __float_as_uint(b.x), b1 = __float_as_uint(b.y);
     if (!B_EXACT) {
         b0 = tf32(b.x), b1 = tf32(b.y);
-        if (!HALF) mma8(acc.l, a.hi, tf32(b.x - __uint_as_float(b0)), tf32(b.y - __uint_as_float(b1)));
+        mma8(acc.l, a.hi, tf32(b.x - __uint_as_float(b0)), tf32(b.y - __uint_as_float(b1)));
     }
-    if (!A_EXACT && !HALF) mma8(acc.l, a.lo, b0, b1);
+    if (!A_EXACT) mma8(acc.l, a.lo, b0, b1);
     mma8(acc.c, a.hi, b0, b1);
 }
 
@@ -520,7 +519,9 @@ __device__ __forceinline__ void gate_sums(const DeltaGeom &geo, int2 ch, int hv,
         const double v = __shfl_up_sync(0xffffffffu, s, o);
         if (lane >= o) s += v;
     }
-    const double b0 = s - x[1], b1 = s;
+    double before = __shfl_up_sync(0xffffffffu, s, 1);
+    if (lane == 0) before = 0.0;
+    const double b0 = before + x[0], b1 = s;
     bh[2 * lane] = (float)b0, bl[2 * lane] = (float)(b0 - (double)(float)b0);
     bh[2 * lane + 1] = (float)b1, bl[2 * lane + 1] = (float)(b1 - (double)(float)b1);
 }
@@ -556,7 +557,8 @@ __device__ __forceinline__ void step_of(int w, int p, int s, int &k, int &n, boo
 }
 
 // x[2p], x[2p + 1] = the pair's results: sums of steps, each from zero and rounded
-// to nearest.  A(k): the step's A operand; B(k, n): its B operand; HALF: see mma_split.
+// to nearest.  A(k): the step's A operand; B(k, n): its B operand; HALF: the hi
+// parts alone.
 template <int WK, bool EARLIER, bool A_EXACT, bool HALF, typename FA, typename FB>
 __device__ __forceinline__ void triangular(int w, float (&x)[8 / WK][4], FA A, FB B) {
 #pragma unroll
@@ -590,6 +592,29 @@ __device__ __forceinline__ void triangular(int w, float (&x)[8 / WK][4], FA A, F
 #pragma unroll
         for (int e = 0; e < 4; e++) x[2 * p][e] = a0[e], x[2 * p + 1][e] = a1[e];
     }
+}
+
+// Whether any of the warp's values is an infinity or NaN.
+template <int N>
+__device__ __forceinline__ bool not_finite(const float (&x)[N][4]) {
+    uint32_t most = 0;
+#pragma unroll
+    for (int q = 0; q < N; q++)
+#pragma unroll
+        for (int e = 0; e < 4; e++) most = max(most, __float_as_uint(x[q][e]) & 0x7fffffffu);
+    return __any_sync(0xffffffffu, most >= 0x7f800000u);
+}
+
+// One value of a triangular product over earlier tokens once more: in a tile on the
+// diagonal that holds an infinity or NaN, the zeros above T's and P's diagonal have
+// made NaN of it for the tokens before it.  Row v, token i; xa(v, j): the other
+// operand; tp as frag_*_earlier reads it, P: of P, else of T.
+template <bool P, typename FX>
+__device__ __forceinline__ float row_again(FX xa, const float *tp, int v, int i) {
+    float sum = P ? 0.f : xa(v, i);
+#pragma unroll 1
+    for (int j = 0; j < (P ? i + 1 : i); j++) sum = fmaf(xa(v, j), P ? tp[j * kLdT + i] : tp[i * kLdT + j], sum);
+    return sum;
 }
 
 // The warps of one column group wait for each other.

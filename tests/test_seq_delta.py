@@ -248,6 +248,43 @@ def test_nonfinite_stays_in_its_sequence_and_head(seq):
     assert torch.isnan(s3[1, 1]).all() and torch.equal(s3[0], s[0])
 
 
+@pytest.mark.parametrize("dtype", ["float32", "bfloat16", "float16"])
+@pytest.mark.parametrize("value", [float("nan"), float("inf")])
+def test_nonfinite_values_reach_no_earlier_token(seq, dtype, value):
+    """A token's infinity or NaN is in what follows it alone, also within its chunk.  (The chunk may be
+    computed in another order because of it: both results lie within the tolerance of the exact one.)"""
+    torch = _torch()
+    x = _inputs([150], 1, 2, 64, 48, dtype, seed=18)
+    names = ("q", "k", "v", "g", "beta", "s0", "offsets")
+    scale = 0.125  # the call's own, 64 ** -0.5
+    ref, _, u_all, size = reference(**x, scale=scale)
+    tol = 2 * _o_tol(ref, u_all, x["offsets"], dtype, 3, size, scale)
+    o, _ = seq.delta(*(x[n] for n in names))
+
+    def same(a, where):
+        return bool(((a.double() - o.double()).abs() <= tol)[where].all())
+
+    for name in ("v", "k", "q", "g", "beta"):
+        for tok in (0, 5, 68, 80, 101, 149):
+            y = {n: t.clone() for n, t in x.items()}
+            if name in "vkq":
+                y[name][tok, 0, 7] = value
+            else:
+                y[name][tok, 0] = float("nan")
+            o2, s2 = seq.delta(*(y[n] for n in names))
+            assert same(o2, slice(0, tok)), (name, tok)
+            if name != "k" and name != "q":  # the other head
+                assert torch.equal(o2[:, 1], o[:, 1]), (name, tok)
+            if name == "v":  # column 7 from there on
+                others = [c for c in range(48) if c != 7]
+                assert not torch.isfinite(o2[tok, 0, 7]) and not torch.isfinite(s2[0, 0, :, 7]).any()
+                assert bool(((o2.double() - o.double()).abs() <= tol)[:, 0, others].all())
+            elif name == "q":
+                assert torch.equal(o2[tok + 1:], o[tok + 1:]) and not torch.isfinite(o2[tok]).any()
+            else:
+                assert not torch.isfinite(s2[0, 0]).any()
+
+
 def test_offsets_out_of_range_are_kept_within_the_tensors(seq):
     """Offsets that do not ascend or leave 0 .. tokens: what is written stays inside the outputs."""
     import mixed_precision_refinement_gb300 as zs

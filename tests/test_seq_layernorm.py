@@ -145,6 +145,18 @@ def test_no_weights_no_rows_constant_rows_and_nonfinite(seq):
 
 
 @pytest.mark.gpu
+@pytest.mark.parametrize("d", [200, 4096, 20000])
+def test_forward_in_place(seq, d):
+    import mixed_precision_refinement_gb300 as zs
+    torch = _torch()
+    x, w, b, _ = _inputs(9, d, torch.bfloat16, torch.float32, seed=12)
+    ref, _, _ = seq.layernorm(x, w, b)
+    y = x.clone()
+    zs.zsolve_layernorm(seq.seq, y, w, b, 1e-5, y)
+    assert torch.equal(y, ref)
+
+
+@pytest.mark.gpu
 def test_large_offset_keeps_the_variance(seq):
     torch = _torch()
     x = torch.randn(9, 1000, device="cuda") + 4096.0

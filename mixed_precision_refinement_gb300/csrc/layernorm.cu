@@ -362,7 +362,7 @@ k_layernorm_bwd_ring(const T *__restrict__ dy, int64_t lddy, const T *__restrict
         const T *xs = ring + 2 * slot * rr + offx, *ds = ring + (2 * slot + 1) * rr + offd;
         // values beyond the row count as zeros of dy
         float2 h[NP], a[NP], sx = make_float2(0.f, 0.f), sy = sx;
-        const float2 rs2 = make_float2(rs, rs), nm2 = make_float2(-mu * rs, -mu * rs);
+        const float2 rs2 = make_float2(rs, rs), nmu2 = make_float2(-mu, -mu);
         constexpr int G = VE > 1 ? VE : 2;  // values at a time
 #pragma unroll
         for (int i = 0; i < NI * VE / G; i++) {
@@ -394,7 +394,8 @@ k_layernorm_bwd_ring(const T *__restrict__ dy, int64_t lddy, const T *__restrict
             for (int e = 0; e < G / 2; e++) {
                 const int j = i * (G / 2) + e;
                 const float2 v = make_float2(af[2 * e], af[2 * e + 1]);
-                h[j] = fma2(make_float2(hf[2 * e], hf[2 * e + 1]), rs2, nm2);
+                // x - mu first: x rs - mu rs would lose the digits of a large offset
+                h[j] = mul2(add2(make_float2(hf[2 * e], hf[2 * e + 1]), nmu2), rs2);
                 aw[j] = fma2(v, h[j], aw[j]);
                 ab[j] = add2(v, ab[j]);
                 a[j] = w ? mul2(v, make_float2(wf[2 * e], wf[2 * e + 1])) : v;

@@ -167,6 +167,28 @@ def test_large_offset_keeps_the_variance(seq):
 
 
 @pytest.mark.gpu
+@pytest.mark.parametrize("rows,d", [(5, 1000), (2000, 1000), (2000, 1001), (700, 4096), (3, 20000)])
+def test_large_offset_keeps_the_gradient(seq, rows, d):
+    """With x and the mean on one grid, x - mean is exact: nothing is relative to the mean's size."""
+    torch = _torch()
+    gen = torch.Generator("cuda").manual_seed(d)
+    x, dy, w = (torch.randn(n, d, device="cuda", generator=gen) for n in (rows, rows, 1))
+    x, w = x + 4096.0, w[0]
+    mean = x.double().mean(1).float()
+    rstd = torch.rsqrt((x.double() - mean.double()[:, None]).square().mean(1)).float()
+    dx, dw, db = seq.layernorm_bwd(dy, x, mean, rstd, w)
+    h = (x.double() - mean.double()[:, None]) * rstd.double()[:, None]
+    a = dy.double() * w.double()
+    m1, m2 = a.mean(1, keepdim=True), (a * h).mean(1, keepdim=True)
+    ref = rstd.double()[:, None] * (a - m1 - h * m2)
+    terms = rstd.double()[:, None] * (a.abs() + a.abs().mean(1, keepdim=True) + h.abs() * (a * h).abs().mean(1, keepdim=True))
+    assert bool(((dx.double() - ref).abs() <= ADDS * U32 * terms + 1e-30).all())
+    # a column's sum: its rows' errors and those of a sum of `rows` terms, of random signs
+    t = dy.double() * h
+    assert bool(((dw.double() - t.sum(0)).abs() <= ADDS * U32 * t.abs().sum(0)).all())
+
+
+@pytest.mark.gpu
 @pytest.mark.parametrize("d", [48, 700])
 def test_gradient_against_differences(seq, d):
     """The directional derivative of sum(c * y) from values of the forward kernel at x +- h p and

@@ -372,10 +372,48 @@ __device__ __forceinline__ void cluster_sync() {
     asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
 }
 
-template <typename T, bool A_MN, bool B_MN>
+// One product, or two whose tiles are dealt together, so that the second fills the
+// SMs that the first's last round leaves idle (both gradients of 8192 x 4096 x 2048:
+// 193 us in two launches).
+enum { PAIR_FWD, PAIR_DX, PAIR_DW, PAIR_GRADS };  // x W^T, dz W, dz^T x, and the last two together
+struct PairSecond {
+    CUtensorMap a, b;
+    int64_t M, N;
+    int kblocks;
+    bool first_mn;  // A of the first product is stored k x M, that of this one M x k; or the reverse
+    int extra;      // tiles of the second that a pair of SMs takes for a tile of the first it has fewer
+    Epilogue epi;
+};
+// Tile i of pair p of the P, of products of t0 and t1 tiles: true, which product and
+// which of its tiles; or false
+template <bool TWO>
+__device__ __forceinline__ bool pair_tile(int t0, int t1, int extra, int p, int P, int i, int *job, int *tile) {
+    if (!TWO) {
+        *job = 0;
+        *tile = i * P + p;
+        return *tile < t0;
+    }
+    const int more = t0 % P, own = t0 / P + (p < more);
+    *job = i >= own;
+    if (i < own) {
+        *tile = i * P + p;
+        return true;
+    }
+    const int r = i - own, fewer = P - more;
+    if (p >= more && r < extra)
+        *tile = r * fewer + p - more;
+    else
+        *tile = extra * fewer + (r - (p >= more ? extra : 0)) * P + p;
+    return *tile < t1;
+}
+
+// FORM: which; the operands' orders and the one product's place are constants but for
+// PAIR_GRADS (read from the arguments for all of them, x W^T took 834 us for 758 at
+// 16384 x 8192 x 4096).
+template <typename T, int FORM>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
-k_linear_pair(const __grid_constant__ CUtensorMap amap, const __grid_constant__ CUtensorMap bmap, int64_t M, int64_t N,
-              int kblocks, const Epilogue epi, unsigned *__restrict__ status) {
+k_linear_pair(const __grid_constant__ CUtensorMap amap, const __grid_constant__ CUtensorMap bmap, int64_t M0, int64_t N0,
+              int kblocks0, const Epilogue epi0, const __grid_constant__ PairSecond two, unsigned *__restrict__ status) {
     extern __shared__ uint8_t smem_raw[];
     __shared__ __align__(8) uint64_t bar_full[kPairStages], bar_empty[kPairStages], bar_accf[2], bar_acce[2], bar_drain;
     __shared__ uint32_t s_tmem;
@@ -383,11 +421,18 @@ k_linear_pair(const __grid_constant__ CUtensorMap amap, const __grid_constant__ 
     const uint32_t base = (smem_u32(smem_raw) + 1023u) & ~1023u;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const uint32_t rank = blockIdx.x & 1u;
-    const int mt = (int)((M + 2 * BM - 1) / (2 * BM)), nt = (int)((N + 255) / 256);
-    const int total = mt * nt, first = blockIdx.x >> 1, step = gridDim.x >> 1;
+    const int pair = blockIdx.x >> 1, pairs = gridDim.x >> 1;
     constexpr uint32_t fmt = std::is_same<T, bf16>::value ? 1u : 0u;
-    constexpr uint32_t idesc = (1u << 4) | (fmt << 7) | (fmt << 10) | ((A_MN ? 1u : 0u) << 15) |
-                               ((B_MN ? 1u : 0u) << 16) | ((uint32_t)(256 >> 3) << 17) | ((uint32_t)(256 >> 4) << 24);
+    constexpr uint32_t shape = (1u << 4) | (fmt << 7) | (fmt << 10) | ((uint32_t)(256 >> 3) << 17) | ((uint32_t)(256 >> 4) << 24);
+    constexpr bool BOTH = FORM == PAIR_GRADS, b_mn = FORM != PAIR_FWD;
+    const int mt0 = (int)((M0 + 2 * BM - 1) / (2 * BM)), nt0 = (int)((N0 + 255) / 256);
+    const int mt1 = BOTH ? (int)((two.M + 2 * BM - 1) / (2 * BM)) : 0, nt1 = BOTH ? (int)((two.N + 255) / 256) : 0;
+    int job, tile;
+    auto next = [&](uint32_t i) {  // the pair's tile i, if there is one
+        return pair_tile<BOTH>(mt0 * nt0, mt1 * nt1, BOTH ? two.extra : 0, pair, pairs, (int)i, &job, &tile);
+    };
+    auto place = [&] { return BOTH && job ? tile_at(tile, mt1, nt1) : tile_at(tile, mt0, nt0); };
+    auto a_major = [&] { return BOTH ? two.first_mn == !job : FORM == PAIR_DW; };
 
     if (threadIdx.x == 0) {
         s_abort = 0;
@@ -421,8 +466,11 @@ k_linear_pair(const __grid_constant__ CUtensorMap amap, const __grid_constant__ 
             asm volatile("prefetch.tensormap [%0];" ::"l"((uint64_t)&bmap) : "memory");
             uint32_t g = 0;
             bool ok = true;
-            for (int t = first; t < total && ok; t += step) {
-                const TileAt x = tile_at(t, mt, nt);
+            for (uint32_t i = 0; ok && next(i); i++) {
+                const TileAt x = place();
+                const CUtensorMap *ma = BOTH && job ? &two.a : &amap, *mb = BOTH && job ? &two.b : &bmap;
+                const int kblocks = BOTH && job ? two.kblocks : kblocks0;
+                const bool a_mn = a_major();
                 const int ra = x.tm * 2 * BM + (int)rank * BM, rb = x.tn * 256 + (int)rank * 128;
                 for (int kb = 0; kb < kblocks; kb++, g++) {
                     const uint32_t st = g % kPairStages, ph = (g / kPairStages) & 1u;
@@ -433,19 +481,17 @@ k_linear_pair(const __grid_constant__ CUtensorMap amap, const __grid_constant__ 
                     const uint32_t own = smem_u32(&bar_full[st]), fb = cluster_addr(own, 0);
                     if (rank == 0) mbar_expect_tx(own, 2 * kPairStage);
                     const uint32_t sa = base + st * kPairStage, sb = sa + BM * BK * 2;
-#pragma unroll
-                    for (int i = 0; i < (A_MN ? 2 : 1); i++) {
-                        if (A_MN)
-                            tma_load_2d_pair(sa + i * kBox, &amap, ra + i * 64, kb * BK, fb);
-                        else
-                            tma_load_2d_pair(sa, &amap, kb * BK, ra, fb);
+                    if (a_mn) {
+                        tma_load_2d_pair(sa, ma, ra, kb * BK, fb);
+                        tma_load_2d_pair(sa + kBox, ma, ra + 64, kb * BK, fb);
+                    } else {
+                        tma_load_2d_pair(sa, ma, kb * BK, ra, fb);
                     }
-#pragma unroll
-                    for (int i = 0; i < (B_MN ? 2 : 1); i++) {
-                        if (B_MN)
-                            tma_load_2d_pair(sb + i * kBox, &bmap, rb + i * 64, kb * BK, fb);
-                        else
-                            tma_load_2d_pair(sb, &bmap, kb * BK, rb, fb);
+                    if (b_mn) {
+                        tma_load_2d_pair(sb, mb, rb, kb * BK, fb);
+                        tma_load_2d_pair(sb + kBox, mb, rb + 64, kb * BK, fb);
+                    } else {
+                        tma_load_2d_pair(sb, mb, kb * BK, rb, fb);
                     }
                 }
             }
@@ -462,7 +508,12 @@ k_linear_pair(const __grid_constant__ CUtensorMap amap, const __grid_constant__ 
         if (lane == 0 && rank == 0) {
             uint32_t g = 0, it = 0;
             bool ok = true;
-            for (int t = first; t < total && ok; t += step, it++) {
+            for (; ok && next(it); it++) {
+                const int kblocks = BOTH && job ? two.kblocks : kblocks0;
+                const bool a_mn = a_major();
+                const uint32_t idesc = shape | (a_mn ? 1u << 15 : 0u) | (b_mn ? 1u << 16 : 0u);
+                const uint64_t da = a_mn ? smem_desc<true>(0) : smem_desc<false>(0), db = b_mn ? smem_desc<true>(0) : smem_desc<false>(0);
+                const uint32_t step_a = a_mn ? 2048 : 32, step_b = b_mn ? 2048 : 32;
                 const uint32_t buf = it & 1u, aph = (it >> 1) & 1u;
                 if (!mbar_wait(smem_u32(&bar_acce[buf]), aph ^ 1u, &s_abort, status)) break;
                 tc_fence_after();
@@ -477,8 +528,8 @@ k_linear_pair(const __grid_constant__ CUtensorMap amap, const __grid_constant__ 
                     const uint32_t sa = base + st * kPairStage, sb = sa + BM * BK * 2;
 #pragma unroll
                     for (int ks = 0; ks < BK / 16; ks++)
-                        mma_f16_pair(d, smem_desc<A_MN>(sa + ks * (A_MN ? 2048 : 32)),
-                                     smem_desc<B_MN>(sb + ks * (B_MN ? 2048 : 32)), idesc, (kb || ks) ? 1u : 0u);
+                        mma_f16_pair(d, da | ((sa + ks * step_a) >> 4 & 0x3FFF), db | ((sb + ks * step_b) >> 4 & 0x3FFF), idesc,
+                                     (kb || ks) ? 1u : 0u);
                     mma_commit_both(smem_u32(&bar_empty[st]));
                 }
                 if (!ok) break;
@@ -494,8 +545,9 @@ k_linear_pair(const __grid_constant__ CUtensorMap amap, const __grid_constant__ 
         // ------------------------------------------------ epilogue (warps 2-5), of its CTA's rows
         const int quad = warp & 3;
         uint32_t it = 0;
-        for (int t = first; t < total; t += step, it++) {
-            const TileAt x = tile_at(t, mt, nt);
+        for (; next(it); it++) {
+            const TileAt x = place();
+            const int64_t M = BOTH && job ? two.M : M0, N = BOTH && job ? two.N : N0;
             const uint32_t buf = it & 1u, aph = (it >> 1) & 1u;
             const bool ok = mbar_wait(smem_u32(&bar_accf[buf]), aph, &s_abort, status);
             if (!__all_sync(0xffffffffu, ok)) break;
@@ -520,7 +572,7 @@ k_linear_pair(const __grid_constant__ CUtensorMap amap, const __grid_constant__ 
                     float f[8];
 #pragma unroll
                     for (int i = 0; i < 8; i++) f[i] = v[j * 8 + i];
-                    finish8<T>(epi, row, cj, nc, f);
+                    finish8<T>(BOTH && job ? two.epi : epi0, row, cj, nc, f);
                 }
             }
         }
@@ -715,45 +767,82 @@ size_t part_values(int64_t M, int64_t N, const Plan &p) {
 template <typename T, bool A_MN, bool B_MN>
 cudaError_t launch_tc(const CUtensorMap &a, const CUtensorMap &b, int64_t M, int64_t N, const Plan &p,
                       const Epilogue &epi, zsolve_seq *s) {
-    s->launches++;
     // attributes once per process (thread-safe initialisation of a local static)
-    if (p.pair) {
-        static const cudaError_t attr =
-            cudaFuncSetAttribute(k_linear_pair<T, A_MN, B_MN>, cudaFuncAttributeMaxDynamicSharedMemorySize, kPairSmem);
-        if (attr != cudaSuccess) return attr;
-        const int64_t total = (M + 2 * BM - 1) / (2 * BM) * ((N + 255) / 256);
-        const unsigned pairs = (unsigned)std::min<int64_t>(total, s->num_sms / 2);
-        k_linear_pair<T, A_MN, B_MN><<<2 * pairs, kThreads, kPairSmem, s->st>>>(a, b, M, N, p.kblocks, epi, s->d_status);
-        return cudaGetLastError();
-    }
     static const cudaError_t attr =
         cudaFuncSetAttribute(k_linear_tc<T, A_MN, B_MN>, cudaFuncAttributeMaxDynamicSharedMemorySize, Cfg::SMEM);
     if (attr != cudaSuccess) return attr;
     const int64_t total = (M + BM - 1) / BM * ((N + BN - 1) / BN) * p.splits;
     k_linear_tc<T, A_MN, B_MN><<<(unsigned)std::min<int64_t>(total, s->num_sms), kThreads, Cfg::SMEM, s->st>>>(
         a, b, M, N, p.kblocks, p.splits, epi, s->d_status);
+    s->launches++;
     return cudaGetLastError();
 }
 
 // D(i, j) = sum_k A(i, k) B(j, k) and the epilogue; a_mn: A is stored k x M, else M x k.
-template <typename T>
-cudaError_t product(zsolve_seq *s, int type, int64_t M, int64_t N, int64_t K, const Mat &A, bool a_mn, const Mat &B,
-                    bool b_mn, Epilogue epi, float *part) {
-    const Plan p = plan_of(M, N, K, s->num_sms);
+struct Product {
+    int64_t M, N, K;
+    Mat A, B;
+    bool a_mn, b_mn;
+    Epilogue epi;
+};
+
+cudaError_t maps(int type, const Product &p, CUtensorMap *a, CUtensorMap *b) {
+    const cudaError_t e = encode(a, type, p.A.p, p.A.rows, p.A.cols, p.A.ld, p.a_mn ? 64 : BM);
+    return e == cudaSuccess ? encode(b, type, p.B.p, p.B.rows, p.B.cols, p.B.ld, p.b_mn ? 64 : BN) : e;
+}
+
+// Products whose plan is pairs of SMs: one, or with PAIR_GRADS two; the longer sums
+// first, so that the last round is of short ones.
+template <typename T, int FORM>
+cudaError_t launch_pair(zsolve_seq *s, int type, const Product *p) {
+    static const cudaError_t attr =
+        cudaFuncSetAttribute(k_linear_pair<T, FORM>, cudaFuncAttributeMaxDynamicSharedMemorySize, kPairSmem);
+    if (attr != cudaSuccess) return attr;
+    constexpr int n = FORM == PAIR_GRADS ? 2 : 1;
+    const int first = n == 2 && p[1].K > p[0].K;
+    const Product &q = p[first];
     CUtensorMap ma, mb;
-    cudaError_t e = encode(&ma, type, A.p, A.rows, A.cols, A.ld, a_mn ? 64 : BM);
-    if (e == cudaSuccess) e = encode(&mb, type, B.p, B.rows, B.cols, B.ld, b_mn ? 64 : BN);
+    cudaError_t e = maps(type, q, &ma, &mb);
     if (e != cudaSuccess) return e;
-    epi.part = p.splits > 1 ? part : nullptr;
-    epi.ldp = ld_part(N);
-#define LIN_GO(AM, BMN) e = launch_tc<T, AM, BMN>(ma, mb, M, N, p, epi, s)
-    if (!a_mn && !b_mn) LIN_GO(false, false);
-    else if (!a_mn) LIN_GO(false, true);
+    auto tiles = [](const Product &p) { return (p.M + 2 * BM - 1) / (2 * BM) * ((p.N + 255) / 256); };
+    auto kblocks = [](const Product &p) { return (int)((p.K + BK - 1) / BK); };
+    int64_t total = tiles(q);
+    PairSecond two{};
+    if (n == 2) {
+        const Product &r = p[first ^ 1];
+        e = maps(type, r, &two.a, &two.b);
+        if (e != cudaSuccess) return e;
+        two.M = r.M, two.N = r.N, two.kblocks = kblocks(r);
+        two.first_mn = q.a_mn, two.epi = r.epi;
+        two.extra = kblocks(q) / kblocks(r);
+        total += tiles(r);
+    }
+    const unsigned pairs = (unsigned)std::min<int64_t>(total, s->num_sms / 2);
+    k_linear_pair<T, FORM><<<2 * pairs, kThreads, kPairSmem, s->st>>>(ma, mb, q.M, q.N, kblocks(q), q.epi, two, s->d_status);
+    s->launches++;
+    return cudaGetLastError();
+}
+
+template <typename T>
+cudaError_t product(zsolve_seq *s, int type, Product q, float *part) {
+    const Plan p = plan_of(q.M, q.N, q.K, s->num_sms);
+    if (p.pair)
+        return !q.b_mn  ? launch_pair<T, PAIR_FWD>(s, type, &q)
+               : q.a_mn ? launch_pair<T, PAIR_DW>(s, type, &q)
+                        : launch_pair<T, PAIR_DX>(s, type, &q);
+    CUtensorMap ma, mb;
+    cudaError_t e = maps(type, q, &ma, &mb);
+    if (e != cudaSuccess) return e;
+    q.epi.part = p.splits > 1 ? part : nullptr;
+    q.epi.ldp = ld_part(q.N);
+#define LIN_GO(AM, BMN) e = launch_tc<T, AM, BMN>(ma, mb, q.M, q.N, p, q.epi, s)
+    if (!q.a_mn && !q.b_mn) LIN_GO(false, false);
+    else if (!q.a_mn) LIN_GO(false, true);
     else LIN_GO(true, true);
 #undef LIN_GO
     if (e != cudaSuccess || p.splits == 1) return e;
-    const int64_t n8 = M * ((N + 7) / 8);
-    k_linear_join<T><<<(unsigned)((n8 + 255) / 256), 256, 0, s->st>>>(M, N, p.splits, epi);
+    const int64_t n8 = q.M * ((q.N + 7) / 8);
+    k_linear_join<T><<<(unsigned)((n8 + 255) / 256), 256, 0, s->st>>>(q.M, q.N, p.splits, q.epi);
     s->launches++;
     return cudaGetLastError();
 }
@@ -803,7 +892,7 @@ int linear_fwd(zsolve_seq *s, int type, int64_t m, int64_t n, int64_t k, Mat x, 
         carve(ws);
     }
     SEQ_CU(packed(s, &x, xp, &w, wp));
-    SEQ_CU(product<T>(s, type, m, n, k, x, false, w, false, epi, part));
+    SEQ_CU(product<T>(s, type, Product{m, n, k, x, w, false, false, epi}, part));
     return ZSOLVE_OK;
 }
 
@@ -861,14 +950,22 @@ int linear_bwd(zsolve_seq *s, int type, int64_t m, int64_t n, int64_t k, Mat dy,
     Mat dz = dy;
     if (form_dz) dz.p = dzp, dz.ld = ldz8;
     SEQ_CU(packed(s, &w, wp, &x, xp));
-    Epilogue epi{};
+    Product pr[2];
+    int np = 0;
     if (dx) {
+        Epilogue epi{};
         epi.y = dx, epi.ldy = lddx, epi.vec = vec8(dx, lddx);
-        SEQ_CU(product<T>(s, type, m, k, n, dz, false, w, true, epi, part));
+        pr[np++] = Product{m, k, n, dz, w, false, true, epi};
     }
     if (dw) {
+        Epilogue epi{};
         epi.y = dw, epi.ldy = lddw, epi.vec = vec8(dw, lddw);
-        SEQ_CU(product<T>(s, type, n, k, m, dz, true, x, true, epi, part));
+        pr[np++] = Product{n, k, m, dz, x, true, true, epi};
+    }
+    if (np == 2 && px.pair && pw.pair) {
+        SEQ_CU((launch_pair<T, PAIR_GRADS>(s, type, pr)));
+    } else {
+        for (int i = 0; i < np; i++) SEQ_CU(product<T>(s, type, pr[i], part));
     }
     return ZSOLVE_OK;
 }

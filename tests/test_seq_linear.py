@@ -180,6 +180,30 @@ def test_same_result_twice(seq):
 
 
 @pytest.mark.gpu
+@pytest.mark.parametrize("m,n,k", [(1024, 1032, 5000), (4100, 1030, 4100), (1030, 4100, 4100)])
+def test_both_gradients_in_one_launch(seq, m, n, k):
+    """Large products whose tiles are dealt together, with sums of the same and of different lengths; each as
+    it is alone."""
+    torch = _torch()
+    gen = torch.Generator("cuda").manual_seed(k)
+    x, w, dy = (_randn(gen, s, torch.bfloat16) for s in ((m, k), (n, k), (m, n)))
+    x, w, dy = (t.contiguous() for t in (x, w, dy))
+    import mixed_precision_refinement_gb300 as zs
+    both = torch.empty_like(x), torch.empty_like(w)
+    alone = torch.empty_like(x), torch.empty_like(w)
+    before = zs.zsolve_seq_launches(seq.seq)
+    zs.zsolve_linear_bwd(seq.seq, dy, x, w, "none", None, *both)
+    assert n % 8 or zs.zsolve_seq_launches(seq.seq) == before + 1
+    zs.zsolve_linear_bwd(seq.seq, dy, x, w, "none", None, alone[0], None)
+    zs.zsolve_linear_bwd(seq.seq, dy, x, w, "none", None, None, alone[1])
+    for got, one, ref, size in ((both[0], alone[0], dy.double() @ w.double(), dy.double().abs() @ w.double().abs()),
+                                (both[1], alone[1], dy.double().T @ x.double(), dy.double().abs().T @ x.double().abs())):
+        assert torch.equal(got, one)
+        # float32 sums of max(m, n) terms on the tensor cores, which cut instead of rounding, and one rounding
+        assert bool(((got.double() - ref).abs() <= max(m, n) * 2.0 ** -23 * size + 2.0 ** -8 * ref.abs()).all())
+
+
+@pytest.mark.gpu
 def test_some_gradients_only(seq):
     import mixed_precision_refinement_gb300 as zs
     torch = _torch()

@@ -575,7 +575,7 @@ int zsolve_delta_step(zsolve_seq *seq, const zsolve_delta_args *args, void *o, i
  * ds0: as s0 (NULL: not formed); all packed, key heads summed over the value
  * heads that share them in a fixed order.  The states are computed once more
  * from the inputs; the workspace holds them and their gradients at every 64th
- * token. */
+ * token.  The outputs overlap no input. */
 int zsolve_delta_bwd(zsolve_seq *seq, const zsolve_delta_args *args, const void *dout, int64_t lddo, const float *ds,
                      void *dq, void *dk, void *dv, float *dg, float *dbeta, float *ds0);
 

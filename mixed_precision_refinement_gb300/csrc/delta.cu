@@ -22,6 +22,8 @@ k_delta_plan(const int64_t *__restrict__ offsets, int nseq, int64_t tokens, int 
     __shared__ int s_sum[32];
     __shared__ int64_t s_carry;
     __shared__ int s_chunks;
+    after_previous();
+    may_start_next();
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     if (threadIdx.x == 0) s_carry = 0, s_chunks = 0;
     __syncthreads();
@@ -133,6 +135,8 @@ k_delta_terms(const DeltaGeom geo, const DeltaTerms out) {
     TermSmem<T, DK> &sm = *reinterpret_cast<TermSmem<T, DK> *>(smem_raw);
     constexpr bool EXACT = sizeof(T) == 2;
     constexpr int LD = tile_ld<T>(DK);
+    after_previous();
+    may_start_next();
     const int2 ch = geo.chunk[blockIdx.x];
     const int n = ch.y;
     if (n == 0) return;
@@ -312,6 +316,8 @@ k_delta_terms(const DeltaGeom geo, const DeltaTerms out) {
 template <typename T>
 __global__ void __launch_bounds__(256)
 k_delta_pack(const T *__restrict__ src, int64_t ld, int64_t tokens, int heads, int d, int dp, T *__restrict__ dst) {
+    after_previous();
+    may_start_next();
     const int64_t n = tokens * heads * dp;
     for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < n; i += (int64_t)gridDim.x * 256) {
         const int64_t row = i / dp, tok = row / heads;
@@ -340,7 +346,7 @@ struct ChainCfg {
     static constexpr int NV = DK == 32 ? 4 : 2;
     static constexpr int NC = 32 * WK * NV;  // threads of the groups
     static constexpr int NTILE = 8 / WK;
-    static constexpr int COLS = 16 * NV;
+    static constexpr int COLS = 16 * NV;  // delta_chain_blocks
     static constexpr int LD = tile_ld<T>(DK), LDV = tile_ld<T>(COLS);
     // two stages of the chunk's operands where they fit
     static constexpr int STAGES = sizeof(T) == 2 || DK == 64 ? 2 : 1;
@@ -457,6 +463,8 @@ k_delta_chain(const DeltaGeom geo, const DeltaTerms terms, const float *__restri
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g = lane >> 2, t = lane & 3;
     const int si = blockIdx.x / geo.hv, hv = blockIdx.x - si * geo.hv, hk = hv / (geo.hv / geo.hk);
     const int vb = (int)blockIdx.y * C::COLS;
+    after_previous();
+    may_start_next();
     const int c0 = geo.first[si], c1 = geo.first[si + 1];
 
     if (tid == 0) {
@@ -732,18 +740,17 @@ k_delta_chain(const DeltaGeom geo, const DeltaTerms terms, const float *__restri
 }
 
 template <typename T, int DK>
-cudaError_t terms_dk(const DeltaGeom &g, const DeltaTerms &t, cudaStream_t st) {
+cudaError_t terms_dk(const DeltaGeom &g, const DeltaTerms &t, bool next, cudaStream_t st) {
     const size_t smem = sizeof(TermSmem<T, DK>);
     static const cudaError_t attr = cudaFuncSetAttribute(
         k_delta_terms<T, DK>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)sizeof(TermSmem<T, DK>));
     if (attr != cudaSuccess) return attr;
-    k_delta_terms<T, DK><<<dim3(g.nchunks, g.hk), kTermThreads, smem, st>>>(g, t);
-    return cudaGetLastError();
+    return launch(next, k_delta_terms<T, DK>, dim3(g.nchunks, g.hk), kTermThreads, smem, st, g, t);
 }
 
 template <typename T, int DK>
 cudaError_t chain_dk(const DeltaGeom &g, const DeltaTerms &t, const float *s0, void *o, int64_t ldo, float *sn,
-                     float *states, float *us, unsigned *status, cudaStream_t st) {
+                     float *states, float *us, unsigned *status, bool next, cudaStream_t st) {
     using C = ChainCfg<T, DK>;
     static_assert(sizeof(ChainSmem<T, DK>) <= 232448, "shared memory of a block");
     const size_t smem = sizeof(ChainSmem<T, DK>);
@@ -752,15 +759,15 @@ cudaError_t chain_dk(const DeltaGeom &g, const DeltaTerms &t, const float *s0, v
         static const cudaError_t attr = cudaFuncSetAttribute(
             k_delta_chain<T, DK, true>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)sizeof(ChainSmem<T, DK>));
         if (attr != cudaSuccess) return attr;
-        k_delta_chain<T, DK, true><<<grid, C::NC + 32 * helpers<true>(), smem, st>>>(g, t, s0, (T *)o, ldo, sn, states, us,
-                                                                    mult16(o, ldo, g.dv, sizeof(T)), status);
+        return launch(next, k_delta_chain<T, DK, true>, grid, C::NC + 32 * helpers<true>(), smem, st, g, t, s0, (T *)o, ldo, sn,
+                      states, us, (int)mult16(o, ldo, g.dv, sizeof(T)), status);
     } else {
         static const cudaError_t attr = cudaFuncSetAttribute(
             k_delta_chain<T, DK, false>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)sizeof(ChainSmem<T, DK>));
         if (attr != cudaSuccess) return attr;
-        k_delta_chain<T, DK, false><<<grid, C::NC + 32 * helpers<false>(), smem, st>>>(g, t, s0, nullptr, 0, sn, states, us, 0, status);
+        return launch(next, k_delta_chain<T, DK, false>, grid, C::NC + 32 * helpers<false>(), smem, st, g, t, s0, (T *)nullptr,
+                      (int64_t)0, sn, states, us, 0, status);
     }
-    return cudaGetLastError();
 }
 
 }  // namespace
@@ -784,15 +791,15 @@ cudaError_t zs_launch_delta_pack(int type, const void *src, int64_t ld, int64_t 
     return cudaGetLastError();
 }
 
-cudaError_t zs_launch_delta_terms(int type, const DeltaGeom &g, const DeltaTerms &t, cudaStream_t st,
+cudaError_t zs_launch_delta_terms(int type, const DeltaGeom &g, const DeltaTerms &t, bool next, cudaStream_t st,
                                   int64_t *launches) {
     ++*launches;
-    return DELTA_TYPE(terms_dk, g, t, st);
+    return DELTA_TYPE(terms_dk, g, t, next, st);
 }
 
 cudaError_t zs_launch_delta_chain(int type, const DeltaGeom &g, const DeltaTerms &t, const float *s0, void *o,
-                                  int64_t ldo, float *sn, float *states, float *us, unsigned *status, cudaStream_t st,
-                                  int64_t *launches) {
+                                  int64_t ldo, float *sn, float *states, float *us, unsigned *status, bool next,
+                                  cudaStream_t st, int64_t *launches) {
     ++*launches;
-    return DELTA_TYPE(chain_dk, g, t, s0, o, ldo, sn, states, us, status, st);
+    return DELTA_TYPE(chain_dk, g, t, s0, o, ldo, sn, states, us, status, next, st);
 }

@@ -642,35 +642,42 @@ inline bool mult16(const void *p, int64_t ld, int64_t d, size_t e) {
 
 // ---------------------------------------------------------------- launchers
 
+// next: the launch before on the stream is of the same call (seq.cuh).
+
 // delta.cu
 cudaError_t zs_launch_delta_plan(const int64_t *offsets, int nseq, int64_t tokens, int nchunks, int *first, int2 *seq,
                                  int2 *chunk, cudaStream_t st, int64_t *launches);
 // tokens x heads x d values at token stride ld into packed heads of dp values
 cudaError_t zs_launch_delta_pack(int type, const void *src, int64_t ld, int64_t tokens, int heads, int d, int dp,
                                  void *dst, int num_sms, cudaStream_t st, int64_t *launches);
-cudaError_t zs_launch_delta_terms(int type, const zs::DeltaGeom &g, const zs::DeltaTerms &t, cudaStream_t st,
+cudaError_t zs_launch_delta_terms(int type, const zs::DeltaGeom &g, const zs::DeltaTerms &t, bool next, cudaStream_t st,
                                   int64_t *launches);
 // The recurrence over the chunks.  o (NULL: not formed), sn (the last states;
 // NULL: not written); states, us (NULL: not kept): the state each chunk
 // starts from (per chunk and value head dk x dv) and U (64 x dv).  status: a
 // word that a bounded wait sets when it gives up.
 cudaError_t zs_launch_delta_chain(int type, const zs::DeltaGeom &g, const zs::DeltaTerms &t, const float *s0, void *o,
-                                  int64_t ldo, float *sn, float *states, float *us, unsigned *status, cudaStream_t st,
-                                  int64_t *launches);
+                                  int64_t ldo, float *sn, float *states, float *us, unsigned *status, bool next,
+                                  cudaStream_t st, int64_t *launches);
 // The recurrence backwards (delta_bwd.cu): from the gradients of o and of the
 // last states (ds; NULL: zero), per chunk and value head the gradient of the
 // state after the chunk (dends, dk x dv) and dX (64 x dv), dv, and the
 // gradient of the first states (ds0; NULL: not written).
 cudaError_t zs_launch_delta_rchain(int type, const zs::DeltaGeom &g, const zs::DeltaTerms &t, const void *dout,
                                    int64_t lddo, const float *ds, float *dends, float *dxs, void *dv, float *ds0,
-                                   unsigned *status, cudaStream_t st, int64_t *launches);
+                                   unsigned *status, bool next, cudaStream_t st, int64_t *launches);
+// The blocks of either recurrence.
+inline int64_t delta_chain_blocks(const zs::DeltaGeom &g) {
+    const int cols = g.dk <= 32 ? 64 : 32;
+    return (int64_t)g.nseq * g.hv * ((g.dv + cols - 1) / cols);
+}
 // The gradients that the chunks give on their own.  parts (tokens x hv x dk
 // float32, one for dq and one for dk) are needed where value heads share a key
 // head; dq, dk: tokens x hk x dk.
 cudaError_t zs_launch_delta_grads(int type, const zs::DeltaGeom &g, const zs::DeltaTerms &t, const void *dout,
                                   int64_t lddo, const float *states, const float *dends, const float *us,
                                   const float *dxs, float *dqp, float *dkp, void *dq, void *dk, float *dg,
-                                  float *dbeta, cudaStream_t st, int64_t *launches);
+                                  float *dbeta, bool next, cudaStream_t st, int64_t *launches);
 // Token by token (delta_step.cu): every sequence's tokens one after the other.
 cudaError_t zs_launch_delta_step(int type, const zs::DeltaGeom &g, const int64_t *offsets, const float *s0, void *o,
                                  int64_t ldo, float *sn, cudaStream_t st, int64_t *launches);

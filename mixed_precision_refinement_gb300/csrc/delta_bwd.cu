@@ -73,6 +73,8 @@ k_delta_rchain(const DeltaGeom geo, const DeltaTerms terms, const T *__restrict_
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g = lane >> 2, t = lane & 3;
     const int si = blockIdx.x / geo.hv, hv = blockIdx.x - si * geo.hv, hk = hv / (geo.hv / geo.hk);
     const int vb = (int)blockIdx.y * C::COLS;
+    after_previous();
+    may_start_next();
     const int cols = min(C::COLS, geo.dvp - vb);  // of the block's dO
     const int c0 = geo.first[si], c1 = geo.first[si + 1];
 
@@ -369,6 +371,8 @@ k_delta_grads(const DeltaGeom geo, const DeltaTerms terms, const T *__restrict__
     constexpr bool EXACT = sizeof(T) == 2;
     extern __shared__ __align__(16) uint8_t smem_raw[];
     GradSmem<T, DK> &sm = *reinterpret_cast<GradSmem<T, DK> *>(smem_raw);
+    after_previous();
+    may_start_next();
     const int2 ch = geo.chunk[blockIdx.x];
     const int n = ch.y;
     if (n == 0) return;
@@ -673,6 +677,7 @@ template <typename T>
 __global__ void __launch_bounds__(256)
 k_delta_join(const float *__restrict__ dqp, const float *__restrict__ dkp, int64_t n, int group, int dk_,
              T *__restrict__ dq, T *__restrict__ dk) {
+    after_previous();
     for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < n; i += (int64_t)gridDim.x * 256) {
         const int64_t head = i / dk_, d = i - head * dk_;
         const int64_t at = head * group * dk_ + d;
@@ -688,57 +693,54 @@ k_delta_join(const float *__restrict__ dqp, const float *__restrict__ dkp, int64
 
 template <typename T, int DK>
 cudaError_t rchain_dk(const DeltaGeom &g, const DeltaTerms &t, const void *dout, int64_t lddo, const float *ds,
-                      float *dends, float *dxs, void *dv, float *ds0, unsigned *status, cudaStream_t st) {
+                      float *dends, float *dxs, void *dv, float *ds0, unsigned *status, bool next, cudaStream_t st) {
     using C = RChainCfg<T, DK>;
     static_assert(sizeof(RChainSmem<T, DK>) <= 232448, "shared memory of a block");
     static const cudaError_t attr = cudaFuncSetAttribute(
         k_delta_rchain<T, DK>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)sizeof(RChainSmem<T, DK>));
     if (attr != cudaSuccess) return attr;
     const dim3 grid((unsigned)(g.nseq * g.hv), (unsigned)((g.dv + C::COLS - 1) / C::COLS));
-    k_delta_rchain<T, DK><<<grid, C::NT, sizeof(RChainSmem<T, DK>), st>>>(g, t, (const T *)dout, lddo, ds, dends, dxs,
-                                                                          (T *)dv, ds0, status);
-    return cudaGetLastError();
+    return launch(next, k_delta_rchain<T, DK>, grid, C::NT, sizeof(RChainSmem<T, DK>), st, g, t, (const T *)dout, lddo, ds, dends,
+                  dxs, (T *)dv, ds0, status);
 }
 
 template <typename T, int DK>
 cudaError_t grads_dk(const DeltaGeom &g, const DeltaTerms &t, const void *dout, int64_t lddo, const float *states,
                      const float *dends, const float *us, const float *dxs, float *dqp, float *dkp, void *dq, void *dk,
-                     float *dg, float *dbeta, cudaStream_t st) {
+                     float *dg, float *dbeta, bool next, cudaStream_t st) {
     using C = GradCfg<T, DK>;
     static_assert(sizeof(GradSmem<T, DK>) <= 232448, "shared memory of a block");
     static const cudaError_t attr = cudaFuncSetAttribute(
         k_delta_grads<T, DK>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)sizeof(GradSmem<T, DK>));
     if (attr != cudaSuccess) return attr;
-    k_delta_grads<T, DK><<<dim3(g.nchunks, g.hv), C::NT, sizeof(GradSmem<T, DK>), st>>>(
-        g, t, (const T *)dout, lddo, states, dends, us, dxs, dqp, dkp, (T *)dq, (T *)dk, dg, dbeta, g.dv % 4 == 0);
-    return cudaGetLastError();
+    return launch(next, k_delta_grads<T, DK>, dim3(g.nchunks, g.hv), C::NT, sizeof(GradSmem<T, DK>), st, g, t, (const T *)dout,
+                  lddo, states, dends, us, dxs, dqp, dkp, (T *)dq, (T *)dk, dg, dbeta, (int)(g.dv % 4 == 0));
 }
 
 }  // namespace
 
 cudaError_t zs_launch_delta_rchain(int type, const DeltaGeom &g, const DeltaTerms &t, const void *dout, int64_t lddo,
                                    const float *ds, float *dends, float *dxs, void *dv, float *ds0, unsigned *status,
-                                   cudaStream_t st, int64_t *launches) {
+                                   bool next, cudaStream_t st, int64_t *launches) {
     ++*launches;
-    return DELTA_TYPE(rchain_dk, g, t, dout, lddo, ds, dends, dxs, dv, ds0, status, st);
+    return DELTA_TYPE(rchain_dk, g, t, dout, lddo, ds, dends, dxs, dv, ds0, status, next, st);
 }
 
 cudaError_t zs_launch_delta_grads(int type, const DeltaGeom &g, const DeltaTerms &t, const void *dout, int64_t lddo,
                                   const float *states, const float *dends, const float *us, const float *dxs,
-                                  float *dqp, float *dkp, void *dq, void *dk, float *dg, float *dbeta, cudaStream_t st,
-                                  int64_t *launches) {
+                                  float *dqp, float *dkp, void *dq, void *dk, float *dg, float *dbeta, bool next,
+                                  cudaStream_t st, int64_t *launches) {
     ++*launches;
-    cudaError_t e = DELTA_TYPE(grads_dk, g, t, dout, lddo, states, dends, us, dxs, dqp, dkp, dq, dk, dg, dbeta, st);
+    cudaError_t e = DELTA_TYPE(grads_dk, g, t, dout, lddo, states, dends, us, dxs, dqp, dkp, dq, dk, dg, dbeta, next, st);
     if (e != cudaSuccess || !dqp) return e;
     const int64_t n = g.tokens * g.hk * g.dk;
     const unsigned blocks = (unsigned)std::min<int64_t>((n + 255) / 256, 152 * 16);
     const int group = g.hv / g.hk;
     ++*launches;
-    if (type == ZSOLVE_F32)
-        k_delta_join<float><<<blocks, 256, 0, st>>>(dqp, dkp, n, group, g.dk, (float *)dq, (float *)dk);
-    else if (type == ZSOLVE_BF16)
-        k_delta_join<bf16><<<blocks, 256, 0, st>>>(dqp, dkp, n, group, g.dk, (bf16 *)dq, (bf16 *)dk);
-    else
-        k_delta_join<f16><<<blocks, 256, 0, st>>>(dqp, dkp, n, group, g.dk, (f16 *)dq, (f16 *)dk);
-    return cudaGetLastError();
+    auto join = [&](auto kernel, auto *q, auto *k) {
+        return launch(true, kernel, blocks, 256, 0, st, (const float *)dqp, (const float *)dkp, n, group, g.dk, q, k);
+    };
+    return type == ZSOLVE_F32    ? join(k_delta_join<float>, (float *)dq, (float *)dk)
+           : type == ZSOLVE_BF16 ? join(k_delta_join<bf16>, (bf16 *)dq, (bf16 *)dk)
+                                 : join(k_delta_join<f16>, (f16 *)dq, (f16 *)dk);
 }

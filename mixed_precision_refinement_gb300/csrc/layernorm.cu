@@ -310,6 +310,7 @@ k_layernorm_bwd_ring(const T *__restrict__ dy, int64_t lddy, const T *__restrict
     __shared__ __align__(8) uint64_t full[kRing];
     __shared__ volatile int s_abort;
     T *ring = reinterpret_cast<T *>(smem_raw);
+    may_start_next();
     const int rr = ring_row<T>(d), t = threadIdx.x;
     void *ws = ring + 2 * kRing * rr;  // w, read again for every row
     if (w)
@@ -490,11 +491,14 @@ __global__ void __launch_bounds__(1024)
 k_layernorm_bwd_sum(const float *__restrict__ parts, int64_t nparts, int64_t d, int wf32, void *__restrict__ dw,
                     void *__restrict__ db) {
     __shared__ float tile[32][33];
+    after_previous();
     const int tx = threadIdx.x & 31, ty = threadIdx.x >> 5;
     const int64_t c = (int64_t)blockIdx.x * 32 + tx;  // column of [dw | db]
     float s = 0.f;
-    if (c < 2 * d)
+    if (c < 2 * d) {
+#pragma unroll 8
         for (int64_t p = ty; p < nparts; p += 32) s += parts[p * 2 * d + c];
+    }
     tile[ty][tx] = s;
     __syncthreads();
     const float v = warp_sum(tile[tx][ty]);
@@ -633,8 +637,8 @@ cudaError_t bwd(int64_t rows, int64_t d, const void *dy, int64_t lddy, const voi
         nparts = blocks * (bwd_tpr(d) == 32 ? 4 : 1);
     }
     if (sums) {
-        k_layernorm_bwd_sum<T><<<(unsigned)((2 * d + 31) / 32), 1024, 0, st>>>(parts, nparts, d, wf32, dw, db);
         ++*launches;
+        return launch(nparts > 0, k_layernorm_bwd_sum<T>, (unsigned)((2 * d + 31) / 32), 1024, 0, st, parts, nparts, d, wf32, dw, db);
     }
     return cudaGetLastError();
 }

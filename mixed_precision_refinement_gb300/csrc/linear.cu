@@ -194,6 +194,8 @@ k_linear_tc(const __grid_constant__ CUtensorMap amap, const __grid_constant__ CU
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
+    after_previous();
+    may_start_next();
     const uint32_t tmem = s_tmem;
     // k blocks of split s: an equal share, the first ones one more
     auto kfirst = [&](int s) { return (int)((int64_t)kblocks * s / splits); };
@@ -457,6 +459,8 @@ k_linear_pair(const __grid_constant__ CUtensorMap amap, const __grid_constant__ 
     __syncthreads();
     cluster_sync();  // both CTAs' barriers are there before anything arrives on them
     tc_fence_after();
+    after_previous();
+    may_start_next();
     const uint32_t tmem = s_tmem;
 
     if (warp == 0) {
@@ -590,6 +594,8 @@ k_linear_pair(const __grid_constant__ CUtensorMap amap, const __grid_constant__ 
 template <typename T>
 __global__ void __launch_bounds__(256)
 k_linear_join(int64_t M, int64_t N, int splits, const Epilogue epi) {
+    after_previous();
+    may_start_next();
     const int64_t groups = (N + 7) / 8;
     const int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x;
     if (i >= M * groups) return;
@@ -614,6 +620,8 @@ struct PackJob {
 };
 __global__ void __launch_bounds__(256)
 k_linear_pack(const PackJob a, const PackJob b) {
+    after_previous();
+    may_start_next();
     const PackJob &j = blockIdx.y ? b : a;
     const int64_t ldd = (j.cols + 7) / 8 * 8, groups = ldd / 8;
     for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < j.rows * groups; i += (int64_t)gridDim.x * 256) {
@@ -638,6 +646,8 @@ __global__ void __launch_bounds__(256, kDzBlocks)
 k_linear_dz(const T *__restrict__ dy, int64_t lddy, const T *__restrict__ z, int64_t ldz, int act, int64_t m, int n,
             T *__restrict__ dz, int64_t ldo, float *__restrict__ parts, int vec) {
     __shared__ float red[8][32][9];
+    after_previous();
+    may_start_next();
     const int tx = threadIdx.x & 31, ty = threadIdx.x >> 5;
     const int64_t c = ((int64_t)blockIdx.x * 32 + tx) * 8;
     const int nc = (int)min((int64_t)8, (int64_t)n - c);
@@ -690,6 +700,8 @@ template <typename T>
 __global__ void __launch_bounds__(256)
 k_linear_db(const float *__restrict__ parts, int nparts, int n, T *__restrict__ db) {
     __shared__ float red[8][32];
+    after_previous();
+    may_start_next();
     const int tx = threadIdx.x & 31, ty = threadIdx.x >> 5;
     const int c = blockIdx.x * 32 + tx;
     float s = 0.f;
@@ -766,16 +778,15 @@ size_t part_values(int64_t M, int64_t N, const Plan &p) {
 
 template <typename T, bool A_MN, bool B_MN>
 cudaError_t launch_tc(const CUtensorMap &a, const CUtensorMap &b, int64_t M, int64_t N, const Plan &p,
-                      const Epilogue &epi, zsolve_seq *s) {
+                      const Epilogue &epi, bool next, zsolve_seq *s) {
     // attributes once per process (thread-safe initialisation of a local static)
     static const cudaError_t attr =
         cudaFuncSetAttribute(k_linear_tc<T, A_MN, B_MN>, cudaFuncAttributeMaxDynamicSharedMemorySize, Cfg::SMEM);
     if (attr != cudaSuccess) return attr;
     const int64_t total = (M + BM - 1) / BM * ((N + BN - 1) / BN) * p.splits;
-    k_linear_tc<T, A_MN, B_MN><<<(unsigned)std::min<int64_t>(total, s->num_sms), kThreads, Cfg::SMEM, s->st>>>(
-        a, b, M, N, p.kblocks, p.splits, epi, s->d_status);
     s->launches++;
-    return cudaGetLastError();
+    return launch(next, k_linear_tc<T, A_MN, B_MN>, (unsigned)std::min<int64_t>(total, s->num_sms), kThreads, Cfg::SMEM,
+                  s->st, a, b, M, N, p.kblocks, p.splits, epi, s->d_status);
 }
 
 // D(i, j) = sum_k A(i, k) B(j, k) and the epilogue; a_mn: A is stored k x M, else M x k.
@@ -794,7 +805,7 @@ cudaError_t maps(int type, const Product &p, CUtensorMap *a, CUtensorMap *b) {
 // Products whose plan is pairs of SMs: one, or with PAIR_GRADS two; the longer sums
 // first, so that the last round is of short ones.
 template <typename T, int FORM>
-cudaError_t launch_pair(zsolve_seq *s, int type, const Product *p) {
+cudaError_t launch_pair(zsolve_seq *s, int type, const Product *p, bool next) {
     static const cudaError_t attr =
         cudaFuncSetAttribute(k_linear_pair<T, FORM>, cudaFuncAttributeMaxDynamicSharedMemorySize, kPairSmem);
     if (attr != cudaSuccess) return attr;
@@ -818,37 +829,36 @@ cudaError_t launch_pair(zsolve_seq *s, int type, const Product *p) {
         total += tiles(r);
     }
     const unsigned pairs = (unsigned)std::min<int64_t>(total, s->num_sms / 2);
-    k_linear_pair<T, FORM><<<2 * pairs, kThreads, kPairSmem, s->st>>>(ma, mb, q.M, q.N, kblocks(q), q.epi, two, s->d_status);
     s->launches++;
-    return cudaGetLastError();
+    return launch(next, k_linear_pair<T, FORM>, 2 * pairs, kThreads, kPairSmem, s->st, ma, mb, q.M, q.N, kblocks(q), q.epi,
+                  two, s->d_status);
 }
 
 template <typename T>
-cudaError_t product(zsolve_seq *s, int type, Product q, float *part) {
+cudaError_t product(zsolve_seq *s, int type, Product q, float *part, bool next) {
     const Plan p = plan_of(q.M, q.N, q.K, s->num_sms);
     if (p.pair)
-        return !q.b_mn  ? launch_pair<T, PAIR_FWD>(s, type, &q)
-               : q.a_mn ? launch_pair<T, PAIR_DW>(s, type, &q)
-                        : launch_pair<T, PAIR_DX>(s, type, &q);
+        return !q.b_mn  ? launch_pair<T, PAIR_FWD>(s, type, &q, next)
+               : q.a_mn ? launch_pair<T, PAIR_DW>(s, type, &q, next)
+                        : launch_pair<T, PAIR_DX>(s, type, &q, next);
     CUtensorMap ma, mb;
     cudaError_t e = maps(type, q, &ma, &mb);
     if (e != cudaSuccess) return e;
     q.epi.part = p.splits > 1 ? part : nullptr;
     q.epi.ldp = ld_part(q.N);
-#define LIN_GO(AM, BMN) e = launch_tc<T, AM, BMN>(ma, mb, q.M, q.N, p, q.epi, s)
+#define LIN_GO(AM, BMN) e = launch_tc<T, AM, BMN>(ma, mb, q.M, q.N, p, q.epi, next, s)
     if (!q.a_mn && !q.b_mn) LIN_GO(false, false);
     else if (!q.a_mn) LIN_GO(false, true);
     else LIN_GO(true, true);
 #undef LIN_GO
     if (e != cudaSuccess || p.splits == 1) return e;
     const int64_t n8 = q.M * ((q.N + 7) / 8);
-    k_linear_join<T><<<(unsigned)((n8 + 255) / 256), 256, 0, s->st>>>(q.M, q.N, p.splits, q.epi);
     s->launches++;
-    return cudaGetLastError();
+    return launch(true, k_linear_join<T>, (unsigned)((n8 + 255) / 256), 256, 0, s->st, q.M, q.N, p.splits, q.epi);
 }
 
 // Matrices that TMA can address: themselves, or their copies.
-cudaError_t packed(zsolve_seq *s, Mat *a, void *dsta, Mat *b, void *dstb) {
+cudaError_t packed(zsolve_seq *s, Mat *a, void *dsta, Mat *b, void *dstb, bool next) {
     PackJob job[2];
     int n = 0;
     int64_t most = 0;
@@ -865,9 +875,8 @@ cudaError_t packed(zsolve_seq *s, Mat *a, void *dsta, Mat *b, void *dstb) {
     }
     if (n == 0) return cudaSuccess;
     const unsigned blocks = (unsigned)std::min<int64_t>((most + 255) / 256, (int64_t)s->num_sms * 8);
-    k_linear_pack<<<dim3(blocks, n), 256, 0, s->st>>>(job[0], job[n - 1]);
     s->launches++;
-    return cudaGetLastError();
+    return launch(next, k_linear_pack, dim3(blocks, n), 256, 0, s->st, job[0], job[n - 1]);
 }
 
 bool vec8(const void *p, int64_t ld) { return !p || (((uintptr_t)p & 15) == 0 && ld % 8 == 0); }
@@ -891,8 +900,9 @@ int linear_fwd(zsolve_seq *s, int type, int64_t m, int64_t n, int64_t k, Mat x, 
         if (!ws) return st;
         carve(ws);
     }
-    SEQ_CU(packed(s, &x, xp, &w, wp));
-    SEQ_CU(product<T>(s, type, Product{m, n, k, x, w, false, false, epi}, part));
+    const int64_t before = s->launches;
+    SEQ_CU(packed(s, &x, xp, &w, wp, false));
+    SEQ_CU(product<T>(s, type, Product{m, n, k, x, w, false, false, epi}, part, s->launches > before));
     return ZSOLVE_OK;
 }
 
@@ -935,6 +945,7 @@ int linear_bwd(zsolve_seq *s, int type, int64_t m, int64_t n, int64_t k, Mat dy,
         if (!ws) return st;
         carve(ws);
     }
+    const int64_t before = s->launches;
     if (form_dz || db) {
         const int vec = vec8(dy.p, dy.ld) && (!has_act || vec8(z.p, z.ld));
         k_linear_dz<T><<<dim3((unsigned)((n + 255) / 256), dzrows), 256, 0, s->st>>>(
@@ -943,13 +954,12 @@ int linear_bwd(zsolve_seq *s, int type, int64_t m, int64_t n, int64_t k, Mat dy,
         SEQ_CU(cudaGetLastError());
     }
     if (db) {
-        k_linear_db<T><<<(unsigned)((n + 31) / 32), 256, 0, s->st>>>(sums, dzrows, (int)n, (T *)db);
         s->launches++;
-        SEQ_CU(cudaGetLastError());
+        SEQ_CU(launch(true, k_linear_db<T>, (unsigned)((n + 31) / 32), 256, 0, s->st, sums, dzrows, (int)n, (T *)db));
     }
     Mat dz = dy;
     if (form_dz) dz.p = dzp, dz.ld = ldz8;
-    SEQ_CU(packed(s, &w, wp, &x, xp));
+    SEQ_CU(packed(s, &w, wp, &x, xp, s->launches > before));
     Product pr[2];
     int np = 0;
     if (dx) {
@@ -963,9 +973,9 @@ int linear_bwd(zsolve_seq *s, int type, int64_t m, int64_t n, int64_t k, Mat dy,
         pr[np++] = Product{n, k, m, dz, x, true, true, epi};
     }
     if (np == 2 && px.pair && pw.pair) {
-        SEQ_CU((launch_pair<T, PAIR_GRADS>(s, type, pr)));
+        SEQ_CU((launch_pair<T, PAIR_GRADS>(s, type, pr, s->launches > before)));
     } else {
-        for (int i = 0; i < np; i++) SEQ_CU(product<T>(s, type, pr[i], part));
+        for (int i = 0; i < np; i++) SEQ_CU(product<T>(s, type, pr[i], part, s->launches > before));
     }
     return ZSOLVE_OK;
 }

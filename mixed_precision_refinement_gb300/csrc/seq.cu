@@ -231,6 +231,10 @@ int zsolve_seq_create(zsolve_seq **out) {
     if (cudaDeviceGetAttribute(&s->num_sms, cudaDevAttrMultiProcessorCount, s->dev) != cudaSuccess)
         return bail(ZSOLVE_ECUDA);
     if (cudaEventCreateWithFlags(&s->ev, cudaEventDisableTiming) != cudaSuccess) return bail(ZSOLVE_ECUDA);
+    if (cudaStreamCreateWithFlags(&s->side, cudaStreamNonBlocking) != cudaSuccess ||
+        cudaEventCreateWithFlags(&s->fork, cudaEventDisableTiming) != cudaSuccess ||
+        cudaEventCreateWithFlags(&s->joined, cudaEventDisableTiming) != cudaSuccess)
+        return bail(ZSOLVE_ECUDA);
     if (cudaMalloc(&s->d_status, sizeof(unsigned)) != cudaSuccess) return bail(ZSOLVE_ENOMEM);
     if (cudaMemset(s->d_status, 0, sizeof(unsigned)) != cudaSuccess) return bail(ZSOLVE_ECUDA);
     *out = s;
@@ -272,6 +276,9 @@ void zsolve_seq_destroy(zsolve_seq *s) {
     for (void *p : s->retired) cudaFree(p);
     cudaFree(s->d_status);
     if (s->ev) cudaEventDestroy(s->ev);
+    if (s->fork) cudaEventDestroy(s->fork);
+    if (s->joined) cudaEventDestroy(s->joined);
+    if (s->side) cudaStreamDestroy(s->side);
     delete s;
 }
 
@@ -375,8 +382,9 @@ int zsolve_delta(zsolve_seq *s, const zsolve_delta_args *a, void *o, int64_t ldo
     if (st == ZSOLVE_OK) st = w.bind(s, a, &g);
     if (st != ZSOLVE_OK) return st;
     SEQ_CU(zs_launch_delta_plan(a->offsets, a->nseq, a->tokens, w.nchunks, w.first, w.seq, w.chunk, s->st, &s->launches));
-    SEQ_CU(zs_launch_delta_terms(a->type, g, w.terms, s->st, &s->launches));
-    SEQ_CU(zs_launch_delta_chain(a->type, g, w.terms, a->s0, o, ldo, sn, nullptr, nullptr, s->d_status, s->st, &s->launches));
+    SEQ_CU(zs_launch_delta_terms(a->type, g, w.terms, true, s->st, &s->launches));
+    SEQ_CU(zs_launch_delta_chain(a->type, g, w.terms, a->s0, o, ldo, sn, nullptr, nullptr, s->d_status, true, s->st,
+                                 &s->launches));
     return ZSOLVE_OK;
 }
 
@@ -410,18 +418,42 @@ int zsolve_delta_bwd(zsolve_seq *s, const zsolve_delta_args *a, const void *dout
     if (st == ZSOLVE_OK) st = w.bind(s, a, &g);
     if (st != ZSOLVE_OK) return st;
     SEQ_CU(zs_launch_delta_plan(a->offsets, a->nseq, a->tokens, w.nchunks, w.first, w.seq, w.chunk, s->st, &s->launches));
-    if (a->tokens > 0) {
-        SEQ_CU(zs_launch_delta_terms(a->type, g, w.terms, s->st, &s->launches));
-        // the states and U once more: keeping them from the forward pass would hold 96 KB a chunk and head
-        // at 128 x 128 until the backward pass
-        SEQ_CU(zs_launch_delta_chain(a->type, g, w.terms, a->s0, nullptr, 0, nullptr, w.states, w.us, s->d_status, s->st,
-                                     &s->launches));
+    if (a->tokens > 0) SEQ_CU(zs_launch_delta_terms(a->type, g, w.terms, true, s->st, &s->launches));
+    auto backwards = [&](bool next, cudaStream_t on) {
+        return zs_launch_delta_rchain(a->type, g, w.terms, w.dout, w.lddo, ds, w.dends, w.dxs, dv, ds0, s->d_status, next, on,
+                                      &s->launches);
+    };
+    // the states and U once more: keeping them from the forward pass would hold 96 KB a chunk and head
+    // at 128 x 128 until the backward pass
+    auto forwards = [&](bool next) {
+        return zs_launch_delta_chain(a->type, g, w.terms, a->s0, nullptr, 0, nullptr, w.states, w.us, s->d_status, next, s->st,
+                                     &s->launches);
+    };
+    if (a->tokens == 0) {
+        SEQ_CU(backwards(true, s->st));
+        return ZSOLVE_OK;
     }
-    SEQ_CU(zs_launch_delta_rchain(a->type, g, w.terms, w.dout, w.lddo, ds, w.dends, w.dxs, dv, ds0, s->d_status, s->st,
-                                  &s->launches));
-    if (a->tokens > 0)
-        SEQ_CU(zs_launch_delta_grads(a->type, g, w.terms, w.dout, w.lddo, w.states, w.dends, w.us, w.dxs, w.dqp, w.dkp, dq,
-                                     dk, dg, dbeta, s->st, &s->launches));
+    // The two recurrences do not need each other.  They run side by side where the SMs
+    // hold both, a block each (24 blocks each, 4000 tokens, float32: 966 -> 640 us; 8 blocks,
+    // 300 tokens: 81 -> 66), else one after the other (128 blocks each, 4096 tokens,
+    // bfloat16: 1057 us side by side, 1043 so), as for a chunk or two, where the events
+    // cost more (20 tokens: 56 us for 53).
+    const bool both = 2 * delta_chain_blocks(g) <= s->num_sms && a->tokens > 2 * zs::kChunk;
+    if (both) {
+        SEQ_CU(cudaEventRecord(s->fork, s->st));
+        SEQ_CU(cudaStreamWaitEvent(s->side, s->fork, 0));
+        const cudaError_t e = backwards(false, s->side), e2 = forwards(false);
+        // joined also after a failed launch: the workspace's next user comes after both
+        SEQ_CU(cudaEventRecord(s->joined, s->side));
+        SEQ_CU(cudaStreamWaitEvent(s->st, s->joined, 0));
+        SEQ_CU(e);
+        SEQ_CU(e2);
+    } else {
+        SEQ_CU(forwards(true));
+        SEQ_CU(backwards(true, s->st));
+    }
+    SEQ_CU(zs_launch_delta_grads(a->type, g, w.terms, w.dout, w.lddo, w.states, w.dends, w.us, w.dxs, w.dqp, w.dkp, dq, dk,
+                                 dg, dbeta, !both, s->st, &s->launches));
     return ZSOLVE_OK;
 }
 

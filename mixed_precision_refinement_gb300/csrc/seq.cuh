@@ -15,6 +15,8 @@
 struct zsolve_seq {
     cudaStream_t st = nullptr;
     cudaEvent_t ev = nullptr;  // orders the workspace's users when the stream changes
+    cudaStream_t side = nullptr;           // beside st within a call; st waits for it before the call returns
+    cudaEvent_t fork = nullptr, joined = nullptr;
     void *ws = nullptr;
     size_t ws_bytes = 0;
     bool ws_captured = false;      // a captured graph uses ws: it is kept until the handle goes
@@ -208,6 +210,28 @@ __device__ __forceinline__ void bulk_load(void *dst, const void *src, uint32_t b
 
 // Two float32 operations in one instruction, each rounded on its own: half the
 // issue slots where those are what a kernel runs out of.
+// A kernel that follows another of the same call is launched with `next`: its blocks
+// may be set up while the one before still runs, and wait in after_previous() until
+// all of that one's results are there.  Every kernel that is launched so, or before
+// one that is, calls after_previous() before it touches memory and may_start_next()
+// when its own blocks are placed.  It hides the launches' gaps and set-up: linear of
+// 801 x 1000 x 2157 (three kernels) 25.9 -> 20.5 us, layer norm backward of 6614 x 2157
+// (two) 55.1 -> 51.3.
+__device__ __forceinline__ void after_previous() {
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+}
+__device__ __forceinline__ void may_start_next() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
+template <typename... P, typename... A>
+inline cudaError_t launch(bool next, void (*kernel)(P...), dim3 grid, int threads, size_t smem, cudaStream_t st, A... args) {
+    cudaLaunchAttribute attr;
+    attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr.val.programmaticStreamSerializationAllowed = 1;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = grid, cfg.blockDim = dim3((unsigned)threads), cfg.dynamicSmemBytes = smem, cfg.stream = st;
+    cfg.attrs = &attr, cfg.numAttrs = next ? 1 : 0;
+    return cudaLaunchKernelEx(&cfg, kernel, P(args)...);
+}
+
 __device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
     float2 d;
     asm("{\n\t.reg .b64 x, y, z, w;\n\t"

@@ -217,3 +217,17 @@ def test_refusals(seq):
         bad[i] = v
         assert lib.zsolve_delta_bwd(seq.seq, ctypes.byref(a), *bad) == zs.ZSOLVE_EINVAL, i
     assert lib.zsolve_delta_bwd(None, ctypes.byref(a), *good) == zs.ZSOLVE_EINVAL
+
+
+def test_many_sequences_equal_one_alone(seq):
+    """One sequence's recurrences run side by side, those of many one after the other: the same gradients."""
+    torch = _torch()
+    x, dout, ds = _case([200] * 40, 1, 2, 64, 64, "bfloat16", 12)
+    order = ("q", "k", "v", "g", "beta")
+    many = seq.delta_bwd(dout, *(x[n] for n in order), x["s0"], ds=ds, offsets=x["offsets"])
+    for i in (0, 39):
+        at = slice(200 * i, 200 * i + 200)
+        one = seq.delta_bwd(dout[at], *(x[n][at] for n in order), x["s0"][i:i + 1], ds=ds[i:i + 1])
+        for a, b in zip(many[:5], one):
+            assert torch.equal(a[at], b)
+        assert torch.equal(many[5][i], one[5][0])

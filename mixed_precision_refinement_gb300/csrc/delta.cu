@@ -103,7 +103,9 @@ k_delta_plan(const int64_t *__restrict__ offsets, int nseq, int64_t tokens, int 
 // substitution, a lane a column; then warp j finds block column j below them,
 //   T_ij = -T_ii (A_ij T_jj + ... + A_i,i-1 T_i-1,j),
 // transposed, so that each finished block is, as an accumulator, the A operand
-// of the next products.  Bound by the latency of these steps; two blocks an SM.
+// of the next products.  Bound by the latency of these steps (1.9 of 4 instructions a
+// cycle, tensor pipe 16%); two blocks an SM.  8192 tokens x 32 heads of 128, bfloat16:
+// 88 us.
 constexpr int kTermThreads = 256;
 constexpr int kLdA = kChunk + 4;
 constexpr int kLdD = 20;
@@ -339,7 +341,9 @@ k_delta_pack(const T *__restrict__ src, int64_t ld, int64_t tokens, int heads, i
 // beside the groups: they keep two stages of chunk operands filled, and form
 // the outputs from S and U as the groups leave them in shared memory (with the
 // outputs in the groups themselves a chunk took 4.0 us).  The groups do not wait
-// for each other, so one's exchanges run beside the other's products.
+// for each other, so one's exchanges run beside the other's products.  A chunk of
+// 128 x 128 heads takes 3.3 us (bfloat16), bound by shared memory (78% of its rate) and
+// the latency from one product to the next; 32768 tokens x 32 heads 1.65 ms.
 template <typename T, int DK>
 struct ChainCfg {
     static constexpr int WK = DK / 32;

@@ -3,7 +3,8 @@
 // other and writes the state back.  Bound by HBM, which the state crosses once
 // each way; one pass over the registers gives both products of a token,
 //   r = S^T k, y = S^T q,  u = beta (v - a r),  o = scale (a y + (q . k) u),
-// so that a token costs one exchange between the warps.
+// so that a token costs one exchange between the warps.  64 sequences x 32 heads of
+// 128 x 128: 268 MB in 54 us, 5.0 TB/s (a copy of as many bytes: 5.3 to 6.3).
 #include "delta.cuh"
 
 namespace {

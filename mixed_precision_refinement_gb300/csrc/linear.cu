@@ -331,7 +331,9 @@ k_linear_tc(const __grid_constant__ CUtensorMap amap, const __grid_constant__ CU
 // of its own, and shared memory, which feeds the MMAs and takes the copies, no
 // longer bounds the rate.  The leader's threads issue the MMAs and own the
 // barriers of full stages and of free accumulators; a stage's release and a
-// finished accumulator are told to both.
+// finished accumulator are told to both.  16384 x 8192 x 4096 with bias, SiLU and
+// residual: 671 us by itself, 1640 TFLOP/s; back to back 750 to 764, 1450 TFLOP/s, where
+// the power limit lowers the clock (a library's plain product: 1685).
 constexpr int kPairStages = 6;
 constexpr int kPairStage = 2 * BM * BK * 2;  // A and B rows of one CTA
 constexpr int kPairSmem = kPairStages * kPairStage + 1024;
@@ -590,7 +592,8 @@ k_linear_pair(const __grid_constant__ CUtensorMap amap, const __grid_constant__ 
 }
 
 // The parts of a product split along k, added in order, and the epilogue; a
-// thread for 8 columns of a row.
+// thread for 8 columns of a row.  Bound by the latency of its loads, which L2 serves:
+// 801 x 1000 in two parts 6 us, partly hidden behind the product's end.
 template <typename T>
 __global__ void __launch_bounds__(256)
 k_linear_join(int64_t M, int64_t N, int splits, const Epilogue epi) {
@@ -639,7 +642,8 @@ k_linear_pack(const PackJob a, const PackJob b) {
 // and, per block row, the columns' float32 sums of it before it is rounded
 // (parts, one row of n a block row; NULL: not formed).  dz is rounded to the
 // inputs' type because it is the tensor cores' operand: it adds one rounding
-// of an input to each product's terms.
+// of an input to each product's terms.  Bound by HBM: 8192 x 4096 bfloat16 in 45 us,
+// 4.5 TB/s.
 constexpr int kDzBlocks = 4;  // of an SM
 template <typename T>
 __global__ void __launch_bounds__(256, kDzBlocks)

@@ -4,7 +4,8 @@
 // m16n8k16 (weights as A, the rows of x as B), 16 bytes a lane: a lane's eight
 // neighbours along k serve two steps, since any order of k serves as long as A
 // and B agree.  The warps' partial sums meet in shared memory, so one launch does
-// all of it, without tensor maps or a workspace.
+// all of it, without tensor maps or a workspace.  One row, 4096 x 2048: 4.6 us with the
+// weight in L2, 3.6 TB/s; 10.7 us from HBM, bound by the loads' latency.
 #include <type_traits>
 
 #include "linear.cuh"

@@ -10,8 +10,8 @@
 // along k, zero-filled beyond the matrices' ends, so ragged sizes need no
 // code in the main loop.
 //
-// Warp roles (192 threads, persistent over the output tiles): warp 0 issues
-// the TMA loads into a ring of stages, warp 1 the MMAs (one thread), warps 2-5
+// Warp roles (320 threads, persistent over the output tiles): warp 0 issues
+// the TMA loads into a ring of stages, warp 1 the MMAs (one thread), warps 2-9
 // drain the accumulator while the next tile's MMAs fill the other half of TMEM.
 // Products with fewer tiles than SMs are split along k: each part leaves its
 // float32 partial sums in the workspace and a second kernel adds them in a
@@ -31,7 +31,8 @@ using namespace zs;
 
 constexpr int BM = 128;       // rows of an output tile
 constexpr int BK = 64;        // k values of a stage: 128 bytes, one swizzle row
-constexpr int kThreads = 192;
+constexpr int kDrain = 8;  // epilogue warps: two for each quarter of the TMEM lanes
+constexpr int kThreads = 64 + 32 * kDrain;
 constexpr uint32_t kTmemCols = 512;
 constexpr uint32_t kWaitLimit = 1u << 19;  // try_wait polls before a wait gives up: about a second
 
@@ -154,6 +155,52 @@ __device__ __forceinline__ TileAt tile_at(int t, int mt, int nt) {
     return x;
 }
 
+// One warp's part of a finished accumulator: 32 rows (a lane a row), CHUNKS x 32
+// columns from `col` on.  ready(): waits for the accumulator, false if that gave up;
+// release(): called once it is read.  Four warps that loaded the residual and the bias
+// where they were added took 20 us for a 128 x 256 part, more than the MMAs of 4096 k
+// values; eight that load a step ahead: 8192 x 8192 x 1024 with SiLU 318 -> 125 us,
+// 8192 x 8192 x 4096 364 -> 324.
+template <typename T, int CHUNKS, typename Ready, typename Release>
+__device__ __forceinline__ bool drain(const Epilogue &epi, int64_t M, int64_t N, int64_t row, int64_t col, int split,
+                                      uint32_t taddr, Ready ready, Release release) {
+    Ahead<T> in;
+    auto whole = [&](int64_t c) { return row < M && c + 32 <= N && epi.vec && !epi.part; };
+    if (whole(col)) in.load(epi, row, col);
+    if (!ready()) return false;
+#pragma unroll 1
+    for (int c = 0; c < CHUNKS; c++, col += 32) {
+        float v[32];
+        __syncwarp();  // lanes beyond the last row come back
+        tmem_ld32(taddr + (uint32_t)(c * 32), v);
+        if (c == CHUNKS - 1) release();
+        if (whole(col)) {
+            const Ahead<T> now = in;
+            if (c + 1 < CHUNKS && whole(col + 32)) in.load(epi, row, col + 32);
+            finish32<T>(epi, row, col, now, v);
+            continue;
+        }
+        if (row >= M) continue;
+#pragma unroll
+        for (int j = 0; j < 4; j++) {
+            const int64_t cj = col + j * 8;
+            const int nc = (int)min((int64_t)8, N - cj);
+            if (nc <= 0) break;
+            float f[8];
+#pragma unroll
+            for (int i = 0; i < 8; i++) f[i] = v[j * 8 + i];
+            if (epi.part) {  // ldp is a multiple of 8 and the padding is ours
+                float4 *p = reinterpret_cast<float4 *>(epi.part + ((int64_t)split * M + row) * epi.ldp + cj);
+                p[0] = make_float4(f[0], f[1], f[2], f[3]);
+                p[1] = make_float4(f[4], f[5], f[6], f[7]);
+            } else {
+                finish8<T>(epi, row, cj, nc, f);
+            }
+        }
+    }
+    return true;
+}
+
 template <typename T, bool A_MN, bool B_MN>
 __global__ void __launch_bounds__(kThreads, 1)
 k_linear_tc(const __grid_constant__ CUtensorMap amap, const __grid_constant__ CUtensorMap bmap, int64_t M, int64_t N,
@@ -180,7 +227,7 @@ k_linear_tc(const __grid_constant__ CUtensorMap amap, const __grid_constant__ CU
         }
         for (int b = 0; b < 2; b++) {
             mbar_init(smem_u32(&bar_accf[b]), 1);
-            mbar_init(smem_u32(&bar_acce[b]), 4);
+            mbar_init(smem_u32(&bar_acce[b]), kDrain);
         }
         mbar_init(smem_u32(&bar_drain), 1);
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
@@ -278,44 +325,26 @@ k_linear_tc(const __grid_constant__ CUtensorMap amap, const __grid_constant__ CU
             }
         }
     } else {
-        // ------------------------------------------------ epilogue (warps 2-5)
-        const int quad = warp & 3;  // TMEM lanes 32 quad .. 32 quad + 31
+        // ------------------------------------------------ epilogue (warps 2-9)
+        const int quad = warp & 3, half = (warp - 2) >> 2;  // TMEM lanes 32 quad .. 32 quad + 31, half the columns
         uint32_t it = 0;
         for (int t = blockIdx.x; t < total; t += gridDim.x, it++) {
             const TileAt x = tile_at(t, mt, nt);
             const uint32_t buf = it & 1u, aph = (it >> 1) & 1u;
-            const bool ok = mbar_wait(smem_u32(&bar_accf[buf]), aph, &s_abort, status);
-            if (!__all_sync(0xffffffffu, ok)) break;
-            tc_fence_after();
-            const int64_t row = (int64_t)x.tm * BM + quad * 32 + lane;
-#pragma unroll 1
-            for (int c = 0; c < BN / 32; c++) {
-                float v[32];
-                tmem_ld32(tmem + buf * 256u + (uint32_t)(c * 32) + ((uint32_t)(quad * 32) << 16), v);
-                if (c == BN / 32 - 1) {  // accumulator fully read: hand it back to the MMA warp
+            const bool ok = drain<T, BN / 64>(
+                epi, M, N, (int64_t)x.tm * BM + quad * 32 + lane, (int64_t)x.tn * BN + half * (BN / 2), x.split,
+                tmem + buf * 256u + (uint32_t)(half * (BN / 2)) + ((uint32_t)(quad * 32) << 16),
+                [&] {
+                    const bool in = __all_sync(0xffffffffu, mbar_wait(smem_u32(&bar_accf[buf]), aph, &s_abort, status));
+                    tc_fence_after();
+                    return in;
+                },
+                [&] {  // accumulator fully read: hand it back to the MMA warp
                     tc_fence_before();
                     __syncwarp();
                     if (lane == 0) mbar_arrive(smem_u32(&bar_acce[buf]));
-                }
-                const int64_t col = (int64_t)x.tn * BN + c * 32;
-                if (row >= M) continue;
-#pragma unroll
-                for (int j = 0; j < 4; j++) {
-                    const int64_t cj = col + j * 8;
-                    const int nc = (int)min((int64_t)8, N - cj);
-                    if (nc <= 0) break;
-                    float f[8];
-#pragma unroll
-                    for (int i = 0; i < 8; i++) f[i] = v[j * 8 + i];
-                    if (epi.part) {  // ldp is a multiple of 8 and the padding is ours
-                        float4 *p = reinterpret_cast<float4 *>(epi.part + ((int64_t)x.split * M + row) * epi.ldp + cj);
-                        p[0] = make_float4(f[0], f[1], f[2], f[3]);
-                        p[1] = make_float4(f[4], f[5], f[6], f[7]);
-                    } else {
-                        finish8<T>(epi, row, cj, nc, f);
-                    }
-                }
-            }
+                });
+            if (!ok) break;
         }
     }
     tc_fence_before();
@@ -332,8 +361,8 @@ k_linear_tc(const __grid_constant__ CUtensorMap amap, const __grid_constant__ CU
 // longer bounds the rate.  The leader's threads issue the MMAs and own the
 // barriers of full stages and of free accumulators; a stage's release and a
 // finished accumulator are told to both.  16384 x 8192 x 4096 with bias, SiLU and
-// residual: 671 us by itself, 1640 TFLOP/s; back to back 750 to 764, 1450 TFLOP/s, where
-// the power limit lowers the clock (a library's plain product: 1685).
+// residual back to back: 732 us, 1500 TFLOP/s, where the power limit lowers the clock (a
+// library's plain product: 1685).
 constexpr int kPairStages = 6;
 constexpr int kPairStage = 2 * BM * BK * 2;  // A and B rows of one CTA
 constexpr int kPairSmem = kPairStages * kPairStage + 1024;
@@ -446,7 +475,7 @@ k_linear_pair(const __grid_constant__ CUtensorMap amap, const __grid_constant__ 
         }
         for (int b = 0; b < 2; b++) {
             mbar_init(smem_u32(&bar_accf[b]), 1);
-            mbar_init(smem_u32(&bar_acce[b]), 8);  // the epilogue warps of both CTAs
+            mbar_init(smem_u32(&bar_acce[b]), 2 * kDrain);  // the epilogue warps of both CTAs
         }
         mbar_init(smem_u32(&bar_drain), 1);
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
@@ -548,39 +577,27 @@ k_linear_pair(const __grid_constant__ CUtensorMap amap, const __grid_constant__ 
             }
         }
     } else {
-        // ------------------------------------------------ epilogue (warps 2-5), of its CTA's rows
-        const int quad = warp & 3;
+        // ------------------------------------------------ epilogue (warps 2-9), of its CTA's rows
+        const int quad = warp & 3, half = (warp - 2) >> 2;
         uint32_t it = 0;
         for (; next(it); it++) {
             const TileAt x = place();
-            const int64_t M = BOTH && job ? two.M : M0, N = BOTH && job ? two.N : N0;
             const uint32_t buf = it & 1u, aph = (it >> 1) & 1u;
-            const bool ok = mbar_wait(smem_u32(&bar_accf[buf]), aph, &s_abort, status);
-            if (!__all_sync(0xffffffffu, ok)) break;
-            tc_fence_after();
-            const int64_t row = (int64_t)x.tm * 2 * BM + rank * BM + quad * 32 + lane;
-#pragma unroll 1
-            for (int c = 0; c < 8; c++) {
-                float v[32];
-                tmem_ld32(tmem + buf * 256u + (uint32_t)(c * 32) + ((uint32_t)(quad * 32) << 16), v);
-                if (c == 7) {  // accumulator fully read: hand it back to the leader's MMA warp
+            const bool ok = drain<T, 4>(
+                BOTH && job ? two.epi : epi0, BOTH && job ? two.M : M0, BOTH && job ? two.N : N0,
+                (int64_t)x.tm * 2 * BM + rank * BM + quad * 32 + lane, (int64_t)x.tn * 256 + half * 128, 0,
+                tmem + buf * 256u + (uint32_t)(half * 128) + ((uint32_t)(quad * 32) << 16),
+                [&] {
+                    const bool in = __all_sync(0xffffffffu, mbar_wait(smem_u32(&bar_accf[buf]), aph, &s_abort, status));
+                    tc_fence_after();
+                    return in;
+                },
+                [&] {  // accumulator fully read: hand it back to the leader's MMA warp
                     tc_fence_before();
                     __syncwarp();
                     if (lane == 0) mbar_arrive_remote(cluster_addr(smem_u32(&bar_acce[buf]), 0));
-                }
-                const int64_t col = (int64_t)x.tn * 256 + c * 32;
-                if (row >= M) continue;
-#pragma unroll
-                for (int j = 0; j < 4; j++) {
-                    const int64_t cj = col + j * 8;
-                    const int nc = (int)min((int64_t)8, N - cj);
-                    if (nc <= 0) break;
-                    float f[8];
-#pragma unroll
-                    for (int i = 0; i < 8; i++) f[i] = v[j * 8 + i];
-                    finish8<T>(BOTH && job ? two.epi : epi0, row, cj, nc, f);
-                }
-            }
+                });
+            if (!ok) break;
         }
     }
     tc_fence_before();
@@ -759,9 +776,11 @@ struct Mat {
 
 // A product's tiles and parts along k.  Pairs of SMs on 256 x 256 tiles where
 // there is a tile for every pair (and rows of tiles enough that a half empty last
-// one does not matter), else single SMs on 128 x 128: four times the tiles.  Parts
-// are for what still leaves SMs idle, of 4 k blocks at least, so that a part's
-// loads outweigh the pass that joins them.
+// one does not matter), else single SMs on 128 x 128: four times the tiles.  Pairs
+// against single SMs: 2048 x 2560 x 2048 (80 tiles for 76 pairs) 31.5 us and 38.2,
+// 4096 x 4096 x 4096 95 and 153, 1100 x 4096 x 2048 (a last row of tiles 3/10 full)
+// 30.7 and 27.5.  Parts are for what still leaves SMs idle, of 4 k blocks at least, so
+// that a part's loads outweigh the pass that joins them.
 struct Plan {
     bool pair;
     int splits, kblocks;

@@ -113,6 +113,45 @@ __device__ __forceinline__ void finish8(const Epilogue &e, int64_t row, int64_t 
     store8<T>(e.y, row * e.ldy + c, nc, e.vec, v);
 }
 
+// 32 consecutive values of a row, all there and aligned: the residual and the bias
+// are loaded a step ahead, so that their latency is not in the way of the stores.
+template <typename T>
+struct Ahead {
+    Vec<T, 8> r[4], b[4];
+    __device__ __forceinline__ void load(const Epilogue &e, int64_t row, int64_t c) {
+#pragma unroll
+        for (int j = 0; j < 4; j++) {
+            if (e.r) r[j].load(reinterpret_cast<const T *>(e.r) + row * e.ldr + c + 8 * j);
+            if (e.bias) b[j].load(reinterpret_cast<const T *>(e.bias) + c + 8 * j);
+        }
+    }
+};
+template <typename T>
+__device__ __forceinline__ void finish32(const Epilogue &e, int64_t row, int64_t c, const Ahead<T> &in, float (&v)[32]) {
+    float f[8];
+    if (e.bias)
+#pragma unroll
+        for (int j = 0; j < 4; j++) {
+            in.b[j].get(f);
+#pragma unroll
+            for (int i = 0; i < 8; i++) v[8 * j + i] += f[i];
+        }
+    Vec<T, 8> u;
+    if (e.z)
+#pragma unroll
+        for (int j = 0; j < 4; j++) u.set(v + 8 * j), u.store(reinterpret_cast<T *>(e.z) + row * e.ldz + c + 8 * j);
+    act_all(v, e.act);
+    if (e.r)
+#pragma unroll
+        for (int j = 0; j < 4; j++) {
+            in.r[j].get(f);
+#pragma unroll
+            for (int i = 0; i < 8; i++) v[8 * j + i] += f[i];
+        }
+#pragma unroll
+    for (int j = 0; j < 4; j++) u.set(v + 8 * j), u.store(reinterpret_cast<T *>(e.y) + row * e.ldy + c + 8 * j);
+}
+
 }  // namespace zs
 
 // linear_few.cu: y for at most kFewRows rows of x, in one kernel without a workspace.

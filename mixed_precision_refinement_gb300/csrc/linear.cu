@@ -37,6 +37,12 @@ constexpr uint32_t kTmemCols = 512;
 constexpr uint32_t kWaitLimit = 1u << 19;  // try_wait polls before a wait gives up: about a second
 
 constexpr int BN = 128;       // columns of an output tile of one CTA
+// Bytes in which the epilogue warps turn their values over where the results' rows
+// start anywhere.  Those kernels are apart: the others need the registers, and L1, whose
+// room this takes, for the other half of each sector of the residual (8192 x 8192 x 1024:
+// 125 us, 134 with both ways in one kernel, 166 with the memory taken as well).
+constexpr int kTurn = kDrain * 32 * kTurnLd * 4;
+inline bool turned(const Epilogue &e) { return !e.vec && !e.part; }
 struct Cfg {
     static constexpr int A_BYTES = BM * BK * 2;
     static constexpr int B_BYTES = BN * BK * 2;
@@ -161,19 +167,28 @@ __device__ __forceinline__ TileAt tile_at(int t, int mt, int nt) {
 // where they were added took 20 us for a 128 x 256 part, more than the MMAs of 4096 k
 // values; eight that load a step ahead: 8192 x 8192 x 1024 with SiLU 318 -> 125 us,
 // 8192 x 8192 x 4096 364 -> 324.
-template <typename T, int CHUNKS, typename Ready, typename Release>
+// TURN: for rows of results that start anywhere (5000 x 1001 x 700: 96 us with a row's
+// values stored one by one by its lane, 46 so).
+template <typename T, int CHUNKS, bool TURN, typename Ready, typename Release>
 __device__ __forceinline__ bool drain(const Epilogue &epi, int64_t M, int64_t N, int64_t row, int64_t col, int split,
-                                      uint32_t taddr, Ready ready, Release release) {
+                                      uint32_t taddr, float *turn, Ready ready, Release release) {
     Ahead<T> in;
-    auto whole = [&](int64_t c) { return row < M && c + 32 <= N && epi.vec && !epi.part; };
+    auto whole = [&](int64_t c) { return !TURN && row < M && c + 32 <= N && epi.vec && !epi.part; };
     if (whole(col)) in.load(epi, row, col);
     if (!ready()) return false;
+    const int lane = threadIdx.x & 31;
 #pragma unroll 1
     for (int c = 0; c < CHUNKS; c++, col += 32) {
         float v[32];
         __syncwarp();  // lanes beyond the last row come back
         tmem_ld32(taddr + (uint32_t)(c * 32), v);
         if (c == CHUNKS - 1) release();
+        if (TURN) {
+            if (row - lane < M && col < N)
+                finish_turned<T>(epi, row - lane, (int)min((int64_t)32, M - (row - lane)), col,
+                                 (int)min((int64_t)32, N - col), v, turn);
+            continue;
+        }
         if (whole(col)) {
             const Ahead<T> now = in;
             if (c + 1 < CHUNKS && whole(col + 32)) in.load(epi, row, col + 32);
@@ -201,7 +216,7 @@ __device__ __forceinline__ bool drain(const Epilogue &epi, int64_t M, int64_t N,
     return true;
 }
 
-template <typename T, bool A_MN, bool B_MN>
+template <typename T, bool A_MN, bool B_MN, bool TURN>
 __global__ void __launch_bounds__(kThreads, 1)
 k_linear_tc(const __grid_constant__ CUtensorMap amap, const __grid_constant__ CUtensorMap bmap, int64_t M, int64_t N,
             int kblocks, int splits, const Epilogue epi, unsigned *__restrict__ status) {
@@ -327,13 +342,14 @@ k_linear_tc(const __grid_constant__ CUtensorMap amap, const __grid_constant__ CU
     } else {
         // ------------------------------------------------ epilogue (warps 2-9)
         const int quad = warp & 3, half = (warp - 2) >> 2;  // TMEM lanes 32 quad .. 32 quad + 31, half the columns
+        float *turn = reinterpret_cast<float *>(smem_raw + (base - smem_u32(smem_raw)) + C::STAGES * C::STAGE) + (warp - 2) * 32 * kTurnLd;
         uint32_t it = 0;
         for (int t = blockIdx.x; t < total; t += gridDim.x, it++) {
             const TileAt x = tile_at(t, mt, nt);
             const uint32_t buf = it & 1u, aph = (it >> 1) & 1u;
-            const bool ok = drain<T, BN / 64>(
+            const bool ok = drain<T, BN / 64, TURN>(
                 epi, M, N, (int64_t)x.tm * BM + quad * 32 + lane, (int64_t)x.tn * BN + half * (BN / 2), x.split,
-                tmem + buf * 256u + (uint32_t)(half * (BN / 2)) + ((uint32_t)(quad * 32) << 16),
+                tmem + buf * 256u + (uint32_t)(half * (BN / 2)) + ((uint32_t)(quad * 32) << 16), turn,
                 [&] {
                     const bool in = __all_sync(0xffffffffu, mbar_wait(smem_u32(&bar_accf[buf]), aph, &s_abort, status));
                     tc_fence_after();
@@ -366,6 +382,7 @@ k_linear_tc(const __grid_constant__ CUtensorMap amap, const __grid_constant__ CU
 constexpr int kPairStages = 6;
 constexpr int kPairStage = 2 * BM * BK * 2;  // A and B rows of one CTA
 constexpr int kPairSmem = kPairStages * kPairStage + 1024;
+static_assert(kPairSmem + kTurn + 512 <= 232448 && Cfg::SMEM + kTurn + 512 <= 232448, "shared memory of a block");
 
 __device__ __forceinline__ uint32_t cluster_addr(uint32_t addr, uint32_t rank) {
     uint32_t r;
@@ -443,7 +460,7 @@ __device__ __forceinline__ bool pair_tile(int t0, int t1, int extra, int p, int 
 // FORM: which; the operands' orders and the one product's place are constants but for
 // PAIR_GRADS (read from the arguments for all of them, x W^T took 834 us for 758 at
 // 16384 x 8192 x 4096).
-template <typename T, int FORM>
+template <typename T, int FORM, bool TURN>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
 k_linear_pair(const __grid_constant__ CUtensorMap amap, const __grid_constant__ CUtensorMap bmap, int64_t M0, int64_t N0,
               int kblocks0, const Epilogue epi0, const __grid_constant__ PairSecond two, unsigned *__restrict__ status) {
@@ -579,14 +596,15 @@ k_linear_pair(const __grid_constant__ CUtensorMap amap, const __grid_constant__ 
     } else {
         // ------------------------------------------------ epilogue (warps 2-9), of its CTA's rows
         const int quad = warp & 3, half = (warp - 2) >> 2;
+        float *turn = reinterpret_cast<float *>(smem_raw + (base - smem_u32(smem_raw)) + kPairStages * kPairStage) + (warp - 2) * 32 * kTurnLd;
         uint32_t it = 0;
         for (; next(it); it++) {
             const TileAt x = place();
             const uint32_t buf = it & 1u, aph = (it >> 1) & 1u;
-            const bool ok = drain<T, 4>(
+            const bool ok = drain<T, 4, TURN>(
                 BOTH && job ? two.epi : epi0, BOTH && job ? two.M : M0, BOTH && job ? two.N : N0,
                 (int64_t)x.tm * 2 * BM + rank * BM + quad * 32 + lane, (int64_t)x.tn * 256 + half * 128, 0,
-                tmem + buf * 256u + (uint32_t)(half * 128) + ((uint32_t)(quad * 32) << 16),
+                tmem + buf * 256u + (uint32_t)(half * 128) + ((uint32_t)(quad * 32) << 16), turn,
                 [&] {
                     const bool in = __all_sync(0xffffffffu, mbar_wait(smem_u32(&bar_accf[buf]), aph, &s_abort, status));
                     tc_fence_after();
@@ -799,17 +817,18 @@ size_t part_values(int64_t M, int64_t N, const Plan &p) {
     return p.splits > 1 ? (size_t)p.splits * M * ld_part(N) : 0;
 }
 
-template <typename T, bool A_MN, bool B_MN>
+template <typename T, bool A_MN, bool B_MN, bool TURN>
 cudaError_t launch_tc(const CUtensorMap &a, const CUtensorMap &b, int64_t M, int64_t N, const Plan &p,
                       const Epilogue &epi, bool next, zsolve_seq *s) {
     // attributes once per process (thread-safe initialisation of a local static)
+    constexpr int smem = Cfg::SMEM + (TURN ? kTurn : 0);
     static const cudaError_t attr =
-        cudaFuncSetAttribute(k_linear_tc<T, A_MN, B_MN>, cudaFuncAttributeMaxDynamicSharedMemorySize, Cfg::SMEM);
+        cudaFuncSetAttribute(k_linear_tc<T, A_MN, B_MN, TURN>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
     if (attr != cudaSuccess) return attr;
     const int64_t total = (M + BM - 1) / BM * ((N + BN - 1) / BN) * p.splits;
     s->launches++;
-    return launch(next, k_linear_tc<T, A_MN, B_MN>, (unsigned)std::min<int64_t>(total, s->num_sms), kThreads, Cfg::SMEM,
-                  s->st, a, b, M, N, p.kblocks, p.splits, epi, s->d_status);
+    return launch(next, k_linear_tc<T, A_MN, B_MN, TURN>, (unsigned)std::min<int64_t>(total, s->num_sms), kThreads, smem, s->st,
+                  a, b, M, N, p.kblocks, p.splits, epi, s->d_status);
 }
 
 // D(i, j) = sum_k A(i, k) B(j, k) and the epilogue; a_mn: A is stored k x M, else M x k.
@@ -827,10 +846,11 @@ cudaError_t maps(int type, const Product &p, CUtensorMap *a, CUtensorMap *b) {
 
 // Products whose plan is pairs of SMs: one, or with PAIR_GRADS two; the longer sums
 // first, so that the last round is of short ones.
-template <typename T, int FORM>
-cudaError_t launch_pair(zsolve_seq *s, int type, const Product *p, bool next) {
+template <typename T, int FORM, bool TURN>
+cudaError_t launch_pair_as(zsolve_seq *s, int type, const Product *p, bool next) {
+    constexpr int smem = kPairSmem + (TURN ? kTurn : 0);
     static const cudaError_t attr =
-        cudaFuncSetAttribute(k_linear_pair<T, FORM>, cudaFuncAttributeMaxDynamicSharedMemorySize, kPairSmem);
+        cudaFuncSetAttribute(k_linear_pair<T, FORM, TURN>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
     if (attr != cudaSuccess) return attr;
     constexpr int n = FORM == PAIR_GRADS ? 2 : 1;
     const int first = n == 2 && p[1].K > p[0].K;
@@ -853,8 +873,13 @@ cudaError_t launch_pair(zsolve_seq *s, int type, const Product *p, bool next) {
     }
     const unsigned pairs = (unsigned)std::min<int64_t>(total, s->num_sms / 2);
     s->launches++;
-    return launch(next, k_linear_pair<T, FORM>, 2 * pairs, kThreads, kPairSmem, s->st, ma, mb, q.M, q.N, kblocks(q), q.epi,
-                  two, s->d_status);
+    return launch(next, k_linear_pair<T, FORM, TURN>, 2 * pairs, kThreads, smem, s->st, ma, mb, q.M, q.N, kblocks(q), q.epi, two,
+                  s->d_status);
+}
+template <typename T, int FORM>
+cudaError_t launch_pair(zsolve_seq *s, int type, const Product *p, bool next) {
+    return turned(p[0].epi) || (FORM == PAIR_GRADS && turned(p[1].epi)) ? launch_pair_as<T, FORM, true>(s, type, p, next)
+                                                                        : launch_pair_as<T, FORM, false>(s, type, p, next);
 }
 
 template <typename T>
@@ -869,7 +894,9 @@ cudaError_t product(zsolve_seq *s, int type, Product q, float *part, bool next) 
     if (e != cudaSuccess) return e;
     q.epi.part = p.splits > 1 ? part : nullptr;
     q.epi.ldp = ld_part(q.N);
-#define LIN_GO(AM, BMN) e = launch_tc<T, AM, BMN>(ma, mb, q.M, q.N, p, q.epi, next, s)
+#define LIN_GO(AM, BMN)                                                                        \
+    e = turned(q.epi) ? launch_tc<T, AM, BMN, true>(ma, mb, q.M, q.N, p, q.epi, next, s) \
+                      : launch_tc<T, AM, BMN, false>(ma, mb, q.M, q.N, p, q.epi, next, s)
     if (!q.a_mn && !q.b_mn) LIN_GO(false, false);
     else if (!q.a_mn) LIN_GO(false, true);
     else LIN_GO(true, true);

@@ -152,6 +152,40 @@ __device__ __forceinline__ void finish32(const Epilogue &e, int64_t row, int64_t
     for (int j = 0; j < 4; j++) u.set(v + 8 * j), u.store(reinterpret_cast<T *>(e.y) + row * e.ldy + c + 8 * j);
 }
 
+// 32 x 32 values, a row a lane, of which `rows` x `cols` exist, at rows that start
+// anywhere: turned over in shared memory (32 x kTurnLd floats of the warp's own), so that a
+// warp's accesses are a row's neighbours.
+constexpr int kTurnLd = 33;
+template <typename T>
+__device__ __forceinline__ void finish_turned(const Epilogue &e, int64_t row, int rows, int64_t c, int cols,
+                                              const float (&v)[32], float *turn) {
+    const int lane = threadIdx.x & 31;
+#pragma unroll
+    for (int i = 0; i < 32; i++) turn[lane * kTurnLd + i] = v[i];
+    __syncwarp();
+    const bool in = lane < cols;
+    c += lane;
+    const float bias = e.bias && in ? to_f32(reinterpret_cast<const T *>(e.bias)[c]) : 0.f;
+#pragma unroll 1
+    for (int r = 0; r < rows; r += 8) {
+        float w[8], f[8];
+#pragma unroll
+        for (int u = 0; u < 8; u++) {
+            f[u] = e.r && in && r + u < rows ? to_f32(reinterpret_cast<const T *>(e.r)[(row + r + u) * e.ldr + c]) : 0.f;
+            w[u] = turn[(r + u) * kTurnLd + lane] + bias;
+        }
+        if (e.z)
+#pragma unroll
+            for (int u = 0; u < 8; u++)
+                if (in && r + u < rows) reinterpret_cast<T *>(e.z)[(row + r + u) * e.ldz + c] = from_f32<T>(w[u]);
+        act_all(w, e.act);
+#pragma unroll
+        for (int u = 0; u < 8; u++)
+            if (in && r + u < rows) reinterpret_cast<T *>(e.y)[(row + r + u) * e.ldy + c] = from_f32<T>(w[u] + f[u]);
+    }
+    __syncwarp();  // read before the warp's next values come
+}
+
 }  // namespace zs
 
 // linear_few.cu: y for at most kFewRows rows of x, in one kernel without a workspace.

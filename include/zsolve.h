@@ -550,6 +550,8 @@ typedef struct {
     int64_t tokens;         /* of all sequences together, one after the other */
     const int64_t *offsets; /* device, nseq + 1: sequence i holds the tokens offsets[i] .. offsets[i+1]-1,
                                ascending within 0 .. tokens; equal ones are an empty sequence.
+                               Tokens before the first or after the last sequence are read by
+                               nothing; their outputs and gradients are zero.
                                NULL: every sequence has tokens / nseq */
     const void *q, *k, *v;  /* tokens x heads x d; the heads of a token are packed */
     int64_t ldq, ldk, ldv;  /* distance of two tokens, elements */

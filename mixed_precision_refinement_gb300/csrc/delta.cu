@@ -470,6 +470,10 @@ k_delta_chain(const DeltaGeom geo, const DeltaTerms terms, const float *__restri
     after_previous();
     may_start_next();
     const int c0 = geo.first[si], c1 = geo.first[si + 1];
+    if (OUT)
+        tokens_outside(geo, si, [&](int64_t t0, int64_t t1) {
+            zero_tokens(o + (int64_t)hv * geo.dv + vb, ldo, t0, t1, min(C::COLS, geo.dv - vb), warp, C::NC / 32 + NH);
+        });
 
     if (tid == 0) {
         sm.abort_word = 0;

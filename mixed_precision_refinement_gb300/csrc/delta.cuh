@@ -56,6 +56,14 @@ struct DeltaTerms {
 };
 constexpr int kVec = 5 * kChunk;
 
+// Gradients that the chunks do not write for tokens of no sequence: dq and dk of the key
+// heads, or (not NULL) their parts of the value heads.
+struct DeltaOutside {
+    float *dqp, *dkp;
+    void *dq, *dk;
+    float *dg, *dbeta;
+};
+
 // ---------------------------------------------------------------- products
 
 __device__ __forceinline__ uint32_t tf32(float x) {
@@ -526,7 +534,24 @@ __device__ __forceinline__ void gate_sums(const DeltaGeom &geo, int2 ch, int hv,
     bh[2 * lane + 1] = (float)b1, bl[2 * lane + 1] = (float)(b1 - (double)(float)b1);
 }
 
+// Zeros in `cols` values of the tokens t0 .. t1 - 1 at stride ld, a warp of the nw a token.
+template <typename T>
+__device__ __forceinline__ void zero_tokens(T *p, int64_t ld, int64_t t0, int64_t t1, int cols, int warp, int nw) {
+    for (int64_t t = t0 + warp; t < t1; t += nw)
+        for (int c = threadIdx.x & 31; c < cols; c += 32) p[t * ld + c] = from_f32<T>(0.f);
+}
+
 // ---------------------------------------------------------------- chains
+
+// The tokens that belong to no sequence, whose outputs and gradients are zero: those before
+// the first one, zero(first, end), are for the blocks of the first sequence, those after the
+// last one for its blocks.
+template <typename F>
+__device__ __forceinline__ void tokens_outside(const DeltaGeom &geo, int si, F zero) {
+    const int2 sq = geo.seq[si];
+    if (si == 0) zero((int64_t)0, (int64_t)sq.x);
+    if (si == geo.nseq - 1) zero((int64_t)sq.x + sq.y, geo.tokens);
+}
 
 // Token tile i (of 8) of warp w of WK: dealt so that triangular work is an
 // equal share for every warp.
@@ -662,10 +687,12 @@ cudaError_t zs_launch_delta_chain(int type, const zs::DeltaGeom &g, const zs::De
 // The recurrence backwards (delta_bwd.cu): from the gradients of o and of the
 // last states (ds; NULL: zero), per chunk and value head the gradient of the
 // state after the chunk (dends, dk x dv) and dX (64 x dv), dv, and the
-// gradient of the first states (ds0; NULL: not written).
+// gradient of the first states (ds0; NULL: not written); and zeros for the
+// tokens outside the sequences.
 cudaError_t zs_launch_delta_rchain(int type, const zs::DeltaGeom &g, const zs::DeltaTerms &t, const void *dout,
                                    int64_t lddo, const float *ds, float *dends, float *dxs, void *dv, float *ds0,
-                                   unsigned *status, bool next, cudaStream_t st, int64_t *launches);
+                                   const zs::DeltaOutside &outside, unsigned *status, bool next, cudaStream_t st,
+                                   int64_t *launches);
 // The blocks of either recurrence.
 inline int64_t delta_chain_blocks(const zs::DeltaGeom &g) {
     const int cols = g.dk <= 32 ? 64 : 32;

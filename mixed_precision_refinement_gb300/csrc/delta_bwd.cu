@@ -63,7 +63,7 @@ template <typename T, int DK>
 __global__ void __launch_bounds__(RChainCfg<T, DK>::NT, 1)
 k_delta_rchain(const DeltaGeom geo, const DeltaTerms terms, const T *__restrict__ dout, int64_t lddo,
                const float *__restrict__ ds, float *__restrict__ dends, float *__restrict__ dxs, T *__restrict__ dv,
-               float *__restrict__ ds0, unsigned *__restrict__ status) {
+               float *__restrict__ ds0, const DeltaOutside outside, unsigned *__restrict__ status) {
     using C = RChainCfg<T, DK>;
     constexpr int WK = C::WK, NTILE = C::NTILE;
     constexpr int LD = tile_ld<T>(DK), LDO = tile_ld<T>(C::COLS);
@@ -78,6 +78,21 @@ k_delta_rchain(const DeltaGeom geo, const DeltaTerms terms, const T *__restrict_
     may_start_next();
     const int cols = min(C::COLS, geo.dvp - vb);  // of the block's dO
     const int c0 = geo.first[si], c1 = geo.first[si + 1];
+    tokens_outside(geo, si, [&](int64_t t0, int64_t t1) {
+        constexpr int NW = C::NT / 32;
+        const int64_t nv = (int64_t)geo.hv * geo.dv, at = (int64_t)hv * geo.dk, nk = (int64_t)geo.hk * geo.dk;
+        zero_tokens(dv + (int64_t)hv * geo.dv + vb, nv, t0, t1, min(C::COLS, geo.dv - vb), warp, NW);
+        if (vb > 0) return;
+        zero_tokens(outside.dg + hv, geo.hv, t0, t1, 1, warp, NW);
+        zero_tokens(outside.dbeta + hv, geo.hv, t0, t1, 1, warp, NW);
+        if (outside.dqp) {
+            zero_tokens(outside.dqp + at, (int64_t)geo.hv * geo.dk, t0, t1, geo.dk, warp, NW);
+            zero_tokens(outside.dkp + at, (int64_t)geo.hv * geo.dk, t0, t1, geo.dk, warp, NW);
+        } else {  // as many key heads as value heads
+            zero_tokens((T *)outside.dq + at, nk, t0, t1, geo.dk, warp, NW);
+            zero_tokens((T *)outside.dk + at, nk, t0, t1, geo.dk, warp, NW);
+        }
+    });
 
     if (tid == 0) {
         sm.abort_word = 0;
@@ -697,7 +712,8 @@ k_delta_join(const float *__restrict__ dqp, const float *__restrict__ dkp, int64
 
 template <typename T, int DK>
 cudaError_t rchain_dk(const DeltaGeom &g, const DeltaTerms &t, const void *dout, int64_t lddo, const float *ds,
-                      float *dends, float *dxs, void *dv, float *ds0, unsigned *status, bool next, cudaStream_t st) {
+                      float *dends, float *dxs, void *dv, float *ds0, const DeltaOutside &outside, unsigned *status,
+                      bool next, cudaStream_t st) {
     using C = RChainCfg<T, DK>;
     static_assert(sizeof(RChainSmem<T, DK>) <= 232448, "shared memory of a block");
     static const cudaError_t attr = cudaFuncSetAttribute(
@@ -705,7 +721,7 @@ cudaError_t rchain_dk(const DeltaGeom &g, const DeltaTerms &t, const void *dout,
     if (attr != cudaSuccess) return attr;
     const dim3 grid((unsigned)(g.nseq * g.hv), (unsigned)((g.dv + C::COLS - 1) / C::COLS));
     return launch(next, k_delta_rchain<T, DK>, grid, C::NT, sizeof(RChainSmem<T, DK>), st, g, t, (const T *)dout, lddo, ds, dends,
-                  dxs, (T *)dv, ds0, status);
+                  dxs, (T *)dv, ds0, outside, status);
 }
 
 template <typename T, int DK>
@@ -724,10 +740,11 @@ cudaError_t grads_dk(const DeltaGeom &g, const DeltaTerms &t, const void *dout, 
 }  // namespace
 
 cudaError_t zs_launch_delta_rchain(int type, const DeltaGeom &g, const DeltaTerms &t, const void *dout, int64_t lddo,
-                                   const float *ds, float *dends, float *dxs, void *dv, float *ds0, unsigned *status,
-                                   bool next, cudaStream_t st, int64_t *launches) {
+                                   const float *ds, float *dends, float *dxs, void *dv, float *ds0,
+                                   const DeltaOutside &outside, unsigned *status, bool next, cudaStream_t st,
+                                   int64_t *launches) {
     ++*launches;
-    return DELTA_TYPE(rchain_dk, g, t, dout, lddo, ds, dends, dxs, dv, ds0, status, next, st);
+    return DELTA_TYPE(rchain_dk, g, t, dout, lddo, ds, dends, dxs, dv, ds0, outside, status, next, st);
 }
 
 cudaError_t zs_launch_delta_grads(int type, const DeltaGeom &g, const DeltaTerms &t, const void *dout, int64_t lddo,

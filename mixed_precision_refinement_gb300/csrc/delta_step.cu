@@ -43,6 +43,11 @@ k_delta_step(const DeltaGeom geo, const int64_t *__restrict__ offsets, const flo
         const int64_t len = geo.tokens / geo.nseq;
         t0 = si * len, t1 = t0 + len;
     }
+    // tokens outside the sequences: their outputs are zero
+    T *oh = o + (int64_t)hv * geo.dv + blockIdx.y * kCols;
+    const int cols = min(kCols, geo.dv - (int)blockIdx.y * kCols);
+    if (si == 0 && t0 > 0) zero_tokens(oh, ldo, 0, t0, cols, warp, NW);
+    if (si == geo.nseq - 1 && t1 < geo.tokens) zero_tokens(oh, ldo, t1 > t0 ? t1 : t0, geo.tokens, cols, warp, NW);
     float S[NR][VE];
 #pragma unroll
     for (int p = 0; p < NR; p++) {

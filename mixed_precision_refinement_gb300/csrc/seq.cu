@@ -421,7 +421,8 @@ int zsolve_delta_bwd(zsolve_seq *s, const zsolve_delta_args *a, const void *dout
     SEQ_CU(zs_launch_delta_plan(a->offsets, a->nseq, a->tokens, w.nchunks, w.first, w.seq, w.chunk, s->st, &s->launches));
     if (a->tokens > 0) SEQ_CU(zs_launch_delta_terms(a->type, g, w.terms, true, s->st, &s->launches));
     auto backwards = [&](bool next, cudaStream_t on) {
-        return zs_launch_delta_rchain(a->type, g, w.terms, w.dout, w.lddo, ds, w.dends, w.dxs, dv, ds0, s->d_status, next, on,
+        return zs_launch_delta_rchain(a->type, g, w.terms, w.dout, w.lddo, ds, w.dends, w.dxs, dv, ds0,
+                                      zs::DeltaOutside{w.dqp, w.dkp, dq, dk, dg, dbeta}, s->d_status, next, on,
                                       &s->launches);
     };
     // the states and U once more: keeping them from the forward pass would hold 96 KB a chunk and head

@@ -13,11 +13,34 @@ __device__ __forceinline__ float sigmoid(float x) { return __fdividef(1.f, 1.f +
 // cancellation of 1 + tanh u for negative u.
 constexpr float kTanhC = 0.7978845608028654f, kTanhA = 0.044715f;
 
+// The exact form in the Gaussian's upper tail Q(y) = erfc(y / sqrt 2) / 2 of y = |z|: 1 + erf
+// would leave no digits of a negative z's value.  With relu and sign,
+//   z Phi(z) = relu(z) - y Q(y),  its slope = w or 1 - w, w = Q(y) - y phi(y),
+// and Q(y) = exp(-y^2 / 2) gauss_tail(y): a smooth function between 1/2 and 0.03, here the
+// polynomial of degree 7 in 1 / (1 + 0.35 y) whose largest relative error over 0 .. 14 is
+// least (3e-7; 6e-7 in float32).  8192 x 8192 x 1024: 143 us, as with erff; with
+// erfcf 212.
+constexpr float kTailEnd = 16.f;  // from here on exp(-y^2 / 2) is 0
+__device__ __forceinline__ float gauss_tail(float y) {
+    const float t = __fdividef(1.f, fmaf(0.35f, y, 1.f));
+    float p = 0.0489424467f;
+    p = fmaf(p, t, -0.202119291f);
+    p = fmaf(p, t, 0.240640819f);
+    p = fmaf(p, t, -0.0170234367f);
+    p = fmaf(p, t, 0.155961484f);
+    p = fmaf(p, t, 0.133355096f);
+    p = fmaf(p, t, 0.140270337f);
+    return fmaf(p, t, -2.73155492e-05f);
+}
+
 template <int ACT>
 __device__ __forceinline__ float act1(float z) {
     if (ACT == ACT_RELU) return z <= 0.f ? 0.f : z;
     if (ACT == ACT_SILU) return __fdividef(z, 1.f + __expf(-z));
-    if (ACT == ACT_GELU) return 0.5f * z * (1.f + erff(z * 0.7071067811865476f));
+    if (ACT == ACT_GELU) {
+        const float y = fminf(fabsf(z), kTailEnd);
+        return fmaf(-y * __expf(-0.5f * y * y), gauss_tail(y), z <= 0.f ? 0.f : z);
+    }
     if (ACT == ACT_GELU_TANH) return __fdividef(z, 1.f + __expf(-2.f * kTanhC * fmaf(kTanhA * z * z, z, z)));
     return z;
 }
@@ -28,8 +51,11 @@ __device__ __forceinline__ float slope1(float z) {
         const float p = sigmoid(z);
         return p * fmaf(z, 1.f - p, 1.f);
     }
-    if (ACT == ACT_GELU)
-        return fmaf(z * 0.3989422804014327f, __expf(-0.5f * z * z), 0.5f * (1.f + erff(z * 0.7071067811865476f)));
+    if (ACT == ACT_GELU) {
+        const float y = fabsf(z) > kTailEnd ? kTailEnd : fabsf(z);  // NaN stays
+        const float w = __expf(-0.5f * y * y) * fmaf(-0.3989422804014327f, y, gauss_tail(y));
+        return z < 0.f ? w : 1.f - w;
+    }
     if (ACT == ACT_GELU_TANH) {
         const float p = sigmoid(2.f * kTanhC * fmaf(kTanhA * z * z, z, z));
         return fmaf(2.f * kTanhC * fmaf(3.f * kTanhA * z, z, 1.f), z * p * (1.f - p), p);

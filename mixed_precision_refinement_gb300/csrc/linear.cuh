@@ -58,7 +58,9 @@ __device__ __forceinline__ float slope1(float z) {
     }
     if (ACT == ACT_GELU_TANH) {
         const float p = sigmoid(2.f * kTanhC * fmaf(kTanhA * z * z, z, z));
-        return fmaf(2.f * kTanhC * fmaf(3.f * kTanhA * z, z, 1.f), z * p * (1.f - p), p);
+        // beyond 32 p (1 - p) is 0, and z^2 may be infinite
+        const float y = fminf(fmaxf(z, -32.f), 32.f);
+        return fmaf(2.f * kTanhC * fmaf(3.f * kTanhA * y, y, 1.f), y * p * (1.f - p), p);
     }
     return 1.f;
 }

@@ -59,3 +59,16 @@ def test_tails(seq, act, dtype, rows):
     dx, _, db = seq.linear_bwd(one.expand(rows, 1).contiguous(), z, one, z, act=act)
     err = (dx.double() - slope).abs()
     assert bool((err <= tol * size * (1 + 2 * u) + (2 * u + u * u) * slope.abs() + 3 * STEP[dtype] + lost).all())
+
+
+@pytest.mark.parametrize("act", ["relu", "silu", "gelu", "gelu_tanh"])
+def test_very_large_values(seq, act):
+    """Where z^2 or z^3 is no longer a float32: the values are z and 0, the slopes 1 and 0."""
+    import torch
+    z = torch.tensor([1e4, 1e15, 1e20, 3e38], device="cuda").bfloat16()[:, None]
+    z = torch.cat([z, -z])
+    one = torch.ones(1, 1, device="cuda", dtype=torch.bfloat16)
+    y = seq.linear(z, one, act=act)
+    assert torch.equal(y[:4], z[:4]) and not y[4:].any()
+    dx, _, _ = seq.linear_bwd(torch.full_like(z, 3.0), z, one, z, act=act)
+    assert bool((dx[:4] == 3.0).all()) and not dx[4:].any()

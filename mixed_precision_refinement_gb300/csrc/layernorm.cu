@@ -4,9 +4,12 @@
 //   backward: a = dy w, dx = rs (a - mean a - h mean(a h)),
 //             dw = sum over rows of dy h, db = sum over rows of dy
 // Both are bound by HBM: each reads its inputs once and holds a row in
-// registers between the reductions and the output.  All sums are float32; the
-// variance is taken around the mean in a second pass over the registers, so a
-// large common offset of a row costs no digits.
+// registers between the reductions and the output.  All sums are float32.  The
+// mean's own error, which grows with a row's common offset, is found again in
+// the second pass over the registers: with m the float32 sum over d and
+// e = mean (x - m), mu = m + e and mean (x - mu)^2 = mean (x - m)^2 - e^2, so h
+// and rs lose no digits to an offset.  The backward pass has mu rounded to a
+// float32, half a unit of its last place.
 #include <algorithm>
 
 #include "seq.cuh"
@@ -77,11 +80,19 @@ __device__ __forceinline__ void load_ws(const void *w, int wf32, int i, float *f
     }
 }
 
+// rs from mean (x - m)^2 and e = mean (x - m), whose square is at most the former but for
+// rounding (NaN stays).
+__device__ __forceinline__ float inv_std(float square, float e, float eps) {
+    const float var = fmaf(-e, e, square);
+    return 1.f / sqrtf((var < 0.f ? 0.f : var) + eps);
+}
+
 // Forward: TPR threads hold a row, VE consecutive values at a time (VE = 1
 // where rows are not 16-byte aligned), NI times; four rows a block of 128 threads
-// where a warp holds one, else a row a block.  8 rows of 2048: 2.4 us, a launch;
-// 32768 x 4096 bfloat16 107 us, 5.0 TB/s, bound by its instructions (3.2 of the 4
-// issued a cycle: conversions, two passes of sums, the output).  A ring of rows as
+// where a warp holds one, else a row a block.  8 rows of 2048: 2.2 us, a launch;
+// 32768 x 4096 bfloat16 111 us, 4.8 TB/s, bound by its instructions (3.2 of the 4
+// issued a cycle: conversions, two passes of sums, the output; 107 us of it without the
+// second reduction's sum of x - m).  A ring of rows as
 // in the backward pass and packed float32 instructions were both slower: they
 // take registers, and with them warps.
 template <typename T, int VE, int TPR, int NI>
@@ -113,7 +124,7 @@ k_layernorm(const T *__restrict__ x, int64_t ldx, const void *__restrict__ w, co
     }
     const float inv = 1.f / (float)d;
     const float mu = row_sum<TPR>(s, red, 0).x * inv;
-    float q = 0.f;
+    s = make_float2(0.f, 0.f);
 #pragma unroll
     for (int i = 0; i < NI; i++) {
         const int c = (i * TPR + t) * VE;
@@ -121,14 +132,16 @@ k_layernorm(const T *__restrict__ x, int64_t ldx, const void *__restrict__ w, co
 #pragma unroll
             for (int e = 0; e < VE; e++) {
                 const float z = v[i * VE + e] - mu;
-                q = fmaf(z, z, q);
+                s.x = fmaf(z, z, s.x);
+                s.y += z;
+                v[i * VE + e] = z;
             }
         }
     }
-    const float var = row_sum<TPR>(make_float2(q, 0.f), red, 1).x * inv;
-    const float rs = 1.f / sqrtf(var + eps);
+    s = row_sum<TPR>(s, red, 1);
+    const float off = s.y * inv, rs = inv_std(s.x * inv, off, eps), shift = -off * rs;
     if (t == 0) {
-        if (mean) mean[row] = mu;
+        if (mean) mean[row] = mu + off;
         if (rstd) rstd[row] = rs;
     }
     T *yr = y + row * ldy;
@@ -138,7 +151,7 @@ k_layernorm(const T *__restrict__ x, int64_t ldx, const void *__restrict__ w, co
         if (c < d) {
             float o[VE], f[VE];
 #pragma unroll
-            for (int e = 0; e < VE; e++) o[e] = (v[i * VE + e] - mu) * rs;
+            for (int e = 0; e < VE; e++) o[e] = fmaf(v[i * VE + e], rs, shift);
             if (w) {
                 load_wv<T, VE>(w, wf32, c, f);
 #pragma unroll
@@ -170,17 +183,20 @@ k_layernorm_long(const T *__restrict__ x, int64_t ldx, const void *__restrict__ 
     float s = 0.f, q = 0.f;
     for (int64_t c = threadIdx.x; c < d; c += kLongThreads) s += to_f32(xr[c]);
     const float mu = row_sum<kLongThreads>(make_float2(s, 0.f), red, 0).x / (float)d;
+    s = 0.f;
     for (int64_t c = threadIdx.x; c < d; c += kLongThreads) {
         const float z = to_f32(xr[c]) - mu;
         q = fmaf(z, z, q);
+        s += z;
     }
-    const float rs = 1.f / sqrtf(row_sum<kLongThreads>(make_float2(q, 0.f), red, 1).x / (float)d + eps);
+    const float2 r = row_sum<kLongThreads>(make_float2(q, s), red, 1);
+    const float off = r.y / (float)d, rs = inv_std(r.x / (float)d, off, eps), shift = -off * rs;
     if (threadIdx.x == 0) {
-        if (mean) mean[row] = mu;
+        if (mean) mean[row] = mu + off;
         if (rstd) rstd[row] = rs;
     }
     for (int64_t c = threadIdx.x; c < d; c += kLongThreads) {
-        float o = (to_f32(xr[c]) - mu) * rs;
+        float o = fmaf(to_f32(xr[c]) - mu, rs, shift);
         if (w) o *= load_w<T>(w, wf32, c);
         if (b) o += load_w<T>(b, wf32, c);
         y[row * ldy + c] = from_f32<T>(o);

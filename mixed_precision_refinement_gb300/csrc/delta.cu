@@ -132,7 +132,7 @@ struct Block {
 
 template <typename T, int DK>
 __global__ void __launch_bounds__(kTermThreads, 2)
-k_delta_terms(const DeltaGeom geo, const DeltaTerms out) {
+k_delta_terms(const DeltaGeom geo, const DeltaTerms out, T *__restrict__ o, int64_t ldo) {
     extern __shared__ __align__(16) uint8_t smem_raw[];
     TermSmem<T, DK> &sm = *reinterpret_cast<TermSmem<T, DK> *>(smem_raw);
     constexpr bool EXACT = sizeof(T) == 2;
@@ -140,9 +140,16 @@ k_delta_terms(const DeltaGeom geo, const DeltaTerms out) {
     after_previous();
     may_start_next();
     const int2 ch = geo.chunk[blockIdx.x];
-    const int n = ch.y;
-    if (n == 0) return;
-    const int hk = blockIdx.y, tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    const int n = ch.y, hk = blockIdx.y;
+    if (n == 0) {
+        const int cols = geo.hv / geo.hk * geo.dv;
+        if (o)
+            tokens_outside(geo, blockIdx.x, [&](int64_t t0, int64_t t1, int worker, int workers) {
+                zero_tokens(o + (int64_t)hk * cols, ldo, t0, t1, cols, worker, workers);
+            });
+        return;
+    }
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const int g = lane >> 2, t = lane & 3;
     load_tile<T, DK, kTermThreads>(sm.k, (const T *)geo.k + (int64_t)ch.x * geo.ldk + (int64_t)hk * geo.dkp, geo.ldk, n, geo.dkp);
     load_tile<T, DK, kTermThreads>(sm.q, (const T *)geo.q + (int64_t)ch.x * geo.ldq + (int64_t)hk * geo.dkp, geo.ldq, n, geo.dkp);
@@ -386,14 +393,7 @@ struct ChainSmem {
     int abort_word;
 };
 
-// Element (v, token) of X^T and U^T as the groups leave them in shared memory.
-struct PairAt {
-    const float4 *x;
-    __device__ __forceinline__ float operator()(int v, int j) const {
-        const float *p = reinterpret_cast<const float *>(x + v * kLdPair + j / 2) + (j & 1);
-        return p[0] + p[2];
-    }
-};
+// Element (v, token) of U^T as the groups leave it for the outputs.
 struct PlainAt {
     const float2 *u;
     __device__ __forceinline__ float operator()(int v, int j) const {
@@ -470,10 +470,6 @@ k_delta_chain(const DeltaGeom geo, const DeltaTerms terms, const float *__restri
     after_previous();
     may_start_next();
     const int c0 = geo.first[si], c1 = geo.first[si + 1];
-    if (OUT)
-        tokens_outside(geo, si, [&](int64_t t0, int64_t t1) {
-            zero_tokens(o + (int64_t)hv * geo.dv + vb, ldo, t0, t1, min(C::COLS, geo.dv - vb), warp, C::NC / 32 + NH);
-        });
 
     if (tid == 0) {
         sm.abort_word = 0;
@@ -748,12 +744,12 @@ k_delta_chain(const DeltaGeom geo, const DeltaTerms terms, const float *__restri
 }
 
 template <typename T, int DK>
-cudaError_t terms_dk(const DeltaGeom &g, const DeltaTerms &t, bool next, cudaStream_t st) {
+cudaError_t terms_dk(const DeltaGeom &g, const DeltaTerms &t, void *o, int64_t ldo, bool next, cudaStream_t st) {
     const size_t smem = sizeof(TermSmem<T, DK>);
     static const cudaError_t attr = cudaFuncSetAttribute(
         k_delta_terms<T, DK>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)sizeof(TermSmem<T, DK>));
     if (attr != cudaSuccess) return attr;
-    return launch(next, k_delta_terms<T, DK>, dim3(g.nchunks, g.hk), kTermThreads, smem, st, g, t);
+    return launch(next, k_delta_terms<T, DK>, dim3(g.nchunks, g.hk), kTermThreads, smem, st, g, t, (T *)o, ldo);
 }
 
 template <typename T, int DK>
@@ -799,10 +795,10 @@ cudaError_t zs_launch_delta_pack(int type, const void *src, int64_t ld, int64_t 
     return cudaGetLastError();
 }
 
-cudaError_t zs_launch_delta_terms(int type, const DeltaGeom &g, const DeltaTerms &t, bool next, cudaStream_t st,
-                                  int64_t *launches) {
+cudaError_t zs_launch_delta_terms(int type, const DeltaGeom &g, const DeltaTerms &t, void *o, int64_t ldo, bool next,
+                                  cudaStream_t st, int64_t *launches) {
     ++*launches;
-    return DELTA_TYPE(terms_dk, g, t, next, st);
+    return DELTA_TYPE(terms_dk, g, t, o, ldo, next, st);
 }
 
 cudaError_t zs_launch_delta_chain(int type, const DeltaGeom &g, const DeltaTerms &t, const float *s0, void *o,

@@ -56,14 +56,6 @@ struct DeltaTerms {
 };
 constexpr int kVec = 5 * kChunk;
 
-// Gradients that the chunks do not write for tokens of no sequence: dq and dk of the key
-// heads, or (not NULL) their parts of the value heads.
-struct DeltaOutside {
-    float *dqp, *dkp;
-    void *dq, *dk;
-    float *dg, *dbeta;
-};
-
 // ---------------------------------------------------------------- products
 
 __device__ __forceinline__ uint32_t tf32(float x) {
@@ -356,6 +348,15 @@ __device__ __forceinline__ void put_pair(float4 *p, float a, float b) {
         *p = split_pair(a, b);
 }
 
+// Element (v, token) of split pairs in shared memory.
+struct PairAt {
+    const float4 *x;
+    __device__ __forceinline__ float operator()(int v, int j) const {
+        const float *p = reinterpret_cast<const float *>(x + v * kLdPair + j / 2) + (j & 1);
+        return p[0] + p[2];
+    }
+};
+
 // r[j] = Y X over the chunk's 64 tokens: Y 16 x 64 from put_pair, X(tokens, key
 // columns d0 + 8 j ..) of the tile, each sum from zero.
 template <typename T, int LD>
@@ -534,24 +535,26 @@ __device__ __forceinline__ void gate_sums(const DeltaGeom &geo, int2 ch, int hv,
     bh[2 * lane + 1] = (float)b1, bl[2 * lane + 1] = (float)(b1 - (double)(float)b1);
 }
 
-// Zeros in `cols` values of the tokens t0 .. t1 - 1 at stride ld, a warp of the nw a token.
+// The tokens that belong to no sequence, before the first and after the last, have outputs
+// and gradients that are zero.  The blocks of the chunk table's unused entries, of which
+// `chunk` is one, write them (there is one at least where the sequences come from offsets),
+// each its share of the tokens: zero(t0, t1, worker, workers), a worker a warp.
+template <typename F>
+__device__ __forceinline__ void tokens_outside(const DeltaGeom &geo, int chunk, F zero) {
+    const int used = geo.first[geo.nseq], warps = blockDim.x >> 5;
+    const int worker = (chunk - used) * warps + (threadIdx.x >> 5), workers = (geo.nchunks - used) * warps;
+    const int2 last = geo.seq[geo.nseq - 1];
+    zero((int64_t)0, (int64_t)geo.seq[0].x, worker, workers);
+    zero((int64_t)last.x + last.y, geo.tokens, worker, workers);
+}
+// Zeros in `cols` values of the tokens t0 .. t1 - 1 at stride ld.
 template <typename T>
-__device__ __forceinline__ void zero_tokens(T *p, int64_t ld, int64_t t0, int64_t t1, int cols, int warp, int nw) {
-    for (int64_t t = t0 + warp; t < t1; t += nw)
+__device__ __forceinline__ void zero_tokens(T *p, int64_t ld, int64_t t0, int64_t t1, int cols, int worker, int workers) {
+    for (int64_t t = t0 + worker; t < t1; t += workers)
         for (int c = threadIdx.x & 31; c < cols; c += 32) p[t * ld + c] = from_f32<T>(0.f);
 }
 
 // ---------------------------------------------------------------- chains
-
-// The tokens that belong to no sequence, whose outputs and gradients are zero: those before
-// the first one, zero(first, end), are for the blocks of the first sequence, those after the
-// last one for its blocks.
-template <typename F>
-__device__ __forceinline__ void tokens_outside(const DeltaGeom &geo, int si, F zero) {
-    const int2 sq = geo.seq[si];
-    if (si == 0) zero((int64_t)0, (int64_t)sq.x);
-    if (si == geo.nseq - 1) zero((int64_t)sq.x + sq.y, geo.tokens);
-}
 
 // Token tile i (of 8) of warp w of WK: dealt so that triangular work is an
 // equal share for every warp.
@@ -675,8 +678,9 @@ cudaError_t zs_launch_delta_plan(const int64_t *offsets, int nseq, int64_t token
 // tokens x heads x d values at token stride ld into packed heads of dp values
 cudaError_t zs_launch_delta_pack(int type, const void *src, int64_t ld, int64_t tokens, int heads, int d, int dp,
                                  void *dst, int num_sms, cudaStream_t st, int64_t *launches);
-cudaError_t zs_launch_delta_terms(int type, const zs::DeltaGeom &g, const zs::DeltaTerms &t, bool next, cudaStream_t st,
-                                  int64_t *launches);
+// The chunks' terms; and zeros in o (NULL: none) for the tokens outside the sequences.
+cudaError_t zs_launch_delta_terms(int type, const zs::DeltaGeom &g, const zs::DeltaTerms &t, void *o, int64_t ldo, bool next,
+                                  cudaStream_t st, int64_t *launches);
 // The recurrence over the chunks.  o (NULL: not formed), sn (the last states;
 // NULL: not written); states, us (NULL: not kept): the state each chunk
 // starts from (per chunk and value head dk x dv) and U (64 x dv).  status: a
@@ -687,24 +691,23 @@ cudaError_t zs_launch_delta_chain(int type, const zs::DeltaGeom &g, const zs::De
 // The recurrence backwards (delta_bwd.cu): from the gradients of o and of the
 // last states (ds; NULL: zero), per chunk and value head the gradient of the
 // state after the chunk (dends, dk x dv) and dX (64 x dv), dv, and the
-// gradient of the first states (ds0; NULL: not written); and zeros for the
-// tokens outside the sequences.
+// gradient of the first states (ds0; NULL: not written).
 cudaError_t zs_launch_delta_rchain(int type, const zs::DeltaGeom &g, const zs::DeltaTerms &t, const void *dout,
                                    int64_t lddo, const float *ds, float *dends, float *dxs, void *dv, float *ds0,
-                                   const zs::DeltaOutside &outside, unsigned *status, bool next, cudaStream_t st,
-                                   int64_t *launches);
+                                   unsigned *status, bool next, cudaStream_t st, int64_t *launches);
 // The blocks of either recurrence.
 inline int64_t delta_chain_blocks(const zs::DeltaGeom &g) {
     const int cols = g.dk <= 32 ? 64 : 32;
     return (int64_t)g.nseq * g.hv * ((g.dv + cols - 1) / cols);
 }
-// The gradients that the chunks give on their own.  parts (tokens x hv x dk
+// The gradients that the chunks give on their own, and zeros in all of them (dv too) for
+// the tokens outside the sequences.  parts (tokens x hv x dk
 // float32, one for dq and one for dk) are needed where value heads share a key
 // head; dq, dk: tokens x hk x dk.
 cudaError_t zs_launch_delta_grads(int type, const zs::DeltaGeom &g, const zs::DeltaTerms &t, const void *dout,
                                   int64_t lddo, const float *states, const float *dends, const float *us,
-                                  const float *dxs, float *dqp, float *dkp, void *dq, void *dk, float *dg,
-                                  float *dbeta, bool next, cudaStream_t st, int64_t *launches);
+                                  const float *dxs, float *dqp, float *dkp, void *dq, void *dk, void *dv,
+                                  float *dg, float *dbeta, bool next, cudaStream_t st, int64_t *launches);
 // Token by token (delta_step.cu): every sequence's tokens one after the other.
 cudaError_t zs_launch_delta_step(int type, const zs::DeltaGeom &g, const int64_t *offsets, const float *s0, void *o,
                                  int64_t ldo, float *sn, cudaStream_t st, int64_t *launches);

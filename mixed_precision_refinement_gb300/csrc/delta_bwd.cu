@@ -63,7 +63,7 @@ template <typename T, int DK>
 __global__ void __launch_bounds__(RChainCfg<T, DK>::NT, 1)
 k_delta_rchain(const DeltaGeom geo, const DeltaTerms terms, const T *__restrict__ dout, int64_t lddo,
                const float *__restrict__ ds, float *__restrict__ dends, float *__restrict__ dxs, T *__restrict__ dv,
-               float *__restrict__ ds0, const DeltaOutside outside, unsigned *__restrict__ status) {
+               float *__restrict__ ds0, unsigned *__restrict__ status) {
     using C = RChainCfg<T, DK>;
     constexpr int WK = C::WK, NTILE = C::NTILE;
     constexpr int LD = tile_ld<T>(DK), LDO = tile_ld<T>(C::COLS);
@@ -78,21 +78,6 @@ k_delta_rchain(const DeltaGeom geo, const DeltaTerms terms, const T *__restrict_
     may_start_next();
     const int cols = min(C::COLS, geo.dvp - vb);  // of the block's dO
     const int c0 = geo.first[si], c1 = geo.first[si + 1];
-    tokens_outside(geo, si, [&](int64_t t0, int64_t t1) {
-        constexpr int NW = C::NT / 32;
-        const int64_t nv = (int64_t)geo.hv * geo.dv, at = (int64_t)hv * geo.dk, nk = (int64_t)geo.hk * geo.dk;
-        zero_tokens(dv + (int64_t)hv * geo.dv + vb, nv, t0, t1, min(C::COLS, geo.dv - vb), warp, NW);
-        if (vb > 0) return;
-        zero_tokens(outside.dg + hv, geo.hv, t0, t1, 1, warp, NW);
-        zero_tokens(outside.dbeta + hv, geo.hv, t0, t1, 1, warp, NW);
-        if (outside.dqp) {
-            zero_tokens(outside.dqp + at, (int64_t)geo.hv * geo.dk, t0, t1, geo.dk, warp, NW);
-            zero_tokens(outside.dkp + at, (int64_t)geo.hv * geo.dk, t0, t1, geo.dk, warp, NW);
-        } else {  // as many key heads as value heads
-            zero_tokens((T *)outside.dq + at, nk, t0, t1, geo.dk, warp, NW);
-            zero_tokens((T *)outside.dk + at, nk, t0, t1, geo.dk, warp, NW);
-        }
-    });
 
     if (tid == 0) {
         sm.abort_word = 0;
@@ -383,7 +368,7 @@ __global__ void __launch_bounds__(GradCfg<T, DK>::NT, 1)
 k_delta_grads(const DeltaGeom geo, const DeltaTerms terms, const T *__restrict__ dout, int64_t lddo,
               const float *__restrict__ states, const float *__restrict__ dends, const float *__restrict__ us,
               const float *__restrict__ dxs, float *__restrict__ dqp, float *__restrict__ dkp, T *__restrict__ dq,
-              T *__restrict__ dk, float *__restrict__ dg, float *__restrict__ dbeta, int vecv) {
+              T *__restrict__ dk, T *__restrict__ dv, float *__restrict__ dg, float *__restrict__ dbeta, int vecv) {
     using C = GradCfg<T, DK>;
     constexpr int NG = C::NG, MG = C::MG, MT = C::MT, NT = C::NT, PT = C::PT, LD = C::LD;
     constexpr bool EXACT = sizeof(T) == 2;
@@ -392,9 +377,23 @@ k_delta_grads(const DeltaGeom geo, const DeltaTerms terms, const T *__restrict__
     after_previous();
     may_start_next();
     const int2 ch = geo.chunk[blockIdx.x];
-    const int n = ch.y;
-    if (n == 0) return;
-    const int hv = blockIdx.y, hk = hv / (geo.hv / geo.hk);
+    const int n = ch.y, hv = blockIdx.y, hk = hv / (geo.hv / geo.hk);
+    if (n == 0) {
+        tokens_outside(geo, blockIdx.x, [&](int64_t t0, int64_t t1, int worker, int workers) {
+            const int64_t at = (int64_t)hv * geo.dk, nk = (int64_t)geo.hv * geo.dk;
+            zero_tokens(dv + (int64_t)hv * geo.dv, (int64_t)geo.hv * geo.dv, t0, t1, geo.dv, worker, workers);
+            zero_tokens(dg + hv, geo.hv, t0, t1, 1, worker, workers);
+            zero_tokens(dbeta + hv, geo.hv, t0, t1, 1, worker, workers);
+            if (dqp) {
+                zero_tokens(dqp + at, nk, t0, t1, geo.dk, worker, workers);
+                zero_tokens(dkp + at, nk, t0, t1, geo.dk, worker, workers);
+            } else {  // as many key heads as value heads
+                zero_tokens(dq + at, nk, t0, t1, geo.dk, worker, workers);
+                zero_tokens(dk + at, nk, t0, t1, geo.dk, worker, workers);
+            }
+        });
+        return;
+    }
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g = lane >> 2, t = lane & 3;
     const int wm = warp % MG, wn = warp / MG, m0 = wm * 16 * MT, d0 = wn * 32, p0 = wn * PT * 8;
     const int64_t slot = (int64_t)blockIdx.x * geo.hv + hv;
@@ -712,8 +711,7 @@ k_delta_join(const float *__restrict__ dqp, const float *__restrict__ dkp, int64
 
 template <typename T, int DK>
 cudaError_t rchain_dk(const DeltaGeom &g, const DeltaTerms &t, const void *dout, int64_t lddo, const float *ds,
-                      float *dends, float *dxs, void *dv, float *ds0, const DeltaOutside &outside, unsigned *status,
-                      bool next, cudaStream_t st) {
+                      float *dends, float *dxs, void *dv, float *ds0, unsigned *status, bool next, cudaStream_t st) {
     using C = RChainCfg<T, DK>;
     static_assert(sizeof(RChainSmem<T, DK>) <= 232448, "shared memory of a block");
     static const cudaError_t attr = cudaFuncSetAttribute(
@@ -721,38 +719,38 @@ cudaError_t rchain_dk(const DeltaGeom &g, const DeltaTerms &t, const void *dout,
     if (attr != cudaSuccess) return attr;
     const dim3 grid((unsigned)(g.nseq * g.hv), (unsigned)((g.dv + C::COLS - 1) / C::COLS));
     return launch(next, k_delta_rchain<T, DK>, grid, C::NT, sizeof(RChainSmem<T, DK>), st, g, t, (const T *)dout, lddo, ds, dends,
-                  dxs, (T *)dv, ds0, outside, status);
+                  dxs, (T *)dv, ds0, status);
 }
 
 template <typename T, int DK>
 cudaError_t grads_dk(const DeltaGeom &g, const DeltaTerms &t, const void *dout, int64_t lddo, const float *states,
                      const float *dends, const float *us, const float *dxs, float *dqp, float *dkp, void *dq, void *dk,
-                     float *dg, float *dbeta, bool next, cudaStream_t st) {
+                     void *dv, float *dg, float *dbeta, bool next, cudaStream_t st) {
     using C = GradCfg<T, DK>;
     static_assert(sizeof(GradSmem<T, DK>) <= 232448, "shared memory of a block");
     static const cudaError_t attr = cudaFuncSetAttribute(
         k_delta_grads<T, DK>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)sizeof(GradSmem<T, DK>));
     if (attr != cudaSuccess) return attr;
     return launch(next, k_delta_grads<T, DK>, dim3(g.nchunks, g.hv), C::NT, sizeof(GradSmem<T, DK>), st, g, t, (const T *)dout,
-                  lddo, states, dends, us, dxs, dqp, dkp, (T *)dq, (T *)dk, dg, dbeta, (int)(g.dv % 4 == 0));
+                  lddo, states, dends, us, dxs, dqp, dkp, (T *)dq, (T *)dk, (T *)dv, dg, dbeta, (int)(g.dv % 4 == 0));
 }
 
 }  // namespace
 
 cudaError_t zs_launch_delta_rchain(int type, const DeltaGeom &g, const DeltaTerms &t, const void *dout, int64_t lddo,
-                                   const float *ds, float *dends, float *dxs, void *dv, float *ds0,
-                                   const DeltaOutside &outside, unsigned *status, bool next, cudaStream_t st,
-                                   int64_t *launches) {
+                                   const float *ds, float *dends, float *dxs, void *dv, float *ds0, unsigned *status,
+                                   bool next, cudaStream_t st, int64_t *launches) {
     ++*launches;
-    return DELTA_TYPE(rchain_dk, g, t, dout, lddo, ds, dends, dxs, dv, ds0, outside, status, next, st);
+    return DELTA_TYPE(rchain_dk, g, t, dout, lddo, ds, dends, dxs, dv, ds0, status, next, st);
 }
 
 cudaError_t zs_launch_delta_grads(int type, const DeltaGeom &g, const DeltaTerms &t, const void *dout, int64_t lddo,
                                   const float *states, const float *dends, const float *us, const float *dxs,
-                                  float *dqp, float *dkp, void *dq, void *dk, float *dg, float *dbeta, bool next,
+                                  float *dqp, float *dkp, void *dq, void *dk, void *dv,
+                                  float *dg, float *dbeta, bool next,
                                   cudaStream_t st, int64_t *launches) {
     ++*launches;
-    cudaError_t e = DELTA_TYPE(grads_dk, g, t, dout, lddo, states, dends, us, dxs, dqp, dkp, dq, dk, dg, dbeta, next, st);
+    cudaError_t e = DELTA_TYPE(grads_dk, g, t, dout, lddo, states, dends, us, dxs, dqp, dkp, dq, dk, dv, dg, dbeta, next, st);
     if (e != cudaSuccess || !dqp) return e;
     const int64_t n = g.tokens * g.hk * g.dk;
     const unsigned blocks = (unsigned)std::min<int64_t>((n + 255) / 256, 152 * 16);

@@ -152,7 +152,7 @@ struct DeltaWork {
         return (((uintptr_t)p | (uint64_t)ld * e | (uint64_t)d * e) & 15) == 0;
     }
     void carve(zs::Carve &c, const zsolve_delta_args *a) {
-        const size_t slots = (size_t)nchunks * a->hv, sq = (size_t)zs::kSquare;
+        const size_t slots = (size_t)(nchunks - (a->offsets ? 1 : 0)) * a->hv, sq = (size_t)zs::kSquare;
         first = c.take<int>((size_t)a->nseq + 1);
         seq = c.take<int2>((size_t)a->nseq);
         chunk = c.take<int2>((size_t)nchunks);
@@ -179,7 +179,8 @@ struct DeltaWork {
         // a sequence's last chunk may be short: one more each at most
         const int64_t most = a->tokens / zs::kChunk + a->nseq;
         if (most > 0x7fffffff / zs::kChunk) return seq_fail(s, ZSOLVE_EINVAL, "too many chunks");
-        nchunks = (int)most;
+        // and an unused entry, whose blocks write what belongs to the tokens outside the offsets
+        nchunks = (int)most + (a->offsets ? 1 : 0);
         zs::Carve size(nullptr);
         carve(size, a);
         int st = ZSOLVE_OK;
@@ -383,7 +384,7 @@ int zsolve_delta(zsolve_seq *s, const zsolve_delta_args *a, void *o, int64_t ldo
     if (st == ZSOLVE_OK) st = w.bind(s, a, &g);
     if (st != ZSOLVE_OK) return st;
     SEQ_CU(zs_launch_delta_plan(a->offsets, a->nseq, a->tokens, w.nchunks, w.first, w.seq, w.chunk, s->st, &s->launches));
-    SEQ_CU(zs_launch_delta_terms(a->type, g, w.terms, true, s->st, &s->launches));
+    SEQ_CU(zs_launch_delta_terms(a->type, g, w.terms, o, ldo, true, s->st, &s->launches));
     SEQ_CU(zs_launch_delta_chain(a->type, g, w.terms, a->s0, o, ldo, sn, nullptr, nullptr, s->d_status, true, s->st,
                                  &s->launches));
     return ZSOLVE_OK;
@@ -419,10 +420,9 @@ int zsolve_delta_bwd(zsolve_seq *s, const zsolve_delta_args *a, const void *dout
     if (st == ZSOLVE_OK) st = w.bind(s, a, &g);
     if (st != ZSOLVE_OK) return st;
     SEQ_CU(zs_launch_delta_plan(a->offsets, a->nseq, a->tokens, w.nchunks, w.first, w.seq, w.chunk, s->st, &s->launches));
-    if (a->tokens > 0) SEQ_CU(zs_launch_delta_terms(a->type, g, w.terms, true, s->st, &s->launches));
+    if (a->tokens > 0) SEQ_CU(zs_launch_delta_terms(a->type, g, w.terms, nullptr, 0, true, s->st, &s->launches));
     auto backwards = [&](bool next, cudaStream_t on) {
-        return zs_launch_delta_rchain(a->type, g, w.terms, w.dout, w.lddo, ds, w.dends, w.dxs, dv, ds0,
-                                      zs::DeltaOutside{w.dqp, w.dkp, dq, dk, dg, dbeta}, s->d_status, next, on,
+        return zs_launch_delta_rchain(a->type, g, w.terms, w.dout, w.lddo, ds, w.dends, w.dxs, dv, ds0, s->d_status, next, on,
                                       &s->launches);
     };
     // the states and U once more: keeping them from the forward pass would hold 96 KB a chunk and head
@@ -455,7 +455,7 @@ int zsolve_delta_bwd(zsolve_seq *s, const zsolve_delta_args *a, const void *dout
         SEQ_CU(backwards(true, s->st));
     }
     SEQ_CU(zs_launch_delta_grads(a->type, g, w.terms, w.dout, w.lddo, w.states, w.dends, w.us, w.dxs, w.dqp, w.dkp, dq, dk,
-                                 dg, dbeta, !both, s->st, &s->launches));
+                                 dv, dg, dbeta, !both, s->st, &s->launches));
     return ZSOLVE_OK;
 }
 

@@ -59,6 +59,16 @@ struct RChainSmem {
     int abort_word;
 };
 
+// One value of a triangular product over later tokens: the sum of x(j) m[j ld] over the tokens j
+// from `from` on.
+template <typename FX>
+__device__ __forceinline__ float later_again(FX x, const float *m, int ld, int from) {
+    float sum = 0.f;
+#pragma unroll 1
+    for (int j = from; j < kChunk; j++) sum = fmaf(x(j), m[j * ld], sum);
+    return sum;
+}
+
 template <typename T, int DK>
 __global__ void __launch_bounds__(RChainCfg<T, DK>::NT, 1)
 k_delta_rchain(const DeltaGeom geo, const DeltaTerms terms, const T *__restrict__ dout, int64_t lddo,
@@ -189,6 +199,23 @@ k_delta_rchain(const DeltaGeom geo, const DeltaTerms terms, const T *__restrict_
             u[0] = split_pair(fmaf(ev.x, lo.x, du[i][0]), fmaf(ev.y, lo.y, du[i][1]));
             u[8 * kLdPair] = split_pair(fmaf(ev.x, hi.x, du[i][2]), fmaf(ev.y, hi.y, du[i][3]));
         }
+        // An infinity or NaN in dO is in the gradients of its token and those before it; in a
+        // tile on the diagonal the zeros of P (and below of T) have made NaN of it for those
+        // after it.  Put right as in the forward pass: one value at a time, from memory.
+        if (not_finite(du)) {
+#pragma unroll 1
+            for (int b = 0; b < 4 * NTILE; b++) {
+                const int r = g + (b & 2) * 4, n = tile_of<WK>(w, b >> 2) * 8 + 2 * t + (b & 1);
+                if (isfinite(PairAt{sm.u[grp]}(r, n))) continue;
+                const T *dot = st.dout + grp * 16 + r;
+                float sum = later_again([&](int j) { return to_f32(dot[j * LDO]); }, st.tp + n * kLdT, 1, n), lo = 0.f;
+                for (int p = 0; p < WK; p++) lo += sm.part[grp][p][r * kLdT + n];
+                sum = fmaf(st.vec[kChunk + n], lo, sum);
+                float *p = reinterpret_cast<float *>(sm.u[grp] + r * kLdPair + n / 2) + (n & 1);
+                p[0] = __uint_as_float(tf32(sum));
+                p[2] = __uint_as_float(tf32(sum - p[0]));
+            }
+        }
         group_sync<WK>(grp);
         // dX^T = dU^T T at the warp's token tiles: T's rows from the tile on
         {
@@ -221,6 +248,19 @@ k_delta_rchain(const DeltaGeom geo, const DeltaTerms terms, const T *__restrict_
                             dv[((int64_t)(ch.x + tok) * geo.hv + hv) * geo.dv + vc] =
                                 from_f32<T>((e & 1 ? bv.y : bv.x) * v[e]);
                     }
+                }
+            }
+            // dS needs no repair: its value column is not finite either way
+            if (not_finite(x)) {
+#pragma unroll 1
+                for (int b = 0; b < 4 * NTILE; b++) {
+                    const int r = g + (b & 2) * 4, n = tile_of<WK>(w, b >> 2) * 8 + 2 * t + (b & 1), vc = v0 + r;
+                    float *p = dxs + (slot * kChunk + n) * geo.dv + vc;
+                    if (vc >= geo.dv || isfinite(*p)) continue;
+                    const PairAt u{sm.u[grp]};
+                    *p = u(r, n) + later_again([&](int j) { return u(r, j); }, st.tp + n, kLdT, n + 1);
+                    if (n < ch.y)
+                        dv[((int64_t)(ch.x + n) * geo.hv + hv) * geo.dv + vc] = from_f32<T>(st.vec[2 * kChunk + n] * *p);
                 }
             }
         }

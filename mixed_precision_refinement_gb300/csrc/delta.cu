@@ -746,8 +746,8 @@ k_delta_chain(const DeltaGeom geo, const DeltaTerms terms, const float *__restri
 template <typename T, int DK>
 cudaError_t terms_dk(const DeltaGeom &g, const DeltaTerms &t, void *o, int64_t ldo, bool next, cudaStream_t st) {
     const size_t smem = sizeof(TermSmem<T, DK>);
-    static const cudaError_t attr = cudaFuncSetAttribute(
-        k_delta_terms<T, DK>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)sizeof(TermSmem<T, DK>));
+    static OncePerDevice limit;
+    const cudaError_t attr = smem_limit(limit, k_delta_terms<T, DK>, (int)sizeof(TermSmem<T, DK>));
     if (attr != cudaSuccess) return attr;
     return launch(next, k_delta_terms<T, DK>, dim3(g.nchunks, g.hk), kTermThreads, smem, st, g, t, (T *)o, ldo);
 }
@@ -760,14 +760,14 @@ cudaError_t chain_dk(const DeltaGeom &g, const DeltaTerms &t, const float *s0, v
     const size_t smem = sizeof(ChainSmem<T, DK>);
     const dim3 grid((unsigned)(g.nseq * g.hv), (unsigned)((g.dv + 16 * C::NV - 1) / (16 * C::NV)));
     if (o) {
-        static const cudaError_t attr = cudaFuncSetAttribute(
-            k_delta_chain<T, DK, true>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)sizeof(ChainSmem<T, DK>));
+        static OncePerDevice limit;
+        const cudaError_t attr = smem_limit(limit, k_delta_chain<T, DK, true>, (int)sizeof(ChainSmem<T, DK>));
         if (attr != cudaSuccess) return attr;
         return launch(next, k_delta_chain<T, DK, true>, grid, C::NC + 32 * helpers<true>(), smem, st, g, t, s0, (T *)o, ldo, sn,
                       states, us, (int)mult16(o, ldo, g.dv, sizeof(T)), status);
     } else {
-        static const cudaError_t attr = cudaFuncSetAttribute(
-            k_delta_chain<T, DK, false>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)sizeof(ChainSmem<T, DK>));
+        static OncePerDevice limit;
+        const cudaError_t attr = smem_limit(limit, k_delta_chain<T, DK, false>, (int)sizeof(ChainSmem<T, DK>));
         if (attr != cudaSuccess) return attr;
         return launch(next, k_delta_chain<T, DK, false>, grid, C::NC + 32 * helpers<false>(), smem, st, g, t, s0, (T *)nullptr,
                       (int64_t)0, sn, states, us, 0, status);

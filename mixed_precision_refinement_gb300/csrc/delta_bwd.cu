@@ -754,8 +754,8 @@ cudaError_t rchain_dk(const DeltaGeom &g, const DeltaTerms &t, const void *dout,
                       float *dends, float *dxs, void *dv, float *ds0, unsigned *status, bool next, cudaStream_t st) {
     using C = RChainCfg<T, DK>;
     static_assert(sizeof(RChainSmem<T, DK>) <= 232448, "shared memory of a block");
-    static const cudaError_t attr = cudaFuncSetAttribute(
-        k_delta_rchain<T, DK>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)sizeof(RChainSmem<T, DK>));
+    static OncePerDevice limit;
+    const cudaError_t attr = smem_limit(limit, k_delta_rchain<T, DK>, (int)sizeof(RChainSmem<T, DK>));
     if (attr != cudaSuccess) return attr;
     const dim3 grid((unsigned)(g.nseq * g.hv), (unsigned)((g.dv + C::COLS - 1) / C::COLS));
     return launch(next, k_delta_rchain<T, DK>, grid, C::NT, sizeof(RChainSmem<T, DK>), st, g, t, (const T *)dout, lddo, ds, dends,
@@ -768,8 +768,8 @@ cudaError_t grads_dk(const DeltaGeom &g, const DeltaTerms &t, const void *dout, 
                      void *dv, float *dg, float *dbeta, bool next, cudaStream_t st) {
     using C = GradCfg<T, DK>;
     static_assert(sizeof(GradSmem<T, DK>) <= 232448, "shared memory of a block");
-    static const cudaError_t attr = cudaFuncSetAttribute(
-        k_delta_grads<T, DK>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)sizeof(GradSmem<T, DK>));
+    static OncePerDevice limit;
+    const cudaError_t attr = smem_limit(limit, k_delta_grads<T, DK>, (int)sizeof(GradSmem<T, DK>));
     if (attr != cudaSuccess) return attr;
     return launch(next, k_delta_grads<T, DK>, dim3(g.nchunks, g.hv), C::NT, sizeof(GradSmem<T, DK>), st, g, t, (const T *)dout,
                   lddo, states, dends, us, dxs, dqp, dkp, (T *)dq, (T *)dk, (T *)dv, dg, dbeta, (int)(g.dv % 4 == 0));

@@ -580,8 +580,8 @@ cudaError_t launch_bwd(int64_t rows, int d, const T *dy, int64_t lddy, const T *
 #define LN_RING(TPR, E)                                                                                             \
     do {                                                                                                           \
         constexpr int kMost = 2 * kRing * ring_row<T>((TPR) * (E)) * (int)sizeof(T) + (TPR) * (E) * 4;               \
-        static const cudaError_t attr = cudaFuncSetAttribute(                                                      \
-            k_layernorm_bwd_ring<T, VE, TPR, (E) / VE>, cudaFuncAttributeMaxDynamicSharedMemorySize, kMost);        \
+        static OncePerDevice limit;                                                                                \
+        const cudaError_t attr = smem_limit(limit, k_layernorm_bwd_ring<T, VE, TPR, (E) / VE>, kMost);             \
         if (attr != cudaSuccess) return attr;                                                                      \
         const int64_t per_sm = std::max<int64_t>(1, std::min<int64_t>(ring_threads<E>() / (TPR), 227 * 1024 / (smem + 1536))); \
         *blocks = std::min({*blocks, rows, per_sm * num_sms});                                                     \

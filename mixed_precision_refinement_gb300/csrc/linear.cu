@@ -820,10 +820,9 @@ size_t part_values(int64_t M, int64_t N, const Plan &p) {
 template <typename T, bool A_MN, bool B_MN, bool TURN>
 cudaError_t launch_tc(const CUtensorMap &a, const CUtensorMap &b, int64_t M, int64_t N, const Plan &p,
                       const Epilogue &epi, bool next, zsolve_seq *s) {
-    // attributes once per process (thread-safe initialisation of a local static)
     constexpr int smem = Cfg::SMEM + (TURN ? kTurn : 0);
-    static const cudaError_t attr =
-        cudaFuncSetAttribute(k_linear_tc<T, A_MN, B_MN, TURN>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+    static OncePerDevice limit;
+    const cudaError_t attr = smem_limit(limit, k_linear_tc<T, A_MN, B_MN, TURN>, smem);
     if (attr != cudaSuccess) return attr;
     const int64_t total = (M + BM - 1) / BM * ((N + BN - 1) / BN) * p.splits;
     s->launches++;
@@ -849,8 +848,8 @@ cudaError_t maps(int type, const Product &p, CUtensorMap *a, CUtensorMap *b) {
 template <typename T, int FORM, bool TURN>
 cudaError_t launch_pair_as(zsolve_seq *s, int type, const Product *p, bool next) {
     constexpr int smem = kPairSmem + (TURN ? kTurn : 0);
-    static const cudaError_t attr =
-        cudaFuncSetAttribute(k_linear_pair<T, FORM, TURN>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+    static OncePerDevice limit;
+    const cudaError_t attr = smem_limit(limit, k_linear_pair<T, FORM, TURN>, smem);
     if (attr != cudaSuccess) return attr;
     constexpr int n = FORM == PAIR_GRADS ? 2 : 1;
     const int first = n == 2 && p[1].K > p[0].K;

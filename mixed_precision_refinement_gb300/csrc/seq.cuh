@@ -10,6 +10,7 @@
 
 #include <vector>
 
+#include "device_once.h"
 #include "zsolve.h"
 
 struct zsolve_seq {
@@ -208,8 +209,6 @@ __device__ __forceinline__ void bulk_load(void *dst, const void *src, uint32_t b
                  : "memory");
 }
 
-// Two float32 operations in one instruction, each rounded on its own: half the
-// issue slots where those are what a kernel runs out of.
 // A kernel that follows another of the same call is launched with `next`: its blocks
 // may be set up while the one before still runs, and wait in after_previous() until
 // all of that one's results are there.  Every kernel that is launched so, or before
@@ -232,6 +231,22 @@ inline cudaError_t launch(bool next, void (*kernel)(P...), dim3 grid, int thread
     return cudaLaunchKernelEx(&cfg, kernel, P(args)...);
 }
 
+// The kernel's limit of dynamic shared memory, which holds for the current device alone; a
+// launcher keeps one OncePerDevice for each of its kernels.
+template <typename K>
+inline cudaError_t smem_limit(OncePerDevice &once, K kernel, int bytes) {
+    int dev = 0;
+    const cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess) return e;
+    return once.run(dev, [&] {
+        const cudaError_t r = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+        if (r != cudaSuccess) cudaGetLastError();  // told here, and not by the next launch
+        return r;
+    });
+}
+
+// Two float32 operations in one instruction, each rounded on its own: half the
+// issue slots where those are what a kernel runs out of.
 __device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
     float2 d;
     asm("{\n\t.reg .b64 x, y, z, w;\n\t"

@@ -8,7 +8,7 @@ from __future__ import annotations
 
 import ctypes
 
-from . import ZSOLVE_OK, ZsolveError, _lib
+from . import ZSOLVE_ETIMEOUT, ZSOLVE_OK, ZsolveError, _lib
 
 ZSOLVE_F32 = 0
 ZSOLVE_BF16 = 1
@@ -297,6 +297,9 @@ def _state(s, a):
 class Seq:
     """Owns one handle of the sequence-layer operators; runs on torch's current stream.
 
+    The calls enqueue their work and return.  A device-side wait that gives up (after about a second, so
+    never on a GPU that works) leaves outputs that are not to be used: check() and close() raise for it.
+
     Example (x: bfloat16 CUDA tensor, tokens x d)::
 
         with Seq() as s:
@@ -381,16 +384,33 @@ class Seq:
         zsolve_delta_step(self.seq, q, k, v, g, beta, o.view(v.shape), s_out, s, None, scale)
         return o, s_out
 
+    def check(self):
+        """Waits for the handle's work; raises if a device-side wait has given up since the last check."""
+        zsolve_seq_check(self.seq)
+
     def close(self):
-        if self.seq:
-            zsolve_seq_destroy(self.seq)
-            self.seq = None
+        """Releases the handle (after the work in flight); raises, once released, as check() does."""
+        if not self.seq:
+            return
+        error = None
+        try:
+            zsolve_seq_check(self.seq)
+        except ZsolveError as e:
+            error = e if e.status == ZSOLVE_ETIMEOUT else None  # what else fails here is not the outputs'
+        zsolve_seq_destroy(self.seq)
+        self.seq = None
+        if error is not None:
+            raise error
 
     def __enter__(self):
         return self
 
-    def __exit__(self, *exc):
-        self.close()
+    def __exit__(self, kind, *exc):
+        try:
+            self.close()
+        except ZsolveError:
+            if kind is None:  # else the block's own exception goes on
+                raise
 
     def __del__(self):
         try:

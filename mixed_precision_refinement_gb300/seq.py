@@ -19,13 +19,15 @@ ZSOLVE_ACTS = {"none": 0, "relu": 1, "silu": 2, "gelu": 3, "gelu_tanh": 4}
 
 torch = None  # imported with the first handle: the rest of the package loads without it
 _TYPES = {}
+_device = None  # torch's current device, an index
 
 
 def _use_torch():
-    global torch
+    global torch, _device
     if torch is None:
         import torch as module
         torch = module
+        _device = getattr(torch._C, "_cuda_getDevice", None) or torch.cuda.current_device
         _TYPES.update({torch.float32: ZSOLVE_F32, torch.bfloat16: ZSOLVE_BF16, torch.float16: ZSOLVE_F16})
 
 
@@ -37,14 +39,14 @@ def _type(t, name) -> int:
 
 
 def _cuda(t, name):
-    if not t.is_cuda:
-        raise ValueError(f"{name}: expected a CUDA tensor")
+    """Refuses a tensor that is not on the current device, which the library holds to be the handle's."""
+    if t.get_device() != _device():
+        raise ValueError(f"{name}: expected a CUDA tensor on the current device, {_device()}, got one on {t.device}")
 
 
 def _rows(t, name, dtype=None, shape=None):
     """(pointer, rows, d, row stride) of a matrix: a tensor (..., d) whose rows lie at one distance."""
-    if not t.is_cuda:
-        raise ValueError(f"{name}: expected a CUDA tensor")
+    _cuda(t, name)
     if dtype is not None and t.dtype != dtype:
         raise TypeError(f"{name}: expected {dtype}, got {t.dtype}")
     size = t.shape
@@ -71,16 +73,21 @@ def _flat(t, name):
         raise ValueError(f"{name}: the rows must lie at one distance") from None
 
 
-def _vector(t, name, n, dtype):
-    """Pointer of a contiguous vector of n values, or 0 for None."""
+def _vector(t, name, n, dtype, lead=None, last=()):
+    """Pointer of n contiguous values, or 0 for None.  With `lead` and `last`, in the order of a tensor of the
+    sizes lead + last: flat, or any shape that ends as `last` does and, with as many sizes before, begins as `lead`."""
     if t is None:
         return 0
-    if not t.is_cuda:
-        raise ValueError(f"{name}: expected a CUDA tensor")
+    _cuda(t, name)
     if t.dtype != dtype:
         raise TypeError(f"{name}: expected {dtype}, got {t.dtype}")
     if t.numel() != n or not t.is_contiguous():
         raise ValueError(f"{name}: expected {n} contiguous values, got {tuple(t.shape)}")
+    dim = t.dim()
+    if dim > 1 and lead is not None:
+        j = min(len(last), dim - 1)
+        if (j and t.shape[-j:] != last[-j:]) or (dim == len(lead) + len(last) and t.shape[:len(lead)] != lead):
+            raise ValueError(f"{name}: expected {tuple(lead) + tuple(last)}, got {tuple(t.shape)}")
     return t.data_ptr()
 
 
@@ -156,8 +163,8 @@ def zsolve_layernorm(seq, x, w, b, eps, y, mean=None, rstd=None) -> None:
     wt = _norm_weights(x, w, b)
     _check_seq(seq, _lib.zsolve_layernorm(seq, _type(x, "x"), _TYPES[wt], m, d, xp, ldx, _vector(w, "w", d, wt),
                                           _vector(b, "b", d, wt), eps, yp, ldy,
-                                          _vector(mean, "mean", m, torch.float32),
-                                          _vector(rstd, "rstd", m, torch.float32)))
+                                          _vector(mean, "mean", m, torch.float32, x.shape[:-1]),
+                                          _vector(rstd, "rstd", m, torch.float32, x.shape[:-1])))
 
 
 def zsolve_layernorm_bwd(seq, dy, x, mean, rstd, w, dx, dw=None, db=None) -> None:
@@ -167,8 +174,8 @@ def zsolve_layernorm_bwd(seq, dy, x, mean, rstd, w, dx, dw=None, db=None) -> Non
     dxp, _, _, lddx = _rows(dx, "dx", x.dtype, (m, d))
     wt = _norm_weights(x, w, dw if dw is not None else db)
     _check_seq(seq, _lib.zsolve_layernorm_bwd(seq, _type(x, "x"), _TYPES[wt], m, d, dyp, lddy, xp, ldx,
-                                              _vector(mean, "mean", m, torch.float32),
-                                              _vector(rstd, "rstd", m, torch.float32), _vector(w, "w", d, wt), dxp,
+                                              _vector(mean, "mean", m, torch.float32, x.shape[:-1]),
+                                              _vector(rstd, "rstd", m, torch.float32, x.shape[:-1]), _vector(w, "w", d, wt), dxp,
                                               lddx, _vector(dw, "dw", d, wt), _vector(db, "db", d, wt)))
 
 
@@ -238,12 +245,20 @@ def _tokens(t, name, dtype=None, shape=None):
     return t.data_ptr(), n, h, d, t.stride(0) if n > 1 else h * d
 
 
+def _like(t, name, other):
+    """Refuses other sequences x tokens than those of `other`."""
+    if t.dim() == other.dim() and t.shape[:-2] != other.shape[:-2]:
+        raise ValueError(f"{name}: expected the tokens {tuple(other.shape[:-2])}, got {tuple(t.shape[:-2])}")
+
+
 def _delta_args(q, k, v, g, beta, s0, offsets, scale):
     qp, n, hk, dk, ldq = _tokens(q, "q")
     kp, _, _, _, ldk = _tokens(k, "k", q.dtype, (n, hk, dk))
     vp, _, hv, dv, ldv = _tokens(v, "v", q.dtype)
-    if v.shape[:-2] != q.shape[:-2]:
-        raise ValueError(f"v: expected the tokens of q, {tuple(q.shape[:-2])}, got {tuple(v.shape[:-2])}")
+    lead = q.shape[:-2]
+    _like(k, "k", q)
+    if v.shape[:-2] != lead:
+        raise ValueError(f"v: expected the tokens of q, {tuple(lead)}, got {tuple(v.shape[:-2])}")
     if offsets is not None:
         nseq = offsets.numel() - 1
         if nseq < 0:
@@ -252,8 +267,9 @@ def _delta_args(q, k, v, g, beta, s0, offsets, scale):
         nseq = q.shape[0] if q.dim() == 4 else 1
     a = zsolve_delta_args(_type(q, "q"), hk, hv, dk, dv, nseq, n,
                           _vector(offsets, "offsets", nseq + 1, torch.int64) or None, qp, kp, vp, ldq, ldk, ldv,
-                          _vector(g, "g", n * hv, torch.float32), _vector(beta, "beta", n * hv, torch.float32),
-                          _vector(s0, "s0", nseq * hv * dk * dv, torch.float32),
+                          _vector(g, "g", n * hv, torch.float32, lead, (hv,)),
+                          _vector(beta, "beta", n * hv, torch.float32, lead, (hv,)),
+                          _vector(s0, "s0", nseq * hv * dk * dv, torch.float32, (nseq,), (hv, dk, dv)),
                           dk ** -0.5 if scale is None else scale)
     return a
 
@@ -268,6 +284,7 @@ def zsolve_delta(seq, q, k, v, g, beta, o, s=None, s0=None, offsets=None, scale=
     """
     a = _delta_args(q, k, v, g, beta, s0, offsets, scale)
     op, _, _, _, ldo = _tokens(o, "o", q.dtype, (a.tokens, a.hv, a.dv))
+    _like(o, "o", v)
     _check_seq(seq, _lib.zsolve_delta(seq, ctypes.byref(a), op, ldo, _state(s, a)))
 
 
@@ -275,6 +292,7 @@ def zsolve_delta_step(seq, q, k, v, g, beta, o, s=None, s0=None, offsets=None, s
     """As zsolve_delta, token by token: for one or a few tokens a sequence."""
     a = _delta_args(q, k, v, g, beta, s0, offsets, scale)
     op, _, _, _, ldo = _tokens(o, "o", q.dtype, (a.tokens, a.hv, a.dv))
+    _like(o, "o", v)
     _check_seq(seq, _lib.zsolve_delta_step(seq, ctypes.byref(a), op, ldo, _state(s, a)))
 
 
@@ -283,15 +301,19 @@ def zsolve_delta_bwd(seq, dout, q, k, v, g, beta, dq, dk, dv, dg, dbeta, ds0=Non
     """dq .. dbeta and ds0 (shapes of q .. beta and s0, contiguous) from dout (as o) and ds (as s, or None)."""
     a = _delta_args(q, k, v, g, beta, s0, offsets, scale)
     op, _, _, _, lddo = _tokens(dout, "dout", q.dtype, (a.tokens, a.hv, a.dv))
+    _like(dout, "dout", v)
+    lead = q.shape[:-2]
     nk, nv, n = a.tokens * a.hk * a.dk, a.tokens * a.hv * a.dv, a.tokens * a.hv
-    _check_seq(seq, _lib.zsolve_delta_bwd(seq, ctypes.byref(a), op, lddo, _state(ds, a), _vector(dq, "dq", nk, q.dtype),
-                                          _vector(dk, "dk", nk, q.dtype), _vector(dv, "dv", nv, q.dtype),
-                                          _vector(dg, "dg", n, torch.float32),
-                                          _vector(dbeta, "dbeta", n, torch.float32), _state(ds0, a)))
+    _check_seq(seq, _lib.zsolve_delta_bwd(seq, ctypes.byref(a), op, lddo, _state(ds, a), 
+                                          _vector(dq, "dq", nk, q.dtype, lead, (a.hk, a.dk)),
+                                          _vector(dk, "dk", nk, q.dtype, lead, (a.hk, a.dk)),
+                                          _vector(dv, "dv", nv, q.dtype, lead, (a.hv, a.dv)),
+                                          _vector(dg, "dg", n, torch.float32, lead, (a.hv,)),
+                                          _vector(dbeta, "dbeta", n, torch.float32, lead, (a.hv,)), _state(ds0, a)))
 
 
 def _state(s, a):
-    return _vector(s, "s", a.nseq * a.hv * a.dk * a.dv, torch.float32)
+    return _vector(s, "s", a.nseq * a.hv * a.dk * a.dv, torch.float32, (a.nseq,), (a.hv, a.dk, a.dv))
 
 
 class Seq:

@@ -20,14 +20,17 @@ ZSOLVE_ACTS = {"none": 0, "relu": 1, "silu": 2, "gelu": 3, "gelu_tanh": 4}
 torch = None  # imported with the first handle: the rest of the package loads without it
 _TYPES = {}
 _device = None  # torch's current device, an index
+_only = -2  # the device of a process that has one, where no tensor is on another
 
 
 def _use_torch():
-    global torch, _device
+    global torch, _device, _only
     if torch is None:
         import torch as module
         torch = module
         _device = getattr(torch._C, "_cuda_getDevice", None) or torch.cuda.current_device
+        if torch.cuda.device_count() == 1:
+            _only = 0
         _TYPES.update({torch.float32: ZSOLVE_F32, torch.bfloat16: ZSOLVE_BF16, torch.float16: ZSOLVE_F16})
 
 
@@ -46,7 +49,8 @@ def _cuda(t, name):
 
 def _rows(t, name, dtype=None, shape=None):
     """(pointer, rows, d, row stride) of a matrix: a tensor (..., d) whose rows lie at one distance."""
-    _cuda(t, name)
+    if t.get_device() != _only:
+        _cuda(t, name)
     if dtype is not None and t.dtype != dtype:
         raise TypeError(f"{name}: expected {dtype}, got {t.dtype}")
     size = t.shape
@@ -73,22 +77,33 @@ def _flat(t, name):
         raise ValueError(f"{name}: the rows must lie at one distance") from None
 
 
-def _vector(t, name, n, dtype, lead=None, last=()):
-    """Pointer of n contiguous values, or 0 for None.  With `lead` and `last`, in the order of a tensor of the
-    sizes lead + last: flat, or any shape that ends as `last` does and, with as many sizes before, begins as `lead`."""
+def _vector(t, name, n, dtype, shape=None, last=0):
+    """Pointer of n contiguous values, or 0 for None; with a shape, in its order, of which `last` sizes are a token's."""
     if t is None:
         return 0
-    _cuda(t, name)
+    if t.get_device() != _only:
+        _cuda(t, name)
     if t.dtype != dtype:
         raise TypeError(f"{name}: expected {dtype}, got {t.dtype}")
-    if t.numel() != n or not t.is_contiguous():
+    if shape is None or t.shape != shape:
+        if t.numel() != n:
+            raise ValueError(f"{name}: expected {n} contiguous values, got {tuple(t.shape)}")
+        if shape is not None:
+            _same_order(t, name, shape, last)
+    if not t.is_contiguous():
         raise ValueError(f"{name}: expected {n} contiguous values, got {tuple(t.shape)}")
-    dim = t.dim()
-    if dim > 1 and lead is not None:
-        j = min(len(last), dim - 1)
-        if (j and t.shape[-j:] != last[-j:]) or (dim == len(lead) + len(last) and t.shape[:len(lead)] != lead):
-            raise ValueError(f"{name}: expected {tuple(lead) + tuple(last)}, got {tuple(t.shape)}")
     return t.data_ptr()
+
+
+def _same_order(t, name, shape, last):
+    """Refuses a shape of as many values whose order is not that of `shape`: it is flat, or ends as `shape` does and,
+    with as many sizes before the last ones, begins so too."""
+    dim = t.dim()
+    if dim < 2:
+        return
+    j = min(last, dim - 1)
+    if (j and t.shape[-j:] != shape[-j:]) or (dim == len(shape) and t.shape != shape):
+        raise ValueError(f"{name}: expected {tuple(shape)}, got {tuple(t.shape)}")
 
 
 def _current_stream() -> int:
@@ -161,10 +176,11 @@ def zsolve_layernorm(seq, x, w, b, eps, y, mean=None, rstd=None) -> None:
     xp, m, d, ldx = _rows(x, "x")
     yp, _, _, ldy = _rows(y, "y", x.dtype, (m, d))
     wt = _norm_weights(x, w, b)
+    rows = (m,) if x.dim() == 2 else x.shape[:-1]
     _check_seq(seq, _lib.zsolve_layernorm(seq, _type(x, "x"), _TYPES[wt], m, d, xp, ldx, _vector(w, "w", d, wt),
                                           _vector(b, "b", d, wt), eps, yp, ldy,
-                                          _vector(mean, "mean", m, torch.float32, x.shape[:-1]),
-                                          _vector(rstd, "rstd", m, torch.float32, x.shape[:-1])))
+                                          _vector(mean, "mean", m, torch.float32, rows),
+                                          _vector(rstd, "rstd", m, torch.float32, rows)))
 
 
 def zsolve_layernorm_bwd(seq, dy, x, mean, rstd, w, dx, dw=None, db=None) -> None:
@@ -173,9 +189,10 @@ def zsolve_layernorm_bwd(seq, dy, x, mean, rstd, w, dx, dw=None, db=None) -> Non
     dyp, _, _, lddy = _rows(dy, "dy", x.dtype, (m, d))
     dxp, _, _, lddx = _rows(dx, "dx", x.dtype, (m, d))
     wt = _norm_weights(x, w, dw if dw is not None else db)
+    rows = (m,) if x.dim() == 2 else x.shape[:-1]
     _check_seq(seq, _lib.zsolve_layernorm_bwd(seq, _type(x, "x"), _TYPES[wt], m, d, dyp, lddy, xp, ldx,
-                                              _vector(mean, "mean", m, torch.float32, x.shape[:-1]),
-                                              _vector(rstd, "rstd", m, torch.float32, x.shape[:-1]), _vector(w, "w", d, wt), dxp,
+                                              _vector(mean, "mean", m, torch.float32, rows),
+                                              _vector(rstd, "rstd", m, torch.float32, rows), _vector(w, "w", d, wt), dxp,
                                               lddx, _vector(dw, "dw", d, wt), _vector(db, "db", d, wt)))
 
 
@@ -225,12 +242,16 @@ class zsolve_delta_args(ctypes.Structure):
                 ("scale", ctypes.c_double)]
 
 
-def _tokens(t, name, dtype=None, shape=None):
-    """(pointer, tokens, heads, d, token stride) of a tensor (tokens, heads, d) or (sequences, tokens, heads, d)."""
-    _cuda(t, name)
+def _tokens(t, name, dtype=None, shape=None, like=None):
+    """(pointer, tokens, heads, d, token stride) of a tensor (tokens, heads, d) or (sequences, tokens, heads, d); with
+    `like`, of its sequences x tokens."""
+    if t.get_device() != _only:
+        _cuda(t, name)
     if dtype is not None and t.dtype != dtype:
         raise TypeError(f"{name}: expected {dtype}, got {t.dtype}")
     if t.dim() == 4:
+        if like is not None and like.dim() == 4 and t.shape[:2] != like.shape[:2]:
+            raise ValueError(f"{name}: expected the tokens {tuple(like.shape[:2])}, got {tuple(t.shape[:2])}")
         try:
             t = t.flatten(0, 1) if t.numel() == 0 else t.view((-1,) + t.shape[2:])
         except RuntimeError:
@@ -245,31 +266,25 @@ def _tokens(t, name, dtype=None, shape=None):
     return t.data_ptr(), n, h, d, t.stride(0) if n > 1 else h * d
 
 
-def _like(t, name, other):
-    """Refuses other sequences x tokens than those of `other`."""
-    if t.dim() == other.dim() and t.shape[:-2] != other.shape[:-2]:
-        raise ValueError(f"{name}: expected the tokens {tuple(other.shape[:-2])}, got {tuple(t.shape[:-2])}")
-
-
-def _delta_args(q, k, v, g, beta, s0, offsets, scale):
+def _delta_args(q, k, v, g, beta, s0, offsets, scale, nseq=None):
     qp, n, hk, dk, ldq = _tokens(q, "q")
-    kp, _, _, _, ldk = _tokens(k, "k", q.dtype, (n, hk, dk))
+    kp, _, _, _, ldk = _tokens(k, "k", q.dtype, (n, hk, dk), q)
     vp, _, hv, dv, ldv = _tokens(v, "v", q.dtype)
     lead = q.shape[:-2]
-    _like(k, "k", q)
     if v.shape[:-2] != lead:
         raise ValueError(f"v: expected the tokens of q, {tuple(lead)}, got {tuple(v.shape[:-2])}")
     if offsets is not None:
         nseq = offsets.numel() - 1
         if nseq < 0:
             raise ValueError("offsets: expected one more than the sequences")
-    else:
+    elif nseq is None:
         nseq = q.shape[0] if q.dim() == 4 else 1
+    gates = (*lead, hv)
     a = zsolve_delta_args(_type(q, "q"), hk, hv, dk, dv, nseq, n,
                           _vector(offsets, "offsets", nseq + 1, torch.int64) or None, qp, kp, vp, ldq, ldk, ldv,
-                          _vector(g, "g", n * hv, torch.float32, lead, (hv,)),
-                          _vector(beta, "beta", n * hv, torch.float32, lead, (hv,)),
-                          _vector(s0, "s0", nseq * hv * dk * dv, torch.float32, (nseq,), (hv, dk, dv)),
+                          _vector(g, "g", n * hv, torch.float32, gates, 1),
+                          _vector(beta, "beta", n * hv, torch.float32, gates, 1),
+                          _vector(s0, "s0", nseq * hv * dk * dv, torch.float32, (nseq, hv, dk, dv), 3),
                           dk ** -0.5 if scale is None else scale)
     return a
 
@@ -283,16 +298,18 @@ def zsolve_delta(seq, q, k, v, g, beta, o, s=None, s0=None, offsets=None, scale=
     scale: 1 / sqrt(dk) unless given.
     """
     a = _delta_args(q, k, v, g, beta, s0, offsets, scale)
-    op, _, _, _, ldo = _tokens(o, "o", q.dtype, (a.tokens, a.hv, a.dv))
-    _like(o, "o", v)
+    op, _, _, _, ldo = _tokens(o, "o", q.dtype, (a.tokens, a.hv, a.dv), v)
     _check_seq(seq, _lib.zsolve_delta(seq, ctypes.byref(a), op, ldo, _state(s, a)))
 
 
 def zsolve_delta_step(seq, q, k, v, g, beta, o, s=None, s0=None, offsets=None, scale=None) -> None:
     """As zsolve_delta, token by token: for one or a few tokens a sequence."""
-    a = _delta_args(q, k, v, g, beta, s0, offsets, scale)
-    op, _, _, _, ldo = _tokens(o, "o", q.dtype, (a.tokens, a.hv, a.dv))
-    _like(o, "o", v)
+    _step(seq, q, k, v, g, beta, o, s, s0, offsets, scale)
+
+
+def _step(seq, q, k, v, g, beta, o, s, s0, offsets, scale, nseq=None):
+    a = _delta_args(q, k, v, g, beta, s0, offsets, scale, nseq)
+    op, _, _, _, ldo = _tokens(o, "o", q.dtype, (a.tokens, a.hv, a.dv), v)
     _check_seq(seq, _lib.zsolve_delta_step(seq, ctypes.byref(a), op, ldo, _state(s, a)))
 
 
@@ -300,20 +317,18 @@ def zsolve_delta_bwd(seq, dout, q, k, v, g, beta, dq, dk, dv, dg, dbeta, ds0=Non
                      scale=None) -> None:
     """dq .. dbeta and ds0 (shapes of q .. beta and s0, contiguous) from dout (as o) and ds (as s, or None)."""
     a = _delta_args(q, k, v, g, beta, s0, offsets, scale)
-    op, _, _, _, lddo = _tokens(dout, "dout", q.dtype, (a.tokens, a.hv, a.dv))
-    _like(dout, "dout", v)
-    lead = q.shape[:-2]
+    op, _, _, _, lddo = _tokens(dout, "dout", q.dtype, (a.tokens, a.hv, a.dv), v)
     nk, nv, n = a.tokens * a.hk * a.dk, a.tokens * a.hv * a.dv, a.tokens * a.hv
     _check_seq(seq, _lib.zsolve_delta_bwd(seq, ctypes.byref(a), op, lddo, _state(ds, a), 
-                                          _vector(dq, "dq", nk, q.dtype, lead, (a.hk, a.dk)),
-                                          _vector(dk, "dk", nk, q.dtype, lead, (a.hk, a.dk)),
-                                          _vector(dv, "dv", nv, q.dtype, lead, (a.hv, a.dv)),
-                                          _vector(dg, "dg", n, torch.float32, lead, (a.hv,)),
-                                          _vector(dbeta, "dbeta", n, torch.float32, lead, (a.hv,)), _state(ds0, a)))
+                                          _vector(dq, "dq", nk, q.dtype, q.shape, 2),
+                                          _vector(dk, "dk", nk, q.dtype, k.shape, 2),
+                                          _vector(dv, "dv", nv, q.dtype, v.shape, 2),
+                                          _vector(dg, "dg", n, torch.float32, g.shape, 1),
+                                          _vector(dbeta, "dbeta", n, torch.float32, beta.shape, 1), _state(ds0, a)))
 
 
 def _state(s, a):
-    return _vector(s, "s", a.nseq * a.hv * a.dk * a.dv, torch.float32, (a.nseq,), (a.hv, a.dk, a.dv))
+    return _vector(s, "s", a.nseq * a.hv * a.dk * a.dv, torch.float32, (a.nseq, a.hv, a.dk, a.dv), 3)
 
 
 class Seq:
@@ -401,9 +416,7 @@ class Seq:
         self._on_stream()
         o = torch.empty(v.shape, dtype=v.dtype, device=v.device)
         s_out = s if s_out is None else s_out
-        if q.dim() == 3:
-            q, k, v = q.unsqueeze(1), k.unsqueeze(1), v.unsqueeze(1)
-        zsolve_delta_step(self.seq, q, k, v, g, beta, o.view(v.shape), s_out, s, None, scale)
+        _step(self.seq, q, k, v, g, beta, o, s_out, s, None, scale, q.shape[0])
         return o, s_out
 
     def check(self):

@@ -331,6 +331,20 @@ def _state(s, a):
     return _vector(s, "s", a.nseq * a.hv * a.dk * a.dv, torch.float32, (a.nseq, a.hv, a.dk, a.dv), 3)
 
 
+def _records(*tensors) -> bool:
+    """Whether autograd is to record a call on these tensors."""
+    if torch.is_grad_enabled():
+        for t in tensors:
+            if t is not None and t.requires_grad:
+                return True
+    return False
+
+
+def _autograd():
+    from . import seq_autograd
+    return seq_autograd
+
+
 class Seq:
     """Owns one handle of the sequence-layer operators; runs on torch's current stream.
 
@@ -342,6 +356,10 @@ class Seq:
         with Seq() as s:
             h, mean, rstd = s.layernorm(x, w, b)
             dx, dw, db = s.layernorm_bwd(dh, x, mean, rstd, w)
+
+    Tensors that require gradients may be given as well: y of layernorm and linear and both outputs of delta then
+    carry them (the handle has to be open in the backward pass).  mean, rstd and z carry none, nor does delta_step:
+    a backward pass that needs theirs raises.
     """
 
     def __init__(self):
@@ -352,6 +370,8 @@ class Seq:
 
     def layernorm(self, x, w=None, b=None, eps=1e-5):
         """Returns (y, mean, rstd); mean and rstd are float32, for layernorm_bwd."""
+        if _records(x, w, b):
+            return _autograd().LayerNorm.apply(self, x, w, b, eps)
         self._on_stream()
         y = torch.empty_like(x)
         rows = x.shape[:-1]
@@ -372,6 +392,8 @@ class Seq:
 
     def linear(self, x, w, b=None, act="none", r=None, keep=False):
         """y = act(x w^T + b) + r; with keep=True (y, z), z for linear_bwd."""
+        if _records(x, w, b, r):
+            return _autograd().Linear.apply(self, x, w, b, act, r, keep)
         self._on_stream()
         shape = x.shape[:-1] + w.shape[:1]
         y = torch.empty(shape, dtype=x.dtype, device=x.device)
@@ -393,6 +415,8 @@ class Seq:
 
         Shapes as for zsolve_delta; s is (sequences, hv, dk, dv) float32.
         """
+        if _records(q, k, v, g, beta, s0):
+            return _autograd().Delta.apply(self, q, k, v, g, beta, s0, offsets, scale)
         self._on_stream()
         o = torch.empty(v.shape, dtype=v.dtype, device=v.device)
         nseq = offsets.numel() - 1 if offsets is not None else q.shape[0] if q.dim() == 4 else 1
@@ -413,6 +437,8 @@ class Seq:
     def delta_step(self, q, k, v, g, beta, s, s_out=None, scale=None):
         """Returns (o, s): the next token of every sequence, q (sequences, hk, dk) and so on (or the next few,
         with two leading dimensions).  The states are updated in place, or written to s_out."""
+        if _records(q, k, v, g, beta, s):
+            return _autograd().Step.apply(self, q, k, v, g, beta, s, s if s_out is None else s_out, scale)
         self._on_stream()
         o = torch.empty(v.shape, dtype=v.dtype, device=v.device)
         s_out = s if s_out is None else s_out

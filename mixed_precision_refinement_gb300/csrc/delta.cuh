@@ -707,7 +707,7 @@ inline int64_t delta_chain_blocks(const zs::DeltaGeom &g) {
 cudaError_t zs_launch_delta_grads(int type, const zs::DeltaGeom &g, const zs::DeltaTerms &t, const void *dout,
                                   int64_t lddo, const float *states, const float *dends, const float *us,
                                   const float *dxs, float *dqp, float *dkp, void *dq, void *dk, void *dv,
-                                  float *dg, float *dbeta, bool next, cudaStream_t st, int64_t *launches);
+                                  float *dg, float *dbeta, int num_sms, bool next, cudaStream_t st, int64_t *launches);
 // Token by token (delta_step.cu): every sequence's tokens one after the other.
 cudaError_t zs_launch_delta_step(int type, const zs::DeltaGeom &g, const int64_t *offsets, const float *s0, void *o,
                                  int64_t ldo, float *sn, cudaStream_t st, int64_t *launches);

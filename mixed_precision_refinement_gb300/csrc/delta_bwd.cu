@@ -282,7 +282,7 @@ k_delta_rchain(const DeltaGeom geo, const DeltaTerms terms, const T *__restrict_
 
 // ---------------------------------------------------------------- gradients of a chunk
 
-// One block for a chunk and a value head; warp (m, n): 16 MT tokens, key columns
+// One block for a chunk and a value head; warp (m, n): 16 tokens, key columns
 // 32 n .. (of F, E, H, dq, dk) and 64 / NG of the 64 x 64 products' columns.  The
 // products over the value columns run in slabs of 32 of them, two stages of slabs;
 // the 64 x 64 matrices then take the slabs' place.  4096 tokens x 32 heads of 128,
@@ -294,8 +294,8 @@ constexpr int kLdS = kSlab + 8;
 template <typename T, int DK>
 struct GradCfg {
     static constexpr int NG = DK / 32;
-    static constexpr int MT = 1;  // token tiles of 16 a warp (two share the B splits, but leave two warps a scheduler: 2104 us for 2047)
-    static constexpr int MG = 4 / MT;
+    // groups of 16 tokens, a warp's (32 a warp would share the B splits, but leave two warps a scheduler: 2104 us for 2047)
+    static constexpr int MG = 4;
     static constexpr int NT = 32 * MG * NG;
     static constexpr int PT = 8 / NG;  // 8-column tiles of the 64 x 64 products a warp
     static constexpr int LD = tile_ld<T>(DK);
@@ -410,7 +410,7 @@ k_delta_grads(const DeltaGeom geo, const DeltaTerms terms, const T *__restrict__
               const float *__restrict__ dxs, float *__restrict__ dqp, float *__restrict__ dkp, T *__restrict__ dq,
               T *__restrict__ dk, T *__restrict__ dv, float *__restrict__ dg, float *__restrict__ dbeta, int vecv) {
     using C = GradCfg<T, DK>;
-    constexpr int NG = C::NG, MG = C::MG, MT = C::MT, NT = C::NT, PT = C::PT, LD = C::LD;
+    constexpr int NG = C::NG, MG = C::MG, NT = C::NT, PT = C::PT, LD = C::LD;
     constexpr bool EXACT = sizeof(T) == 2;
     extern __shared__ __align__(16) uint8_t smem_raw[];
     GradSmem<T, DK> &sm = *reinterpret_cast<GradSmem<T, DK> *>(smem_raw);
@@ -435,7 +435,7 @@ k_delta_grads(const DeltaGeom geo, const DeltaTerms terms, const T *__restrict__
         return;
     }
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g = lane >> 2, t = lane & 3;
-    const int wm = warp % MG, wn = warp / MG, m0 = wm * 16 * MT, d0 = wn * 32, p0 = wn * PT * 8;
+    const int wm = warp % MG, wn = warp / MG, m0 = wm * 16, d0 = wn * 32, p0 = wn * PT * 8;
     const int64_t slot = (int64_t)blockIdx.x * geo.hv + hv;
     const float *S = states + slot * geo.dk * geo.dv, *DS = dends + slot * geo.dk * geo.dv;
     const float *Us = us + slot * kChunk * geo.dv, *DXs = dxs + slot * kChunk * geo.dv;
@@ -460,7 +460,7 @@ k_delta_grads(const DeltaGeom geo, const DeltaTerms terms, const T *__restrict__
     if (tid < kChunk) sm.row_xv[tid] = 0.f;
 
     // the products over the value columns
-    float F[MT][4][4] = {}, E[MT][4][4] = {}, H[MT][4][4] = {}, dp[MT][PT][4] = {}, da[MT][PT][4] = {};
+    float F[4][4] = {}, E[4][4] = {}, H[4][4] = {}, dp[PT][4] = {}, da[PT][4] = {};
     float sds = 0.f;
     for (int v = 0, it = 0; v < geo.dv; v += kSlab, it++) {
         cp_wait<0>();
@@ -478,33 +478,20 @@ k_delta_grads(const DeltaGeom geo, const DeltaTerms terms, const T *__restrict__
         }
 #pragma unroll 1
         for (int c = 0; c < kSlab; c += 8) {
-            SplitA ao[MT], ax[MT], au[MT];
-#pragma unroll
-            for (int i = 0; i < MT; i++) {
-                const int m = m0 + 16 * i;
-                ao[i] = rows_a<T, kLdS>(s.dout, m, c);
-                ax[i] = rows_a<float, kLdS>(s.dx, m, c);
-                au[i] = rows_a<float, kLdS>(s.u, m, c);
-            }
+            const SplitA ao = rows_a<T, kLdS>(s.dout, m0, c), ax = rows_a<float, kLdS>(s.dx, m0, c), au = rows_a<float, kLdS>(s.u, m0, c);
 #pragma unroll
             for (int j = 0; j < 4; j++) {
                 const SplitB b = split_b(frag1<float, kLdS>(s.s, d0 + 8 * j, c)), e = split_b(frag1<float, kLdS>(s.ds, d0 + 8 * j, c));
-#pragma unroll
-                for (int i = 0; i < MT; i++) {
-                    mma_add<EXACT>(F[i][j], ao[i], b);
-                    mma_add<false>(E[i][j], ax[i], b);
-                    mma_add<false>(H[i][j], au[i], e);
-                }
+                mma_add<EXACT>(F[j], ao, b);
+                mma_add<false>(E[j], ax, b);
+                mma_add<false>(H[j], au, e);
             }
 #pragma unroll
             for (int j = 0; j < PT; j++) {
-                if (p0 + 8 * j > m0 + 16 * MT - 8) continue;  // above the diagonal
+                if (p0 + 8 * j > m0 + 8) continue;  // above the diagonal
                 const SplitB b = split_b(frag1<float, kLdS>(s.u, p0 + 8 * j, c));
-#pragma unroll
-                for (int i = 0; i < MT; i++) {
-                    mma_add<EXACT>(dp[i][j], ao[i], b);
-                    mma_add<false>(da[i][j], ax[i], b);
-                }
+                mma_add<EXACT>(dp[j], ao, b);
+                mma_add<false>(da[j], ax, b);
             }
         }
         // dX_i . v_i, two columns a lane, and <S, dS'>
@@ -530,53 +517,46 @@ k_delta_grads(const DeltaGeom geo, const DeltaTerms terms, const T *__restrict__
     // K K^T: the warp's tiles; of Q K^T only P is needed, which the terms have
     {
         const float *bh = sm.vec + 3 * kChunk, *bl = sm.vec + 4 * kChunk;
-        float pt[MT][PT][4];
+        float pt[PT][4];
 #pragma unroll
-        for (int i = 0; i < MT; i++)
+        for (int j = 0; j < PT; j++)
 #pragma unroll
-            for (int j = 0; j < PT; j++)
-#pragma unroll
-                for (int e = 0; e < 4; e++) {
-                    const int y = m0 + 16 * i + g + (e >> 1) * 8, x = p0 + 8 * j + 2 * t + (e & 1);
-                    pt[i][j][e] = x <= y ? terms.tp[slot * kSquare + x * kLdT + y] : 0.f;
-                }
-        float kk[MT][PT][4] = {};
+            for (int e = 0; e < 4; e++) {
+                const int y = m0 + g + (e >> 1) * 8, x = p0 + 8 * j + 2 * t + (e & 1);
+                pt[j][e] = x <= y ? terms.tp[slot * kSquare + x * kLdT + y] : 0.f;
+            }
+        float kk[PT][4] = {};
 #pragma unroll 4
         for (int c = 0; c < DK; c += 8) {
-            SplitA ak[MT];
-#pragma unroll
-            for (int i = 0; i < MT; i++) ak[i] = rows_a<T, LD>(sm.k, m0 + 16 * i, c);
+            const SplitA ak = rows_a<T, LD>(sm.k, m0, c);
 #pragma unroll
             for (int j = 0; j < PT; j++) {
                 const float2 b = frag1<T, LD>(sm.k, p0 + 8 * j, c);
-#pragma unroll
-                for (int i = 0; i < MT; i++) mma_add<EXACT, EXACT>(kk[i][j], ak[i], b);
+                mma_add<EXACT, EXACT>(kk[j], ak, b);
             }
         }
         // r, beta w and their sums with the raw products
-        float rm[MT][2] = {}, rw[MT][2] = {};
+        float rm[2] = {}, rw[2] = {};
 #pragma unroll
         for (int j = 0; j < PT; j++) {
             float cm[2] = {};
 #pragma unroll
-            for (int i = 0; i < MT; i++)
-#pragma unroll
-                for (int e = 0; e < 4; e++) {
-                    const int y = m0 + 16 * i + g + (e >> 1) * 8, x = p0 + 8 * j + 2 * t + (e & 1);
-                    float r = 0.f, w = 0.f;
-                    if (x <= y) {
-                        const float ex = expf((bh[y] - bh[x]) + (bl[y] - bl[x]));
-                        r = geo.scale * ex * dp[i][j][e];
-                        if (x < y) w = -ex * da[i][j][e];
-                    }
-                    const float bw = sm.vec[2 * kChunk + y] * w;
-                    sm.sq.r[y * kLdT + x] = r;
-                    sm.sq.w[y * kLdT + x] = bw;
-                    const float mm = x <= y ? fmaf(dp[i][j][e], pt[i][j][e], bw * kk[i][j][e]) : 0.f;
-                    rm[i][e >> 1] += mm;
-                    cm[e & 1] += mm;
-                    if (x < y) rw[i][e >> 1] = fmaf(w, kk[i][j][e], rw[i][e >> 1]);
+            for (int e = 0; e < 4; e++) {
+                const int y = m0 + g + (e >> 1) * 8, x = p0 + 8 * j + 2 * t + (e & 1);
+                float r = 0.f, w = 0.f;
+                if (x <= y) {
+                    const float ex = expf((bh[y] - bh[x]) + (bl[y] - bl[x]));
+                    r = geo.scale * ex * dp[j][e];
+                    if (x < y) w = -ex * da[j][e];
                 }
+                const float bw = sm.vec[2 * kChunk + y] * w;
+                sm.sq.r[y * kLdT + x] = r;
+                sm.sq.w[y * kLdT + x] = bw;
+                const float mm = x <= y ? fmaf(dp[j][e], pt[j][e], bw * kk[j][e]) : 0.f;
+                rm[e >> 1] += mm;
+                cm[e & 1] += mm;
+                if (x < y) rw[e >> 1] = fmaf(w, kk[j][e], rw[e >> 1]);
+            }
 #pragma unroll
             for (int e = 0; e < 2; e++) {  // over the warp's rows
                 cm[e] += __shfl_xor_sync(0xffffffffu, cm[e], 4);
@@ -586,39 +566,36 @@ k_delta_grads(const DeltaGeom geo, const DeltaTerms terms, const T *__restrict__
             }
         }
 #pragma unroll
-        for (int i = 0; i < MT; i++)
+        for (int h = 0; h < 2; h++) {
 #pragma unroll
-            for (int h = 0; h < 2; h++) {
-#pragma unroll
-                for (int o = 1; o < 4; o <<= 1) {
-                    rm[i][h] += __shfl_xor_sync(0xffffffffu, rm[i][h], o);
-                    rw[i][h] += __shfl_xor_sync(0xffffffffu, rw[i][h], o);
-                }
-                if (t == 0) {
-                    sm.row_m[wn][m0 + 16 * i + g + 8 * h] = rm[i][h];
-                    sm.row_w[wn][m0 + 16 * i + g + 8 * h] = rw[i][h];
-                }
+            for (int o = 1; o < 4; o <<= 1) {
+                rm[h] += __shfl_xor_sync(0xffffffffu, rm[h], o);
+                rw[h] += __shfl_xor_sync(0xffffffffu, rw[h], o);
             }
+            if (t == 0) {
+                sm.row_m[wn][m0 + g + 8 * h] = rm[h];
+                sm.row_w[wn][m0 + g + 8 * h] = rw[h];
+            }
+        }
     }
     // rows' products with k and q; then dq and dk begin with c F and e H - beta c E, in F's and H's place
-#pragma unroll
-    for (int i = 0; i < MT; i++) {
+    {
         float kE[2] = {}, kH[2] = {}, qF[2] = {};
-        const int y0 = m0 + 16 * i + g;
+        const int y0 = m0 + g;
 #pragma unroll
         for (int j = 0; j < 4; j++)
 #pragma unroll
             for (int h = 0; h < 2; h++) {
-                const float2 kv = frag1<T, LD>(sm.k, m0 + 16 * i + 8 * h, d0 + 8 * j), qv = frag1<T, LD>(sm.q, m0 + 16 * i + 8 * h, d0 + 8 * j);
+                const float2 kv = frag1<T, LD>(sm.k, m0 + 8 * h, d0 + 8 * j), qv = frag1<T, LD>(sm.q, m0 + 8 * h, d0 + 8 * j);
                 const int y = y0 + 8 * h, e = 2 * h;
-                kE[h] = fmaf(kv.x, E[i][j][e], fmaf(kv.y, E[i][j][e + 1], kE[h]));
-                kH[h] = fmaf(kv.x, H[i][j][e], fmaf(kv.y, H[i][j][e + 1], kH[h]));
-                qF[h] = fmaf(qv.x, F[i][j][e], fmaf(qv.y, F[i][j][e + 1], qF[h]));
+                kE[h] = fmaf(kv.x, E[j][e], fmaf(kv.y, E[j][e + 1], kE[h]));
+                kH[h] = fmaf(kv.x, H[j][e], fmaf(kv.y, H[j][e + 1], kH[h]));
+                qF[h] = fmaf(qv.x, F[j][e], fmaf(qv.y, F[j][e + 1], qF[h]));
                 const float c = sm.vec[y], en = sm.vec[kChunk + y], bc = sm.vec[2 * kChunk + y] * c;
 #pragma unroll
                 for (int q = e; q < e + 2; q++) {
-                    F[i][j][q] *= geo.scale * c;
-                    H[i][j][q] = fmaf(en, H[i][j][q], -bc * E[i][j][q]);
+                    F[j][q] *= geo.scale * c;
+                    H[j][q] = fmaf(en, H[j][q], -bc * E[j][q]);
                 }
             }
 #pragma unroll
@@ -673,60 +650,52 @@ k_delta_grads(const DeltaGeom geo, const DeltaTerms terms, const T *__restrict__
     }
     // dq += r K, dk += (beta w) K: columns up to the diagonal
 #pragma unroll 2
-    for (int k = 0; k < 2 * MT * (wm + 1); k++) {
+    for (int k = 0; k < 2 * (wm + 1); k++) {
         float2 b[4];
         frag4<T, LD, true>(sm.k, k * 8, d0, b);
+        const SplitA ar = rows_a<float, kLdT>(sm.sq.r, m0, k * 8), aw = rows_a<float, kLdT>(sm.sq.w, m0, k * 8);
 #pragma unroll
-        for (int i = 0; i < MT; i++) {
-            const SplitA ar = rows_a<float, kLdT>(sm.sq.r, m0 + 16 * i, k * 8), aw = rows_a<float, kLdT>(sm.sq.w, m0 + 16 * i, k * 8);
-#pragma unroll
-            for (int j = 0; j < 4; j++) {
-                mma_add<false, EXACT>(F[i][j], ar, b[j]);
-                mma_add<false, EXACT>(H[i][j], aw, b[j]);
-            }
+        for (int j = 0; j < 4; j++) {
+            mma_add<false, EXACT>(F[j], ar, b[j]);
+            mma_add<false, EXACT>(H[j], aw, b[j]);
         }
     }
     // dk += r^T Q + (beta w)^T K: the transposes' rows, columns from the diagonal on
 #pragma unroll 2
-    for (int k = 2 * MT * wm; k < 8; k++) {
+    for (int k = 2 * wm; k < 8; k++) {
         float2 bq[4], bk[4];
         frag4<T, LD, true>(sm.q, k * 8, d0, bq);
         frag4<T, LD, true>(sm.k, k * 8, d0, bk);
+        const int at = (k * 8 + 2 * t) * kLdT + m0 + g;
+        SplitA ar, aw;
+        ar.set(sm.sq.r[at], sm.sq.r[at + kLdT], sm.sq.r[at + 8], sm.sq.r[at + kLdT + 8]);
+        aw.set(sm.sq.w[at], sm.sq.w[at + kLdT], sm.sq.w[at + 8], sm.sq.w[at + kLdT + 8]);
 #pragma unroll
-        for (int i = 0; i < MT; i++) {
-            const int at = (k * 8 + 2 * t) * kLdT + m0 + 16 * i + g;
-            SplitA ar, aw;
-            ar.set(sm.sq.r[at], sm.sq.r[at + kLdT], sm.sq.r[at + 8], sm.sq.r[at + kLdT + 8]);
-            aw.set(sm.sq.w[at], sm.sq.w[at + kLdT], sm.sq.w[at + 8], sm.sq.w[at + kLdT + 8]);
-#pragma unroll
-            for (int j = 0; j < 4; j++) {
-                mma_add<false, EXACT>(H[i][j], ar, bq[j]);
-                mma_add<false, EXACT>(H[i][j], aw, bk[j]);
-            }
+        for (int j = 0; j < 4; j++) {
+            mma_add<false, EXACT>(H[j], ar, bq[j]);
+            mma_add<false, EXACT>(H[j], aw, bk[j]);
         }
     }
 #pragma unroll
-    for (int i = 0; i < MT; i++)
+    for (int j = 0; j < 4; j++)
 #pragma unroll
-        for (int j = 0; j < 4; j++)
+        for (int h = 0; h < 2; h++) {
+            const int y = m0 + g + 8 * h, d = d0 + 8 * j + 2 * t;
+            if (y >= n) continue;
 #pragma unroll
-            for (int h = 0; h < 2; h++) {
-                const int y = m0 + 16 * i + g + 8 * h, d = d0 + 8 * j + 2 * t;
-                if (y >= n) continue;
-#pragma unroll
-                for (int e = 0; e < 2; e++) {
-                    if (d + e >= geo.dk) continue;
-                    if (dqp) {
-                        const int64_t at = ((int64_t)(ch.x + y) * geo.hv + hv) * geo.dk + d + e;
-                        dqp[at] = F[i][j][2 * h + e];
-                        dkp[at] = H[i][j][2 * h + e];
-                    } else {
-                        const int64_t at = ((int64_t)(ch.x + y) * geo.hk + hk) * geo.dk + d + e;
-                        dq[at] = from_f32<T>(F[i][j][2 * h + e]);
-                        dk[at] = from_f32<T>(H[i][j][2 * h + e]);
-                    }
+            for (int e = 0; e < 2; e++) {
+                if (d + e >= geo.dk) continue;
+                if (dqp) {
+                    const int64_t at = ((int64_t)(ch.x + y) * geo.hv + hv) * geo.dk + d + e;
+                    dqp[at] = F[j][2 * h + e];
+                    dkp[at] = H[j][2 * h + e];
+                } else {
+                    const int64_t at = ((int64_t)(ch.x + y) * geo.hk + hk) * geo.dk + d + e;
+                    dq[at] = from_f32<T>(F[j][2 * h + e]);
+                    dk[at] = from_f32<T>(H[j][2 * h + e]);
                 }
             }
+        }
 }
 
 // dq and dk of the key heads: the sums over the value heads that share them, in order.
@@ -786,14 +755,13 @@ cudaError_t zs_launch_delta_rchain(int type, const DeltaGeom &g, const DeltaTerm
 
 cudaError_t zs_launch_delta_grads(int type, const DeltaGeom &g, const DeltaTerms &t, const void *dout, int64_t lddo,
                                   const float *states, const float *dends, const float *us, const float *dxs,
-                                  float *dqp, float *dkp, void *dq, void *dk, void *dv,
-                                  float *dg, float *dbeta, bool next,
-                                  cudaStream_t st, int64_t *launches) {
+                                  float *dqp, float *dkp, void *dq, void *dk, void *dv, float *dg,
+                                  float *dbeta, int num_sms, bool next, cudaStream_t st, int64_t *launches) {
     ++*launches;
     cudaError_t e = DELTA_TYPE(grads_dk, g, t, dout, lddo, states, dends, us, dxs, dqp, dkp, dq, dk, dv, dg, dbeta, next, st);
     if (e != cudaSuccess || !dqp) return e;
     const int64_t n = g.tokens * g.hk * g.dk;
-    const unsigned blocks = (unsigned)std::min<int64_t>((n + 255) / 256, 152 * 16);
+    const unsigned blocks = (unsigned)std::min<int64_t>((n + 255) / 256, (int64_t)num_sms * 16);
     const int group = g.hv / g.hk;
     ++*launches;
     auto join = [&](auto kernel, auto *q, auto *k) {

@@ -13,7 +13,6 @@ using namespace zs;
 
 constexpr int kCols = 32;     // value columns of a block
 constexpr int kThreads = 256;
-constexpr int kMaxRows = 4;   // of 32 key rows: dk <= 128
 
 // VE: value columns of a thread (4: dv a multiple of 4), 32 / VE threads a
 // row, ROWS rows a thread.

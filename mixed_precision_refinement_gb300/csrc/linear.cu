@@ -34,7 +34,6 @@ constexpr int BK = 64;        // k values of a stage: 128 bytes, one swizzle row
 constexpr int kDrain = 8;  // epilogue warps: two for each quarter of the TMEM lanes
 constexpr int kThreads = 64 + 32 * kDrain;
 constexpr uint32_t kTmemCols = 512;
-constexpr uint32_t kWaitLimit = 1u << 19;  // try_wait polls before a wait gives up: about a second
 
 constexpr int BN = 128;       // columns of an output tile of one CTA
 // Bytes in which the epilogue warps turn their values over where the results' rows
@@ -55,39 +54,6 @@ struct Cfg {
 
 __device__ __forceinline__ uint32_t smem_u32(const void *p) { return (uint32_t)__cvta_generic_to_shared(p); }
 
-__device__ __forceinline__ void mbar_init(uint32_t bar, uint32_t count) {
-    asm volatile("mbarrier.init.shared::cta.b64 [%0], %1;" ::"r"(bar), "r"(count) : "memory");
-}
-__device__ __forceinline__ void mbar_expect_tx(uint32_t bar, uint32_t bytes) {
-    asm volatile("mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;" ::"r"(bar), "r"(bytes) : "memory");
-}
-__device__ __forceinline__ void mbar_arrive(uint32_t bar) {
-    asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(bar) : "memory");
-}
-__device__ __forceinline__ bool mbar_try_wait(uint32_t bar, uint32_t parity) {
-    uint32_t ok;
-    asm volatile(
-        "{\n\t.reg .pred p;\n\t"
-        "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
-        "selp.u32 %0, 1, 0, p;\n\t}"
-        : "=r"(ok)
-        : "r"(bar), "r"(parity)
-        : "memory");
-    return ok != 0;
-}
-// Bounded wait: false once it or another role of the block has given up.
-__device__ __forceinline__ bool mbar_wait(uint32_t bar, uint32_t parity, volatile int *abort_flag, unsigned *status) {
-    uint32_t it = 0;
-    while (!mbar_try_wait(bar, parity)) {
-        if (*abort_flag) return false;
-        if (++it > kWaitLimit) {
-            *abort_flag = 1;
-            atomicOr(status, 1u);
-            return false;
-        }
-    }
-    return true;
-}
 __device__ __forceinline__ void tma_load_2d(uint32_t dst, const CUtensorMap *map, int c0, int c1, uint32_t bar) {
     asm volatile(
         "cp.async.bulk.tensor.2d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
@@ -237,14 +203,14 @@ k_linear_tc(const __grid_constant__ CUtensorMap amap, const __grid_constant__ CU
     if (threadIdx.x == 0) {
         s_abort = 0;
         for (int s = 0; s < C::STAGES; s++) {
-            mbar_init(smem_u32(&bar_full[s]), 1);
-            mbar_init(smem_u32(&bar_empty[s]), 1);
+            bar_init(&bar_full[s], 1);
+            bar_init(&bar_empty[s], 1);
         }
         for (int b = 0; b < 2; b++) {
-            mbar_init(smem_u32(&bar_accf[b]), 1);
-            mbar_init(smem_u32(&bar_acce[b]), kDrain);
+            bar_init(&bar_accf[b], 1);
+            bar_init(&bar_acce[b], kDrain);
         }
-        mbar_init(smem_u32(&bar_drain), 1);
+        bar_init(&bar_drain, 1);
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     }
     if (warp == 1) {
@@ -274,12 +240,12 @@ k_linear_tc(const __grid_constant__ CUtensorMap amap, const __grid_constant__ CU
                 const int k1 = kfirst(x.split + 1);
                 for (int kb = kfirst(x.split); kb < k1; kb++, g++) {
                     const uint32_t st = g % C::STAGES, ph = (g / C::STAGES) & 1u;
-                    if (!mbar_wait(smem_u32(&bar_empty[st]), ph ^ 1u, &s_abort, status)) {
+                    if (!bar_wait(&bar_empty[st], ph ^ 1u, &s_abort, status)) {
                         ok = false;
                         break;
                     }
                     const uint32_t fb = smem_u32(&bar_full[st]);
-                    mbar_expect_tx(fb, C::STAGE);
+                    bar_expect(&bar_full[st], C::STAGE);
                     const uint32_t sa = base + st * C::STAGE, sb = sa + C::A_BYTES;
                     if (A_MN) {
 #pragma unroll
@@ -300,7 +266,7 @@ k_linear_tc(const __grid_constant__ CUtensorMap amap, const __grid_constant__ CU
             // our own copies in flight: wait (bounded) for the last stages to land
             for (uint32_t q = g > (uint32_t)C::STAGES ? g - C::STAGES : 0; q < g; q++) {
                 uint32_t it = 0;
-                while (!mbar_try_wait(smem_u32(&bar_full[q % C::STAGES]), (q / C::STAGES) & 1u) && ++it < kWaitLimit) {
+                while (!bar_try(&bar_full[q % C::STAGES], (q / C::STAGES) & 1u) && ++it < kWaitLimit) {
                 }
             }
         }
@@ -313,12 +279,12 @@ k_linear_tc(const __grid_constant__ CUtensorMap amap, const __grid_constant__ CU
                 const TileAt x = tile_at(t, mt, nt);
                 const int k0 = kfirst(x.split), k1 = kfirst(x.split + 1);
                 const uint32_t buf = it & 1u, aph = (it >> 1) & 1u;
-                if (!mbar_wait(smem_u32(&bar_acce[buf]), aph ^ 1u, &s_abort, status)) break;
+                if (!bar_wait(&bar_acce[buf], aph ^ 1u, &s_abort, status)) break;
                 tc_fence_after();
                 const uint32_t d = tmem + buf * 256u;
                 for (int kb = k0; kb < k1; kb++, g++) {
                     const uint32_t st = g % C::STAGES, ph = (g / C::STAGES) & 1u;
-                    if (!mbar_wait(smem_u32(&bar_full[st]), ph, &s_abort, status)) {
+                    if (!bar_wait(&bar_full[st], ph, &s_abort, status)) {
                         ok = false;
                         break;
                     }
@@ -336,7 +302,7 @@ k_linear_tc(const __grid_constant__ CUtensorMap amap, const __grid_constant__ CU
             // every MMA issued so far completes before TMEM is freed
             mma_commit(smem_u32(&bar_drain));
             uint32_t w = 0;
-            while (!mbar_try_wait(smem_u32(&bar_drain), 0) && ++w < kWaitLimit) {
+            while (!bar_try(&bar_drain, 0) && ++w < kWaitLimit) {
             }
         }
     } else {
@@ -351,14 +317,14 @@ k_linear_tc(const __grid_constant__ CUtensorMap amap, const __grid_constant__ CU
                 epi, M, N, (int64_t)x.tm * BM + quad * 32 + lane, (int64_t)x.tn * BN + half * (BN / 2), x.split,
                 tmem + buf * 256u + (uint32_t)(half * (BN / 2)) + ((uint32_t)(quad * 32) << 16), turn,
                 [&] {
-                    const bool in = __all_sync(0xffffffffu, mbar_wait(smem_u32(&bar_accf[buf]), aph, &s_abort, status));
+                    const bool in = __all_sync(0xffffffffu, bar_wait(&bar_accf[buf], aph, &s_abort, status));
                     tc_fence_after();
                     return in;
                 },
                 [&] {  // accumulator fully read: hand it back to the MMA warp
                     tc_fence_before();
                     __syncwarp();
-                    if (lane == 0) mbar_arrive(smem_u32(&bar_acce[buf]));
+                    if (lane == 0) bar_arrive(&bar_acce[buf]);
                 });
             if (!ok) break;
         }
@@ -487,14 +453,14 @@ k_linear_pair(const __grid_constant__ CUtensorMap amap, const __grid_constant__ 
     if (threadIdx.x == 0) {
         s_abort = 0;
         for (int s = 0; s < kPairStages; s++) {
-            mbar_init(smem_u32(&bar_full[s]), 1);
-            mbar_init(smem_u32(&bar_empty[s]), 1);
+            bar_init(&bar_full[s], 1);
+            bar_init(&bar_empty[s], 1);
         }
         for (int b = 0; b < 2; b++) {
-            mbar_init(smem_u32(&bar_accf[b]), 1);
-            mbar_init(smem_u32(&bar_acce[b]), 2 * kDrain);  // the epilogue warps of both CTAs
+            bar_init(&bar_accf[b], 1);
+            bar_init(&bar_acce[b], 2 * kDrain);  // the epilogue warps of both CTAs
         }
-        mbar_init(smem_u32(&bar_drain), 1);
+        bar_init(&bar_drain, 1);
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     }
     if (warp == 1) {
@@ -526,12 +492,12 @@ k_linear_pair(const __grid_constant__ CUtensorMap amap, const __grid_constant__ 
                 const int ra = x.tm * 2 * BM + (int)rank * BM, rb = x.tn * 256 + (int)rank * 128;
                 for (int kb = 0; kb < kblocks; kb++, g++) {
                     const uint32_t st = g % kPairStages, ph = (g / kPairStages) & 1u;
-                    if (!mbar_wait(smem_u32(&bar_empty[st]), ph ^ 1u, &s_abort, status)) {
+                    if (!bar_wait(&bar_empty[st], ph ^ 1u, &s_abort, status)) {
                         ok = false;
                         break;
                     }
-                    const uint32_t own = smem_u32(&bar_full[st]), fb = cluster_addr(own, 0);
-                    if (rank == 0) mbar_expect_tx(own, 2 * kPairStage);
+                    const uint32_t fb = cluster_addr(smem_u32(&bar_full[st]), 0);
+                    if (rank == 0) bar_expect(&bar_full[st], 2 * kPairStage);
                     const uint32_t sa = base + st * kPairStage, sb = sa + BM * BK * 2;
                     if (a_mn) {
                         tma_load_2d_pair(sa, ma, ra, kb * BK, fb);
@@ -551,7 +517,7 @@ k_linear_pair(const __grid_constant__ CUtensorMap amap, const __grid_constant__ 
             if (rank == 0)
                 for (uint32_t q = g > (uint32_t)kPairStages ? g - kPairStages : 0; q < g; q++) {
                     uint32_t it = 0;
-                    while (!mbar_try_wait(smem_u32(&bar_full[q % kPairStages]), (q / kPairStages) & 1u) && ++it < kWaitLimit) {
+                    while (!bar_try(&bar_full[q % kPairStages], (q / kPairStages) & 1u) && ++it < kWaitLimit) {
                     }
                 }
         }
@@ -567,12 +533,12 @@ k_linear_pair(const __grid_constant__ CUtensorMap amap, const __grid_constant__ 
                 const uint64_t da = a_mn ? smem_desc<true>(0) : smem_desc<false>(0), db = b_mn ? smem_desc<true>(0) : smem_desc<false>(0);
                 const uint32_t step_a = a_mn ? 2048 : 32, step_b = b_mn ? 2048 : 32;
                 const uint32_t buf = it & 1u, aph = (it >> 1) & 1u;
-                if (!mbar_wait(smem_u32(&bar_acce[buf]), aph ^ 1u, &s_abort, status)) break;
+                if (!bar_wait(&bar_acce[buf], aph ^ 1u, &s_abort, status)) break;
                 tc_fence_after();
                 const uint32_t d = tmem + buf * 256u;
                 for (int kb = 0; kb < kblocks; kb++, g++) {
                     const uint32_t st = g % kPairStages, ph = (g / kPairStages) & 1u;
-                    if (!mbar_wait(smem_u32(&bar_full[st]), ph, &s_abort, status)) {
+                    if (!bar_wait(&bar_full[st], ph, &s_abort, status)) {
                         ok = false;
                         break;
                     }
@@ -590,7 +556,7 @@ k_linear_pair(const __grid_constant__ CUtensorMap amap, const __grid_constant__ 
             // every MMA issued so far completes before TMEM is freed
             mma_commit_pair(smem_u32(&bar_drain));
             uint32_t w = 0;
-            while (!mbar_try_wait(smem_u32(&bar_drain), 0) && ++w < kWaitLimit) {
+            while (!bar_try(&bar_drain, 0) && ++w < kWaitLimit) {
             }
         }
     } else {
@@ -606,7 +572,7 @@ k_linear_pair(const __grid_constant__ CUtensorMap amap, const __grid_constant__ 
                 (int64_t)x.tm * 2 * BM + rank * BM + quad * 32 + lane, (int64_t)x.tn * 256 + half * 128, 0,
                 tmem + buf * 256u + (uint32_t)(half * 128) + ((uint32_t)(quad * 32) << 16), turn,
                 [&] {
-                    const bool in = __all_sync(0xffffffffu, mbar_wait(smem_u32(&bar_accf[buf]), aph, &s_abort, status));
+                    const bool in = __all_sync(0xffffffffu, bar_wait(&bar_accf[buf], aph, &s_abort, status));
                     tc_fence_after();
                     return in;
                 },

@@ -455,7 +455,7 @@ int zsolve_delta_bwd(zsolve_seq *s, const zsolve_delta_args *a, const void *dout
         SEQ_CU(backwards(true, s->st));
     }
     SEQ_CU(zs_launch_delta_grads(a->type, g, w.terms, w.dout, w.lddo, w.states, w.dends, w.us, w.dxs, w.dqp, w.dkp, dq, dk,
-                                 dv, dg, dbeta, !both, s->st, &s->launches));
+                                 dv, dg, dbeta, s->num_sms, !both, s->st, &s->launches));
     return ZSOLVE_OK;
 }
 

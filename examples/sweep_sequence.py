@@ -6,9 +6,9 @@ with one token a frequency.  A pre-norm token-mixing layer
     h = norm(x),  a = silu(h Wi^T + bi) = [q | k | v],  q, k normalised per head,
     o = gated delta rule (q, k, v, g(h), beta(h)),  y = o Wo^T + bo + x
 
-learns to give the next frequency's features from those so far.  All of it runs on the sequence-layer
-operators of the library; training takes whole sequences, answering takes one token at a time and keeps
-only the states.
+learns to give the next frequency's features from those so far.  Norms, projections and the delta rule run on
+the sequence-layer operators of the library, the gates' two small projections in float32 in torch; training
+takes whole sequences, answering takes one token at a time and keeps only the states.
 
     python examples/sweep_sequence.py
 """

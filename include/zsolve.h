@@ -529,7 +529,8 @@ int zsolve_linear(zsolve_seq *seq, int type, int64_t m, int64_t n, int64_t k, co
                   int64_t ldy, void *z, int64_t ldz);
 
 /* Its gradients: with dz = dy act'(z) rounded to `type`, dx = dz W, dW = dz^T x,
- * and db = the sum over rows of dy act'(z) in float32 (r's gradient is dy).
+ * and db = the sum over rows of dy act'(z) in float32 (r's gradient is dy).  A
+ * float16 dz above 65504 (slopes reach 1.13) is an infinity.
  * Each of dx, dw, db may be NULL (not formed), as may then what only it needs;
  * z is not read without an activation. */
 int zsolve_linear_bwd(zsolve_seq *seq, int type, int64_t m, int64_t n, int64_t k, const void *dy, int64_t lddy,

@@ -25,8 +25,8 @@ using namespace zs;
 // Laid out as the forward chain: a group of WK warps owns 16 value columns of
 // dS^T, 32 key columns a warp, and one more warp fetches the chunks' operands;
 // the exchanges are the partial sums of (K dS')^T, then dU^T, then dX^T and
-// (scale c dO)^T, split where they are written.  A chunk of 128 x 128 heads takes 4.6
-// us (bfloat16; 2 x 2048 tokens x 32 heads 295 us), bound by the latency of these steps.
+// (scale c dO)^T, split where they are written.  A chunk of 128 x 128 heads takes 4.4
+// us (bfloat16; 2 x 2048 tokens x 32 heads 284 us), bound by the latency of these steps.
 template <typename T, int DK>
 struct RChainCfg {
     static constexpr int WK = DK / 32;

@@ -537,6 +537,25 @@ int zsolve_linear_bwd(zsolve_seq *seq, int type, int64_t m, int64_t n, int64_t k
                       const void *x, int64_t ldx, const void *w, int64_t ldw, int act, const void *z, int64_t ldz,
                       void *dx, int64_t lddx, void *dw, int64_t lddw, void *db);
 
+/* The projections of a gated feed-forward block: zg = x Wg^T + bg, zu = x Wu^T + bu,
+ * y = act(zg) zu: x is m x k, Wg and Wu n x k, y m x n, all of `type` (ZSOLVE_BF16 or
+ * ZSOLVE_F16), both products in one pass over x with float32 sums.  The projection after it is
+ * zsolve_linear.
+ *   bg, bu   n values each (NULL: none)
+ *   zg, zu   m x n: rounded to `type`, for the backward pass (NULL, both: not kept) */
+int zsolve_glu(zsolve_seq *seq, int type, int64_t m, int64_t n, int64_t k, const void *x, int64_t ldx, const void *wg,
+               int64_t ldwg, const void *wu, int64_t ldwu, const void *bg, const void *bu, int act, void *y, int64_t ldy,
+               void *zg, int64_t ldzg, void *zu, int64_t ldzu);
+
+/* Its gradients: with dzg = dy zu act'(zg) and dzu = dy act(zg) rounded to `type` (a float16 one
+ * above 65504 is an infinity), dx = dzg Wg + dzu Wu, dWg = dzg^T x, dWu = dzu^T x, and dbg, dbu =
+ * the sums over the rows of dzg and dzu in float32.  Each of them may be NULL (not formed), as may
+ * then what only it needs. */
+int zsolve_glu_bwd(zsolve_seq *seq, int type, int64_t m, int64_t n, int64_t k, const void *dy, int64_t lddy,
+                   const void *x, int64_t ldx, const void *wg, int64_t ldwg, const void *wu, int64_t ldwu, int act,
+                   const void *zg, int64_t ldzg, const void *zu, int64_t ldzu, void *dx, int64_t lddx, void *dwg,
+                   int64_t lddwg, void *dwu, int64_t lddwu, void *dbg, void *dbu);
+
 /* The gated delta rule.  Each value head of a sequence has a state S (dk x dv,
  * float32), and every token t, with a_t = exp(g_t),
  *   u_t = beta_t (v_t - a_t S^T k_t),  S <- a_t S + k_t u_t^T,  o_t = scale S^T q_t.

@@ -214,9 +214,127 @@ __device__ __forceinline__ void finish_turned(const Epilogue &e, int64_t row, in
     __syncwarp();  // read before the warp's next values come
 }
 
+// The gated form's: y = act(g + bg) (u + bu) of the two products g and u.  part: float32
+// partial sums, rows of 2 ldp: g's, then u's.
+struct GluEpilogue {
+    const void *bg, *bu;  // NULL: none
+    void *y;
+    void *zg, *zu;        // g + bg and u + bu, NULL: not kept (both or neither)
+    int64_t ldy, ldzg, ldzu;
+    float *part;
+    int64_t ldp;
+    int act;
+    int vec;              // 16-byte accesses allowed in all of them
+};
+
+// y into g
+template <int N>
+__device__ __forceinline__ void glu_all(float (&g)[N], const float (&u)[N], int act) {
+    act_all(g, act);
+#pragma unroll
+    for (int i = 0; i < N; i++) g[i] *= u[i];
+}
+
+template <typename T>
+__device__ __forceinline__ void glu_finish8(const GluEpilogue &e, int64_t row, int64_t c, int nc, float (&g)[8], float (&u)[8]) {
+    float f[8];
+    if (e.bg) {
+        load8<T>(e.bg, c, nc, e.vec, f);
+#pragma unroll
+        for (int i = 0; i < 8; i++) g[i] += f[i];
+    }
+    if (e.bu) {
+        load8<T>(e.bu, c, nc, e.vec, f);
+#pragma unroll
+        for (int i = 0; i < 8; i++) u[i] += f[i];
+    }
+    if (e.zg) {
+        store8<T>(e.zg, row * e.ldzg + c, nc, e.vec, g);
+        store8<T>(e.zu, row * e.ldzu + c, nc, e.vec, u);
+    }
+    glu_all(g, u, e.act);
+    store8<T>(e.y, row * e.ldy + c, nc, e.vec, g);
+}
+
+// 32 columns' biases, all there and aligned, loaded a step ahead.
+template <typename T>
+struct GluAhead {
+    Vec<T, 8> g[4], u[4];
+    __device__ __forceinline__ void load(const GluEpilogue &e, int64_t c) {
+#pragma unroll
+        for (int j = 0; j < 4; j++) {
+            if (e.bg) g[j].load(reinterpret_cast<const T *>(e.bg) + c + 8 * j);
+            if (e.bu) u[j].load(reinterpret_cast<const T *>(e.bu) + c + 8 * j);
+        }
+    }
+};
+template <typename T>
+__device__ __forceinline__ void store32(void *base, int64_t at, const float (&v)[32]) {
+    Vec<T, 8> w;
+#pragma unroll
+    for (int j = 0; j < 4; j++) w.set(v + 8 * j), w.store(reinterpret_cast<T *>(base) + at + 8 * j);
+}
+template <typename T>
+__device__ __forceinline__ void glu_finish32(const GluEpilogue &e, int64_t row, int64_t c, const GluAhead<T> &in, float (&g)[32],
+                                             float (&u)[32]) {
+    float f[8];
+#pragma unroll
+    for (int j = 0; j < 4; j++) {
+        if (e.bg) {
+            in.g[j].get(f);
+#pragma unroll
+            for (int i = 0; i < 8; i++) g[8 * j + i] += f[i];
+        }
+        if (e.bu) {
+            in.u[j].get(f);
+#pragma unroll
+            for (int i = 0; i < 8; i++) u[8 * j + i] += f[i];
+        }
+    }
+    if (e.zg) {
+        store32<T>(e.zg, row * e.ldzg + c, g);
+        store32<T>(e.zu, row * e.ldzu + c, u);
+    }
+    glu_all(g, u, e.act);
+    store32<T>(e.y, row * e.ldy + c, g);
+}
+
+// As finish_turned, a matrix at a time.
+template <typename T>
+__device__ __forceinline__ void store_turned(void *base, int64_t ld, int64_t row, int rows, int64_t c, int cols,
+                                             const float (&v)[32], float *turn) {
+    const int lane = threadIdx.x & 31;
+#pragma unroll
+    for (int i = 0; i < 32; i++) turn[lane * kTurnLd + i] = v[i];
+    __syncwarp();
+    T *p = reinterpret_cast<T *>(base) + row * ld + c + lane;
+    if (lane < cols)
+#pragma unroll 8
+        for (int r = 0; r < rows; r++) p[r * ld] = from_f32<T>(turn[r * kTurnLd + lane]);
+    __syncwarp();  // read before the warp's next values come
+}
+template <typename T>
+__device__ __forceinline__ void glu_turned(const GluEpilogue &e, int64_t row, int rows, int64_t c, int cols, float (&g)[32],
+                                           float (&u)[32], float *turn) {
+#pragma unroll
+    for (int i = 0; i < 32; i++) {
+        if (e.bg && i < cols) g[i] += to_f32(reinterpret_cast<const T *>(e.bg)[c + i]);
+        if (e.bu && i < cols) u[i] += to_f32(reinterpret_cast<const T *>(e.bu)[c + i]);
+    }
+    if (e.zg) {
+        store_turned<T>(e.zg, e.ldzg, row, rows, c, cols, g, turn);
+        store_turned<T>(e.zu, e.ldzu, row, rows, c, cols, u, turn);
+    }
+    glu_all(g, u, e.act);
+    store_turned<T>(e.y, e.ldy, row, rows, c, cols, g, turn);
+}
+
 }  // namespace zs
 
 // linear_few.cu: y for at most kFewRows rows of x, in one kernel without a workspace.
 constexpr int kFewRows = 16;
 cudaError_t zs_launch_linear_few(int type, int64_t m, int64_t n, int64_t k, const void *x, int64_t ldx, const void *w,
                                  int64_t ldw, const zs::Epilogue &epi, cudaStream_t st, int64_t *launches);
+// The gated form's, in the same way.
+cudaError_t zs_launch_glu_few(int type, int64_t m, int64_t n, int64_t k, const void *x, int64_t ldx, const void *wg, int64_t ldwg,
+                              const void *wu, int64_t ldwu, const zs::GluEpilogue &epi, cudaStream_t st, int64_t *launches);

@@ -93,6 +93,88 @@ k_linear_few(const uint16_t *__restrict__ x, int64_t ldx, const uint16_t *__rest
     }
 }
 
+// The gated form's: a block owns 16 columns of both products, so that a warp has the loads of
+// both weights on their way.
+template <typename T, int NT, bool VEC>
+__global__ void __launch_bounds__(kWarps * 32)
+k_glu_few(const uint16_t *__restrict__ x, int64_t ldx, const uint16_t *__restrict__ wg, int64_t ldwg, const uint16_t *__restrict__ wu,
+          int64_t ldwu, int m, int64_t n, int64_t k, const GluEpilogue epi) {
+    __shared__ float part[kWarps][2][8 * NT][kOut + 1];
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
+    const int64_t n0 = (int64_t)blockIdx.x * kOut;
+    const bool in0 = n0 + g < n, in1 = n0 + g + 8 < n;
+    const int64_t r0 = in0 ? n0 + g : 0, r1 = in1 ? n0 + g + 8 : 0;
+    const uint16_t *w0[2] = {wg + r0 * ldwg, wu + r0 * ldwu}, *w1[2] = {wg + r1 * ldwg, wu + r1 * ldwu};
+    const uint16_t *xr[NT];
+    bool xin[NT];
+#pragma unroll
+    for (int j = 0; j < NT; j++) {
+        xin[j] = j * 8 + g < m;
+        xr[j] = x + (xin[j] ? j * 8 + g : 0) * ldx;
+    }
+    float acc[2][NT][4] = {};
+#pragma unroll 4
+    for (int64_t c = warp * 32 + t * 8; c < (k + 31) / 32 * 32; c += kWarps * 32) {
+        uint32_t a0[2][4], a1[2][4];
+#pragma unroll
+        for (int p = 0; p < 2; p++) {
+            const uint4 a = row8<VEC>(w0[p], c, k, in0), b = row8<VEC>(w1[p], c, k, in1);
+            a0[p][0] = a.x, a0[p][1] = b.x, a0[p][2] = a.y, a0[p][3] = b.y;
+            a1[p][0] = a.z, a1[p][1] = b.z, a1[p][2] = a.w, a1[p][3] = b.w;
+        }
+#pragma unroll
+        for (int j = 0; j < NT; j++) {
+            const uint4 v = row8<VEC>(xr[j], c, k, xin[j]);
+#pragma unroll
+            for (int p = 0; p < 2; p++) {
+                mma16<T>(acc[p][j], a0[p], v.x, v.y);
+                mma16<T>(acc[p][j], a1[p], v.z, v.w);
+            }
+        }
+    }
+#pragma unroll
+    for (int p = 0; p < 2; p++)
+#pragma unroll
+        for (int j = 0; j < NT; j++)
+#pragma unroll
+            for (int e = 0; e < 4; e++) part[warp][p][j * 8 + 2 * t + (e & 1)][g + (e >> 1) * 8] = acc[p][j][e];
+    __syncthreads();
+    for (int i = threadIdx.x; i < 8 * NT * kOut; i += kWarps * 32) {
+        const int r = i / kOut, c = i - r * kOut;
+        if (r >= m || n0 + c >= n) continue;
+        float vg[1] = {0.f}, vu[1] = {0.f};
+#pragma unroll
+        for (int q = 0; q < kWarps; q++) vg[0] += part[q][0][r][c], vu[0] += part[q][1][r][c];
+        const int64_t col = n0 + c;
+        if (epi.bg) vg[0] += to_f32(reinterpret_cast<const T *>(epi.bg)[col]);
+        if (epi.bu) vu[0] += to_f32(reinterpret_cast<const T *>(epi.bu)[col]);
+        if (epi.zg) {
+            reinterpret_cast<T *>(epi.zg)[r * epi.ldzg + col] = from_f32<T>(vg[0]);
+            reinterpret_cast<T *>(epi.zu)[r * epi.ldzu + col] = from_f32<T>(vu[0]);
+        }
+        glu_all(vg, vu, epi.act);
+        reinterpret_cast<T *>(epi.y)[r * epi.ldy + col] = from_f32<T>(vg[0]);
+    }
+}
+
+template <typename T>
+cudaError_t glu_few(int64_t m, int64_t n, int64_t k, const void *x, int64_t ldx, const void *wg, int64_t ldwg, const void *wu,
+                    int64_t ldwu, const GluEpilogue &epi, cudaStream_t st) {
+    const uint16_t *px = (const uint16_t *)x, *pg = (const uint16_t *)wg, *pu = (const uint16_t *)wu;
+    const bool vec = (((uintptr_t)x | (uintptr_t)wg | (uintptr_t)wu | (uint64_t)ldx * 2 | (uint64_t)ldwg * 2 | (uint64_t)ldwu * 2) & 15) == 0;
+    const unsigned grid = (unsigned)((n + kOut - 1) / kOut);
+#define FEW_GO(NT, V) k_glu_few<T, NT, V><<<grid, kWarps * 32, 0, st>>>(px, ldx, pg, ldwg, pu, ldwu, (int)m, n, k, epi)
+    if (m <= 8) {
+        if (vec) FEW_GO(1, true);
+        else FEW_GO(1, false);
+    } else {
+        if (vec) FEW_GO(2, true);
+        else FEW_GO(2, false);
+    }
+#undef FEW_GO
+    return cudaGetLastError();
+}
+
 template <typename T>
 cudaError_t few(int64_t m, int64_t n, int64_t k, const void *x, int64_t ldx, const void *w, int64_t ldw,
                 const Epilogue &epi, cudaStream_t st) {
@@ -117,4 +199,11 @@ cudaError_t zs_launch_linear_few(int type, int64_t m, int64_t n, int64_t k, cons
                                  int64_t ldw, const Epilogue &epi, cudaStream_t st, int64_t *launches) {
     ++*launches;
     return type == ZSOLVE_BF16 ? few<bf16>(m, n, k, x, ldx, w, ldw, epi, st) : few<f16>(m, n, k, x, ldx, w, ldw, epi, st);
+}
+
+cudaError_t zs_launch_glu_few(int type, int64_t m, int64_t n, int64_t k, const void *x, int64_t ldx, const void *wg, int64_t ldwg,
+                              const void *wu, int64_t ldwu, const GluEpilogue &epi, cudaStream_t st, int64_t *launches) {
+    ++*launches;
+    return type == ZSOLVE_BF16 ? glu_few<bf16>(m, n, k, x, ldx, wg, ldwg, wu, ldwu, epi, st)
+                               : glu_few<f16>(m, n, k, x, ldx, wg, ldwg, wu, ldwu, epi, st);
 }

@@ -368,6 +368,38 @@ int zsolve_linear_bwd(zsolve_seq *s, int type, int64_t m, int64_t n, int64_t k, 
     return zs_linear_bwd(s, type, m, n, k, dy, lddy, x, ldx, w, ldw, act, z, ldz, dx, lddx, dw, lddw, db);
 }
 
+int zsolve_glu(zsolve_seq *s, int type, int64_t m, int64_t n, int64_t k, const void *x, int64_t ldx, const void *wg, int64_t ldwg,
+               const void *wu, int64_t ldwu, const void *bg, const void *bu, int act, void *y, int64_t ldy, void *zg, int64_t ldzg,
+               void *zu, int64_t ldzu) {
+    if (!s) return ZSOLVE_EINVAL;
+    int st = check_linear(s, type, act, m, n, k);
+    if (st != ZSOLVE_OK || m == 0) return st;
+    if (!x || !wg || !wu || !y || !zg != !zu) return seq_fail(s, ZSOLVE_EINVAL, "NULL x, wg, wu or y, or one of zg and zu without the other");
+    if (ldx < k || ldwg < k || ldwu < k || ldy < n || (zg && (ldzg < n || ldzu < n)))
+        return seq_fail(s, ZSOLVE_EINVAL, "a row stride is below its row's length");
+    st = check_device(s);
+    if (st != ZSOLVE_OK) return st;
+    return zs_glu(s, type, m, n, k, x, ldx, wg, ldwg, wu, ldwu, bg, bu, act, y, ldy, zg, ldzg, zu, ldzu);
+}
+
+int zsolve_glu_bwd(zsolve_seq *s, int type, int64_t m, int64_t n, int64_t k, const void *dy, int64_t lddy, const void *x, int64_t ldx,
+                   const void *wg, int64_t ldwg, const void *wu, int64_t ldwu, int act, const void *zg, int64_t ldzg, const void *zu,
+                   int64_t ldzu, void *dx, int64_t lddx, void *dwg, int64_t lddwg, void *dwu, int64_t lddwu, void *dbg, void *dbu) {
+    if (!s) return ZSOLVE_EINVAL;
+    int st = check_linear(s, type, act, m, n, k);
+    if (st != ZSOLVE_OK) return st;
+    const bool dw = dwg || dwu;
+    if (m > 0 && (!dy || !zg || !zu || (dw && !x) || (dx && (!wg || !wu))))
+        return seq_fail(s, ZSOLVE_EINVAL, "NULL dy, zg, zu, or an x, wg or wu that the gradients asked for need");
+    if ((m > 0 && (lddy < n || ldzg < n || ldzu < n || (dw && ldx < k) || (dx && (ldwg < k || ldwu < k || lddx < k)))) ||
+        (dwg && lddwg < k) || (dwu && lddwu < k))
+        return seq_fail(s, ZSOLVE_EINVAL, "a row stride is below its row's length");
+    st = check_device(s);
+    if (st != ZSOLVE_OK) return st;
+    return zs_glu_bwd(s, type, m, n, k, dy, lddy, x, ldx, wg, ldwg, wu, ldwu, act, zg, ldzg, zu, ldzu, dx, lddx, dwg, lddwg, dwu, lddwu,
+                      dbg, dbu);
+}
+
 int zsolve_delta(zsolve_seq *s, const zsolve_delta_args *a, void *o, int64_t ldo, float *sn) {
     if (!s) return ZSOLVE_EINVAL;
     zs::DeltaGeom g;

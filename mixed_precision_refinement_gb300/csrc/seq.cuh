@@ -305,3 +305,10 @@ int zs_linear(zsolve_seq *s, int type, int64_t m, int64_t n, int64_t k, const vo
 int zs_linear_bwd(zsolve_seq *s, int type, int64_t m, int64_t n, int64_t k, const void *dy, int64_t lddy,
                   const void *x, int64_t ldx, const void *w, int64_t ldw, int act, const void *z, int64_t ldz,
                   void *dx, int64_t lddx, void *dw, int64_t lddw, void *db);
+// glu.cu: the same
+int zs_glu(zsolve_seq *s, int type, int64_t m, int64_t n, int64_t k, const void *x, int64_t ldx, const void *wg, int64_t ldwg,
+           const void *wu, int64_t ldwu, const void *bg, const void *bu, int act, void *y, int64_t ldy, void *zg, int64_t ldzg,
+           void *zu, int64_t ldzu);
+int zs_glu_bwd(zsolve_seq *s, int type, int64_t m, int64_t n, int64_t k, const void *dy, int64_t lddy, const void *x, int64_t ldx,
+               const void *wg, int64_t ldwg, const void *wu, int64_t ldwu, int act, const void *zg, int64_t ldzg, const void *zu,
+               int64_t ldzu, void *dx, int64_t lddx, void *dwg, int64_t lddwg, void *dwu, int64_t lddwu, void *dbg, void *dbu);

@@ -233,6 +233,35 @@ def zsolve_linear_bwd(seq, dy, x, w, act, z, dx=None, dw=None, db=None) -> None:
                                            ldz, dxp, lddx, dwp, lddw, _vector(db, "db", n, x.dtype)))
 
 
+def zsolve_glu(seq, x, wg, wu, bg, bu, act, y, zg=None, zu=None) -> None:
+    """y <- act(x wg^T + bg) (x wu^T + bu); x (..., k), wg, wu (n, k), bg, bu (n,) or None, y (..., n); zg, zu: as y, or None."""
+    xp, m, k, ldx = _rows(x, "x")
+    gp, n, _, ldg = _rows(wg, "wg", x.dtype, (wg.shape[0], k))
+    up, _, _, ldu = _rows(wu, "wu", x.dtype, (n, k))
+    yp, _, _, ldy = _rows(y, "y", x.dtype, (m, n))
+    zgp, ldzg = _optional_rows(zg, "zg", x.dtype, (m, n))
+    zup, ldzu = _optional_rows(zu, "zu", x.dtype, (m, n))
+    _check_seq(seq, _lib.zsolve_glu(seq, _type(x, "x"), m, n, k, xp, ldx, gp, ldg, up, ldu, _vector(bg, "bg", n, x.dtype),
+                                    _vector(bu, "bu", n, x.dtype), _act(act), yp, ldy, zgp, ldzg, zup, ldzu))
+
+
+def zsolve_glu_bwd(seq, dy, x, wg, wu, act, zg, zu, dx=None, dwg=None, dwu=None, dbg=None, dbu=None) -> None:
+    """dx, dwg, dwu, dbg and dbu (shapes of x, the weights and the biases; None: not formed) from dy; zg, zu: as zsolve_glu
+    kept them."""
+    xp, m, k, ldx = _rows(x, "x")
+    gp, n, _, ldg = _rows(wg, "wg", x.dtype, (wg.shape[0], k))
+    up, _, _, ldu = _rows(wu, "wu", x.dtype, (n, k))
+    dyp, _, _, lddy = _rows(dy, "dy", x.dtype, (m, n))
+    zgp, _, _, ldzg = _rows(zg, "zg", x.dtype, (m, n))
+    zup, _, _, ldzu = _rows(zu, "zu", x.dtype, (m, n))
+    dxp, lddx = _optional_rows(dx, "dx", x.dtype, (m, k))
+    dgp, lddg = _optional_rows(dwg, "dwg", x.dtype, (n, k))
+    dup, lddu = _optional_rows(dwu, "dwu", x.dtype, (n, k))
+    _check_seq(seq, _lib.zsolve_glu_bwd(seq, _type(x, "x"), m, n, k, dyp, lddy, xp, ldx, gp, ldg, up, ldu, _act(act), zgp, ldzg,
+                                        zup, ldzu, dxp, lddx, dgp, lddg, dup, lddu, _vector(dbg, "dbg", n, x.dtype),
+                                        _vector(dbu, "dbu", n, x.dtype)))
+
+
 class zsolve_delta_args(ctypes.Structure):
     _fields_ = [("type", ctypes.c_int), ("hk", ctypes.c_int), ("hv", ctypes.c_int), ("dk", ctypes.c_int),
                 ("dv", ctypes.c_int), ("nseq", ctypes.c_int), ("tokens", ctypes.c_int64),
@@ -409,6 +438,28 @@ class Seq:
         db = torch.empty(w.shape[:1], dtype=x.dtype, device=x.device)
         zsolve_linear_bwd(self.seq, dy, x, w, act, z, dx, dw, db)
         return dx, dw, db
+
+    def glu(self, x, wg, wu, bg=None, bu=None, act="silu", keep=False):
+        """y = act(x wg^T + bg) (x wu^T + bu); with keep=True (y, zg, zu), zg and zu for glu_bwd."""
+        if _records(x, wg, wu, bg, bu):
+            return _autograd().Glu.apply(self, x, wg, wu, bg, bu, act, keep)
+        self._on_stream()
+        shape = x.shape[:-1] + wg.shape[:1]
+        y = torch.empty(shape, dtype=x.dtype, device=x.device)
+        zg = torch.empty_like(y) if keep else None
+        zu = torch.empty_like(y) if keep else None
+        zsolve_glu(self.seq, x, wg, wu, bg, bu, act, y, zg, zu)
+        return (y, zg, zu) if keep else y
+
+    def glu_bwd(self, dy, x, wg, wu, zg, zu, act="silu"):
+        """Returns (dx, dwg, dwu, dbg, dbu); zg and zu as glu(keep=True) returned them."""
+        self._on_stream()
+        dx = torch.empty(x.shape, dtype=x.dtype, device=x.device)
+        n, k = wg.shape
+        dwg, dwu = torch.empty((2, n, k), dtype=x.dtype, device=x.device).unbind()
+        dbg, dbu = torch.empty((2, n), dtype=x.dtype, device=x.device).unbind()
+        zsolve_glu_bwd(self.seq, dy, x, wg, wu, act, zg, zu, dx, dwg, dwu, dbg, dbu)
+        return dx, dwg, dwu, dbg, dbu
 
     def delta(self, q, k, v, g, beta, s0=None, offsets=None, scale=None):
         """Returns (o, s): the gated delta rule over whole sequences, from the states s0 (zero without) to s.

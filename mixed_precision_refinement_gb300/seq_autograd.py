@@ -63,6 +63,31 @@ class Linear(torch.autograd.Function):
         return None, dx, dw, db, None, dy if needs[5] else None, None
 
 
+class Glu(torch.autograd.Function):
+    @staticmethod
+    def forward(ctx, seq, x, wg, wu, bg, bu, act, keep):
+        y, zg, zu = seq.glu(x, wg, wu, bg, bu, act, keep=True)
+        ctx.seq, ctx.act = seq, act
+        ctx.set_materialize_grads(False)
+        ctx.save_for_backward(x, wg, wu, zg, zu)
+        return (y, zg, zu) if keep else y
+
+    @staticmethod
+    @once_differentiable
+    def backward(ctx, dy, dzg=None, dzu=None):
+        _unused("glu: zg and zu", dzg, dzu)
+        if dy is None:
+            return (None,) * 8
+        x, wg, wu, zg, zu = ctx.saved_tensors
+        needs = ctx.needs_input_grad[1:6]
+        shapes = (x.shape, wg.shape, wu.shape, wg.shape[:1], wu.shape[:1])
+        grads = [torch.empty(n, dtype=x.dtype, device=x.device) if need else None for n, need in zip(shapes, needs)]
+        if any(needs):
+            ctx.seq._on_stream()
+            binding.zsolve_glu_bwd(ctx.seq.seq, dy.contiguous(), x, wg, wu, ctx.act, zg, zu, *grads)
+        return (None, *grads, None, None)
+
+
 class Delta(torch.autograd.Function):
     @staticmethod
     def forward(ctx, seq, q, k, v, g, beta, s0, offsets, scale):

@@ -518,6 +518,39 @@ int zsolve_layernorm_bwd(zsolve_seq *seq, int type, int wtype, int64_t rows, int
                          const void *x, int64_t ldx, const float *mean, const float *rstd, const void *w, void *dx,
                          int64_t lddx, void *dw, void *db);
 
+/* The join of a block and the residual stream x: the norm of the block's output o, its gate z and
+ * residual scale c, the sum, and the norm in front of the next block,
+ *   t = norm(o) w1 + b1, y = x + c act(z) t, h = norm(y) w2 + b2,
+ * each of `rows` rows of d values of `type`; norm(v) = (v - mu) rs with mu = mean v, rs = (mean
+ * (v - mu)^2 + eps)^-1/2 (ZSOLVE_NORM_LAYER), or mu = 0 (ZSOLVE_NORM_RMS). */
+#define ZSOLVE_NORM_LAYER 0
+#define ZSOLVE_NORM_RMS 1
+
+typedef struct {
+    int type, wtype;        /* of the tensors; of w1 .. b2: `type` or ZSOLVE_F32 */
+    int kind;               /* ZSOLVE_NORM_* of both norms */
+    int after;              /* 0: without the first norm, t = o w1 + b1 */
+    int act;                /* ZSOLVE_ACT_* of the gate */
+    int64_t rows, d;
+    const void *o, *z;      /* z NULL: no gate */
+    int64_t ldo, ldz;
+    const void *w1, *b1, *c, *w2, *b2; /* d values each (NULL: 1, 0, 1, 1, 0) */
+    double eps;
+} zsolve_resnorm_args;
+
+/* y, h, and stats: four float32 values a row, mu and rs of the first norm (0 and 1 without it) and
+ * of the second, for the backward pass (NULL: not written).  h comes from y before it is rounded.
+ * y may be x itself (ldy = ldx). */
+int zsolve_resnorm(zsolve_seq *seq, const zsolve_resnorm_args *args, const void *x, int64_t ldx, void *y, int64_t ldy,
+                   void *h, int64_t ldh, float *stats);
+
+/* Its gradients, from dh and dy, those of h and y (dy NULL: zero): dx is x's, dout o's, dz the
+ * gate's (NULL: not formed), and dw1 .. db2, of `wtype`, the weights' (NULL: not formed), whose sums over the
+ * rows are added in a fixed order.  args as for the forward pass; eps and b2 are not used. */
+int zsolve_resnorm_bwd(zsolve_seq *seq, const zsolve_resnorm_args *args, const void *dh, int64_t lddh, const void *dy,
+                       int64_t lddy, const void *y, int64_t ldy, const float *stats, void *dx, int64_t lddx, void *dout,
+                       int64_t lddo, void *dz, int64_t lddz, void *dw1, void *db1, void *dc, void *dw2, void *db2);
+
 /* z = x W^T + b, y = act(z) + r: x is m x k, W n x k, y m x n, all of `type`
  * (ZSOLVE_BF16 or ZSOLVE_F16), on the tensor cores with float32 sums.
  *   b      n values (NULL: none);  r   m x n (NULL: none)

@@ -12,80 +12,11 @@
 // float32, half a unit of its last place.
 #include <algorithm>
 
-#include "seq.cuh"
+#include "rownorm.cuh"
 
 namespace {
 
 using namespace zs;
-
-// Sum of v over the TPR threads of a row.  TPR = 32: one warp; else the row's
-// warps exchange their sums through `red` (one slot a warp; `flip` alternates
-// two sets, so that one barrier a reduction is enough).
-template <int TPR>
-__device__ __forceinline__ float2 row_sum(float2 v, float2 *red, int flip) {
-    v.x = warp_sum(v.x);
-    v.y = warp_sum(v.y);
-    if (TPR == 32) return v;
-    constexpr int NW = TPR / 32;
-    float2 *r = red + flip * NW;
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    if (lane == 0) r[warp] = v;
-    __syncthreads();
-    // every thread adds the warps' sums itself: broadcast reads, without the
-    // latency of five more shuffles
-    float2 t = r[0], u = r[1];
-#pragma unroll
-    for (int w = 2; w < NW; w += 2) {
-        t.x += r[w].x, t.y += r[w].y;
-        u.x += r[w + 1].x, u.y += r[w + 1].y;
-    }
-    return make_float2(t.x + u.x, t.y + u.y);
-}
-
-// A load that stays where it is written: the next rows' mean and rstd, which the
-// compiler would otherwise be free to move down to their use, a row later.
-__device__ __forceinline__ float load_early(const float *p) {
-    float v;
-    asm volatile("ld.global.nc.f32 %0, [%1];" : "=f"(v) : "l"(p));
-    return v;
-}
-
-template <typename T>
-__device__ __forceinline__ float load_w(const void *w, int wf32, int64_t i) {
-    return wf32 ? reinterpret_cast<const float *>(w)[i] : to_f32(reinterpret_cast<const T *>(w)[i]);
-}
-
-// w at N consecutive columns (aligned as x is when N > 1)
-template <typename T, int N>
-__device__ __forceinline__ void load_wv(const void *w, int wf32, int64_t i, float *f) {
-    if (N > 1 && !wf32) {
-        Vec<T, N> v;
-        v.load(reinterpret_cast<const T *>(w) + i);
-        v.get(f);
-        return;
-    }
-#pragma unroll
-    for (int e = 0; e < N; e++) f[e] = load_w<T>(w, wf32, i + e);
-}
-
-// The same from shared memory, where both types of w are aligned.
-template <typename T, int N>
-__device__ __forceinline__ void load_ws(const void *w, int wf32, int i, float *f) {
-    if (N > 1 && wf32) {
-#pragma unroll
-        for (int e = 0; e < N; e += 4)
-            *reinterpret_cast<float4 *>(f + e) = *reinterpret_cast<const float4 *>(reinterpret_cast<const float *>(w) + i + e);
-    } else {
-        load_wv<T, N>(w, wf32, i, f);
-    }
-}
-
-// rs from mean (x - m)^2 and e = mean (x - m), whose square is at most the former but for
-// rounding (NaN stays).
-__device__ __forceinline__ float inv_std(float square, float e, float eps) {
-    const float var = fmaf(-e, e, square);
-    return 1.f / sqrtf((var < 0.f ? 0.f : var) + eps);
-}
 
 // Forward: TPR threads hold a row, VE consecutive values at a time (VE = 1
 // where rows are not 16-byte aligned), NI times; four rows a block of 128 threads
@@ -316,10 +247,6 @@ template <int E>
 __host__ __device__ constexpr int ring_threads() {
     return E > 8 ? 768 : 1024;
 }
-template <typename T>
-__host__ __device__ constexpr int ring_row(int d) {  // values of a ring row
-    return (d + 2 * (16 / (int)sizeof(T)) - 1) / (16 / (int)sizeof(T)) * (16 / (int)sizeof(T));
-}
 
 template <typename T, int VE, int TPR, int NI>
 __global__ void __launch_bounds__(TPR, ring_threads<NI * VE>() / TPR > 0 ? ring_threads<NI * VE>() / TPR : 1)
@@ -534,8 +461,6 @@ k_layernorm_bwd_sum(const float *__restrict__ parts, int64_t nparts, int64_t d, 
     else
         reinterpret_cast<T *>(dst)[i] = from_f32<T>(v);
 }
-
-bool aligned16(const void *p) { return ((uintptr_t)p & 15) == 0; }
 
 // Longest rows held in registers.
 constexpr int64_t kMaxRow = 16384;

@@ -1,0 +1,786 @@
+// The join of a block and the residual stream: the norm of the block's output, its gate and
+// residual scale, the sum, and the norm in front of the next block, in one pass.
+//   h1 = (o - mu1) rs1, t = h1 w1 + b1, y = x + c act(z) t, h2 = (y - mu2) rs2, h = h2 w2 + b2
+//   (layer norm: mu the row's mean, rs = (mean (v - mu)^2 + eps)^-1/2; root mean square: mu = 0;
+//   without the first norm: mu1 = 0, rs1 = 1)
+// and backwards, a2 = dh w2, norm'(a, h, rs) = rs (a - mean a - h mean(a h)) (root mean square:
+// without mean a):
+//   dx = dy + norm'(a2, h2, rs2), p = dx c act(z) (the gradient of t),
+//   do = norm'(p w1, h1, rs1), dz = dx c t act'(z),
+//   dw1 = sum p h1, db1 = sum p, dw2 = sum dh h2, db2 = sum dh over the rows,
+//   dc = sum dx act(z) t.
+// With u = dx act(z), Q = sum u h1 and R = sum u: dw1 = c Q, db1 = c R, dc = w1 Q + b1 R, so four
+// sums a column serve all five.
+// Both are bound by HBM: each tensor crosses it once, a row is held in registers between its
+// reductions.  Sums, statistics and what lies between the norms are float32; y is rounded for
+// memory alone, and h comes from the value before that rounding.  As in layernorm.cu, a mean's
+// own error is found again in the second pass.
+#include <algorithm>
+
+#include "linear.cuh"
+#include "rownorm.cuh"
+
+namespace {
+
+using namespace zs;
+
+// What the kernels take beside the tensors' places.
+struct ResGeom {
+    const void *w1, *b1, *c, *w2, *b2;  // d values each; NULL: ones, zeros, ones, ...
+    int wf32;                           // they are float32, else of the tensors' type
+    int64_t rows;
+    int d;
+    float eps;
+    int act, after, rms;
+};
+
+// 1 / sqrt(mean square + eps) and the correction of the mean, from the sums over a row of
+// (v - m)^2 and v - m.
+struct Stat {
+    float rs, off;
+};
+__device__ __forceinline__ Stat stat_of(float2 s, float inv, float eps, int rms) {
+    Stat r;
+    r.off = rms ? 0.f : s.y * inv;
+    r.rs = inv_std(s.x * inv, r.off, eps);
+    return r;
+}
+
+template <int N>
+__device__ __forceinline__ void slopes_all(const float (&z)[N], int act, float (&a)[N], float (&s)[N]) {
+#define RES_CASE(A)                                                                                  \
+    case A: {                                                                                        \
+        _Pragma("unroll") for (int i = 0; i < N; i++) a[i] = act1<A>(z[i]), s[i] = slope1<A>(z[i]); \
+        break;                                                                                       \
+    }
+    switch (act) {
+        RES_CASE(ACT_NONE)
+        RES_CASE(ACT_RELU)
+        RES_CASE(ACT_SILU)
+        RES_CASE(ACT_GELU)
+        RES_CASE(ACT_GELU_TANH)
+    }
+#undef RES_CASE
+}
+
+// Forward: TPR threads hold a row, VE consecutive values at a time (VE = 1 where rows are not
+// 16-byte aligned), NI times; four rows a block where a warp holds one, else a row a block.
+template <typename T, int VE, int TPR, int NI>
+__global__ void __launch_bounds__(TPR < 128 ? 128 : TPR)
+k_resnorm(const T *x, int64_t ldx, const T *__restrict__ o, int64_t ldo, const T *__restrict__ z, int64_t ldz, const ResGeom g,
+          T *y, int64_t ldy, T *__restrict__ h, int64_t ldh, float *__restrict__ stats) {
+    __shared__ float2 red[TPR == 32 ? 1 : 2 * (TPR / 32)];
+    const int64_t row = TPR == 32 ? (int64_t)blockIdx.x * 4 + (threadIdx.x >> 5) : (int64_t)blockIdx.x;
+    const int t = TPR == 32 ? threadIdx.x & 31 : threadIdx.x;
+    if (row >= g.rows) return;  // whole rows leave: no barrier is missed
+    const int d = g.d;
+    Vec<T, VE> ux[NI], uo[NI], uz[NI];
+#pragma unroll
+    for (int i = 0; i < NI; i++) {
+        const int c = (i * TPR + t) * VE;
+        if (c < d) {
+            uo[i].load(o + row * ldo + c);
+            ux[i].load(x + row * ldx + c);
+            if (z) uz[i].load(z + row * ldz + c);
+        }
+    }
+    const float inv = 1.f / (float)d;
+    float v[NI * VE];
+    auto each = [&](auto f) {  // f(i, c): the thread's pieces of the row
+#pragma unroll
+        for (int i = 0; i < NI; i++) {
+            const int c = (i * TPR + t) * VE;
+            if (c < d) f(i, c);
+        }
+    };
+    int flip = 0;
+    // v - its mean, and the statistics: the mean first, unless it counts as zero
+    auto standard = [&](float &mu) {
+        float2 s = make_float2(0.f, 0.f);
+        mu = 0.f;
+        if (!g.rms) {
+            each([&](int i, int) {
+#pragma unroll
+                for (int e = 0; e < VE; e++) s.x += v[i * VE + e];
+            });
+            mu = row_sum<TPR>(s, red, flip).x * inv;
+            flip ^= 1;
+            s = make_float2(0.f, 0.f);
+        }
+        each([&](int i, int) {
+#pragma unroll
+            for (int e = 0; e < VE; e++) {
+                float &w = v[i * VE + e];
+                w -= mu;
+                s.x = fmaf(w, w, s.x);
+                s.y += w;
+            }
+        });
+        s = row_sum<TPR>(s, red, flip);
+        flip ^= 1;
+        return stat_of(s, inv, g.eps, g.rms);
+    };
+    each([&](int i, int) { uo[i].get(v + i * VE); });
+    float mu1 = 0.f, mu2;
+    Stat s1 = {1.f, 0.f};
+    if (g.after) s1 = standard(mu1);
+    const float shift1 = -s1.off * s1.rs;
+    each([&](int i, int c) {
+        float f[VE], a[VE];
+#pragma unroll
+        for (int e = 0; e < VE; e++) a[e] = g.after ? fmaf(v[i * VE + e], s1.rs, shift1) : v[i * VE + e];
+        if (g.w1) {
+            load_wv<T, VE>(g.w1, g.wf32, c, f);
+#pragma unroll
+            for (int e = 0; e < VE; e++) a[e] *= f[e];
+        }
+        if (g.b1) {
+            load_wv<T, VE>(g.b1, g.wf32, c, f);
+#pragma unroll
+            for (int e = 0; e < VE; e++) a[e] += f[e];
+        }
+        if (z) {
+            uz[i].get(f);
+            act_all(f, g.act);
+#pragma unroll
+            for (int e = 0; e < VE; e++) a[e] *= f[e];
+        }
+        float w[VE];
+        ux[i].get(w);
+        if (g.c) {
+            load_wv<T, VE>(g.c, g.wf32, c, f);
+#pragma unroll
+            for (int e = 0; e < VE; e++) w[e] = fmaf(f[e], a[e], w[e]);
+        } else {
+#pragma unroll
+            for (int e = 0; e < VE; e++) w[e] += a[e];
+        }
+        Vec<T, VE> r;
+        r.set(w);
+        r.store(y + row * ldy + c);
+#pragma unroll
+        for (int e = 0; e < VE; e++) v[i * VE + e] = w[e];
+    });
+    const Stat s2 = standard(mu2);
+    const float shift2 = -s2.off * s2.rs;
+    if (t == 0 && stats) {
+        float *p = stats + 4 * row;
+        p[0] = mu1 + s1.off, p[1] = s1.rs, p[2] = mu2 + s2.off, p[3] = s2.rs;
+    }
+    each([&](int i, int c) {
+        float a[VE], f[VE];
+#pragma unroll
+        for (int e = 0; e < VE; e++) a[e] = fmaf(v[i * VE + e], s2.rs, shift2);
+        if (g.w2) {
+            load_wv<T, VE>(g.w2, g.wf32, c, f);
+#pragma unroll
+            for (int e = 0; e < VE; e++) a[e] *= f[e];
+        }
+        if (g.b2) {
+            load_wv<T, VE>(g.b2, g.wf32, c, f);
+#pragma unroll
+            for (int e = 0; e < VE; e++) a[e] += f[e];
+        }
+        Vec<T, VE> r;
+        r.set(a);
+        r.store(h + row * ldh + c);
+    });
+}
+
+// Rows too long for the registers: one block a row in passes over it, mostly from L2.
+constexpr int kLong = 1024;
+template <typename T>
+struct ResValue {  // y before its rounding
+    const T *x, *o, *z;
+    const ResGeom &g;
+    float mu1, rs1;
+    __device__ __forceinline__ float t(int64_t c) const {
+        float a = (to_f32(o[c]) - mu1) * rs1;
+        if (g.w1) a *= load_w<T>(g.w1, g.wf32, c);
+        if (g.b1) a += load_w<T>(g.b1, g.wf32, c);
+        return a;
+    }
+    __device__ __forceinline__ float operator()(int64_t c) const {
+        float a[1] = {1.f};
+        if (z) {
+            a[0] = to_f32(z[c]);
+            act_all(a, g.act);
+        }
+        const float v = a[0] * t(c);
+        return fmaf(g.c ? load_w<T>(g.c, g.wf32, c) : 1.f, v, to_f32(x[c]));
+    }
+};
+template <typename T>
+__global__ void __launch_bounds__(kLong)
+k_resnorm_long(const T *x, int64_t ldx, const T *__restrict__ o, int64_t ldo, const T *__restrict__ z, int64_t ldz, const ResGeom g,
+               T *y, int64_t ldy, T *__restrict__ h, int64_t ldh, float *__restrict__ stats) {
+    __shared__ float2 red[2 * (kLong / 32)];
+    const int64_t row = blockIdx.x;
+    ResValue<T> val{x + row * ldx, o + row * ldo, z ? z + row * ldz : nullptr, g, 0.f, 1.f};
+    int flip = 0;
+    auto standard = [&](auto f, float &mu) {
+        float2 s = make_float2(0.f, 0.f);
+        mu = 0.f;
+        if (!g.rms) {
+            for (int c = threadIdx.x; c < g.d; c += kLong) s.x += f(c);
+            mu = row_sum<kLong>(s, red, flip).x / (float)g.d;
+            flip ^= 1;
+            s = make_float2(0.f, 0.f);
+        }
+        for (int c = threadIdx.x; c < g.d; c += kLong) {
+            const float w = f(c) - mu;
+            s.x = fmaf(w, w, s.x);
+            s.y += w;
+        }
+        s = row_sum<kLong>(s, red, flip);
+        flip ^= 1;
+        const Stat r = stat_of(s, 1.f / (float)g.d, g.eps, g.rms);
+        mu += r.off;
+        return r.rs;
+    };
+    if (g.after) {
+        float mu1;
+        const float rs1 = standard([&](int c) { return to_f32(val.o[c]); }, mu1);
+        val.mu1 = mu1, val.rs1 = rs1;
+    }
+    float mu2;
+    const float rs2 = standard(val, mu2);
+    if (threadIdx.x == 0 && stats) {
+        float *p = stats + 4 * row;
+        p[0] = val.mu1, p[1] = val.rs1, p[2] = mu2, p[3] = rs2;
+    }
+    for (int c = threadIdx.x; c < g.d; c += kLong) {
+        const float w = val(c);
+        y[row * ldy + c] = from_f32<T>(w);
+        float a = (w - mu2) * rs2;
+        if (g.w2) a *= load_w<T>(g.w2, g.wf32, c);
+        if (g.b2) a += load_w<T>(g.b2, g.wf32, c);
+        h[row * ldh + c] = from_f32<T>(a);
+    }
+}
+
+// ---------------------------------------------------------------- backward
+
+struct ResBack {
+    const void *dh, *dy, *y, *o, *z;  // dy NULL: zeros; z NULL: no gate
+    int64_t lddh, lddy, ldy, ldo, ldz;
+    const float *stats;
+    void *dx, *dout, *dz;             // dz NULL: not formed
+    int64_t lddx, lddo, lddz;
+};
+
+// A block takes a share of the rows, which arrive in a ring of rows in shared memory, a bulk copy
+// for each of the up to five tensors, issued as soon as the row's second reduction shows that every
+// thread has read it.  A thread holds 8 values of a row (16 where the row has more than 4096) and its columns' four sums; the
+// weights lie in shared memory.  A row need not start on 16 bytes (the tensors do): the copy takes the
+// whole 16 bytes that begin in it, and the last values are read directly.
+constexpr int ring_blocks(int tpr) {  // of an SM, as far as the registers go
+    return std::max(1, 65536 / (tpr * 128));
+}
+template <typename T, int VE, int TPR, int E>
+__global__ void __launch_bounds__(TPR, ring_blocks(TPR))
+k_resnorm_bwd(const ResBack p, const ResGeom g, int stages, float *__restrict__ parts, unsigned *__restrict__ status) {
+    extern __shared__ __align__(16) uint8_t smem_raw[];
+    constexpr int kMost = 8;
+    __shared__ float2 red[2 * (TPR < 64 ? 2 : TPR / 32)];
+    __shared__ __align__(8) uint64_t full[kMost];
+    __shared__ volatile int s_abort;
+    may_start_next();
+    const int d = g.d, rr = ring_row<T>(d), t = threadIdx.x;
+    const T *const src[5] = {(const T *)p.dh, (const T *)p.y, (const T *)p.o, (const T *)p.dy, (const T *)p.z};
+    const int64_t lds[5] = {p.lddh, p.ldy, p.ldo, p.lddy, p.ldz};
+    const int place[5] = {0, 1, 2, 3, p.dy ? 4 : 3};
+    const int tensors = 3 + (p.dy ? 1 : 0) + (p.z ? 1 : 0);
+    T *const ring = reinterpret_cast<T *>(smem_raw);
+    const int wsize = ((g.wf32 ? 4 : (int)sizeof(T)) * d + 15) / 16 * 16;
+    uint8_t *const wbase = smem_raw + (size_t)stages * tensors * rr * sizeof(T);
+    const void *const weights[4] = {g.w1, g.b1, g.c, g.w2};
+    const void *ws[4];
+    {
+        int n = 0;
+#pragma unroll
+        for (int k = 0; k < 4; k++) {
+            ws[k] = nullptr;
+            if (!weights[k]) continue;
+            uint8_t *const w = wbase + (size_t)n++ * wsize;
+            ws[k] = w;
+            for (int c = t; c < d; c += TPR) {
+                if (g.wf32)
+                    reinterpret_cast<float *>(w)[c] = reinterpret_cast<const float *>(weights[k])[c];
+                else
+                    reinterpret_cast<T *>(w)[c] = reinterpret_cast<const T *>(weights[k])[c];
+            }
+        }
+    }
+    constexpr int A = 16 / (int)sizeof(T);
+    const float inv = 1.f / (float)d;
+    if (t == 0) {
+        s_abort = 0;
+        for (int i = 0; i < stages; i++) bar_init(&full[i], 1);
+        asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+    }
+    __syncthreads();
+    auto offset = [&](int64_t at) { return (int)((unsigned)at % A); };
+    auto whole = [&](int off) { return (off + d) / A * A; };
+    auto slot_of = [&](int slot, int k) { return ring + ((size_t)slot * tensors + place[k]) * rr; };
+    auto issue = [&](int64_t row, int slot) {
+        uint32_t bytes = 0;
+#pragma unroll
+        for (int k = 0; k < 5; k++)
+            if (src[k]) bytes += (uint32_t)(whole(offset(row * lds[k])) * sizeof(T));
+        bar_expect(&full[slot], bytes);
+#pragma unroll
+        for (int k = 0; k < 5; k++) {
+            if (!src[k]) continue;
+            const int64_t at = row * lds[k];
+            const int off = offset(at), n = whole(off);
+            if (n) bulk_load(slot_of(slot, k), src[k] + (at - off), (uint32_t)(n * sizeof(T)), &full[slot]);
+        }
+    };
+    const int64_t row0 = g.rows * blockIdx.x / gridDim.x, row1 = g.rows * (blockIdx.x + 1) / gridDim.x;
+    if (t == 0)
+        for (int i = 0; i < stages; i++)
+            if (row0 + i < row1) issue(row0 + i, i);
+    constexpr int NP = E / 2;
+    float2 aq[NP], ar[NP], aw[NP], ab[NP];
+#pragma unroll
+    for (int i = 0; i < NP; i++) aq[i] = ar[i] = aw[i] = ab[i] = make_float2(0.f, 0.f);
+    float st[4] = {0.f, 1.f, 0.f, 1.f}, later[4] = {0.f, 1.f, 0.f, 1.f};
+#pragma unroll
+    for (int i = 0; i < 4; i++) {
+        if (row0 < row1) st[i] = p.stats[4 * row0 + i];
+        if (row0 + 1 < row1) later[i] = p.stats[4 * (row0 + 1) + i];
+    }
+    // the value i of the thread: columns are VE together, so i and i + 1 (i even) are a pair of them
+    auto column = [&](int i) { return VE > 1 ? ((i / VE) * TPR + t) * VE + i % VE : i * TPR + t; };
+    int it = 0;
+    for (int64_t row = row0; row < row1; row++, it++) {
+        const float mu1 = st[0], rs1 = st[1], mu2 = st[2], rs2 = st[3];
+#pragma unroll
+        for (int i = 0; i < 4; i++) {
+            st[i] = later[i];
+            if (row + 2 < row1) later[i] = load_early(p.stats + 4 * (row + 2) + i);
+        }
+        const int slot = it % stages;
+        bar_wait(&full[slot], (it / stages) & 1, &s_abort, status);
+        // VE values from column c on of tensor k: zeros beyond the row
+        auto read = [&](int k, int c, float *f) {
+            const int64_t at = row * lds[k];
+            const int off = offset(at);
+            const T *s = slot_of(slot, k) + off;
+            if (VE > 1) {  // whole 16 bytes: all of them copied
+                Vec<T, VE> u;
+                u.load(s + c);
+                u.get(f);
+            } else {
+                f[0] = to_f32(c < whole(off) - off ? s[c] : src[k][at + c]);
+            }
+        };
+        auto weight = [&](int k, int c, float *f) { load_ws<T, VE>(ws[k], g.wf32, c, f); };
+        float h[E], a[E];
+        float2 sx = make_float2(0.f, 0.f), sy = sx;
+        const float2 r2 = make_float2(rs2, rs2), nm2 = make_float2(-mu2, -mu2);
+#pragma unroll
+        for (int i = 0; i < E; i++) h[i] = a[i] = 0.f;
+#pragma unroll
+        for (int i = 0; i < E; i += VE) {
+            const int c = column(i);
+            if (c < d) {
+                read(1, c, h + i);
+                read(0, c, a + i);
+            }
+        }
+        auto pair = [](float *f, int j) { return make_float2(f[2 * j], f[2 * j + 1]); };
+        auto put = [](float *f, int j, float2 v) { f[2 * j] = v.x, f[2 * j + 1] = v.y; };
+        float w[E];
+#pragma unroll
+        for (int i = 0; i < E; i++) w[i] = 1.f;
+        if (ws[3])
+#pragma unroll
+            for (int i = 0; i < E; i += VE)
+                if (column(i) < d) weight(3, column(i), w + i);
+#pragma unroll
+        for (int j = 0; j < NP; j++) {
+            const float2 v = pair(a, j);
+            // values beyond the row: a = 0, and their h counts for nothing
+            const float2 hj = mul2(add2(pair(h, j), nm2), r2);
+            put(h, j, hj);
+            aw[j] = fma2(v, hj, aw[j]);
+            ab[j] = add2(v, ab[j]);
+            const float2 x = mul2(v, pair(w, j));
+            put(a, j, x);
+            sx = add2(x, sx);
+            sy = fma2(x, hj, sy);
+        }
+        float2 s = row_sum<TPR>(make_float2(sx.x + sx.y, sy.x + sy.y), red, 0);
+        const float m1 = g.rms ? 0.f : -rs2 * s.x * inv, m2 = -rs2 * s.y * inv;
+#pragma unroll
+        for (int j = 0; j < NP; j++)  // dx but for dy
+            put(a, j, fma2(pair(h, j), make_float2(m2, m2), fma2(pair(a, j), r2, make_float2(m1, m1))));
+        if (p.dy)
+#pragma unroll
+            for (int i = 0; i < E; i += VE) {
+                const int c = column(i);
+                float f[VE];
+                if (c < d) {
+                    read(3, c, f);
+#pragma unroll
+                    for (int e = 0; e < VE; e++) a[i + e] += f[e];
+                }
+            }
+        sx = sy = make_float2(0.f, 0.f);
+        // a VE's worth at a time: dx out, then the branch's gradients
+#pragma unroll
+        for (int i = 0; i < E; i += VE) {
+            const int c = column(i);
+            if (c >= d) {
+#pragma unroll
+                for (int e = 0; e < VE; e++) a[i + e] = h[i + e] = 0.f;
+                continue;
+            }
+            Vec<T, VE> out;
+            out.set(a + i);
+            out.store((T *)p.dx + row * p.lddx + c);
+            float o[VE], w1[VE], tt[VE], cc[VE], act[VE], slope[VE], u[VE];
+            read(2, c, o);
+#pragma unroll
+            for (int e = 0; e < VE; e++) o[e] = (o[e] - mu1) * rs1, w1[e] = cc[e] = act[e] = 1.f, tt[e] = 0.f;
+            if (ws[0]) weight(0, c, w1);
+            if (ws[1]) weight(1, c, tt);
+            if (ws[2]) weight(2, c, cc);
+            if (p.z) {
+                read(4, c, u);
+                slopes_all(u, g.act, act, slope);
+            }
+#pragma unroll
+            for (int e = 0; e < VE; e++) {
+                tt[e] = fmaf(o[e], w1[e], tt[e]);
+                u[e] = a[i + e] * act[e];
+                if (p.z) slope[e] *= a[i + e] * cc[e] * tt[e];
+                a[i + e] = u[e] * cc[e] * w1[e];
+                h[i + e] = o[e];
+            }
+            if (p.dz) {
+                out.set(slope);
+                out.store((T *)p.dz + row * p.lddz + c);
+            }
+#pragma unroll
+            for (int e = 0; e < VE; e++) {
+                float &q = (i + e) & 1 ? aq[(i + e) / 2].y : aq[(i + e) / 2].x, &r = (i + e) & 1 ? ar[(i + e) / 2].y : ar[(i + e) / 2].x;
+                q = fmaf(u[e], o[e], q);
+                r += u[e];
+            }
+        }
+#pragma unroll
+        for (int j = 0; j < NP; j++) sx = add2(pair(a, j), sx), sy = fma2(pair(a, j), pair(h, j), sy);
+        s = row_sum<TPR>(make_float2(sx.x + sx.y, sy.x + sy.y), red, 1);
+        if (TPR == 32) __syncwarp();
+        if (t == 0 && row + stages < row1) issue(row + stages, slot);
+        const float k1 = g.after && !g.rms ? -rs1 * s.x * inv : 0.f, k2 = g.after ? -rs1 * s.y * inv : 0.f;
+#pragma unroll
+        for (int j = 0; j < NP; j++)
+            put(a, j, fma2(pair(h, j), make_float2(k2, k2), fma2(pair(a, j), make_float2(rs1, rs1), make_float2(k1, k1))));
+#pragma unroll
+        for (int i = 0; i < E; i += VE) {
+            const int c = column(i);
+            if (c < d) {
+                Vec<T, VE> out;
+                out.set(a + i);
+                out.store((T *)p.dout + row * p.lddo + c);
+            }
+        }
+    }
+    if (t == 0 && s_abort) bar_drain(full, stages, it);
+    if (!parts) return;
+    float *q = parts + (int64_t)blockIdx.x * 4 * d;
+#pragma unroll
+    for (int i = 0; i < E; i++) {
+        const int c = column(i);
+        if (c < d) {
+            q[c] = i & 1 ? aq[i / 2].y : aq[i / 2].x;
+            q[d + c] = i & 1 ? ar[i / 2].y : ar[i / 2].x;
+            q[2 * d + c] = i & 1 ? aw[i / 2].y : aw[i / 2].x;
+            q[3 * d + c] = i & 1 ? ab[i / 2].y : ab[i / 2].x;
+        }
+    }
+}
+
+// Rows for which no ring has room, and tensors that do not start on 16 bytes: one block a row in
+// passes over it, and the columns' sums with a thread a column over a share of the rows, from the rows' means
+// of the first reduction.
+template <typename T>
+struct ResGrad {
+    const ResBack &p;
+    const ResGeom &g;
+    int64_t row;
+    float mu1, rs1, mu2, rs2, m1, m2;  // m1, m2: the means, times -rs2
+    __device__ __forceinline__ ResGrad(const ResBack &p_, const ResGeom &g_, int64_t r) : p(p_), g(g_), row(r), m1(0.f), m2(0.f) {
+        const float *s = p.stats + 4 * r;
+        mu1 = s[0], rs1 = s[1], mu2 = s[2], rs2 = s[3];
+    }
+    __device__ __forceinline__ float dh(int64_t c) const { return to_f32(((const T *)p.dh)[row * p.lddh + c]); }
+    __device__ __forceinline__ float h2(int64_t c) const { return (to_f32(((const T *)p.y)[row * p.ldy + c]) - mu2) * rs2; }
+    __device__ __forceinline__ float a2(int64_t c) const { return dh(c) * (g.w2 ? load_w<T>(g.w2, g.wf32, c) : 1.f); }
+    __device__ __forceinline__ float dx(int64_t c) const {
+        const float v = fmaf(h2(c), m2, fmaf(a2(c), rs2, m1));
+        return p.dy ? v + to_f32(((const T *)p.dy)[row * p.lddy + c]) : v;
+    }
+    __device__ __forceinline__ float h1(int64_t c) const { return (to_f32(((const T *)p.o)[row * p.ldo + c]) - mu1) * rs1; }
+    __device__ __forceinline__ float w1(int64_t c) const { return g.w1 ? load_w<T>(g.w1, g.wf32, c) : 1.f; }
+    __device__ __forceinline__ float scale(int64_t c) const { return g.c ? load_w<T>(g.c, g.wf32, c) : 1.f; }
+    __device__ __forceinline__ float2 gate(int64_t c) const {
+        float z[1] = {p.z ? to_f32(((const T *)p.z)[row * p.ldz + c]) : 0.f}, a[1] = {1.f}, s[1] = {0.f};
+        if (p.z) slopes_all(z, g.act, a, s);
+        return make_float2(a[0], s[0]);
+    }
+};
+template <typename T>
+__global__ void __launch_bounds__(kLong)
+k_resnorm_bwd_long(const ResBack p, const ResGeom g, float2 *__restrict__ means) {
+    __shared__ float2 red[2 * (kLong / 32)];
+    ResGrad<T> r(p, g, blockIdx.x);
+    float2 s = make_float2(0.f, 0.f);
+    for (int c = threadIdx.x; c < g.d; c += kLong) {
+        const float a = r.a2(c);
+        s.x += a;
+        s.y = fmaf(a, r.h2(c), s.y);
+    }
+    s = row_sum<kLong>(s, red, 0);
+    const float inv = 1.f / (float)g.d;
+    r.m1 = g.rms ? 0.f : -r.rs2 * s.x * inv, r.m2 = -r.rs2 * s.y * inv;
+    if (threadIdx.x == 0 && means) means[r.row] = make_float2(r.m1, r.m2);
+    float k1 = 0.f, k2 = 0.f;
+    if (g.after) {
+        s = make_float2(0.f, 0.f);
+        for (int c = threadIdx.x; c < g.d; c += kLong) {
+            const float a = r.dx(c) * r.gate(c).x * r.scale(c) * r.w1(c);
+            s.x += a;
+            s.y = fmaf(a, r.h1(c), s.y);
+        }
+        s = row_sum<kLong>(s, red, 1);
+        k1 = g.rms ? 0.f : -r.rs1 * s.x * inv, k2 = -r.rs1 * s.y * inv;
+    }
+    for (int c = threadIdx.x; c < g.d; c += kLong) {
+        const float dx = r.dx(c), h1 = r.h1(c), w1 = r.w1(c), b = dx * r.scale(c);
+        const float2 a = r.gate(c);
+        ((T *)p.dx)[r.row * p.lddx + c] = from_f32<T>(dx);
+        if (p.dz) {
+            const float t = fmaf(h1, w1, g.b1 ? load_w<T>(g.b1, g.wf32, c) : 0.f);
+            ((T *)p.dz)[r.row * p.lddz + c] = from_f32<T>(b * t * a.y);
+        }
+        ((T *)p.dout)[r.row * p.lddo + c] = from_f32<T>(fmaf(h1, k2, fmaf(b * a.x * w1, r.rs1, k1)));
+    }
+}
+template <typename T>
+__global__ void __launch_bounds__(256)
+k_resnorm_bwd_cols(const ResBack p, const ResGeom g, const float2 *__restrict__ means, float *__restrict__ parts) {
+    const int64_t c = (int64_t)blockIdx.x * 256 + threadIdx.x;
+    if (c >= g.d) return;
+    float q = 0.f, r = 0.f, w = 0.f, b = 0.f;
+    for (int64_t row = blockIdx.y; row < g.rows; row += gridDim.y) {
+        ResGrad<T> v(p, g, row);
+        v.m1 = means[row].x, v.m2 = means[row].y;
+        const float u = v.dx(c) * v.gate(c).x, dh = v.dh(c);
+        q = fmaf(u, v.h1(c), q);
+        r += u;
+        w = fmaf(dh, v.h2(c), w);
+        b += dh;
+    }
+    float *to = parts + (int64_t)blockIdx.y * 4 * g.d + c;
+    to[0] = q, to[g.d] = r, to[2 * (int64_t)g.d] = w, to[3 * (int64_t)g.d] = b;
+}
+
+// The weights' gradients from the partial sums, which are added in a fixed order: 32 columns a
+// block, 32 threads a column.
+struct ResSums {
+    void *dw1, *db1, *dc, *dw2, *db2;  // NULL: not formed
+};
+template <typename T>
+__global__ void __launch_bounds__(1024)
+k_resnorm_bwd_sum(const float *__restrict__ parts, int64_t nparts, const ResGeom g, const ResSums to) {
+    __shared__ float tile[4][32][33];
+    after_previous();
+    const int tx = threadIdx.x & 31, ty = threadIdx.x >> 5;
+    const int64_t d = g.d, c = (int64_t)blockIdx.x * 32 + tx;
+    float s[4] = {};
+    if (c < d) {
+#pragma unroll 4
+        for (int64_t p = ty; p < nparts; p += 32)
+#pragma unroll
+            for (int k = 0; k < 4; k++) s[k] += parts[(p * 4 + k) * d + c];
+    }
+#pragma unroll
+    for (int k = 0; k < 4; k++) tile[k][ty][tx] = s[k];
+    __syncthreads();
+#pragma unroll
+    for (int k = 0; k < 4; k++) s[k] = warp_sum(tile[k][tx][ty]);
+    const int64_t o = (int64_t)blockIdx.x * 32 + ty;
+    if (tx != 0 || o >= d) return;
+    auto store = [&](void *p, float v) {
+        if (!p) return;
+        if (g.wf32)
+            reinterpret_cast<float *>(p)[o] = v;
+        else
+            reinterpret_cast<T *>(p)[o] = from_f32<T>(v);
+    };
+    const float cc = g.c ? load_w<T>(g.c, g.wf32, o) : 1.f;
+    store(to.dw1, cc * s[0]);
+    store(to.db1, cc * s[1]);
+    if (to.dc) {
+        const float v = (g.w1 ? load_w<T>(g.w1, g.wf32, o) : 1.f) * s[0];
+        store(to.dc, g.b1 ? fmaf(load_w<T>(g.b1, g.wf32, o), s[1], v) : v);
+    }
+    store(to.dw2, s[2]);
+    store(to.db2, s[3]);
+}
+
+// ---------------------------------------------------------------- host
+
+constexpr int64_t kMaxRow = 16384;  // of the forward pass in registers
+constexpr int64_t kParts = 64;      // shares of the rows, where a thread takes a column
+
+ResGeom geom_of(const zsolve_resnorm_args *a) {
+    return ResGeom{a->w1, a->b1, a->c, a->w2, a->b2, a->wtype == ZSOLVE_F32, a->rows, (int)a->d, (float)a->eps, a->act, a->after != 0,
+                   a->kind == ZSOLVE_NORM_RMS};
+}
+bool weights_aligned(const zsolve_resnorm_args *a) {
+    return aligned16(a->w1) && aligned16(a->b1) && aligned16(a->c) && aligned16(a->w2) && aligned16(a->b2);
+}
+
+template <typename T>
+int fwd(zsolve_seq *s, const zsolve_resnorm_args *a, const void *x, int64_t ldx, void *y, int64_t ldy, void *h, int64_t ldh, float *stats) {
+    constexpr int V = 16 / (int)sizeof(T);
+    const ResGeom g = geom_of(a);
+    const int64_t d = a->d;
+    const bool vec = d % V == 0 && ldx % V == 0 && a->ldo % V == 0 && (!a->z || a->ldz % V == 0) && ldy % V == 0 && ldh % V == 0 &&
+                     aligned16(x) && aligned16(a->o) && aligned16(a->z) && aligned16(y) && aligned16(h) &&
+                     (a->wtype == ZSOLVE_F32 || weights_aligned(a));
+    s->launches++;
+#define RES_ARGS (const T *)x, ldx, (const T *)a->o, a->ldo, (const T *)a->z, a->ldz, g, (T *)y, ldy, (T *)h, ldh, stats
+#define RES_GO(VE, TPR, E) \
+    k_resnorm<T, VE, TPR, (E) / VE><<<(unsigned)((TPR) == 32 ? (a->rows + 3) / 4 : a->rows), (TPR) < 128 ? 128 : (TPR), 0, s->st>>>(RES_ARGS)
+#define RES_SIZES(VE)                         \
+    if (d <= 256) RES_GO(VE, 32, 8);          \
+    else if (d <= 1024) RES_GO(VE, 128, 8);   \
+    else if (d <= 2048) RES_GO(VE, 256, 8);   \
+    else if (d <= 4096) RES_GO(VE, 512, 8);   \
+    else if (d <= 8192) RES_GO(VE, 1024, 8);  \
+    else RES_GO(VE, 1024, 16)
+    if (d > kMaxRow) {
+        k_resnorm_long<T><<<(unsigned)a->rows, kLong, 0, s->st>>>(RES_ARGS);
+    } else if (vec) {
+        RES_SIZES(V);
+    } else {
+        RES_SIZES(1);
+    }
+#undef RES_SIZES
+#undef RES_GO
+#undef RES_ARGS
+    SEQ_CU(cudaGetLastError());
+    return ZSOLVE_OK;
+}
+
+// The backward kernel's blocks and stages, or none where no ring has room.
+struct RingPlan {
+    int tpr = 0, stages = 0;
+    int64_t blocks = 0;
+    size_t smem = 0;
+};
+constexpr size_t kRingMost = 225 * 1024;  // beside the static shared memory
+template <typename T>
+RingPlan ring_plan(const zsolve_resnorm_args *a, const ResBack &p, int num_sms) {
+    RingPlan r;
+    const int64_t d = a->d;
+    if (d > 8192 || !aligned16(p.dh) || !aligned16(p.dy) || !aligned16(p.y) || !aligned16(p.o) || !aligned16(p.z)) return r;
+    const int e = d > 4096 ? 16 : 8;
+    r.tpr = 32;
+    while (r.tpr * e < d) r.tpr *= 2;
+    const size_t row = (size_t)(3 + (p.dy != nullptr) + (p.z != nullptr)) * ring_row<T>((int)d) * sizeof(T);
+    const int n = (a->w1 != nullptr) + (a->b1 != nullptr) + (a->c != nullptr) + (a->w2 != nullptr);
+    const size_t weights = (size_t)n * ((d * (a->wtype == ZSOLVE_F32 ? 4 : sizeof(T)) + 15) / 16 * 16);
+    if (2 * row + weights > kRingMost) return RingPlan{};
+    // as many blocks as the registers allow, with four rows each or as many as there is room for
+    const int64_t per_sm = std::max<int64_t>(1, std::min<int64_t>(ring_blocks(r.tpr), (int64_t)(kRingMost / (2 * row + weights + 1536))));
+    r.stages = (int)std::max<int64_t>(2, std::min<int64_t>(4, ((int64_t)(kRingMost / per_sm) - (int64_t)weights - 1536) / (int64_t)row));
+    r.smem = r.stages * row + weights;
+    r.blocks = std::min(a->rows, per_sm * num_sms);
+    return r;
+}
+
+template <typename T, int VE, int TPR, int E>
+cudaError_t launch_ring(const ResBack &p, const ResGeom &g, const RingPlan &r, float *parts, unsigned *status, cudaStream_t st) {
+    static OncePerDevice limit;
+    const cudaError_t attr = smem_limit(limit, k_resnorm_bwd<T, VE, TPR, E>, (int)kRingMost);
+    if (attr != cudaSuccess) return attr;
+    k_resnorm_bwd<T, VE, TPR, E><<<(unsigned)r.blocks, TPR, r.smem, st>>>(p, g, r.stages, parts, status);
+    return cudaGetLastError();
+}
+
+template <typename T>
+int bwd(zsolve_seq *s, const zsolve_resnorm_args *a, const ResBack &p, const ResSums &to) {
+    constexpr int V = 16 / (int)sizeof(T);
+    const ResGeom g = geom_of(a);
+    const int64_t d = a->d;
+    const bool sums = to.dw1 || to.db1 || to.dc || to.dw2 || to.db2;
+    const RingPlan r = a->rows > 0 ? ring_plan<T>(a, p, s->num_sms) : RingPlan{};
+    const int64_t nparts = !sums ? 0 : r.blocks ? r.blocks : std::min(a->rows, kParts);
+    float *parts = nullptr;
+    float2 *means = nullptr;
+    if (nparts) {
+        auto carve = [&](void *base) {
+            Carve c(base);
+            parts = c.take<float>((size_t)nparts * 4 * d);
+            means = r.blocks ? nullptr : c.take<float2>((size_t)a->rows);
+            return c.at;
+        };
+        int st = ZSOLVE_OK;
+        void *ws = seq_workspace(s, carve(nullptr), &st);
+        if (!ws) return st;
+        carve(ws);
+    }
+    if (a->rows > 0) {
+        s->launches++;
+        if (r.blocks) {
+            const bool vec = d % V == 0 && p.lddh % V == 0 && (!p.dy || p.lddy % V == 0) && p.ldy % V == 0 && p.ldo % V == 0 &&
+                             (!p.z || p.ldz % V == 0) && p.lddx % V == 0 && p.lddo % V == 0 && (!p.dz || p.lddz % V == 0) &&
+                             aligned16(p.dx) && aligned16(p.dout) && aligned16(p.dz);
+#define RES_RING(TPR, E) (vec ? launch_ring<T, V, TPR, E>(p, g, r, parts, s->d_status, s->st) : launch_ring<T, 1, TPR, E>(p, g, r, parts, s->d_status, s->st))
+            SEQ_CU(d > 4096       ? RES_RING(512, 16)
+                   : r.tpr == 32  ? RES_RING(32, 8)
+                   : r.tpr == 64  ? RES_RING(64, 8)
+                   : r.tpr == 128 ? RES_RING(128, 8)
+                   : r.tpr == 256 ? RES_RING(256, 8)
+                                  : RES_RING(512, 8));
+#undef RES_RING
+        } else {
+            k_resnorm_bwd_long<T><<<(unsigned)a->rows, kLong, 0, s->st>>>(p, g, means);
+            SEQ_CU(cudaGetLastError());
+            if (sums) {
+                s->launches++;
+                k_resnorm_bwd_cols<T><<<dim3((unsigned)((d + 255) / 256), (unsigned)nparts), 256, 0, s->st>>>(p, g, means, parts);
+                SEQ_CU(cudaGetLastError());
+            }
+        }
+    }
+    if (!sums) return ZSOLVE_OK;
+    s->launches++;
+    SEQ_CU(launch(nparts > 0, k_resnorm_bwd_sum<T>, (unsigned)((d + 31) / 32), 1024, 0, s->st, parts, nparts, g, to));
+    return ZSOLVE_OK;
+}
+
+}  // namespace
+
+int zs_resnorm(zsolve_seq *s, const zsolve_resnorm_args *a, const void *x, int64_t ldx, void *y, int64_t ldy, void *h, int64_t ldh,
+               float *stats) {
+    if (a->type == ZSOLVE_F32) return fwd<float>(s, a, x, ldx, y, ldy, h, ldh, stats);
+    return a->type == ZSOLVE_BF16 ? fwd<bf16>(s, a, x, ldx, y, ldy, h, ldh, stats) : fwd<f16>(s, a, x, ldx, y, ldy, h, ldh, stats);
+}
+
+int zs_resnorm_bwd(zsolve_seq *s, const zsolve_resnorm_args *a, const void *dh, int64_t lddh, const void *dy, int64_t lddy, const void *y,
+                   int64_t ldy, const float *stats, void *dx, int64_t lddx, void *dout, int64_t lddo, void *dz, int64_t lddz, void *dw1,
+                   void *db1, void *dc, void *dw2, void *db2) {
+    const ResBack p{dh, dy, y, a->o, a->z, lddh, lddy, ldy, a->ldo, a->ldz, stats, dx, dout, a->z ? dz : nullptr, lddx, lddo, lddz};
+    const ResSums to{dw1, db1, dc, dw2, db2};
+    if (a->type == ZSOLVE_F32) return bwd<float>(s, a, p, to);
+    return a->type == ZSOLVE_BF16 ? bwd<bf16>(s, a, p, to) : bwd<f16>(s, a, p, to);
+}

@@ -100,6 +100,20 @@ int check_linear(zsolve_seq *s, int type, int act, int64_t m, int64_t n, int64_t
     return ZSOLVE_OK;
 }
 
+int check_resnorm(zsolve_seq *s, const zsolve_resnorm_args *a) {
+    if (!a) return seq_fail(s, ZSOLVE_EINVAL, "NULL arguments");
+    if (!zs::type_ok(a->type) || (a->wtype != a->type && a->wtype != ZSOLVE_F32))
+        return seq_fail(s, ZSOLVE_EINVAL, "type %d, wtype %d: wtype is the type of the tensors or ZSOLVE_F32", a->type, a->wtype);
+    if (a->kind != ZSOLVE_NORM_LAYER && a->kind != ZSOLVE_NORM_RMS) return seq_fail(s, ZSOLVE_EINVAL, "kind = %d", a->kind);
+    if (a->act < ZSOLVE_ACT_NONE || a->act > ZSOLVE_ACT_GELU_TANH) return seq_fail(s, ZSOLVE_EINVAL, "act = %d", a->act);
+    if (a->rows < 0 || a->rows > 0x7fffffff || a->d < 1 || a->d > 1 << 24)
+        return seq_fail(s, ZSOLVE_EINVAL, "rows = %lld, d = %lld", (long long)a->rows, (long long)a->d);
+    if (!(a->eps >= 0.0) || !std::isfinite(a->eps)) return seq_fail(s, ZSOLVE_EINVAL, "eps = %g", a->eps);
+    if (a->rows > 0 && (!a->o || a->ldo < a->d || (a->z && a->ldz < a->d)))
+        return seq_fail(s, ZSOLVE_EINVAL, "NULL o, or a row stride below d = %lld", (long long)a->d);
+    return ZSOLVE_OK;
+}
+
 // The longest a sequence of the call can be.
 int64_t longest(const zsolve_delta_args *a) {
     return a->nseq == 0 ? 0 : a->offsets ? a->tokens : a->tokens / a->nseq;
@@ -324,6 +338,33 @@ int zsolve_layernorm_bwd(zsolve_seq *s, int type, int wtype, int64_t rows, int64
     SEQ_CU(zs_launch_layernorm_bwd(type, wtype == ZSOLVE_F32, rows, d, dy, lddy, x, ldx, mean, rstd, w, dx, lddx, dw,
                                    db, parts, s->num_sms, s->d_status, s->st, &s->launches));
     return ZSOLVE_OK;
+}
+
+int zsolve_resnorm(zsolve_seq *s, const zsolve_resnorm_args *a, const void *x, int64_t ldx, void *y, int64_t ldy, void *h, int64_t ldh,
+                   float *stats) {
+    if (!s) return ZSOLVE_EINVAL;
+    int st = check_resnorm(s, a);
+    if (st != ZSOLVE_OK || a->rows == 0) return st;
+    if (!x || !y || !h) return seq_fail(s, ZSOLVE_EINVAL, "NULL x, y or h");
+    if (ldx < a->d || ldy < a->d || ldh < a->d) return seq_fail(s, ZSOLVE_EINVAL, "a row stride is below d = %lld", (long long)a->d);
+    st = check_device(s);
+    if (st != ZSOLVE_OK) return st;
+    return zs_resnorm(s, a, x, ldx, y, ldy, h, ldh, stats);
+}
+
+int zsolve_resnorm_bwd(zsolve_seq *s, const zsolve_resnorm_args *a, const void *dh, int64_t lddh, const void *dy, int64_t lddy,
+                       const void *y, int64_t ldy, const float *stats, void *dx, int64_t lddx, void *dout, int64_t lddo, void *dz,
+                       int64_t lddz, void *dw1, void *db1, void *dc, void *dw2, void *db2) {
+    if (!s) return ZSOLVE_EINVAL;
+    int st = check_resnorm(s, a);
+    if (st != ZSOLVE_OK) return st;
+    if (a->rows > 0 && (!dh || !y || !stats || !dx || !dout)) return seq_fail(s, ZSOLVE_EINVAL, "NULL dh, y, stats, dx or do");
+    if (dz && !a->z) return seq_fail(s, ZSOLVE_EINVAL, "dz without z");
+    if (a->rows > 0 && (lddh < a->d || ldy < a->d || lddx < a->d || lddo < a->d || (dy && lddy < a->d) || (dz && lddz < a->d)))
+        return seq_fail(s, ZSOLVE_EINVAL, "a row stride is below d = %lld", (long long)a->d);
+    st = check_device(s);
+    if (st != ZSOLVE_OK) return st;
+    return zs_resnorm_bwd(s, a, dh, lddh, dy, lddy, y, ldy, stats, dx, lddx, dout, lddo, dz, lddz, dw1, db1, dc, dw2, db2);
 }
 
 int zsolve_seq_check(zsolve_seq *s) {

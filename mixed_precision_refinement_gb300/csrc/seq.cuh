@@ -298,6 +298,13 @@ cudaError_t zs_launch_layernorm_bwd(int type, int wf32, int64_t rows, int64_t d,
                                     void *dx, int64_t lddx, void *dw, void *db, float *parts, int num_sms,
                                     unsigned *status, cudaStream_t st, int64_t *launches);
 
+// resnorm.cu: the whole call (arguments checked), a ZSOLVE_* status.
+int zs_resnorm(zsolve_seq *s, const zsolve_resnorm_args *a, const void *x, int64_t ldx, void *y, int64_t ldy, void *h, int64_t ldh,
+               float *stats);
+int zs_resnorm_bwd(zsolve_seq *s, const zsolve_resnorm_args *a, const void *dh, int64_t lddh, const void *dy, int64_t lddy, const void *y,
+                   int64_t ldy, const float *stats, void *dx, int64_t lddx, void *dout, int64_t lddo, void *dz, int64_t lddz, void *dw1,
+                   void *db1, void *dc, void *dw2, void *db2);
+
 // linear.cu: the whole call (arguments checked), a ZSOLVE_* status.
 int zs_linear(zsolve_seq *s, int type, int64_t m, int64_t n, int64_t k, const void *x, int64_t ldx, const void *w,
               int64_t ldw, const void *b, int act, const void *r, int64_t ldr, void *y, int64_t ldy, void *z,

@@ -15,6 +15,7 @@ ZSOLVE_BF16 = 1
 ZSOLVE_F16 = 2
 
 ZSOLVE_ACTS = {"none": 0, "relu": 1, "silu": 2, "gelu": 3, "gelu_tanh": 4}
+ZSOLVE_NORMS = {"layer": 0, "rms": 1}
 
 
 torch = None  # imported with the first handle: the rest of the package loads without it
@@ -262,6 +263,63 @@ def zsolve_glu_bwd(seq, dy, x, wg, wu, act, zg, zu, dx=None, dwg=None, dwu=None,
                                         _vector(dbu, "dbu", n, x.dtype)))
 
 
+class zsolve_resnorm_args(ctypes.Structure):
+    _fields_ = [("type", ctypes.c_int), ("wtype", ctypes.c_int), ("kind", ctypes.c_int), ("after", ctypes.c_int),
+                ("act", ctypes.c_int), ("rows", ctypes.c_int64), ("d", ctypes.c_int64), ("o", ctypes.c_void_p),
+                ("z", ctypes.c_void_p), ("ldo", ctypes.c_int64), ("ldz", ctypes.c_int64), ("w1", ctypes.c_void_p),
+                ("b1", ctypes.c_void_p), ("c", ctypes.c_void_p), ("w2", ctypes.c_void_p), ("b2", ctypes.c_void_p),
+                ("eps", ctypes.c_double)]
+
+
+def _resnorm_args(o, w1, b1, z, act, c, w2, b2, kind, after, eps, weights=()):
+    """The arguments, rows, d and the weights' torch type; `weights`: the gradients, where a weight itself is not given."""
+    op, m, d, ldo = _rows(o, "o")
+    zp, ldz = _optional_rows(z, "z", o.dtype, (m, d))
+    if kind not in ZSOLVE_NORMS:
+        raise ValueError(f"kind: expected one of {', '.join(ZSOLVE_NORMS)}, got {kind!r}")
+    wt = o.dtype
+    for t in (w1, b1, c, w2, b2, *weights):
+        if t is not None:
+            wt = t.dtype
+            break
+    if wt not in (o.dtype, torch.float32):
+        raise TypeError(f"w1, b1, c, w2 and b2: expected {o.dtype} or torch.float32, got {wt}")
+    a = zsolve_resnorm_args(_type(o, "o"), _TYPES[wt], ZSOLVE_NORMS[kind], bool(after), _act(act), m, d, op, zp, ldo, ldz,
+                            _vector(w1, "w1", d, wt), _vector(b1, "b1", d, wt), _vector(c, "c", d, wt), _vector(w2, "w2", d, wt),
+                            _vector(b2, "b2", d, wt), eps)
+    return a, m, d, wt
+
+
+def _stats(stats, o, m):
+    lead = (m,) if o.dim() == 2 else o.shape[:-1]
+    return _vector(stats, "stats", 4 * m, torch.float32, (*lead, 4), 1)
+
+
+def zsolve_resnorm(seq, x, o, w1, b1, z, act, c, w2, b2, kind, after, eps, y, h, stats=None) -> None:
+    """y <- x + c act(z) (norm(o) w1 + b1), h <- norm(y) w2 + b2; x, o, z, y and h (..., d), the weights (d,) or None, z or
+    None; kind "layer" or "rms"; after=False: without the first norm; stats: float32 (..., 4) or None."""
+    a, m, d, _ = _resnorm_args(o, w1, b1, z, act, c, w2, b2, kind, after, eps)
+    xp, _, _, ldx = _rows(x, "x", o.dtype, (m, d))
+    yp, _, _, ldy = _rows(y, "y", o.dtype, (m, d))
+    hp, _, _, ldh = _rows(h, "h", o.dtype, (m, d))
+    _check_seq(seq, _lib.zsolve_resnorm(seq, ctypes.byref(a), xp, ldx, yp, ldy, hp, ldh, _stats(stats, o, m)))
+
+
+def zsolve_resnorm_bwd(seq, dh, dy, y, o, stats, w1, b1, z, act, c, w2, b2, kind, after, dx, do, dz=None, dw1=None, db1=None, dc=None,
+                       dw2=None, db2=None) -> None:
+    """dx, do, dz (the shape of o) and dw1 .. db2 (the type of the weights; None: not formed) from dh and dy (None: zero)."""
+    a, m, d, wt = _resnorm_args(o, w1, b1, z, act, c, w2, b2, kind, after, 0.0, (dw1, db1, dc, dw2, db2))
+    dhp, _, _, lddh = _rows(dh, "dh", o.dtype, (m, d))
+    dyp, lddy = _optional_rows(dy, "dy", o.dtype, (m, d))
+    yp, _, _, ldy = _rows(y, "y", o.dtype, (m, d))
+    dxp, _, _, lddx = _rows(dx, "dx", o.dtype, (m, d))
+    dop, _, _, lddo = _rows(do, "do", o.dtype, (m, d))
+    dzp, lddz = _optional_rows(dz, "dz", o.dtype, (m, d))
+    _check_seq(seq, _lib.zsolve_resnorm_bwd(seq, ctypes.byref(a), dhp, lddh, dyp, lddy, yp, ldy, _stats(stats, o, m), dxp, lddx, dop,
+                                            lddo, dzp, lddz, _vector(dw1, "dw1", d, wt), _vector(db1, "db1", d, wt),
+                                            _vector(dc, "dc", d, wt), _vector(dw2, "dw2", d, wt), _vector(db2, "db2", d, wt)))
+
+
 class zsolve_delta_args(ctypes.Structure):
     _fields_ = [("type", ctypes.c_int), ("hk", ctypes.c_int), ("hv", ctypes.c_int), ("dk", ctypes.c_int),
                 ("dv", ctypes.c_int), ("nseq", ctypes.c_int), ("tokens", ctypes.c_int64),
@@ -418,6 +476,33 @@ class Seq:
         db = torch.empty(x.shape[-1], dtype=dt, device=x.device)
         zsolve_layernorm_bwd(self.seq, dy, x, mean, rstd, w, dx, dw, db)
         return dx, dw, db
+
+    def resnorm(self, x, o, w1=None, b1=None, z=None, act="silu", c=None, w2=None, b2=None, kind="layer", after=True, eps=1e-5):
+        """Returns (y, h, stats): y = x + c act(z) (norm(o) w1 + b1), the residual stream x with a block's output o, gated and
+        scaled; h = norm(y) w2 + b2 for the next block; stats is float32 (..., 4), for resnorm_bwd.
+
+        Each of z, c and the weights may be None; kind: "layer" or "rms" of both norms; after=False: o is not normed.
+        """
+        if _records(x, o, w1, b1, z, c, w2, b2):
+            return _autograd().ResNorm.apply(self, x, o, w1, b1, z, act, c, w2, b2, kind, after, eps)
+        self._on_stream()
+        y = torch.empty(x.shape, dtype=x.dtype, device=x.device)
+        h = torch.empty_like(y)
+        stats = torch.empty((*x.shape[:-1], 4), dtype=torch.float32, device=x.device)
+        zsolve_resnorm(self.seq, x, o, w1, b1, z, act, c, w2, b2, kind, after, eps, y, h, stats)
+        return y, h, stats
+
+    def resnorm_bwd(self, dh, y, o, stats, w1=None, b1=None, z=None, act="silu", c=None, w2=None, b2=None, dy=None, kind="layer",
+                    after=True):
+        """Returns (dx, do, dz, dw1, db1, dc, dw2, db2) from the gradients of h and, unless None, of y; None for what is not
+        given."""
+        self._on_stream()
+        dx = torch.empty(o.shape, dtype=o.dtype, device=o.device)
+        do = torch.empty_like(dx)
+        dz = None if z is None else torch.empty_like(dx)
+        sums = [None if t is None else torch.empty_like(t) for t in (w1, b1, c, w2, b2)]
+        zsolve_resnorm_bwd(self.seq, dh, dy, y, o, stats, w1, b1, z, act, c, w2, b2, kind, after, dx, do, dz, *sums)
+        return (dx, do, dz, *sums)
 
     def linear(self, x, w, b=None, act="none", r=None, keep=False):
         """y = act(x w^T + b) + r; with keep=True (y, z), z for linear_bwd."""

@@ -8,9 +8,9 @@ from torch.autograd.function import once_differentiable
 from . import seq as binding
 
 
-def _unused(name, *grads):
+def _unused(name, *grads, which="only the operator's first output does"):
     if any(g is not None for g in grads):
-        raise RuntimeError(f"{name} carries no gradients: only the operator's first output does")
+        raise RuntimeError(f"{name} carries no gradients: {which}")
 
 
 class LayerNorm(torch.autograd.Function):
@@ -35,6 +35,36 @@ class LayerNorm(torch.autograd.Function):
         ctx.seq._on_stream()
         binding.zsolve_layernorm_bwd(ctx.seq.seq, dy.contiguous(), x, mean, rstd, w, dx, dw, db)
         return None, dx, dw, db, None
+
+
+class ResNorm(torch.autograd.Function):
+    @staticmethod
+    def forward(ctx, seq, x, o, w1, b1, z, act, c, w2, b2, kind, after, eps):
+        y, h, stats = seq.resnorm(x, o, w1, b1, z, act, c, w2, b2, kind, after, eps)
+        ctx.seq, ctx.options = seq, (act, kind, after)
+        ctx.set_materialize_grads(False)
+        ctx.save_for_backward(y, o, stats, w1, b1, z, c, w2, b2)
+        return y, h, stats
+
+    @staticmethod
+    @once_differentiable
+    def backward(ctx, dy, dh, dstats):
+        _unused("resnorm: stats", dstats, which="its first two outputs do")
+        if dy is None and dh is None:
+            return (None,) * 13
+        y, o, stats, w1, b1, z, c, w2, b2 = ctx.saved_tensors
+        act, kind, after = ctx.options
+        dh = torch.zeros(o.shape, dtype=o.dtype, device=o.device) if dh is None else dh.contiguous()
+        dy = None if dy is None else dy.contiguous()
+        needs = ctx.needs_input_grad
+        dx, do = (torch.empty(o.shape, dtype=o.dtype, device=o.device) for _ in range(2))
+        dz = torch.empty_like(dx) if needs[5] else None
+        dw1, db1, dc, dw2, db2 = (torch.empty(t.shape, dtype=t.dtype, device=t.device) if need else None
+                                  for t, need in ((w1, needs[3]), (b1, needs[4]), (c, needs[7]), (w2, needs[8]), (b2, needs[9])))
+        ctx.seq._on_stream()
+        binding.zsolve_resnorm_bwd(ctx.seq.seq, dh, dy, y, o, stats, w1, b1, z, act, c, w2, b2, kind, after, dx, do, dz, dw1, db1, dc,
+                                   dw2, db2)
+        return None, dx, do, dw1, db1, dz, None, dc, dw2, db2, None, None, None
 
 
 class Linear(torch.autograd.Function):

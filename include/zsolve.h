@@ -634,6 +634,45 @@ int zsolve_delta_step(zsolve_seq *seq, const zsolve_delta_args *args, void *o, i
 int zsolve_delta_bwd(zsolve_seq *seq, const zsolve_delta_args *args, const void *dout, int64_t lddo, const float *ds,
                      void *dq, void *dk, void *dv, float *dg, float *dbeta, float *ds0);
 
+/* Linear attention with a decay for each head.  Each value head of a sequence has a state S (dk x dv,
+ * float32), and every token t, with a_t = exp(g_t),
+ *   S <- a_t S + k_t v_t^T,  o_t = scale S^T q_t.
+ * Value head h uses key head h / (hv / hk).  g_t = -infinity empties the state before the token. */
+#define ZSOLVE_DECAY_MAX_DK 128
+
+typedef struct {
+    int type;               /* of q, k, v and o: ZSOLVE_F32, ZSOLVE_BF16 or ZSOLVE_F16 */
+    int hk, hv;             /* key and value heads; hv is a multiple of hk, at most 65535 */
+    int dk, dv;             /* their sizes; dk <= ZSOLVE_DECAY_MAX_DK */
+    int nseq;               /* sequences */
+    int64_t tokens;         /* of all sequences together, one after the other */
+    const int64_t *offsets; /* as for zsolve_delta_args */
+    const void *q, *k, *v;  /* tokens x heads x d; the heads of a token are packed */
+    int64_t ldq, ldk, ldv;  /* distance of two tokens, elements */
+    const float *g;         /* log decays: tokens x hv, packed (ldg = hv), or hv, one a head (ldg = 0) */
+    int64_t ldg;
+    const float *s0;        /* nseq x hv x dk x dv: the states to start from (NULL: zero) */
+    double scale;
+} zsolve_decay_args;
+
+/* o (tokens x hv x dv, token stride ldo) and the states after the last tokens, s (as s0, and may be s0; NULL: not
+ * written).  In spans of tokens, whose products run on the tensor cores at float32 accuracy and do not wait for
+ * each other, but for one elementwise recurrence over the spans' states; sequences of a few tokens
+ * at most go token by token (zsolve_decay_step). */
+int zsolve_decay(zsolve_seq *seq, const zsolve_decay_args *args, void *o, int64_t ldo, float *s);
+
+/* The same token by token in float32, one kernel and no workspace: for decoding, one or a few tokens a
+ * sequence. */
+int zsolve_decay_step(zsolve_seq *seq, const zsolve_decay_args *args, void *o, int64_t ldo, float *s);
+
+/* The gradients of zsolve_decay from those of its outputs, dout (tokens x hv x dv of args->type, token stride
+ * lddo) and ds (as s; NULL: zero).  dq, dk: tokens x hk x dk and dv: tokens x hv x dv of args->type, dg float32,
+ * as g (one decay a head: its sum over all tokens), ds0: as s0 (NULL: not formed); all packed, key heads summed
+ * over the value heads that share them in a fixed order.  The states are computed once more from the inputs.  The
+ * outputs overlap no input. */
+int zsolve_decay_bwd(zsolve_seq *seq, const zsolve_decay_args *args, const void *dout, int64_t lddo, const float *ds,
+                     void *dq, void *dk, void *dv, float *dg, float *ds0);
+
 /* Static string for a status code.  No passage: error reporting of the library. */
 const char *zsolve_strerror(int status);
 

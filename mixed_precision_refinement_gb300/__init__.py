@@ -155,6 +155,9 @@ def _load():
         "zsolve_glu_bwd": (I, [P, I, I64, I64, I64] + 4 * [P, I64] + [I] + 5 * [P, I64] + [P, P]),
         "zsolve_resnorm": (I, [P, P, P, I64, P, I64, P, I64, P]),
         "zsolve_resnorm_bwd": (I, [P, P] + 3 * [P, I64] + [P] + 3 * [P, I64] + 5 * [P]),
+        "zsolve_decay": (I, [P, P, P, I64, P]),
+        "zsolve_decay_bwd": (I, [P, P, P, I64, P, P, P, P, P, P]),
+        "zsolve_decay_step": (I, [P, P, P, I64, P]),
         "zsolve_delta": (I, [P, P, P, I64, P]),
         "zsolve_delta_bwd": (I, [P, P, P, I64, P, P, P, P, P, P, P]),
         "zsolve_delta_step": (I, [P, P, P, I64, P]),
@@ -538,6 +541,7 @@ class Afs:
 
 
 from .seq import (  # noqa: E402  (the sequence-layer operators use the names above)
-    Seq, ZSOLVE_ACTS, ZSOLVE_BF16, ZSOLVE_F16, ZSOLVE_F32, ZSOLVE_NORMS, zsolve_resnorm, zsolve_resnorm_args, zsolve_resnorm_bwd, zsolve_delta, zsolve_delta_args, zsolve_delta_bwd, zsolve_delta_step,
+    Seq, ZSOLVE_ACTS, ZSOLVE_BF16, ZSOLVE_F16, ZSOLVE_F32, ZSOLVE_NORMS, zsolve_resnorm, zsolve_resnorm_args, zsolve_resnorm_bwd,
+    zsolve_decay, zsolve_decay_args, zsolve_decay_bwd, zsolve_decay_step, zsolve_delta, zsolve_delta_args, zsolve_delta_bwd, zsolve_delta_step,
     zsolve_glu, zsolve_glu_bwd, zsolve_layernorm, zsolve_layernorm_bwd, zsolve_linear, zsolve_linear_bwd, zsolve_seq_check, zsolve_seq_create, zsolve_seq_destroy, zsolve_seq_last_error, zsolve_seq_launches, zsolve_seq_reserve, zsolve_seq_set_stream,
     zsolve_seq_workspace_bytes)

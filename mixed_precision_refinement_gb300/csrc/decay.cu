@@ -1,0 +1,327 @@
+// Linear attention with a decay for each head: the spans' sums, the recurrence over the spans, and the
+// gradients of the decays (formulas and geometry in decay.cuh).
+#include <algorithm>
+
+#include "decay.cuh"
+
+namespace {
+
+using namespace zs;
+
+// ---------------------------------------------------------------- sums
+
+// A block of warps holds DX x NB values of one span's sum in registers, 32 x 64 a warp, and goes through the
+// span's tokens 64 at a time; their tiles come in two stages.  The weights enter x's side, whose
+// product with y keeps float32 accuracy (two tf32 parts, added to nearest).
+template <typename T, int DX, int NB>
+struct SumSmem {
+    static constexpr int LDX = tile_ld<T>(DX), LDY = tile_ld<T>(NB);
+    T x[2][kChunk * LDX];
+    T y[2][kChunk * LDY];
+    float2 b[kSpanMost];
+    float w[kSpanMost];
+};
+template <int DX, int NB>
+constexpr int sum_threads() { return DX * NB / 64; }
+
+template <typename T, int DX, int NB>
+__global__ void __launch_bounds__(sum_threads<DX, NB>(), DX * NB / 64 >= 256 ? 2 : 4)
+k_decay_sums(const DecayGeom geo, const DecayRows x, const DecayRows y, int query, int gates, float *__restrict__ out) {
+    using Smem = SumSmem<T, DX, NB>;
+    constexpr int LDX = Smem::LDX, LDY = Smem::LDY, NT = sum_threads<DX, NB>();
+    extern __shared__ __align__(16) uint8_t smem_raw[];
+    Smem &sm = *reinterpret_cast<Smem *>(smem_raw);
+    after_previous();
+    may_start_next();
+    const int span = blockIdx.x, hv = blockIdx.y, c0 = blockIdx.z * NB;
+    const int2 sp = geo.d.chunk[span];
+    if (sp.y == 0) return;
+    const int group = geo.d.hv / geo.d.hk, hk = hv / group;
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g = lane >> 2, t = lane & 3;
+    const T *px = (const T *)x.p + (int64_t)sp.x * x.ld + (int64_t)(x.key ? hk : hv) * x.dist;
+    const T *py = (const T *)y.p + (int64_t)sp.x * y.ld + (int64_t)(y.key ? hk : hv) * y.dist + c0;
+    const int ycols = min(NB, y.dist - c0), chunks = (sp.y + kChunk - 1) / kChunk;
+    auto fetch = [&](int i) {
+        const int n = min(kChunk, sp.y - i * kChunk);
+        load_tile<T, DX, NT>(sm.x[i & 1], px + (int64_t)i * kChunk * x.ld, x.ld, n, x.dist);
+        load_tile<T, NB, NT>(sm.y[i & 1], py + (int64_t)i * kChunk * y.ld, y.ld, n, ycols);
+        cp_commit();
+    };
+    fetch(0);
+    if (warp == 0) decay_sums(geo, sp, hv, sm.b);
+    __syncthreads();
+    const float2 last = sm.b[sp.y - 1];
+    for (int i = tid; i < chunks * kChunk; i += NT)
+        sm.w[i] = i >= sp.y ? 0.f : query ? geo.d.scale * decay_exp(sm.b[i], make_float2(0.f, 0.f)) : decay_exp(last, sm.b[i]);
+    if (gates && blockIdx.z == 0)
+        for (int i = tid; i < sp.y; i += NT) geo.gates[((int64_t)span * geo.d.hv + hv) * geo.span + i] = sm.b[i];
+    constexpr int WN = NB / 64;  // warps side by side
+    const int d0 = warp / WN * 32, v0 = warp % WN * 64;
+    float acc[2][8][4] = {};
+    for (int i = 0; i < chunks; i++) {
+        if (i + 1 < chunks) {
+            fetch(i + 1);
+            cp_wait<1>();
+        } else {
+            cp_wait<0>();
+        }
+        __syncthreads();
+        const T *xs = sm.x[i & 1], *ys = sm.y[i & 1];
+        const float *w = sm.w + i * kChunk;
+#pragma unroll 2
+        for (int k = 0; k < 8; k++) {
+            const float2 wk = *reinterpret_cast<const float2 *>(w + k * 8 + 2 * t);
+            float2 f[4];
+            frag4<T, LDX, true>(xs, k * 8, d0, f);
+            SplitA a[2];
+#pragma unroll
+            for (int m = 0; m < 2; m++)
+                a[m].set(f[2 * m].x * wk.x, f[2 * m].y * wk.y, f[2 * m + 1].x * wk.x, f[2 * m + 1].y * wk.y);
+#pragma unroll
+            for (int n = 0; n < 2; n++) {
+                frag4<T, LDY, true>(ys, k * 8, v0 + 32 * n, f);
+#pragma unroll
+                for (int j = 0; j < 4; j++)
+#pragma unroll
+                    for (int m = 0; m < 2; m++) mma_add<false, sizeof(T) == 2>(acc[m][4 * n + j], a[m], f[j]);
+            }
+        }
+        __syncthreads();  // the stage is free
+    }
+    float *po = out + ((int64_t)span * geo.d.hv + hv) * x.cols * y.cols;
+#pragma unroll
+    for (int m = 0; m < 2; m++)
+#pragma unroll
+        for (int j = 0; j < 8; j++)
+#pragma unroll
+            for (int e = 0; e < 4; e++) {
+                const int r = d0 + 16 * m + g + (e >> 1) * 8, c = c0 + v0 + 8 * j + 2 * t + (e & 1);
+                if (r < x.cols && c < y.cols) po[(int64_t)r * y.cols + c] = acc[m][j][e];
+            }
+}
+
+// ---------------------------------------------------------------- the recurrence over the spans
+
+constexpr int kScanThreads = 256;
+constexpr int kAhead = 4;  // spans whose sums are on their way
+
+__device__ __forceinline__ float span_decay(const DecayGeom &geo, int span, int hv) {
+    return decay_exp(geo.gates[((int64_t)span * geo.d.hv + hv) * geo.span + geo.d.chunk[span].y - 1], make_float2(0.f, 0.f));
+}
+
+// A thread VE neighbouring values of a state.
+template <int VE>
+__global__ void __launch_bounds__(kScanThreads)
+k_decay_scan(const DecayGeom geo, float *u, const float *s0, float *sn) {
+    after_previous();
+    may_start_next();
+    const int si = blockIdx.x / geo.d.hv, hv = blockIdx.x - si * geo.d.hv, size = geo.d.dk * geo.d.dv;
+    const int at = ((int)blockIdx.y * kScanThreads + (int)threadIdx.x) * VE;
+    if (at >= size) return;
+    const int first = geo.d.first[si], n = geo.d.first[si + 1] - first;
+    const int64_t step = (int64_t)geo.d.hv * size;
+    float *p = u + ((int64_t)first * geo.d.hv + hv) * size + at;
+    float s[VE] = {};
+    Vec<float, VE> v;
+    if (s0) v.load(s0 + (int64_t)blockIdx.x * size + at), v.get(s);
+    for (int i = 0; i < n; i += kAhead) {
+        Vec<float, VE> w[kAhead];
+        float a[kAhead];
+#pragma unroll
+        for (int k = 0; k < kAhead; k++)
+            if (i + k < n) w[k].load(p + (i + k) * step), a[k] = span_decay(geo, first + i + k, hv);
+#pragma unroll
+        for (int k = 0; k < kAhead; k++) {
+            if (i + k >= n) break;
+            float f[VE];
+            w[k].get(f);
+            v.set(s);
+            v.store(p + (i + k) * step);
+#pragma unroll
+            for (int e = 0; e < VE; e++) s[e] = fmaf(a[k], s[e], f[e]);
+        }
+    }
+    if (sn) v.set(s), v.store(sn + (int64_t)blockIdx.x * size + at);
+}
+
+template <int VE>
+__global__ void __launch_bounds__(kScanThreads)
+k_decay_rscan(const DecayGeom geo, float *w, const float *__restrict__ states, const float *ds, float *ds0, float *__restrict__ dots) {
+    after_previous();
+    may_start_next();
+    const int si = blockIdx.x / geo.d.hv, hv = blockIdx.x - si * geo.d.hv, size = geo.d.dk * geo.d.dv;
+    const int at = ((int)blockIdx.y * kScanThreads + (int)threadIdx.x) * VE;
+    const bool in = at < size;
+    const int first = geo.d.first[si], n = geo.d.first[si + 1] - first;
+    const int64_t step = (int64_t)geo.d.hv * size, base = ((int64_t)first * geo.d.hv + hv) * size + at;
+    float s[VE] = {};
+    Vec<float, VE> v;
+    if (ds && in) v.load(ds + (int64_t)blockIdx.x * size + at), v.get(s);
+    const int warps = kScanThreads / 32, parts = gridDim.y * warps;
+    for (int i = n - 1; i >= 0; i -= kAhead) {
+        Vec<float, VE> x[kAhead], y[kAhead];
+        float a[kAhead];
+#pragma unroll
+        for (int k = 0; k < kAhead; k++)
+            if (i - k >= 0) {
+                if (in) x[k].load(w + base + (i - k) * step), y[k].load(states + base + (i - k) * step);
+                a[k] = span_decay(geo, first + i - k, hv);
+            }
+#pragma unroll
+        for (int k = 0; k < kAhead; k++) {
+            if (i - k < 0) break;
+            float dot = 0.f;
+            if (in) {
+                float f[VE], q[VE];
+                x[k].get(f);
+                y[k].get(q);
+                v.set(s);
+                v.store(w + base + (i - k) * step);
+#pragma unroll
+                for (int e = 0; e < VE; e++) dot = fmaf(q[e], s[e], dot), s[e] = fmaf(a[k], s[e], f[e]);
+            }
+            dot = warp_sum(dot) * a[k];
+            if ((threadIdx.x & 31) == 0)
+                dots[((int64_t)(first + i - k) * geo.d.hv + hv) * parts + blockIdx.y * warps + (threadIdx.x >> 5)] = dot;
+        }
+    }
+    if (ds0 && in) v.set(s), v.store(ds0 + (int64_t)blockIdx.x * size + at);
+}
+
+// ---------------------------------------------------------------- gradients of the decays
+
+struct DecayDots {
+    const float *xq, *rq, *xk, *rk;  // tokens x hv: the state's share and the pairs, as queries and as keys
+    const float *dots;
+    int parts;
+};
+
+// A warp a span and head: within the span the sums over the tokens after and before t.
+__global__ void __launch_bounds__(128)
+k_decay_dg(const DecayGeom geo, const DecayDots in, float *__restrict__ parts, float *__restrict__ dg) {
+    after_previous();
+    may_start_next();
+    const int lane = threadIdx.x & 31, hv = (int)blockIdx.y * 4 + (threadIdx.x >> 5), span = blockIdx.x;
+    if (hv >= geo.d.hv) return;
+    const int2 sp = geo.d.chunk[span];
+    if (sp.y == 0) {
+        if (parts) {
+            if (lane == 0) parts[(int64_t)span * geo.d.hv + hv] = 0.f;
+        } else {
+            tokens_outside(geo.d, span, [&](int64_t t0, int64_t t1, int worker, int workers) {
+                // a warp here is a head: the block's four share no tokens
+                const int blocks = workers / 4, block = worker / 4;
+                for (int64_t t = t0 + block * 32 + lane; t < t1; t += blocks * 32) dg[t * geo.d.hv + hv] = 0.f;
+            });
+        }
+        return;
+    }
+    double z = 0.0;
+    const float *d = in.dots + ((int64_t)span * geo.d.hv + hv) * in.parts;
+    for (int i = lane; i < in.parts; i += 32) z += (double)d[i];
+    const int per = (sp.y + 31) / 32, i0 = lane * per, i1 = min(i0 + per, sp.y);
+    auto at = [&](int i) { return (int64_t)(sp.x + i) * geo.d.hv + hv; };
+    double later = 0.0, before = 0.0;  // the lane's tokens' sums
+    for (int i = i0; i < i1; i++) {
+        later += (double)in.xq[at(i)] + ((double)in.rq[at(i)] - (double)in.rk[at(i)]);
+        before += (double)in.xk[at(i)];
+    }
+    double all = later, sum = before;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        z += __shfl_xor_sync(0xffffffffu, z, o);
+        const double u = __shfl_down_sync(0xffffffffu, all, o), v = __shfl_up_sync(0xffffffffu, sum, o);
+        if (lane + o < 32) all += u;
+        if (lane >= o) sum += v;
+    }
+    // of the lanes after and before this one: their own sums, so that nothing is subtracted
+    double tail = __shfl_down_sync(0xffffffffu, all, 1), head = __shfl_up_sync(0xffffffffu, sum, 1);
+    if (lane == 31) tail = 0.0;
+    if (lane == 0) head = 0.0;
+    double total = 0.0;
+    for (int i = i1 - 1; i >= i0; i--) {
+        tail += (double)in.xq[at(i)] + ((double)in.rq[at(i)] - (double)in.rk[at(i)]);
+        double h = head;
+        for (int j = i0; j < i; j++) h += (double)in.xk[at(j)];
+        const double v = tail + h + z;
+        if (parts)
+            total += v;
+        else
+            dg[at(i)] = (float)v;
+    }
+    if (!parts) return;
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) total += __shfl_xor_sync(0xffffffffu, total, o);
+    if (lane == 0) parts[(int64_t)span * geo.d.hv + hv] = (float)total;
+}
+
+// One decay a head: the spans' parts, a warp a head.
+__global__ void __launch_bounds__(128)
+k_decay_dg_heads(const float *__restrict__ parts, int spans, int hv, float *__restrict__ dg) {
+    after_previous();
+    const int lane = threadIdx.x & 31, h = (int)blockIdx.x * 4 + (threadIdx.x >> 5);
+    if (h >= hv) return;
+    double s = 0.0;
+    for (int i = lane; i < spans; i += 32) s += (double)parts[(int64_t)i * hv + h];
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
+    if (lane == 0) dg[h] = (float)s;
+}
+
+// ---------------------------------------------------------------- host
+
+template <typename T, int DX, int NB>
+cudaError_t sums_as(const DecayGeom &g, const DecayRows &x, const DecayRows &y, bool query, bool gates, float *out, bool next, cudaStream_t st) {
+    constexpr int smem = (int)sizeof(SumSmem<T, DX, NB>);
+    static OncePerDevice limit;
+    const cudaError_t attr = smem_limit(limit, k_decay_sums<T, DX, NB>, smem);
+    if (attr != cudaSuccess) return attr;
+    return launch(next, k_decay_sums<T, DX, NB>, dim3(g.d.nchunks, g.d.hv, (y.cols + NB - 1) / NB), sum_threads<DX, NB>(), smem, st, g, x, y,
+                  (int)query, (int)gates, out);
+}
+template <typename T>
+cudaError_t sums(const DecayGeom &g, const DecayRows &x, const DecayRows &y, bool query, bool gates, float *out, bool next, cudaStream_t st) {
+#define SUM_GO(DX) (y.cols <= 64 ? sums_as<T, DX, 64>(g, x, y, query, gates, out, next, st) : sums_as<T, DX, 128>(g, x, y, query, gates, out, next, st))
+    return x.cols <= 32 ? SUM_GO(32) : x.cols <= 64 ? SUM_GO(64) : SUM_GO(128);
+#undef SUM_GO
+}
+
+}  // namespace
+
+cudaError_t zs_launch_decay_sums(int type, const DecayGeom &g, const DecayRows &x, const DecayRows &y, bool query, bool gates, float *out,
+                                 bool next, cudaStream_t st, int64_t *launches) {
+    ++*launches;
+    if (type == ZSOLVE_F32) return sums<float>(g, x, y, query, gates, out, next, st);
+    if (type == ZSOLVE_BF16) return sums<bf16>(g, x, y, query, gates, out, next, st);
+    return sums<f16>(g, x, y, query, gates, out, next, st);
+}
+
+cudaError_t zs_launch_decay_scan(const DecayGeom &g, float *u, const float *s0, float *sn, bool next, cudaStream_t st, int64_t *launches) {
+    ++*launches;
+    const int size = g.d.dk * g.d.dv;
+    const unsigned heads = (unsigned)(g.d.nseq * g.d.hv);
+    if (zs_decay_vec(g, s0, sn))
+        return launch(next, k_decay_scan<4>, dim3(heads, (size + 4 * kScanThreads - 1) / (4 * kScanThreads)), kScanThreads, 0, st, g, u, s0, sn);
+    return launch(next, k_decay_scan<1>, dim3(heads, (size + kScanThreads - 1) / kScanThreads), kScanThreads, 0, st, g, u, s0, sn);
+}
+
+cudaError_t zs_launch_decay_rscan(const DecayGeom &g, float *w, const float *states, const float *ds, float *ds0, float *dots, bool next,
+                                  cudaStream_t st, int64_t *launches) {
+    ++*launches;
+    const int size = g.d.dk * g.d.dv;
+    const unsigned heads = (unsigned)(g.d.nseq * g.d.hv);
+    if (zs_decay_vec(g, ds, ds0))
+        return launch(next, k_decay_rscan<4>, dim3(heads, (size + 4 * kScanThreads - 1) / (4 * kScanThreads)), kScanThreads, 0, st, g, w, states,
+                      ds, ds0, dots);
+    return launch(next, k_decay_rscan<1>, dim3(heads, (size + kScanThreads - 1) / kScanThreads), kScanThreads, 0, st, g, w, states, ds, ds0, dots);
+}
+
+cudaError_t zs_launch_decay_dg(const DecayGeom &g, const float *const from_q[2], const float *const from_k[2], const float *dots,
+                               int ndots, float *parts, float *dg, cudaStream_t st, int64_t *launches) {
+    const DecayDots in{from_q[0], from_q[1], from_k[0], from_k[1], dots, ndots};
+    ++*launches;
+    const cudaError_t e = launch(true, k_decay_dg, dim3(g.d.nchunks, (g.d.hv + 3) / 4), 128, 0, st, g, in, g.ldg ? (float *)nullptr : parts, dg);
+    if (e != cudaSuccess || g.ldg) return e;
+    ++*launches;
+    return launch(true, k_decay_dg_heads, (unsigned)((g.d.hv + 3) / 4), 128, 0, st, parts, g.d.nchunks, g.d.hv, dg);
+}

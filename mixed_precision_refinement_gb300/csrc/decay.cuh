@@ -1,0 +1,128 @@
+// Linear attention with a decay for each head: the geometry of its spans, and what its kernels share.
+//
+// Per value head, with the state S (dk x dv) and a_t = exp g_t,
+//   S_t = a_t S_{t-1} + k_t v_t^T,  o_t = scale S_t^T q_t.
+// A span of up to L tokens with b_i = g_1 + ... + g_i:
+//   U = sum_j exp(b_L - b_j) k_j v_j^T,  S' = exp(b_L) S + U,
+//   o_i = scale (exp(b_i) S^T q_i + sum_{j <= i} exp(b_i - b_j) (q_i . k_j) v_j).
+// Backwards, with D the gradient of the state after the span,
+//   W = sum_i scale exp(b_i) q_i do_i^T,  D' (of the state before it) = exp(b_L) D + W,
+//   dq_i = scale (exp(b_i) S do_i + sum_{j <= i} exp(b_i - b_j) (do_i . v_j) k_j)
+//   dk_j = exp(b_L - b_j) D v_j + scale sum_{i >= j} exp(b_i - b_j) (do_i . v_j) q_i
+//   dv_j = exp(b_L - b_j) D^T k_j + scale sum_{i >= j} exp(b_i - b_j) (q_i . k_j) do_i
+//   dg_t = sum_{i >= t} q_i . dq_i|state + sum_{j < t} k_j . dk_j|state + exp(b_L) <S, D>
+//          + sum_{i >= t > j} scale exp(b_i - b_j) (do_i . v_j)(q_i . k_j).
+// U and W are one kernel (a weighted sum of outer products), and o, dq, dk and dv another: rows
+// x_i against rows y_j, with the scores' products with rows z_j, and a state's share,
+//   out_i = f_i M^T x_i + scale sum_j e_ij (x_i . y_j) z_j,
+// forwards (j <= i) or backwards (j >= i) in time.  Between the two, the states of all spans are
+// an elementwise recurrence over the spans.  So nothing but that recurrence goes token by token or
+// span by span, and every span, head and block of rows is on its own.
+//
+// The terms of dg that cancel (pairs of tokens on the same side of t) are left out of its sums,
+// not subtracted from them, but for those of one span.
+#pragma once
+
+#include "delta.cuh"
+
+namespace zs {
+
+constexpr int kSpanMost = 512;  // tokens of a span at most; a multiple of 64
+
+struct DecayGeom {
+    DeltaGeom d;        // its chunks are the spans; beta is not used
+    int64_t ldg;        // tokens' distance in g: hv, or 0 where each head has one
+    int span;           // tokens of a span, at most
+    float2 *gates;      // per span and head `span` values: b_i / ln 2 in two floats
+};
+
+// The state's or the score's rows: a tensor tokens x heads x cols.
+struct DecayRows {
+    const void *p;
+    int64_t ld;
+    int cols, dist;     // values of a head, and from one head to the next
+    bool key;           // heads are hk
+};
+
+// The products of rows (the formulas above): out, tokens x heads x z's columns at token stride ldo.
+//   m        per span and value head dk x dv; its rows meet x's columns, or (`turned`) its columns do
+//   back     backwards in time
+//   self     NULL, or what the gates' gradients need: out's heads are key heads, summed over the value heads that
+//            share one; self's rows (tokens x hk x z's columns) times the state's share of out go to sums[0], and the sums
+//            over j != i of scale e_ij (x_i . y_j)(self_i . z_j) to sums[1] (tokens x hv each)
+struct DecayProduct {
+    DecayRows x, y, z;
+    const float *m;
+    bool turned, back;
+    void *out;
+    int64_t ldo;
+    int heads;
+    const DecayRows *self;
+    float *sums[2];
+};
+
+// exp(b - c) of two sums in two floats each (in units of ln 2).
+__device__ __forceinline__ float decay_exp(float2 b, float2 c) { return exp2f((b.x - c.x) + (b.y - c.y)); }
+
+// One warp: the sums b_i of a span's tokens into `b`, in float64 (few additions), kept as two floats, so
+// that their differences keep their digits after a strong decay.  exp(-1e4) is 0, and finite
+// sums leave no inf - inf.
+__device__ __forceinline__ void decay_sums(const DecayGeom &geo, int2 sp, int hv, float2 *b) {
+    const int lane = threadIdx.x & 31;
+    const int per = (sp.y + 31) / 32, i0 = lane * per;
+    double s = 0.0;
+    for (int i = i0; i < min(i0 + per, sp.y); i++) {
+        float g = geo.d.g[(int64_t)(sp.x + i) * geo.ldg + hv];
+        if (g < -1e4f) g = -1e4f;
+        s += (double)g;
+    }
+    double before = s;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const double v = __shfl_up_sync(0xffffffffu, before, o);
+        if (lane >= o) before += v;
+    }
+    before = __shfl_up_sync(0xffffffffu, before, 1);
+    if (lane == 0) before = 0.0;
+    for (int i = i0; i < min(i0 + per, sp.y); i++) {
+        float g = geo.d.g[(int64_t)(sp.x + i) * geo.ldg + hv];
+        if (g < -1e4f) g = -1e4f;
+        before += (double)g;
+        const double x = before * 1.4426950408889634;
+        const float hi = (float)x;
+        b[i] = make_float2(hi, (float)(x - (double)hi));
+    }
+}
+
+}  // namespace zs
+
+// ---------------------------------------------------------------- launchers
+
+// out (per span and value head xc x yc float32): the sum of w_j x_j y_j^T over the span's tokens;
+// w_j = exp(b_L - b_j), or (`query`) scale exp(b_j).  The first launch of a call (`gates`) writes geo.gates.
+cudaError_t zs_launch_decay_sums(int type, const zs::DecayGeom &g, const zs::DecayRows &x, const zs::DecayRows &y, bool query,
+                                 bool gates, float *out, bool next, cudaStream_t st, int64_t *launches);
+// The states: of the spans' sums u (in place: in front of each span) and s0 (NULL: zero), the last ones to sn (NULL: not
+// written).
+cudaError_t zs_launch_decay_scan(const zs::DecayGeom &g, float *u, const float *s0, float *sn, bool next, cudaStream_t st,
+                                 int64_t *launches);
+// Their gradients: of the sums w (in place: after each span) and ds (NULL: zero), the first ones' to ds0 (NULL: not written); and
+// per span and head zs_decay_dots() partial sums of exp(b_L) <S, D> to dots.
+cudaError_t zs_launch_decay_rscan(const zs::DecayGeom &g, float *w, const float *states, const float *ds, float *ds0, float *dots,
+                                  bool next, cudaStream_t st, int64_t *launches);
+inline bool zs_decay_vec(const zs::DecayGeom &g, const float *s, const float *t) {
+    return g.d.dk * (int64_t)g.d.dv % 4 == 0 && (((uintptr_t)s | (uintptr_t)t) & 15) == 0;
+}
+inline int zs_decay_dots(const zs::DecayGeom &g, const float *ds, const float *ds0) {
+    const int64_t block = zs_decay_vec(g, ds, ds0) ? 1024 : 256;
+    return (int)(((int64_t)g.d.dk * g.d.dv + block - 1) / block) * 8;
+}
+
+cudaError_t zs_launch_decay_rows(int type, const zs::DecayGeom &g, const zs::DecayProduct &p, bool next, cudaStream_t st, int64_t *launches);
+// dg from the sums of both directions and the dots: tokens x hv, or where each head has one decay (ldg = 0) per span in `parts`
+// (spans x hv) and then in dg (hv).
+cudaError_t zs_launch_decay_dg(const zs::DecayGeom &g, const float *const from_q[2], const float *const from_k[2], const float *dots,
+                               int ndots, float *parts, float *dg, cudaStream_t st, int64_t *launches);
+// Token by token (decay_step.cu).
+cudaError_t zs_launch_decay_step(int type, const zs::DecayGeom &g, const int64_t *offsets, const float *s0, void *o, int64_t ldo, float *sn,
+                                 cudaStream_t st, int64_t *launches);

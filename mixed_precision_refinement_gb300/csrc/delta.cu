@@ -11,12 +11,12 @@ using namespace zs;
 
 // ---------------------------------------------------------------- chunk table
 
-// Sequences from their offsets (NULL: equal lengths), their first chunks, and
+// Sequences from their offsets (NULL: equal lengths), their first chunks of `len` tokens, and
 // the chunks' tokens.  Offsets that do not ascend within 0 .. tokens are
 // brought into that range one after the other, so that no later access leaves
 // the tensors.  One block: the sequences are few beside the tokens.
 __global__ void __launch_bounds__(1024)
-k_delta_plan(const int64_t *__restrict__ offsets, int nseq, int64_t tokens, int nchunks, int *first, int2 *seq,
+k_delta_plan(const int64_t *__restrict__ offsets, int nseq, int64_t tokens, int len, int nchunks, int *first, int2 *seq,
              int2 *chunk) {
     __shared__ int64_t s_end[32];
     __shared__ int s_sum[32];
@@ -50,7 +50,7 @@ k_delta_plan(const int64_t *__restrict__ offsets, int nseq, int64_t tokens, int 
         int64_t start = __shfl_up_sync(0xffffffffu, end, 1);
         if (lane == 0) start = before;
         if (start < lo) start = lo;
-        int n = i < nseq ? (int)((end - start + kChunk - 1) / kChunk) : 0;
+        int n = i < nseq ? (int)((end - start + len - 1) / len) : 0;
         int sum = n;
 #pragma unroll
         for (int o = 1; o < 32; o <<= 1) {
@@ -88,8 +88,8 @@ k_delta_plan(const int64_t *__restrict__ offsets, int nseq, int64_t tokens, int 
                     hi = mid;
             }
             const int2 sq = seq[lo];
-            const int at = (c - first[lo]) * kChunk;
-            ch = make_int2(sq.x + at, min(sq.y - at, kChunk));
+            const int at = (c - first[lo]) * len;
+            ch = make_int2(sq.x + at, min(sq.y - at, len));
         }
         chunk[c] = ch;
     }
@@ -776,9 +776,9 @@ cudaError_t chain_dk(const DeltaGeom &g, const DeltaTerms &t, const float *s0, v
 
 }  // namespace
 
-cudaError_t zs_launch_delta_plan(const int64_t *offsets, int nseq, int64_t tokens, int nchunks, int *first, int2 *seq,
+cudaError_t zs_launch_delta_plan(const int64_t *offsets, int nseq, int64_t tokens, int len, int nchunks, int *first, int2 *seq,
                                  int2 *chunk, cudaStream_t st, int64_t *launches) {
-    k_delta_plan<<<1, 1024, 0, st>>>(offsets, nseq, tokens, nchunks, first, seq, chunk);
+    k_delta_plan<<<1, 1024, 0, st>>>(offsets, nseq, tokens, len, nchunks, first, seq, chunk);
     ++*launches;
     return cudaGetLastError();
 }

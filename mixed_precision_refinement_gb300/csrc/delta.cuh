@@ -673,7 +673,7 @@ inline bool mult16(const void *p, int64_t ld, int64_t d, size_t e) {
 // next: the launch before on the stream is of the same call (seq.cuh).
 
 // delta.cu
-cudaError_t zs_launch_delta_plan(const int64_t *offsets, int nseq, int64_t tokens, int nchunks, int *first, int2 *seq,
+cudaError_t zs_launch_delta_plan(const int64_t *offsets, int nseq, int64_t tokens, int len, int nchunks, int *first, int2 *seq,
                                  int2 *chunk, cudaStream_t st, int64_t *launches);
 // tokens x heads x d values at token stride ld into packed heads of dp values
 cudaError_t zs_launch_delta_pack(int type, const void *src, int64_t ld, int64_t tokens, int heads, int d, int dp,

@@ -1,5 +1,6 @@
 // The C-ABI of the sequence-layer operators: the handle, its workspace, and
 // the argument checks in front of the kernels.
+#include "decay.cuh"
 #include "delta.cuh"
 #include "seq.cuh"
 
@@ -230,6 +231,93 @@ struct DeltaWork {
     }
 };
 
+// The arguments of a decayed attention call, checked, as the kernels take them.
+int check_decay(zsolve_seq *s, const zsolve_decay_args *a, const void *o, int64_t ldo, zs::DecayGeom *g) {
+    if (!a) return seq_fail(s, ZSOLVE_EINVAL, "NULL arguments");
+    if (!zs::type_ok(a->type)) return seq_fail(s, ZSOLVE_EINVAL, "type %d", a->type);
+    if (a->hk < 1 || a->hv < 1 || a->hv % a->hk != 0 || a->hv > 65535)
+        return seq_fail(s, ZSOLVE_EINVAL, "hk = %d, hv = %d: hv is a multiple of hk up to 65535", a->hk, a->hv);
+    if (a->dk < 1 || a->dk > ZSOLVE_DECAY_MAX_DK || a->dv < 1 || a->dv > 65536)
+        return seq_fail(s, ZSOLVE_EINVAL, "dk = %d outside 1..%d or dv = %d outside 1..65536", a->dk, ZSOLVE_DECAY_MAX_DK, a->dv);
+    if (a->nseq < 0 || a->tokens < 0 || a->tokens > 0x7fffff00 || (int64_t)a->nseq * a->hv > 0x7fffffff ||
+        (a->nseq == 0 && a->tokens > 0) || (!a->offsets && a->nseq > 0 && a->tokens % a->nseq != 0))
+        return seq_fail(s, ZSOLVE_EINVAL, "nseq = %d, tokens = %lld", a->nseq, (long long)a->tokens);
+    if (!std::isfinite(a->scale)) return seq_fail(s, ZSOLVE_EINVAL, "scale = %g", a->scale);
+    if (a->ldg != 0 && a->ldg != a->hv) return seq_fail(s, ZSOLVE_EINVAL, "ldg = %lld: hv, or 0 for one decay a head", (long long)a->ldg);
+    if (a->tokens > 0) {
+        if (!a->q || !a->k || !a->v || !a->g || !o) return seq_fail(s, ZSOLVE_EINVAL, "NULL q, k, v, g or output");
+        const int64_t rk = (int64_t)a->hk * a->dk, rv = (int64_t)a->hv * a->dv;
+        if (a->ldq < rk || a->ldk < rk || a->ldv < rv || ldo < rv)
+            return seq_fail(s, ZSOLVE_EINVAL, "a token stride is below its heads' values");
+    }
+    const int ve = 16 / (int)zs::type_bytes(a->type);
+    *g = zs::DecayGeom{};
+    g->d = zs::DeltaGeom{a->q, a->k, a->v, a->ldq, a->ldk, a->ldv, (a->dk + ve - 1) / ve * ve, (a->dv + ve - 1) / ve * ve, a->g, nullptr,
+                         a->hk, a->hv, a->dk, a->dv, a->nseq, a->tokens, (float)a->scale, nullptr, nullptr, nullptr, 0};
+    g->ldg = a->ldg;
+    return ZSOLVE_OK;
+}
+
+// The spans' workspace.
+struct DecayWork {
+    int *first = nullptr;
+    int2 *seq = nullptr, *chunk = nullptr;
+    float2 *gates = nullptr;
+    float *u = nullptr, *w = nullptr, *dots = nullptr, *parts = nullptr, *sums[4] = {};
+    void *copy[4] = {};  // packed q, k, v and dout, where needed
+    int ndots = 0;
+    zs::DecayRows q{}, k{}, v{}, dout{};
+
+    // Copies of rows that 16-byte loads cannot address, and the tables; dout NULL: the forward pass.
+    int place(zsolve_seq *s, const zsolve_decay_args *a, zs::DecayGeom *g, const void *dout_p, int64_t lddo, bool backward, const float *ds,
+              const float *ds0) {
+        g->span = 256;
+        const int64_t most = a->tokens / g->span + a->nseq;
+        if (most > 0x7fffffff / zs::kSpanMost) return seq_fail(s, ZSOLVE_EINVAL, "too many spans");
+        // and an unused entry, whose blocks write what belongs to the tokens outside the offsets
+        g->d.nchunks = (int)most + (a->offsets ? 1 : 0);
+        const size_t slots = (size_t)most * a->hv, state = (size_t)a->dk * a->dv, e = zs::type_bytes(a->type);
+        const void *src[4] = {a->q, a->k, a->v, dout_p};
+        const int64_t ld[4] = {a->ldq, a->ldk, a->ldv, lddo};
+        const int heads[4] = {a->hk, a->hk, a->hv, a->hv}, cols[4] = {a->dk, a->dk, a->dv, a->dv}, dist[4] = {g->d.dkp, g->d.dkp, g->d.dvp, g->d.dvp};
+        ndots = backward ? zs_decay_dots(*g, ds, ds0) : 0;
+        auto carve = [&](zs::Carve c) {
+            first = c.take<int>((size_t)a->nseq + 1);
+            seq = c.take<int2>((size_t)a->nseq);
+            chunk = c.take<int2>((size_t)g->d.nchunks);
+            gates = c.take<float2>(slots * g->span);
+            u = c.take<float>(slots * state);
+            for (int i = 0; i < (backward ? 4 : 3); i++)
+                copy[i] = zs::mult16(src[i], ld[i], cols[i], e) ? nullptr : c.take<char>((size_t)a->tokens * heads[i] * dist[i] * e);
+            if (!backward) return c.at;
+            w = c.take<float>(slots * state);
+            dots = c.take<float>(slots * ndots);
+            parts = a->ldg ? nullptr : c.take<float>((size_t)g->d.nchunks * a->hv);
+            for (float *&x : sums) x = c.take<float>((size_t)a->tokens * a->hv);
+            return c.at;
+        };
+        const size_t bytes = carve(zs::Carve(nullptr));
+        int st = ZSOLVE_OK;
+        void *ws = zs::seq_workspace(s, bytes, &st);
+        if (!ws) return st;
+        carve(zs::Carve(ws));
+        zs::DecayRows *const rows[4] = {&q, &k, &v, &dout};
+        for (int i = 0; i < (backward ? 4 : 3); i++) {
+            *rows[i] = zs::DecayRows{src[i], ld[i], cols[i], copy[i] ? dist[i] : cols[i], i < 2};
+            if (!copy[i] || a->tokens == 0) continue;
+            SEQ_CU(zs_launch_delta_pack(a->type, src[i], ld[i], a->tokens, heads[i], cols[i], dist[i], copy[i], s->num_sms, s->st, &s->launches));
+            rows[i]->p = copy[i];
+            rows[i]->ld = (int64_t)heads[i] * dist[i];
+        }
+        g->d.first = first;
+        g->d.seq = seq;
+        g->d.chunk = chunk;
+        g->gates = gates;
+        SEQ_CU(zs_launch_delta_plan(a->offsets, a->nseq, a->tokens, g->span, g->d.nchunks, first, seq, chunk, s->st, &s->launches));
+        return ZSOLVE_OK;
+    }
+};
+
 }  // namespace
 
 extern "C" {
@@ -456,7 +544,7 @@ int zsolve_delta(zsolve_seq *s, const zsolve_delta_args *a, void *o, int64_t ldo
     st = w.place(s, a);
     if (st == ZSOLVE_OK) st = w.bind(s, a, &g);
     if (st != ZSOLVE_OK) return st;
-    SEQ_CU(zs_launch_delta_plan(a->offsets, a->nseq, a->tokens, w.nchunks, w.first, w.seq, w.chunk, s->st, &s->launches));
+    SEQ_CU(zs_launch_delta_plan(a->offsets, a->nseq, a->tokens, zs::kChunk, w.nchunks, w.first, w.seq, w.chunk, s->st, &s->launches));
     SEQ_CU(zs_launch_delta_terms(a->type, g, w.terms, o, ldo, true, s->st, &s->launches));
     SEQ_CU(zs_launch_delta_chain(a->type, g, w.terms, a->s0, o, ldo, sn, nullptr, nullptr, s->d_status, true, s->st,
                                  &s->launches));
@@ -471,6 +559,78 @@ int zsolve_delta_step(zsolve_seq *s, const zsolve_delta_args *a, void *o, int64_
     st = check_device(s);
     if (st != ZSOLVE_OK) return st;
     SEQ_CU(zs_launch_delta_step(a->type, g, a->offsets, a->s0, o, ldo, sn, s->st, &s->launches));
+    return ZSOLVE_OK;
+}
+
+int zsolve_decay(zsolve_seq *s, const zsolve_decay_args *a, void *o, int64_t ldo, float *sn) {
+    if (!s) return ZSOLVE_EINVAL;
+    zs::DecayGeom g;
+    int st = check_decay(s, a, o, ldo, &g);
+    if (st != ZSOLVE_OK || a->nseq == 0) return st;
+    st = check_device(s);
+    if (st != ZSOLVE_OK) return st;
+    const int64_t longest = a->offsets ? a->tokens : a->tokens / a->nseq;
+    if (longest <= kStepTokens) {
+        SEQ_CU(zs_launch_decay_step(a->type, g, a->offsets, a->s0, o, ldo, sn, s->st, &s->launches));
+        return ZSOLVE_OK;
+    }
+    DecayWork w;
+    st = w.place(s, a, &g, nullptr, 0, false, nullptr, nullptr);
+    if (st != ZSOLVE_OK) return st;
+    SEQ_CU(zs_launch_decay_sums(a->type, g, w.k, w.v, false, true, w.u, true, s->st, &s->launches));
+    SEQ_CU(zs_launch_decay_scan(g, w.u, a->s0, sn, true, s->st, &s->launches));
+    const zs::DecayProduct p{w.q, w.k, w.v, w.u, false, false, o, ldo, a->hv, nullptr, {nullptr, nullptr}};
+    SEQ_CU(zs_launch_decay_rows(a->type, g, p, true, s->st, &s->launches));
+    return ZSOLVE_OK;
+}
+
+int zsolve_decay_step(zsolve_seq *s, const zsolve_decay_args *a, void *o, int64_t ldo, float *sn) {
+    if (!s) return ZSOLVE_EINVAL;
+    zs::DecayGeom g;
+    int st = check_decay(s, a, o, ldo, &g);
+    if (st != ZSOLVE_OK || a->nseq == 0) return st;
+    st = check_device(s);
+    if (st != ZSOLVE_OK) return st;
+    SEQ_CU(zs_launch_decay_step(a->type, g, a->offsets, a->s0, o, ldo, sn, s->st, &s->launches));
+    return ZSOLVE_OK;
+}
+
+int zsolve_decay_bwd(zsolve_seq *s, const zsolve_decay_args *a, const void *dout, int64_t lddo, const float *ds, void *dq, void *dk,
+                     void *dv, float *dg, float *ds0) {
+    if (!s) return ZSOLVE_EINVAL;
+    zs::DecayGeom g;
+    int st = check_decay(s, a, dout, lddo, &g);
+    if (st != ZSOLVE_OK) return st;
+    if ((a->tokens > 0 && (!dq || !dk || !dv || !dg)) || (a->ldg == 0 && !dg)) return seq_fail(s, ZSOLVE_EINVAL, "NULL dq, dk, dv or dg");
+    st = check_device(s);
+    if (st != ZSOLVE_OK) return st;
+    if (a->nseq == 0 || a->tokens == 0) {  // sums over nothing, and the states' gradients as they are
+        const size_t states = (size_t)a->nseq * a->hv * a->dk * a->dv * sizeof(float);
+        if (a->ldg == 0) SEQ_CU(cudaMemsetAsync(dg, 0, (size_t)a->hv * sizeof(float), s->st));
+        if (ds0 && states && ds0 != ds) {
+            if (ds)
+                SEQ_CU(cudaMemcpyAsync(ds0, ds, states, cudaMemcpyDeviceToDevice, s->st));
+            else
+                SEQ_CU(cudaMemsetAsync(ds0, 0, states, s->st));
+        }
+        return ZSOLVE_OK;
+    }
+    DecayWork w;
+    st = w.place(s, a, &g, dout, lddo, true, ds, ds0);
+    if (st != ZSOLVE_OK) return st;
+    SEQ_CU(zs_launch_decay_sums(a->type, g, w.k, w.v, false, true, w.u, true, s->st, &s->launches));
+    SEQ_CU(zs_launch_decay_sums(a->type, g, w.q, w.dout, true, false, w.w, true, s->st, &s->launches));
+    SEQ_CU(zs_launch_decay_scan(g, w.u, a->s0, nullptr, true, s->st, &s->launches));
+    SEQ_CU(zs_launch_decay_rscan(g, w.w, w.u, ds, ds0, w.dots, true, s->st, &s->launches));
+    const int64_t rk = (int64_t)a->hk * a->dk, rv = (int64_t)a->hv * a->dv;
+    const zs::DecayProduct pq{w.dout, w.v, w.k, w.u, true, false, dq, rk, a->hk, &w.q, {w.sums[0], w.sums[1]}};
+    const zs::DecayProduct pk{w.v, w.dout, w.q, w.w, true, true, dk, rk, a->hk, &w.k, {w.sums[2], w.sums[3]}};
+    const zs::DecayProduct pv{w.k, w.q, w.dout, w.w, false, true, dv, rv, a->hv, nullptr, {nullptr, nullptr}};
+    SEQ_CU(zs_launch_decay_rows(a->type, g, pq, true, s->st, &s->launches));
+    SEQ_CU(zs_launch_decay_rows(a->type, g, pk, true, s->st, &s->launches));
+    SEQ_CU(zs_launch_decay_rows(a->type, g, pv, true, s->st, &s->launches));
+    const float *const from_q[2] = {w.sums[0], w.sums[1]}, *const from_k[2] = {w.sums[2], w.sums[3]};
+    SEQ_CU(zs_launch_decay_dg(g, from_q, from_k, w.dots, w.ndots, w.parts, dg, s->st, &s->launches));
     return ZSOLVE_OK;
 }
 
@@ -492,7 +652,7 @@ int zsolve_delta_bwd(zsolve_seq *s, const zsolve_delta_args *a, const void *dout
     st = w.place(s, a);
     if (st == ZSOLVE_OK) st = w.bind(s, a, &g);
     if (st != ZSOLVE_OK) return st;
-    SEQ_CU(zs_launch_delta_plan(a->offsets, a->nseq, a->tokens, w.nchunks, w.first, w.seq, w.chunk, s->st, &s->launches));
+    SEQ_CU(zs_launch_delta_plan(a->offsets, a->nseq, a->tokens, zs::kChunk, w.nchunks, w.first, w.seq, w.chunk, s->st, &s->launches));
     if (a->tokens > 0) SEQ_CU(zs_launch_delta_terms(a->type, g, w.terms, nullptr, 0, true, s->st, &s->launches));
     auto backwards = [&](bool next, cudaStream_t on) {
         return zs_launch_delta_rchain(a->type, g, w.terms, w.dout, w.lddo, ds, w.dends, w.dxs, dv, ds0, s->d_status, next, on,

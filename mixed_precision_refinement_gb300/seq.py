@@ -414,6 +414,81 @@ def zsolve_delta_bwd(seq, dout, q, k, v, g, beta, dq, dk, dv, dg, dbeta, ds0=Non
                                           _vector(dbeta, "dbeta", n, torch.float32, beta.shape, 1), _state(ds0, a)))
 
 
+class zsolve_decay_args(ctypes.Structure):
+    _fields_ = [("type", ctypes.c_int), ("hk", ctypes.c_int), ("hv", ctypes.c_int), ("dk", ctypes.c_int),
+                ("dv", ctypes.c_int), ("nseq", ctypes.c_int), ("tokens", ctypes.c_int64),
+                ("offsets", ctypes.c_void_p), ("q", ctypes.c_void_p), ("k", ctypes.c_void_p),
+                ("v", ctypes.c_void_p), ("ldq", ctypes.c_int64), ("ldk", ctypes.c_int64), ("ldv", ctypes.c_int64),
+                ("g", ctypes.c_void_p), ("ldg", ctypes.c_int64), ("s0", ctypes.c_void_p), ("scale", ctypes.c_double)]
+
+
+def _sequences(q, offsets) -> int:
+    if offsets is None:
+        return q.shape[0] if q.dim() == 4 else 1
+    if offsets.numel() < 1:
+        raise ValueError("offsets: expected one more than the sequences")
+    return offsets.numel() - 1
+
+
+def _per_head(g, hv) -> bool:
+    """Whether g has one log decay a head, not one a token and head."""
+    return g.dim() == 1 and g.shape[0] == hv
+
+
+def _decays(g, name, n, hv, lead):
+    if _per_head(g, hv):
+        return _vector(g, name, hv, torch.float32), 0
+    return _vector(g, name, n * hv, torch.float32, (*lead, hv), 1), hv
+
+
+def _decay_args(q, k, v, g, s0, offsets, scale, nseq=None):
+    qp, n, hk, dk, ldq = _tokens(q, "q")
+    kp, _, _, _, ldk = _tokens(k, "k", q.dtype, (n, hk, dk), q)
+    vp, _, hv, dv, ldv = _tokens(v, "v", q.dtype)
+    lead = q.shape[:-2]
+    if v.shape[:-2] != lead:
+        raise ValueError(f"v: expected the tokens of q, {tuple(lead)}, got {tuple(v.shape[:-2])}")
+    if nseq is None:
+        nseq = _sequences(q, offsets)
+    gp, ldg = _decays(g, "g", n, hv, lead)
+    return zsolve_decay_args(_type(q, "q"), hk, hv, dk, dv, nseq, n, _vector(offsets, "offsets", nseq + 1, torch.int64) or None, qp, kp,
+                             vp, ldq, ldk, ldv, gp, ldg,
+                             _vector(s0, "s0", nseq * hv * dk * dv, torch.float32, (nseq, hv, dk, dv), 3),
+                             dk ** -0.5 if scale is None else scale)
+
+
+def zsolve_decay(seq, q, k, v, g, o, s=None, s0=None, offsets=None, scale=None) -> None:
+    """o, s <- linear attention with a decay for each head over whole sequences.
+
+    q, k: (tokens, hk, dk), v, o: (tokens, hv, dv), g: float32 (tokens, hv), or (hv,) for one log decay a head; or
+    with two leading dimensions, sequences x tokens.  offsets, s0, s and scale: as for zsolve_delta.
+    """
+    a = _decay_args(q, k, v, g, s0, offsets, scale)
+    op, _, _, _, ldo = _tokens(o, "o", q.dtype, (a.tokens, a.hv, a.dv), v)
+    _check_seq(seq, _lib.zsolve_decay(seq, ctypes.byref(a), op, ldo, _state(s, a)))
+
+
+def zsolve_decay_step(seq, q, k, v, g, o, s=None, s0=None, offsets=None, scale=None) -> None:
+    """As zsolve_decay, token by token: for one or a few tokens a sequence."""
+    _decay_step(seq, q, k, v, g, o, s, s0, offsets, scale)
+
+
+def _decay_step(seq, q, k, v, g, o, s, s0, offsets, scale, nseq=None):
+    a = _decay_args(q, k, v, g, s0, offsets, scale, nseq)
+    op, _, _, _, ldo = _tokens(o, "o", q.dtype, (a.tokens, a.hv, a.dv), v)
+    _check_seq(seq, _lib.zsolve_decay_step(seq, ctypes.byref(a), op, ldo, _state(s, a)))
+
+
+def zsolve_decay_bwd(seq, dout, q, k, v, g, dq, dk, dv, dg, ds0=None, s0=None, ds=None, offsets=None, scale=None) -> None:
+    """dq .. dg and ds0 (shapes of q .. g and s0, contiguous) from dout (as o) and ds (as s, or None)."""
+    a = _decay_args(q, k, v, g, s0, offsets, scale)
+    op, _, _, _, lddo = _tokens(dout, "dout", q.dtype, (a.tokens, a.hv, a.dv), v)
+    nk, nv = a.tokens * a.hk * a.dk, a.tokens * a.hv * a.dv
+    _check_seq(seq, _lib.zsolve_decay_bwd(seq, ctypes.byref(a), op, lddo, _state(ds, a), _vector(dq, "dq", nk, q.dtype, q.shape, 2),
+                                          _vector(dk, "dk", nk, q.dtype, k.shape, 2), _vector(dv, "dv", nv, q.dtype, v.shape, 2),
+                                          _vector(dg, "dg", g.numel(), torch.float32, g.shape, 1), _state(ds0, a)))
+
+
 def _state(s, a):
     return _vector(s, "s", a.nseq * a.hv * a.dk * a.dv, torch.float32, (a.nseq, a.hv, a.dk, a.dv), 3)
 
@@ -579,6 +654,42 @@ class Seq:
         o = torch.empty(v.shape, dtype=v.dtype, device=v.device)
         s_out = s if s_out is None else s_out
         _step(self.seq, q, k, v, g, beta, o, s_out, s, None, scale, q.shape[0])
+        return o, s_out
+
+    def decay(self, q, k, v, g, s0=None, offsets=None, scale=None):
+        """Returns (o, s): linear attention with a decay for each head over whole sequences, from the states s0 (zero
+        without) to s.
+
+        Shapes as for zsolve_decay; s is (sequences, hv, dk, dv) float32.
+        """
+        if _records(q, k, v, g, s0):
+            return _autograd().Decay.apply(self, q, k, v, g, s0, offsets, scale)
+        self._on_stream()
+        o = torch.empty(v.shape, dtype=v.dtype, device=v.device)
+        nseq = _sequences(q, offsets)
+        s = torch.empty((nseq, v.shape[-2], q.shape[-1], v.shape[-1]), dtype=torch.float32, device=v.device)
+        zsolve_decay(self.seq, q, k, v, g, o, s, s0, offsets, scale)
+        return o, s
+
+    def decay_bwd(self, dout, q, k, v, g, s0=None, ds=None, offsets=None, scale=None):
+        """Returns (dq, dk, dv, dg, ds0) from the gradients of o and, unless None, of s."""
+        self._on_stream()
+        dq, dk, dv = (torch.empty(t.shape, dtype=t.dtype, device=t.device) for t in (q, k, v))
+        dg = torch.empty(g.shape, dtype=torch.float32, device=g.device)
+        nseq = _sequences(q, offsets)
+        ds0 = torch.empty((nseq, v.shape[-2], q.shape[-1], v.shape[-1]), dtype=torch.float32, device=v.device)
+        zsolve_decay_bwd(self.seq, dout, q, k, v, g, dq, dk, dv, dg, ds0, s0, ds, offsets, scale)
+        return dq, dk, dv, dg, ds0
+
+    def decay_step(self, q, k, v, g, s, s_out=None, scale=None):
+        """Returns (o, s): the next token of every sequence, q (sequences, hk, dk) and so on (or the next few,
+        with two leading dimensions), g (sequences, hv) or (hv,).  The states are updated in place, or written to s_out."""
+        if _records(q, k, v, g, s):
+            return _autograd().DecayStep.apply(self, q, k, v, g, s, s if s_out is None else s_out, scale)
+        self._on_stream()
+        o = torch.empty(v.shape, dtype=v.dtype, device=v.device)
+        s_out = s if s_out is None else s_out
+        _decay_step(self.seq, q, k, v, g, o, s_out, s, None, scale, q.shape[0])
         return o, s_out
 
     def check(self):

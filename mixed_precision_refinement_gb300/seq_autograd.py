@@ -139,6 +139,39 @@ class Delta(torch.autograd.Function):
         return (None, *grads, ds0 if s0 is not None else None, None, None)
 
 
+class Decay(torch.autograd.Function):
+    @staticmethod
+    def forward(ctx, seq, q, k, v, g, s0, offsets, scale):
+        o, s = seq.decay(q, k, v, g, s0, offsets, scale)
+        ctx.seq, ctx.scale = seq, scale
+        ctx.set_materialize_grads(False)
+        ctx.save_for_backward(q, k, v, g, s0, offsets)
+        return o, s
+
+    @staticmethod
+    @once_differentiable
+    def backward(ctx, do, ds):
+        if do is None and ds is None:
+            return (None,) * 8
+        q, k, v, g, s0, offsets = ctx.saved_tensors
+        do = torch.zeros(v.shape, dtype=v.dtype, device=v.device) if do is None else do.contiguous()
+        ds = None if ds is None else ds.contiguous()
+        *grads, ds0 = ctx.seq.decay_bwd(do, q, k, v, g, s0, ds, offsets, ctx.scale)
+        return (None, *grads, ds0 if s0 is not None else None, None, None)
+
+
+class DecayStep(torch.autograd.Function):
+    @staticmethod
+    def forward(ctx, seq, q, k, v, g, s, s_out, scale):
+        o, s_out = seq.decay_step(q, k, v, g, s, s_out, scale)
+        ctx.mark_dirty(s_out)
+        return o, s_out
+
+    @staticmethod
+    def backward(ctx, do, ds):
+        raise RuntimeError("decay_step carries no gradients: train with decay")
+
+
 class Step(torch.autograd.Function):
     """The token-by-token form, for answering, has no gradients: a backward pass that reaches it is an error."""
 

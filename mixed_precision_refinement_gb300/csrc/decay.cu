@@ -109,18 +109,64 @@ __device__ __forceinline__ float span_decay(const DecayGeom &geo, int span, int 
     return decay_exp(geo.gates[((int64_t)span * geo.d.hv + hv) * geo.span + geo.d.chunk[span].y - 1], make_float2(0.f, 0.f));
 }
 
+// A state's value as the next kernels take it: float32 in the place of the sum, or PARTS bfloat16 values that add up
+// to it (16 or 24 bits), each part a matrix of its own.
+template <int VE, int PARTS>
+struct StatePut {
+    __device__ __forceinline__ static void put(float *u, bf16 *planes, int64_t slot, int size, int at, const float (&s)[VE]) {
+        if (PARTS == 0) {
+            Vec<float, VE> v;
+            v.set(s);
+            v.store(u + slot * size + at);
+            return;
+        }
+        float f[VE];
+#pragma unroll
+        for (int e = 0; e < VE; e++) f[e] = s[e];
+        bf16 *p = planes + slot * PARTS * size + at;
+#pragma unroll
+        for (int i = 0; i < PARTS; i++, p += size) {
+            Vec<bf16, VE> v;
+            v.set(f);
+            v.store(p);
+            float g[VE];
+            v.get(g);
+#pragma unroll
+            for (int e = 0; e < VE; e++) f[e] -= g[e];
+        }
+    }
+    __device__ __forceinline__ static void get(const float *u, const bf16 *planes, int64_t slot, int size, int at, float (&s)[VE]) {
+        if (PARTS == 0) {
+            Vec<float, VE> v;
+            v.load(u + slot * size + at);
+            v.get(s);
+            return;
+        }
+        const bf16 *p = planes + slot * PARTS * size + at;
+#pragma unroll
+        for (int e = 0; e < VE; e++) s[e] = 0.f;
+#pragma unroll
+        for (int i = 0; i < PARTS; i++) {
+            Vec<bf16, VE> v;
+            v.load(p + (int64_t)(PARTS - 1 - i) * size);
+            float g[VE];
+            v.get(g);
+#pragma unroll
+            for (int e = 0; e < VE; e++) s[e] += g[e];
+        }
+    }
+};
+
 // A thread VE neighbouring values of a state.
-template <int VE>
+template <int VE, int PARTS>
 __global__ void __launch_bounds__(kScanThreads)
-k_decay_scan(const DecayGeom geo, float *u, const float *s0, float *sn) {
+k_decay_scan(const DecayGeom geo, float *u, bf16 *planes, const float *s0, float *sn) {
     after_previous();
     may_start_next();
     const int si = blockIdx.x / geo.d.hv, hv = blockIdx.x - si * geo.d.hv, size = geo.d.dk * geo.d.dv;
     const int at = ((int)blockIdx.y * kScanThreads + (int)threadIdx.x) * VE;
     if (at >= size) return;
     const int first = geo.d.first[si], n = geo.d.first[si + 1] - first;
-    const int64_t step = (int64_t)geo.d.hv * size;
-    float *p = u + ((int64_t)first * geo.d.hv + hv) * size + at;
     float s[VE] = {};
     Vec<float, VE> v;
     if (s0) v.load(s0 + (int64_t)blockIdx.x * size + at), v.get(s);
@@ -129,14 +175,13 @@ k_decay_scan(const DecayGeom geo, float *u, const float *s0, float *sn) {
         float a[kAhead];
 #pragma unroll
         for (int k = 0; k < kAhead; k++)
-            if (i + k < n) w[k].load(p + (i + k) * step), a[k] = span_decay(geo, first + i + k, hv);
+            if (i + k < n) w[k].load(u + ((int64_t)(first + i + k) * geo.d.hv + hv) * size + at), a[k] = span_decay(geo, first + i + k, hv);
 #pragma unroll
         for (int k = 0; k < kAhead; k++) {
             if (i + k >= n) break;
             float f[VE];
             w[k].get(f);
-            v.set(s);
-            v.store(p + (i + k) * step);
+            StatePut<VE, PARTS>::put(u, planes, (int64_t)(first + i + k) * geo.d.hv + hv, size, at, s);
 #pragma unroll
             for (int e = 0; e < VE; e++) s[e] = fmaf(a[k], s[e], f[e]);
         }
@@ -144,45 +189,45 @@ k_decay_scan(const DecayGeom geo, float *u, const float *s0, float *sn) {
     if (sn) v.set(s), v.store(sn + (int64_t)blockIdx.x * size + at);
 }
 
-template <int VE>
+// PARTS: of the states and of their gradients.
+template <int VE, int PARTS>
 __global__ void __launch_bounds__(kScanThreads)
-k_decay_rscan(const DecayGeom geo, float *w, const float *__restrict__ states, const float *ds, float *ds0, float *__restrict__ dots) {
+k_decay_rscan(const DecayGeom geo, float *w, bf16 *planes, const float *__restrict__ states, const bf16 *__restrict__ splanes, const float *ds,
+              float *ds0, float *__restrict__ dots) {
     after_previous();
     may_start_next();
     const int si = blockIdx.x / geo.d.hv, hv = blockIdx.x - si * geo.d.hv, size = geo.d.dk * geo.d.dv;
     const int at = ((int)blockIdx.y * kScanThreads + (int)threadIdx.x) * VE;
     const bool in = at < size;
     const int first = geo.d.first[si], n = geo.d.first[si + 1] - first;
-    const int64_t step = (int64_t)geo.d.hv * size, base = ((int64_t)first * geo.d.hv + hv) * size + at;
     float s[VE] = {};
     Vec<float, VE> v;
     if (ds && in) v.load(ds + (int64_t)blockIdx.x * size + at), v.get(s);
     const int warps = kScanThreads / 32, parts = gridDim.y * warps;
     for (int i = n - 1; i >= 0; i -= kAhead) {
-        Vec<float, VE> x[kAhead], y[kAhead];
-        float a[kAhead];
+        Vec<float, VE> x[kAhead];
+        float y[kAhead][VE], a[kAhead];
 #pragma unroll
         for (int k = 0; k < kAhead; k++)
             if (i - k >= 0) {
-                if (in) x[k].load(w + base + (i - k) * step), y[k].load(states + base + (i - k) * step);
+                const int64_t slot = (int64_t)(first + i - k) * geo.d.hv + hv;
+                if (in) x[k].load(w + slot * size + at), StatePut<VE, PARTS>::get(states, splanes, slot, size, at, y[k]);
                 a[k] = span_decay(geo, first + i - k, hv);
             }
 #pragma unroll
         for (int k = 0; k < kAhead; k++) {
             if (i - k < 0) break;
+            const int64_t slot = (int64_t)(first + i - k) * geo.d.hv + hv;
             float dot = 0.f;
             if (in) {
-                float f[VE], q[VE];
+                float f[VE];
                 x[k].get(f);
-                y[k].get(q);
-                v.set(s);
-                v.store(w + base + (i - k) * step);
+                StatePut<VE, PARTS>::put(w, planes, slot, size, at, s);
 #pragma unroll
-                for (int e = 0; e < VE; e++) dot = fmaf(q[e], s[e], dot), s[e] = fmaf(a[k], s[e], f[e]);
+                for (int e = 0; e < VE; e++) dot = fmaf(y[k][e], s[e], dot), s[e] = fmaf(a[k], s[e], f[e]);
             }
             dot = warp_sum(dot) * a[k];
-            if ((threadIdx.x & 31) == 0)
-                dots[((int64_t)(first + i - k) * geo.d.hv + hv) * parts + blockIdx.y * warps + (threadIdx.x >> 5)] = dot;
+            if ((threadIdx.x & 31) == 0) dots[slot * parts + blockIdx.y * warps + (threadIdx.x >> 5)] = dot;
         }
     }
     if (ds0 && in) v.set(s), v.store(ds0 + (int64_t)blockIdx.x * size + at);
@@ -296,24 +341,32 @@ cudaError_t zs_launch_decay_sums(int type, const DecayGeom &g, const DecayRows &
     return sums<f16>(g, x, y, query, gates, out, next, st);
 }
 
-cudaError_t zs_launch_decay_scan(const DecayGeom &g, float *u, const float *s0, float *sn, bool next, cudaStream_t st, int64_t *launches) {
+cudaError_t zs_launch_decay_scan(const DecayGeom &g, float *u, void *planes, int parts, const float *s0, float *sn, bool next, cudaStream_t st,
+                                 int64_t *launches) {
     ++*launches;
     const int size = g.d.dk * g.d.dv;
     const unsigned heads = (unsigned)(g.d.nseq * g.d.hv);
-    if (zs_decay_vec(g, s0, sn))
-        return launch(next, k_decay_scan<4>, dim3(heads, (size + 4 * kScanThreads - 1) / (4 * kScanThreads)), kScanThreads, 0, st, g, u, s0, sn);
-    return launch(next, k_decay_scan<1>, dim3(heads, (size + kScanThreads - 1) / kScanThreads), kScanThreads, 0, st, g, u, s0, sn);
+    bf16 *const pl = (bf16 *)planes;
+#define SCAN_GO(VE, P) \
+    launch(next, k_decay_scan<VE, P>, dim3(heads, (size + VE * kScanThreads - 1) / (VE * kScanThreads)), kScanThreads, 0, st, g, u, pl, s0, sn)
+    if (zs_decay_vec(g, s0, sn)) return parts == 0 ? SCAN_GO(4, 0) : parts == 2 ? SCAN_GO(4, 2) : SCAN_GO(4, 3);
+    return parts == 0 ? SCAN_GO(1, 0) : parts == 2 ? SCAN_GO(1, 2) : SCAN_GO(1, 3);
+#undef SCAN_GO
 }
 
-cudaError_t zs_launch_decay_rscan(const DecayGeom &g, float *w, const float *states, const float *ds, float *ds0, float *dots, bool next,
-                                  cudaStream_t st, int64_t *launches) {
+cudaError_t zs_launch_decay_rscan(const DecayGeom &g, float *w, void *planes, int parts, const float *states, const void *splanes,
+                                  const float *ds, float *ds0, float *dots, bool next, cudaStream_t st, int64_t *launches) {
     ++*launches;
     const int size = g.d.dk * g.d.dv;
     const unsigned heads = (unsigned)(g.d.nseq * g.d.hv);
-    if (zs_decay_vec(g, ds, ds0))
-        return launch(next, k_decay_rscan<4>, dim3(heads, (size + 4 * kScanThreads - 1) / (4 * kScanThreads)), kScanThreads, 0, st, g, w, states,
-                      ds, ds0, dots);
-    return launch(next, k_decay_rscan<1>, dim3(heads, (size + kScanThreads - 1) / kScanThreads), kScanThreads, 0, st, g, w, states, ds, ds0, dots);
+    bf16 *const pl = (bf16 *)planes;
+    const bf16 *const spl = (const bf16 *)splanes;
+#define SCAN_GO(VE, P)                                                                                                              \
+    launch(next, k_decay_rscan<VE, P>, dim3(heads, (size + VE * kScanThreads - 1) / (VE * kScanThreads)), kScanThreads, 0, st, g, w, pl, \
+           states, spl, ds, ds0, dots)
+    if (zs_decay_vec(g, ds, ds0)) return parts == 0 ? SCAN_GO(4, 0) : SCAN_GO(4, 3);
+    return parts == 0 ? SCAN_GO(1, 0) : SCAN_GO(1, 3);
+#undef SCAN_GO
 }
 
 cudaError_t zs_launch_decay_dg(const DecayGeom &g, const float *const from_q[2], const float *const from_k[2], const float *dots,

@@ -52,7 +52,7 @@ struct DecayRows {
 //            over j != i of scale e_ij (x_i . y_j)(self_i . z_j) to sums[1] (tokens x hv each)
 struct DecayProduct {
     DecayRows x, y, z;
-    const float *m;
+    const void *m;      // float32 (zs_launch_decay_rows)
     bool turned, back;
     void *out;
     int64_t ldo;
@@ -102,14 +102,14 @@ __device__ __forceinline__ void decay_sums(const DecayGeom &geo, int2 sp, int hv
 // w_j = exp(b_L - b_j), or (`query`) scale exp(b_j).  The first launch of a call (`gates`) writes geo.gates.
 cudaError_t zs_launch_decay_sums(int type, const zs::DecayGeom &g, const zs::DecayRows &x, const zs::DecayRows &y, bool query,
                                  bool gates, float *out, bool next, cudaStream_t st, int64_t *launches);
-// The states: of the spans' sums u (in place: in front of each span) and s0 (NULL: zero), the last ones to sn (NULL: not
-// written).
-cudaError_t zs_launch_decay_scan(const zs::DecayGeom &g, float *u, const float *s0, float *sn, bool next, cudaStream_t st,
-                                 int64_t *launches);
-// Their gradients: of the sums w (in place: after each span) and ds (NULL: zero), the first ones' to ds0 (NULL: not written); and
-// per span and head zs_decay_dots() partial sums of exp(b_L) <S, D> to dots.
-cudaError_t zs_launch_decay_rscan(const zs::DecayGeom &g, float *w, const float *states, const float *ds, float *ds0, float *dots,
-                                  bool next, cudaStream_t st, int64_t *launches);
+// The states in front of each span, of the spans' sums u and s0 (NULL: zero): in u's place (parts = 0), or in `parts` bfloat16 matrices
+// each that add up to them (planes); and the last ones to sn (NULL: not written).
+cudaError_t zs_launch_decay_scan(const zs::DecayGeom &g, float *u, void *planes, int parts, const float *s0, float *sn, bool next,
+                                 cudaStream_t st, int64_t *launches);
+// Their gradients after each span in the same forms (parts = 0 or 3, as the states have), of the sums w and ds (NULL: zero), the first
+// ones' to ds0 (NULL: not written); and per span and head zs_decay_dots() partial sums of exp(b_L) <S, D> to dots.
+cudaError_t zs_launch_decay_rscan(const zs::DecayGeom &g, float *w, void *planes, int parts, const float *states, const void *splanes,
+                                  const float *ds, float *ds0, float *dots, bool next, cudaStream_t st, int64_t *launches);
 inline bool zs_decay_vec(const zs::DecayGeom &g, const float *s, const float *t) {
     return g.d.dk * (int64_t)g.d.dv % 4 == 0 && (((uintptr_t)s | (uintptr_t)t) & 15) == 0;
 }
@@ -119,6 +119,12 @@ inline int zs_decay_dots(const zs::DecayGeom &g, const float *ds, const float *d
 }
 
 cudaError_t zs_launch_decay_rows(int type, const zs::DecayGeom &g, const zs::DecayProduct &p, bool next, cudaStream_t st, int64_t *launches);
+// The same for bfloat16 on the 5th-generation tensor cores (decay_tc.cu): dv a multiple of 8; x of at most 128 columns; spans of whole
+// 128 tokens; and p.m `parts` bfloat16 matrices a state.  status: a word that a bounded wait sets when it gives up.
+cudaError_t zs_launch_decay_sums_tc(const zs::DecayGeom &g, const zs::DecayRows &x, const zs::DecayRows &y, bool query, bool gates, float *out,
+                                    unsigned *status, bool next, cudaStream_t st, int64_t *launches);
+cudaError_t zs_launch_decay_rows_tc(const zs::DecayGeom &g, const zs::DecayProduct &p, int parts, int num_sms, unsigned *status, bool next,
+                                    cudaStream_t st, int64_t *launches);
 // dg from the sums of both directions and the dots: tokens x hv, or where each head has one decay (ldg = 0) per span in `parts`
 // (spans x hv) and then in dg (hv).
 cudaError_t zs_launch_decay_dg(const zs::DecayGeom &g, const float *const from_q[2], const float *const from_k[2], const float *dots,

@@ -84,7 +84,7 @@ k_decay_rows(const DecayGeom geo, const DecayProduct p, const DecayRows self) {
         for (int i = tid; i < n; i += kThreads) sm.b[i] = geo.gates[slot * geo.span + i];
         if (SELF && r == 0) load_tile<T, CB, kThreads>(sm.self, at(self, hv, i0), self.ld, rows, self.dist);
         // ---------------------------------------------------- the state's share
-        const float *M = p.m + slot * geo.d.dk * geo.d.dv;
+        const float *M = (const float *)p.m + slot * geo.d.dk * geo.d.dv;
         float share[SELF ? NB : 1][4] = {};
         float(&s)[SELF ? NB : NB][4] = *reinterpret_cast<float(*)[NB][4]>(SELF ? &share[0][0] : &acc[0][0]);
 #pragma unroll 1

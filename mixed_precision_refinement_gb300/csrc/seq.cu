@@ -266,12 +266,28 @@ struct DecayWork {
     float *u = nullptr, *w = nullptr, *dots = nullptr, *parts = nullptr, *sums[4] = {};
     void *copy[4] = {};  // packed q, k, v and dout, where needed
     int ndots = 0;
+    int nparts = 0;      // bfloat16 matrices of a state, where the kernels of decay_tc.cu take them (else 0)
+    void *uplanes = nullptr, *wplanes = nullptr;
     zs::DecayRows q{}, k{}, v{}, dout{};
+
+    const void *states() const { return nparts ? uplanes : u; }
+    const void *dstates() const { return nparts ? wplanes : w; }
+    cudaError_t sums_of(zsolve_seq *s, const zsolve_decay_args *a, const zs::DecayGeom &g, const zs::DecayRows &x, const zs::DecayRows &y,
+                        bool query, bool first_sums, float *out) const {
+        return nparts ? zs_launch_decay_sums_tc(g, x, y, query, first_sums, out, s->d_status, true, s->st, &s->launches)
+                      : zs_launch_decay_sums(a->type, g, x, y, query, first_sums, out, true, s->st, &s->launches);
+    }
+    cudaError_t rows_of(zsolve_seq *s, const zsolve_decay_args *a, const zs::DecayGeom &g, const zs::DecayProduct &p) const {
+        return nparts ? zs_launch_decay_rows_tc(g, p, nparts, s->num_sms, s->d_status, true, s->st, &s->launches)
+                      : zs_launch_decay_rows(a->type, g, p, true, s->st, &s->launches);
+    }
 
     // Copies of rows that 16-byte loads cannot address, and the tables; dout NULL: the forward pass.
     int place(zsolve_seq *s, const zsolve_decay_args *a, zs::DecayGeom *g, const void *dout_p, int64_t lddo, bool backward, const float *ds,
               const float *ds0) {
         g->span = 256;
+        const bool tc = a->type == ZSOLVE_BF16 && a->dv % 8 == 0 && (!backward || a->dv <= 128);
+        nparts = !tc ? 0 : backward ? 3 : 2;
         const int64_t most = a->tokens / g->span + a->nseq;
         if (most > 0x7fffffff / zs::kSpanMost) return seq_fail(s, ZSOLVE_EINVAL, "too many spans");
         // and an unused entry, whose blocks write what belongs to the tokens outside the offsets
@@ -287,10 +303,12 @@ struct DecayWork {
             chunk = c.take<int2>((size_t)g->d.nchunks);
             gates = c.take<float2>(slots * g->span);
             u = c.take<float>(slots * state);
+            uplanes = nparts ? c.take<uint16_t>(slots * nparts * state) : nullptr;
             for (int i = 0; i < (backward ? 4 : 3); i++)
                 copy[i] = zs::mult16(src[i], ld[i], cols[i], e) ? nullptr : c.take<char>((size_t)a->tokens * heads[i] * dist[i] * e);
             if (!backward) return c.at;
             w = c.take<float>(slots * state);
+            wplanes = nparts ? c.take<uint16_t>(slots * nparts * state) : nullptr;
             dots = c.take<float>(slots * ndots);
             parts = a->ldg ? nullptr : c.take<float>((size_t)g->d.nchunks * a->hv);
             for (float *&x : sums) x = c.take<float>((size_t)a->tokens * a->hv);
@@ -577,10 +595,9 @@ int zsolve_decay(zsolve_seq *s, const zsolve_decay_args *a, void *o, int64_t ldo
     DecayWork w;
     st = w.place(s, a, &g, nullptr, 0, false, nullptr, nullptr);
     if (st != ZSOLVE_OK) return st;
-    SEQ_CU(zs_launch_decay_sums(a->type, g, w.k, w.v, false, true, w.u, true, s->st, &s->launches));
-    SEQ_CU(zs_launch_decay_scan(g, w.u, a->s0, sn, true, s->st, &s->launches));
-    const zs::DecayProduct p{w.q, w.k, w.v, w.u, false, false, o, ldo, a->hv, nullptr, {nullptr, nullptr}};
-    SEQ_CU(zs_launch_decay_rows(a->type, g, p, true, s->st, &s->launches));
+    SEQ_CU(w.sums_of(s, a, g, w.k, w.v, false, true, w.u));
+    SEQ_CU(zs_launch_decay_scan(g, w.u, w.uplanes, w.nparts, a->s0, sn, true, s->st, &s->launches));
+    SEQ_CU(w.rows_of(s, a, g, {w.q, w.k, w.v, w.states(), false, false, o, ldo, a->hv, nullptr, {nullptr, nullptr}}));
     return ZSOLVE_OK;
 }
 
@@ -618,17 +635,14 @@ int zsolve_decay_bwd(zsolve_seq *s, const zsolve_decay_args *a, const void *dout
     DecayWork w;
     st = w.place(s, a, &g, dout, lddo, true, ds, ds0);
     if (st != ZSOLVE_OK) return st;
-    SEQ_CU(zs_launch_decay_sums(a->type, g, w.k, w.v, false, true, w.u, true, s->st, &s->launches));
-    SEQ_CU(zs_launch_decay_sums(a->type, g, w.q, w.dout, true, false, w.w, true, s->st, &s->launches));
-    SEQ_CU(zs_launch_decay_scan(g, w.u, a->s0, nullptr, true, s->st, &s->launches));
-    SEQ_CU(zs_launch_decay_rscan(g, w.w, w.u, ds, ds0, w.dots, true, s->st, &s->launches));
+    SEQ_CU(w.sums_of(s, a, g, w.k, w.v, false, true, w.u));
+    SEQ_CU(w.sums_of(s, a, g, w.q, w.dout, true, false, w.w));
+    SEQ_CU(zs_launch_decay_scan(g, w.u, w.uplanes, w.nparts, a->s0, nullptr, true, s->st, &s->launches));
+    SEQ_CU(zs_launch_decay_rscan(g, w.w, w.wplanes, w.nparts, w.u, w.uplanes, ds, ds0, w.dots, true, s->st, &s->launches));
     const int64_t rk = (int64_t)a->hk * a->dk, rv = (int64_t)a->hv * a->dv;
-    const zs::DecayProduct pq{w.dout, w.v, w.k, w.u, true, false, dq, rk, a->hk, &w.q, {w.sums[0], w.sums[1]}};
-    const zs::DecayProduct pk{w.v, w.dout, w.q, w.w, true, true, dk, rk, a->hk, &w.k, {w.sums[2], w.sums[3]}};
-    const zs::DecayProduct pv{w.k, w.q, w.dout, w.w, false, true, dv, rv, a->hv, nullptr, {nullptr, nullptr}};
-    SEQ_CU(zs_launch_decay_rows(a->type, g, pq, true, s->st, &s->launches));
-    SEQ_CU(zs_launch_decay_rows(a->type, g, pk, true, s->st, &s->launches));
-    SEQ_CU(zs_launch_decay_rows(a->type, g, pv, true, s->st, &s->launches));
+    SEQ_CU(w.rows_of(s, a, g, {w.dout, w.v, w.k, w.states(), true, false, dq, rk, a->hk, &w.q, {w.sums[0], w.sums[1]}}));
+    SEQ_CU(w.rows_of(s, a, g, {w.v, w.dout, w.q, w.dstates(), true, true, dk, rk, a->hk, &w.k, {w.sums[2], w.sums[3]}}));
+    SEQ_CU(w.rows_of(s, a, g, {w.k, w.q, w.dout, w.dstates(), false, true, dv, rv, a->hv, nullptr, {nullptr, nullptr}}));
     const float *const from_q[2] = {w.sums[0], w.sums[1]}, *const from_k[2] = {w.sums[2], w.sums[3]};
     SEQ_CU(zs_launch_decay_dg(g, from_q, from_k, w.dots, w.ndots, w.parts, dg, s->st, &s->launches));
     return ZSOLVE_OK;

@@ -128,7 +128,7 @@ def test_float32_accuracy(seq, n, hk, hv, dk, dv, dtype):
     x["s0"] *= 0.2
     exact, (oe, se) = _grads(x, dout, ds, 0.6), (t.detach() for t in _all_pairs(x, 0.6))
     group = hv // hk
-    y = {i: t if i == "offsets" else t.float().requires_grad_() for i, t in x.items()}
+    y = {i: t if i == "offsets" else t.float().clone().requires_grad_() for i, t in x.items()}
     q, k = (y[i].repeat_interleave(group, 1).transpose(0, 1) for i in ("q", "k"))
     v, b = y["v"].transpose(0, 1), y["g"].T.cumsum(1)
     d = (b[:, :, None] - b[:, None, :]).masked_fill(torch.ones(n, n, device="cuda", dtype=torch.bool).triu(1), -float("inf"))

@@ -48,13 +48,17 @@ k_decay_sums(const DecayGeom geo, const DecayRows x, const DecayRows y, int quer
         cp_commit();
     };
     fetch(0);
-    if (warp == 0) decay_sums(geo, sp, hv, sm.b);
+    decay_loads(geo, sp, hv, sm.b, tid, NT);
+    __syncthreads();
+    if (warp == 0) decay_sums(sp, sm.b);
     __syncthreads();
     const float2 last = sm.b[sp.y - 1];
     for (int i = tid; i < chunks * kChunk; i += NT)
         sm.w[i] = i >= sp.y ? 0.f : query ? geo.d.scale * decay_exp(sm.b[i], make_float2(0.f, 0.f)) : decay_exp(last, sm.b[i]);
-    if (gates && blockIdx.z == 0)
+    if (gates && blockIdx.z == 0) {
         for (int i = tid; i < sp.y; i += NT) geo.gates[((int64_t)span * geo.d.hv + hv) * geo.span + i] = sm.b[i];
+        if (tid == 0) geo.ends[(int64_t)span * geo.d.hv + hv] = decay_exp(last, make_float2(0.f, 0.f));
+    }
     constexpr int WN = NB / 64;  // warps side by side
     const int d0 = warp / WN * 32, v0 = warp % WN * 64;
     float acc[2][8][4] = {};
@@ -103,63 +107,61 @@ k_decay_sums(const DecayGeom geo, const DecayRows x, const DecayRows y, int quer
 // ---------------------------------------------------------------- the recurrence over the spans
 
 constexpr int kScanThreads = 256;
-constexpr int kAhead = 4;  // spans whose sums are on their way
+constexpr int kAhead = 5;  // spans whose sums are on their way
 
-__device__ __forceinline__ float span_decay(const DecayGeom &geo, int span, int hv) {
-    return decay_exp(geo.gates[((int64_t)span * geo.d.hv + hv) * geo.span + geo.d.chunk[span].y - 1], make_float2(0.f, 0.f));
-}
+__device__ __forceinline__ float span_decay(const DecayGeom &geo, int span, int hv) { return geo.ends[(int64_t)span * geo.d.hv + hv]; }
 
 // A state's value as the next kernels take it: float32 in the place of the sum, or PARTS bfloat16 values that add up
 // to it (16 or 24 bits), each part a matrix of its own.
 template <int VE, int PARTS>
 struct StatePut {
     __device__ __forceinline__ static void put(float *u, bf16 *planes, int64_t slot, int size, int at, const float (&s)[VE]) {
-        if (PARTS == 0) {
+        if constexpr (PARTS == 0) {
             Vec<float, VE> v;
             v.set(s);
             v.store(u + slot * size + at);
-            return;
-        }
-        float f[VE];
+        } else {
+            float f[VE];
 #pragma unroll
-        for (int e = 0; e < VE; e++) f[e] = s[e];
-        bf16 *p = planes + slot * PARTS * size + at;
+            for (int e = 0; e < VE; e++) f[e] = s[e];
+            bf16 *p = planes + slot * PARTS * size + at;
 #pragma unroll
-        for (int i = 0; i < PARTS; i++, p += size) {
-            Vec<bf16, VE> v;
-            v.set(f);
-            v.store(p);
-            float g[VE];
-            v.get(g);
+            for (int i = 0; i < PARTS; i++, p += size) {
+                Vec<bf16, VE> v;
+                v.set(f);
+                v.store(p);
+                float g[VE];
+                v.get(g);
 #pragma unroll
-            for (int e = 0; e < VE; e++) f[e] -= g[e];
+                for (int e = 0; e < VE; e++) f[e] -= g[e];
+            }
         }
     }
     __device__ __forceinline__ static void get(const float *u, const bf16 *planes, int64_t slot, int size, int at, float (&s)[VE]) {
-        if (PARTS == 0) {
+        if constexpr (PARTS == 0) {
             Vec<float, VE> v;
             v.load(u + slot * size + at);
             v.get(s);
-            return;
-        }
-        const bf16 *p = planes + slot * PARTS * size + at;
+        } else {
+            const bf16 *p = planes + slot * PARTS * size + at;
 #pragma unroll
-        for (int e = 0; e < VE; e++) s[e] = 0.f;
+            for (int e = 0; e < VE; e++) s[e] = 0.f;
 #pragma unroll
-        for (int i = 0; i < PARTS; i++) {
-            Vec<bf16, VE> v;
-            v.load(p + (int64_t)(PARTS - 1 - i) * size);
-            float g[VE];
-            v.get(g);
+            for (int i = 0; i < PARTS; i++) {
+                Vec<bf16, VE> v;
+                v.load(p + (int64_t)(PARTS - 1 - i) * size);
+                float g[VE];
+                v.get(g);
 #pragma unroll
-            for (int e = 0; e < VE; e++) s[e] += g[e];
+                for (int e = 0; e < VE; e++) s[e] += g[e];
+            }
         }
     }
 };
 
 // A thread VE neighbouring values of a state.
 template <int VE, int PARTS>
-__global__ void __launch_bounds__(kScanThreads)
+__global__ void __launch_bounds__(kScanThreads, 4)
 k_decay_scan(const DecayGeom geo, float *u, bf16 *planes, const float *s0, float *sn) {
     after_previous();
     may_start_next();
@@ -170,20 +172,24 @@ k_decay_scan(const DecayGeom geo, float *u, bf16 *planes, const float *s0, float
     float s[VE] = {};
     Vec<float, VE> v;
     if (s0) v.load(s0 + (int64_t)blockIdx.x * size + at), v.get(s);
-    for (int i = 0; i < n; i += kAhead) {
-        Vec<float, VE> w[kAhead];
-        float a[kAhead];
+    Vec<float, VE> w[kAhead];
+    float a[kAhead];
+    auto fetch = [&](int k, int i) {
+        if (i < n) w[k].load(u + ((int64_t)(first + i) * geo.d.hv + hv) * size + at), a[k] = span_decay(geo, first + i, hv);
+    };
 #pragma unroll
-        for (int k = 0; k < kAhead; k++)
-            if (i + k < n) w[k].load(u + ((int64_t)(first + i + k) * geo.d.hv + hv) * size + at), a[k] = span_decay(geo, first + i + k, hv);
+    for (int k = 0; k < kAhead; k++) fetch(k, k);
+    for (int i = 0; i < n; i += kAhead) {
 #pragma unroll
         for (int k = 0; k < kAhead; k++) {
             if (i + k >= n) break;
             float f[VE];
             w[k].get(f);
+            const float ak = a[k];
+            fetch(k, i + k + kAhead);
             StatePut<VE, PARTS>::put(u, planes, (int64_t)(first + i + k) * geo.d.hv + hv, size, at, s);
 #pragma unroll
-            for (int e = 0; e < VE; e++) s[e] = fmaf(a[k], s[e], f[e]);
+            for (int e = 0; e < VE; e++) s[e] = fmaf(ak, s[e], f[e]);
         }
     }
     if (sn) v.set(s), v.store(sn + (int64_t)blockIdx.x * size + at);
@@ -191,7 +197,7 @@ k_decay_scan(const DecayGeom geo, float *u, bf16 *planes, const float *s0, float
 
 // PARTS: of the states and of their gradients.
 template <int VE, int PARTS>
-__global__ void __launch_bounds__(kScanThreads)
+__global__ void __launch_bounds__(kScanThreads, 3)
 k_decay_rscan(const DecayGeom geo, float *w, bf16 *planes, const float *__restrict__ states, const bf16 *__restrict__ splanes, const float *ds,
               float *ds0, float *__restrict__ dots) {
     after_previous();
@@ -204,29 +210,33 @@ k_decay_rscan(const DecayGeom geo, float *w, bf16 *planes, const float *__restri
     Vec<float, VE> v;
     if (ds && in) v.load(ds + (int64_t)blockIdx.x * size + at), v.get(s);
     const int warps = kScanThreads / 32, parts = gridDim.y * warps;
-    for (int i = n - 1; i >= 0; i -= kAhead) {
-        Vec<float, VE> x[kAhead];
-        float y[kAhead][VE], a[kAhead];
+    Vec<float, VE> x[kAhead];
+    float y[kAhead][VE], a[kAhead];
+    auto fetch = [&](int k, int i) {
+        if (i < 0) return;
+        const int64_t slot = (int64_t)(first + i) * geo.d.hv + hv;
+        if (in) x[k].load(w + slot * size + at), StatePut<VE, PARTS>::get(states, splanes, slot, size, at, y[k]);
+        a[k] = span_decay(geo, first + i, hv);
+    };
 #pragma unroll
-        for (int k = 0; k < kAhead; k++)
-            if (i - k >= 0) {
-                const int64_t slot = (int64_t)(first + i - k) * geo.d.hv + hv;
-                if (in) x[k].load(w + slot * size + at), StatePut<VE, PARTS>::get(states, splanes, slot, size, at, y[k]);
-                a[k] = span_decay(geo, first + i - k, hv);
-            }
+    for (int k = 0; k < kAhead; k++) fetch(k, n - 1 - k);
+    for (int i = n - 1; i >= 0; i -= kAhead) {
 #pragma unroll
         for (int k = 0; k < kAhead; k++) {
             if (i - k < 0) break;
             const int64_t slot = (int64_t)(first + i - k) * geo.d.hv + hv;
-            float dot = 0.f;
+            float dot = 0.f, f[VE], q[VE];
+            const float ak = a[k];
+#pragma unroll
+            for (int e = 0; e < VE; e++) q[e] = y[k][e];
+            x[k].get(f);
+            fetch(k, i - k - kAhead);
             if (in) {
-                float f[VE];
-                x[k].get(f);
                 StatePut<VE, PARTS>::put(w, planes, slot, size, at, s);
 #pragma unroll
-                for (int e = 0; e < VE; e++) dot = fmaf(y[k][e], s[e], dot), s[e] = fmaf(a[k], s[e], f[e]);
+                for (int e = 0; e < VE; e++) dot = fmaf(q[e], s[e], dot), s[e] = fmaf(ak, s[e], f[e]);
             }
-            dot = warp_sum(dot) * a[k];
+            dot = warp_sum(dot) * ak;
             if ((threadIdx.x & 31) == 0) dots[slot * parts + blockIdx.y * warps + (threadIdx.x >> 5)] = dot;
         }
     }
@@ -241,63 +251,76 @@ struct DecayDots {
     int parts;
 };
 
-// A warp a span and head: within the span the sums over the tokens after and before t.
-__global__ void __launch_bounds__(128)
+// A block a span and eight heads: a thread has a thirty-second of the span's tokens of a head.  Within the span the sums
+// over the tokens after and before t; float32, in pieces of at most 16 tokens and 32 pieces.
+constexpr int kDgHeads = 8, kDgPieces = 32, kDgTokens = kSpanMost / kDgPieces;
+__global__ void __launch_bounds__(kDgHeads * kDgPieces)
 k_decay_dg(const DecayGeom geo, const DecayDots in, float *__restrict__ parts, float *__restrict__ dg) {
+    __shared__ float s_later[kDgPieces + 1][kDgHeads], s_before[kDgPieces + 1][kDgHeads], s_z[kDgHeads];
     after_previous();
     may_start_next();
-    const int lane = threadIdx.x & 31, hv = (int)blockIdx.y * 4 + (threadIdx.x >> 5), span = blockIdx.x;
-    if (hv >= geo.d.hv) return;
+    const int h = threadIdx.x % kDgHeads, piece = threadIdx.x / kDgHeads, hv = (int)blockIdx.y * kDgHeads + h, span = blockIdx.x;
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const bool live = hv < geo.d.hv;
     const int2 sp = geo.d.chunk[span];
     if (sp.y == 0) {
         if (parts) {
-            if (lane == 0) parts[(int64_t)span * geo.d.hv + hv] = 0.f;
-        } else {
-            tokens_outside(geo.d, span, [&](int64_t t0, int64_t t1, int worker, int workers) {
-                // a warp here is a head: the block's four share no tokens
-                const int blocks = workers / 4, block = worker / 4;
-                for (int64_t t = t0 + block * 32 + lane; t < t1; t += blocks * 32) dg[t * geo.d.hv + hv] = 0.f;
-            });
+            if (live && piece == 0) parts[(int64_t)span * geo.d.hv + hv] = 0.f;
+        } else if (live) {
+            const int used = geo.d.first[geo.d.nseq], workers = (geo.d.nchunks - used) * kDgPieces, worker = (span - used) * kDgPieces + piece;
+            const int2 last = geo.d.seq[geo.d.nseq - 1];
+            for (int64_t t = worker; t < geo.d.seq[0].x; t += workers) dg[t * geo.d.hv + hv] = 0.f;
+            for (int64_t t = (int64_t)last.x + last.y + worker; t < geo.d.tokens; t += workers) dg[t * geo.d.hv + hv] = 0.f;
         }
         return;
     }
-    double z = 0.0;
-    const float *d = in.dots + ((int64_t)span * geo.d.hv + hv) * in.parts;
-    for (int i = lane; i < in.parts; i += 32) z += (double)d[i];
-    const int per = (sp.y + 31) / 32, i0 = lane * per, i1 = min(i0 + per, sp.y);
-    auto at = [&](int i) { return (int64_t)(sp.x + i) * geo.d.hv + hv; };
-    double later = 0.0, before = 0.0;  // the lane's tokens' sums
-    for (int i = i0; i < i1; i++) {
-        later += (double)in.xq[at(i)] + ((double)in.rq[at(i)] - (double)in.rk[at(i)]);
-        before += (double)in.xk[at(i)];
+    // exp(b_L) <S, D>: a warp a head
+    {
+        const int head = (int)blockIdx.y * kDgHeads + warp;
+        float z = 0.f;
+        if (head < geo.d.hv)
+            for (int i = lane; i < in.parts; i += 32) z += in.dots[((int64_t)span * geo.d.hv + head) * in.parts + i];
+        z = warp_sum(z);
+        if (lane == 0) s_z[warp] = z;
     }
-    double all = later, sum = before;
+    const int per = (sp.y + kDgPieces - 1) / kDgPieces, i0 = min(piece * per, sp.y), i1 = min(i0 + per, sp.y);
+    float own[kDgTokens], key[kDgTokens], later = 0.f, before = 0.f;
 #pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-        z += __shfl_xor_sync(0xffffffffu, z, o);
-        const double u = __shfl_down_sync(0xffffffffu, all, o), v = __shfl_up_sync(0xffffffffu, sum, o);
-        if (lane + o < 32) all += u;
-        if (lane >= o) sum += v;
+    for (int k = 0; k < kDgTokens; k++) {
+        own[k] = key[k] = 0.f;
+        if (live && i0 + k < i1) {
+            const int64_t at = (int64_t)(sp.x + i0 + k) * geo.d.hv + hv;
+            own[k] = in.xq[at] + (in.rq[at] - in.rk[at]);
+            key[k] = in.xk[at];
+        }
     }
-    // of the lanes after and before this one: their own sums, so that nothing is subtracted
-    double tail = __shfl_down_sync(0xffffffffu, all, 1), head = __shfl_up_sync(0xffffffffu, sum, 1);
-    if (lane == 31) tail = 0.0;
-    if (lane == 0) head = 0.0;
-    double total = 0.0;
-    for (int i = i1 - 1; i >= i0; i--) {
-        tail += (double)in.xq[at(i)] + ((double)in.rq[at(i)] - (double)in.rk[at(i)]);
-        double h = head;
-        for (int j = i0; j < i; j++) h += (double)in.xk[at(j)];
-        const double v = tail + h + z;
-        if (parts)
-            total += v;
-        else
-            dg[at(i)] = (float)v;
+#pragma unroll
+    for (int k = 0; k < kDgTokens; k++) later += own[kDgTokens - 1 - k], before += key[k];
+    s_later[piece][h] = later, s_before[piece][h] = before;
+    __syncthreads();
+    float tail = 0.f, head = 0.f;  // of the pieces after and before this one
+    for (int w = kDgPieces - 1; w > piece; w--) tail += s_later[w][h];
+    for (int w = 0; w < piece; w++) head += s_before[w][h];
+    const float z = s_z[h];
+    float total = 0.f, v[kDgTokens];
+#pragma unroll
+    for (int k = kDgTokens - 1; k >= 0; k--) tail += own[k], v[k] = tail;
+#pragma unroll
+    for (int k = 0; k < kDgTokens; k++) {
+        if (live && i0 + k < i1) {
+            v[k] += head + z;
+            total += v[k];
+            if (!parts) dg[(int64_t)(sp.x + i0 + k) * geo.d.hv + hv] = v[k];
+        }
+        head += key[k];
     }
     if (!parts) return;
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) total += __shfl_xor_sync(0xffffffffu, total, o);
-    if (lane == 0) parts[(int64_t)span * geo.d.hv + hv] = (float)total;
+    __syncthreads();
+    s_later[piece][h] = total;
+    __syncthreads();
+    if (piece || !live) return;
+    for (int w = 1; w < kDgPieces; w++) total += s_later[w][h];
+    parts[(int64_t)span * geo.d.hv + hv] = total;
 }
 
 // One decay a head: the spans' parts, a warp a head.
@@ -306,11 +329,10 @@ k_decay_dg_heads(const float *__restrict__ parts, int spans, int hv, float *__re
     after_previous();
     const int lane = threadIdx.x & 31, h = (int)blockIdx.x * 4 + (threadIdx.x >> 5);
     if (h >= hv) return;
-    double s = 0.0;
-    for (int i = lane; i < spans; i += 32) s += (double)parts[(int64_t)i * hv + h];
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
-    if (lane == 0) dg[h] = (float)s;
+    float s = 0.f;
+    for (int i = lane; i < spans; i += 32) s += parts[(int64_t)i * hv + h];
+    s = warp_sum(s);
+    if (lane == 0) dg[h] = s;
 }
 
 // ---------------------------------------------------------------- host
@@ -373,7 +395,7 @@ cudaError_t zs_launch_decay_dg(const DecayGeom &g, const float *const from_q[2],
                                int ndots, float *parts, float *dg, cudaStream_t st, int64_t *launches) {
     const DecayDots in{from_q[0], from_q[1], from_k[0], from_k[1], dots, ndots};
     ++*launches;
-    const cudaError_t e = launch(true, k_decay_dg, dim3(g.d.nchunks, (g.d.hv + 3) / 4), 128, 0, st, g, in, g.ldg ? (float *)nullptr : parts, dg);
+    const cudaError_t e = launch(true, k_decay_dg, dim3(g.d.nchunks, (g.d.hv + kDgHeads - 1) / kDgHeads), kDgHeads * kDgPieces, 0, st, g, in, g.ldg ? (float *)nullptr : parts, dg);
     if (e != cudaSuccess || g.ldg) return e;
     ++*launches;
     return launch(true, k_decay_dg_heads, (unsigned)((g.d.hv + 3) / 4), 128, 0, st, parts, g.d.nchunks, g.d.hv, dg);

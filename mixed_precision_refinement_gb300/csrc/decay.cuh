@@ -34,6 +34,7 @@ struct DecayGeom {
     int64_t ldg;        // tokens' distance in g: hv, or 0 where each head has one
     int span;           // tokens of a span, at most
     float2 *gates;      // per span and head `span` values: b_i / ln 2 in two floats
+    float *ends;        // per span and head: exp(b_L)
 };
 
 // The state's or the score's rows: a tensor tokens x heads x cols.
@@ -64,34 +65,39 @@ struct DecayProduct {
 // exp(b - c) of two sums in two floats each (in units of ln 2).
 __device__ __forceinline__ float decay_exp(float2 b, float2 c) { return exp2f((b.x - c.x) + (b.y - c.y)); }
 
-// One warp: the sums b_i of a span's tokens into `b`, in float64 (few additions), kept as two floats, so
-// that their differences keep their digits after a strong decay.  exp(-1e4) is 0, and finite
-// sums leave no inf - inf.
-__device__ __forceinline__ void decay_sums(const DecayGeom &geo, int2 sp, int hv, float2 *b) {
-    const int lane = threadIdx.x & 31;
-    const int per = (sp.y + 31) / 32, i0 = lane * per;
-    double s = 0.0;
-    for (int i = i0; i < min(i0 + per, sp.y); i++) {
+// The sums b_i of a span's tokens into `b`, in units of ln 2 and in two floats, so that their differences keep their digits
+// after a strong decay (float64 would do, but its additions are many times slower here).  exp(-1e4) is 0, and finite
+// sums leave no inf - inf.  First the log decays by all of the block's `threads` threads (thread t of them), and then, once
+// those are there, one warp the sums.
+__device__ __forceinline__ void decay_loads(const DecayGeom &geo, int2 sp, int hv, float2 *b, int t, int threads) {
+    for (int i = t; i < sp.y; i += threads) {
         float g = geo.d.g[(int64_t)(sp.x + i) * geo.ldg + hv];
         if (g < -1e4f) g = -1e4f;
-        s += (double)g;
+        // 1 / ln 2 in two floats
+        const float hi = g * 1.44269502f;
+        b[i] = make_float2(hi, fmaf(g, 1.44269502f, -hi) + g * 1.92596299e-8f);
     }
-    double before = s;
+}
+// a + b of two floats each: the large parts' sum and its own rounding error exactly (Knuth), the small parts with it.
+__device__ __forceinline__ float2 decay_add(float2 a, float2 b) {
+    const float s = a.x + b.x, t = s - a.x, e = (a.x - (s - t)) + (b.x - t) + (a.y + b.y);
+    const float hi = s + e;
+    return make_float2(hi, e - (hi - s));
+}
+__device__ __forceinline__ void decay_sums(int2 sp, float2 *b) {
+    const int lane = threadIdx.x & 31;
+    const int per = (sp.y + 31) / 32, i0 = lane * per, i1 = min(i0 + per, sp.y);
+    float2 s = make_float2(0.f, 0.f);
+    for (int i = i0; i < i1; i++) s = decay_add(s, b[i]);
+    float2 before = s;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
-        const double v = __shfl_up_sync(0xffffffffu, before, o);
-        if (lane >= o) before += v;
+        const float2 v = make_float2(__shfl_up_sync(0xffffffffu, before.x, o), __shfl_up_sync(0xffffffffu, before.y, o));
+        if (lane >= o) before = decay_add(v, before);
     }
-    before = __shfl_up_sync(0xffffffffu, before, 1);
-    if (lane == 0) before = 0.0;
-    for (int i = i0; i < min(i0 + per, sp.y); i++) {
-        float g = geo.d.g[(int64_t)(sp.x + i) * geo.ldg + hv];
-        if (g < -1e4f) g = -1e4f;
-        before += (double)g;
-        const double x = before * 1.4426950408889634;
-        const float hi = (float)x;
-        b[i] = make_float2(hi, (float)(x - (double)hi));
-    }
+    before = make_float2(__shfl_up_sync(0xffffffffu, before.x, 1), __shfl_up_sync(0xffffffffu, before.y, 1));
+    if (lane == 0) before = make_float2(0.f, 0.f);
+    for (int i = i0; i < i1; i++) b[i] = before = decay_add(before, b[i]);
 }
 
 }  // namespace zs

@@ -263,6 +263,7 @@ struct DecayWork {
     int *first = nullptr;
     int2 *seq = nullptr, *chunk = nullptr;
     float2 *gates = nullptr;
+    float *ends = nullptr;
     float *u = nullptr, *w = nullptr, *dots = nullptr, *parts = nullptr, *sums[4] = {};
     void *copy[4] = {};  // packed q, k, v and dout, where needed
     int ndots = 0;
@@ -302,6 +303,7 @@ struct DecayWork {
             seq = c.take<int2>((size_t)a->nseq);
             chunk = c.take<int2>((size_t)g->d.nchunks);
             gates = c.take<float2>(slots * g->span);
+            ends = c.take<float>(slots);
             u = c.take<float>(slots * state);
             uplanes = nparts ? c.take<uint16_t>(slots * nparts * state) : nullptr;
             for (int i = 0; i < (backward ? 4 : 3); i++)
@@ -331,6 +333,7 @@ struct DecayWork {
         g->d.seq = seq;
         g->d.chunk = chunk;
         g->gates = gates;
+        g->ends = ends;
         SEQ_CU(zs_launch_delta_plan(a->offsets, a->nseq, a->tokens, g->span, g->d.nchunks, first, seq, chunk, s->st, &s->launches));
         return ZSOLVE_OK;
     }

@@ -274,6 +274,31 @@ struct ResBack {
 // thread has read it.  A thread holds 8 values of a row (16 where the row has more than 4096) and its columns' four sums; the
 // weights lie in shared memory.  A row need not start on 16 bytes (the tensors do): the copy takes the
 // whole 16 bytes that begin in it, and the last values are read directly.
+template <int N>
+struct Count {
+    static constexpr int value = N;
+};
+// Sums over the block of v[k], N rows' at once; `red`: N slots a warp, which the next sums may not use.
+template <int TPR, int N>
+__device__ __forceinline__ void row_sums(float2 (&v)[N], float2 *red) {
+#pragma unroll
+    for (int k = 0; k < N; k++) v[k].x = warp_sum(v[k].x), v[k].y = warp_sum(v[k].y);
+    if (TPR == 32) return;
+    constexpr int NW = TPR / 32;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    if (lane == 0)
+#pragma unroll
+        for (int k = 0; k < N; k++) red[k * NW + warp] = v[k];
+    __syncthreads();
+#pragma unroll
+    for (int k = 0; k < N; k++) {
+        const float2 *r = red + k * NW;
+        float2 t = r[0], u = NW > 1 ? r[1] : make_float2(0.f, 0.f);
+#pragma unroll
+        for (int w = 2; w < NW; w += 2) t = add2(r[w], t), u = w + 1 < NW ? add2(r[w + 1], u) : u;
+        v[k] = add2(t, u);
+    }
+}
 constexpr int ring_blocks(int tpr) {  // of an SM, as far as the registers go
     return std::max(1, 65536 / (tpr * 128));
 }
@@ -282,7 +307,7 @@ __global__ void __launch_bounds__(TPR, ring_blocks(TPR))
 k_resnorm_bwd(const ResBack p, const ResGeom g, int stages, float *__restrict__ parts, unsigned *__restrict__ status) {
     extern __shared__ __align__(16) uint8_t smem_raw[];
     constexpr int kMost = 8;
-    __shared__ float2 red[2 * (TPR < 64 ? 2 : TPR / 32)];
+    __shared__ float2 red[4 * (TPR / 32)];
     __shared__ __align__(8) uint64_t full[kMost];
     __shared__ volatile int s_abort;
     may_start_next();
@@ -345,151 +370,207 @@ k_resnorm_bwd(const ResBack p, const ResGeom g, int stages, float *__restrict__ 
     float2 aq[NP], ar[NP], aw[NP], ab[NP];
 #pragma unroll
     for (int i = 0; i < NP; i++) aq[i] = ar[i] = aw[i] = ab[i] = make_float2(0.f, 0.f);
-    float st[4] = {0.f, 1.f, 0.f, 1.f}, later[4] = {0.f, 1.f, 0.f, 1.f};
-#pragma unroll
-    for (int i = 0; i < 4; i++) {
-        if (row0 < row1) st[i] = p.stats[4 * row0 + i];
-        if (row0 + 1 < row1) later[i] = p.stats[4 * (row0 + 1) + i];
-    }
     // the value i of the thread: columns are VE together, so i and i + 1 (i even) are a pair of them
     auto column = [&](int i) { return VE > 1 ? ((i / VE) * TPR + t) * VE + i % VE : i * TPR + t; };
-    int it = 0;
-    for (int64_t row = row0; row < row1; row++, it++) {
-        const float mu1 = st[0], rs1 = st[1], mu2 = st[2], rs2 = st[3];
+    auto pair = [](const float *f, int j) { return make_float2(f[2 * j], f[2 * j + 1]); };
+    auto put = [](float *f, int j, float2 v) { f[2 * j] = v.x, f[2 * j + 1] = v.y; };
+    auto weight = [&](int k, int c, float *f) { load_ws<T, VE>(ws[k], g.wf32, c, f); };
+    // the statistics of the next rows and of those after them
+    constexpr int R = E > 8 ? 1 : 2;
+    const int step = R == 2 && stages >= 4 ? 2 : 1;
+    float st[R][4], later[R][4];
+    auto stats_of = [&](float (&to)[R][4], int64_t row) {
 #pragma unroll
-        for (int i = 0; i < 4; i++) {
-            st[i] = later[i];
-            if (row + 2 < row1) later[i] = load_early(p.stats + 4 * (row + 2) + i);
+        for (int k = 0; k < R; k++)
+            if (row + k < row1)
+#pragma unroll
+                for (int i = 0; i < 4; i++) to[k][i] = load_early(p.stats + 4 * (row + k) + i);
+    };
+    stats_of(st, row0), stats_of(later, row0 + step);
+    int it = 0;
+    // N rows from `row` on, side by side
+    auto rows = [&](auto count, int64_t row) {
+        constexpr int N = decltype(count)::value;
+        float mu1[N], rs1[N], mu2[N], rs2[N];
+        const T *from[N][5];
+        int rest[N][5];  // values of the row that were copied
+#pragma unroll
+        for (int k = 0; k < N; k++) {
+            mu1[k] = st[k][0], rs1[k] = st[k][1], mu2[k] = st[k][2], rs2[k] = st[k][3];
+            const int slot = (it + k) % stages;
+#pragma unroll
+            for (int i = 0; i < 5; i++) {
+                const int off = offset((row + k) * lds[i]);
+                from[k][i] = slot_of(slot, i) + off;
+                rest[k][i] = whole(off) - off;
+            }
         }
-        const int slot = it % stages;
-        bar_wait(&full[slot], (it / stages) & 1, &s_abort, status);
-        // VE values from column c on of tensor k: zeros beyond the row
-        auto read = [&](int k, int c, float *f) {
-            const int64_t at = row * lds[k];
-            const int off = offset(at);
-            const T *s = slot_of(slot, k) + off;
+#pragma unroll
+        for (int k = 0; k < R; k++)
+#pragma unroll
+            for (int i = 0; i < 4; i++) st[k][i] = later[k][i];
+        stats_of(later, row + 2 * step);
+#pragma unroll
+        for (int k = 0; k < N; k++) bar_wait(&full[(it + k) % stages], ((it + k) / stages) & 1, &s_abort, status);
+        // VE values from column c on of tensor i
+        auto read = [&](int k, int i, int c, float *f) {
             if (VE > 1) {  // whole 16 bytes: all of them copied
                 Vec<T, VE> u;
-                u.load(s + c);
+                u.load(from[k][i] + c);
                 u.get(f);
             } else {
-                f[0] = to_f32(c < whole(off) - off ? s[c] : src[k][at + c]);
+                f[0] = to_f32(c < rest[k][i] ? from[k][i][c] : src[i][(row + k) * lds[i] + c]);
             }
         };
-        auto weight = [&](int k, int c, float *f) { load_ws<T, VE>(ws[k], g.wf32, c, f); };
-        float h[E], a[E];
-        float2 sx = make_float2(0.f, 0.f), sy = sx;
-        const float2 r2 = make_float2(rs2, rs2), nm2 = make_float2(-mu2, -mu2);
+        float h[N][E], a[N][E], w[E];
 #pragma unroll
-        for (int i = 0; i < E; i++) h[i] = a[i] = 0.f;
+        for (int k = 0; k < N; k++)
+#pragma unroll
+            for (int i = 0; i < E; i++) h[k][i] = a[k][i] = 0.f;
 #pragma unroll
         for (int i = 0; i < E; i += VE) {
             const int c = column(i);
-            if (c < d) {
-                read(1, c, h + i);
-                read(0, c, a + i);
-            }
+            if (c < d)
+#pragma unroll
+                for (int k = 0; k < N; k++) read(k, 1, c, h[k] + i), read(k, 0, c, a[k] + i);
         }
-        auto pair = [](float *f, int j) { return make_float2(f[2 * j], f[2 * j + 1]); };
-        auto put = [](float *f, int j, float2 v) { f[2 * j] = v.x, f[2 * j + 1] = v.y; };
-        float w[E];
 #pragma unroll
         for (int i = 0; i < E; i++) w[i] = 1.f;
         if (ws[3])
 #pragma unroll
             for (int i = 0; i < E; i += VE)
                 if (column(i) < d) weight(3, column(i), w + i);
+        float2 s[N];
 #pragma unroll
-        for (int j = 0; j < NP; j++) {
-            const float2 v = pair(a, j);
-            // values beyond the row: a = 0, and their h counts for nothing
-            const float2 hj = mul2(add2(pair(h, j), nm2), r2);
-            put(h, j, hj);
-            aw[j] = fma2(v, hj, aw[j]);
-            ab[j] = add2(v, ab[j]);
-            const float2 x = mul2(v, pair(w, j));
-            put(a, j, x);
-            sx = add2(x, sx);
-            sy = fma2(x, hj, sy);
+        for (int k = 0; k < N; k++) {
+            const float2 r2 = make_float2(rs2[k], rs2[k]), nm2 = make_float2(-mu2[k], -mu2[k]);
+            float2 sx = make_float2(0.f, 0.f), sy = sx;
+#pragma unroll
+            for (int j = 0; j < NP; j++) {
+                const float2 v = pair(a[k], j);
+                // values beyond the row: a = 0, and their h counts for nothing
+                const float2 hj = mul2(add2(pair(h[k], j), nm2), r2);
+                put(h[k], j, hj);
+                aw[j] = fma2(v, hj, aw[j]);
+                ab[j] = add2(v, ab[j]);
+                const float2 x = mul2(v, pair(w, j));
+                put(a[k], j, x);
+                sx = add2(x, sx);
+                sy = fma2(x, hj, sy);
+            }
+            s[k] = make_float2(sx.x + sx.y, sy.x + sy.y);
         }
-        float2 s = row_sum<TPR>(make_float2(sx.x + sx.y, sy.x + sy.y), red, 0);
-        const float m1 = g.rms ? 0.f : -rs2 * s.x * inv, m2 = -rs2 * s.y * inv;
+        row_sums<TPR, N>(s, red);
 #pragma unroll
-        for (int j = 0; j < NP; j++)  // dx but for dy
-            put(a, j, fma2(pair(h, j), make_float2(m2, m2), fma2(pair(a, j), r2, make_float2(m1, m1))));
+        for (int k = 0; k < N; k++) {
+            const float m1 = g.rms ? 0.f : -rs2[k] * s[k].x * inv, m2 = -rs2[k] * s[k].y * inv;
+            const float2 r2 = make_float2(rs2[k], rs2[k]);
+#pragma unroll
+            for (int j = 0; j < NP; j++)  // dx but for dy
+                put(a[k], j, fma2(pair(h[k], j), make_float2(m2, m2), fma2(pair(a[k], j), r2, make_float2(m1, m1))));
+        }
         if (p.dy)
 #pragma unroll
             for (int i = 0; i < E; i += VE) {
                 const int c = column(i);
-                float f[VE];
-                if (c < d) {
-                    read(3, c, f);
+                if (c < d)
 #pragma unroll
-                    for (int e = 0; e < VE; e++) a[i + e] += f[e];
-                }
+                    for (int k = 0; k < N; k++) {
+                        float f[VE];
+                        read(k, 3, c, f);
+#pragma unroll
+                        for (int e = 0; e < VE; e++) a[k][i + e] += f[e];
+                    }
             }
-        sx = sy = make_float2(0.f, 0.f);
         // a VE's worth at a time: dx out, then the branch's gradients
 #pragma unroll
         for (int i = 0; i < E; i += VE) {
             const int c = column(i);
             if (c >= d) {
 #pragma unroll
-                for (int e = 0; e < VE; e++) a[i + e] = h[i + e] = 0.f;
+                for (int k = 0; k < N; k++)
+#pragma unroll
+                    for (int e = 0; e < VE; e++) a[k][i + e] = h[k][i + e] = 0.f;
                 continue;
             }
-            Vec<T, VE> out;
-            out.set(a + i);
-            out.store((T *)p.dx + row * p.lddx + c);
-            float o[VE], w1[VE], tt[VE], cc[VE], act[VE], slope[VE], u[VE];
-            read(2, c, o);
+            float w1[VE], b1[VE], cc[VE], act[N * VE], slope[N * VE], z[N * VE];
 #pragma unroll
-            for (int e = 0; e < VE; e++) o[e] = (o[e] - mu1) * rs1, w1[e] = cc[e] = act[e] = 1.f, tt[e] = 0.f;
+            for (int e = 0; e < VE; e++) w1[e] = cc[e] = 1.f, b1[e] = 0.f;
+#pragma unroll
+            for (int e = 0; e < N * VE; e++) act[e] = 1.f;
             if (ws[0]) weight(0, c, w1);
-            if (ws[1]) weight(1, c, tt);
+            if (ws[1]) weight(1, c, b1);
             if (ws[2]) weight(2, c, cc);
             if (p.z) {
-                read(4, c, u);
-                slopes_all(u, g.act, act, slope);
+#pragma unroll
+                for (int k = 0; k < N; k++) read(k, 4, c, z + k * VE);
+                slopes_all(z, g.act, act, slope);
             }
 #pragma unroll
-            for (int e = 0; e < VE; e++) {
-                tt[e] = fmaf(o[e], w1[e], tt[e]);
-                u[e] = a[i + e] * act[e];
-                if (p.z) slope[e] *= a[i + e] * cc[e] * tt[e];
-                a[i + e] = u[e] * cc[e] * w1[e];
-                h[i + e] = o[e];
-            }
-            if (p.dz) {
-                out.set(slope);
-                out.store((T *)p.dz + row * p.lddz + c);
-            }
+            for (int k = 0; k < N; k++) {
+                Vec<T, VE> out;
+                out.set(a[k] + i);
+                out.store((T *)p.dx + (row + k) * p.lddx + c);
+                float o[VE], u[VE];
+                read(k, 2, c, o);
 #pragma unroll
-            for (int e = 0; e < VE; e++) {
-                float &q = (i + e) & 1 ? aq[(i + e) / 2].y : aq[(i + e) / 2].x, &r = (i + e) & 1 ? ar[(i + e) / 2].y : ar[(i + e) / 2].x;
-                q = fmaf(u[e], o[e], q);
-                r += u[e];
+                for (int e = 0; e < VE; e++) {
+                    float &v = a[k][i + e];
+                    o[e] = (o[e] - mu1[k]) * rs1[k];
+                    u[e] = v * act[k * VE + e];
+                    if (p.z) slope[k * VE + e] *= v * cc[e] * fmaf(o[e], w1[e], b1[e]);
+                    v = u[e] * cc[e] * w1[e];
+                    h[k][i + e] = o[e];
+                }
+                if (p.dz) {
+                    out.set(slope + k * VE);
+                    out.store((T *)p.dz + (row + k) * p.lddz + c);
+                }
+#pragma unroll
+                for (int e = 0; e < VE; e++) {
+                    float &q = (i + e) & 1 ? aq[(i + e) / 2].y : aq[(i + e) / 2].x, &r = (i + e) & 1 ? ar[(i + e) / 2].y : ar[(i + e) / 2].x;
+                    q = fmaf(u[e], o[e], q);
+                    r += u[e];
+                }
             }
         }
 #pragma unroll
-        for (int j = 0; j < NP; j++) sx = add2(pair(a, j), sx), sy = fma2(pair(a, j), pair(h, j), sy);
-        s = row_sum<TPR>(make_float2(sx.x + sx.y, sy.x + sy.y), red, 1);
-        if (TPR == 32) __syncwarp();
-        if (t == 0 && row + stages < row1) issue(row + stages, slot);
-        const float k1 = g.after && !g.rms ? -rs1 * s.x * inv : 0.f, k2 = g.after ? -rs1 * s.y * inv : 0.f;
+        for (int k = 0; k < N; k++) {
+            float2 sx = make_float2(0.f, 0.f), sy = sx;
 #pragma unroll
-        for (int j = 0; j < NP; j++)
-            put(a, j, fma2(pair(h, j), make_float2(k2, k2), fma2(pair(a, j), make_float2(rs1, rs1), make_float2(k1, k1))));
+            for (int j = 0; j < NP; j++) sx = add2(pair(a[k], j), sx), sy = fma2(pair(a[k], j), pair(h[k], j), sy);
+            s[k] = make_float2(sx.x + sx.y, sy.x + sy.y);
+        }
+        row_sums<TPR, N>(s, red + N * (TPR / 32));
+        if (TPR == 32) __syncwarp();
+        if (t == 0)
+#pragma unroll
+            for (int k = 0; k < N; k++)
+                if (row + k + stages < row1) issue(row + k + stages, (it + k) % stages);
+#pragma unroll
+        for (int k = 0; k < N; k++) {
+            const float k1 = g.after && !g.rms ? -rs1[k] * s[k].x * inv : 0.f, k2 = g.after ? -rs1[k] * s[k].y * inv : 0.f;
+#pragma unroll
+            for (int j = 0; j < NP; j++)
+                put(a[k], j, fma2(pair(h[k], j), make_float2(k2, k2), fma2(pair(a[k], j), make_float2(rs1[k], rs1[k]), make_float2(k1, k1))));
+        }
 #pragma unroll
         for (int i = 0; i < E; i += VE) {
             const int c = column(i);
-            if (c < d) {
-                Vec<T, VE> out;
-                out.set(a + i);
-                out.store((T *)p.dout + row * p.lddo + c);
-            }
+            if (c < d)
+#pragma unroll
+                for (int k = 0; k < N; k++) {
+                    Vec<T, VE> out;
+                    out.set(a[k] + i);
+                    out.store((T *)p.dout + (row + k) * p.lddo + c);
+                }
         }
-    }
+        it += N;
+    };
+    int64_t row = row0;
+    if (step == 2)
+        for (; row + 1 < row1; row += 2) rows(Count<R>(), row);
+    for (; row < row1; row++) rows(Count<1>(), row);
     if (t == 0 && s_abort) bar_drain(full, stages, it);
     if (!parts) return;
     float *q = parts + (int64_t)blockIdx.x * 4 * d;

@@ -46,27 +46,83 @@ __device__ __forceinline__ Stat stat_of(float2 s, float inv, float eps, int rms)
     return r;
 }
 
+// Two values at a time.  In both directions the instructions count as much as the bytes: a value of a row takes the share of a
+// pair of each of its own, so they are held to pairs (packed float32) wherever neither memory nor the gate is concerned.
+__device__ __forceinline__ float2 both(float v) { return make_float2(v, v); }
+__device__ __forceinline__ float2 pair(const float *f, int j) { return make_float2(f[2 * j], f[2 * j + 1]); }
+__device__ __forceinline__ void put(float *f, int j, float2 v) { f[2 * j] = v.x, f[2 * j + 1] = v.y; }
+// f(j): each j of N / 2 pairs; g(e): the value left over
+template <int N, typename F, typename G>
+__device__ __forceinline__ void pairs(F f, G g) {
+#pragma unroll
+    for (int j = 0; j < N / 2; j++) f(j);
+    if (N % 2) g(N - 1);
+}
 template <int N>
-__device__ __forceinline__ void slopes_all(const float (&z)[N], int act, float (&a)[N], float (&s)[N]) {
-#define RES_CASE(A)                                                                                  \
-    case A: {                                                                                        \
-        _Pragma("unroll") for (int i = 0; i < N; i++) a[i] = act1<A>(z[i]), s[i] = slope1<A>(z[i]); \
-        break;                                                                                       \
+__device__ __forceinline__ void times(float *a, const float *b) {
+    pairs<N>([&](int j) { put(a, j, mul2(pair(a, j), pair(b, j))); }, [&](int e) { a[e] *= b[e]; });
+}
+template <int N>
+__device__ __forceinline__ void plus(float *a, const float *b) {
+    pairs<N>([&](int j) { put(a, j, add2(pair(a, j), pair(b, j))); }, [&](int e) { a[e] += b[e]; });
+}
+// a = a s + b for two numbers s and b
+template <int N>
+__device__ __forceinline__ void scale_shift(float *a, float s, float b) {
+    pairs<N>([&](int j) { put(a, j, fma2(pair(a, j), both(s), both(b))); }, [&](int e) { a[e] = fmaf(a[e], s, b); });
+}
+
+// The gate and, with SLOPE, its slope.  silu z = z p with p = 1 / (1 + exp(-z)), silu' z = p + silu z (1 - p): one exponential and one
+// reciprocal serve both.
+__device__ __forceinline__ float2 logistic(float2 z) {
+    const float2 t = mul2(z, both(-1.4426950408889634f));
+    float2 p;
+    asm("ex2.approx.f32 %0, %1;" : "=f"(p.x) : "f"(t.x));
+    asm("ex2.approx.f32 %0, %1;" : "=f"(p.y) : "f"(t.y));
+    p = add2(p, both(1.f));
+    asm("rcp.approx.f32 %0, %1;" : "=f"(p.x) : "f"(p.x));
+    asm("rcp.approx.f32 %0, %1;" : "=f"(p.y) : "f"(p.y));
+    return p;
+}
+template <bool SLOPE, int N>
+__device__ __forceinline__ void gates_all(const float (&z)[N], int act, float (&a)[N], float (&s)[N]) {
+#define RES_CASE(A)                                        \
+    case A: {                                              \
+        _Pragma("unroll") for (int i = 0; i < N; i++) {    \
+            a[i] = act1<A>(z[i]);                          \
+            if (SLOPE) s[i] = slope1<A>(z[i]);             \
+        }                                                  \
+        break;                                             \
     }
     switch (act) {
         RES_CASE(ACT_NONE)
         RES_CASE(ACT_RELU)
-        RES_CASE(ACT_SILU)
         RES_CASE(ACT_GELU)
         RES_CASE(ACT_GELU_TANH)
+        case ACT_SILU: {
+#pragma unroll
+            for (int i = 0; i < N; i += 2) {
+                const bool two = i + 1 < N;
+                const float2 v = make_float2(z[i], two ? z[i + 1 < N ? i + 1 : i] : 0.f), p = logistic(v), x = mul2(v, p);
+                const float2 g = fma2(x, fma2(p, both(-1.f), both(1.f)), p);
+                a[i] = x.x;
+                if (SLOPE) s[i] = g.x;
+                if (two) {
+                    a[i + 1 < N ? i + 1 : i] = x.y;
+                    if (SLOPE) s[i + 1 < N ? i + 1 : i] = g.y;
+                }
+            }
+            break;
+        }
     }
 #undef RES_CASE
 }
 
 // Forward: TPR threads hold a row, VE consecutive values at a time (VE = 1 where rows are not
-// 16-byte aligned), NI times; four rows a block where a warp holds one, else a row a block.
+// 16-byte aligned), NI times; four rows a block where a warp holds one, else a row a block.  Sixteen values a thread: the sums over the
+// threads are then a small part of the instructions, and two thirds of an SM's threads have their row in flight.
 template <typename T, int VE, int TPR, int NI>
-__global__ void __launch_bounds__(TPR < 128 ? 128 : TPR)
+__global__ void __launch_bounds__(TPR < 128 ? 128 : TPR, TPR < 128 ? 8 : 1024 / TPR)
 k_resnorm(const T *x, int64_t ldx, const T *__restrict__ o, int64_t ldo, const T *__restrict__ z, int64_t ldz, const ResGeom g,
           T *y, int64_t ldy, T *__restrict__ h, int64_t ldh, float *__restrict__ stats) {
     __shared__ float2 red[TPR == 32 ? 1 : 2 * (TPR / 32)];
@@ -86,11 +142,11 @@ k_resnorm(const T *x, int64_t ldx, const T *__restrict__ o, int64_t ldo, const T
     }
     const float inv = 1.f / (float)d;
     float v[NI * VE];
-    auto each = [&](auto f) {  // f(i, c): the thread's pieces of the row
+    auto each = [&](auto f) {  // f(i, c, values): the thread's pieces of the row
 #pragma unroll
         for (int i = 0; i < NI; i++) {
             const int c = (i * TPR + t) * VE;
-            if (c < d) f(i, c);
+            if (c < d) f(i, c, v + i * VE);
         }
     };
     int flip = 0;
@@ -99,67 +155,52 @@ k_resnorm(const T *x, int64_t ldx, const T *__restrict__ o, int64_t ldo, const T
         float2 s = make_float2(0.f, 0.f);
         mu = 0.f;
         if (!g.rms) {
-            each([&](int i, int) {
-#pragma unroll
-                for (int e = 0; e < VE; e++) s.x += v[i * VE + e];
-            });
-            mu = row_sum<TPR>(s, red, flip).x * inv;
+            each([&](int, int, float *a) { pairs<VE>([&](int j) { s = add2(s, pair(a, j)); }, [&](int e) { s.x += a[e]; }); });
+            mu = row_sum<TPR>(make_float2(s.x + s.y, 0.f), red, flip).x * inv;
             flip ^= 1;
-            s = make_float2(0.f, 0.f);
         }
-        each([&](int i, int) {
-#pragma unroll
-            for (int e = 0; e < VE; e++) {
-                float &w = v[i * VE + e];
-                w -= mu;
-                s.x = fmaf(w, w, s.x);
-                s.y += w;
-            }
+        float2 q = make_float2(0.f, 0.f);
+        s = q;
+        each([&](int, int, float *a) {
+            scale_shift<VE>(a, 1.f, -mu);
+            pairs<VE>([&](int j) { q = fma2(pair(a, j), pair(a, j), q), s = add2(s, pair(a, j)); },
+                      [&](int e) { q.x = fmaf(a[e], a[e], q.x), s.x += a[e]; });
         });
-        s = row_sum<TPR>(s, red, flip);
+        s = row_sum<TPR>(make_float2(q.x + q.y, s.x + s.y), red, flip);
         flip ^= 1;
         return stat_of(s, inv, g.eps, g.rms);
     };
-    each([&](int i, int) { uo[i].get(v + i * VE); });
+    each([&](int i, int, float *a) { uo[i].get(a); });
     float mu1 = 0.f, mu2;
     Stat s1 = {1.f, 0.f};
     if (g.after) s1 = standard(mu1);
     const float shift1 = -s1.off * s1.rs;
-    each([&](int i, int c) {
-        float f[VE], a[VE];
-#pragma unroll
-        for (int e = 0; e < VE; e++) a[e] = g.after ? fmaf(v[i * VE + e], s1.rs, shift1) : v[i * VE + e];
+    each([&](int i, int c, float *a) {
+        float f[VE], w[VE];
+        if (g.after) scale_shift<VE>(a, s1.rs, shift1);
         if (g.w1) {
             load_wv<T, VE>(g.w1, g.wf32, c, f);
-#pragma unroll
-            for (int e = 0; e < VE; e++) a[e] *= f[e];
+            times<VE>(a, f);
         }
         if (g.b1) {
             load_wv<T, VE>(g.b1, g.wf32, c, f);
-#pragma unroll
-            for (int e = 0; e < VE; e++) a[e] += f[e];
+            plus<VE>(a, f);
         }
         if (z) {
+            float r[VE];
             uz[i].get(f);
-            act_all(f, g.act);
-#pragma unroll
-            for (int e = 0; e < VE; e++) a[e] *= f[e];
+            gates_all<false>(f, g.act, r, r);
+            times<VE>(a, r);
         }
-        float w[VE];
-        ux[i].get(w);
         if (g.c) {
             load_wv<T, VE>(g.c, g.wf32, c, f);
-#pragma unroll
-            for (int e = 0; e < VE; e++) w[e] = fmaf(f[e], a[e], w[e]);
-        } else {
-#pragma unroll
-            for (int e = 0; e < VE; e++) w[e] += a[e];
+            times<VE>(a, f);
         }
+        ux[i].get(w);
+        plus<VE>(a, w);
         Vec<T, VE> r;
-        r.set(w);
+        r.set(a);
         r.store(y + row * ldy + c);
-#pragma unroll
-        for (int e = 0; e < VE; e++) v[i * VE + e] = w[e];
     });
     const Stat s2 = standard(mu2);
     const float shift2 = -s2.off * s2.rs;
@@ -167,19 +208,16 @@ k_resnorm(const T *x, int64_t ldx, const T *__restrict__ o, int64_t ldo, const T
         float *p = stats + 4 * row;
         p[0] = mu1 + s1.off, p[1] = s1.rs, p[2] = mu2 + s2.off, p[3] = s2.rs;
     }
-    each([&](int i, int c) {
-        float a[VE], f[VE];
-#pragma unroll
-        for (int e = 0; e < VE; e++) a[e] = fmaf(v[i * VE + e], s2.rs, shift2);
+    each([&](int, int c, float *a) {
+        float f[VE];
+        scale_shift<VE>(a, s2.rs, shift2);
         if (g.w2) {
             load_wv<T, VE>(g.w2, g.wf32, c, f);
-#pragma unroll
-            for (int e = 0; e < VE; e++) a[e] *= f[e];
+            times<VE>(a, f);
         }
         if (g.b2) {
             load_wv<T, VE>(g.b2, g.wf32, c, f);
-#pragma unroll
-            for (int e = 0; e < VE; e++) a[e] += f[e];
+            plus<VE>(a, f);
         }
         Vec<T, VE> r;
         r.set(a);
@@ -278,26 +316,34 @@ template <int N>
 struct Count {
     static constexpr int value = N;
 };
-// Sums over the block of v[k], N rows' at once; `red`: N slots a warp, which the next sums may not use.
+// Sums over the block of v[k], N rows' at once; `red`: N slots a warp, which the next sums may not use.  A shuffle moves two values
+// that are still to be added up: lanes that differ in its bit keep one of them each.
 template <int TPR, int N>
 __device__ __forceinline__ void row_sums(float2 (&v)[N], float2 *red) {
-#pragma unroll
-    for (int k = 0; k < N; k++) v[k].x = warp_sum(v[k].x), v[k].y = warp_sum(v[k].y);
-    if (TPR == 32) return;
-    constexpr int NW = TPR / 32;
+    constexpr int NW = TPR / 32, V = 2 * N;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    if (lane == 0)
+    auto fold = [&](float a, float b, int o) {  // of a pair of lanes the lower has the sum of a's, the upper that of b's
+        const bool up = lane & o;
+        return (up ? b : a) + __shfl_xor_sync(0xffffffffu, up ? a : b, o);
+    };
+    float x = N == 1 ? fold(v[0].x, v[0].y, 16) : fold(fold(v[0].x, v[N - 1].x, 16), fold(v[0].y, v[N - 1].y, 16), 8);
 #pragma unroll
-        for (int k = 0; k < N; k++) red[k * NW + warp] = v[k];
+    for (int o = N == 1 ? 8 : 4; o > 0; o >>= 1) x += __shfl_xor_sync(0xffffffffu, x, o);
+    // value lane * V / 32: of row k its x, then its y
+    if (TPR == 32) {
+#pragma unroll
+        for (int k = 0; k < N; k++) v[k] = make_float2(__shfl_sync(0xffffffffu, x, 32 / N * k), __shfl_sync(0xffffffffu, x, 32 / N * k + 32 / V));
+        return;
+    }
+    float *to = reinterpret_cast<float *>(red);
+    if (lane % (32 / V) == 0) to[warp * V + lane / (32 / V)] = x;
     __syncthreads();
 #pragma unroll
-    for (int k = 0; k < N; k++) {
-        const float2 *r = red + k * NW;
-        float2 t = r[0], u = NW > 1 ? r[1] : make_float2(0.f, 0.f);
+    for (int k = 0; k < N; k++) v[k] = red[k];
 #pragma unroll
-        for (int w = 2; w < NW; w += 2) t = add2(r[w], t), u = w + 1 < NW ? add2(r[w + 1], u) : u;
-        v[k] = add2(t, u);
-    }
+    for (int w = 1; w < NW; w++)
+#pragma unroll
+        for (int k = 0; k < N; k++) v[k] = add2(v[k], red[w * N + k]);
 }
 constexpr int ring_blocks(int tpr) {  // of an SM, as far as the registers go
     return std::max(1, 65536 / (tpr * 128));
@@ -372,8 +418,6 @@ k_resnorm_bwd(const ResBack p, const ResGeom g, int stages, float *__restrict__ 
     for (int i = 0; i < NP; i++) aq[i] = ar[i] = aw[i] = ab[i] = make_float2(0.f, 0.f);
     // the value i of the thread: columns are VE together, so i and i + 1 (i even) are a pair of them
     auto column = [&](int i) { return VE > 1 ? ((i / VE) * TPR + t) * VE + i % VE : i * TPR + t; };
-    auto pair = [](const float *f, int j) { return make_float2(f[2 * j], f[2 * j + 1]); };
-    auto put = [](float *f, int j, float2 v) { f[2 * j] = v.x, f[2 * j + 1] = v.y; };
     auto weight = [&](int k, int c, float *f) { load_ws<T, VE>(ws[k], g.wf32, c, f); };
     // the statistics of the next rows and of those after them
     constexpr int R = E > 8 ? 1 : 2;
@@ -478,8 +522,7 @@ k_resnorm_bwd(const ResBack p, const ResGeom g, int stages, float *__restrict__ 
                     for (int k = 0; k < N; k++) {
                         float f[VE];
                         read(k, 3, c, f);
-#pragma unroll
-                        for (int e = 0; e < VE; e++) a[k][i + e] += f[e];
+                        plus<VE>(a[k] + i, f);
                     }
             }
         // a VE's worth at a time: dx out, then the branch's gradients
@@ -504,33 +547,47 @@ k_resnorm_bwd(const ResBack p, const ResGeom g, int stages, float *__restrict__ 
             if (p.z) {
 #pragma unroll
                 for (int k = 0; k < N; k++) read(k, 4, c, z + k * VE);
-                slopes_all(z, g.act, act, slope);
+                gates_all<true>(z, g.act, act, slope);
             }
 #pragma unroll
             for (int k = 0; k < N; k++) {
                 Vec<T, VE> out;
                 out.set(a[k] + i);
                 out.store((T *)p.dx + (row + k) * p.lddx + c);
-                float o[VE], u[VE];
+                float o[VE];
                 read(k, 2, c, o);
+                float *const v = a[k] + i;
+                // of two values v of dx: u = v act(z), dz, the gradient of h1, and the columns' sums
+                auto two = [&](float2 v, float2 o, float2 ac, float2 &sl, float2 w, float2 b, float2 sc, float2 &q, float2 &r) {
+                    const float2 u = mul2(v, ac);
+                    if (p.z) sl = mul2(mul2(sl, mul2(v, sc)), fma2(o, w, b));
+                    q = fma2(u, o, q);
+                    r = add2(u, r);
+                    return mul2(u, mul2(sc, w));
+                };
+                // the mean first: times rs1 it may be large beside h1
+                scale_shift<VE>(o, 1.f, -mu1[k]);
+                scale_shift<VE>(o, rs1[k], 0.f);
+                pairs<VE>(
+                    [&](int j) {
+                        float2 sl = pair(slope + k * VE, j);
+                        put(v, j, two(pair(v, j), pair(o, j), pair(act + k * VE, j), sl, pair(w1, j), pair(b1, j), pair(cc, j), aq[i / 2 + j], ar[i / 2 + j]));
+                        put(slope + k * VE, j, sl);
+                    },
+                    [&](int e) {
+                        float &q = i & 1 ? aq[i / 2].y : aq[i / 2].x, &r = i & 1 ? ar[i / 2].y : ar[i / 2].x;
+                        const float u = v[e] * act[k * VE + e];
+                        if (p.z) slope[k * VE + e] *= v[e] * cc[e] * fmaf(o[e], w1[e], b1[e]);
+                        q = fmaf(u, o[e], q);
+                        r += u;
+                        v[e] = u * cc[e] * w1[e];
+                    });
 #pragma unroll
-                for (int e = 0; e < VE; e++) {
-                    float &v = a[k][i + e];
-                    o[e] = (o[e] - mu1[k]) * rs1[k];
-                    u[e] = v * act[k * VE + e];
-                    if (p.z) slope[k * VE + e] *= v * cc[e] * fmaf(o[e], w1[e], b1[e]);
-                    v = u[e] * cc[e] * w1[e];
-                    h[k][i + e] = o[e];
-                }
+                for (int e = 0; e < VE; e++) h[k][i + e] = o[e];
                 if (p.dz) {
+                    Vec<T, VE> out;
                     out.set(slope + k * VE);
                     out.store((T *)p.dz + (row + k) * p.lddz + c);
-                }
-#pragma unroll
-                for (int e = 0; e < VE; e++) {
-                    float &q = (i + e) & 1 ? aq[(i + e) / 2].y : aq[(i + e) / 2].x, &r = (i + e) & 1 ? ar[(i + e) / 2].y : ar[(i + e) / 2].x;
-                    q = fmaf(u[e], o[e], q);
-                    r += u[e];
                 }
             }
         }
@@ -611,7 +668,7 @@ struct ResGrad {
     __device__ __forceinline__ float scale(int64_t c) const { return g.c ? load_w<T>(g.c, g.wf32, c) : 1.f; }
     __device__ __forceinline__ float2 gate(int64_t c) const {
         float z[1] = {p.z ? to_f32(((const T *)p.z)[row * p.ldz + c]) : 0.f}, a[1] = {1.f}, s[1] = {0.f};
-        if (p.z) slopes_all(z, g.act, a, s);
+        if (p.z) gates_all<true>(z, g.act, a, s);
         return make_float2(a[0], s[0]);
     }
 };
@@ -740,19 +797,19 @@ int fwd(zsolve_seq *s, const zsolve_resnorm_args *a, const void *x, int64_t ldx,
 #define RES_ARGS (const T *)x, ldx, (const T *)a->o, a->ldo, (const T *)a->z, a->ldz, g, (T *)y, ldy, (T *)h, ldh, stats
 #define RES_GO(VE, TPR, E) \
     k_resnorm<T, VE, TPR, (E) / VE><<<(unsigned)((TPR) == 32 ? (a->rows + 3) / 4 : a->rows), (TPR) < 128 ? 128 : (TPR), 0, s->st>>>(RES_ARGS)
-#define RES_SIZES(VE)                         \
-    if (d <= 256) RES_GO(VE, 32, 8);          \
-    else if (d <= 1024) RES_GO(VE, 128, 8);   \
-    else if (d <= 2048) RES_GO(VE, 256, 8);   \
-    else if (d <= 4096) RES_GO(VE, 512, 8);   \
-    else if (d <= 8192) RES_GO(VE, 1024, 8);  \
+#define RES_SIZES(VE, E)                        \
+    if (d <= 256) RES_GO(VE, 32, 8);            \
+    else if (d <= 128 * E) RES_GO(VE, 128, E);  \
+    else if (d <= 256 * E) RES_GO(VE, 256, E);  \
+    else if (d <= 512 * E) RES_GO(VE, 512, E);  \
+    else if (d <= 1024 * E) RES_GO(VE, 1024, E); \
     else RES_GO(VE, 1024, 16)
     if (d > kMaxRow) {
         k_resnorm_long<T><<<(unsigned)a->rows, kLong, 0, s->st>>>(RES_ARGS);
     } else if (vec) {
-        RES_SIZES(V);
+        RES_SIZES(V, 16);
     } else {
-        RES_SIZES(1);
+        RES_SIZES(1, 8);
     }
 #undef RES_SIZES
 #undef RES_GO

@@ -179,11 +179,11 @@ k_resnorm(const T *x, int64_t ldx, const T *__restrict__ o, int64_t ldo, const T
         float f[VE], w[VE];
         if (g.after) scale_shift<VE>(a, s1.rs, shift1);
         if (g.w1) {
-            load_wv<T, VE>(g.w1, g.wf32, c, f);
+            load_ws<T, VE>(g.w1, g.wf32, c, f);
             times<VE>(a, f);
         }
         if (g.b1) {
-            load_wv<T, VE>(g.b1, g.wf32, c, f);
+            load_ws<T, VE>(g.b1, g.wf32, c, f);
             plus<VE>(a, f);
         }
         if (z) {
@@ -193,7 +193,7 @@ k_resnorm(const T *x, int64_t ldx, const T *__restrict__ o, int64_t ldo, const T
             times<VE>(a, r);
         }
         if (g.c) {
-            load_wv<T, VE>(g.c, g.wf32, c, f);
+            load_ws<T, VE>(g.c, g.wf32, c, f);
             times<VE>(a, f);
         }
         ux[i].get(w);
@@ -212,11 +212,11 @@ k_resnorm(const T *x, int64_t ldx, const T *__restrict__ o, int64_t ldo, const T
         float f[VE];
         scale_shift<VE>(a, s2.rs, shift2);
         if (g.w2) {
-            load_wv<T, VE>(g.w2, g.wf32, c, f);
+            load_ws<T, VE>(g.w2, g.wf32, c, f);
             times<VE>(a, f);
         }
         if (g.b2) {
-            load_wv<T, VE>(g.b2, g.wf32, c, f);
+            load_ws<T, VE>(g.b2, g.wf32, c, f);
             plus<VE>(a, f);
         }
         Vec<T, VE> r;
@@ -310,8 +310,8 @@ struct ResBack {
 // A block takes a share of the rows, which arrive in a ring of rows in shared memory, a bulk copy
 // for each of the up to five tensors, issued as soon as the row's second reduction shows that every
 // thread has read it.  A thread holds 8 values of a row (16 where the row has more than 4096) and its columns' four sums; the
-// weights lie in shared memory.  A row need not start on 16 bytes (the tensors do): the copy takes the
-// whole 16 bytes that begin in it, and the last values are read directly.
+// weights lie in shared memory.  A row need not start or end on 16 bytes (the tensors start there): the copy takes what lies around it
+// too, but for a tensor's last values, which the threads put in place.
 template <int N>
 struct Count {
     static constexpr int value = N;
@@ -355,6 +355,7 @@ k_resnorm_bwd(const ResBack p, const ResGeom g, int stages, float *__restrict__ 
     constexpr int kMost = 8;
     __shared__ float2 red[4 * (TPR / 32)];
     __shared__ __align__(8) uint64_t full[kMost];
+    __shared__ __align__(16) float s_stats[kMost][4];
     __shared__ volatile int s_abort;
     may_start_next();
     const int d = g.d, rr = ring_row<T>(d), t = threadIdx.x;
@@ -391,21 +392,28 @@ k_resnorm_bwd(const ResBack p, const ResGeom g, int stages, float *__restrict__ 
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     }
     __syncthreads();
-    auto offset = [&](int64_t at) { return (int)((unsigned)at % A); };
-    auto whole = [&](int off) { return (off + d) / A * A; };
-    auto slot_of = [&](int slot, int k) { return ring + ((size_t)slot * tensors + place[k]) * rr; };
+    auto offset = [&](int64_t at) { return VE > 1 ? 0 : (int)((unsigned)at % A); };
+    // values from the 16 bytes that a row begins in to those that it ends in, or begins to end in where those are the tensor's last
+    auto whole = [&](int64_t row, int k) {
+        if (VE > 1) return d;
+        const int64_t at = row * lds[k];
+        const int off = offset(at), n = (off + d + A - 1) / A * A;
+        return at - off + n <= (g.rows - 1) * lds[k] + d ? n : (off + d) / A * A;
+    };
+    auto slot_of = [&](int slot, int k) { return (slot * tensors + place[k]) * rr; };
     auto issue = [&](int64_t row, int slot) {
-        uint32_t bytes = 0;
+        uint32_t bytes = 16;
 #pragma unroll
         for (int k = 0; k < 5; k++)
-            if (src[k]) bytes += (uint32_t)(whole(offset(row * lds[k])) * sizeof(T));
+            if (src[k]) bytes += (uint32_t)(whole(row, k) * sizeof(T));
         bar_expect(&full[slot], bytes);
+        bulk_load(s_stats[slot], p.stats + 4 * row, 16, &full[slot]);
 #pragma unroll
         for (int k = 0; k < 5; k++) {
             if (!src[k]) continue;
             const int64_t at = row * lds[k];
-            const int off = offset(at), n = whole(off);
-            if (n) bulk_load(slot_of(slot, k), src[k] + (at - off), (uint32_t)(n * sizeof(T)), &full[slot]);
+            const int off = offset(at), n = whole(row, k);
+            if (n) bulk_load(ring + slot_of(slot, k), src[k] + (at - off), (uint32_t)(n * sizeof(T)), &full[slot]);
         }
     };
     const int64_t row0 = g.rows * blockIdx.x / gridDim.x, row1 = g.rows * (blockIdx.x + 1) / gridDim.x;
@@ -418,72 +426,90 @@ k_resnorm_bwd(const ResBack p, const ResGeom g, int stages, float *__restrict__ 
     for (int i = 0; i < NP; i++) aq[i] = ar[i] = aw[i] = ab[i] = make_float2(0.f, 0.f);
     // the value i of the thread: columns are VE together, so i and i + 1 (i even) are a pair of them
     auto column = [&](int i) { return VE > 1 ? ((i / VE) * TPR + t) * VE + i % VE : i * TPR + t; };
-    auto weight = [&](int k, int c, float *f) { load_ws<T, VE>(ws[k], g.wf32, c, f); };
-    // the statistics of the next rows and of those after them
     constexpr int R = E > 8 ? 1 : 2;
     const int step = R == 2 && stages >= 4 ? 2 : 1;
-    float st[R][4], later[R][4];
-    auto stats_of = [&](float (&to)[R][4], int64_t row) {
-#pragma unroll
-        for (int k = 0; k < R; k++)
-            if (row + k < row1)
-#pragma unroll
-                for (int i = 0; i < 4; i++) to[k][i] = load_early(p.stats + 4 * (row + k) + i);
-    };
-    stats_of(st, row0), stats_of(later, row0 + step);
     int it = 0;
     // N rows from `row` on, side by side
     auto rows = [&](auto count, int64_t row) {
         constexpr int N = decltype(count)::value;
         float mu1[N], rs1[N], mu2[N], rs2[N];
-        const T *from[N][5];
-        int rest[N][5];  // values of the row that were copied
+        int from[N][5];  // places in the ring
 #pragma unroll
         for (int k = 0; k < N; k++) {
-            mu1[k] = st[k][0], rs1[k] = st[k][1], mu2[k] = st[k][2], rs2[k] = st[k][3];
             const int slot = (it + k) % stages;
 #pragma unroll
-            for (int i = 0; i < 5; i++) {
-                const int off = offset((row + k) * lds[i]);
-                from[k][i] = slot_of(slot, i) + off;
-                rest[k][i] = whole(off) - off;
-            }
+            for (int i = 0; i < 5; i++) from[k][i] = slot_of(slot, i) + offset((row + k) * lds[i]);
         }
 #pragma unroll
-        for (int k = 0; k < R; k++)
-#pragma unroll
-            for (int i = 0; i < 4; i++) st[k][i] = later[k][i];
-        stats_of(later, row + 2 * step);
-#pragma unroll
         for (int k = 0; k < N; k++) bar_wait(&full[(it + k) % stages], ((it + k) / stages) & 1, &s_abort, status);
-        // VE values from column c on of tensor i
-        auto read = [&](int k, int i, int c, float *f) {
-            if (VE > 1) {  // whole 16 bytes: all of them copied
-                Vec<T, VE> u;
-                u.load(from[k][i] + c);
-                u.get(f);
-            } else {
-                f[0] = to_f32(c < rest[k][i] ? from[k][i][c] : src[i][(row + k) * lds[i] + c]);
+#pragma unroll
+        for (int k = 0; k < N; k++) {
+            const float4 v = *reinterpret_cast<const float4 *>(s_stats[(it + k) % stages]);
+            mu1[k] = v.x, rs1[k] = v.y, mu2[k] = v.z, rs2[k] = v.w;
+        }
+        if (VE == 1 && row + N + A > g.rows) {  // the tensors' last values
+#pragma unroll
+            for (int k = 0; k < N; k++)
+#pragma unroll
+                for (int i = 0; i < 5; i++) {
+                    if (!src[i]) continue;
+                    const int c = whole(row + k, i) - offset((row + k) * lds[i]) + t;
+                    if (t < A && c < d) ring[from[k][i] + c] = src[i][(row + k) * lds[i] + c];
+                }
+            asm volatile("fence.proxy.async.shared::cta;" ::: "memory");  // of their places, before other copies into them
+            __syncthreads();
+        }
+        // The thread's values from i on, G together.  Single columns beyond the row are the row's last, with weights of zero; where a
+        // thread has several of them together, it has none beyond the row.
+        constexpr int G = VE > 1 ? 4 : 2, U = VE > 1 ? 4 : 1;
+        auto inside = [&](int i) { return column(i) < d; };
+        auto any = [&](int i) { return VE == 1 || inside(i); };
+        auto at = [&](int i) { return VE == 1 ? min(column(i), d - 1) : column(i); };
+        auto read = [&](int k, int tensor, int i, float *f) {
+#pragma unroll
+            for (int e = 0; e < G; e += U) {
+                Vec<T, U> u;
+                u.load(ring + from[k][tensor] + at(i + e));
+                u.get(f + e);
             }
+        };
+        auto weight = [&](int k, int i, float *f, float other) {
+#pragma unroll
+            for (int e = 0; e < G; e++) f[e] = other;
+            if (ws[k])
+#pragma unroll
+                for (int e = 0; e < G; e += U) load_ws<T, U>(ws[k], g.wf32, at(i + e), f + e);
+        };
+        auto mask = [&](int i, float *f) {
+            if (VE == 1)
+#pragma unroll
+                for (int e = 0; e < G; e++)
+                    if (!inside(i + e)) f[e] = 0.f;
+        };
+        auto store = [&](void *to, int64_t row, int i, const float *f) {
+#pragma unroll
+            for (int e = 0; e < G; e += U)
+                if (inside(i + e)) {
+                    Vec<T, U> out;
+                    out.set(f + e);
+                    out.store((T *)to + row + column(i + e));
+                }
         };
         float h[N][E], a[N][E], w[E];
 #pragma unroll
-        for (int k = 0; k < N; k++)
+        for (int i = 0; i < E; i += G) {
 #pragma unroll
-            for (int i = 0; i < E; i++) h[k][i] = a[k][i] = 0.f;
+            for (int e = 0; e < G; e++) {
+                w[i + e] = 0.f;
 #pragma unroll
-        for (int i = 0; i < E; i += VE) {
-            const int c = column(i);
-            if (c < d)
+                for (int k = 0; k < N; k++) h[k][i + e] = a[k][i + e] = 0.f;
+            }
+            if (!any(i)) continue;
 #pragma unroll
-                for (int k = 0; k < N; k++) read(k, 1, c, h[k] + i), read(k, 0, c, a[k] + i);
+            for (int k = 0; k < N; k++) read(k, 1, i, h[k] + i), read(k, 0, i, a[k] + i);
+            weight(3, i, w + i, 1.f);
+            mask(i, w + i);
         }
-#pragma unroll
-        for (int i = 0; i < E; i++) w[i] = 1.f;
-        if (ws[3])
-#pragma unroll
-            for (int i = 0; i < E; i += VE)
-                if (column(i) < d) weight(3, column(i), w + i);
         float2 s[N];
 #pragma unroll
         for (int k = 0; k < N; k++) {
@@ -515,80 +541,52 @@ k_resnorm_bwd(const ResBack p, const ResGeom g, int stages, float *__restrict__ 
         }
         if (p.dy)
 #pragma unroll
-            for (int i = 0; i < E; i += VE) {
-                const int c = column(i);
-                if (c < d)
+            for (int i = 0; i < E; i += G)
+                if (any(i))
 #pragma unroll
                     for (int k = 0; k < N; k++) {
-                        float f[VE];
-                        read(k, 3, c, f);
-                        plus<VE>(a[k] + i, f);
+                        float f[G];
+                        read(k, 3, i, f);
+                        plus<G>(a[k] + i, f);
                     }
-            }
-        // a VE's worth at a time: dx out, then the branch's gradients
+        // the branch's gradients; where w1 is 0 beyond the row, the gradient of h1 is
 #pragma unroll
-        for (int i = 0; i < E; i += VE) {
-            const int c = column(i);
-            if (c >= d) {
+        for (int i = 0; i < E; i += G) {
+            if (!any(i)) {
 #pragma unroll
                 for (int k = 0; k < N; k++)
 #pragma unroll
-                    for (int e = 0; e < VE; e++) a[k][i + e] = h[k][i + e] = 0.f;
+                    for (int e = 0; e < G; e++) a[k][i + e] = h[k][i + e] = 0.f;
                 continue;
             }
-            float w1[VE], b1[VE], cc[VE], act[N * VE], slope[N * VE], z[N * VE];
+            float w1[G], b1[G], cc[G], act[N * G], slope[N * G], z[N * G];
+            weight(0, i, w1, 1.f), weight(1, i, b1, 0.f), weight(2, i, cc, 1.f);
+            mask(i, w1);
 #pragma unroll
-            for (int e = 0; e < VE; e++) w1[e] = cc[e] = 1.f, b1[e] = 0.f;
-#pragma unroll
-            for (int e = 0; e < N * VE; e++) act[e] = 1.f;
-            if (ws[0]) weight(0, c, w1);
-            if (ws[1]) weight(1, c, b1);
-            if (ws[2]) weight(2, c, cc);
+            for (int e = 0; e < N * G; e++) act[e] = 1.f, slope[e] = 0.f;
             if (p.z) {
 #pragma unroll
-                for (int k = 0; k < N; k++) read(k, 4, c, z + k * VE);
+                for (int k = 0; k < N; k++) read(k, 4, i, z + k * G);
                 gates_all<true>(z, g.act, act, slope);
             }
 #pragma unroll
             for (int k = 0; k < N; k++) {
-                Vec<T, VE> out;
-                out.set(a[k] + i);
-                out.store((T *)p.dx + (row + k) * p.lddx + c);
-                float o[VE];
-                read(k, 2, c, o);
-                float *const v = a[k] + i;
-                // of two values v of dx: u = v act(z), dz, the gradient of h1, and the columns' sums
-                auto two = [&](float2 v, float2 o, float2 ac, float2 &sl, float2 w, float2 b, float2 sc, float2 &q, float2 &r) {
-                    const float2 u = mul2(v, ac);
-                    if (p.z) sl = mul2(mul2(sl, mul2(v, sc)), fma2(o, w, b));
-                    q = fma2(u, o, q);
-                    r = add2(u, r);
-                    return mul2(u, mul2(sc, w));
-                };
-                // the mean first: times rs1 it may be large beside h1
-                scale_shift<VE>(o, 1.f, -mu1[k]);
-                scale_shift<VE>(o, rs1[k], 0.f);
-                pairs<VE>(
-                    [&](int j) {
-                        float2 sl = pair(slope + k * VE, j);
-                        put(v, j, two(pair(v, j), pair(o, j), pair(act + k * VE, j), sl, pair(w1, j), pair(b1, j), pair(cc, j), aq[i / 2 + j], ar[i / 2 + j]));
-                        put(slope + k * VE, j, sl);
-                    },
-                    [&](int e) {
-                        float &q = i & 1 ? aq[i / 2].y : aq[i / 2].x, &r = i & 1 ? ar[i / 2].y : ar[i / 2].x;
-                        const float u = v[e] * act[k * VE + e];
-                        if (p.z) slope[k * VE + e] *= v[e] * cc[e] * fmaf(o[e], w1[e], b1[e]);
-                        q = fmaf(u, o[e], q);
-                        r += u;
-                        v[e] = u * cc[e] * w1[e];
-                    });
+                store(p.dx, (row + k) * p.lddx, i, a[k] + i);
+                float o[G];
+                read(k, 2, i, o);
+                float *const sl = slope + k * G;
 #pragma unroll
-                for (int e = 0; e < VE; e++) h[k][i + e] = o[e];
-                if (p.dz) {
-                    Vec<T, VE> out;
-                    out.set(slope + k * VE);
-                    out.store((T *)p.dz + (row + k) * p.lddz + c);
+                for (int j = 0; j < G / 2; j++) {
+                    // the mean first: times rs1 it may be large beside h1
+                    const float2 v = pair(a[k] + i, j), hj = mul2(add2(pair(o, j), both(-mu1[k])), both(rs1[k]));
+                    const float2 u = mul2(v, pair(act + k * G, j)), wj = pair(w1, j), cj = pair(cc, j);
+                    if (p.z) put(sl, j, mul2(mul2(pair(sl, j), mul2(v, cj)), fma2(hj, wj, pair(b1, j))));
+                    float2 &q = aq[i / 2 + j], &r = ar[i / 2 + j];
+                    q = fma2(u, hj, q);
+                    r = add2(u, r);
+                    put(a[k] + i, j, mul2(u, mul2(cj, wj))), put(h[k] + i, j, hj);
                 }
+                if (p.dz) store(p.dz, (row + k) * p.lddz, i, sl);
             }
         }
 #pragma unroll
@@ -612,16 +610,9 @@ k_resnorm_bwd(const ResBack p, const ResGeom g, int stages, float *__restrict__ 
                 put(a[k], j, fma2(pair(h[k], j), make_float2(k2, k2), fma2(pair(a[k], j), make_float2(rs1[k], rs1[k]), make_float2(k1, k1))));
         }
 #pragma unroll
-        for (int i = 0; i < E; i += VE) {
-            const int c = column(i);
-            if (c < d)
+        for (int k = 0; k < N; k++)
 #pragma unroll
-                for (int k = 0; k < N; k++) {
-                    Vec<T, VE> out;
-                    out.set(a[k] + i);
-                    out.store((T *)p.dout + (row + k) * p.lddo + c);
-                }
-        }
+            for (int i = 0; i < E; i += G) store(p.dout, (row + k) * p.lddo, i, a[k] + i);
         it += N;
     };
     int64_t row = row0;
@@ -791,8 +782,7 @@ int fwd(zsolve_seq *s, const zsolve_resnorm_args *a, const void *x, int64_t ldx,
     const ResGeom g = geom_of(a);
     const int64_t d = a->d;
     const bool vec = d % V == 0 && ldx % V == 0 && a->ldo % V == 0 && (!a->z || a->ldz % V == 0) && ldy % V == 0 && ldh % V == 0 &&
-                     aligned16(x) && aligned16(a->o) && aligned16(a->z) && aligned16(y) && aligned16(h) &&
-                     (a->wtype == ZSOLVE_F32 || weights_aligned(a));
+                     aligned16(x) && aligned16(a->o) && aligned16(a->z) && aligned16(y) && aligned16(h) && weights_aligned(a);
     s->launches++;
 #define RES_ARGS (const T *)x, ldx, (const T *)a->o, a->ldo, (const T *)a->z, a->ldz, g, (T *)y, ldy, (T *)h, ldh, stats
 #define RES_GO(VE, TPR, E) \
@@ -829,7 +819,7 @@ template <typename T>
 RingPlan ring_plan(const zsolve_resnorm_args *a, const ResBack &p, int num_sms) {
     RingPlan r;
     const int64_t d = a->d;
-    if (d > 8192 || !aligned16(p.dh) || !aligned16(p.dy) || !aligned16(p.y) || !aligned16(p.o) || !aligned16(p.z)) return r;
+    if (d > 8192 || !aligned16(p.stats) || !aligned16(p.dh) || !aligned16(p.dy) || !aligned16(p.y) || !aligned16(p.o) || !aligned16(p.z)) return r;
     const int e = d > 4096 ? 16 : 8;
     r.tpr = 32;
     while (r.tpr * e < d) r.tpr *= 2;
@@ -882,14 +872,17 @@ int bwd(zsolve_seq *s, const zsolve_resnorm_args *a, const ResBack &p, const Res
             const bool vec = d % V == 0 && p.lddh % V == 0 && (!p.dy || p.lddy % V == 0) && p.ldy % V == 0 && p.ldo % V == 0 &&
                              (!p.z || p.ldz % V == 0) && p.lddx % V == 0 && p.lddo % V == 0 && (!p.dz || p.lddz % V == 0) &&
                              aligned16(p.dx) && aligned16(p.dout) && aligned16(p.dz);
+#define RES_SINGLE(TPR, E) (launch_ring<T, 1, TPR, E>(p, g, r, parts, s->d_status, s->st))
 #define RES_RING(TPR, E) (vec ? launch_ring<T, V, TPR, E>(p, g, r, parts, s->d_status, s->st) : launch_ring<T, 1, TPR, E>(p, g, r, parts, s->d_status, s->st))
             SEQ_CU(d > 4096       ? RES_RING(512, 16)
+                   : !vec && d > 256 * 8 && d <= 512 * 6 ? RES_SINGLE(512, 6)
                    : r.tpr == 32  ? RES_RING(32, 8)
                    : r.tpr == 64  ? RES_RING(64, 8)
                    : r.tpr == 128 ? RES_RING(128, 8)
                    : r.tpr == 256 ? RES_RING(256, 8)
                                   : RES_RING(512, 8));
 #undef RES_RING
+#undef RES_SINGLE
         } else {
             k_resnorm_bwd_long<T><<<(unsigned)a->rows, kLong, 0, s->st>>>(p, g, means);
             SEQ_CU(cudaGetLastError());

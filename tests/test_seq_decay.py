@@ -185,6 +185,13 @@ def test_strong_decays_keep_the_digits_after_them(seq, dtype):
 
 
 @gpu
+@pytest.mark.parametrize("dtype", ["float32", "bfloat16"])
+def test_positive_decays_grow(seq, dtype):
+    """g above zero: states that grow, up to e^40 over two spans and a part."""
+    _check(seq, [600, 3, 130], 1, 2, 64, 64, dtype, seed=10, decay=-0.2)
+
+
+@gpu
 @pytest.mark.parametrize("dtype", ["float32", "bfloat16", "float16"])
 def test_strides_batches_and_states_in_place(seq, dtype):
     """q, k and v as slices of one projection's output, equal lengths in two leading dimensions, s over s0:

@@ -98,6 +98,11 @@ def test_without_states(seq, s0, last, dtype):
 
 
 @pytest.mark.parametrize("dtype", ["float32", "bfloat16"])
+def test_positive_decays_grow(seq, dtype):
+    _check(seq, [600, 3, 130], 1, 2, 64, 64, dtype, seed=10, decay=-0.2)
+
+
+@pytest.mark.parametrize("dtype", ["float32", "bfloat16"])
 def test_strong_and_infinite_decays(seq, dtype):
     import torch
     x, dout, ds = _case([400], 1, 2, 64, 32, dtype, 8)

@@ -18,7 +18,7 @@ constexpr int kThreads = 128;
 template <typename T, int CA, int CB, bool SELF>
 struct RowSmem {
     static constexpr int LDA = tile_ld<T>(CA), LDB = tile_ld<T>(CB);
-    static constexpr int LDM = CB + 8, LDMT = 40;  // a state's 32 rows, or CB rows of 32 columns
+    static constexpr int LDM = CB + 8, LDMT = CA + 8;  // CA rows of a state's, or CB rows of CA columns
     T x[kChunk * LDA];
     T self[SELF ? kChunk * LDB : 8];
     union {
@@ -26,7 +26,7 @@ struct RowSmem {
             T y[kChunk * LDA];
             T z[kChunk * LDB];
         };
-        float m[32 * LDM > CB * LDMT ? 32 * LDM : CB * LDMT];
+        float m[CA * LDM > CB * LDMT ? CA * LDM : CB * LDMT];
     };
     float2 b[kSpanMost];
 };
@@ -40,6 +40,27 @@ __device__ __noinline__ int bad_row(const T *z, int c, bool back) {
         if (!isfinite(to_f32(z[r * LD + c]))) return r;
     }
     return back ? -1 : kChunk;
+}
+
+// `rows` x `cols` float32 values at distance ld, of which those below n and d are there, zeros elsewhere.
+template <int LD>
+__device__ __forceinline__ void load_state(float *dst, const float *src, int64_t ld, int rows, int cols, int n, int d) {
+    if (((uintptr_t)src & 15) == 0 && ld % 4 == 0 && d % 4 == 0) {
+        const int per = cols / 4;
+        for (int i = threadIdx.x; i < rows * per; i += kThreads) {
+            const int r = i / per, c = (i - r * per) * 4;
+            const bool in = r < n && c < d;
+            cp_async16(dst + r * LD + c, src + (in ? r * ld + c : 0), in ? 16 : 0);
+        }
+    } else {
+        for (int i = threadIdx.x; i < rows * cols; i += kThreads) {
+            const int r = i / cols, c = i - r * cols;
+            const bool in = r < n && c < d;
+            asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"((uint32_t)__cvta_generic_to_shared(dst + r * LD + c)),
+                         "l"(src + (in ? r * ld + c : 0)), "r"(in ? 4 : 0)
+                         : "memory");
+        }
+    }
 }
 
 template <typename T, int CA, int CB, bool SELF>
@@ -81,7 +102,6 @@ k_decay_rows(const DecayGeom geo, const DecayProduct p, const DecayRows self) {
         const int hv = SELF ? head * group + r : head;
         const int64_t slot = (int64_t)span * geo.d.hv + hv;
         __syncthreads();  // the last value head's tiles are read
-        for (int i = tid; i < n; i += kThreads) sm.b[i] = geo.gates[slot * geo.span + i];
         if (SELF && r == 0) load_tile<T, CB, kThreads>(sm.self, at(self, hv, i0), self.ld, rows, self.dist);
         // ---------------------------------------------------- the state's share
         const float *M = (const float *)p.m + slot * geo.d.dk * geo.d.dv;
@@ -91,23 +111,17 @@ k_decay_rows(const DecayGeom geo, const DecayProduct p, const DecayRows self) {
         for (int a0 = 0; a0 < acols; a0 += CA) {
             if (a0) __syncthreads();
             load_tile<T, CA, kThreads>(sm.x, at(p.x, hv, i0) + a0, p.x.ld, rows, min(CA, p.x.dist - a0));
+            if (p.turned)  // M is CB's rows x acols
+                load_state<LDMT>(sm.m, M + (int64_t)c0 * acols + a0, acols, CB, CA, bcols - c0, acols - a0);
+            else
+                load_state<LDM>(sm.m, M + (int64_t)a0 * bcols + c0, bcols, CA, CB, acols - a0, bcols - c0);
             cp_commit();
+            if (a0 == 0)
+                for (int i = tid; i < n; i += kThreads) sm.b[i] = geo.gates[slot * geo.span + i];
             cp_wait<0>();
+            __syncthreads();
 #pragma unroll 1
             for (int c = 0; c < CA && a0 + c < acols; c += 32) {
-                __syncthreads();
-                if (p.turned) {  // M is CB's rows x acols
-                    for (int i = tid; i < CB * 32; i += kThreads) {
-                        const int rr = i >> 5, cc = i & 31;
-                        sm.m[rr * LDMT + cc] = c0 + rr < bcols && a0 + c + cc < acols ? M[(int64_t)(c0 + rr) * acols + a0 + c + cc] : 0.f;
-                    }
-                } else {
-                    for (int i = tid; i < 32 * CB; i += kThreads) {
-                        const int rr = i / CB, cc = i - rr * CB;
-                        sm.m[rr * LDM + cc] = a0 + c + rr < acols && c0 + cc < bcols ? M[(int64_t)(a0 + c + rr) * bcols + c0 + cc] : 0.f;
-                    }
-                }
-                __syncthreads();
                 float2 r0[4], r1[4];
                 frag4<T, LDA, false>(sm.x, m0, c, r0);
                 frag4<T, LDA, false>(sm.x, m0 + 8, c, r1);
@@ -121,13 +135,13 @@ k_decay_rows(const DecayGeom geo, const DecayProduct p, const DecayRows self) {
 #pragma unroll
                         for (int u = 0; u < 4; u++) {
                             float2 h[4];
-                            frag4<float, LDMT, false>(sm.m, (j + u) * 8, 0, h);
+                            frag4<float, LDMT, false>(sm.m, (j + u) * 8, c, h);
 #pragma unroll
                             for (int i = 0; i < 4; i++) f[i][u] = h[i];
                         }
                     } else {
 #pragma unroll
-                        for (int i = 0; i < 4; i++) frag4<float, LDM, true>(sm.m, i * 8, j * 8, f[i]);
+                        for (int i = 0; i < 4; i++) frag4<float, LDM, true>(sm.m, c + i * 8, j * 8, f[i]);
                     }
 #pragma unroll
                     for (int u = 0; u < 4; u++) {

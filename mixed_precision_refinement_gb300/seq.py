@@ -563,7 +563,7 @@ class Seq:
         self._on_stream()
         y = torch.empty(x.shape, dtype=x.dtype, device=x.device)
         h = torch.empty_like(y)
-        stats = torch.empty((*x.shape[:-1], 4), dtype=torch.float32, device=x.device)
+        stats = torch.empty((x.shape[0], 4) if x.dim() == 2 else (*x.shape[:-1], 4), dtype=torch.float32, device=x.device)
         zsolve_resnorm(self.seq, x, o, w1, b1, z, act, c, w2, b2, kind, after, eps, y, h, stats)
         return y, h, stats
 

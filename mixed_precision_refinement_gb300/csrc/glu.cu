@@ -25,47 +25,53 @@ k_glu_dz(const T *__restrict__ dy, int64_t lddy, const T *__restrict__ zg, int64
     const int tx = threadIdx.x & 31, ty = threadIdx.x >> 5;
     const int64_t c = ((int64_t)blockIdx.x * 32 + tx) * 8;
     const int nc = (int)min((int64_t)8, (int64_t)n - c);
-    float sg[8] = {}, su[8] = {};
-    if (c < (n + 63) / 64 * 64) {
+    float2 sg[4] = {}, su[4] = {};
+    // behind the last column d is zero, and with it everything
+    auto one = [&](int64_t row, const float (&d)[8], float (&g)[8], float (&u)[8]) {
+        float a[8], s[8];
+        gates_all<true>(g, act, a, s);
+#pragma unroll
+        for (int i = 0; i < 8; i += 2) {
+            const float2 di = make_float2(d[i], d[i + 1]);
+            const float2 x = mul2(mul2(di, make_float2(u[i], u[i + 1])), make_float2(s[i], s[i + 1])), y = mul2(di, make_float2(a[i], a[i + 1]));
+            g[i] = x.x, g[i + 1] = x.y, u[i] = y.x, u[i + 1] = y.y;
+            sg[i / 2] = add2(sg[i / 2], x), su[i / 2] = add2(su[i / 2], y);
+        }
+        if (!dz) return;
+        Vec<T, 8> w;
+        w.set(g);
+        w.store(dz + row * 2 * nz + c);
+        w.set(u);
+        w.store(dz + row * 2 * nz + nz + c);
+    };
+    const int64_t first = (int64_t)blockIdx.y * 8 + ty, step = (int64_t)gridDim.y * 8;
+    if (vec && nc == 8) {
 #pragma unroll 2
-        for (int64_t row = (int64_t)blockIdx.y * 8 + ty; row < m; row += (int64_t)gridDim.y * 8) {
+        for (int64_t row = first; row < m; row += step) {
+            Vec<T, 8> vd, vg, vu;
+            vd.load(dy + row * lddy + c), vg.load(zg + row * ldzg + c), vu.load(zu + row * ldzu + c);
+            float d[8], g[8], u[8];
+            vd.get(d), vg.get(g), vu.get(u);
+            one(row, d, g, u);
+        }
+    } else if (c < (n + 63) / 64 * 64) {
+#pragma unroll 1
+        for (int64_t row = first; row < m; row += step) {
             float d[8] = {}, g[8] = {}, u[8] = {};
             if (nc > 0) {
-                load8<T>(dy, row * lddy + c, nc, vec, d);
-                load8<T>(zg, row * ldzg + c, nc, vec, g);
-                load8<T>(zu, row * ldzu + c, nc, vec, u);
+                load8<T>(dy, row * lddy + c, nc, 0, d);
+                load8<T>(zg, row * ldzg + c, nc, 0, g);
+                load8<T>(zu, row * ldzu + c, nc, 0, u);
             }
-#define DZ_CASE(A)                                                     \
-    case A: {                                                          \
-        _Pragma("unroll") for (int i = 0; i < 8; i++) {                \
-            const float z = g[i];                                      \
-            g[i] = i < nc ? d[i] * u[i] * slope1<A>(z) : 0.f;          \
-            u[i] = i < nc ? d[i] * act1<A>(z) : 0.f;                   \
-        }                                                              \
-        break;                                                         \
-    }
-            switch (act) {
-                DZ_CASE(ACT_NONE)
-                DZ_CASE(ACT_RELU)
-                DZ_CASE(ACT_SILU)
-                DZ_CASE(ACT_GELU)
-                DZ_CASE(ACT_GELU_TANH)
-            }
-#undef DZ_CASE
-#pragma unroll
-            for (int i = 0; i < 8; i++) sg[i] += g[i], su[i] += u[i];
-            if (dz) {
-                Vec<T, 8> w;
-                w.set(g);
-                w.store(dz + row * 2 * nz + c);
-                w.set(u);
-                w.store(dz + row * 2 * nz + nz + c);
-            }
+            one(row, d, g, u);
         }
     }
     if (!parts) return;
 #pragma unroll
-    for (int i = 0; i < 8; i++) red[0][ty][tx][i] = sg[i], red[1][ty][tx][i] = su[i];
+    for (int i = 0; i < 4; i++) {
+        red[0][ty][tx][2 * i] = sg[i].x, red[0][ty][tx][2 * i + 1] = sg[i].y;
+        red[1][ty][tx][2 * i] = su[i].x, red[1][ty][tx][2 * i + 1] = su[i].y;
+    }
     __syncthreads();
     // thread (ty, tx): column 8 tx + ty of the block's 256, of both
     float a = 0.f, b = 0.f;

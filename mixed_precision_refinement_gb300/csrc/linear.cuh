@@ -65,6 +65,53 @@ __device__ __forceinline__ float slope1(float z) {
     return 1.f;
 }
 
+__device__ __forceinline__ float2 both(float v) { return make_float2(v, v); }
+// Activations of a gate and, with SLOPE, their slopes.  silu z = z p with p = 1 / (1 + exp(-z)), silu' z = p + silu z (1 - p): one exponential and one
+// reciprocal serve both.
+__device__ __forceinline__ float2 logistic(float2 z) {
+    const float2 t = mul2(z, both(-1.4426950408889634f));
+    float2 p;
+    asm("ex2.approx.f32 %0, %1;" : "=f"(p.x) : "f"(t.x));
+    asm("ex2.approx.f32 %0, %1;" : "=f"(p.y) : "f"(t.y));
+    p = add2(p, both(1.f));
+    asm("rcp.approx.f32 %0, %1;" : "=f"(p.x) : "f"(p.x));
+    asm("rcp.approx.f32 %0, %1;" : "=f"(p.y) : "f"(p.y));
+    return p;
+}
+template <bool SLOPE, int N>
+__device__ __forceinline__ void gates_all(const float (&z)[N], int act, float (&a)[N], float (&s)[N]) {
+#define GATE_CASE(A)                                        \
+    case A: {                                              \
+        _Pragma("unroll") for (int i = 0; i < N; i++) {    \
+            a[i] = act1<A>(z[i]);                          \
+            if (SLOPE) s[i] = slope1<A>(z[i]);             \
+        }                                                  \
+        break;                                             \
+    }
+    switch (act) {
+        GATE_CASE(ACT_NONE)
+        GATE_CASE(ACT_RELU)
+        GATE_CASE(ACT_GELU)
+        GATE_CASE(ACT_GELU_TANH)
+        case ACT_SILU: {
+#pragma unroll
+            for (int i = 0; i < N; i += 2) {
+                const bool two = i + 1 < N;
+                const float2 v = make_float2(z[i], two ? z[i + 1 < N ? i + 1 : i] : 0.f), p = logistic(v), x = mul2(v, p);
+                const float2 g = fma2(x, fma2(p, both(-1.f), both(1.f)), p);
+                a[i] = x.x;
+                if (SLOPE) s[i] = g.x;
+                if (two) {
+                    a[i + 1 < N ? i + 1 : i] = x.y;
+                    if (SLOPE) s[i + 1 < N ? i + 1 : i] = g.y;
+                }
+            }
+            break;
+        }
+    }
+#undef GATE_CASE
+}
+
 template <int N>
 __device__ __forceinline__ void act_all(float (&v)[N], int act) {
 #define ACT_CASE(A)                                        \

@@ -48,7 +48,6 @@ __device__ __forceinline__ Stat stat_of(float2 s, float inv, float eps, int rms)
 
 // Two values at a time.  In both directions the instructions count as much as the bytes: a value of a row takes the share of a
 // pair of each of its own, so they are held to pairs (packed float32) wherever neither memory nor the gate is concerned.
-__device__ __forceinline__ float2 both(float v) { return make_float2(v, v); }
 __device__ __forceinline__ float2 pair(const float *f, int j) { return make_float2(f[2 * j], f[2 * j + 1]); }
 __device__ __forceinline__ void put(float *f, int j, float2 v) { f[2 * j] = v.x, f[2 * j + 1] = v.y; }
 // f(j): each j of N / 2 pairs; g(e): the value left over
@@ -70,52 +69,6 @@ __device__ __forceinline__ void plus(float *a, const float *b) {
 template <int N>
 __device__ __forceinline__ void scale_shift(float *a, float s, float b) {
     pairs<N>([&](int j) { put(a, j, fma2(pair(a, j), both(s), both(b))); }, [&](int e) { a[e] = fmaf(a[e], s, b); });
-}
-
-// The gate and, with SLOPE, its slope.  silu z = z p with p = 1 / (1 + exp(-z)), silu' z = p + silu z (1 - p): one exponential and one
-// reciprocal serve both.
-__device__ __forceinline__ float2 logistic(float2 z) {
-    const float2 t = mul2(z, both(-1.4426950408889634f));
-    float2 p;
-    asm("ex2.approx.f32 %0, %1;" : "=f"(p.x) : "f"(t.x));
-    asm("ex2.approx.f32 %0, %1;" : "=f"(p.y) : "f"(t.y));
-    p = add2(p, both(1.f));
-    asm("rcp.approx.f32 %0, %1;" : "=f"(p.x) : "f"(p.x));
-    asm("rcp.approx.f32 %0, %1;" : "=f"(p.y) : "f"(p.y));
-    return p;
-}
-template <bool SLOPE, int N>
-__device__ __forceinline__ void gates_all(const float (&z)[N], int act, float (&a)[N], float (&s)[N]) {
-#define RES_CASE(A)                                        \
-    case A: {                                              \
-        _Pragma("unroll") for (int i = 0; i < N; i++) {    \
-            a[i] = act1<A>(z[i]);                          \
-            if (SLOPE) s[i] = slope1<A>(z[i]);             \
-        }                                                  \
-        break;                                             \
-    }
-    switch (act) {
-        RES_CASE(ACT_NONE)
-        RES_CASE(ACT_RELU)
-        RES_CASE(ACT_GELU)
-        RES_CASE(ACT_GELU_TANH)
-        case ACT_SILU: {
-#pragma unroll
-            for (int i = 0; i < N; i += 2) {
-                const bool two = i + 1 < N;
-                const float2 v = make_float2(z[i], two ? z[i + 1 < N ? i + 1 : i] : 0.f), p = logistic(v), x = mul2(v, p);
-                const float2 g = fma2(x, fma2(p, both(-1.f), both(1.f)), p);
-                a[i] = x.x;
-                if (SLOPE) s[i] = g.x;
-                if (two) {
-                    a[i + 1 < N ? i + 1 : i] = x.y;
-                    if (SLOPE) s[i + 1 < N ? i + 1 : i] = g.y;
-                }
-            }
-            break;
-        }
-    }
-#undef RES_CASE
 }
 
 // Forward: TPR threads hold a row, VE consecutive values at a time (VE = 1 where rows are not

@@ -283,11 +283,23 @@ struct DecayWork {
                       : zs_launch_decay_rows(a->type, g, p, true, s->st, &s->launches);
     }
 
+    // Tokens of a span.  Short spans are short chains of products and many blocks, which is what few tokens need; long ones are few states
+    // to write and read, which is what many tokens cost.  Heads of 128 x 128, one sequence of T tokens, us forwards / backwards:
+    //   mma.sync, float32       64: 46 / 184, 166 / 673, 503 / 1918   128: 63 / 257, 158 / 637, 506 / 2022   256: 97 / 405, 190 / 833, 611 / 2608
+    //     (8 heads T = 256, 8 heads T = 5000, 32 heads T = 5000)
+    //   tensor memory, bfloat16 128: 25 / 83, 164 / 532, 995 / -      256: 30 / 100, 134 / 461, 710 / -      512: 30 / 100, 135 / 483, 663 / -
+    //     (8 heads T = 256, 32 heads T = 5000, 32 heads T = 32768)
+    static int span_of(const zsolve_decay_args *a, bool tc, bool backward) {
+        const int64_t rows = a->tokens * a->hv;
+        if (!tc) return rows <= 40000 ? 64 : 128;
+        return rows <= 16384 ? 128 : rows <= 65536 || backward ? 256 : 512;
+    }
+
     // Copies of rows that 16-byte loads cannot address, and the tables; dout NULL: the forward pass.
     int place(zsolve_seq *s, const zsolve_decay_args *a, zs::DecayGeom *g, const void *dout_p, int64_t lddo, bool backward, const float *ds,
               const float *ds0) {
-        g->span = 256;
         const bool tc = a->type == ZSOLVE_BF16 && a->dv % 8 == 0 && (!backward || a->dv <= 128);
+        g->span = span_of(a, tc, backward);
         nparts = !tc ? 0 : backward ? 3 : 2;
         const int64_t most = a->tokens / g->span + a->nseq;
         if (most > 0x7fffffff / zs::kSpanMost) return seq_fail(s, ZSOLVE_EINVAL, "too many spans");

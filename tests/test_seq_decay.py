@@ -184,6 +184,17 @@ def test_strong_decays_keep_the_digits_after_them(seq, dtype):
     _verify(x, 1.0, o, s, dtype)
 
 
+# tokens x heads that each length of a span is taken for
+SPANS = [([600, 3, 130], 8, 24, 32, 48), ([1030, 70, 0, 1], 16, 64, 32, 32), ([700, 3], 32, 64, 64, 32)]
+
+
+@gpu
+@pytest.mark.parametrize("dtype", ["float32", "bfloat16", "float16"])
+@pytest.mark.parametrize("lens,hk,hv,dk,dv", SPANS)
+def test_many_rows(seq, lens, hk, hv, dk, dv, dtype):
+    _check(seq, lens, hk, hv, dk, dv, dtype, seed=11)
+
+
 @gpu
 @pytest.mark.parametrize("dtype", ["float32", "bfloat16"])
 def test_positive_decays_grow(seq, dtype):

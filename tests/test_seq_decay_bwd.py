@@ -1,7 +1,7 @@
 """Gradients of linear attention with a decay for each head against float64 (limits: test_seq_decay.py)."""
 import pytest
 
-from test_seq_decay import LAYOUTS, OUTSIDE, U, _all_pairs, _inputs, _limit, _near, _outside, _sizes
+from test_seq_decay import LAYOUTS, OUTSIDE, SPANS, U, _all_pairs, _inputs, _limit, _near, _outside, _sizes
 
 pytestmark = pytest.mark.gpu
 NAMES = ("q", "k", "v", "g", "s0")
@@ -95,6 +95,12 @@ def test_head_layouts(seq, hk, hv, dtype):
 @pytest.mark.parametrize("dtype", ["float32", "bfloat16"])
 def test_without_states(seq, s0, last, dtype):
     _check(seq, [130, 270], 2, 2, 64, 48, dtype, seed=6, s0=s0, last=last)
+
+
+@pytest.mark.parametrize("dtype", ["float32", "bfloat16", "float16"])
+@pytest.mark.parametrize("lens,hk,hv,dk,dv", SPANS)
+def test_many_rows(seq, lens, hk, hv, dk, dv, dtype):
+    _check(seq, lens, hk, hv, dk, dv, dtype, seed=11)
 
 
 @pytest.mark.parametrize("dtype", ["float32", "bfloat16"])

@@ -431,8 +431,10 @@ const char *zsolve_afs_last_error(const zsolve_afs *afs);
 void zsolve_afs_destroy(zsolve_afs *afs);
 
 /* ---------------------------------------------------------------------------
- * Operators of a sequence layer: layer norm, the matrix product with its
- * epilogue, and the gated delta rule.  A sweep's solutions are sequences
+ * Operators of a sequence layer: layer norm, the norms around a block with its
+ * gate and residual, the matrix product with its epilogue, the gated
+ * feed-forward projections, the gated delta rule, and linear attention with a
+ * decay for each head.  A sweep's solutions are sequences
  * (one token a frequency), and a model that learns them is made of these; the
  * delta rule's chunked form is the blocked triangular solve of the
  * factorisation above, one 64 x 64 unit triangle a chunk.  No passage: the

@@ -1,4 +1,4 @@
-"""Binding of the sequence-layer operators (layer norm, linear, delta rule) of include/zsolve.h.
+"""Binding of the sequence-layer operators (norms, products, delta rule, decayed attention) of include/zsolve.h.
 
 As in the rest of the binding, a function with a C entry point's name calls it
 on tensors that the caller holds; `Seq` owns a handle, allocates the outputs
@@ -519,9 +519,9 @@ class Seq:
             h, mean, rstd = s.layernorm(x, w, b)
             dx, dw, db = s.layernorm_bwd(dh, x, mean, rstd, w)
 
-    Tensors that require gradients may be given as well: y of layernorm and linear and both outputs of delta then
-    carry them (the handle has to be open in the backward pass).  mean, rstd and z carry none, nor does delta_step:
-    a backward pass that needs theirs raises.
+    Tensors that require gradients may be given as well: y of layernorm, linear and glu, y and h of resnorm and both outputs
+    of delta and decay then carry them (the handle has to be open in the backward pass).  mean, rstd, stats, z, zg and
+    zu carry none, nor do delta_step and decay_step: a backward pass that needs theirs raises.
     """
 
     def __init__(self):

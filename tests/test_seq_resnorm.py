@@ -158,6 +158,32 @@ def test_widths(seq, d, types):
 
 
 @pytest.mark.gpu
+@pytest.mark.parametrize("rows,d", [(12001, 1), (12000, 5), (12003, 64), (9001, 250), (5000, 520), (3001, 1111), (1501, 4100), (900, 8192)])
+@pytest.mark.parametrize("types", TYPES, ids="-".join)
+def test_many_rows_a_block(seq, rows, d, types):
+    torch = _torch()
+    i, dy, dh = _inputs(rows, d, *(getattr(torch, t) for t in types), seed=d + 1)
+    _check(seq, i, dy, dh, ACTS[d % 5], "layer" if d % 3 == 1 else "rms", True, types)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("d", [5, 264, 2157])
+def test_statistics_off_16_bytes(seq, d):
+    """Statistics that start anywhere give what aligned ones do, but for the order of the sums."""
+    import mixed_precision_refinement_gb300 as zs
+    torch = _torch()
+    i, dy, dh = _inputs(300, d, torch.float32, torch.float32, seed=3)
+    weights = dict(z=i["z"], act="silu", c=i["c"], w2=i["w2"], b2=i["b2"])
+    y, _, stats = seq.resnorm(i["x"], i["o"], i["w1"], i["b1"], **weights)
+    moved = torch.empty(1201, device="cuda")[1:].view(300, 4)
+    moved.copy_(stats)
+    one, other = (seq.resnorm_bwd(dh, y, i["o"], t, i["w1"], i["b1"], dy=dy, **weights) for t in (stats, moved))
+    for a, b in zip(one, other):
+        # each is off by at most a few hundred float32 roundings of its terms, which are of a few times the largest result
+        assert float((a - b).abs().max()) <= 2.0 ** -24 * 600 * 4 * float(a.abs().max())
+
+
+@pytest.mark.gpu
 @pytest.mark.parametrize("kind", ["layer", "rms"])
 @pytest.mark.parametrize("after", [True, False])
 @pytest.mark.parametrize("gate", [None] + ACTS)

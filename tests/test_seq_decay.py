@@ -184,6 +184,22 @@ def test_strong_decays_keep_the_digits_after_them(seq, dtype):
     _verify(x, 1.0, o, s, dtype)
 
 
+@gpu
+@pytest.mark.parametrize("dtype", ["float32", "bfloat16"])
+def test_nonfinite_values_stay_in_their_head(seq, dtype):
+    """More rows of blocks than the GPU holds at a time: what is not finite in one head's diagonal tiles changes no bit elsewhere."""
+    torch = _torch()
+    x = _inputs([1100], 16, 64, 64, 64, dtype, seed=12)
+    clean = seq.decay(x["q"], x["k"], x["v"], x["g"], x["s0"], x["offsets"], 0.7)
+    for token, head, column in ((700, 5, 3), (0, 40, 63), (1099, 63, 0)):
+        v = x["v"].clone()
+        v[token, head, column] = float("nan")
+        o, s = seq.decay(x["q"], x["k"], v, x["g"], x["s0"], x["offsets"], 0.7)
+        assert bool(o[token:, head, column].isnan().all()) and bool(s[0, head, :, column].isnan().all())
+        o[token:, head, column], s[0, head, :, column] = clean[0][token:, head, column], clean[1][0, head, :, column]
+        assert torch.equal(o, clean[0]) and torch.equal(s, clean[1])
+
+
 # tokens x heads that each length of a span is taken for
 SPANS = [([600, 3, 130], 8, 24, 32, 48), ([1030, 70, 0, 1], 16, 64, 32, 32), ([700, 3], 32, 64, 64, 32)]
 

@@ -97,6 +97,25 @@ def test_without_states(seq, s0, last, dtype):
     _check(seq, [130, 270], 2, 2, 64, 48, dtype, seed=6, s0=s0, last=last)
 
 
+@pytest.mark.parametrize("dtype", ["float32", "bfloat16"])
+def test_nonfinite_gradients_stay_in_their_heads(seq, dtype):
+    """More rows of blocks than the GPU holds at a time: a gradient that is not finite changes no bit of later tokens, nor of other heads."""
+    import torch
+    x, dout, ds = _case([1100], 16, 64, 64, 64, dtype, 12)
+    call = lambda d: seq.decay_bwd(d, x["q"], x["k"], x["v"], x["g"], x["s0"], ds, x["offsets"], 0.7)  # noqa: E731
+    clean = call(dout)
+    for token, head in ((700, 5), (0, 40), (1099, 63)):
+        d = dout.clone()
+        d[token, head, 7] = float("nan")
+        got = call(d)
+        assert bool(got[2][:token + 1, head, 7].isnan().all()) and bool(got[0][token, head // 4].isnan().all())
+        for i, (a, b) in enumerate(zip(got[:4], clean)):
+            own = head // 4 if i < 2 else head
+            others = [h for h in range(a.shape[1]) if h != own]
+            assert torch.equal(a[:, others], b[:, others])
+            assert torch.equal(a[token + 1:, own], b[token + 1:, own])
+
+
 @pytest.mark.parametrize("dtype", ["float32", "bfloat16", "float16"])
 @pytest.mark.parametrize("lens,hk,hv,dk,dv", SPANS)
 def test_many_rows(seq, lens, hk, hv, dk, dv, dtype):

@@ -737,6 +737,8 @@ k_decay_rows_self(const __grid_constant__ CUtensorMap xmap, const __grid_constan
                 const int j0 = jb * kTile, rest = n - j0;
                 const bool diag = jb == rb;
                 if (checked(x, jb)) {
+                    // the tile before it in its place has arrived: it is one of the state's, or one that S2 was formed from, and the
+                    // warps have waited for those products
                     const uint32_t z = m + 4 + 2 * (jb - first);
                     if (!wait(&bar_full[z % kRing], z / kRing)) break;
                     look_over(ring + z % kRing * kTileBytes, zboxes, rest, diag, p.back, s_bad, &s_anybad, &s_badtok, et, 512);
@@ -1084,8 +1086,10 @@ k_decay_rows_tc(const __grid_constant__ CUtensorMap xmap, const __grid_constant_
             for (int jb = first; ok && jb < end; jb++, k++) {
                 const int j0 = jb * kTile, rest = n - j0;
                 const bool diag = jb == rb;
+                // Every tile of z takes the place of the one before it, and the warps wait for each of them, also where there is nothing to
+                // look over: with the one before still on its way, a wait for this one would be told of the fill before both.
+                const uint32_t z = m + 3 + 2 * (jb - first);
                 if (checked(x, jb)) {
-                    const uint32_t z = m + 3 + 2 * (jb - first);
                     if (!wait(&bar_full[z % kHalfRing], z / kHalfRing)) break;
                     look_over(ring + z % kHalfRing * kTileBytes, zboxes, rest, diag, p.back, s_bad[i % 3], &s_anybad[i % 3], nullptr, et, 256);
                     arrive(&bar_checked[ck++ & 1]);
@@ -1116,6 +1120,8 @@ k_decay_rows_tc(const __grid_constant__ CUtensorMap xmap, const __grid_constant_
                     tmem_st16(t_s + c, u);
                 }
                 tmem_wait_st();
+                // before the weights are handed over: z's place is not free, nor filled again, until all warps have done so
+                if (!checked(x, jb) && !wait(&bar_full[z % kHalfRing], z / kHalfRing)) break;
                 arrive(&bar_p[k & 1]);
             }
             m += 2 + 2 * (end - first);

@@ -572,9 +572,9 @@ class Seq:
         """Returns (dx, do, dz, dw1, db1, dc, dw2, db2) from the gradients of h and, unless None, of y; None for what is not
         given."""
         self._on_stream()
-        dx = torch.empty(o.shape, dtype=o.dtype, device=o.device)
-        do = torch.empty_like(dx)
-        dz = None if z is None else torch.empty_like(dx)
+        dx = torch.empty(y.shape, dtype=y.dtype, device=y.device)
+        do = torch.empty(o.shape, dtype=o.dtype, device=o.device)
+        dz = None if z is None else torch.empty(z.shape, dtype=z.dtype, device=z.device)
         sums = [None if t is None else torch.empty_like(t) for t in (w1, b1, c, w2, b2)]
         zsolve_resnorm_bwd(self.seq, dh, dy, y, o, stats, w1, b1, z, act, c, w2, b2, kind, after, dx, do, dz, *sums)
         return (dx, do, dz, *sums)

@@ -54,11 +54,11 @@ class ResNorm(torch.autograd.Function):
             return (None,) * 13
         y, o, stats, w1, b1, z, c, w2, b2 = ctx.saved_tensors
         act, kind, after = ctx.options
-        dh = torch.zeros(o.shape, dtype=o.dtype, device=o.device) if dh is None else dh.contiguous()
+        dh = torch.zeros(y.shape, dtype=y.dtype, device=y.device) if dh is None else dh.contiguous()
         dy = None if dy is None else dy.contiguous()
         needs = ctx.needs_input_grad
-        dx, do = (torch.empty(o.shape, dtype=o.dtype, device=o.device) for _ in range(2))
-        dz = torch.empty_like(dx) if needs[5] else None
+        dx, do = (torch.empty(t.shape, dtype=t.dtype, device=t.device) for t in (y, o))
+        dz = torch.empty(z.shape, dtype=z.dtype, device=z.device) if needs[5] else None
         dw1, db1, dc, dw2, db2 = (torch.empty(t.shape, dtype=t.dtype, device=t.device) if need else None
                                   for t, need in ((w1, needs[3]), (b1, needs[4]), (c, needs[7]), (w2, needs[8]), (b2, needs[9])))
         ctx.seq._on_stream()
@@ -71,7 +71,7 @@ class Linear(torch.autograd.Function):
     @staticmethod
     def forward(ctx, seq, x, w, b, act, r, keep):
         y, z = seq.linear(x, w, b, act, r, keep=True) if keep or act != "none" else (seq.linear(x, w, b, act, r), None)
-        ctx.seq, ctx.act = seq, act
+        ctx.seq, ctx.act, ctx.added = seq, act, None if r is None else r.shape
         ctx.set_materialize_grads(False)
         ctx.save_for_backward(x, w, z)
         return (y, z) if keep else y
@@ -90,7 +90,7 @@ class Linear(torch.autograd.Function):
         if any(needs[1:4]):
             ctx.seq._on_stream()
             binding.zsolve_linear_bwd(ctx.seq.seq, dy.contiguous(), x, w, ctx.act, z, dx, dw, db)
-        return None, dx, dw, db, None, dy if needs[5] else None, None
+        return None, dx, dw, db, None, dy.reshape(ctx.added) if needs[5] else None, None
 
 
 class Glu(torch.autograd.Function):
@@ -136,7 +136,7 @@ class Delta(torch.autograd.Function):
         do = torch.zeros(v.shape, dtype=v.dtype, device=v.device) if do is None else do.contiguous()
         ds = None if ds is None else ds.contiguous()
         *grads, ds0 = ctx.seq.delta_bwd(do, q, k, v, g, beta, s0, ds, offsets, ctx.scale)
-        return (None, *grads, ds0 if s0 is not None else None, None, None)
+        return (None, *grads, ds0.view(s0.shape) if s0 is not None else None, None, None)
 
 
 class Decay(torch.autograd.Function):
@@ -157,7 +157,7 @@ class Decay(torch.autograd.Function):
         do = torch.zeros(v.shape, dtype=v.dtype, device=v.device) if do is None else do.contiguous()
         ds = None if ds is None else ds.contiguous()
         *grads, ds0 = ctx.seq.decay_bwd(do, q, k, v, g, s0, ds, offsets, ctx.scale)
-        return (None, *grads, ds0 if s0 is not None else None, None, None)
+        return (None, *grads, ds0.view(s0.shape) if s0 is not None else None, None, None)
 
 
 class DecayStep(torch.autograd.Function):

@@ -594,7 +594,9 @@ int zsolve_glu_bwd(zsolve_seq *seq, int type, int64_t m, int64_t n, int64_t k, c
 /* The gated delta rule.  Each value head of a sequence has a state S (dk x dv,
  * float32), and every token t, with a_t = exp(g_t),
  *   u_t = beta_t (v_t - a_t S^T k_t),  S <- a_t S + k_t u_t^T,  o_t = scale S^T q_t.
- * Value head h uses key head h / (hv / hk).  g_t = -infinity empties the state. */
+ * Value head h uses key head h / (hv / hk).  g_t = -infinity empties the state.  An infinity or
+ * NaN in the inputs stays out of earlier tokens' results; in those that it belongs to, what the
+ * formulas make an infinity may be a NaN. */
 #define ZSOLVE_DELTA_MAX_DK 128
 
 typedef struct {
@@ -639,7 +641,10 @@ int zsolve_delta_bwd(zsolve_seq *seq, const zsolve_delta_args *args, const void 
 /* Linear attention with a decay for each head.  Each value head of a sequence has a state S (dk x dv,
  * float32), and every token t, with a_t = exp(g_t),
  *   S <- a_t S + k_t v_t^T,  o_t = scale S^T q_t.
- * Value head h uses key head h / (hv / hk).  g_t = -infinity empties the state before the token. */
+ * Value head h uses key head h / (hv / hk).  g_t = -infinity empties the state before the token.
+ * An infinity or NaN in the inputs stays out of earlier tokens' results; in those that it belongs
+ * to, what the formulas make an infinity may be a NaN.  g above zero is growth: where log decays
+ * of up to 512 tokens in a row add up to more than 88, the results may be infinities or NaN. */
 #define ZSOLVE_DECAY_MAX_DK 128
 
 typedef struct {

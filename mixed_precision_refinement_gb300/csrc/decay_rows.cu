@@ -8,7 +8,7 @@
 // Products keep float32 accuracy: an operand that is not exact in tf32 goes in two tf32 parts (delta.cuh), every sum is short and
 // joins the others by float32 additions.
 //
-// 2467 tokens x 8 heads of 96 x 80 in float32, spans of 64: 50 us, bound by the products of a block in order (two warps a
+// 2467 tokens x 8 heads of 96 x 80 in float32, spans of 64: 44 us, bound by the products of a block in order (two warps a
 // scheduler, which is what 255 registers allow; tensor pipe 34 %).  A state in four pieces, each waited for, was 6 us slower.
 #include "decay.cuh"
 

@@ -61,7 +61,7 @@ __device__ __forceinline__ void load4(const float *p, float2 &a, float2 &b) {
 // three parts by eight warps, in shared memory, where they are the MN-major A operand (the large part in the tile's own
 // place); y's are the B operand as TMA leaves them.  Two accumulators, one for the small parts; after 128 tokens both are
 // added to the float32 sums in the warps' registers.  Two blocks an SM, so that one's
-// conversions run beside the other's products.  32768 tokens x 32 heads of 128 x 128 in spans of 512: 206 us, the tensor pipe busy
+// conversions run beside the other's products.  32768 tokens x 32 heads of 128 x 128 in spans of 512: 204 us, the tensor pipe busy
 // 19 % of the time; what a chunk waits for is the way from its tile over its parts to the products, and two blocks are what
 // shared memory holds.
 constexpr int kSumWorkers = 256, kSumThreads = kSumWorkers + 32;
@@ -453,7 +453,7 @@ __device__ __forceinline__ void put_row(bf16 *o, int c, int cols, int vec, const
 // beside S the other scores S2 = self Z^T, for the sums of pairs.  One block of threads an SM, sixteen warps, a quarter of a row a
 // thread.  Its events, a state's share or a block of tokens each, use two places for S in turn: the next one's product is
 // under way while this one's weights are found; S2 has one place and follows once it is read.  2 x 4096 tokens x 32 heads (16 key heads)
-// of 128: 177 us, 2.0 TB/s, the tensor pipe busy 21 %: the way from an event to the next.  TMEM has no room for a second block beside
+// of 128: 142 us, the tensor pipe busy 21 %: the way from an event to the next.  TMEM has no room for a second block beside
 // its 512 columns.
 constexpr uint32_t kSelfSmem = kTileBytes * (2 + kRing) + 1024;
 
@@ -816,8 +816,8 @@ k_decay_rows_self(const __grid_constant__ CUtensorMap xmap, const __grid_constan
 
 // Without SELF (o and dv): two blocks of threads an SM, of eight warps each, half a row a thread; their items are 128 rows of a span
 // and head.  An item is a chain (the state's share, scores, weights, products, results), and each block has one at a time:
-// what runs side by side is the two blocks' chains.  32768 tokens x 32 heads of 128 in spans of 256: the call takes 742 us, 778 with
-// one block of sixteen warps whose chains overlap by two places for S and O (backwards 656 and 675).
+// what runs side by side is the two blocks' chains.  32768 tokens x 32 heads of 128 in spans of 512: 402 us.  One block of sixteen warps whose
+// chains overlap by two places for S and O was slower: the call 778 us for 742 when both took spans of 256, backwards 675 for 656.
 constexpr int kHalfThreads = 64 + 256;
 constexpr int kHalfRing = 2;
 constexpr uint32_t kRowsSmem = kTileBytes * (1 + kHalfRing) + 1024;

@@ -6,7 +6,7 @@
 // side in one accumulator, and the epilogue multiplies what it reads (linear_tc.cuh).  Nothing
 // but y is written unless zg and zu are kept.  Backward, dzg and dzu are the halves of one
 // matrix, so that dx is one sum over both and dW one product with the rows of both.  16384 x 8192 x 4096 bfloat16: 1187 us alone,
-// 1345 back to back under the power limit (1635 TFLOP/s); backwards 8192 x 4096 x 2048 398 us, 312 of them the products.
+// 1345 to 1380 back to back under the power limit (1635 to 1590 TFLOP/s); backwards 8192 x 4096 x 2048 390 to 404 us, 307 of them the products.
 #include "linear_tc.cuh"
 
 namespace {
@@ -296,6 +296,9 @@ int zs_glu(zsolve_seq *s, int type, int64_t m, int64_t n, int64_t k, const void 
     epi.vec = vec8(bg, 0) && vec8(bu, 0) && vec8(y, ldy) && vec8(zg, ldzg) && vec8(zu, ldzu);
     const Mat mx{x, m, k, ldx}, mg{wg, n, k, ldwg}, mu{wu, n, k, ldwu};
     const bool aligned = mx.tma_ok() && mg.tma_ok() && mu.tma_ok();
+    // Few rows: one kernel that reads each weight once and waits for its loads, against tiles of 128 rows.  The small kernel and the tiles at
+    // 16 rows, bfloat16, weights from HBM, us: 1024 x 1024 6.5 and 8.0, 2048 x 2048 11.1 and 10.3, 4096 x 2048 12.7 and 14.1,
+    // 4096 x 4096 22.1 and 17.9 (9 rows: 21.3 and 22.7), 8192 x 4096 43.2 and 29.6.
     if (m <= 8 || (m <= kFewRows && aligned && n * k <= 1 << 23)) {
         SEQ_CU(zs_launch_glu_few(type, m, n, k, x, ldx, wg, ldwg, wu, ldwu, epi, s->st, &s->launches));
         return ZSOLVE_OK;

@@ -12,7 +12,7 @@
 // With u = dx act(z), Q = sum u h1 and R = sum u: dw1 = c Q, db1 = c R, dc = w1 Q + b1 R, so four
 // sums a column serve all five.
 // Both are bound by HBM: each tensor crosses it once, a row is held in registers between its
-// reductions.  16384 x 4096 bfloat16 with a gate: 127 us, 5.0 TB/s; backwards, 32768 x 4096, 519 us, 4.1 TB/s, bound by what a row's
+// reductions.  16384 x 4096 bfloat16 with a gate: 127 us, 5.0 TB/s; backwards, 32768 x 4096, 518 us and 7 for the weights' sums, 4.1 TB/s, bound by what a row's
 // two reductions wait for with 16 warps an SM.  Sums, statistics and what lies between the norms are float32; y is rounded for
 // memory alone, and h comes from the value before that rounding.  As in layernorm.cu, a mean's
 // own error is found again in the second pass.
@@ -591,7 +591,8 @@ k_resnorm_bwd(const ResBack p, const ResGeom g, int stages, float *__restrict__ 
 }
 
 // Rows for which no ring has room, and tensors that do not start on 16 bytes: one block a row in
-// passes over it, and the columns' sums with a thread a column over a share of the rows, from the rows' means
+// passes over it (8192 x 8192 float32: 1787 us, 1.2 TB/s; bfloat16 with float32 weights, for which the ring has no room there, 1777, and with
+// bfloat16 weights, from the ring, 290), and the columns' sums with a thread a column over a share of the rows, from the rows' means
 // of the first reduction.
 template <typename T>
 struct ResGrad {
@@ -830,6 +831,9 @@ int bwd(zsolve_seq *s, const zsolve_resnorm_args *a, const ResBack &p, const Res
                              aligned16(p.dx) && aligned16(p.dout) && aligned16(p.dz);
 #define RES_SINGLE(TPR, E) (launch_ring<T, 1, TPR, E>(p, g, r, parts, s->d_status, s->st))
 #define RES_RING(TPR, E) (vec ? launch_ring<T, V, TPR, E>(p, g, r, parts, s->d_status, s->st) : launch_ring<T, 1, TPR, E>(p, g, r, parts, s->d_status, s->st))
+            // Single columns: between four and six for each of 512 threads, six are enough, and the registers of two more are free (6614 rows of
+            // 2157 float32 131 us, 156 with eight; of 2901 149 and 187; of 2501 bfloat16 141 and 162).  The like brackets of
+            // fewer threads, 513 to 768 and 1025 to 1536 columns, have no such kernel.
             SEQ_CU(d > 4096       ? RES_RING(512, 16)
                    : !vec && d > 256 * 8 && d <= 512 * 6 ? RES_SINGLE(512, 6)
                    : r.tpr == 32  ? RES_RING(32, 8)

@@ -283,12 +283,20 @@ struct DecayWork {
                       : zs_launch_decay_rows(a->type, g, p, true, s->st, &s->launches);
     }
 
-    // Tokens of a span.  Short spans are short chains of products and many blocks, which is what few tokens need; long ones are few states
-    // to write and read, which is what many tokens cost.  Heads of 128 x 128, one sequence of T tokens, us forwards / backwards:
-    //   mma.sync, float32       64: 46 / 184, 166 / 673, 503 / 1918   128: 63 / 257, 158 / 637, 506 / 2022   256: 97 / 405, 190 / 833, 611 / 2608
-    //     (8 heads T = 256, 8 heads T = 5000, 32 heads T = 5000)
-    //   tensor memory, bfloat16 128: 25 / 83, 164 / 532, 995 / -      256: 30 / 100, 134 / 461, 710 / -      512: 30 / 100, 135 / 483, 663 / -
-    //     (8 heads T = 256, 32 heads T = 5000, 32 heads T = 32768)
+    // Tokens of a span, by the rows (tokens x heads) of the call.  Short spans are short chains of products and many blocks, which is what few
+    // tokens need; long ones are few states to write, read and hold, which is what many tokens cost.  One sequence, heads of 128 x 128,
+    // us forwards / backwards (in brackets heads of 64 x 64):
+    //   mma.sync, float32    rows  16000 (8 heads)    30000 (8)   40000 (8)   40000 (32)              80000 (32)   160000 (32)
+    //     spans of  64       67 / 233 (37 / 132)      120 / 464   163 / 675   145 / 619 (65 / 215)    269 / 1058   502 / 1919 (215 / 660)
+    //     spans of 128       69 / 280 (40 / 176)      121 / 528   156 / 639   148 / 622 (72 / 258)    273 / 1101   506 / 2017 (214 / 756)
+    //     spans of 256       101 / 425 (56 / 283)     144 / 675   190 / 833   195 / 840 (87 / 353)    338 / 1462   610 / 2603 (267 / 1036)
+    //   float16, 160000 rows:  64: 352 / 1034, 128: 326 / 1048.  So 64 is as fast or faster backwards at any size but one, and above 40000 rows the
+    //   rule takes 128 for the workspace: half the states, 82 MB for 164 in float32 at 160000 rows (twice that backwards).
+    //   tensor memory        rows  16000 (8 heads)    32000 (8)   64000 (8)   64000 (32)              160000 (32)             1048576 (32)
+    //     spans of 128       31 / 103 (24 / 85)       46 / 148    81 / 275    66 / 233 (44 / 149)     164 / 530 (91 / 321)    993 / 2889 (530 / 1698)
+    //     spans of 256       35 / 113 (27 / 92)       40 / 128    66 / 224    57 / 204 (42 / 150)     134 / 458 (87 / 321)    731 / 2327 (462 / 1645)
+    //     spans of 512       46 / 149 (35 / 123)      49 / 156    67 / 224    64 / 228 (49 / 178)     137 / 484 (95 / 371)    670 / 2283 (461 / 1767)
+    //   Forwards 512 costs 2 % (heads of 64: 9) at 160000 rows and gains 8 % at a million; where they cross was not looked for.
     static int span_of(const zsolve_decay_args *a, bool tc, bool backward) {
         const int64_t rows = a->tokens * a->hv;
         if (!tc) return rows <= 40000 ? 64 : 128;
@@ -603,6 +611,8 @@ int zsolve_decay(zsolve_seq *s, const zsolve_decay_args *a, void *o, int64_t ldo
     st = check_device(s);
     if (st != ZSOLVE_OK) return st;
     const int64_t longest = a->offsets ? a->tokens : a->tokens / a->nseq;
+    // The delta rule's bound.  Here the two cross later: heads of 128 x 128 in bfloat16, token by token / in spans, 8 tokens of one sequence
+    // x 32 heads 7.2 / 22.4 us, 16 tokens 12.0 / 22.4, 32 tokens 21.8 / 22.4; 64 such sequences 133 / 233, 242 / 238, 462 / 243.
     if (longest <= kStepTokens) {
         SEQ_CU(zs_launch_decay_step(a->type, g, a->offsets, a->s0, o, ldo, sn, s->st, &s->launches));
         return ZSOLVE_OK;
